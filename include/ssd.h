@@ -1,5 +1,7 @@
 /*
- * ssd.h -- C ABI of the MI355X (gfx950) chunked SSD forward pass and decode step.
+ * ssd.h -- C ABI of the MI355X (gfx950) chunked SSD forward pass and decode step,
+ * and (last three parts) of linear attention with one decay a head, group norm and
+ * the pages of a state pool.
  *
  * The operator is the scalar-decay state space model of "Transformers are
  * SSMs" (paper card at wikillm.com/papers/2405.21060, Method 1 and Method 2,
@@ -434,6 +436,158 @@ ssd_status ssd_step(float* state, const void* x, const float* log_a, const void*
 ssd_status ssd_step_mamba2(float* state, const void* x, const float* dt, const float* dt_bias,
                            const float* A_log, const float* D, const void* z, const void* B,
                            const void* C, void* y, const ssd_shape* shape, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Linear attention with one fixed decay a head. For query head h, with
+ * lam = exp(log_decay[h]) and D the head's state [dv][dk]:
+ *     D_t = lam D_{t-1} + v_t k_t^T,    o_t = scale D_t q_t.
+ * It is the recurrence of ssd_fwd with a decay that no token changes, for the
+ * layouts such layers have: query heads that share keys and values (head h
+ * reads key/value head h / (nheads / nkv_heads); every query head has a decay
+ * and a state of its own), sizes in steps of 8, rows inside a wider projection,
+ * sequences of any length, states in a pool of slots. No segment sums are
+ * formed: the weights are powers of lam.
+ *   q [batch, seqlen, nheads, dk], k [.., nkv_heads, dk], v [.., nkv_heads, dv] dtype:
+ *       element (token, head, i) at token * row + head * d + i, with row the
+ *       shape's q_row, k_row or v_row (0: contiguous); 16-byte aligned rows
+ *   log_decay [nheads] fp32, <= 0 (-inf: no memory); a constant of the layer,
+ *       its gradient is not formed
+ *   o [batch, seqlen, nheads, dv] dtype, contiguous
+ *   states fp32 [batch or num_seqs, nheads, dv, dk], 16-byte aligned: the
+ *       layout of ssd_step's [H][P][N]
+ * cu_seqlens (device, int32, num_seqs + 1 entries, batch 1): non-decreasing;
+ * a sequence may be empty, its final state is then its initial one. Rows of o
+ * and of the gradients before cu[0] or from cu[num_seqs] on are left as they
+ * were. Entries outside [0, seqlen] are brought into it.
+ * dk and dv: multiples of 8 up to 256. bf16 products are formed with fp32
+ * sums; states are carried in fp32.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t batch;      /* rows; 1 with cu_seqlens; the step: entries            */
+  int32_t seqlen;     /* tokens a row (packed: in all); ignored by the step    */
+  int32_t nheads;     /* query heads                                           */
+  int32_t nkv_heads;  /* key and value heads, nheads % nkv_heads == 0          */
+  int32_t dk;         /* size of a query and of a key                          */
+  int32_t dv;         /* size of a value                                       */
+  int32_t num_seqs;   /* packed sequences with cu_seqlens, else 0              */
+  int32_t dtype;      /* ssd_dtype of q, k, v, o and their gradients           */
+  int64_t q_row;      /* elements from token to token, 0: nheads * dk          */
+  int64_t k_row;      /* 0: nkv_heads * dk                                     */
+  int64_t v_row;      /* 0: nkv_heads * dv                                     */
+} ssd_lin_shape;
+
+/* Workspace of a forward and of a backward call; may be 0, and the workspace
+ * pointer NULL then. */
+ssd_status ssd_lin_attn_workspace_bytes(const ssd_lin_shape* shape, size_t* bytes);
+ssd_status ssd_lin_attn_bwd_workspace_bytes(const ssd_lin_shape* shape, size_t* bytes);
+
+/* The form over prompts. initial_state and final_state may be NULL (zero; not
+ * wanted). scale: finite and not 0. */
+ssd_status ssd_lin_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                            const int32_t* cu_seqlens, float scale, const float* initial_state, void* o,
+                            float* final_state, const ssd_lin_shape* shape, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
+ * Gradients of <d_o, o> + <dfinal_state, final_state>, with the adjoint
+ * L_t = scale do_t q_t^T + lam L_{t+1} (the last token's also has dfinal_state):
+ *   dq_t = scale D_t^T do_t,  dk_t = L_t^T v_t,  dv_t = L_t k_t (dk and dv summed
+ *   over the heads that share them),  dinitial_state = lam L_first.
+ * d_o [batch, seqlen, nheads, dv] dtype; dq, dk, dv contiguous, of q's, k's
+ * and v's shapes; dfinal_state and dinitial_state may be NULL. Everything is
+ * recomputed from the inputs.
+ */
+ssd_status ssd_lin_attn_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                            const int32_t* cu_seqlens, float scale, const float* initial_state, const void* d_o,
+                            const float* dfinal_state, void* dq, void* dk, void* dv, float* dinitial_state,
+                            const ssd_lin_shape* shape, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token for each of `batch` entries (q [batch, nheads, dk], k, v, o
+ * likewise, contiguous; the shape's rows and num_seqs are ignored), against
+ * state [num_slots, nheads, dv, dk] fp32, updated in place.
+ *   slots [batch] int32 device: the state each entry uses, or NULL: entry i
+ *   uses state i. An entry whose slot lies outside [0, num_slots) is padding:
+ *   its o is 0 and no state is touched. Entries that name one slot are taken
+ *   in the order of the batch, as tokens of one stream.
+ */
+ssd_status ssd_lin_attn_step(float* state, const void* q, const void* k, const void* v, const float* log_decay,
+                             const int32_t* slots, int32_t num_slots, float scale, void* o,
+                             const ssd_lin_shape* shape, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Group norm over channels-last rows, with an activation or a gate. A sample
+ * has `positions` rows of `channels`; a group is channels / groups consecutive
+ * channels over all of a sample's positions:
+ *     u = x (gate none, after) or x silu(z) (gate before)
+ *     xh = (u - mean) / sqrt(var + eps)       center = 0: mean := 0, var := mean(u^2)
+ *     t = xh weight + bias,  a = t or silu(t),  y = a or a silu(z) (gate after).
+ * positions = 1 is the norm of a token: over its heads after the scan (groups
+ * = heads), or, with the gate before and center = 0, over the whole inner row,
+ * as the Mamba-2 block does between the scan and its output projection.
+ *   x, z: rows of dtype x_row, z_row elements apart (0: channels); y, dy, dx,
+ *   dz contiguous; weight, bias [channels] fp32 or NULL (1 and 0); z and dz
+ *   NULL exactly when gate is none; stats [samples][groups][2] fp32: mean (0
+ *   when not centred) and 1 / sqrt(var + eps), may be NULL in the forward call
+ *   and is what the backward call needs of it. eps > 0. dweight and dbias
+ *   [channels] fp32, each may be NULL. Sums are fixed in order: results repeat
+ *   bit for bit.
+ * ------------------------------------------------------------------------- */
+typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1 } ssd_act;
+typedef enum { SSD_GATE_NONE = 0, SSD_GATE_AFTER = 1, SSD_GATE_BEFORE = 2 } ssd_gate;
+typedef struct {
+  int32_t samples;
+  int32_t positions;
+  int32_t channels;
+  int32_t groups;     /* channels % groups == 0                    */
+  int64_t x_row;
+  int64_t z_row;
+  int32_t dtype;      /* ssd_dtype of x, z, y and their gradients  */
+  int32_t act;        /* ssd_act                                   */
+  int32_t gate;       /* ssd_gate                                  */
+  int32_t center;     /* 1: subtract the mean, 0: root mean square */
+} ssd_norm_shape;
+
+ssd_status ssd_group_norm_workspace_bytes(const ssd_norm_shape* shape, int32_t backward, size_t* bytes);
+ssd_status ssd_group_norm(const void* x, const void* z, const float* weight, const float* bias, float eps, void* y,
+                          float* stats, const ssd_norm_shape* shape, void* workspace, size_t workspace_bytes,
+                          void* stream);
+ssd_status ssd_group_norm_bwd(const void* x, const void* z, const float* weight, const float* bias, const float* stats,
+                              const void* dy, void* dx, void* dz, float* dweight, float* dbias,
+                              const ssd_norm_shape* shape, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Pages of a pool of states, [layers][slots][page_bytes]: any per-sequence
+ * state (the states of ssd_step, ssd_step_mamba2 and ssd_lin_attn_step, a
+ * convolution's tail) with the slot as its page. Index lists are device int32;
+ * an entry with an index outside [0, slots) is left out. All layers of a page
+ * move together.
+ *   ssd_pages_copy     pool[dst[i]] = pool[src[i]] for all pairs at once: every
+ *                      source is read as it was before the call, also where
+ *                      src and dst share pages (a fork, a permutation of beams).
+ *                      Of pairs with one destination the last is kept. At most
+ *                      SSD_PAGES_MAX_PAIRS pairs.
+ *   ssd_pages_clear    zeroes pages: the state a new sequence starts from
+ *                      (at most 65535 entries).
+ *   ssd_pages_compact  live [slots] uint8: with `count` live pages, moves the
+ *                      k-th live page at or above count into the k-th hole
+ *                      below it, so that pages 0 .. count - 1 are the live ones.
+ *                      Writes where [slots] int32 (each old page's new index,
+ *                      -1 for the dead) and count [1] int32. Pages from count
+ *                      on keep what they held.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t layers;
+  int32_t slots;
+  int64_t page_bytes;
+} ssd_pages_shape;
+#define SSD_PAGES_MAX_PAIRS 1024
+ssd_status ssd_pages_copy(void* pool, const int32_t* src, const int32_t* dst, int32_t pairs,
+                          const ssd_pages_shape* shape, void* stream);
+ssd_status ssd_pages_clear(void* pool, const int32_t* slots, int32_t count, const ssd_pages_shape* shape, void* stream);
+ssd_status ssd_pages_compact_workspace_bytes(const ssd_pages_shape* shape, size_t* bytes);
+ssd_status ssd_pages_compact(void* pool, const uint8_t* live, int32_t* where, int32_t* count,
+                             const ssd_pages_shape* shape, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -7,6 +7,8 @@ the first call does, and it raises if the library is missing.
 """
 from . import synth  # noqa: F401
 from .binding import (  # noqa: F401
+    PAGES_MAX_PAIRS,
+    LinShape,
     SSDError,
     Shape,
     Workspace,
@@ -21,9 +23,20 @@ from .binding import (  # noqa: F401
     fwd,
     fwd_mamba2,
     fwd_noalloc,
+    group_norm,
+    group_norm_bwd,
     layout,
     lib,
+    lin_attn_bwd,
+    lin_attn_bwd_workspace_bytes,
+    lin_attn_fwd,
+    lin_attn_shape,
+    lin_attn_step,
+    lin_attn_workspace_bytes,
     make_shape,
+    pages_clear,
+    pages_compact,
+    pages_copy,
     set_state_chain,
     state_chain_cooperative,
     chunk_scan_kernel,
@@ -40,4 +53,7 @@ __all__ = [
     "chunk_cumsum", "chunk_state", "state_passing", "chunk_scan",
     "set_state_chain", "state_chain_cooperative", "chunk_scan_kernel", "Workspace", "Shape", "SSDError", "layout", "workspace_bytes", "make_shape", "lib",
     "default_state_block",
+    "lin_attn_fwd", "lin_attn_bwd", "lin_attn_step", "lin_attn_shape", "lin_attn_workspace_bytes",
+    "lin_attn_bwd_workspace_bytes", "LinShape", "group_norm", "group_norm_bwd", "pages_copy", "pages_clear",
+    "pages_compact", "PAGES_MAX_PAIRS",
 ]

@@ -29,7 +29,10 @@ EXPORTS = ("ssd_abi_version", "ssd_status_string", "ssd_default_state_block", "s
            "ssd_fwd_workspace_bytes", "ssd_fwd", "ssd_fwd_ex", "ssd_chunk_cumsum", "ssd_chunk_state",
            "ssd_state_passing", "ssd_chunk_scan", "ssd_step", "ssd_fwd_mamba2", "ssd_step_mamba2",
            "ssd_bwd_workspace_bytes", "ssd_bwd", "ssd_set_state_chain", "ssd_state_chain_cooperative",
-           "ssd_chunk_scan_kernel", "ssd_bwd_mamba2_workspace_bytes", "ssd_bwd_mamba2", "ssd_fwd_noalloc")
+           "ssd_chunk_scan_kernel", "ssd_bwd_mamba2_workspace_bytes", "ssd_bwd_mamba2", "ssd_fwd_noalloc",
+           "ssd_lin_attn_workspace_bytes", "ssd_lin_attn_bwd_workspace_bytes", "ssd_lin_attn_fwd", "ssd_lin_attn_bwd",
+           "ssd_lin_attn_step", "ssd_group_norm_workspace_bytes", "ssd_group_norm", "ssd_group_norm_bwd",
+           "ssd_pages_copy", "ssd_pages_clear", "ssd_pages_compact_workspace_bytes", "ssd_pages_compact")
 
 
 class SSDError(RuntimeError):
@@ -50,6 +53,23 @@ class Layout(ctypes.Structure):
                 ("block_table_offset", ctypes.c_size_t), ("cumsum_offset", ctypes.c_size_t),
                 ("key_cumsum_offset", ctypes.c_size_t), ("block_decay_offset", ctypes.c_size_t), ("block_states_offset", ctypes.c_size_t),
                 ("start_states_offset", ctypes.c_size_t), ("total_bytes", ctypes.c_size_t)]
+
+
+class LinShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32), ("nheads", ctypes.c_int32),
+                ("nkv_heads", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
+                ("num_seqs", ctypes.c_int32), ("dtype", ctypes.c_int32), ("q_row", ctypes.c_int64),
+                ("k_row", ctypes.c_int64), ("v_row", ctypes.c_int64)]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [("samples", ctypes.c_int32), ("positions", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("x_row", ctypes.c_int64), ("z_row", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("gate", ctypes.c_int32), ("center", ctypes.c_int32)]
+
+
+class PagesShape(ctypes.Structure):
+    _fields_ = [("layers", ctypes.c_int32), ("slots", ctypes.c_int32), ("page_bytes", ctypes.c_int64)]
 
 
 def library_path() -> str:
@@ -109,6 +129,21 @@ def lib():
         L.ssd_bwd_mamba2_workspace_bytes.argtypes = [shp, i32, i32, ctypes.POINTER(sz)]
         L.ssd_bwd_mamba2.restype = ctypes.c_int
         L.ssd_bwd_mamba2.argtypes = [vp] * 12 + [i32, i32] + [vp] * 9 + [shp, vp, sz, vp]
+        f32, lin, norm, pages = ctypes.c_float, ctypes.POINTER(LinShape), ctypes.POINTER(NormShape), ctypes.POINTER(PagesShape)
+        for name, args in (("ssd_lin_attn_workspace_bytes", [lin, ctypes.POINTER(sz)]),
+                           ("ssd_lin_attn_bwd_workspace_bytes", [lin, ctypes.POINTER(sz)]),
+                           ("ssd_lin_attn_fwd", [vp] * 5 + [f32] + [vp] * 3 + [lin, vp, sz, vp]),
+                           ("ssd_lin_attn_bwd", [vp] * 5 + [f32] + [vp] * 7 + [lin, vp, sz, vp]),
+                           ("ssd_lin_attn_step", [vp] * 6 + [i32, f32, vp, lin, vp]),
+                           ("ssd_group_norm_workspace_bytes", [norm, i32, ctypes.POINTER(sz)]),
+                           ("ssd_group_norm", [vp] * 4 + [f32] + [vp] * 2 + [norm, vp, sz, vp]),
+                           ("ssd_group_norm_bwd", [vp] * 10 + [norm, vp, sz, vp]),
+                           ("ssd_pages_copy", [vp, vp, vp, i32, pages, vp]),
+                           ("ssd_pages_clear", [vp, vp, i32, pages, vp]),
+                           ("ssd_pages_compact_workspace_bytes", [pages, ctypes.POINTER(sz)]),
+                           ("ssd_pages_compact", [vp] * 4 + [pages, vp, sz, vp])):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = args
         _lib = L
     return _lib
 
@@ -572,3 +607,412 @@ def bwd_mamba2(X: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.
           _ptr(out["dz"]), _ptr(out["dB"]), _ptr(out["dC"]), _ptr(out["dinit"]), ctypes.byref(shape),
           _ptr(workspace), workspace.numel(), _stream(X.device))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Linear attention with one decay a head
+# ---------------------------------------------------------------------------
+
+def _call_on(device: torch.device, fn: str, *args):
+    """_call with `device` current, whichever device the caller's is."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        _call(fn, *args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            _call(fn, *args, _stream(device))
+
+
+def _check_dtype(t, name: str, dim: str, dims: int):
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"{name} must be a {dims}-d tensor {dim}")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} has dtype {t.dtype}; bfloat16 and float32 are supported")
+
+
+def _token_row(t: torch.Tensor, name: str) -> int:
+    """Elements from token to token of [batch, seqlen, heads, d]: heads and their
+    elements lie together, tokens at one distance, rows of the batch follow on."""
+    b, T, H, D = t.shape
+    st = t.stride()
+    if (D > 1 and st[3] != 1) or (H > 1 and st[2] != D):
+        raise ValueError(f"{name} must have its heads contiguous (strides {st})")
+    row = st[1] if T > 1 else (st[0] if b > 1 else H * D)
+    if row < H * D or (b > 1 and st[0] != T * row):
+        raise ValueError(f"{name} must have its tokens at one distance (strides {st})")
+    return row
+
+
+def _expect_device(specs, device, align: int = 16):
+    """Device and alignment of every given (tensor, name)."""
+    for t, name in specs:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.data_ptr() % align:
+            raise ValueError(f"{name} must be {align}-byte aligned")
+
+
+def _lin_shape(q, k, v, log_decay, cu_seqlens):
+    """The shape of a call over prompts, its tensors checked against one another
+    (their devices and alignment come after, with the outputs')."""
+    _check_dtype(q, "q", "[batch, seqlen, nheads, dk]", 4)
+    b, T, H, Dk = q.shape
+    if not isinstance(k, torch.Tensor) or k.dim() != 4 or k.shape[0] != b or k.shape[1] != T or k.shape[3] != Dk:
+        raise ValueError(f"k must be a 4-d tensor [{b}, {T}, nkv_heads, {Dk}]")
+    Hk = k.shape[2]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"nheads {H} must be a multiple of nkv_heads {Hk}")
+    if not isinstance(v, torch.Tensor) or v.dim() != 4 or tuple(v.shape[:3]) != (b, T, Hk):
+        raise ValueError(f"v must be a 4-d tensor [{b}, {T}, {Hk}, dv]")
+    for t, name in ((k, "k"), (v, "v")):
+        if t.dtype != q.dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {q.dtype}")
+    S = 0
+    if cu_seqlens is not None:
+        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be a 1-d tensor of num_seqs + 1 >= 2 entries")
+        if b != 1:
+            raise ValueError("packed sequences (cu_seqlens) need batch 1")
+        S = cu_seqlens.numel() - 1
+    return LinShape(b, T, H, Hk, Dk, v.shape[3], S, _dtype_code(q.dtype), _token_row(q, "q"), _token_row(k, "k"),
+                    _token_row(v, "v"))
+
+
+def _structure(specs):
+    """Shape, dtype and contiguity of every given (tensor, name, shape, dtype)."""
+    for t, name, shape, dtype in specs:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a torch tensor")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _lin_workspace(fn: str, shape: LinShape, workspace, device):
+    n = ctypes.c_size_t(0)
+    _call(fn, ctypes.byref(shape), ctypes.byref(n))
+    if workspace is None or workspace.numel() < n.value:
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
+    return workspace, (0 if workspace is None else workspace.numel())
+
+
+def lin_attn_shape(q, k, v, cu_seqlens=None) -> LinShape:
+    """The shape of a call with these tensors (for lin_attn_workspace_bytes)."""
+    return _lin_shape(q, k, v, None, cu_seqlens)
+
+
+def lin_attn_workspace_bytes(shape: LinShape) -> int:
+    n = ctypes.c_size_t(0)
+    _call("ssd_lin_attn_workspace_bytes", ctypes.byref(shape), ctypes.byref(n))
+    return int(n.value)
+
+
+def lin_attn_bwd_workspace_bytes(shape: LinShape) -> int:
+    n = ctypes.c_size_t(0)
+    _call("ssd_lin_attn_bwd_workspace_bytes", ctypes.byref(shape), ctypes.byref(n))
+    return int(n.value)
+
+
+def lin_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                 cu_seqlens: Optional[torch.Tensor] = None, scale: float = 1.0,
+                 initial_state: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
+                 final_state: Optional[torch.Tensor] = None, want_final: bool = True,
+                 workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with one decay a head over prompts (ssd_lin_attn_fwd). Returns (o, final_state or None).
+
+    q [b, T, H, dk], k [b, T, Hk, dk], v [b, T, Hk, dv] (bf16 or fp32; tokens may lie
+    in wider rows, as slices of one projection do), log_decay [H] fp32 <= 0, states
+    fp32 [rows or sequences, H, dv, dk]. cu_seqlens may hold empty sequences; rows
+    of o that belong to no sequence are left as they were (undefined in an o made here).
+    """
+    shape = _lin_shape(q, k, v, log_decay, cu_seqlens)
+    b, T, H, Dk = q.shape
+    Dv, nseq = v.shape[3], shape.num_seqs or b
+    if log_decay is None:
+        raise ValueError("log_decay is required")
+    st = (nseq, H, Dv, Dk)
+    _structure([(log_decay, "log_decay", (H,), torch.float32), (cu_seqlens, "cu_seqlens", None, torch.int32),
+                (initial_state, "initial_state", st, torch.float32), (o, "o", (b, T, H, Dv), q.dtype),
+                (final_state, "final_state", st, torch.float32), (workspace, "workspace", None, torch.uint8)])
+    _expect_device([(q, "q"), (k, "k"), (v, "v"), (initial_state, "initial_state"), (o, "o"), (final_state, "final_state")],
+                   q.device)
+    _expect_device([(log_decay, "log_decay"), (cu_seqlens, "cu_seqlens")], q.device, 4)
+    _expect_device([(workspace, "workspace")], q.device, 256)
+    workspace, have = _lin_workspace("ssd_lin_attn_workspace_bytes", shape, workspace, q.device)
+    if o is None:
+        o = torch.empty(b, T, H, Dv, dtype=q.dtype, device=q.device)
+    if final_state is None and want_final:
+        final_state = torch.empty(st, dtype=torch.float32, device=q.device)
+    _call_on(q.device, "ssd_lin_attn_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), float(scale),
+             _ptr(initial_state), _ptr(o), _ptr(final_state), ctypes.byref(shape), _ptr(workspace), have)
+    return o, final_state
+
+
+def lin_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, do: torch.Tensor,
+                 cu_seqlens: Optional[torch.Tensor] = None, scale: float = 1.0,
+                 initial_state: Optional[torch.Tensor] = None, dfinal_state: Optional[torch.Tensor] = None,
+                 want_dinit: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Gradients of <do, o> + <dfinal_state, final_state> of lin_attn_fwd with these
+    inputs (ssd_lin_attn_bwd). Returns dict(dq, dk, dv, dinit or None); log_decay is
+    a constant of the layer. Rows that belong to no sequence are undefined."""
+    shape = _lin_shape(q, k, v, log_decay, cu_seqlens)
+    b, T, H, Dk = q.shape
+    Dv, nseq = v.shape[3], shape.num_seqs or b
+    if log_decay is None or do is None:
+        raise ValueError("log_decay and do are required")
+    st = (nseq, H, Dv, Dk)
+    _structure([(log_decay, "log_decay", (H,), torch.float32), (cu_seqlens, "cu_seqlens", None, torch.int32),
+                (do, "do", (b, T, H, Dv), q.dtype), (initial_state, "initial_state", st, torch.float32),
+                (dfinal_state, "dfinal_state", st, torch.float32), (workspace, "workspace", None, torch.uint8)])
+    _expect_device([(q, "q"), (k, "k"), (v, "v"), (do, "do"), (initial_state, "initial_state"),
+                    (dfinal_state, "dfinal_state")], q.device)
+    _expect_device([(log_decay, "log_decay"), (cu_seqlens, "cu_seqlens")], q.device, 4)
+    _expect_device([(workspace, "workspace")], q.device, 256)
+    workspace, have = _lin_workspace("ssd_lin_attn_bwd_workspace_bytes", shape, workspace, q.device)
+    out = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=q.device), dk=torch.empty(k.shape, dtype=q.dtype, device=q.device),
+               dv=torch.empty(v.shape, dtype=q.dtype, device=q.device),
+               dinit=torch.empty(st, dtype=torch.float32, device=q.device) if want_dinit else None)
+    _call_on(q.device, "ssd_lin_attn_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), float(scale),
+             _ptr(initial_state), _ptr(do), _ptr(dfinal_state), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
+             _ptr(out["dinit"]), ctypes.byref(shape), _ptr(workspace), have)
+    return out
+
+
+def lin_attn_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                  slots: Optional[torch.Tensor] = None, scale: float = 1.0,
+                  o: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token for each entry of a batch (ssd_lin_attn_step): updates `state`
+    [num_slots, H, dv, dk] fp32 in place and returns o [b, H, dv].
+
+    q [b, H, dk], k [b, Hk, dk], v [b, Hk, dv]; slots int32 [b]: the state each entry
+    uses (None: entry i uses state i). Slots outside the pool are padding (o = 0);
+    entries that name one slot are taken in the order of the batch.
+    """
+    _check_dtype(q, "q", "[batch, nheads, dk]", 3)
+    b, H, Dk = q.shape
+    if not isinstance(k, torch.Tensor) or k.dim() != 3 or k.shape[0] != b or k.shape[2] != Dk:
+        raise ValueError(f"k must be a 3-d tensor [{b}, nkv_heads, {Dk}]")
+    Hk = k.shape[1]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"nheads {H} must be a multiple of nkv_heads {Hk}")
+    if not isinstance(v, torch.Tensor) or v.dim() != 3 or tuple(v.shape[:2]) != (b, Hk):
+        raise ValueError(f"v must be a 3-d tensor [{b}, {Hk}, dv]")
+    Dv = v.shape[2]
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be a 4-d tensor [num_slots, nheads, dv, dk]")
+    if log_decay is None:
+        raise ValueError("log_decay is required")
+    n = state.shape[0]
+    if slots is None and n < b:
+        raise ValueError(f"state has {n} slots for {b} entries")
+    _structure([(q, "q", None, q.dtype), (k, "k", None, q.dtype), (v, "v", None, q.dtype),
+                (state, "state", (n, H, Dv, Dk), torch.float32), (log_decay, "log_decay", (H,), torch.float32),
+                (slots, "slots", (b,), torch.int32), (o, "o", (b, H, Dv), q.dtype)])
+    _expect_device([(q, "q"), (k, "k"), (v, "v"), (state, "state"), (o, "o")], q.device)
+    _expect_device([(log_decay, "log_decay"), (slots, "slots")], q.device, 4)
+    if o is None:
+        o = torch.empty(b, H, Dv, dtype=q.dtype, device=q.device)
+    shape = LinShape(b, 1, H, Hk, Dk, Dv, 0, _dtype_code(q.dtype), 0, 0, 0)
+    _call_on(q.device, "ssd_lin_attn_step", _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(slots), n,
+             float(scale), _ptr(o), ctypes.byref(shape))
+    return o
+
+
+# ---------------------------------------------------------------------------
+# Group norm over channels-last rows
+# ---------------------------------------------------------------------------
+
+_ACTS = {"none": 0, "silu": 1}
+_GATES = {"after": 1, "before": 2}
+
+
+def _row_pitch(t: torch.Tensor, name: str) -> int:
+    """Elements from row to row of [samples, ..., channels]."""
+    C = t.shape[-1]
+    if C > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have its channels contiguous")
+    pitch, rows = None, 1
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size > 1:
+            if pitch is None:
+                pitch = stride
+            if stride != rows * pitch:
+                raise ValueError(f"{name} must have its rows at one distance")
+        rows *= size
+    pitch = C if pitch is None else pitch
+    if pitch < C:
+        raise ValueError(f"{name} must have its rows at one distance of at least {C} channels")
+    return pitch
+
+
+def _norm_shape(x, groups, z, act, gate, center) -> NormShape:
+    if not isinstance(x, torch.Tensor) or x.dim() < 2:
+        raise ValueError("x must be a tensor [samples, ..., channels]")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"x has dtype {x.dtype}; bfloat16 and float32 are supported")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    if gate not in _GATES:
+        raise ValueError(f"gate must be one of {sorted(_GATES)}")
+    C = x.shape[-1]
+    if groups < 1 or C % groups:
+        raise ValueError(f"channels {C} must be a multiple of groups {groups}")
+    if z is not None:
+        if not isinstance(z, torch.Tensor) or z.shape != x.shape:
+            raise ValueError(f"z must have x's shape {tuple(x.shape)}")
+        if z.dtype != x.dtype:
+            raise ValueError(f"z has dtype {z.dtype}, expected {x.dtype}")
+    positions = 1
+    for d in x.shape[1:-1]:
+        positions *= d
+    return NormShape(x.shape[0], positions, C, int(groups), _row_pitch(x, "x"), 0 if z is None else _row_pitch(z, "z"),
+                     _dtype_code(x.dtype), _ACTS[act], 0 if z is None else _GATES[gate], 1 if center else 0)
+
+
+def _norm_workspace(shape: NormShape, backward: int, workspace, device):
+    n = ctypes.c_size_t(0)
+    _call("ssd_group_norm_workspace_bytes", ctypes.byref(shape), backward, ctypes.byref(n))
+    if workspace is None or workspace.numel() < n.value:
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
+    return workspace, (0 if workspace is None else workspace.numel())
+
+
+def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               z: Optional[torch.Tensor] = None, eps: float = 1e-5, act: str = "none", gate: str = "after",
+               center: bool = True, y: Optional[torch.Tensor] = None, stats: Optional[torch.Tensor] = None,
+               want_stats: bool = True, workspace: Optional[torch.Tensor] = None):
+    """Group norm over channels-last x [samples, ..., channels] (ssd_group_norm). Returns (y, stats or None).
+
+    A group is channels / groups channels over every position of a sample; for the
+    norm of a token pass [tokens, channels]. act ("none", "silu") follows the norm;
+    with z, gate "after" multiplies y by silu(z), "before" the input. weight and
+    bias are fp32 [channels]; center=False takes the root mean square. x and z may
+    have rows in wider rows. stats [samples, groups, 2] fp32 are the mean and
+    1 / sqrt(var + eps) that group_norm_bwd takes.
+    """
+    shape = _norm_shape(x, groups, z, act, gate, center)
+    C, st = shape.channels, (shape.samples, shape.groups, 2)
+    _structure([(weight, "weight", (C,), torch.float32), (bias, "bias", (C,), torch.float32), (y, "y", x.shape, x.dtype),
+                (stats, "stats", st, torch.float32), (workspace, "workspace", None, torch.uint8)])
+    _expect_device([(x, "x"), (z, "z"), (weight, "weight"), (bias, "bias"), (y, "y"), (stats, "stats")], x.device,
+                   x.element_size())
+    _expect_device([(workspace, "workspace")], x.device, 256)
+    workspace, have = _norm_workspace(shape, 0, workspace, x.device)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if stats is None and want_stats:
+        stats = torch.empty(st, dtype=torch.float32, device=x.device)
+    _call_on(x.device, "ssd_group_norm", _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(stats),
+             ctypes.byref(shape), _ptr(workspace), have)
+    return y, stats
+
+
+def group_norm_bwd(x: torch.Tensor, groups: int, stats: torch.Tensor, dy: torch.Tensor,
+                   weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                   z: Optional[torch.Tensor] = None, act: str = "none", gate: str = "after", center: bool = True,
+                   workspace: Optional[torch.Tensor] = None):
+    """Gradients of <dy, y> of group_norm with these inputs and its stats
+    (ssd_group_norm_bwd). Returns dict(dx, dz, dweight, dbias), dz, dweight and
+    dbias None where z, weight or bias is."""
+    shape = _norm_shape(x, groups, z, act, gate, center)
+    C, st = shape.channels, (shape.samples, shape.groups, 2)
+    if stats is None or dy is None:
+        raise ValueError("stats and dy are required")
+    _structure([(weight, "weight", (C,), torch.float32), (bias, "bias", (C,), torch.float32), (dy, "dy", x.shape, x.dtype),
+                (stats, "stats", st, torch.float32), (workspace, "workspace", None, torch.uint8)])
+    _expect_device([(x, "x"), (z, "z"), (dy, "dy"), (weight, "weight"), (bias, "bias"), (stats, "stats")], x.device,
+                   x.element_size())
+    _expect_device([(workspace, "workspace")], x.device, 256)
+    workspace, have = _norm_workspace(shape, 1, workspace, x.device)
+    out = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=x.device),
+               dz=None if z is None else torch.empty(x.shape, dtype=x.dtype, device=x.device),
+               dweight=None if weight is None else torch.empty(C, dtype=torch.float32, device=x.device),
+               dbias=None if bias is None else torch.empty(C, dtype=torch.float32, device=x.device))
+    _call_on(x.device, "ssd_group_norm_bwd", _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(stats), _ptr(dy),
+             _ptr(out["dx"]), _ptr(out["dz"]), _ptr(out["dweight"]), _ptr(out["dbias"]), ctypes.byref(shape),
+             _ptr(workspace), have)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Pages of a pool of states
+# ---------------------------------------------------------------------------
+
+PAGES_MAX_PAIRS = 1024   # SSD_PAGES_MAX_PAIRS
+
+
+def _pages_shape(pool) -> PagesShape:
+    if not isinstance(pool, torch.Tensor) or pool.dim() < 3:
+        raise ValueError("pool must be a tensor [layers, slots, ...]")
+    if not pool.is_contiguous():
+        raise ValueError("pool must be contiguous")
+    if pool.numel() == 0:
+        raise ValueError("pool is empty")
+    return PagesShape(pool.shape[0], pool.shape[1], pool.numel() // (pool.shape[0] * pool.shape[1]) * pool.element_size())
+
+
+def pages_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor) -> torch.Tensor:
+    """pool[:, dst[i]] = pool[:, src[i]] for all pairs at once (ssd_pages_copy), in place:
+    every source is read as it was before the call. pool [layers, slots, ...] of any
+    type; src and dst int32 [n], n <= PAGES_MAX_PAIRS. A pair with an index outside the
+    pool is left out; of pairs with one destination the last is kept."""
+    shape = _pages_shape(pool)
+    if not isinstance(src, torch.Tensor) or src.dim() != 1:
+        raise ValueError("src must be a 1-d tensor")
+    _structure([(src, "src", None, torch.int32), (dst, "dst", src.shape, torch.int32)])
+    if dst is None:
+        raise ValueError("dst is required")
+    _expect_device([(pool, "pool")], pool.device, 1)
+    _expect_device([(src, "src"), (dst, "dst")], pool.device, 4)
+    if src.numel():
+        _call_on(pool.device, "ssd_pages_copy", _ptr(pool), _ptr(src), _ptr(dst), src.numel(), ctypes.byref(shape))
+    return pool
+
+
+def pages_clear(pool: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
+    """Zeroes pool[:, slots] in place (ssd_pages_clear); slots int32 [n], indices outside the pool are left out."""
+    shape = _pages_shape(pool)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a 1-d tensor")
+    _structure([(slots, "slots", None, torch.int32)])
+    _expect_device([(pool, "pool")], pool.device, 1)
+    _expect_device([(slots, "slots")], pool.device, 4)
+    if slots.numel():
+        _call_on(pool.device, "ssd_pages_clear", _ptr(pool), _ptr(slots), slots.numel(), ctypes.byref(shape))
+    return pool
+
+
+def pages_compact(pool: torch.Tensor, live: torch.Tensor, where: Optional[torch.Tensor] = None,
+                  count: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Moves the live pages of pool [layers, slots, ...] into its first `count` slots, in
+    place (ssd_pages_compact). live: uint8 or bool [slots]. Returns (where, count): int32
+    [slots], each old page's new index (-1: dead), and int32 [1]."""
+    shape = _pages_shape(pool)
+    if isinstance(live, torch.Tensor) and live.dtype == torch.bool:
+        live = live.view(torch.uint8)
+    if live is None:
+        raise ValueError("live is required")
+    _structure([(live, "live", (shape.slots,), torch.uint8), (where, "where", (shape.slots,), torch.int32),
+                (count, "count", (1,), torch.int32), (workspace, "workspace", None, torch.uint8)])
+    _expect_device([(pool, "pool"), (live, "live")], pool.device, 1)
+    _expect_device([(where, "where"), (count, "count")], pool.device, 4)
+    _expect_device([(workspace, "workspace")], pool.device, 256)
+    n = ctypes.c_size_t(0)
+    _call("ssd_pages_compact_workspace_bytes", ctypes.byref(shape), ctypes.byref(n))
+    if workspace is None or workspace.numel() < n.value:
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=pool.device)
+    if where is None:
+        where = torch.empty(shape.slots, dtype=torch.int32, device=pool.device)
+    if count is None:
+        count = torch.empty(1, dtype=torch.int32, device=pool.device)
+    _call_on(pool.device, "ssd_pages_compact", _ptr(pool), _ptr(live), _ptr(where), _ptr(count), ctypes.byref(shape),
+             _ptr(workspace), workspace.numel())
+    return where, count

@@ -1,0 +1,748 @@
+// ssd_group_norm.hip -- group norm over channels-last rows with an activation
+// or a gate, forwards and backwards. All of it is bound by the bytes of x, z,
+// y and their gradients.
+//
+// Over the channels of a group and the s positions of a sample:
+//     u = x or x silu(z),  xh = (u - mean) rstd,  t = xh w + bias,
+//     y = a or a silu(z),  a = t or silu(t).
+// With g = dL/dt and M values a group:
+//     du = rstd (g w - mean(g w) - xh mean(g w xh)),  dw = sum g xh,  dbias = sum g.
+//
+// Two forms. One position a sample (s = 1: the norm of a token): a group is
+// one run of channels, held in registers by the lanes that share it, so that
+// x is read once. More positions: the rows are cut into slabs; a first launch
+// leaves each slab's mean and squared deviations per channel, a second joins
+// them per group, a third applies them. Means and deviations are joined about
+// their own means, in 32 bits; nothing subtracts two large sums.
+#include <type_traits>
+
+#include "ssd_device.h"
+#include "ssd_layer.h"
+
+namespace ssd {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_plus(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+// Sum over aligned groups of n lanes (a power of two up to 64); every lane receives it.
+__device__ __forceinline__ float lanes_sum(float v, int n) {
+  if (n > 1) v = dpp_plus<0xB1>(v);
+  if (n > 2) v = dpp_plus<0x4E>(v);
+  if (n > 4) v = dpp_plus<0x141>(v);
+  if (n > 8) v = dpp_plus<0x140>(v);
+  if (n > 16) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  }
+  if (n > 32) {
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  }
+  return v;
+}
+
+// Sum over the `lanes` threads (a power of two) that share a group; above 64
+// through LDS (`red`, one float a wave), every thread of the workgroup taking part.
+__device__ __forceinline__ float group_total(float v, int lanes, float* red) {
+  v = lanes_sum(v, lanes < 64 ? lanes : 64);
+  if (lanes <= 64) return v;
+  const int wave = threadIdx.x >> 6, per = lanes >> 6;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[wave] = v;
+  __syncthreads();
+  float t = 0.f;
+  for (int w = 0; w < per; ++w) t += red[(wave & ~(per - 1)) + w];
+  return t;
+}
+
+__device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + fast_exp2(-v * kLog2e)); }
+// silu'(v) = s (1 + v (1 - s))
+__device__ __forceinline__ float silu_slope(float v, float s) { return s * (1.f + v * (1.f - s)); }
+
+// VEC consecutive elements (8: sixteen-byte pieces; 1: any alignment).
+template <bool BF16, int VEC>
+__device__ __forceinline__ void load_vec(const void* p, long i, float* v) {
+  if constexpr (VEC == 8) {
+    if constexpr (BF16) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = bf16_lo(w[j]);
+        v[2 * j + 1] = bf16_hi(w[j]);
+      }
+    } else {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+      const f32x4 b = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = a[j];
+        v[4 + j] = b[j];
+      }
+    }
+  } else {
+    v[0] = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+  }
+}
+template <bool BF16, int VEC>
+__device__ __forceinline__ void store_vec(void* p, long i, const float* v) {
+  if constexpr (VEC == 8) {
+    if constexpr (BF16) {
+      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) =
+          u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    } else {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(p) + i) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4*>(static_cast<float*>(p) + i + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    }
+  } else {
+    if (BF16) static_cast<uint16_t*>(p)[i] = f32_to_bf16(v[0]);
+    else static_cast<float*>(p)[i] = v[0];
+  }
+}
+// Parameters of VEC channels, `other` where the pointer is null.
+template <int VEC>
+__device__ __forceinline__ void load_par(const float* p, int c, float other, float* v) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) v[j] = p ? p[c + j] : other;
+}
+
+// t -> y for one element; sz = silu(z) where the gate comes after.
+__device__ __forceinline__ float finish(const NormArgs& a, float t, float sz) {
+  const float v = a.silu ? t * sigmoid(t) : t;
+  return a.gate == kGateAfter ? v * sz : v;
+}
+// dL/dt from dL/dy, and the gate's own gradient where it comes after.
+__device__ __forceinline__ float unfinish(const NormArgs& a, float t, float z, float dy, float& dz) {
+  float slope = 1.f, v = t;
+  if (a.silu) {
+    const float s = sigmoid(t);
+    v = t * s;
+    slope = silu_slope(t, s);
+  }
+  if (a.gate == kGateAfter) {
+    const float s = sigmoid(z);
+    dz = dy * v * silu_slope(z, s);
+    dy *= z * s;
+  }
+  return dy * slope;
+}
+
+// ---------------------------------------------------------------- one position a sample
+
+// `lanes` threads share one (row, group), NV pieces of VEC channels each.
+template <bool BF16, int VEC, int NV>
+__global__ __launch_bounds__(kThreads) void norm_row_kernel(NormArgs a, int lanes) {
+  __shared__ float red[kThreads / 64];
+  const int Cg = a.C / a.G, l = threadIdx.x & (lanes - 1);
+  const long item = (long)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
+  const bool on = item < a.n * a.G;
+  const long row = on ? item / a.G : 0;
+  const int g = on ? (int)(item % a.G) : 0;
+  float u[NV][VEC], z[NV][VEC];
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (l + i * lanes) * VEC;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) u[i][j] = z[i][j] = 0.f;
+    if (on && c < Cg) {
+      load_vec<BF16, VEC>(a.x, row * a.x_row + g * Cg + c, u[i]);
+      if (a.gate) load_vec<BF16, VEC>(a.z, row * a.z_row + g * Cg + c, z[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      if (a.gate) z[i][j] *= sigmoid(z[i][j]);
+      if (a.gate == kGateBefore) u[i][j] *= z[i][j];
+      sum += u[i][j];
+    }
+  const float inv = 1.f / (float)Cg;
+  const float mean = a.center ? group_total(sum, lanes, red) * inv : 0.f;
+  float sq = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const bool in = (l + i * lanes) * VEC < Cg;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      u[i][j] = in ? u[i][j] - mean : 0.f;
+      sq += u[i][j] * u[i][j];
+    }
+  }
+  const float rstd = 1.f / sqrtf(group_total(sq, lanes, red) * inv + a.eps);
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (l + i * lanes) * VEC;
+    if (c >= Cg) break;
+    float w[VEC], b[VEC];
+    load_par<VEC>(a.w, g * Cg + c, 1.f, w);
+    load_par<VEC>(a.bias, g * Cg + c, 0.f, b);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) u[i][j] = finish(a, u[i][j] * rstd * w[j] + b[j], z[i][j]);
+    store_vec<BF16, VEC>(a.y, row * a.C + g * Cg + c, u[i]);
+  }
+  if (a.stats && l == 0) {
+    a.stats[2 * (row * a.G + g)] = mean;
+    a.stats[2 * (row * a.G + g) + 1] = rstd;
+  }
+}
+
+// Backwards: `lanes` threads keep one group and walk rows, so that dw and
+// dbias of their channels stay in registers; each leaves one row of partial
+// sums in ws ([part][2][C]).
+template <bool BF16, int VEC, int NV>
+__global__ __launch_bounds__(kThreads) void norm_row_bwd_kernel(NormArgs a, int lanes, int groups, int rows, int row_blocks) {
+  __shared__ float red[kThreads / 64];
+  const int Cg = a.C / a.G, l = threadIdx.x & (lanes - 1), worker = threadIdx.x / lanes;
+  const int tiles = (a.G + groups - 1) / groups;
+  const int g = (int)(blockIdx.x % tiles) * groups + worker % groups;
+  const int part = (int)(blockIdx.x / tiles) * rows + worker / groups;
+  const int parts = row_blocks * rows;
+  const bool on = worker < groups * rows && g < a.G;
+  const int c0 = (on ? g : 0) * Cg;
+  const float inv = 1.f / (float)Cg;
+  float dw[NV][VEC], db[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) dw[i][j] = db[i][j] = 0.f;
+  // Every thread of the workgroup makes the same number of rounds (the sums meet at barriers).
+  for (long r0 = 0; r0 < a.n; r0 += parts) {
+    const long row = r0 + part;
+    const bool live = on && row < a.n;
+    float xh[NV][VEC], g1[NV][VEC], zz[NV][VEC], gu[NV][VEC];
+    float mean = 0.f, rstd = 0.f;
+    if (live) {
+      mean = a.stats[2 * (row * a.G + g)];
+      rstd = a.stats[2 * (row * a.G + g) + 1];
+    }
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (l + i * lanes) * VEC;
+      float x[VEC], w[VEC], b[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) x[j] = zz[i][j] = g1[i][j] = 0.f;
+      const bool in = live && c < Cg;
+      if (in) {
+        load_vec<BF16, VEC>(a.x, row * a.x_row + c0 + c, x);
+        if (a.gate) load_vec<BF16, VEC>(a.z, row * a.z_row + c0 + c, zz[i]);
+        load_vec<BF16, VEC>(a.dy, row * a.C + c0 + c, g1[i]);
+      }
+      const int cp = c < Cg ? c : 0;
+      load_par<VEC>(a.w, c0 + cp, 1.f, w);
+      load_par<VEC>(a.bias, c0 + cp, 0.f, b);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float u = a.gate == kGateBefore ? x[j] * zz[i][j] * sigmoid(zz[i][j]) : x[j];
+        gu[i][j] = x[j];
+        xh[i][j] = in ? (u - mean) * rstd : 0.f;
+        float dz = 0.f;
+        const float gt = unfinish(a, xh[i][j] * w[j] + b[j], zz[i][j], g1[i][j], dz);
+        if (a.gate == kGateAfter) gu[i][j] = dz;
+        dw[i][j] += gt * xh[i][j];
+        db[i][j] += gt;
+        g1[i][j] = gt * w[j];
+        s0 += g1[i][j];
+        s1 += g1[i][j] * xh[i][j];
+      }
+    }
+    const float m0 = a.center ? group_total(s0, lanes, red) * inv : 0.f;
+    const float m1 = group_total(s1, lanes, red) * inv;
+    if (!live) continue;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (l + i * lanes) * VEC;
+      if (c >= Cg) break;
+      float dx[VEC], dz[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float du = rstd * (g1[i][j] - m0 - xh[i][j] * m1);
+        dx[j] = du;
+        dz[j] = gu[i][j];
+        if (a.gate == kGateBefore) {
+          const float s = sigmoid(zz[i][j]);
+          dz[j] = du * gu[i][j] * silu_slope(zz[i][j], s);
+          dx[j] = du * zz[i][j] * s;
+        }
+      }
+      store_vec<BF16, VEC>(a.dx, row * a.C + c0 + c, dx);
+      if (a.gate) store_vec<BF16, VEC>(a.dz, row * a.C + c0 + c, dz);
+    }
+  }
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (l + i * lanes) * VEC;
+    if (c >= Cg) break;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      a.ws[((long)part * 2) * a.C + c0 + c + j] = dw[i][j];
+      a.ws[((long)part * 2 + 1) * a.C + c0 + c + j] = db[i][j];
+    }
+  }
+}
+
+// dw[c] = sum over parts of ws[part][0][c], dbias likewise: 32 channels by 8
+// lanes of parts a workgroup, joined in a fixed order.
+__global__ __launch_bounds__(kThreads) void norm_sum_parts_kernel(const float* __restrict__ ws, int parts, int C,
+                                                                  float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float acc[2][8][33];
+  const int cl = threadIdx.x & 31, pl = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + cl;
+  float s0 = 0.f, s1 = 0.f;
+  if (c < C)
+    for (int p = pl; p < parts; p += 8) {
+      s0 += ws[((long)p * 2) * C + c];
+      s1 += ws[((long)p * 2 + 1) * C + c];
+    }
+  acc[0][pl][cl] = s0;
+  acc[1][pl][cl] = s1;
+  __syncthreads();
+  if (pl == 0 && c < C) {
+    for (int p = 1; p < 8; ++p) {
+      s0 += acc[0][p][cl];
+      s1 += acc[1][p][cl];
+    }
+    if (dw) dw[c] = s0;
+    if (db) db[c] = s1;
+  }
+}
+
+// ---------------------------------------------------------------- several positions a sample
+
+// A workgroup takes `cols` columns of VEC channels (a power of two of threads)
+// by kThreads / cols rows at a time, kSlabRounds rounds: one slab.
+constexpr int kSlabRounds = 8;
+
+struct Slabs {
+  int cols, rows, tiles;   // thread columns, rows a round, column tiles
+  long count;              // slabs a sample
+};
+inline Slabs slabs_of(long s, int C, int vec) {
+  Slabs b;
+  const int pieces = (C + vec - 1) / vec;
+  b.cols = 1;
+  while (b.cols < pieces && b.cols < 64) b.cols *= 2;
+  b.rows = kThreads / b.cols;
+  b.tiles = (pieces + b.cols - 1) / b.cols;
+  b.count = (s + (long)b.rows * kSlabRounds - 1) / ((long)b.rows * kSlabRounds);
+  return b;
+}
+
+template <bool BF16, int VEC>
+__device__ __forceinline__ void load_u(const NormArgs& a, long row, int c, float* u) {
+  load_vec<BF16, VEC>(a.x, row * a.x_row + c, u);
+  if (a.gate == kGateBefore) {
+    float z[VEC];
+    load_vec<BF16, VEC>(a.z, row * a.z_row + c, z);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) u[j] *= z[j] * sigmoid(z[j]);
+  }
+}
+
+// Sum of v[VEC] over the workgroup's thread rows, in row order; every thread receives its column's.
+template <int VEC>
+__device__ __forceinline__ void rows_total(float* v, int cols, int rows, float* lds) {
+  const int tx = threadIdx.x % cols, ty = threadIdx.x / cols;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) lds[(ty * VEC + j) * cols + tx] = v[j];
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    float t = 0.f;
+    for (int r = 0; r < rows; ++r) t += lds[(r * VEC + j) * cols + tx];
+    v[j] = t;
+  }
+}
+
+// ws [n][slab][2][C]: each slab's mean and squared deviations from it, per channel.
+template <bool BF16, int VEC>
+__global__ __launch_bounds__(kThreads) void norm_slab_kernel(NormArgs a, Slabs b) {
+  __shared__ float lds[kThreads * VEC];
+  const int tile = (int)(blockIdx.x % b.tiles);
+  const long slab = blockIdx.x / b.tiles % b.count, n = blockIdx.x / b.tiles / b.count;
+  const int tx = threadIdx.x % b.cols, ty = threadIdx.x / b.cols;
+  const int c = (tile * b.cols + tx) * VEC;
+  const long r0 = slab * b.rows * kSlabRounds;
+  const long have = min((long)b.rows * kSlabRounds, a.s - r0);
+  float u[kSlabRounds][VEC], sum[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) sum[j] = 0.f;
+#pragma unroll
+  for (int k = 0; k < kSlabRounds; ++k) {
+    const long r = ty + (long)k * b.rows;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) u[k][j] = 0.f;
+    if (c < a.C && r < have) load_u<BF16, VEC>(a, n * a.s + r0 + r, c, u[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kSlabRounds; ++k)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) sum[j] += u[k][j];
+  rows_total<VEC>(sum, b.cols, b.rows, lds);
+  float dev[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    sum[j] /= (float)have;
+    dev[j] = 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < kSlabRounds; ++k)
+    if (ty + (long)k * b.rows < have)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) dev[j] += (u[k][j] - sum[j]) * (u[k][j] - sum[j]);
+  rows_total<VEC>(dev, b.cols, b.rows, lds);
+  if (ty == 0 && c < a.C) {
+    float* out = a.ws + (n * b.count + slab) * 2 * a.C + c;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      out[j] = sum[j];
+      out[a.C + j] = dev[j];
+    }
+  }
+}
+
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = lanes_sum(v, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float t = 0.f;
+  for (int w = 0; w < kThreads / 64; ++w) t += red[w];
+  return t;
+}
+
+// One group of one sample: joins its slabs and channels about their common mean.
+__global__ __launch_bounds__(kThreads) void norm_join_kernel(NormArgs a, long slabs, long slab_rows, float* stats) {
+  __shared__ float red[kThreads / 64];
+  const int Cg = a.C / a.G;
+  const long n = blockIdx.x / a.G;
+  const int g = (int)(blockIdx.x % a.G);
+  const float* ws = a.ws + n * slabs * 2 * a.C + (long)g * Cg;
+  const long items = slabs * Cg;
+  float s = 0.f;
+  for (long i = threadIdx.x; i < items; i += kThreads) {
+    const long slab = i / Cg;
+    const float rows = (float)min(slab_rows, a.s - slab * slab_rows);
+    s += ws[slab * 2 * a.C + i % Cg] * (rows / (float)a.s);
+  }
+  const float mean = block_sum(s, red) / (float)Cg;
+  float d = 0.f;
+  for (long i = threadIdx.x; i < items; i += kThreads) {
+    const long slab = i / Cg;
+    const float rows = (float)min(slab_rows, a.s - slab * slab_rows);
+    const float off = ws[slab * 2 * a.C + i % Cg] - mean;
+    d += ws[(slab * 2 + 1) * a.C + i % Cg] + rows * off * off;
+  }
+  float var = block_sum(d, red) / ((float)a.s * (float)Cg);
+  if (!a.center) var += mean * mean;
+  if (threadIdx.x == 0) {
+    stats[2 * blockIdx.x] = a.center ? mean : 0.f;
+    stats[2 * blockIdx.x + 1] = 1.f / sqrtf(var + a.eps);
+  }
+}
+
+template <bool BF16, int VEC>
+__global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a, Slabs b, const float* __restrict__ stats) {
+  const int tile = (int)(blockIdx.x % b.tiles);
+  const long slab = blockIdx.x / b.tiles % b.count, n = blockIdx.x / b.tiles / b.count;
+  const int tx = threadIdx.x % b.cols, ty = threadIdx.x / b.cols;
+  const int c = (tile * b.cols + tx) * VEC, Cg = a.C / a.G;
+  if (c >= a.C) return;
+  float mean[VEC], rstd[VEC], w[VEC], bias[VEC];
+  load_par<VEC>(a.w, c, 1.f, w);
+  load_par<VEC>(a.bias, c, 0.f, bias);
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    const long g = n * a.G + (c + j) / Cg;
+    mean[j] = stats[2 * g];
+    rstd[j] = stats[2 * g + 1];
+  }
+#pragma unroll
+  for (int k = 0; k < kSlabRounds; ++k) {
+    const long r = slab * b.rows * kSlabRounds + ty + (long)k * b.rows;
+    if (r >= a.s) break;
+    const long row = n * a.s + r;
+    float u[VEC], z[VEC];
+    load_vec<BF16, VEC>(a.x, row * a.x_row + c, u);
+    if (a.gate) load_vec<BF16, VEC>(a.z, row * a.z_row + c, z);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const float sz = a.gate ? z[j] * sigmoid(z[j]) : 0.f;
+      const float v = a.gate == kGateBefore ? u[j] * sz : u[j];
+      u[j] = finish(a, (v - mean[j]) * rstd[j] * w[j] + bias[j], sz);
+    }
+    store_vec<BF16, VEC>(a.y, row * a.C + c, u);
+  }
+}
+
+// Backwards, first launch: ws [n][slab][2][C]: each slab's sums of g xh and g per channel.
+template <bool BF16, int VEC>
+__global__ __launch_bounds__(kThreads) void norm_slab_bwd_kernel(NormArgs a, Slabs b) {
+  __shared__ float lds[kThreads * VEC];
+  const int tile = (int)(blockIdx.x % b.tiles);
+  const long slab = blockIdx.x / b.tiles % b.count, n = blockIdx.x / b.tiles / b.count;
+  const int tx = threadIdx.x % b.cols, ty = threadIdx.x / b.cols;
+  const int c = (tile * b.cols + tx) * VEC, Cg = a.C / a.G;
+  float mean[VEC], rstd[VEC], w[VEC], bias[VEC], s0[VEC], s1[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) s0[j] = s1[j] = 0.f;
+  if (c < a.C) {
+    load_par<VEC>(a.w, c, 1.f, w);
+    load_par<VEC>(a.bias, c, 0.f, bias);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const long g = n * a.G + (c + j) / Cg;
+      mean[j] = a.stats[2 * g];
+      rstd[j] = a.stats[2 * g + 1];
+    }
+#pragma unroll
+    for (int k = 0; k < kSlabRounds; ++k) {
+      const long r = slab * b.rows * kSlabRounds + ty + (long)k * b.rows;
+      if (r >= a.s) break;
+      const long row = n * a.s + r;
+      float u[VEC], z[VEC], dy[VEC];
+      load_vec<BF16, VEC>(a.x, row * a.x_row + c, u);
+      if (a.gate) load_vec<BF16, VEC>(a.z, row * a.z_row + c, z);
+      load_vec<BF16, VEC>(a.dy, row * a.C + c, dy);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float v = a.gate == kGateBefore ? u[j] * z[j] * sigmoid(z[j]) : u[j];
+        const float xh = (v - mean[j]) * rstd[j];
+        float dz;
+        const float gt = unfinish(a, xh * w[j] + bias[j], a.gate ? z[j] : 0.f, dy[j], dz);
+        s0[j] += gt * xh;
+        s1[j] += gt;
+      }
+    }
+  }
+  rows_total<VEC>(s0, b.cols, b.rows, lds);
+  rows_total<VEC>(s1, b.cols, b.rows, lds);
+  if (ty == 0 && c < a.C) {
+    float* out = a.ws + (n * b.count + slab) * 2 * a.C + c;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      out[j] = s0[j];
+      out[a.C + j] = s1[j];
+    }
+  }
+}
+
+// means[n][G][2]: a group's means of g w xh and of g w.
+__global__ __launch_bounds__(kThreads) void norm_join_bwd_kernel(NormArgs a, long slabs, float* means) {
+  __shared__ float red[kThreads / 64];
+  const int Cg = a.C / a.G;
+  const long n = blockIdx.x / a.G;
+  const int g = (int)(blockIdx.x % a.G);
+  const float* ws = a.ws + n * slabs * 2 * a.C + (long)g * Cg;
+  float s0 = 0.f, s1 = 0.f;
+  for (long i = threadIdx.x; i < slabs * Cg; i += kThreads) {
+    const int c = (int)(i % Cg);
+    const float w = a.w ? a.w[g * Cg + c] : 1.f;
+    s0 += w * ws[i / Cg * 2 * a.C + c];
+    s1 += w * ws[(i / Cg * 2 + 1) * a.C + c];
+  }
+  const float inv = 1.f / ((float)a.s * (float)Cg);
+  const float t0 = block_sum(s0, red) * inv, t1 = block_sum(s1, red) * inv;
+  if (threadIdx.x == 0) {
+    means[2 * blockIdx.x] = t0;
+    means[2 * blockIdx.x + 1] = a.center ? t1 : 0.f;
+  }
+}
+
+template <bool BF16, int VEC>
+__global__ __launch_bounds__(kThreads) void norm_apply_bwd_kernel(NormArgs a, Slabs b, const float* __restrict__ means) {
+  const int tile = (int)(blockIdx.x % b.tiles);
+  const long slab = blockIdx.x / b.tiles % b.count, n = blockIdx.x / b.tiles / b.count;
+  const int tx = threadIdx.x % b.cols, ty = threadIdx.x / b.cols;
+  const int c = (tile * b.cols + tx) * VEC, Cg = a.C / a.G;
+  if (c >= a.C) return;
+  float mean[VEC], rstd[VEC], w[VEC], bias[VEC], m0[VEC], m1[VEC];
+  load_par<VEC>(a.w, c, 1.f, w);
+  load_par<VEC>(a.bias, c, 0.f, bias);
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    const long g = n * a.G + (c + j) / Cg;
+    mean[j] = a.stats[2 * g];
+    rstd[j] = a.stats[2 * g + 1];
+    m1[j] = means[2 * g];
+    m0[j] = means[2 * g + 1];
+  }
+#pragma unroll
+  for (int k = 0; k < kSlabRounds; ++k) {
+    const long r = slab * b.rows * kSlabRounds + ty + (long)k * b.rows;
+    if (r >= a.s) break;
+    const long row = n * a.s + r;
+    float x[VEC], z[VEC], dy[VEC], dx[VEC], dzv[VEC];
+    load_vec<BF16, VEC>(a.x, row * a.x_row + c, x);
+    if (a.gate) load_vec<BF16, VEC>(a.z, row * a.z_row + c, z);
+    load_vec<BF16, VEC>(a.dy, row * a.C + c, dy);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const float sg = a.gate == kGateBefore ? sigmoid(z[j]) : 0.f;
+      const float u = a.gate == kGateBefore ? x[j] * z[j] * sg : x[j];
+      const float xh = (u - mean[j]) * rstd[j];
+      dzv[j] = 0.f;
+      const float gt = unfinish(a, xh * w[j] + bias[j], a.gate ? z[j] : 0.f, dy[j], dzv[j]);
+      dx[j] = rstd[j] * (gt * w[j] - m0[j] - xh * m1[j]);
+      if (a.gate == kGateBefore) {
+        dzv[j] = dx[j] * x[j] * silu_slope(z[j], sg);
+        dx[j] *= z[j] * sg;
+      }
+    }
+    store_vec<BF16, VEC>(a.dx, row * a.C + c, dx);
+    if (a.gate) store_vec<BF16, VEC>(a.dz, row * a.C + c, dzv);
+  }
+}
+
+// Whether (and how) a group fits the registers of the threads that share it.
+struct RowPlan {
+  int vec, nv, lanes;
+};
+bool row_plan(const NormArgs& a, RowPlan* p) {
+  if (a.s != 1) return false;
+  const int Cg = a.C / a.G;
+  p->vec = a.vec && Cg % 8 == 0 ? 8 : 1;
+  const int pieces = Cg / p->vec;
+  p->lanes = 1;
+  while (p->lanes < pieces && p->lanes < kThreads) p->lanes *= 2;
+  p->nv = (pieces + p->lanes - 1) / p->lanes;
+  if (p->nv > 4) return false;
+  if (p->nv == 3) p->nv = 4;
+  return true;
+}
+
+// Rows of partial sums of the one-position backward pass: enough for four
+// workgroups a CU, no more than there are rows.
+struct RowParts {
+  int groups, rows, tiles, blocks;
+};
+RowParts row_parts(const NormArgs& a, int lanes) {
+  RowParts r;
+  const int workers = kThreads / lanes;
+  r.groups = a.G < workers ? a.G : workers;
+  r.rows = workers / r.groups;
+  r.tiles = (a.G + r.groups - 1) / r.groups;
+  long blocks = 1024 / r.tiles;
+  const long most = (a.n + r.rows - 1) / r.rows;
+  if (blocks > most) blocks = most;
+  if (blocks * r.rows > 1024) blocks = 1024 / r.rows;
+  r.blocks = blocks < 1 ? 1 : (int)blocks;
+  return r;
+}
+
+
+}  // namespace
+
+size_t norm_ws_floats(long n, long s, int C, int G, bool backward) {
+  // The slab form with the narrowest pieces has the most slabs; the
+  // one-position backward pass leaves at most 1024 rows of partial sums.
+  size_t most = 0;
+  for (int vec : {1, 8}) {
+    const Slabs b = slabs_of(s, C, vec);
+    const size_t f = (size_t)n * b.count * 2 * C + (size_t)n * G * 2;
+    if (f > most) most = f;
+  }
+  if (s == 1) {
+    const size_t rows = n < 1024 ? (size_t)n : 1024;
+    const size_t parts = backward ? 2 * (rows + 256) * C : 0;
+    // a group that fits no registers takes the slab form
+    if (C / G <= 1024) return parts;
+    if (parts > most) most = parts;
+  }
+  return most;
+}
+
+namespace {
+
+template <bool BF16, int VEC>
+void row_launch(const NormArgs& a, const RowPlan& p, hipStream_t stream) {
+  const long workers = kThreads / p.lanes;
+  const dim3 grid((unsigned)((a.n * a.G + workers - 1) / workers));
+  if (p.nv == 1) hipLaunchKernelGGL((norm_row_kernel<BF16, VEC, 1>), grid, dim3(kThreads), 0, stream, a, p.lanes);
+  else if (p.nv == 2) hipLaunchKernelGGL((norm_row_kernel<BF16, VEC, 2>), grid, dim3(kThreads), 0, stream, a, p.lanes);
+  else hipLaunchKernelGGL((norm_row_kernel<BF16, VEC, 4>), grid, dim3(kThreads), 0, stream, a, p.lanes);
+}
+
+template <bool BF16, int VEC>
+void row_bwd_launch(const NormArgs& a, const RowPlan& p, hipStream_t stream) {
+  const RowParts r = row_parts(a, p.lanes);
+  const dim3 grid((unsigned)(r.tiles * r.blocks)), block(kThreads);
+  if (p.nv == 1)
+    hipLaunchKernelGGL((norm_row_bwd_kernel<BF16, VEC, 1>), grid, block, 0, stream, a, p.lanes, r.groups, r.rows, r.blocks);
+  else if (p.nv == 2)
+    hipLaunchKernelGGL((norm_row_bwd_kernel<BF16, VEC, 2>), grid, block, 0, stream, a, p.lanes, r.groups, r.rows, r.blocks);
+  else
+    hipLaunchKernelGGL((norm_row_bwd_kernel<BF16, VEC, 4>), grid, block, 0, stream, a, p.lanes, r.groups, r.rows, r.blocks);
+  if (a.dw || a.db)
+    hipLaunchKernelGGL(norm_sum_parts_kernel, dim3((unsigned)((a.C + 31) / 32)), block, 0, stream, a.ws, r.rows * r.blocks,
+                       a.C, a.dw, a.db);
+}
+
+template <bool BF16, int VEC>
+void slab_launch(const NormArgs& a, hipStream_t stream) {
+  const Slabs b = slabs_of(a.s, a.C, VEC);
+  const dim3 grid((unsigned)(a.n * b.count * b.tiles)), groups((unsigned)(a.n * a.G)), block(kThreads);
+  float* stats = a.stats ? a.stats : a.ws + a.n * b.count * 2 * a.C;
+  hipLaunchKernelGGL((norm_slab_kernel<BF16, VEC>), grid, block, 0, stream, a, b);
+  hipLaunchKernelGGL(norm_join_kernel, groups, block, 0, stream, a, b.count, (long)b.rows * kSlabRounds, stats);
+  hipLaunchKernelGGL((norm_apply_kernel<BF16, VEC>), grid, block, 0, stream, a, b, (const float*)stats);
+}
+
+template <bool BF16, int VEC>
+void slab_bwd_launch(const NormArgs& a, hipStream_t stream) {
+  const Slabs b = slabs_of(a.s, a.C, VEC);
+  const dim3 grid((unsigned)(a.n * b.count * b.tiles)), groups((unsigned)(a.n * a.G)), block(kThreads);
+  float* means = a.ws + a.n * b.count * 2 * a.C;
+  hipLaunchKernelGGL((norm_slab_bwd_kernel<BF16, VEC>), grid, block, 0, stream, a, b);
+  hipLaunchKernelGGL(norm_join_bwd_kernel, groups, block, 0, stream, a, b.count, means);
+  hipLaunchKernelGGL((norm_apply_bwd_kernel<BF16, VEC>), grid, block, 0, stream, a, b, (const float*)means);
+  if (a.dw || a.db)
+    hipLaunchKernelGGL(norm_sum_parts_kernel, dim3((unsigned)((a.C + 31) / 32)), block, 0, stream, a.ws,
+                       (int)(a.n * b.count), a.C, a.dw, a.db);
+}
+
+template <typename F>
+void by_type(bool bf16, bool vec, F f) {
+  using T = std::true_type;
+  using N = std::false_type;
+  if (bf16) {
+    if (vec) f(T{}, std::integral_constant<int, 8>{});
+    else f(T{}, std::integral_constant<int, 1>{});
+  } else {
+    if (vec) f(N{}, std::integral_constant<int, 8>{});
+    else f(N{}, std::integral_constant<int, 1>{});
+  }
+}
+
+}  // namespace
+
+hipError_t launch_group_norm(const NormArgs& a, hipStream_t stream) {
+  RowPlan p;
+  const bool row = row_plan(a, &p);
+  by_type(a.bf16, row ? p.vec == 8 : a.vec, [&](auto bf, auto vec) {
+    if (row) row_launch<decltype(bf)::value, decltype(vec)::value>(a, p, stream);
+    else slab_launch<decltype(bf)::value, decltype(vec)::value>(a, stream);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_group_norm_bwd(const NormArgs& a, hipStream_t stream) {
+  RowPlan p;
+  const bool row = row_plan(a, &p);
+  by_type(a.bf16, row ? p.vec == 8 : a.vec, [&](auto bf, auto vec) {
+    if (row) row_bwd_launch<decltype(bf)::value, decltype(vec)::value>(a, p, stream);
+    else slab_bwd_launch<decltype(bf)::value, decltype(vec)::value>(a, stream);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace ssd

@@ -1,0 +1,443 @@
+// ssd_layer_api.cpp -- the C ABI (include/ssd.h) of the layer operators around
+// the scan: linear attention with one decay a head, the group norm with its
+// gate, and the pages of a state pool. As in ssd_api.cpp, every argument is
+// checked on the host before any HIP call; nothing is allocated, synchronised
+// or thrown.
+#include <hip/hip_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "ssd.h"
+#include "ssd_layer.h"
+#include "ssd_lin_attn.h"
+
+namespace {
+
+ssd_status hip_status(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+bool scale_ok(float s) { return std::isfinite(s) && s != 0.f; }
+
+// ---------------------------------------------------------------- linear attention
+
+struct LinDims {
+  int64_t q_row, k_row, v_row, tokens, nseq;
+  int esz;
+};
+
+ssd_status check_heads(const ssd_lin_shape* s) {
+  if (s->nheads < 1 || s->nkv_heads < 1 || s->dk < 1 || s->dv < 1 || s->batch < 1) return SSD_ERR_INVALID_ARGUMENT;
+  if (s->nheads % s->nkv_heads) return SSD_ERR_INVALID_ARGUMENT;
+  if (s->dtype != SSD_DTYPE_F32 && s->dtype != SSD_DTYPE_BF16) return SSD_ERR_UNSUPPORTED;
+  if (s->dk % 8 || s->dv % 8 || s->dk > 256 || s->dv > 256) return SSD_ERR_UNSUPPORTED;
+  if (s->nheads > 65535 || s->batch > 65535) return SSD_ERR_UNSUPPORTED;
+  return SSD_OK;
+}
+
+ssd_status check_lin(const ssd_lin_shape* s, LinDims* d) {
+  if (!s) return SSD_ERR_INVALID_ARGUMENT;
+  ssd_status st = check_heads(s);
+  if (st != SSD_OK) return st;
+  if (s->seqlen < 1 || s->num_seqs < 0) return SSD_ERR_INVALID_ARGUMENT;
+  if (s->num_seqs > 0 && s->batch != 1) return SSD_ERR_INVALID_ARGUMENT;
+  if (s->num_seqs > 65535) return SSD_ERR_UNSUPPORTED;
+  d->esz = s->dtype == SSD_DTYPE_BF16 ? 2 : 4;
+  d->q_row = s->q_row ? s->q_row : (int64_t)s->nheads * s->dk;
+  d->k_row = s->k_row ? s->k_row : (int64_t)s->nkv_heads * s->dk;
+  d->v_row = s->v_row ? s->v_row : (int64_t)s->nkv_heads * s->dv;
+  if (d->q_row < (int64_t)s->nheads * s->dk || d->k_row < (int64_t)s->nkv_heads * s->dk ||
+      d->v_row < (int64_t)s->nkv_heads * s->dv)
+    return SSD_ERR_INVALID_ARGUMENT;
+  // rows start on 16-byte boundaries
+  if ((d->q_row | d->k_row | d->v_row) * d->esz % 16) return SSD_ERR_UNSUPPORTED;
+  // 64 rows are addressed as one buffer range of fewer than 2^31 bytes
+  const int64_t most = INT32_MAX / 64 / 4;
+  if (d->q_row > most || d->k_row > most || d->v_row > most || (int64_t)s->nheads * (s->dk > s->dv ? s->dk : s->dv) > most)
+    return SSD_ERR_UNSUPPORTED;
+  d->tokens = (int64_t)s->batch * s->seqlen;
+  if (d->tokens > INT32_MAX / 2) return SSD_ERR_UNSUPPORTED;
+  d->nseq = s->num_seqs > 0 ? s->num_seqs : s->batch;
+  return SSD_OK;
+}
+
+// The blocks of one scan with contraction size dk and value size dv.
+struct LinPlan {
+  int L;
+  int64_t spr, slots;
+  size_t state_bytes;  // 0: no sequence is cut
+};
+ssd_status lin_plan(const ssd_lin_shape* s, int dk, int dv, LinPlan* p) {
+  p->L = ssd::lin_block_tokens(s->batch, s->seqlen, s->num_seqs, s->nheads, dk, dv, s->dtype == SSD_DTYPE_BF16);
+  p->spr = ssd::lin_slots_per_row(s->seqlen, s->num_seqs, p->L);
+  p->slots = s->num_seqs > 0 ? p->spr : p->spr * s->batch;
+  if (p->slots * s->nheads > INT32_MAX / 64) return SSD_ERR_UNSUPPORTED;  // workgroups of one launch
+  p->state_bytes = p->L >= s->seqlen ? 0 : (size_t)p->slots * s->nheads * dk * dv * 4;
+  return SSD_OK;
+}
+
+struct LinBwdLayout {
+  LinPlan dq, dv, dk;
+  size_t st_dq, st_dv, st_dk, part_k, part_v, total;
+};
+ssd_status lin_bwd_layout(const ssd_lin_shape* s, LinBwdLayout* L) {
+  LinDims d;
+  ssd_status st = check_lin(s, &d);
+  if (st != SSD_OK) return st;
+  if ((st = lin_plan(s, s->dv, s->dk, &L->dq)) != SSD_OK) return st;
+  if ((st = lin_plan(s, s->dk, s->dv, &L->dv)) != SSD_OK) return st;
+  if ((st = lin_plan(s, s->dv, s->dk, &L->dk)) != SSD_OK) return st;
+  size_t off = 0;
+  auto take = [&](size_t b) {
+    const size_t o = off;
+    off = align256(off + b);
+    return o;
+  };
+  L->st_dq = take(L->dq.state_bytes);
+  L->st_dv = take(L->dv.state_bytes);
+  L->st_dk = take(L->dk.state_bytes);
+  const bool shared = s->nheads != s->nkv_heads;
+  L->part_k = take(shared ? (size_t)d.tokens * s->nheads * s->dk * 4 : 0);
+  L->part_v = take(shared ? (size_t)d.tokens * s->nheads * s->dv * 4 : 0);
+  L->total = off;
+  return SSD_OK;
+}
+
+ssd::LinScan base_scan(const ssd_lin_shape* s, const float* ld, const int32_t* cu, float scale) {
+  ssd::LinScan a;
+  a.ld = ld;
+  a.scale = scale;
+  a.cu = cu;
+  a.S = s->num_seqs;
+  a.batch = s->batch;
+  a.T = s->seqlen;
+  a.H = s->nheads;
+  a.bf16 = s->dtype == SSD_DTYPE_BF16;
+  return a;
+}
+
+void set_plan(ssd::LinScan* a, const LinPlan& p, char* states) {
+  a->L = p.L;
+  a->slots_per_row = (long)p.spr;
+  a->states = p.state_bytes ? reinterpret_cast<float*>(states) : nullptr;
+}
+
+ssd_status check_ws(const void* workspace, size_t have, size_t need) {
+  if (need == 0) return SSD_OK;
+  if (!workspace || ((uintptr_t)workspace & 255)) return SSD_ERR_INVALID_ARGUMENT;
+  return have < need ? SSD_ERR_WORKSPACE_TOO_SMALL : SSD_OK;
+}
+
+// ---------------------------------------------------------------- group norm
+
+ssd_status check_norm(const ssd_norm_shape* s) {
+  if (!s) return SSD_ERR_INVALID_ARGUMENT;
+  if (s->samples < 1 || s->positions < 1 || s->channels < 1 || s->groups < 1) return SSD_ERR_INVALID_ARGUMENT;
+  if (s->channels % s->groups) return SSD_ERR_INVALID_ARGUMENT;
+  if (s->x_row != 0 && s->x_row < s->channels) return SSD_ERR_INVALID_ARGUMENT;
+  if (s->z_row != 0 && s->z_row < s->channels) return SSD_ERR_INVALID_ARGUMENT;
+  if (s->dtype != SSD_DTYPE_F32 && s->dtype != SSD_DTYPE_BF16) return SSD_ERR_UNSUPPORTED;
+  if (s->act != SSD_ACT_NONE && s->act != SSD_ACT_SILU) return SSD_ERR_UNSUPPORTED;
+  if (s->gate != SSD_GATE_NONE && s->gate != SSD_GATE_AFTER && s->gate != SSD_GATE_BEFORE) return SSD_ERR_UNSUPPORTED;
+  if (s->center != 0 && s->center != 1) return SSD_ERR_INVALID_ARGUMENT;
+  // rows, and workgroups of a launch (at most one per eight rows and channel tile, or per row and group)
+  const int64_t rows = (int64_t)s->samples * s->positions;
+  if (rows > INT32_MAX / 4 || rows * s->groups > INT32_MAX / 4) return SSD_ERR_UNSUPPORTED;
+  if (rows * ((s->channels + 63) / 64) > INT32_MAX) return SSD_ERR_UNSUPPORTED;
+  return SSD_OK;
+}
+
+ssd::NormArgs norm_args(const ssd_norm_shape* s) {
+  ssd::NormArgs a;
+  a.n = s->samples;
+  a.s = s->positions;
+  a.C = s->channels;
+  a.G = s->groups;
+  a.x_row = s->x_row ? s->x_row : s->channels;
+  a.z_row = s->z_row ? s->z_row : s->channels;
+  a.bf16 = s->dtype == SSD_DTYPE_BF16;
+  a.silu = s->act == SSD_ACT_SILU;
+  a.gate = s->gate;
+  a.center = s->center;
+  return a;
+}
+
+// Elements start on their own size; 8-channel pieces need 16-byte rows throughout.
+ssd_status norm_align(ssd::NormArgs* a) {
+  const int esz = a->bf16 ? 2 : 4;
+  const uintptr_t all = (uintptr_t)a->x | (uintptr_t)a->z | (uintptr_t)a->dy | (uintptr_t)a->y | (uintptr_t)a->dx |
+                        (uintptr_t)a->dz;
+  if (all % esz) return SSD_ERR_INVALID_ARGUMENT;
+  if (((uintptr_t)a->w | (uintptr_t)a->bias | (uintptr_t)a->stats | (uintptr_t)a->dw | (uintptr_t)a->db) & 3)
+    return SSD_ERR_INVALID_ARGUMENT;
+  a->vec = all % 16 == 0 && a->C % 8 == 0 && a->x_row % 8 == 0 && a->z_row % 8 == 0;
+  return SSD_OK;
+}
+
+ssd_status check_pages(const ssd_pages_shape* s) {
+  if (!s) return SSD_ERR_INVALID_ARGUMENT;
+  if (s->layers < 1 || s->slots < 1 || s->page_bytes < 1) return SSD_ERR_INVALID_ARGUMENT;
+  if (s->layers > 65535 || s->slots > (1 << 24)) return SSD_ERR_UNSUPPORTED;
+  if (s->page_bytes > ((int64_t)1 << 40)) return SSD_ERR_UNSUPPORTED;
+  return SSD_OK;
+}
+ssd::PagesArgs pages_args(void* pool, const ssd_pages_shape* s) {
+  ssd::PagesArgs a;
+  a.pool = static_cast<char*>(pool);
+  a.layers = s->layers;
+  a.slots = s->slots;
+  a.page = (long)s->page_bytes;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+ssd_status ssd_lin_attn_workspace_bytes(const ssd_lin_shape* shape, size_t* bytes) {
+  if (!bytes) return SSD_ERR_INVALID_ARGUMENT;
+  LinDims d;
+  LinPlan p;
+  ssd_status st = check_lin(shape, &d);
+  if (st == SSD_OK) st = lin_plan(shape, shape->dk, shape->dv, &p);
+  if (st == SSD_OK) *bytes = p.state_bytes;
+  return st;
+}
+
+ssd_status ssd_lin_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                            const int32_t* cu_seqlens, float scale, const float* initial_state, void* o,
+                            float* final_state, const ssd_lin_shape* shape, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  LinDims d;
+  LinPlan p;
+  ssd_status st = check_lin(shape, &d);
+  if (st != SSD_OK) return st;
+  if (!q || !k || !v || !log_decay || !o || !scale_ok(scale)) return SSD_ERR_INVALID_ARGUMENT;
+  if ((cu_seqlens != nullptr) != (shape->num_seqs > 0)) return SSD_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(initial_state) || !aligned16(final_state))
+    return SSD_ERR_INVALID_ARGUMENT;
+  if ((st = lin_plan(shape, shape->dk, shape->dv, &p)) != SSD_OK) return st;
+  if ((st = check_ws(workspace, workspace_bytes, p.state_bytes)) != SSD_OK) return st;
+  const int rep = shape->nheads / shape->nkv_heads;
+  ssd::LinScan a = base_scan(shape, log_decay, cu_seqlens, scale);
+  a.q = {q, (long)d.q_row, 1};
+  a.k = {k, (long)d.k_row, rep};
+  a.v = {v, (long)d.v_row, rep};
+  a.o = o;
+  a.dk = shape->dk;
+  a.dv = shape->dv;
+  a.init = initial_state;
+  a.fin = final_state;
+  set_plan(&a, p, static_cast<char*>(workspace));
+  return hip_status(ssd::launch_lin_scan(a, (hipStream_t)stream));
+}
+
+ssd_status ssd_lin_attn_bwd_workspace_bytes(const ssd_lin_shape* shape, size_t* bytes) {
+  if (!bytes) return SSD_ERR_INVALID_ARGUMENT;
+  LinBwdLayout L;
+  ssd_status st = lin_bwd_layout(shape, &L);
+  if (st == SSD_OK) *bytes = L.total;
+  return st;
+}
+
+ssd_status ssd_lin_attn_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                            const int32_t* cu_seqlens, float scale, const float* initial_state, const void* d_o,
+                            const float* dfinal_state, void* dq, void* dk, void* dv, float* dinitial_state,
+                            const ssd_lin_shape* shape, void* workspace, size_t workspace_bytes, void* stream) {
+  LinDims d;
+  LinBwdLayout L;
+  ssd_status st = check_lin(shape, &d);
+  if (st != SSD_OK) return st;
+  if (!q || !k || !v || !log_decay || !d_o || !dq || !dk || !dv || !scale_ok(scale)) return SSD_ERR_INVALID_ARGUMENT;
+  if ((cu_seqlens != nullptr) != (shape->num_seqs > 0)) return SSD_ERR_INVALID_ARGUMENT;
+  for (const void* t : {q, k, v, d_o, (const void*)initial_state, (const void*)dfinal_state, (const void*)dq, (const void*)dk,
+                        (const void*)dv, (const void*)dinitial_state})
+    if (!aligned16(t)) return SSD_ERR_INVALID_ARGUMENT;
+  if ((st = lin_bwd_layout(shape, &L)) != SSD_OK) return st;
+  if ((st = check_ws(workspace, workspace_bytes, L.total)) != SSD_OK) return st;
+  char* ws = static_cast<char*>(workspace);
+  hipStream_t hs = (hipStream_t)stream;
+  const int H = shape->nheads, Hk = shape->nkv_heads, rep = H / Hk;
+  const ssd::LinOperand oq{q, (long)d.q_row, 1}, ok{k, (long)d.k_row, rep}, ov{v, (long)d.v_row, rep},
+      og{d_o, (long)H * shape->dv, 1};
+  hipError_t e;
+  {  // dq
+    ssd::LinScan a = base_scan(shape, log_decay, cu_seqlens, scale);
+    a.q = og;
+    a.k = ov;
+    a.v = ok;
+    a.o = dq;
+    a.dk = shape->dv;
+    a.dv = shape->dk;
+    a.init = initial_state;
+    a.init_tr = 1;
+    set_plan(&a, L.dq, ws + L.st_dq);
+    e = ssd::launch_lin_scan(a, hs);
+    if (e != hipSuccess) return SSD_ERR_HIP;
+  }
+  // The reversed scans carry the adjoint divided by `scale`, which multiplies their outputs.
+  {  // dv and the initial state's gradient
+    ssd::LinScan a = base_scan(shape, log_decay, cu_seqlens, scale);
+    a.q = ok;
+    a.k = oq;
+    a.v = og;
+    a.o = rep > 1 ? static_cast<void*>(ws + L.part_v) : dv;
+    a.o_f32 = rep > 1;
+    a.dk = shape->dk;
+    a.dv = shape->dv;
+    a.init = dfinal_state;
+    a.init_scale = 1.f / scale;
+    a.fin = dinitial_state;
+    a.fin_scale = scale;
+    a.rev = 1;
+    set_plan(&a, L.dv, ws + L.st_dv);
+    e = ssd::launch_lin_scan(a, hs);
+    if (e != hipSuccess) return SSD_ERR_HIP;
+  }
+  {  // dk
+    ssd::LinScan a = base_scan(shape, log_decay, cu_seqlens, scale);
+    a.q = ov;
+    a.k = og;
+    a.v = oq;
+    a.o = rep > 1 ? static_cast<void*>(ws + L.part_k) : dk;
+    a.o_f32 = rep > 1;
+    a.dk = shape->dv;
+    a.dv = shape->dk;
+    a.init = dfinal_state;
+    a.init_scale = 1.f / scale;
+    a.init_tr = 1;
+    a.rev = 1;
+    set_plan(&a, L.dk, ws + L.st_dk);
+    e = ssd::launch_lin_scan(a, hs);
+    if (e != hipSuccess) return SSD_ERR_HIP;
+  }
+  if (rep > 1) {
+    const int bf16 = shape->dtype == SSD_DTYPE_BF16;
+    e = ssd::launch_lin_share_sum(reinterpret_cast<const float*>(ws + L.part_v), dv, cu_seqlens, shape->num_seqs,
+                                  (long)d.tokens, shape->seqlen, H, Hk, shape->dv, hs, bf16);
+    if (e == hipSuccess)
+      e = ssd::launch_lin_share_sum(reinterpret_cast<const float*>(ws + L.part_k), dk, cu_seqlens, shape->num_seqs,
+                                    (long)d.tokens, shape->seqlen, H, Hk, shape->dk, hs, bf16);
+  }
+  return hip_status(e);
+}
+
+ssd_status ssd_lin_attn_step(float* state, const void* q, const void* k, const void* v, const float* log_decay,
+                             const int32_t* slots, int32_t num_slots, float scale, void* o, const ssd_lin_shape* shape,
+                             void* stream) {
+  if (!shape) return SSD_ERR_INVALID_ARGUMENT;
+  ssd_status st = check_heads(shape);
+  if (st != SSD_OK) return st;
+  if (!state || !q || !k || !v || !log_decay || !o || !scale_ok(scale)) return SSD_ERR_INVALID_ARGUMENT;
+  if (num_slots < 1 || (!slots && num_slots < shape->batch)) return SSD_ERR_INVALID_ARGUMENT;
+  if (!aligned16(state) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return SSD_ERR_INVALID_ARGUMENT;
+  ssd::LinStep a;
+  a.state = state;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.ld = log_decay;
+  a.slots = slots;
+  a.o = o;
+  a.scale = scale;
+  a.batch = shape->batch;
+  a.H = shape->nheads;
+  a.Hk = shape->nkv_heads;
+  a.dk = shape->dk;
+  a.dv = shape->dv;
+  a.num_slots = num_slots;
+  a.bf16 = shape->dtype == SSD_DTYPE_BF16;
+  return hip_status(ssd::launch_lin_step(a, (hipStream_t)stream));
+}
+
+ssd_status ssd_group_norm_workspace_bytes(const ssd_norm_shape* shape, int32_t backward, size_t* bytes) {
+  if (!bytes) return SSD_ERR_INVALID_ARGUMENT;
+  ssd_status st = check_norm(shape);
+  if (st != SSD_OK) return st;
+  *bytes = 4 * ssd::norm_ws_floats(shape->samples, shape->positions, shape->channels, shape->groups, backward != 0);
+  return SSD_OK;
+}
+
+ssd_status ssd_group_norm(const void* x, const void* z, const float* weight, const float* bias, float eps, void* y,
+                          float* stats, const ssd_norm_shape* shape, void* workspace, size_t workspace_bytes, void* stream) {
+  ssd_status st = check_norm(shape);
+  if (st != SSD_OK) return st;
+  if (!x || !y || (z != nullptr) != (shape->gate != SSD_GATE_NONE)) return SSD_ERR_INVALID_ARGUMENT;
+  if (!(eps > 0.f) || !std::isfinite(eps)) return SSD_ERR_INVALID_ARGUMENT;
+  ssd::NormArgs a = norm_args(shape);
+  a.x = x;
+  a.z = z;
+  a.w = weight;
+  a.bias = bias;
+  a.eps = eps;
+  a.y = y;
+  a.stats = stats;
+  if ((st = norm_align(&a)) != SSD_OK) return st;
+  size_t need = 0;
+  ssd_group_norm_workspace_bytes(shape, 0, &need);
+  if ((st = check_ws(workspace, workspace_bytes, need)) != SSD_OK) return st;
+  a.ws = static_cast<float*>(workspace);
+  return hip_status(ssd::launch_group_norm(a, (hipStream_t)stream));
+}
+
+ssd_status ssd_group_norm_bwd(const void* x, const void* z, const float* weight, const float* bias, const float* stats,
+                              const void* dy, void* dx, void* dz, float* dweight, float* dbias, const ssd_norm_shape* shape,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  ssd_status st = check_norm(shape);
+  if (st != SSD_OK) return st;
+  if (!x || !stats || !dy || !dx) return SSD_ERR_INVALID_ARGUMENT;
+  if ((z != nullptr) != (shape->gate != SSD_GATE_NONE) || (dz != nullptr) != (z != nullptr)) return SSD_ERR_INVALID_ARGUMENT;
+  ssd::NormArgs a = norm_args(shape);
+  a.x = x;
+  a.z = z;
+  a.w = weight;
+  a.bias = bias;
+  a.stats = const_cast<float*>(stats);  // read only here
+  a.dy = dy;
+  a.dx = dx;
+  a.dz = dz;
+  a.dw = dweight;
+  a.db = dbias;
+  if ((st = norm_align(&a)) != SSD_OK) return st;
+  size_t need = 0;
+  ssd_group_norm_workspace_bytes(shape, 1, &need);
+  if ((st = check_ws(workspace, workspace_bytes, need)) != SSD_OK) return st;
+  a.ws = static_cast<float*>(workspace);
+  return hip_status(ssd::launch_group_norm_bwd(a, (hipStream_t)stream));
+}
+
+ssd_status ssd_pages_copy(void* pool, const int32_t* src, const int32_t* dst, int32_t pairs, const ssd_pages_shape* shape,
+                          void* stream) {
+  ssd_status st = check_pages(shape);
+  if (st != SSD_OK) return st;
+  if (!pool || !src || !dst || pairs < 1) return SSD_ERR_INVALID_ARGUMENT;
+  if (pairs > ssd::kMaxPagePairs) return SSD_ERR_UNSUPPORTED;
+  return hip_status(ssd::launch_pages_copy(pages_args(pool, shape), src, dst, pairs, (hipStream_t)stream));
+}
+
+ssd_status ssd_pages_clear(void* pool, const int32_t* slots, int32_t count, const ssd_pages_shape* shape, void* stream) {
+  ssd_status st = check_pages(shape);
+  if (st != SSD_OK) return st;
+  if (!pool || !slots || count < 1) return SSD_ERR_INVALID_ARGUMENT;
+  if (count > 65535) return SSD_ERR_UNSUPPORTED;
+  return hip_status(ssd::launch_pages_clear(pages_args(pool, shape), slots, count, (hipStream_t)stream));
+}
+
+ssd_status ssd_pages_compact_workspace_bytes(const ssd_pages_shape* shape, size_t* bytes) {
+  if (!bytes) return SSD_ERR_INVALID_ARGUMENT;
+  ssd_status st = check_pages(shape);
+  if (st == SSD_OK) *bytes = ssd::pages_compact_ws_bytes(shape->slots);
+  return st;
+}
+
+ssd_status ssd_pages_compact(void* pool, const uint8_t* live, int32_t* where, int32_t* count, const ssd_pages_shape* shape,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  ssd_status st = check_pages(shape);
+  if (st != SSD_OK) return st;
+  if (!pool || !live || !where || !count) return SSD_ERR_INVALID_ARGUMENT;
+  if ((st = check_ws(workspace, workspace_bytes, ssd::pages_compact_ws_bytes(shape->slots))) != SSD_OK) return st;
+  return hip_status(ssd::launch_pages_compact(pages_args(pool, shape), live, where, count, workspace, (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,132 @@
+// ssd_lin_attn.h -- internal interface of the linear-attention kernels
+// (one fixed decay a head): the scan over prompts and the one-token step.
+//
+// A scan computes, for every head of every sequence,
+//     D_t = lam D_{t-1} + v_t k_t^T,   o_t = scale D_t q_t,   D [dv][dk],
+// over the tokens in order or, reversed, from each sequence's last token to
+// its first. The backward pass is three scans with the roles exchanged:
+//     dq: forwards, q := do, k := v, v := k, from the transposed initial state;
+//     dv: reversed, q := k, k := q, v := do, from dfinal;
+//     dk: reversed, q := v, k := do, v := q, from the transposed dfinal.
+// In a reversed scan the state handed in is added where the last token's own
+// product is (L_T = scale do_T q_T^T + dfinal), so it is not decayed before
+// that token; `lead` below is 0 there and 1 in a forward scan.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ssd {
+
+// One operand: element (token, head, i) at base + token * row + (head / div) * d + i.
+struct LinOperand {
+  const void* base = nullptr;
+  long row = 0;
+  int div = 1;
+};
+
+struct LinScan {
+  LinOperand q, k, v;
+  void* o = nullptr;           // [tokens][H][dv], bf16 or fp32
+  int o_f32 = 0;               // bf16 operands only: write o in fp32 (partials summed over shared heads)
+  const float* ld = nullptr;   // [H] natural log decay
+  float scale = 1.f;
+  const float* init = nullptr; // [nseq][H] matrices, or null for zero
+  float init_scale = 1.f;
+  int init_tr = 0;             // the matrices are [dk][dv] instead of [dv][dk]
+  float* fin = nullptr;        // [nseq][H][dv][dk] or null: the state after the last token,
+  float fin_scale = 1.f;       //   times this,
+  int rev = 0;                 //   and in a reversed scan of at least one token times lam
+  const int32_t* cu = nullptr; // packed sequence starts, or null
+  int S = 0;                   // packed sequences
+  int batch = 1, T = 0, H = 0; // rows, tokens a row, heads
+  int dk = 0, dv = 0;          // this scan's contraction and value sizes
+  int bf16 = 0;
+  // Sequences are cut into blocks of L tokens (from the end in a reversed
+  // scan); block b of packed sequence s has slot floor(cu[s] / L) + s + b, of
+  // row r slot r * slots_per_row + b. A sequence without tokens has one block.
+  int L = 0;
+  long slots_per_row = 0;
+  float* states = nullptr;     // [slots][H][dv][dk]: each block's own sum, then its entering state
+};
+
+// Tokens a block for a scan of these sizes; a value >= T means that no
+// sequence is cut and no block states are needed.
+int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16);
+inline long lin_slots_per_row(int T, int S, int L) { return S > 0 ? (long)(T / L) + S : (T + (long)L - 1) / L; }
+
+hipError_t launch_lin_scan(const LinScan& a, hipStream_t stream);
+
+// out[token][kv head][i] = sum of in over the heads that share it, in head order.
+hipError_t launch_lin_share_sum(const float* in, void* out, const int32_t* cu, int S, long tokens, int T, int H, int Hk,
+                                int d, hipStream_t stream, int bf16);
+
+struct LinStep {
+  float* state = nullptr;      // [num_slots][H][dv][dk]
+  const void *q = nullptr, *k = nullptr, *v = nullptr;
+  const float* ld = nullptr;
+  const int32_t* slots = nullptr;
+  void* o = nullptr;
+  float scale = 1.f;
+  int batch = 0, H = 0, Hk = 0, dk = 0, dv = 0, num_slots = 0, bf16 = 0;
+};
+hipError_t launch_lin_step(const LinStep& a, hipStream_t stream);
+
+#ifdef __HIPCC__
+
+// ---- device side ----------------------------------------------------------
+
+struct LinPiece {
+  int seq;     // sequence
+  int blk;     // block in the sequence, -1: the slot holds no block
+  int len;     // tokens of the sequence
+  long start;  // its first token, flattened over rows
+};
+
+// The sequence and block of a slot. cu's entries are brought into [0, T] and
+// into order, so that no content of cu leads outside the tensors. Every lane of
+// the calling wave must be active; all receive the same answer.
+__device__ __forceinline__ LinPiece lin_piece(const LinScan& a, long slot) {
+  LinPiece p;
+  if (!a.cu) {
+    p.seq = (int)(slot / a.slots_per_row);
+    p.blk = (int)(slot % a.slots_per_row);
+    p.len = a.T;
+    p.start = (long)p.seq * a.T;
+    return p;
+  }
+  // Slots of sequence s begin at floor(cu[s] / L) + s, which grows with s: count those at or before `slot`.
+  const int lane = (int)threadIdx.x & 63;
+  int n = 0;
+  for (int i0 = 0; i0 < a.S; i0 += 64) {
+    const int i = i0 + lane;
+    bool in = false;
+    if (i < a.S) in = (long)min(max(a.cu[i], 0), a.T) / a.L + i <= slot;
+    n += __popcll(__ballot(in));
+  }
+  p.seq = __builtin_amdgcn_readfirstlane(n - 1);
+  if (p.seq < 0) {
+    p.seq = 0;
+    p.blk = -1;
+    p.len = 0;
+    p.start = 0;
+    return p;
+  }
+  const int c0 = min(max(a.cu[p.seq], 0), a.T);
+  const int c1 = min(max(a.cu[p.seq + 1], c0), a.T);
+  p.start = c0;
+  p.len = c1 - c0;
+  const long b = slot - ((long)c0 / a.L + p.seq);
+  p.blk = b >= 0 && (b == 0 || b * a.L < p.len) ? (int)b : -1;
+  return p;
+}
+
+// log2 of the decay; a log decay of -inf becomes a finite value whose first
+// power already underflows to 0, while its power 0 stays 1.
+__device__ __forceinline__ float lin_log2_decay(const float* ld, int h) {
+  return fmaxf(ld[h] * 1.4426950408889634f, -16384.f);
+}
+
+#endif
+
+}  // namespace ssd

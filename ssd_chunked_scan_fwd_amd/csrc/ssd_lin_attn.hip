@@ -1,0 +1,400 @@
+// ssd_lin_attn.hip -- linear attention with one fixed decay a head: the scan
+// token by token (fp32 operands), the states passed between blocks of tokens,
+// the sums over shared heads, and the one-token step on a pool of states.
+#include <type_traits>
+
+#include "ssd_device.h"
+#include "ssd_lin_attn.h"
+
+namespace ssd {
+
+namespace {
+
+// Sum over aligned groups of 16 lanes; every lane receives it.
+template <int CTRL>
+__device__ __forceinline__ float dpp_plus(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float sum16(float v) {
+  v = dpp_plus<0xB1>(v);    // quad_perm [1, 0, 3, 2]
+  v = dpp_plus<0x4E>(v);    // quad_perm [2, 3, 0, 1]
+  v = dpp_plus<0x141>(v);   // row_half_mirror
+  return dpp_plus<0x140>(v);  // row_mirror
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_el(const void* p, long i) {
+  if constexpr (BF16) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
+  else return static_cast<const float*>(p)[i];
+}
+
+// ----------------------------------------------------------------------------
+// The recurrence itself, token by token. A workgroup takes 16 rows of the
+// state of one (block, head): 16 lanes a row, 16 columns a lane, all in
+// registers; tokens are staged 16 at a time through LDS. lam is used as a sum
+// of two floats, so that its rounding does not compound over the block.
+// STATE_ONLY leaves each block's own sum (from a zero state) in a.states;
+// the other form starts from the block's entering state and writes o.
+// ----------------------------------------------------------------------------
+constexpr int kRecRows = 16, kRecTok = 16, kRecMaxK = 256;
+
+template <bool BF16, bool STATE_ONLY>
+__global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
+  __shared__ float qs[kRecTok][kRecMaxK], ks[kRecTok][kRecMaxK], vs[kRecTok][kRecRows];
+  const int tiles = (a.dv + kRecRows - 1) / kRecRows;
+  const long u = blockIdx.x;
+  const int row0 = (int)(u % tiles) * kRecRows;
+  const int h = (int)((u / tiles) % a.H);
+  const long slot = u / ((long)tiles * a.H);
+  const LinPiece p = lin_piece(a, slot);
+  if (p.blk < 0) return;
+  const int pos0 = p.blk * a.L;
+  const int n = min(p.len - pos0, a.L);
+  const bool last = pos0 + n >= p.len;
+  if (STATE_ONLY && last) return;  // the scan carries the last block's state itself
+  const int r = threadIdx.x >> 4, c = threadIdx.x & 15;
+  const int row = row0 + r;
+  const double lam = exp((double)fmaxf(a.ld[h], -11356.f));
+  const float lam_hi = (float)lam, lam_lo = (float)(lam - (double)lam_hi);
+
+  float s[16];  // columns 128 m + 8 c + j at 8 m + j
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = 0.f;
+  const long mat = (long)a.dv * a.dk;
+  if (!STATE_ONLY) {
+    const float* src = p.blk > 0 ? a.states + (slot * a.H + h) * mat : a.init;
+    if (p.blk == 0 && src) src += ((long)p.seq * a.H + h) * mat;
+    const bool tr = p.blk == 0 && a.init_tr;
+    const float sc = p.blk == 0 ? a.init_scale : 1.f;
+    if (src && row < a.dv) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int col = 128 * (i >> 3) + 8 * c + (i & 7);
+        if (col < a.dk) s[i] = sc * (tr ? src[(long)col * a.dv + row] : src[(long)row * a.dk + col]);
+      }
+    }
+  }
+
+  for (int t0 = 0; t0 < n; t0 += kRecTok) {
+    const int nt = min(kRecTok, n - t0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRecTok * kRecMaxK; i += 256) {
+      const int t = i / kRecMaxK, col = i % kRecMaxK;
+      float kv = 0.f, qv = 0.f;
+      if (t < nt && col < a.dk) {
+        const int pos = pos0 + t0 + t;
+        const long tok = p.start + (a.rev ? p.len - 1 - pos : pos);
+        kv = load_el<BF16>(a.k.base, tok * a.k.row + (long)(h / a.k.div) * a.dk + col);
+        if (!STATE_ONLY) qv = load_el<BF16>(a.q.base, tok * a.q.row + (long)(h / a.q.div) * a.dk + col);
+      }
+      ks[t][col] = kv;
+      qs[t][col] = qv;
+    }
+    {
+      const int t = threadIdx.x >> 4, i = threadIdx.x & 15;
+      float x = 0.f;
+      if (t < nt && row0 + i < a.dv) {
+        const int pos = pos0 + t0 + t;
+        const long tok = p.start + (a.rev ? p.len - 1 - pos : pos);
+        x = load_el<BF16>(a.v.base, tok * a.v.row + (long)(h / a.v.div) * a.dv + row0 + i);
+      }
+      vs[t][i] = x;
+    }
+    __syncthreads();
+    for (int t = 0; t < nt; ++t) {
+      const bool keep = a.rev && pos0 + t0 + t == 0;  // the state handed to a reversed scan is not decayed first
+      const float hi = keep ? 1.f : lam_hi, lo = keep ? 0.f : lam_lo;
+      const float v = vs[t][r];
+      float part = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int col = 128 * (i >> 3) + 8 * c + (i & 7);
+        s[i] = fmaf(s[i], hi, fmaf(s[i], lo, v * ks[t][col]));
+        if (!STATE_ONLY) part = fmaf(s[i], qs[t][col], part);
+      }
+      if (!STATE_ONLY) {
+        part = sum16(part) * a.scale;
+        if (c == 0 && row < a.dv) {
+          const int pos = pos0 + t0 + t;
+          const long tok = p.start + (a.rev ? p.len - 1 - pos : pos);
+          const long at = (tok * a.H + h) * a.dv + row;
+          if (!BF16 || a.o_f32) static_cast<float*>(a.o)[at] = part;
+          else static_cast<uint16_t*>(a.o)[at] = f32_to_bf16(part);
+        }
+      }
+    }
+  }
+
+  float* dst = nullptr;
+  float sc = 1.f;
+  if (STATE_ONLY) {
+    dst = a.states + (slot * a.H + h) * mat;
+  } else if (last && a.fin) {
+    dst = a.fin + ((long)p.seq * a.H + h) * mat;
+    sc = a.fin_scale * (a.rev && p.len > 0 ? lam_hi : 1.f);
+  }
+  if (dst && row < a.dv) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int col = 128 * (i >> 3) + 8 * c + (i & 7);
+      if (col < a.dk) dst[(long)row * a.dk + col] = s[i] * sc;
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------
+// Entering states: for blocks b = 0, 1, ... of a sequence, with own sums s_b,
+// D = initial state; states[b] = D (b >= 1); D = lam^n_b D + s_b. Four
+// elements a thread; the next block's sum is loaded ahead.
+// ----------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void lin_passing_kernel(LinScan a) {
+  const int h = blockIdx.y, s = blockIdx.z;
+  const int mat = a.dv * a.dk;
+  const int e = 4 * (int)(blockIdx.x * 256 + threadIdx.x);
+  long slot0;
+  int len;
+  if (a.cu) {
+    const int c0 = min(max(a.cu[s], 0), a.T), c1 = min(max(a.cu[s + 1], c0), a.T);
+    slot0 = (long)c0 / a.L + s;
+    len = c1 - c0;
+  } else {
+    slot0 = s * a.slots_per_row;
+    len = a.T;
+  }
+  const int nb = (len + a.L - 1) / a.L;
+  if (nb < 2 || e >= mat) return;
+  f32x4 D = {0.f, 0.f, 0.f, 0.f};
+  if (a.init) {
+    const float* src = a.init + ((long)s * a.H + h) * mat;
+    if (a.init_tr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) D[i] = src[(long)((e + i) % a.dk) * a.dv + (e + i) / a.dk] * a.init_scale;
+    } else {
+      D = *reinterpret_cast<const f32x4*>(src + e) * a.init_scale;
+    }
+  }
+  const float g = lin_log2_decay(a.ld, h);
+  const float w0 = fast_exp2(g * (float)(a.L - (a.rev ? 1 : 0)));
+  const float w = fast_exp2(g * (float)a.L);
+  const long step = (long)a.H * mat;
+  float* at = a.states + (slot0 * a.H + h) * mat + e;
+  f32x4 own = *reinterpret_cast<const f32x4*>(at);
+  for (int b = 1; b < nb; ++b) {
+    f32x4 next = {0.f, 0.f, 0.f, 0.f};
+    if (b + 1 < nb) next = *reinterpret_cast<const f32x4*>(at + b * step);
+    D = D * (b == 1 ? w0 : w) + own;
+    *reinterpret_cast<f32x4*>(at + b * step) = D;
+    own = next;
+  }
+}
+
+// Sum over the heads that share a key head, eight values a thread, in head
+// order. Packed batches: tokens before the first and behind the last sequence
+// are left as they were.
+template <bool BF16>
+__global__ __launch_bounds__(256) void lin_share_sum_kernel(const float* __restrict__ in, void* __restrict__ out,
+                                                            const int32_t* __restrict__ cu, int S, long tokens, int T,
+                                                            int H, int Hk, int d) {
+  const int pieces = d >> 3;
+  const long i = (long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= tokens * Hk * pieces) return;
+  const int c = (int)(i % pieces);
+  const long th = i / pieces;
+  const long tok = th / Hk;
+  const int hk = (int)(th % Hk), rep = H / Hk;
+  if (cu && (tok < max(cu[0], 0) || tok >= min(cu[S], T))) return;
+  const float* src = in + (tok * H + (long)hk * rep) * d + 8 * c;
+  f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
+  for (int j = 1; j < rep; ++j) {
+    lo += *reinterpret_cast<const f32x4*>(src + (long)j * d);
+    hi += *reinterpret_cast<const f32x4*>(src + (long)j * d + 4);
+  }
+  const long at = (tok * Hk + hk) * d + 8 * c;
+  if constexpr (BF16) {
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + at) =
+        u32x4{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
+  } else {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = lo;
+    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at + 4) = hi;
+  }
+}
+
+// ----------------------------------------------------------------------------
+// The one-token step: D = lam D + v k^T, o = scale D q, for the state of each
+// entry's slot. The state's read and write bound it (2 dv dk 4 bytes a head).
+// A state row takes `tpr` lanes of four columns each (a power of two; lanes
+// past dk / 4 idle), a thread ROWS rows; a workgroup one (entry, head, row
+// range). Entries whose slot is outside the pool are padding: o = 0 and no
+// state is touched. Entries that name the same slot are taken in the order of
+// the batch: the first one's workgroup runs them all, so a stream may bring
+// several tokens in one call and nothing is raced.
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ float lanes_sum(float v, int n) {
+  if (n > 1) v = dpp_plus<0xB1>(v);
+  if (n > 2) v = dpp_plus<0x4E>(v);
+  if (n > 4) v = dpp_plus<0x141>(v);
+  if (n > 8) v = dpp_plus<0x140>(v);
+  if (n > 16) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  }
+  if (n > 32) {
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  }
+  return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ f32x4 load4(const void* p, long i) {
+  if constexpr (BF16) {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p) + i);
+    return f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+  } else {
+    return *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+  }
+}
+
+template <bool BF16, int ROWS>
+__global__ __launch_bounds__(256) void lin_step_kernel(LinStep a, int tpr, int parts) {
+  const int h = (int)(blockIdx.x / parts), part = (int)(blockIdx.x % parts);
+  int e = blockIdx.y;
+  const int hk = h / (a.H / a.Hk);
+  const int c4 = threadIdx.x & (tpr - 1), rpp = 256 / tpr;
+  const int r0 = part * ROWS * rpp + (int)threadIdx.x / tpr;
+  const bool col_in = 4 * c4 < a.dk;
+  const int slot = a.slots ? a.slots[e] : e;
+  if (slot < 0 || slot >= a.num_slots) {
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const int r = r0 + j * rpp;
+      if (c4 == 0 && r < a.dv) {
+        const long at = ((long)e * a.H + h) * a.dv + r;
+        if (BF16) static_cast<uint16_t*>(a.o)[at] = 0;
+        else static_cast<float*>(a.o)[at] = 0.f;
+      }
+    }
+    return;
+  }
+  float* st = a.state + ((long)slot * a.H + h) * a.dv * a.dk + 4 * c4;
+  f32x4 s[ROWS];
+#pragma unroll
+  for (int j = 0; j < ROWS; ++j) {
+    const int r = r0 + j * rpp;
+    s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (col_in && r < a.dv) s[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(st + (long)r * a.dk));
+  }
+  const float lam = fast_exp2(lin_log2_decay(a.ld, h));
+  if (a.slots) {
+    int same = 0;
+    for (int i = threadIdx.x; i < e; i += 256) same |= a.slots[i] == slot;
+    if (__syncthreads_or(same)) return;  // an earlier entry's workgroup runs this one
+  }
+  for (;;) {
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    const f32x4 k = col_in ? load4<BF16>(a.k, ((long)e * a.Hk + hk) * a.dk + 4 * c4) : zero;
+    const f32x4 q = col_in ? load4<BF16>(a.q, ((long)e * a.H + h) * a.dk + 4 * c4) : zero;
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const int r = r0 + j * rpp;
+      const float v = load_el<BF16>(a.v, ((long)e * a.Hk + hk) * a.dv + min(r, a.dv - 1));
+      float acc = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[j][i] = fmaf(s[j][i], lam, v * k[i]);
+        acc = fmaf(s[j][i], q[i], acc);
+      }
+      acc = lanes_sum(acc, tpr) * a.scale;
+      if (c4 == 0 && r < a.dv) {
+        const long at = ((long)e * a.H + h) * a.dv + r;
+        if (BF16) static_cast<uint16_t*>(a.o)[at] = f32_to_bf16(acc);
+        else static_cast<float*>(a.o)[at] = acc;
+      }
+    }
+    if (!a.slots) break;
+    __shared__ int next;
+    if (threadIdx.x == 0) next = a.batch;
+    __syncthreads();
+    for (int i = e + 1 + (int)threadIdx.x; i < a.batch; i += 256)
+      if (a.slots[i] == slot) {
+        atomicMin(&next, i);
+        break;
+      }
+    __syncthreads();
+    const int nx = next;
+    __syncthreads();
+    if (nx >= a.batch) break;
+    e = nx;
+  }
+#pragma unroll
+  for (int j = 0; j < ROWS; ++j) {
+    const int r = r0 + j * rpp;
+    if (col_in && r < a.dv) __builtin_nontemporal_store(s[j], reinterpret_cast<f32x4*>(st + (long)r * a.dk));
+  }
+}
+
+}  // namespace
+
+int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16) {
+  const long seqs = S > 0 ? S : batch;
+  const long units = (long)H * ((dv + kRecRows - 1) / kRecRows);
+  const long target = 1024;
+  if (seqs * units >= target) return (T + 63) / 64 * 64;
+  long L = (long)batch * T * units / target;
+  L = (L + 63) / 64 * 64;
+  if (L < 64) L = 64;
+  if (L > T) L = ((long)T + 63) / 64 * 64;
+  return (int)L;
+}
+
+hipError_t launch_lin_scan(const LinScan& a, hipStream_t stream) {
+  const long slots = a.S > 0 ? a.slots_per_row : a.slots_per_row * a.batch;
+  const int tiles = (a.dv + kRecRows - 1) / kRecRows;
+  const dim3 grid((unsigned)(slots * a.H * tiles));
+  if (a.states) {
+    if (a.bf16) hipLaunchKernelGGL((lin_rec_kernel<true, true>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((lin_rec_kernel<false, true>), grid, dim3(256), 0, stream, a);
+    const dim3 pg((unsigned)((a.dv * a.dk / 4 + 255) / 256), (unsigned)a.H, (unsigned)(a.S > 0 ? a.S : a.batch));
+    hipLaunchKernelGGL(lin_passing_kernel, pg, dim3(256), 0, stream, a);
+  }
+  if (a.bf16) hipLaunchKernelGGL((lin_rec_kernel<true, false>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((lin_rec_kernel<false, false>), grid, dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_lin_share_sum(const float* in, void* out, const int32_t* cu, int S, long tokens, int T, int H, int Hk,
+                                int d, hipStream_t stream, int bf16) {
+  const long n = tokens * Hk * (d / 8);
+  const dim3 grid((unsigned)((n + 255) / 256));
+  if (bf16) hipLaunchKernelGGL(lin_share_sum_kernel<true>, grid, dim3(256), 0, stream, in, out, cu, S, tokens, T, H, Hk, d);
+  else hipLaunchKernelGGL(lin_share_sum_kernel<false>, grid, dim3(256), 0, stream, in, out, cu, S, tokens, T, H, Hk, d);
+  return hipGetLastError();
+}
+
+namespace {
+template <bool BF16>
+void step_launch(const LinStep& a, int rows, int tpr, int parts, hipStream_t stream) {
+  const dim3 grid((unsigned)(a.H * parts), (unsigned)a.batch);
+  if (rows == 8) hipLaunchKernelGGL((lin_step_kernel<BF16, 8>), grid, dim3(256), 0, stream, a, tpr, parts);
+  else if (rows == 4) hipLaunchKernelGGL((lin_step_kernel<BF16, 4>), grid, dim3(256), 0, stream, a, tpr, parts);
+  else if (rows == 2) hipLaunchKernelGGL((lin_step_kernel<BF16, 2>), grid, dim3(256), 0, stream, a, tpr, parts);
+  else hipLaunchKernelGGL((lin_step_kernel<BF16, 1>), grid, dim3(256), 0, stream, a, tpr, parts);
+}
+}  // namespace
+
+hipError_t launch_lin_step(const LinStep& a, hipStream_t stream) {
+  int tpr = 2;
+  while (tpr * 4 < a.dk) tpr *= 2;
+  const int rpp = 256 / tpr;
+  // Rows a thread: as many (up to 8, the loads each thread keeps in flight) as
+  // still leave two workgroups for every CU.
+  int rows = 8;
+  while (rows > 1 && ((rows / 2) * rpp >= a.dv || (long)a.batch * a.H * ((a.dv + rows * rpp - 1) / (rows * rpp)) < 512))
+    rows /= 2;
+  const int parts = (a.dv + rows * rpp - 1) / (rows * rpp);
+  if (a.bf16) step_launch<true>(a, rows, tpr, parts, stream);
+  else step_launch<false>(a, rows, tpr, parts, stream);
+  return hipGetLastError();
+}
+
+}  // namespace ssd
