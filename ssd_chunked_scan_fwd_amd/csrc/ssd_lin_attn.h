@@ -57,6 +57,11 @@ inline long lin_slots_per_row(int T, int S, int L) { return S > 0 ? (long)(T / L
 
 hipError_t launch_lin_scan(const LinScan& a, hipStream_t stream);
 
+// bf16 operands: the scan on matrix instructions (ssd_lin_scan.hip), either the
+// blocks' own sums or, from the entering states, the outputs.
+int lin_mfma_tile(int dv);
+hipError_t launch_lin_mfma(const LinScan& a, bool states, hipStream_t stream);
+
 // out[token][kv head][i] = sum of in over the heads that share it, in head order.
 hipError_t launch_lin_share_sum(const float* in, void* out, const int32_t* cu, int S, long tokens, int T, int H, int Hk,
                                 int d, hipStream_t stream, int bf16);

@@ -29,7 +29,7 @@ __device__ __forceinline__ float load_el(const void* p, long i) {
 }
 
 // ----------------------------------------------------------------------------
-// The recurrence itself, token by token. A workgroup takes 16 rows of the
+// The recurrence itself, token by token, for fp32 operands. A workgroup takes 16 rows of the
 // state of one (block, head): 16 lanes a row, 16 columns a lane, all in
 // registers; tokens are staged 16 at a time through LDS. lam is used as a sum
 // of two floats, so that its rounding does not compound over the block.
@@ -38,7 +38,7 @@ __device__ __forceinline__ float load_el(const void* p, long i) {
 // ----------------------------------------------------------------------------
 constexpr int kRecRows = 16, kRecTok = 16, kRecMaxK = 256;
 
-template <bool BF16, bool STATE_ONLY>
+template <bool STATE_ONLY>
 __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
   __shared__ float qs[kRecTok][kRecMaxK], ks[kRecTok][kRecMaxK], vs[kRecTok][kRecRows];
   const int tiles = (a.dv + kRecRows - 1) / kRecRows;
@@ -84,8 +84,8 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
       if (t < nt && col < a.dk) {
         const int pos = pos0 + t0 + t;
         const long tok = p.start + (a.rev ? p.len - 1 - pos : pos);
-        kv = load_el<BF16>(a.k.base, tok * a.k.row + (long)(h / a.k.div) * a.dk + col);
-        if (!STATE_ONLY) qv = load_el<BF16>(a.q.base, tok * a.q.row + (long)(h / a.q.div) * a.dk + col);
+        kv = load_el<false>(a.k.base, tok * a.k.row + (long)(h / a.k.div) * a.dk + col);
+        if (!STATE_ONLY) qv = load_el<false>(a.q.base, tok * a.q.row + (long)(h / a.q.div) * a.dk + col);
       }
       ks[t][col] = kv;
       qs[t][col] = qv;
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
       if (t < nt && row0 + i < a.dv) {
         const int pos = pos0 + t0 + t;
         const long tok = p.start + (a.rev ? p.len - 1 - pos : pos);
-        x = load_el<BF16>(a.v.base, tok * a.v.row + (long)(h / a.v.div) * a.dv + row0 + i);
+        x = load_el<false>(a.v.base, tok * a.v.row + (long)(h / a.v.div) * a.dv + row0 + i);
       }
       vs[t][i] = x;
     }
@@ -118,8 +118,7 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
           const int pos = pos0 + t0 + t;
           const long tok = p.start + (a.rev ? p.len - 1 - pos : pos);
           const long at = (tok * a.H + h) * a.dv + row;
-          if (!BF16 || a.o_f32) static_cast<float*>(a.o)[at] = part;
-          else static_cast<uint16_t*>(a.o)[at] = f32_to_bf16(part);
+          static_cast<float*>(a.o)[at] = part;
         }
       }
     }
@@ -335,12 +334,14 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStep a, int tpr, int p
 
 }  // namespace
 
+// Sequences are cut only as far as it takes to fill the chip: every cut costs
+// its state's way through memory, and the products k v^T a second time.
 int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16) {
   const long seqs = S > 0 ? S : batch;
-  const long units = (long)H * ((dv + kRecRows - 1) / kRecRows);
-  const long target = 1024;
-  if (seqs * units >= target) return (T + 63) / 64 * 64;
-  long L = (long)batch * T * units / target;
+  const int tile = bf16 ? lin_mfma_tile(dv) : kRecRows;
+  const long units = (long)H * ((dv + tile - 1) / tile);
+  const long target = bf16 ? 512 : 1024;
+  long L = seqs * units >= target ? T : (long)batch * T * units / target;
   L = (L + 63) / 64 * 64;
   if (L < 64) L = 64;
   if (L > T) L = ((long)T + 63) / 64 * 64;
@@ -349,16 +350,19 @@ int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16) {
 
 hipError_t launch_lin_scan(const LinScan& a, hipStream_t stream) {
   const long slots = a.S > 0 ? a.slots_per_row : a.slots_per_row * a.batch;
-  const int tiles = (a.dv + kRecRows - 1) / kRecRows;
-  const dim3 grid((unsigned)(slots * a.H * tiles));
+  const dim3 grid((unsigned)(slots * a.H * ((a.dv + kRecRows - 1) / kRecRows)));
+  hipError_t e;
   if (a.states) {
-    if (a.bf16) hipLaunchKernelGGL((lin_rec_kernel<true, true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((lin_rec_kernel<false, true>), grid, dim3(256), 0, stream, a);
+    if (a.bf16) {
+      if ((e = launch_lin_mfma(a, true, stream)) != hipSuccess) return e;
+    } else {
+      hipLaunchKernelGGL(lin_rec_kernel<true>, grid, dim3(256), 0, stream, a);
+    }
     const dim3 pg((unsigned)((a.dv * a.dk / 4 + 255) / 256), (unsigned)a.H, (unsigned)(a.S > 0 ? a.S : a.batch));
     hipLaunchKernelGGL(lin_passing_kernel, pg, dim3(256), 0, stream, a);
   }
-  if (a.bf16) hipLaunchKernelGGL((lin_rec_kernel<true, false>), grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((lin_rec_kernel<false, false>), grid, dim3(256), 0, stream, a);
+  if (a.bf16) return launch_lin_mfma(a, false, stream);
+  hipLaunchKernelGGL(lin_rec_kernel<false>, grid, dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
