@@ -24,6 +24,8 @@ namespace ssd {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCus = 256, kMaxParts = 1024;
+constexpr int kMaxWaves = 16;   // of a workgroup that shares one group
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_plus(float v) {
@@ -46,18 +48,25 @@ __device__ __forceinline__ float lanes_sum(float v, int n) {
   return v;
 }
 
-// Sum over the `lanes` threads (a power of two) that share a group; above 64
-// through LDS (`red`, one float a wave), every thread of the workgroup taking part.
-__device__ __forceinline__ float group_total(float v, int lanes, float* red) {
-  v = lanes_sum(v, lanes < 64 ? lanes : 64);
-  if (lanes <= 64) return v;
-  const int wave = threadIdx.x >> 6, per = lanes >> 6;
+// Sums over the `lanes` threads that share a group: a power of two up to 64, or
+// the whole workgroup, then through LDS (`red`, a slot of two floats a wave;
+// calls in turn use the two halves of it, so that one barrier a call is enough).
+__device__ __forceinline__ void group_totals(float& v0, float& v1, int lanes, float* red, int half) {
+  const int n = lanes < 64 ? lanes : 64;
+  v0 = lanes_sum(v0, n);
+  v1 = lanes_sum(v1, n);
+  if (lanes <= 64) return;
+  float* at = red + 2 * kMaxWaves * half;
+  if ((threadIdx.x & 63) == 0) {
+    at[2 * (threadIdx.x >> 6)] = v0;
+    at[2 * (threadIdx.x >> 6) + 1] = v1;
+  }
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[wave] = v;
-  __syncthreads();
-  float t = 0.f;
-  for (int w = 0; w < per; ++w) t += red[(wave & ~(per - 1)) + w];
-  return t;
+  v0 = v1 = 0.f;
+  for (int w = 0; w < (int)blockDim.x >> 6; ++w) {
+    v0 += at[2 * w];
+    v1 += at[2 * w + 1];
+  }
 }
 
 __device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + fast_exp2(-v * kLog2e)); }
@@ -110,60 +119,104 @@ __device__ __forceinline__ void load_par(const float* p, int c, float other, flo
   for (int j = 0; j < VEC; ++j) v[j] = p ? p[c + j] : other;
 }
 
+// A form of the norm fixed at compile time (GATE and SILU), or read from the
+// arguments (GATE < 0).
+template <int GATE, bool SILU>
+struct Form {
+  static __device__ __forceinline__ int gate(const NormArgs& a) { return GATE < 0 ? a.gate : GATE; }
+  static __device__ __forceinline__ bool silu(const NormArgs& a) { return GATE < 0 ? a.silu != 0 : SILU; }
+};
+
 // t -> y for one element; sz = silu(z) where the gate comes after.
+template <class F>
 __device__ __forceinline__ float finish(const NormArgs& a, float t, float sz) {
-  const float v = a.silu ? t * sigmoid(t) : t;
-  return a.gate == kGateAfter ? v * sz : v;
+  const float v = F::silu(a) ? t * sigmoid(t) : t;
+  return F::gate(a) == kGateAfter ? v * sz : v;
 }
 // dL/dt from dL/dy, and the gate's own gradient where it comes after.
+template <class F>
 __device__ __forceinline__ float unfinish(const NormArgs& a, float t, float z, float dy, float& dz) {
   float slope = 1.f, v = t;
-  if (a.silu) {
+  if (F::silu(a)) {
     const float s = sigmoid(t);
     v = t * s;
     slope = silu_slope(t, s);
   }
-  if (a.gate == kGateAfter) {
+  if (F::gate(a) == kGateAfter) {
     const float s = sigmoid(z);
     dz = dy * v * silu_slope(z, s);
     dy *= z * s;
   }
   return dy * slope;
 }
+typedef Form<-1, false> AnyForm;
 
 // ---------------------------------------------------------------- one position a sample
 
-// `lanes` threads share one (row, group), NV pieces of VEC channels each.
-template <bool BF16, int VEC, int NV>
-__global__ __launch_bounds__(kThreads) void norm_row_kernel(NormArgs a, int lanes) {
-  __shared__ float red[kThreads / 64];
-  const int Cg = a.C / a.G, l = threadIdx.x & (lanes - 1);
-  const long item = (long)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
+// VEC elements as they lie in memory, so that the next row's loads wait in few registers.
+template <bool BF16, int VEC>
+struct Raw {
+  u32x4 w[VEC == 8 ? (BF16 ? 1 : 2) : 1];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (auto& x : w) x = u32x4{0u, 0u, 0u, 0u};
+  }
+  __device__ __forceinline__ void load(const void* p, long i) {
+    if constexpr (VEC == 8) {
+      const u32x4* at = reinterpret_cast<const u32x4*>(static_cast<const char*>(p) + i * (BF16 ? 2 : 4));
+#pragma unroll
+      for (int k = 0; k < (BF16 ? 1 : 2); ++k) w[k] = at[k];
+    } else {
+      w[0].x = BF16 ? (uint32_t)static_cast<const uint16_t*>(p)[i] << 16 : static_cast<const uint32_t*>(p)[i];
+    }
+  }
+  __device__ __forceinline__ float operator[](int j) const {
+    if constexpr (VEC == 8 && BF16) return j & 1 ? bf16_hi(w[0][j >> 1]) : bf16_lo(w[0][j >> 1]);
+    else return __uint_as_float(w[VEC == 8 ? j >> 2 : 0][j & 3]);
+  }
+};
+
+// `lanes` threads share one (row, group), NV pieces of VEC channels each; WHOLE:
+// all threads of the workgroup do.
+template <bool BF16, int VEC, int NV, int GATE, bool SILU, bool WHOLE>
+__global__ __launch_bounds__(WHOLE ? 1024 : kThreads) void norm_row_kernel(NormArgs a, int lanes) {
+  using F = Form<GATE, SILU>;
+  __shared__ float red[4 * kMaxWaves];
+  const int Cg = a.C / a.G;
+  const int l = WHOLE ? (int)threadIdx.x : (int)threadIdx.x & (lanes - 1);
+  const long item = WHOLE ? (long)blockIdx.x : (long)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
   const bool on = item < a.n * a.G;
   const long row = on ? item / a.G : 0;
   const int g = on ? (int)(item % a.G) : 0;
+  Raw<BF16, VEC> rx[NV], rz[NV];
   float u[NV][VEC], z[NV][VEC];
-  float sum = 0.f;
+  float sum = 0.f, none = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (l + i * lanes) * VEC;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) u[i][j] = z[i][j] = 0.f;
+    rx[i].zero();
+    rz[i].zero();
     if (on && c < Cg) {
-      load_vec<BF16, VEC>(a.x, row * a.x_row + g * Cg + c, u[i]);
-      if (a.gate) load_vec<BF16, VEC>(a.z, row * a.z_row + g * Cg + c, z[i]);
+      rx[i].load(a.x, row * a.x_row + g * Cg + c);
+      if (F::gate(a)) rz[i].load(a.z, row * a.z_row + g * Cg + c);
     }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      if (a.gate) z[i][j] *= sigmoid(z[i][j]);
-      if (a.gate == kGateBefore) u[i][j] *= z[i][j];
+      u[i][j] = rx[i][j];
+      z[i][j] = 0.f;
+      if (F::gate(a)) z[i][j] = rz[i][j] * sigmoid(rz[i][j]);
+      if (F::gate(a) == kGateBefore) u[i][j] *= z[i][j];
       sum += u[i][j];
     }
   const float inv = 1.f / (float)Cg;
-  const float mean = a.center ? group_total(sum, lanes, red) * inv : 0.f;
+  float mean = 0.f;
+  if (a.center) {
+    group_totals(sum, none, lanes, red, 0);
+    mean = sum * inv;
+  }
   float sq = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -174,7 +227,8 @@ __global__ __launch_bounds__(kThreads) void norm_row_kernel(NormArgs a, int lane
       sq += u[i][j] * u[i][j];
     }
   }
-  const float rstd = 1.f / sqrtf(group_total(sq, lanes, red) * inv + a.eps);
+  group_totals(sq, none, lanes, red, 1);
+  const float rstd = 1.f / sqrtf(sq * inv + a.eps);
   if (!on) return;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -184,7 +238,7 @@ __global__ __launch_bounds__(kThreads) void norm_row_kernel(NormArgs a, int lane
     load_par<VEC>(a.w, g * Cg + c, 1.f, w);
     load_par<VEC>(a.bias, g * Cg + c, 0.f, b);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) u[i][j] = finish(a, u[i][j] * rstd * w[j] + b[j], z[i][j]);
+    for (int j = 0; j < VEC; ++j) u[i][j] = finish<F>(a, u[i][j] * rstd * w[j] + b[j], z[i][j]);
     store_vec<BF16, VEC>(a.y, row * a.C + g * Cg + c, u[i]);
   }
   if (a.stats && l == 0) {
@@ -195,11 +249,14 @@ __global__ __launch_bounds__(kThreads) void norm_row_kernel(NormArgs a, int lane
 
 // Backwards: `lanes` threads keep one group and walk rows, so that dw and
 // dbias of their channels stay in registers; each leaves one row of partial
-// sums in ws ([part][2][C]).
-template <bool BF16, int VEC, int NV>
-__global__ __launch_bounds__(kThreads) void norm_row_bwd_kernel(NormArgs a, int lanes, int groups, int rows, int row_blocks) {
-  __shared__ float red[kThreads / 64];
-  const int Cg = a.C / a.G, l = threadIdx.x & (lanes - 1), worker = threadIdx.x / lanes;
+// sums in ws ([part][2][C]). The next row's loads are issued before this row's
+// sums are taken.
+template <bool BF16, int VEC, int NV, int GATE, bool SILU, bool WHOLE>
+__global__ __launch_bounds__(WHOLE ? 1024 : kThreads) void norm_row_bwd_kernel(NormArgs a, int lanes, int groups, int rows, int row_blocks) {
+  using F = Form<GATE, SILU>;
+  __shared__ float red[4 * kMaxWaves];
+  const int Cg = a.C / a.G;
+  const int l = WHOLE ? (int)threadIdx.x : (int)threadIdx.x & (lanes - 1), worker = WHOLE ? 0 : (int)threadIdx.x / lanes;
   const int tiles = (a.G + groups - 1) / groups;
   const int g = (int)(blockIdx.x % tiles) * groups + worker % groups;
   const int part = (int)(blockIdx.x / tiles) * rows + worker / groups;
@@ -207,55 +264,83 @@ __global__ __launch_bounds__(kThreads) void norm_row_bwd_kernel(NormArgs a, int 
   const bool on = worker < groups * rows && g < a.G;
   const int c0 = (on ? g : 0) * Cg;
   const float inv = 1.f / (float)Cg;
-  float dw[NV][VEC], db[NV][VEC];
+  float dw[NV][VEC], db[NV][VEC], w[NV][VEC], b[NV][VEC];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    const int c = (l + i * lanes) * VEC;
+    load_par<VEC>(a.w, c0 + (c < Cg ? c : 0), 1.f, w[i]);
+    load_par<VEC>(a.bias, c0 + (c < Cg ? c : 0), 0.f, b[i]);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) dw[i][j] = db[i][j] = 0.f;
-  // Every thread of the workgroup makes the same number of rounds (the sums meet at barriers).
-  for (long r0 = 0; r0 < a.n; r0 += parts) {
+  }
+  Raw<BF16, VEC> nx[NV], nz[NV], ng[NV];
+  float nmean = 0.f, nrstd = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    nx[i].zero();
+    nz[i].zero();
+    ng[i].zero();
+  }
+  auto fetch = [&](long row) {
+    if (!on || row >= a.n) return;
+    nmean = a.stats[2 * (row * a.G + g)];
+    nrstd = a.stats[2 * (row * a.G + g) + 1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (l + i * lanes) * VEC;
+      if (c >= Cg) break;
+      nx[i].load(a.x, row * a.x_row + c0 + c);
+      if (F::gate(a)) nz[i].load(a.z, row * a.z_row + c0 + c);
+      ng[i].load(a.dy, row * a.C + c0 + c);
+    }
+  };
+  fetch(part);
+  int half = 0;
+  // Every thread of the workgroup makes the same number of rounds (the sums meet at a barrier).
+  for (long r0 = 0; r0 < a.n; r0 += parts, half ^= 1) {
     const long row = r0 + part;
     const bool live = on && row < a.n;
-    float xh[NV][VEC], g1[NV][VEC], zz[NV][VEC], gu[NV][VEC];
-    float mean = 0.f, rstd = 0.f;
-    if (live) {
-      mean = a.stats[2 * (row * a.G + g)];
-      rstd = a.stats[2 * (row * a.G + g) + 1];
+    Raw<BF16, VEC> x[NV], z[NV], dy[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      x[i] = nx[i];
+      z[i] = nz[i];
+      dy[i] = ng[i];
     }
+    const float mean = nmean, rstd = nrstd;
+    fetch(row + parts);
+    // g w and xh; with the gate before also silu(z) and x silu'(z). dz of a gate after is final here.
+    float xh[NV][VEC], gw[NV][VEC], p[NV][VEC], q[NV][VEC];
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (l + i * lanes) * VEC;
-      float x[VEC], w[VEC], b[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) x[j] = zz[i][j] = g1[i][j] = 0.f;
       const bool in = live && c < Cg;
-      if (in) {
-        load_vec<BF16, VEC>(a.x, row * a.x_row + c0 + c, x);
-        if (a.gate) load_vec<BF16, VEC>(a.z, row * a.z_row + c0 + c, zz[i]);
-        load_vec<BF16, VEC>(a.dy, row * a.C + c0 + c, g1[i]);
-      }
-      const int cp = c < Cg ? c : 0;
-      load_par<VEC>(a.w, c0 + cp, 1.f, w);
-      load_par<VEC>(a.bias, c0 + cp, 0.f, b);
+      float dzv[VEC];
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const float u = a.gate == kGateBefore ? x[j] * zz[i][j] * sigmoid(zz[i][j]) : x[j];
-        gu[i][j] = x[j];
-        xh[i][j] = in ? (u - mean) * rstd : 0.f;
-        float dz = 0.f;
-        const float gt = unfinish(a, xh[i][j] * w[j] + b[j], zz[i][j], g1[i][j], dz);
-        if (a.gate == kGateAfter) gu[i][j] = dz;
+        float u = x[i][j], dz = 0.f;
+        if (F::gate(a) == kGateBefore) {
+          const float s = sigmoid(z[i][j]);
+          p[i][j] = z[i][j] * s;
+          q[i][j] = u * (s + p[i][j] * (1.f - s));
+          u *= p[i][j];
+        }
+        xh[i][j] = (u - mean) * rstd;
+        float gt = unfinish<F>(a, xh[i][j] * w[i][j] + b[i][j], z[i][j], dy[i][j], dz);
+        dzv[j] = dz;
+        if (!in) xh[i][j] = gt = 0.f;
         dw[i][j] += gt * xh[i][j];
         db[i][j] += gt;
-        g1[i][j] = gt * w[j];
-        s0 += g1[i][j];
-        s1 += g1[i][j] * xh[i][j];
+        gw[i][j] = gt * w[i][j];
+        s0 += gw[i][j];
+        s1 += gw[i][j] * xh[i][j];
       }
+      if (F::gate(a) == kGateAfter && in) store_vec<BF16, VEC>(a.dz, row * a.C + c0 + c, dzv);
     }
-    const float m0 = a.center ? group_total(s0, lanes, red) * inv : 0.f;
-    const float m1 = group_total(s1, lanes, red) * inv;
+    group_totals(s0, s1, lanes, red, half);
     if (!live) continue;
+    const float m0 = a.center ? s0 * inv : 0.f, m1 = s1 * inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (l + i * lanes) * VEC;
@@ -263,17 +348,14 @@ __global__ __launch_bounds__(kThreads) void norm_row_bwd_kernel(NormArgs a, int 
       float dx[VEC], dz[VEC];
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const float du = rstd * (g1[i][j] - m0 - xh[i][j] * m1);
-        dx[j] = du;
-        dz[j] = gu[i][j];
-        if (a.gate == kGateBefore) {
-          const float s = sigmoid(zz[i][j]);
-          dz[j] = du * gu[i][j] * silu_slope(zz[i][j], s);
-          dx[j] = du * zz[i][j] * s;
+        dx[j] = rstd * (gw[i][j] - m0 - xh[i][j] * m1);
+        if (F::gate(a) == kGateBefore) {
+          dz[j] = dx[j] * q[i][j];
+          dx[j] *= p[i][j];
         }
       }
       store_vec<BF16, VEC>(a.dx, row * a.C + c0 + c, dx);
-      if (a.gate) store_vec<BF16, VEC>(a.dz, row * a.C + c0 + c, dz);
+      if (F::gate(a) == kGateBefore) store_vec<BF16, VEC>(a.dz, row * a.C + c0 + c, dz);
     }
   }
   if (!on) return;
@@ -283,35 +365,39 @@ __global__ __launch_bounds__(kThreads) void norm_row_bwd_kernel(NormArgs a, int 
     if (c >= Cg) break;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      a.ws[((long)part * 2) * a.C + c0 + c + j] = dw[i][j];
-      a.ws[((long)part * 2 + 1) * a.C + c0 + c + j] = db[i][j];
+      if (a.dw) a.ws[((long)part * 2) * a.C + c0 + c + j] = dw[i][j];
+      if (a.db) a.ws[((long)part * 2 + 1) * a.C + c0 + c + j] = db[i][j];
     }
   }
 }
 
-// dw[c] = sum over parts of ws[part][0][c], dbias likewise: 32 channels by 8
-// lanes of parts a workgroup, joined in a fixed order.
+// out[c] = sum over parts of ws[part][which][c] (which = blockIdx.y: dw or
+// dbias): 16 channels by 16 lanes of parts a workgroup, joined in a fixed order.
 __global__ __launch_bounds__(kThreads) void norm_sum_parts_kernel(const float* __restrict__ ws, int parts, int C,
                                                                   float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float acc[2][8][33];
-  const int cl = threadIdx.x & 31, pl = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + cl;
-  float s0 = 0.f, s1 = 0.f;
-  if (c < C)
-    for (int p = pl; p < parts; p += 8) {
-      s0 += ws[((long)p * 2) * C + c];
-      s1 += ws[((long)p * 2 + 1) * C + c];
-    }
-  acc[0][pl][cl] = s0;
-  acc[1][pl][cl] = s1;
+  __shared__ float acc[16][17];
+  float* out = blockIdx.y ? db : dw;
+  if (!out) return;
+  const int cl = threadIdx.x & 15, pl = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + cl;
+  const float* src = ws + (long)blockIdx.y * C + (c < C ? c : 0);
+  constexpr int kAhead = 8;
+  float s[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) s[k] = 0.f;
+  int p = pl;
+  for (; p + 16 * (kAhead - 1) < parts; p += 16 * kAhead)
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) s[k] += src[(long)(p + 16 * k) * 2 * C];
+  for (; p < parts; p += 16) s[0] += src[(long)p * 2 * C];
+#pragma unroll
+  for (int k = 1; k < kAhead; ++k) s[0] += s[k];
+  acc[pl][cl] = s[0];
   __syncthreads();
   if (pl == 0 && c < C) {
-    for (int p = 1; p < 8; ++p) {
-      s0 += acc[0][p][cl];
-      s1 += acc[1][p][cl];
-    }
-    if (dw) dw[c] = s0;
-    if (db) db[c] = s1;
+    float t = 0.f;
+    for (int k = 0; k < 16; ++k) t += acc[k][cl];
+    out[c] = t;
   }
 }
 
@@ -478,7 +564,7 @@ __global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a, Slabs 
     for (int j = 0; j < VEC; ++j) {
       const float sz = a.gate ? z[j] * sigmoid(z[j]) : 0.f;
       const float v = a.gate == kGateBefore ? u[j] * sz : u[j];
-      u[j] = finish(a, (v - mean[j]) * rstd[j] * w[j] + bias[j], sz);
+      u[j] = finish<AnyForm>(a, (v - mean[j]) * rstd[j] * w[j] + bias[j], sz);
     }
     store_vec<BF16, VEC>(a.y, row * a.C + c, u);
   }
@@ -518,7 +604,7 @@ __global__ __launch_bounds__(kThreads) void norm_slab_bwd_kernel(NormArgs a, Sla
         const float v = a.gate == kGateBefore ? u[j] * z[j] * sigmoid(z[j]) : u[j];
         const float xh = (v - mean[j]) * rstd[j];
         float dz;
-        const float gt = unfinish(a, xh * w[j] + bias[j], a.gate ? z[j] : 0.f, dy[j], dz);
+        const float gt = unfinish<AnyForm>(a, xh * w[j] + bias[j], a.gate ? z[j] : 0.f, dy[j], dz);
         s0[j] += gt * xh;
         s1[j] += gt;
       }
@@ -591,7 +677,7 @@ __global__ __launch_bounds__(kThreads) void norm_apply_bwd_kernel(NormArgs a, Sl
       const float u = a.gate == kGateBefore ? x[j] * z[j] * sg : x[j];
       const float xh = (u - mean[j]) * rstd[j];
       dzv[j] = 0.f;
-      const float gt = unfinish(a, xh * w[j] + bias[j], a.gate ? z[j] : 0.f, dy[j], dzv[j]);
+      const float gt = unfinish<AnyForm>(a, xh * w[j] + bias[j], a.gate ? z[j] : 0.f, dy[j], dzv[j]);
       dx[j] = rstd[j] * (gt * w[j] - m0[j] - xh * m1[j]);
       if (a.gate == kGateBefore) {
         dzv[j] = dx[j] * x[j] * silu_slope(z[j], sg);
@@ -603,42 +689,53 @@ __global__ __launch_bounds__(kThreads) void norm_apply_bwd_kernel(NormArgs a, Sl
   }
 }
 
-// Whether (and how) a group fits the registers of the threads that share it.
+// Whether (and how) a group fits the registers of the threads that share it:
+// up to 64 pieces a power of two of lanes, one piece each; above that the
+// workgroup, in as many whole waves as the pieces fill (up to 16), so that no
+// lane idles for a power of two. Beyond that (8192 channels in pieces of 8,
+// 2048 in single ones, two a lane) the slab form takes over.
 struct RowPlan {
-  int vec, nv, lanes;
+  int vec, nv, lanes, threads;
 };
 bool row_plan(const NormArgs& a, RowPlan* p) {
   if (a.s != 1) return false;
   const int Cg = a.C / a.G;
   p->vec = a.vec && Cg % 8 == 0 ? 8 : 1;
   const int pieces = Cg / p->vec;
-  p->lanes = 1;
-  while (p->lanes < pieces && p->lanes < kThreads) p->lanes *= 2;
-  p->nv = (pieces + p->lanes - 1) / p->lanes;
-  if (p->nv > 4) return false;
-  if (p->nv == 3) p->nv = 4;
+  p->threads = kThreads;
+  p->nv = 1;
+  if (pieces <= 64) {
+    p->lanes = 1;
+    while (p->lanes < pieces) p->lanes *= 2;
+    return true;
+  }
+  p->nv = (pieces + 1023) / 1024;
+  if (p->nv > (p->vec == 8 ? 1 : 2)) return false;
+  p->lanes = ((pieces + p->nv - 1) / p->nv + 63) / 64 * 64;
+  p->threads = p->lanes;
   return true;
 }
 
-// Rows of partial sums of the one-position backward pass: enough for four
-// workgroups a CU, no more than there are rows.
+// Rows of partial sums of the one-position backward pass: workgroups of eight
+// waves for every CU, which with the next row's loads in flight keep the
+// memory busy, and no more rows than there are.
 struct RowParts {
   int groups, rows, tiles, blocks;
 };
-RowParts row_parts(const NormArgs& a, int lanes) {
+RowParts row_parts(const NormArgs& a, const RowPlan& p) {
   RowParts r;
-  const int workers = kThreads / lanes;
+  const int workers = p.lanes > 64 ? 1 : kThreads / p.lanes;
   r.groups = a.G < workers ? a.G : workers;
   r.rows = workers / r.groups;
   r.tiles = (a.G + r.groups - 1) / r.groups;
-  long blocks = 1024 / r.tiles;
+  const int want = kCus * (p.threads > 512 ? 1 : 512 / p.threads);
+  long blocks = (want + r.tiles - 1) / r.tiles;
   const long most = (a.n + r.rows - 1) / r.rows;
   if (blocks > most) blocks = most;
-  if (blocks * r.rows > 1024) blocks = 1024 / r.rows;
+  if (blocks * r.rows > kMaxParts) blocks = kMaxParts / r.rows;
   r.blocks = blocks < 1 ? 1 : (int)blocks;
   return r;
 }
-
 
 }  // namespace
 
@@ -652,10 +749,9 @@ size_t norm_ws_floats(long n, long s, int C, int G, bool backward) {
     if (f > most) most = f;
   }
   if (s == 1) {
-    const size_t rows = n < 1024 ? (size_t)n : 1024;
-    const size_t parts = backward ? 2 * (rows + 256) * C : 0;
-    // a group that fits no registers takes the slab form
-    if (C / G <= 1024) return parts;
+    const size_t rows = (n < kMaxParts ? (size_t)n : kMaxParts) + kThreads;
+    const size_t parts = backward ? 2 * rows * C : 0;
+    if (C / G <= 2048) return parts;  // fits registers with any alignment
     if (parts > most) most = parts;
   }
   return most;
@@ -663,28 +759,41 @@ size_t norm_ws_floats(long n, long s, int C, int G, bool backward) {
 
 namespace {
 
-template <bool BF16, int VEC>
-void row_launch(const NormArgs& a, const RowPlan& p, hipStream_t stream) {
-  const long workers = kThreads / p.lanes;
-  const dim3 grid((unsigned)((a.n * a.G + workers - 1) / workers));
-  if (p.nv == 1) hipLaunchKernelGGL((norm_row_kernel<BF16, VEC, 1>), grid, dim3(kThreads), 0, stream, a, p.lanes);
-  else if (p.nv == 2) hipLaunchKernelGGL((norm_row_kernel<BF16, VEC, 2>), grid, dim3(kThreads), 0, stream, a, p.lanes);
-  else hipLaunchKernelGGL((norm_row_kernel<BF16, VEC, 4>), grid, dim3(kThreads), 0, stream, a, p.lanes);
+template <bool BF16, int VEC, int NV, int GATE, bool SILU, bool WHOLE>
+void row_form(const NormArgs& a, const RowPlan& p, bool backward, hipStream_t stream) {
+  const dim3 block((unsigned)p.threads);
+  if (!backward) {
+    const long workers = p.lanes > 64 ? 1 : kThreads / p.lanes;
+    const dim3 grid((unsigned)((a.n * a.G + workers - 1) / workers));
+    hipLaunchKernelGGL((norm_row_kernel<BF16, VEC, NV, GATE, SILU, WHOLE>), grid, block, 0, stream, a, p.lanes);
+    return;
+  }
+  const RowParts r = row_parts(a, p);
+  hipLaunchKernelGGL((norm_row_bwd_kernel<BF16, VEC, NV, GATE, SILU, WHOLE>), dim3((unsigned)(r.tiles * r.blocks)), block, 0,
+                     stream, a, p.lanes, r.groups, r.rows, r.blocks);
+  if (a.dw || a.db)
+    hipLaunchKernelGGL(norm_sum_parts_kernel, dim3((unsigned)((a.C + 15) / 16), 2), dim3(kThreads), 0, stream, a.ws,
+                       r.rows * r.blocks, a.C, a.dw, a.db);
 }
 
-template <bool BF16, int VEC>
-void row_bwd_launch(const NormArgs& a, const RowPlan& p, hipStream_t stream) {
-  const RowParts r = row_parts(a, p.lanes);
-  const dim3 grid((unsigned)(r.tiles * r.blocks)), block(kThreads);
-  if (p.nv == 1)
-    hipLaunchKernelGGL((norm_row_bwd_kernel<BF16, VEC, 1>), grid, block, 0, stream, a, p.lanes, r.groups, r.rows, r.blocks);
-  else if (p.nv == 2)
-    hipLaunchKernelGGL((norm_row_bwd_kernel<BF16, VEC, 2>), grid, block, 0, stream, a, p.lanes, r.groups, r.rows, r.blocks);
-  else
-    hipLaunchKernelGGL((norm_row_bwd_kernel<BF16, VEC, 4>), grid, block, 0, stream, a, p.lanes, r.groups, r.rows, r.blocks);
-  if (a.dw || a.db)
-    hipLaunchKernelGGL(norm_sum_parts_kernel, dim3((unsigned)((a.C + 31) / 32)), block, 0, stream, a.ws, r.rows * r.blocks,
-                       a.C, a.dw, a.db);
+// Pieces of eight: the form is fixed at compile time, as the arithmetic of the
+// gate is a good part of the time; single channels read it from the arguments.
+template <bool BF16, int VEC, bool WHOLE>
+void row_launch(const NormArgs& a, const RowPlan& p, bool backward, hipStream_t stream) {
+  if constexpr (VEC == 8) {
+    switch (2 * a.gate + (a.silu ? 1 : 0)) {
+      case 0: return row_form<BF16, 8, 1, 0, false, WHOLE>(a, p, backward, stream);
+      case 1: return row_form<BF16, 8, 1, 0, true, WHOLE>(a, p, backward, stream);
+      case 2: return row_form<BF16, 8, 1, 1, false, WHOLE>(a, p, backward, stream);
+      case 3: return row_form<BF16, 8, 1, 1, true, WHOLE>(a, p, backward, stream);
+      case 4: return row_form<BF16, 8, 1, 2, false, WHOLE>(a, p, backward, stream);
+      default: return row_form<BF16, 8, 1, 2, true, WHOLE>(a, p, backward, stream);
+    }
+  } else if (p.nv == 1) {
+    row_form<BF16, 1, 1, -1, false, WHOLE>(a, p, backward, stream);
+  } else {
+    row_form<BF16, 1, 2, -1, false, true>(a, p, backward, stream);
+  }
 }
 
 template <bool BF16, int VEC>
@@ -706,7 +815,7 @@ void slab_bwd_launch(const NormArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(norm_join_bwd_kernel, groups, block, 0, stream, a, b.count, means);
   hipLaunchKernelGGL((norm_apply_bwd_kernel<BF16, VEC>), grid, block, 0, stream, a, b, (const float*)means);
   if (a.dw || a.db)
-    hipLaunchKernelGGL(norm_sum_parts_kernel, dim3((unsigned)((a.C + 31) / 32)), block, 0, stream, a.ws,
+    hipLaunchKernelGGL(norm_sum_parts_kernel, dim3((unsigned)((a.C + 15) / 16), 2), block, 0, stream, a.ws,
                        (int)(a.n * b.count), a.C, a.dw, a.db);
 }
 
@@ -729,7 +838,8 @@ hipError_t launch_group_norm(const NormArgs& a, hipStream_t stream) {
   RowPlan p;
   const bool row = row_plan(a, &p);
   by_type(a.bf16, row ? p.vec == 8 : a.vec, [&](auto bf, auto vec) {
-    if (row) row_launch<decltype(bf)::value, decltype(vec)::value>(a, p, stream);
+    if (row && p.lanes > 64) row_launch<decltype(bf)::value, decltype(vec)::value, true>(a, p, false, stream);
+    else if (row) row_launch<decltype(bf)::value, decltype(vec)::value, false>(a, p, false, stream);
     else slab_launch<decltype(bf)::value, decltype(vec)::value>(a, stream);
   });
   return hipGetLastError();
@@ -739,7 +849,8 @@ hipError_t launch_group_norm_bwd(const NormArgs& a, hipStream_t stream) {
   RowPlan p;
   const bool row = row_plan(a, &p);
   by_type(a.bf16, row ? p.vec == 8 : a.vec, [&](auto bf, auto vec) {
-    if (row) row_bwd_launch<decltype(bf)::value, decltype(vec)::value>(a, p, stream);
+    if (row && p.lanes > 64) row_launch<decltype(bf)::value, decltype(vec)::value, true>(a, p, true, stream);
+    else if (row) row_launch<decltype(bf)::value, decltype(vec)::value, false>(a, p, true, stream);
     else slab_bwd_launch<decltype(bf)::value, decltype(vec)::value>(a, stream);
   });
   return hipGetLastError();
