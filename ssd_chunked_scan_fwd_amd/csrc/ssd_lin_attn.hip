@@ -144,7 +144,7 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
 // ----------------------------------------------------------------------------
 // Entering states: for blocks b = 0, 1, ... of a sequence, with own sums s_b,
 // D = initial state; states[b] = D (b >= 1); D = lam^n_b D + s_b. Four
-// elements a thread; the next block's sum is loaded ahead.
+// elements a thread; kAhead blocks' sums are in flight at a time.
 // ----------------------------------------------------------------------------
 __global__ __launch_bounds__(256) void lin_passing_kernel(LinScan a) {
   const int h = blockIdx.y, s = blockIdx.z;
@@ -177,13 +177,20 @@ __global__ __launch_bounds__(256) void lin_passing_kernel(LinScan a) {
   const float w = fast_exp2(g * (float)a.L);
   const long step = (long)a.H * mat;
   float* at = a.states + (slot0 * a.H + h) * mat + e;
-  f32x4 own = *reinterpret_cast<const f32x4*>(at);
-  for (int b = 1; b < nb; ++b) {
-    f32x4 next = {0.f, 0.f, 0.f, 0.f};
-    if (b + 1 < nb) next = *reinterpret_cast<const f32x4*>(at + b * step);
-    D = D * (b == 1 ? w0 : w) + own;
-    *reinterpret_cast<f32x4*>(at + b * step) = D;
-    own = next;
+  constexpr int kAhead = 8;
+  f32x4 own = *reinterpret_cast<const f32x4*>(at);   // of block b0, before its place is taken by D
+  for (int b0 = 0; b0 + 1 < nb; b0 += kAhead) {
+    f32x4 next[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) next[k] = *reinterpret_cast<const f32x4*>(at + min(b0 + k + 1, nb - 1) * step);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int b = b0 + k + 1;
+      if (b >= nb) break;
+      D = D * (b == 1 ? w0 : w) + own;
+      *reinterpret_cast<f32x4*>(at + b * step) = D;
+      own = next[k];
+    }
   }
 }
 

@@ -118,9 +118,15 @@ __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void lin_mfma_kernel(LinScan 
     }
   };
 
-  if (total > 0) load(0);
-  for (int t0 = 0; t0 < total; t0 += kC) {
+  // The blocks' own sums walk their chunks backwards, weighting each V by its whole
+  // distance to the block's end: the scan, which walks forwards and comes next,
+  // finds the rows that were read last in the memory-side cache.
+  const int chunks = (total + kC - 1) / kC;
+  if (chunks > 0) load(STATE_ONLY ? (chunks - 1) * kC : 0);
+  for (int ci = 0; ci < chunks; ++ci) {
+    const int t0 = (STATE_ONLY ? chunks - 1 - ci : ci) * kC;
     const int n = min(kC, total - t0);
+    const int after = STATE_ONLY ? total - t0 - n : 0;  // tokens of the block behind this chunk
     const int lead = a.rev && pos0 + t0 == 0 ? 0 : 1;  // the state handed to a reversed scan is not decayed first
     __syncthreads();
 #pragma unroll
@@ -162,7 +168,7 @@ __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void lin_mfma_kernel(LinScan 
         }
       }
     }
-    if (t0 + kC < total) load(t0 + kC);
+    if (ci + 1 < chunks) load(STATE_ONLY ? t0 - kC : t0 + kC);
 
     u32x4 vf[NB][2];
 #pragma unroll
@@ -231,7 +237,7 @@ __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void lin_mfma_kernel(LinScan 
     for (int kp = 0; kp < 2; ++kp) {
       float w[8];
 #pragma unroll
-      for (int s = 0; s < 8; ++s) w[s] = fast_exp2(g2 * (float)max(n - 1 - (32 * kp + 16 * (s >> 2) + 4 * g + (s & 3)), 0));
+      for (int s = 0; s < 8; ++s) w[s] = fast_exp2(g2 * (float)(after + max(n - 1 - (32 * kp + 16 * (s >> 2) + 4 * g + (s & 3)), 0)));
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -246,7 +252,8 @@ __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void lin_mfma_kernel(LinScan 
 #pragma unroll
     for (int b = 0; b < 2 * KB; ++b) {
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) S[nb][b] *= keep;
+      for (int nb = 0; nb < NB; ++nb)
+        if (!STATE_ONLY) S[nb][b] *= keep;
 #pragma unroll
       for (int kp = 0; kp < 2; ++kp) {
         const u32x4 kf = frag_k_rows_accpair(Ks, kPitchK, 32 * kp, 16 * b, lane);
