@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libssd_mi355x.so")
 SOURCES = ["ssd_api.cpp", "ssd_cumsum_passing.hip", "ssd_chunk_state.hip", "ssd_chunk_scan.hip", "ssd_bwd.hip", "ssd_bwd_chunk.hip", "ssd_bwd_mamba2.hip",
-           "ssd_layer_api.cpp", "ssd_lin_attn.hip", "ssd_lin_scan.hip", "ssd_group_norm.hip", "ssd_pages.hip"]
+           "ssd_layer_api.cpp", "ssd_lin_attn.hip", "ssd_lin_scan.hip", "ssd_lin_bwd.hip", "ssd_group_norm.hip", "ssd_pages.hip"]
 
 
 def hipcc() -> str:

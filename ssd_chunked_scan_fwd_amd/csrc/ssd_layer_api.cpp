@@ -68,8 +68,8 @@ struct LinPlan {
   int64_t spr, slots;
   size_t state_bytes;  // 0: no sequence is cut
 };
-ssd_status lin_plan(const ssd_lin_shape* s, int dk, int dv, LinPlan* p) {
-  p->L = ssd::lin_block_tokens(s->batch, s->seqlen, s->num_seqs, s->nheads, dk, dv, s->dtype == SSD_DTYPE_BF16);
+ssd_status lin_plan(const ssd_lin_shape* s, int dk, int dv, LinPlan* p, bool kv = false) {
+  p->L = ssd::lin_block_tokens(s->batch, s->seqlen, s->num_seqs, s->nheads, dk, dv, s->dtype == SSD_DTYPE_BF16, kv);
   p->spr = ssd::lin_slots_per_row(s->seqlen, s->num_seqs, p->L);
   p->slots = s->num_seqs > 0 ? p->spr : p->spr * s->batch;
   if (p->slots * s->nheads > INT32_MAX / 64) return SSD_ERR_UNSUPPORTED;  // workgroups of one launch
@@ -79,6 +79,7 @@ ssd_status lin_plan(const ssd_lin_shape* s, int dk, int dv, LinPlan* p) {
 
 struct LinBwdLayout {
   LinPlan dq, dv, dk;
+  bool kv;  // dk and dv come from one scan
   size_t st_dq, st_dv, st_dk, part_k, part_v, total;
 };
 ssd_status lin_bwd_layout(const ssd_lin_shape* s, LinBwdLayout* L) {
@@ -86,8 +87,10 @@ ssd_status lin_bwd_layout(const ssd_lin_shape* s, LinBwdLayout* L) {
   ssd_status st = check_lin(s, &d);
   if (st != SSD_OK) return st;
   if ((st = lin_plan(s, s->dv, s->dk, &L->dq)) != SSD_OK) return st;
-  if ((st = lin_plan(s, s->dk, s->dv, &L->dv)) != SSD_OK) return st;
-  if ((st = lin_plan(s, s->dv, s->dk, &L->dk)) != SSD_OK) return st;
+  L->kv = ssd::lin_kv_supported(s->dk, s->dv, s->dtype == SSD_DTYPE_BF16);
+  if ((st = lin_plan(s, s->dk, s->dv, &L->dv, L->kv)) != SSD_OK) return st;
+  L->dk = LinPlan{};
+  if (!L->kv && (st = lin_plan(s, s->dv, s->dk, &L->dk)) != SSD_OK) return st;
   size_t off = 0;
   auto take = [&](size_t b) {
     const size_t o = off;
@@ -261,57 +264,53 @@ ssd_status ssd_lin_attn_bwd(const void* q, const void* k, const void* v, const f
   const int H = shape->nheads, Hk = shape->nkv_heads, rep = H / Hk;
   const ssd::LinOperand oq{q, (long)d.q_row, 1}, ok{k, (long)d.k_row, rep}, ov{v, (long)d.v_row, rep},
       og{d_o, (long)H * shape->dv, 1};
-  hipError_t e;
-  {  // dq
-    ssd::LinScan a = base_scan(shape, log_decay, cu_seqlens, scale);
-    a.q = og;
-    a.k = ov;
-    a.v = ok;
-    a.o = dq;
-    a.dk = shape->dv;
-    a.dv = shape->dk;
-    a.init = initial_state;
-    a.init_tr = 1;
-    set_plan(&a, L.dq, ws + L.st_dq);
-    e = ssd::launch_lin_scan(a, hs);
-    if (e != hipSuccess) return SSD_ERR_HIP;
-  }
+  ssd::LinScan sq = base_scan(shape, log_decay, cu_seqlens, scale);
+  sq.q = og;
+  sq.k = ov;
+  sq.v = ok;
+  sq.o = dq;
+  sq.dk = shape->dv;
+  sq.dv = shape->dk;
+  sq.init = initial_state;
+  sq.init_tr = 1;
+  set_plan(&sq, L.dq, ws + L.st_dq);
   // The reversed scans carry the adjoint divided by `scale`, which multiplies their outputs.
-  {  // dv and the initial state's gradient
-    ssd::LinScan a = base_scan(shape, log_decay, cu_seqlens, scale);
-    a.q = ok;
-    a.k = oq;
-    a.v = og;
-    a.o = rep > 1 ? static_cast<void*>(ws + L.part_v) : dv;
-    a.o_f32 = rep > 1;
-    a.dk = shape->dk;
-    a.dv = shape->dv;
-    a.init = dfinal_state;
-    a.init_scale = 1.f / scale;
-    a.fin = dinitial_state;
-    a.fin_scale = scale;
-    a.rev = 1;
-    set_plan(&a, L.dv, ws + L.st_dv);
-    e = ssd::launch_lin_scan(a, hs);
-    if (e != hipSuccess) return SSD_ERR_HIP;
+  void* const dv_out = rep > 1 ? static_cast<void*>(ws + L.part_v) : dv;
+  void* const dk_out = rep > 1 ? static_cast<void*>(ws + L.part_k) : dk;
+  ssd::LinScan sv = base_scan(shape, log_decay, cu_seqlens, scale);
+  sv.q = ok;
+  sv.k = oq;
+  sv.v = og;
+  sv.o = dv_out;
+  sv.o_f32 = rep > 1;
+  sv.dk = shape->dk;
+  sv.dv = shape->dv;
+  sv.init = dfinal_state;
+  sv.init_scale = 1.f / scale;
+  sv.fin = dinitial_state;
+  sv.fin_scale = scale;
+  sv.rev = 1;
+  set_plan(&sv, L.dv, ws + L.st_dv);
+  hipError_t e = ssd::launch_lin_states(sq, &sv, hs);
+  if (e == hipSuccess) e = ssd::launch_lin_outputs(sq, hs);
+  if (e == hipSuccess) e = L.kv ? ssd::launch_lin_kv(sv, ov, dk_out, hs) : ssd::launch_lin_outputs(sv, hs);
+  if (e == hipSuccess && !L.kv) {
+    ssd::LinScan sk = base_scan(shape, log_decay, cu_seqlens, scale);
+    sk.q = ov;
+    sk.k = og;
+    sk.v = oq;
+    sk.o = dk_out;
+    sk.o_f32 = rep > 1;
+    sk.dk = shape->dv;
+    sk.dv = shape->dk;
+    sk.init = dfinal_state;
+    sk.init_scale = 1.f / scale;
+    sk.init_tr = 1;
+    sk.rev = 1;
+    set_plan(&sk, L.dk, ws + L.st_dk);
+    e = ssd::launch_lin_scan(sk, hs);
   }
-  {  // dk
-    ssd::LinScan a = base_scan(shape, log_decay, cu_seqlens, scale);
-    a.q = ov;
-    a.k = og;
-    a.v = oq;
-    a.o = rep > 1 ? static_cast<void*>(ws + L.part_k) : dk;
-    a.o_f32 = rep > 1;
-    a.dk = shape->dv;
-    a.dv = shape->dk;
-    a.init = dfinal_state;
-    a.init_scale = 1.f / scale;
-    a.init_tr = 1;
-    a.rev = 1;
-    set_plan(&a, L.dk, ws + L.st_dk);
-    e = ssd::launch_lin_scan(a, hs);
-    if (e != hipSuccess) return SSD_ERR_HIP;
-  }
+  if (e != hipSuccess) return SSD_ERR_HIP;
   if (rep > 1) {
     const int bf16 = shape->dtype == SSD_DTYPE_BF16;
     e = ssd::launch_lin_share_sum(reinterpret_cast<const float*>(ws + L.part_v), dv, cu_seqlens, shape->num_seqs,

@@ -50,17 +50,29 @@ struct LinScan {
   float* states = nullptr;     // [slots][H][dv][dk]: each block's own sum, then its entering state
 };
 
-// Tokens a block for a scan of these sizes; a value >= T means that no
-// sequence is cut and no block states are needed.
-int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16);
+// Tokens a block for a scan of these sizes (kv: the scan of launch_lin_kv); a
+// value >= T means that no sequence is cut and no block states are needed.
+int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16, bool kv = false);
 inline long lin_slots_per_row(int T, int S, int L) { return S > 0 ? (long)(T / L) + S : (T + (long)L - 1) / L; }
 
 hipError_t launch_lin_scan(const LinScan& a, hipStream_t stream);
+// The two parts of it: the states that enter the blocks (nothing without
+// a.states), for one scan or for two at once, and the outputs.
+hipError_t launch_lin_states(const LinScan& a, const LinScan* b, hipStream_t stream);
+hipError_t launch_lin_outputs(const LinScan& a, hipStream_t stream);
 
 // bf16 operands: the scan on matrix instructions (ssd_lin_scan.hip), either the
 // blocks' own sums or, from the entering states, the outputs.
 int lin_mfma_tile(int dv);
-hipError_t launch_lin_mfma(const LinScan& a, bool states, hipStream_t stream);
+hipError_t launch_lin_mfma(const LinScan& a, hipStream_t stream);
+hipError_t launch_lin_mfma_states(const LinScan& a, const LinScan* b, hipStream_t stream);
+
+// dk and dv of the backward pass in one reversed scan, bf16, dk and dv up to
+// 128 (ssd_lin_bwd.hip): `a` is the scan for dv; `v` and `dk_out` are what dk
+// takes besides.
+bool lin_kv_supported(int dk, int dv, int bf16);
+int lin_kv_target(int dv);
+hipError_t launch_lin_kv(const LinScan& a, const LinOperand& v, void* dk_out, hipStream_t stream);
 
 // out[token][kv head][i] = sum of in over the heads that share it, in head order.
 hipError_t launch_lin_share_sum(const float* in, void* out, const int32_t* cu, int S, long tokens, int T, int H, int Hk,

@@ -146,8 +146,8 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
 // D = initial state; states[b] = D (b >= 1); D = lam^n_b D + s_b. Four
 // elements a thread; kAhead blocks' sums are in flight at a time.
 // ----------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void lin_passing_kernel(LinScan a) {
-  const int h = blockIdx.y, s = blockIdx.z;
+__device__ __forceinline__ void lin_pass(const LinScan& a, int s) {
+  const int h = blockIdx.y;
   const int mat = a.dv * a.dk;
   const int e = 4 * (int)(blockIdx.x * 256 + threadIdx.x);
   long slot0;
@@ -192,6 +192,14 @@ __global__ __launch_bounds__(256) void lin_passing_kernel(LinScan a) {
       own = next[k];
     }
   }
+}
+
+// One scan's states, or two scans' (of equal dv * dk) in the halves of grid.z.
+__global__ __launch_bounds__(256) void lin_passing_kernel(LinScan a) { lin_pass(a, blockIdx.z); }
+__global__ __launch_bounds__(256) void lin_passing2_kernel(LinScan a, LinScan b) {
+  const int half = gridDim.z / 2;
+  if ((int)blockIdx.z < half) lin_pass(a, blockIdx.z);
+  else lin_pass(b, blockIdx.z - half);
 }
 
 // Sum over the heads that share a key head, eight values a thread, in head
@@ -343,11 +351,11 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStep a, int tpr, int p
 
 // Sequences are cut only as far as it takes to fill the chip: every cut costs
 // its state's way through memory, and the products k v^T a second time.
-int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16) {
+int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16, bool kv) {
   const long seqs = S > 0 ? S : batch;
-  const int tile = bf16 ? lin_mfma_tile(dv) : kRecRows;
+  const int tile = kv ? dv : bf16 ? lin_mfma_tile(dv) : kRecRows;
   const long units = (long)H * ((dv + tile - 1) / tile);
-  const long target = bf16 ? 512 : 1024;
+  const long target = kv ? lin_kv_target(dv) : bf16 ? 512 : 1024;
   long L = seqs * units >= target ? T : (long)batch * T * units / target;
   L = (L + 63) / 64 * 64;
   if (L < 64) L = 64;
@@ -355,22 +363,40 @@ int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16) {
   return (int)L;
 }
 
-hipError_t launch_lin_scan(const LinScan& a, hipStream_t stream) {
+namespace {
+dim3 rec_grid(const LinScan& a) {
   const long slots = a.S > 0 ? a.slots_per_row : a.slots_per_row * a.batch;
-  const dim3 grid((unsigned)(slots * a.H * ((a.dv + kRecRows - 1) / kRecRows)));
-  hipError_t e;
-  if (a.states) {
-    if (a.bf16) {
-      if ((e = launch_lin_mfma(a, true, stream)) != hipSuccess) return e;
-    } else {
-      hipLaunchKernelGGL(lin_rec_kernel<true>, grid, dim3(256), 0, stream, a);
-    }
-    const dim3 pg((unsigned)((a.dv * a.dk / 4 + 255) / 256), (unsigned)a.H, (unsigned)(a.S > 0 ? a.S : a.batch));
-    hipLaunchKernelGGL(lin_passing_kernel, pg, dim3(256), 0, stream, a);
+  return dim3((unsigned)(slots * a.H * ((a.dv + kRecRows - 1) / kRecRows)));
+}
+}  // namespace
+
+hipError_t launch_lin_states(const LinScan& a, const LinScan* b, hipStream_t stream) {
+  if (b && !b->states) b = nullptr;
+  if (!a.states) return b ? launch_lin_states(*b, nullptr, stream) : hipSuccess;
+  if (a.bf16) {
+    // The scan with the longer blocks first, so that the shorter ones fill the last round.
+    const hipError_t e = b && b->L > a.L ? launch_lin_mfma_states(*b, &a, stream) : launch_lin_mfma_states(a, b, stream);
+    if (e != hipSuccess) return e;
+  } else {
+    hipLaunchKernelGGL(lin_rec_kernel<true>, rec_grid(a), dim3(256), 0, stream, a);
+    if (b) hipLaunchKernelGGL(lin_rec_kernel<true>, rec_grid(*b), dim3(256), 0, stream, *b);
   }
-  if (a.bf16) return launch_lin_mfma(a, false, stream);
-  hipLaunchKernelGGL(lin_rec_kernel<false>, grid, dim3(256), 0, stream, a);
+  const unsigned seqs = (unsigned)(a.S > 0 ? a.S : a.batch);
+  dim3 grid((unsigned)((a.dv * a.dk / 4 + 255) / 256), (unsigned)a.H, b ? 2 * seqs : seqs);
+  if (b) hipLaunchKernelGGL(lin_passing2_kernel, grid, dim3(256), 0, stream, a, *b);
+  else hipLaunchKernelGGL(lin_passing_kernel, grid, dim3(256), 0, stream, a);
   return hipGetLastError();
+}
+
+hipError_t launch_lin_outputs(const LinScan& a, hipStream_t stream) {
+  if (a.bf16) return launch_lin_mfma(a, stream);
+  hipLaunchKernelGGL(lin_rec_kernel<false>, rec_grid(a), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_lin_scan(const LinScan& a, hipStream_t stream) {
+  const hipError_t e = launch_lin_states(a, nullptr, stream);
+  return e == hipSuccess ? launch_lin_outputs(a, stream) : e;
 }
 
 hipError_t launch_lin_share_sum(const float* in, void* out, const int32_t* cu, int S, long tokens, int T, int H, int Hk,

@@ -23,6 +23,8 @@
 // bounds it once the matrix pipes are a third busy. The next chunk's rows are in flight
 // in registers while this one is computed. Q's loads have the layout of the
 // score product's operand, which so needs no LDS read for it.
+#include <type_traits>
+
 #include "ssd_device.h"
 #include "ssd_lin_attn.h"
 
@@ -34,7 +36,7 @@ constexpr int kC = 64;
 constexpr int kPitchP = lds_pitch(kC);
 
 template <int KB, int NB, bool STATE_ONLY>
-__global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void lin_mfma_kernel(LinScan a) {
+__device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks) {
   constexpr int kDk = 32 * KB, kDv = 64 * NB;
   constexpr int kPitchK = lds_pitch(kDk), kPitchV = lds_pitch(kDv);
   __shared__ __align__(16) uint16_t Ks[kC * kPitchK];
@@ -43,7 +45,7 @@ __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void lin_mfma_kernel(LinScan 
   __shared__ __align__(16) uint16_t Ps[STATE_ONLY ? 8 : kC * kPitchP];
 
   const int tiles = (a.dv + kDv - 1) / kDv;
-  const long u = xcd_unit(blockIdx.x, gridDim.x);
+  const long u = xcd_unit(bid, blocks);
   const int dv0 = (int)(u % tiles) * kDv;
   const int h = (int)((u / tiles) % a.H);
   const long slot = u / ((long)tiles * a.H);
@@ -288,25 +290,63 @@ __global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void lin_mfma_kernel(LinScan 
 }
 
 template <int KB, int NB>
-void launch_mfma(const LinScan& a, bool states, hipStream_t stream) {
-  const long slots = a.S > 0 ? a.slots_per_row : a.slots_per_row * a.batch;
-  const int tiles = (a.dv + 64 * NB - 1) / (64 * NB);
-  const dim3 grid((unsigned)(slots * a.H * tiles)), block(256);
-  if (states) hipLaunchKernelGGL((lin_mfma_kernel<KB, NB, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((lin_mfma_kernel<KB, NB, false>), grid, block, 0, stream, a);
+__global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void lin_mfma_kernel(LinScan a) {
+  lin_mfma<KB, NB, false>(a, blockIdx.x, gridDim.x);
 }
+
+// The blocks' own sums of one scan, or of two: the first `na` workgroups are a's.
+template <int KB, int NB>
+__global__ __launch_bounds__(256, KB <= 4 ? 2 : 1) void lin_mfma_states_kernel(LinScan a, LinScan b, long na) {
+  const bool first = (long)blockIdx.x < na;
+  const LinScan& s = first ? a : b;
+  lin_mfma<KB, NB, true>(s, first ? blockIdx.x : blockIdx.x - na, first ? na : gridDim.x - na);
+}
+
+template <int KB, int NB>
+long mfma_blocks(const LinScan& a) {
+  const long slots = a.S > 0 ? a.slots_per_row : a.slots_per_row * a.batch;
+  return slots * a.H * ((a.dv + 64 * NB - 1) / (64 * NB));
+}
+
+// The instance for sizes dk and dv: f(KB, NB) as integral constants.
+template <typename F>
+void mfma_instance(int dk, int dv, F f) {
+  using std::integral_constant;
+  auto wide = [&](auto kb) {
+    if (lin_mfma_tile(dv) == 128) f(kb, integral_constant<int, 2>{});
+    else f(kb, integral_constant<int, 1>{});
+  };
+  if (dk <= 32) wide(integral_constant<int, 1>{});
+  else if (dk <= 64) wide(integral_constant<int, 2>{});
+  else if (dk <= 128) wide(integral_constant<int, 4>{});
+  else wide(integral_constant<int, 8>{});
+}
+
+int k_class(int dk) { return dk <= 32 ? 1 : dk <= 64 ? 2 : dk <= 128 ? 4 : 8; }
 
 }  // namespace
 
 // Value columns of one workgroup: 64 up to dv = 64, else 128.
 int lin_mfma_tile(int dv) { return dv <= 64 ? 64 : 128; }
 
-hipError_t launch_lin_mfma(const LinScan& a, bool states, hipStream_t stream) {
-  const bool wide = lin_mfma_tile(a.dv) == 128;
-  if (a.dk <= 32) wide ? launch_mfma<1, 2>(a, states, stream) : launch_mfma<1, 1>(a, states, stream);
-  else if (a.dk <= 64) wide ? launch_mfma<2, 2>(a, states, stream) : launch_mfma<2, 1>(a, states, stream);
-  else if (a.dk <= 128) wide ? launch_mfma<4, 2>(a, states, stream) : launch_mfma<4, 1>(a, states, stream);
-  else wide ? launch_mfma<8, 2>(a, states, stream) : launch_mfma<8, 1>(a, states, stream);
+hipError_t launch_lin_mfma(const LinScan& a, hipStream_t stream) {
+  mfma_instance(a.dk, a.dv, [&](auto kb, auto nb) {
+    constexpr int KB = decltype(kb)::value, NB = decltype(nb)::value;
+    hipLaunchKernelGGL((lin_mfma_kernel<KB, NB>), dim3((unsigned)mfma_blocks<KB, NB>(a)), dim3(256), 0, stream, a);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_lin_mfma_states(const LinScan& a, const LinScan* b, hipStream_t stream) {
+  if (b && (k_class(a.dk) != k_class(b->dk) || lin_mfma_tile(a.dv) != lin_mfma_tile(b->dv))) {
+    const hipError_t e = launch_lin_mfma_states(a, nullptr, stream);
+    return e == hipSuccess ? launch_lin_mfma_states(*b, nullptr, stream) : e;
+  }
+  mfma_instance(a.dk, a.dv, [&](auto kb, auto nb) {
+    constexpr int KB = decltype(kb)::value, NB = decltype(nb)::value;
+    const long na = mfma_blocks<KB, NB>(a), all = na + (b ? mfma_blocks<KB, NB>(*b) : 0);
+    hipLaunchKernelGGL((lin_mfma_states_kernel<KB, NB>), dim3((unsigned)all), dim3(256), 0, stream, a, b ? *b : a, na);
+  });
   return hipGetLastError();
 }
 
