@@ -232,6 +232,7 @@ ssd_status ssd_lin_attn_fwd(const void* q, const void* k, const void* v, const f
   a.dv = shape->dv;
   a.init = initial_state;
   a.fin = final_state;
+  a.q_once = 1;
   set_plan(&a, p, static_cast<char*>(workspace));
   return hip_status(ssd::launch_lin_scan(a, (hipStream_t)stream));
 }

@@ -42,6 +42,7 @@ struct LinScan {
   int batch = 1, T = 0, H = 0; // rows, tokens a row, heads
   int dk = 0, dv = 0;          // this scan's contraction and value sizes
   int bf16 = 0;
+  int q_once = 0;              // no later launch of the call reads q's rows
   // Sequences are cut into blocks of L tokens (from the end in a reversed
   // scan); block b of packed sequence s has slot floor(cu[s] / L) + s + b, of
   // row r slot r * slots_per_row + b. A sequence without tokens has one block.

@@ -1,0 +1,87 @@
+// ssd_lin_chunk.h -- what the linear-attention kernels on matrix instructions
+// share: chunks of 64 tokens, powers of the decay in LDS, rows staged by
+// 16-byte pieces, LDS operands in the order of an accumulator pair.
+#pragma once
+
+#include "ssd_device.h"
+#include "ssd_lin_attn.h"
+
+namespace ssd {
+
+constexpr int kC = 64;                       // tokens a chunk
+constexpr int kPitchP = lds_pitch(kC);       // LDS row of 64 scores
+
+// Powers of the decay, pw[kPowZero + e] = factor lam^e for e = 0 .. 64 and 0 for
+// e = -64 .. -1: the weight of every pair and token of a chunk is one LDS read
+// (an exponential costs a wave as long as sixteen multiplies, and a chunk has
+// some forty weights a lane).
+constexpr int kPowZero = 64, kPowSize = 132;
+__device__ __forceinline__ void fill_powers(float* pw, float g2, float factor) {
+  for (int i = threadIdx.x; i < kPowSize; i += blockDim.x)
+    pw[i] = i < kPowZero ? 0.f : factor * fast_exp2(g2 * (float)(i - kPowZero));
+}
+
+// Weights of the tokens 32 kp + 16 (s / 4) + 4 g + s % 4, s = 0 .. 7, of a chunk
+// of n: lam^(n - 1 - token), 0 behind the chunk. pw is 16-byte aligned.
+__device__ __forceinline__ void token_weights(const float* pw, int n, int kp, int g, float* w) {
+  if (n == kC) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(pw + kPowZero + 60 - 32 * kp - 16 * t - 4 * g);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) w[4 * t + r] = x[3 - r];
+    }
+  } else {
+    const float* at = pw + kPowZero + n - 1 - 32 * kp - 4 * g;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) w[s] = at[-16 * (s >> 2) - (s & 3)];
+  }
+}
+
+// v w, element by element, as the sum of two bf16 values, each rounded to nearest.
+__device__ __forceinline__ void split_weighted(u32x4 v, const float* w, u32x4& hi, u32x4& lo) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float x = bf16_lo(v[c]) * w[2 * c], y = bf16_hi(v[c]) * w[2 * c + 1];
+    hi[c] = pack_bf16x2(x, y);
+    lo[c] = pack_bf16x2(x - bf16_lo(hi[c]), y - bf16_hi(hi[c]));
+  }
+}
+
+// A load of rows that no later launch reads again: it leaves the caches to
+// those that are (with it, the forward pass of 16384 tokens takes 191 us
+// instead of 199).
+__device__ __forceinline__ u32x4 buf_load16_once(rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 2));
+}
+
+// Byte offset, from a chunk's lowest row in memory, of a piece at row r and
+// column col: fixed for whole chunks (`full`); a short reversed chunk starts
+// nearer. Rows behind the chunk and columns behind `end` give kOffNone.
+struct Piece {
+  uint32_t full;
+  int row;   // chunk row, or kC where the columns end before
+};
+__device__ __forceinline__ Piece make_piece(int r, int col, int end, int row_bytes, int esz, int rev) {
+  return Piece{(uint32_t)((rev ? kC - 1 - r : r) * row_bytes + col * esz), col < end ? r : kC};
+}
+__device__ __forceinline__ uint32_t piece_offset(const Piece& p, int n, int row_bytes, int rev) {
+  return p.row < n ? p.full - (rev ? (uint32_t)((kC - n) * row_bytes) : 0u) : kOffNone;
+}
+
+// A 16-byte piece c8 (of four) of 32 columns, stored in the order of an
+// accumulator pair: column 16 t + 4 g + k at 8 g + 4 t + k.
+__device__ __forceinline__ void store_paired(uint16_t* row, int j, int c8, u32x4 v) {
+  uint16_t* at = row + 32 * j + 16 * (c8 & 1) + 4 * (c8 >> 1);
+  *reinterpret_cast<u32x2*>(at) = u32x2{v.x, v.y};
+  *reinterpret_cast<u32x2*>(at + 8) = u32x2{v.z, v.w};
+}
+// The operand of rows row0 + c16 in the columns' own order, from such rows.
+__device__ __forceinline__ u32x4 frag_k_cols_unpaired(const uint16_t* W, int pitch, int row0, int col0, int lane) {
+  const int g = lane >> 4;
+  const uint16_t* at = W + (row0 + (lane & 15)) * pitch + col0 + 16 * (g & 1) + 4 * (g >> 1);
+  const u32x2 lo = *reinterpret_cast<const u32x2*>(at), hi = *reinterpret_cast<const u32x2*>(at + 8);
+  return u32x4{lo.x, lo.y, hi.x, hi.y};
+}
+
+}  // namespace ssd

@@ -23,45 +23,24 @@
 // in registers while this one is computed.
 #include <type_traits>
 
-#include "ssd_device.h"
-#include "ssd_lin_attn.h"
+#include "ssd_lin_chunk.h"
 
 namespace ssd {
 
 namespace {
 
-constexpr int kC = 64;
-constexpr int kPitchP = lds_pitch(kC);
-
-// Keeps what is computed from v where it is: the weights are powers with
-// exponents known before the loop, but held over it they would cost registers
-// that the fourth wave of a SIMD needs, and computing them is cheap.
-__device__ __forceinline__ void here(int& v) { asm volatile("" : "+v"(v)); }
-
-// A 16-byte piece c8 (of four) of 32 columns, stored in the order of an
-// accumulator pair: column 16 t + 4 g + k at 8 g + 4 t + k.
-__device__ __forceinline__ void store_paired(uint16_t* row, int j, int c8, u32x4 v) {
-  uint16_t* at = row + 32 * j + 16 * (c8 & 1) + 4 * (c8 >> 1);
-  *reinterpret_cast<u32x2*>(at) = u32x2{v.x, v.y};
-  *reinterpret_cast<u32x2*>(at + 8) = u32x2{v.z, v.w};
-}
-// The operand of rows row0 + c16 in that order, from columns stored as they are.
-__device__ __forceinline__ u32x4 frag_k_cols_paired(const uint16_t* W, int pitch, int row0, int col0, int lane) {
-  const uint16_t* at = W + (row0 + (lane & 15)) * pitch + col0 + 4 * (lane >> 4);
-  const u32x2 lo = *reinterpret_cast<const u32x2*>(at), hi = *reinterpret_cast<const u32x2*>(at + 16);
-  return u32x4{lo.x, lo.y, hi.x, hi.y};
-}
-
-// KB: dk in units of 32. NB: 64 NB value columns a workgroup of 4 NB waves.
-template <int KB, int NB, bool STATE_ONLY>
+// KB: dk in units of 32. W waves of CB blocks of 16 value columns.
+template <int KB, int W, int CB, bool STATE_ONLY>
 __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks) {
-  constexpr int kDk = 32 * KB, kDv = 64 * NB, kThreads = 256 * NB;
+  constexpr int kDk = 32 * KB, kDv = 16 * W * CB, kThreads = 64 * W;
   constexpr int kPitchK = lds_pitch(kDk), kPitchV = lds_pitch(kDv);
   __shared__ __align__(16) uint16_t Ks[kC * kPitchK];
   __shared__ __align__(16) uint16_t Vs[kC * kPitchV];
   __shared__ __align__(16) uint16_t Qs[STATE_ONLY ? 8 : kC * kPitchK];
   __shared__ __align__(16) uint16_t Ps[STATE_ONLY ? 8 : kC * kPitchP];
-  constexpr int kQK = (256 * KB + kThreads - 1) / kThreads;   // 16-byte pieces a thread stages of q and of k
+  __shared__ __align__(16) float pw[kPowSize], spw[STATE_ONLY ? 4 : kPowSize];   // powers of lam, and scale times them
+  constexpr int kQK = (256 * KB + kThreads - 1) / kThreads;   // 16-byte pieces a thread stages of q and of k,
+  constexpr int kV = 2 * CB;                                  // and of v
 
   const int tiles = (a.dv + kDv - 1) / kDv;
   const long u = xcd_unit(bid, blocks);
@@ -77,35 +56,57 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
   const float g2 = lin_log2_decay(a.ld, h);
   const long mat = (long)a.dv * a.dk;
-  const int dvc = dv0 + 16 * wave + c16;
 
-  // The state: block b holds D[dvc][dk] at dk = 16 b + 4 g + r.
-  f32x4 S[2 * KB];
+  // The state: block b of column block cb holds D[dv][dk] at dv = dv0 + 16 (CB wave + cb) + c16, dk = 16 b + 4 g + r.
+  f32x4 S[CB][2 * KB];
 #pragma unroll
-  for (int b = 0; b < 2 * KB; ++b) S[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+    for (int b = 0; b < 2 * KB; ++b) S[cb][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (!STATE_ONLY) {
     const float* src = p.blk > 0 ? a.states + (slot * a.H + h) * mat : a.init;
     if (p.blk == 0 && src) src += ((long)p.seq * a.H + h) * mat;
     const bool tr = p.blk == 0 && a.init_tr;
     const float sc = p.blk == 0 ? a.init_scale : 1.f;
-    if (src && dvc < a.dv) {
+    if (src) {
 #pragma unroll
-      for (int b = 0; b < 2 * KB; ++b) {
-        const int dk = 16 * b + 4 * g;
-        if (dk >= a.dk) continue;
-        if (tr) {
+      for (int cb = 0; cb < CB; ++cb) {
+        const int dv = dv0 + 16 * (CB * wave + cb) + c16;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[b][r] = sc * src[(long)(dk + r) * a.dv + dvc];
-        } else {
-          S[b] = *reinterpret_cast<const f32x4*>(src + (long)dvc * a.dk + dk) * sc;
+        for (int b = 0; b < 2 * KB; ++b) {
+          const int dk = 16 * b + 4 * g;
+          if (dk >= a.dk || dv >= a.dv) continue;
+          if (tr) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[cb][b][r] = sc * src[(long)(dk + r) * a.dv + dv];
+          } else {
+            S[cb][b] = *reinterpret_cast<const f32x4*>(src + (long)dv * a.dk + dk) * sc;
+          }
         }
       }
     }
   }
 
-  constexpr int kTasks = 2 / NB;   // score tasks (16 queries by 32 keys) a wave
+  constexpr int kTasks = 8 / W;   // score tasks (16 queries by 32 keys) a wave
 
-  u32x4 qn[kQK], kn[kQK], vn[2];
+  fill_powers(pw, g2, 1.f);
+  if (!STATE_ONLY) fill_powers(spw, g2, a.scale);
+
+  const int qrow = (int)a.q.row * 2, krow = (int)a.k.row * 2, vrow = (int)a.v.row * 2;  // 64 rows are fewer than 2^31 bytes
+  Piece qp[STATE_ONLY ? 1 : kQK], kp_[kQK], vp[kV];
+#pragma unroll
+  for (int j = 0; j < kQK; ++j) {
+    const int i = threadIdx.x + kThreads * j;
+    const int r = i / (4 * KB), col = 8 * (i % (4 * KB));
+    kp_[j] = make_piece(r, col, a.dk, krow, 2, a.rev);
+    if (!STATE_ONLY) qp[j] = make_piece(r, col, a.dk, qrow, 2, a.rev);
+  }
+#pragma unroll
+  for (int j = 0; j < kV; ++j) {
+    const int i = threadIdx.x + kThreads * j;
+    vp[j] = make_piece(i / (kDv / 8), 8 * (i % (kDv / 8)), a.dv - dv0, vrow, 2, a.rev);
+  }
+  u32x4 qn[kQK], kn[kQK], vn[kV];
   auto load = [&](int t0) {  // rows of the chunk that starts t0 tokens into the block
     const int n = min(kC, total - t0);
     const long low = p.start + (a.rev ? (long)p.len - (pos0 + t0) - n : (long)pos0 + t0);
@@ -113,30 +114,26 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
       const uint16_t* base = static_cast<const uint16_t*>(x.base) + low * x.row + (long)(h / x.div) * d + col0;
       return make_rsrc(base, (uint32_t)(n * x.row * 2));
     };
-    auto offset = [&](const LinOperand& x, int r, int col, int end) {  // 64 rows are fewer than 2^31 bytes
-      const int row = (int)x.row * 2;
-      return r < n && col < end ? (uint32_t)((a.rev ? n - 1 - r : r) * row + col * 2) : kOffNone;
-    };
     const rsrc_t rk = rows(a.k, a.dk, 0), rv = rows(a.v, a.dv, dv0);
 #pragma unroll
-    for (int j = 0; j < kQK; ++j) {
-      const int i = threadIdx.x + kThreads * j;
-      kn[j] = buf_load16(rk, offset(a.k, i / (4 * KB), 8 * (i % (4 * KB)), a.dk));
-    }
+    for (int j = 0; j < kQK; ++j) kn[j] = buf_load16(rk, piece_offset(kp_[j], n, krow, a.rev));
     if (!STATE_ONLY) {
       const rsrc_t rq = rows(a.q, a.dk, 0);
 #pragma unroll
       for (int j = 0; j < kQK; ++j) {
-        const int i = threadIdx.x + kThreads * j;
-        qn[j] = buf_load16(rq, offset(a.q, i / (4 * KB), 8 * (i % (4 * KB)), a.dk));
+        const uint32_t off = piece_offset(qp[j], n, qrow, a.rev);
+        qn[j] = a.q_once ? buf_load16_once(rq, off) : buf_load16(rq, off);
       }
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = threadIdx.x + kThreads * j;
-      vn[j] = buf_load16(rv, offset(a.v, i / (8 * NB), 8 * (i % (8 * NB)), a.dv - dv0));
-    }
+    for (int j = 0; j < kV; ++j) vn[j] = buf_load16(rv, piece_offset(vp[j], n, vrow, a.rev));
   };
+
+  // This lane's pieces of O at token c16; those of the other token blocks lie 16 rows on.
+  Piece o0[CB];
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb)
+    o0[cb] = make_piece(c16, dv0 + 16 * (CB * wave + cb) + 4 * g, a.dv, a.H * a.dv * (a.o_f32 ? 4 : 2), a.o_f32 ? 4 : 2, a.rev);
 
   // The blocks' own sums walk their chunks backwards, weighting each V by its whole
   // distance to the block's end: the scan, which walks forwards and comes next,
@@ -159,31 +156,31 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
       }
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < kV; ++j) {
       const int i = threadIdx.x + kThreads * j;
-      *reinterpret_cast<u32x4*>(Vs + i / (8 * NB) * kPitchV + 8 * (i % (8 * NB))) = vn[j];
+      *reinterpret_cast<u32x4*>(Vs + i / (kDv / 8) * kPitchV + 8 * (i % (kDv / 8))) = vn[j];
     }
     __syncthreads();
 
     if (!STATE_ONLY) {
 #pragma unroll
       for (int k = 0; k < kTasks; ++k) {
-        const int qb = wave & 3, kp = NB == 2 ? wave >> 2 : k;
+        const int qb = wave & 3, kp = W == 8 ? wave >> 2 : k;
         if (kp > qb / 2) continue;   // all keys are later; never read
         f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
-          const u32x4 q = frag_k_cols(Qs, kPitchK, 16 * qb, 32 * j, lane);
-          s0 = mfma16x16x32(frag_k_cols_paired(Ks, kPitchK, 32 * kp, 32 * j, lane), q, s0);
-          s1 = mfma16x16x32(frag_k_cols_paired(Ks, kPitchK, 32 * kp + 16, 32 * j, lane), q, s1);
+          const u32x4 q = frag_k_cols_unpaired(Qs, kPitchK, 16 * qb, 32 * j, lane);
+          s0 = mfma16x16x32(frag_k_cols(Ks, kPitchK, 32 * kp, 32 * j, lane), q, s0);
+          s1 = mfma16x16x32(frag_k_cols(Ks, kPitchK, 32 * kp + 16, 32 * j, lane), q, s1);
         }
         // Query minus key, of the first key (r = 0); weighted, or 0 (selected: a later key may hold anything).
-        int diff = 16 * qb - 32 * kp + c16 - 4 * g;
-        here(diff);
+        const int diff = 16 * qb - 32 * kp + c16 - 4 * g;
+        const float* w = spw + kPowZero + diff;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          s0[r] = diff >= r ? s0[r] * fast_exp2(g2 * (float)(diff - r)) : 0.f;
-          s1[r] = diff - 16 >= r ? s1[r] * fast_exp2(g2 * (float)(diff - 16 - r)) : 0.f;
+          s0[r] = diff >= r ? s0[r] * w[-r] : 0.f;
+          s1[r] = diff - 16 >= r ? s1[r] * w[-16 - r] : 0.f;
         }
         *reinterpret_cast<u32x4*>(Ps + (16 * qb + c16) * kPitchP + 32 * kp + 8 * g) =
             u32x4{pack_bf16x2(s0[0], s0[1]), pack_bf16x2(s0[2], s0[3]), pack_bf16x2(s1[0], s1[1]), pack_bf16x2(s1[2], s1[3])};
@@ -191,69 +188,92 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
     }
     if (ci + 1 < chunks) load(STATE_ONLY ? t0 - kC : t0 + kC);
 
-    u32x4 vf[2];
+    u32x4 vf[CB][2];
 #pragma unroll
-    for (int kp = 0; kp < 2; ++kp) vf[kp] = frag_k_rows_accpair(Vs, kPitchV, 32 * kp, 16 * wave, lane);
+    for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+      for (int kp = 0; kp < 2; ++kp) vf[cb][kp] = frag_k_rows_accpair(Vs, kPitchV, 32 * kp, 16 * (CB * wave + cb), lane);
 
     if (!STATE_ONLY) {
-      f32x4 O[4];
+      f32x4 O[4][CB];
 #pragma unroll
-      for (int qb = 0; qb < 4; ++qb) O[qb] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int qb = 0; qb < 4; ++qb)
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) O[qb][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < KB; ++j) {
-        const f32x4 x = S[2 * j], y = S[2 * j + 1];
-        const u32x4 sf = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+        u32x4 sf[CB];
 #pragma unroll
-        for (int qb = 0; qb < 4; ++qb) O[qb] = mfma16x16x32(sf, frag_k_cols(Qs, kPitchK, 16 * qb, 32 * j, lane), O[qb]);
+        for (int cb = 0; cb < CB; ++cb) {
+          const f32x4 x = S[cb][2 * j], y = S[cb][2 * j + 1];
+          sf[cb] = u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+        }
+#pragma unroll
+        for (int qb = 0; qb < 4; ++qb) {
+          const u32x4 qf = frag_k_cols(Qs, kPitchK, 16 * qb, 32 * j, lane);
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb) O[qb][cb] = mfma16x16x32(sf[cb], qf, O[qb][cb]);
+        }
       }
 #pragma unroll
-      for (int qb = 0; qb < 4; ++qb) O[qb] *= fast_exp2(g2 * (float)(16 * qb)) * fast_exp2(g2 * (float)(c16 + lead));
+      for (int qb = 0; qb < 4; ++qb) {
+        const float w = spw[kPowZero + 16 * qb + c16 + lead];
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) O[qb][cb] *= w;
+      }
       __syncthreads();
 #pragma unroll
       for (int qb = 0; qb < 4; ++qb)
 #pragma unroll
-        for (int kp = 0; kp <= qb / 2; ++kp)
-          O[qb] = mfma16x16x32(vf[kp], frag_k_cols(Ps, kPitchP, 16 * qb, 32 * kp, lane), O[qb]);
+        for (int kp = 0; kp <= qb / 2; ++kp) {
+          const u32x4 pf = frag_k_cols(Ps, kPitchP, 16 * qb, 32 * kp, lane);
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb) O[qb][cb] = mfma16x16x32(vf[cb][kp], pf, O[qb][cb]);
+        }
       // O^T: column c16 is the query, rows 4 g + r the value columns.
       const long low = p.start + (a.rev ? (long)p.len - (pos0 + t0) - n : (long)pos0 + t0);
-      const int esz = a.o_f32 ? 4 : 2, orow = a.H * a.dv;
-      const rsrc_t ro = make_rsrc(static_cast<char*>(a.o) + (low * orow + (long)h * a.dv) * esz, (uint32_t)(n * orow * esz));
-      const int dv = dv0 + 16 * wave + 4 * g;
+      const int esz = a.o_f32 ? 4 : 2, orow = a.H * a.dv * esz;
+      const rsrc_t ro = make_rsrc(static_cast<char*>(a.o) + low * orow + (long)h * a.dv * esz, (uint32_t)(n * orow));
 #pragma unroll
-      for (int qb = 0; qb < 4; ++qb) {
-        const int r = 16 * qb + c16;
-        const uint32_t off = r < n && dv < a.dv ? (uint32_t)(((a.rev ? n - 1 - r : r) * orow + dv) * esz) : kOffNone;
-        const f32x4 o = O[qb] * a.scale;
-        if (a.o_f32) buf_store16(__builtin_bit_cast(u32x4, o), ro, off);
-        else buf_store8(u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])}, ro, off);
-      }
+      for (int qb = 0; qb < 4; ++qb)
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+          const Piece at = {o0[cb].full + (uint32_t)((a.rev ? -16 : 16) * qb * orow), o0[cb].row + 16 * qb};
+          const uint32_t off = piece_offset(at, n, orow, a.rev);
+          const f32x4 o = O[qb][cb];
+          if (a.o_f32) buf_store16(__builtin_bit_cast(u32x4, o), ro, off);
+          else buf_store8(u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])}, ro, off);
+        }
     }
 
     // State: decay by the chunk, add K^T (weighted V). Token of slot s of pair kp: 32 kp + 16 (s / 4) + 4 g + s % 4.
-    u32x4 hi[2], lo[2];
+    u32x4 hi[CB][2], lo[CB][2];
 #pragma unroll
     for (int kp = 0; kp < 2; ++kp) {
       float w[8];
-      int first = 32 * kp + 4 * g;
-      here(first);
+      token_weights(pw, n, kp, g, w);
+      if (STATE_ONLY) {
+        const float behind = fast_exp2(g2 * (float)after);
 #pragma unroll
-      for (int s = 0; s < 8; ++s) w[s] = fast_exp2(g2 * (float)(after + max(n - 1 - (first + 16 * (s >> 2) + (s & 3)), 0)));
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float x = bf16_lo(vf[kp][c]) * w[2 * c], y = bf16_hi(vf[kp][c]) * w[2 * c + 1];
-        hi[kp][c] = pack_bf16x2(x, y);
-        lo[kp][c] = pack_bf16x2(x - bf16_lo(hi[kp][c]), y - bf16_hi(hi[kp][c]));
+        for (int s = 0; s < 8; ++s) w[s] *= behind;
       }
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) split_weighted(vf[cb][kp], w, hi[cb][kp], lo[cb][kp]);
     }
-    const float keep = fast_exp2(g2 * (float)(n - 1 + lead));
+    const float keep = pw[kPowZero + n - 1 + lead];
 #pragma unroll
     for (int b = 0; b < 2 * KB; ++b) {
-      if (!STATE_ONLY) S[b] *= keep;
+      if (!STATE_ONLY) {
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) S[cb][b] *= keep;
+      }
 #pragma unroll
       for (int kp = 0; kp < 2; ++kp) {
         const u32x4 kf = frag_k_rows_accpair(Ks, kPitchK, 32 * kp, 16 * b, lane);
-        S[b] = mfma16x16x32(kf, hi[kp], S[b]);
-        S[b] = mfma16x16x32(kf, lo[kp], S[b]);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) S[cb][b] = mfma16x16x32(kf, hi[cb][kp], S[cb][b]);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) S[cb][b] = mfma16x16x32(kf, lo[cb][kp], S[cb][b]);
       }
     }
   }
@@ -266,42 +286,44 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
     dst = a.fin + ((long)p.seq * a.H + h) * mat;
     sc = a.fin_scale * (a.rev && p.len > 0 ? fast_exp2(g2) : 1.f);
   }
-  if (dst && dvc < a.dv) {
+  if (dst) {
 #pragma unroll
-    for (int b = 0; b < 2 * KB; ++b) {
-      const int dk = 16 * b + 4 * g;
-      if (dk < a.dk) *reinterpret_cast<f32x4*>(dst + (long)dvc * a.dk + dk) = S[b] * sc;
+    for (int cb = 0; cb < CB; ++cb) {
+      const int dv = dv0 + 16 * (CB * wave + cb) + c16;
+#pragma unroll
+      for (int b = 0; b < 2 * KB; ++b) {
+        const int dk = 16 * b + 4 * g;
+        if (dv < a.dv && dk < a.dk) *reinterpret_cast<f32x4*>(dst + (long)dv * a.dk + dk) = S[cb][b] * sc;
+      }
     }
   }
 }
 
-// Four waves a SIMD (two workgroups of eight waves a CU) hide the barriers'
-// and LDS reads' waits; dk above 128 leaves registers and LDS for half of that.
-template <int KB, int NB>
-__global__ __launch_bounds__(256 * NB, KB <= 4 ? 4 : 2) void lin_mfma_kernel(LinScan a) {
-  lin_mfma<KB, NB, false>(a, blockIdx.x, gridDim.x);
+template <int KB, int W, int CB>
+__global__ __launch_bounds__(64 * W, KB <= 4 ? W / 2 : W / 4) void lin_mfma_kernel(LinScan a) {
+  lin_mfma<KB, W, CB, false>(a, blockIdx.x, gridDim.x);
 }
 
 // The blocks' own sums of one scan, or of two: the first `na` workgroups are a's.
-template <int KB, int NB>
-__global__ __launch_bounds__(256 * NB, KB <= 4 ? 4 : 2) void lin_mfma_states_kernel(LinScan a, LinScan b, long na) {
-  if ((long)blockIdx.x < na) lin_mfma<KB, NB, true>(a, blockIdx.x, na);
-  else lin_mfma<KB, NB, true>(b, blockIdx.x - na, gridDim.x - na);
+template <int KB, int W, int CB>
+__global__ __launch_bounds__(64 * W, KB <= 4 ? W / 2 : W / 4) void lin_mfma_states_kernel(LinScan a, LinScan b, long na) {
+  if ((long)blockIdx.x < na) lin_mfma<KB, W, CB, true>(a, blockIdx.x, na);
+  else lin_mfma<KB, W, CB, true>(b, blockIdx.x - na, gridDim.x - na);
 }
 
-template <int KB, int NB>
 long mfma_blocks(const LinScan& a) {
   const long slots = a.S > 0 ? a.slots_per_row : a.slots_per_row * a.batch;
-  return slots * a.H * ((a.dv + 64 * NB - 1) / (64 * NB));
+  const int tile = lin_mfma_tile(a.dv);
+  return slots * a.H * ((a.dv + tile - 1) / tile);
 }
 
-// The instance for sizes dk and dv: f(KB, NB) as integral constants.
+// The instance for sizes dk and dv: f(KB, W, CB) as integral constants.
 template <typename F>
 void mfma_instance(int dk, int dv, F f) {
   using std::integral_constant;
   auto wide = [&](auto kb) {
-    if (lin_mfma_tile(dv) == 128) f(kb, integral_constant<int, 2>{});
-    else f(kb, integral_constant<int, 1>{});
+    if (lin_mfma_tile(dv) == 128) f(kb, integral_constant<int, 8>{}, integral_constant<int, 1>{});
+    else f(kb, integral_constant<int, 4>{}, integral_constant<int, 1>{});
   };
   if (dk <= 32) wide(integral_constant<int, 1>{});
   else if (dk <= 64) wide(integral_constant<int, 2>{});
@@ -317,9 +339,9 @@ int k_class(int dk) { return dk <= 32 ? 1 : dk <= 64 ? 2 : dk <= 128 ? 4 : 8; }
 int lin_mfma_tile(int dv) { return dv <= 64 ? 64 : 128; }
 
 hipError_t launch_lin_mfma(const LinScan& a, hipStream_t stream) {
-  mfma_instance(a.dk, a.dv, [&](auto kb, auto nb) {
-    constexpr int KB = decltype(kb)::value, NB = decltype(nb)::value;
-    hipLaunchKernelGGL((lin_mfma_kernel<KB, NB>), dim3((unsigned)mfma_blocks<KB, NB>(a)), dim3(256 * NB), 0, stream, a);
+  mfma_instance(a.dk, a.dv, [&](auto kb, auto w, auto cb) {
+    constexpr int KB = decltype(kb)::value, W = decltype(w)::value, CB = decltype(cb)::value;
+    hipLaunchKernelGGL((lin_mfma_kernel<KB, W, CB>), dim3((unsigned)mfma_blocks(a)), dim3(64 * W), 0, stream, a);
   });
   return hipGetLastError();
 }
@@ -329,10 +351,10 @@ hipError_t launch_lin_mfma_states(const LinScan& a, const LinScan* b, hipStream_
     const hipError_t e = launch_lin_mfma_states(a, nullptr, stream);
     return e == hipSuccess ? launch_lin_mfma_states(*b, nullptr, stream) : e;
   }
-  mfma_instance(a.dk, a.dv, [&](auto kb, auto nb) {
-    constexpr int KB = decltype(kb)::value, NB = decltype(nb)::value;
-    const long na = mfma_blocks<KB, NB>(a), all = na + (b ? mfma_blocks<KB, NB>(*b) : 0);
-    hipLaunchKernelGGL((lin_mfma_states_kernel<KB, NB>), dim3((unsigned)all), dim3(256 * NB), 0, stream, a, b ? *b : a, na);
+  mfma_instance(a.dk, a.dv, [&](auto kb, auto w, auto cb) {
+    constexpr int KB = decltype(kb)::value, W = decltype(w)::value, CB = decltype(cb)::value;
+    const long na = mfma_blocks(a), all = na + (b ? mfma_blocks(*b) : 0);
+    hipLaunchKernelGGL((lin_mfma_states_kernel<KB, W, CB>), dim3((unsigned)all), dim3(64 * W), 0, stream, a, b ? *b : a, na);
   });
   return hipGetLastError();
 }
