@@ -269,12 +269,28 @@ __device__ __forceinline__ f32x4 load4(const void* p, long i) {
   }
 }
 
+// Whether an earlier entry names entry e's slot, and the next entry that does
+// (a.batch if none). Each wave looks for itself: no barrier stands between the
+// state's loads and their use.
+__device__ __forceinline__ bool step_peers(const LinStep& a, int e, int slot, int lane, int& next) {
+  next = a.batch;
+  bool before = false;
+  for (int i0 = 0; i0 < a.batch; i0 += 64) {
+    const int i = i0 + lane;
+    const bool same = i < a.batch && i != e && a.slots[i] == slot;
+    before |= __ballot(same && i < e) != 0;
+    const unsigned long long later = __ballot(same && i > e);
+    if (later && next == a.batch) next = i0 + __builtin_ctzll(later);
+  }
+  return before;
+}
+
 template <bool BF16, int ROWS>
 __global__ __launch_bounds__(256) void lin_step_kernel(LinStep a, int tpr, int parts) {
   const int h = (int)(blockIdx.x / parts), part = (int)(blockIdx.x % parts);
   int e = blockIdx.y;
   const int hk = h / (a.H / a.Hk);
-  const int c4 = threadIdx.x & (tpr - 1), rpp = 256 / tpr;
+  const int c4 = threadIdx.x & (tpr - 1), rpp = 256 / tpr, lane = threadIdx.x & 63;
   const int r0 = part * ROWS * rpp + (int)threadIdx.x / tpr;
   const bool col_in = 4 * c4 < a.dk;
   const int slot = a.slots ? a.slots[e] : e;
@@ -290,60 +306,44 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStep a, int tpr, int p
     }
     return;
   }
-  float* st = a.state + ((long)slot * a.H + h) * a.dv * a.dk + 4 * c4;
+  // Rows and columns past the ends read their nearest neighbour inside, and are not written.
+  float* st = a.state + ((long)slot * a.H + h) * a.dv * a.dk + (col_in ? 4 * c4 : 0);
   f32x4 s[ROWS];
 #pragma unroll
-  for (int j = 0; j < ROWS; ++j) {
-    const int r = r0 + j * rpp;
-    s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (col_in && r < a.dv) s[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(st + (long)r * a.dk));
-  }
+  for (int j = 0; j < ROWS; ++j)
+    s[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(st + (long)min(r0 + j * rpp, a.dv - 1) * a.dk));
   const float lam = fast_exp2(lin_log2_decay(a.ld, h));
-  if (a.slots) {
-    int same = 0;
-    for (int i = threadIdx.x; i < e; i += 256) same |= a.slots[i] == slot;
-    if (__syncthreads_or(same)) return;  // an earlier entry's workgroup runs this one
-  }
+  int next = a.batch;
+  if (a.slots && step_peers(a, e, slot, lane, next)) return;  // an earlier entry's workgroup runs this one
   for (;;) {
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    const f32x4 k = col_in ? load4<BF16>(a.k, ((long)e * a.Hk + hk) * a.dk + 4 * c4) : zero;
-    const f32x4 q = col_in ? load4<BF16>(a.q, ((long)e * a.H + h) * a.dk + 4 * c4) : zero;
+    const long ek = (long)e * a.Hk + hk, eh = (long)e * a.H + h;
+    f32x4 k = load4<BF16>(a.k, ek * a.dk + (col_in ? 4 * c4 : 0));
+    f32x4 q = load4<BF16>(a.q, eh * a.dk + (col_in ? 4 * c4 : 0));
+    float v[ROWS];
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) v[j] = load_el<BF16>(a.v, ek * a.dv + min(r0 + j * rpp, a.dv - 1));
+    if (!col_in) k = q = zero;
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
       const int r = r0 + j * rpp;
-      const float v = load_el<BF16>(a.v, ((long)e * a.Hk + hk) * a.dv + min(r, a.dv - 1));
       float acc = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[j][i] = fmaf(s[j][i], lam, v * k[i]);
+        s[j][i] = fmaf(s[j][i], lam, v[j] * k[i]);
         acc = fmaf(s[j][i], q[i], acc);
       }
-      acc = lanes_sum(acc, tpr) * a.scale;
+      if (next == a.batch && col_in && r < a.dv)
+        __builtin_nontemporal_store(s[j], reinterpret_cast<f32x4*>(st + (long)r * a.dk));
+      acc = lanes_sum(col_in ? acc : 0.f, tpr) * a.scale;
       if (c4 == 0 && r < a.dv) {
-        const long at = ((long)e * a.H + h) * a.dv + r;
-        if (BF16) static_cast<uint16_t*>(a.o)[at] = f32_to_bf16(acc);
-        else static_cast<float*>(a.o)[at] = acc;
+        if (BF16) static_cast<uint16_t*>(a.o)[eh * a.dv + r] = f32_to_bf16(acc);
+        else static_cast<float*>(a.o)[eh * a.dv + r] = acc;
       }
     }
-    if (!a.slots) break;
-    __shared__ int next;
-    if (threadIdx.x == 0) next = a.batch;
-    __syncthreads();
-    for (int i = e + 1 + (int)threadIdx.x; i < a.batch; i += 256)
-      if (a.slots[i] == slot) {
-        atomicMin(&next, i);
-        break;
-      }
-    __syncthreads();
-    const int nx = next;
-    __syncthreads();
-    if (nx >= a.batch) break;
-    e = nx;
-  }
-#pragma unroll
-  for (int j = 0; j < ROWS; ++j) {
-    const int r = r0 + j * rpp;
-    if (col_in && r < a.dv) __builtin_nontemporal_store(s[j], reinterpret_cast<f32x4*>(st + (long)r * a.dk));
+    if (next == a.batch) break;
+    e = next;
+    step_peers(a, e, slot, lane, next);
   }
 }
 
