@@ -29,18 +29,22 @@ __device__ __forceinline__ float load_el(const void* p, long i) {
 }
 
 // ----------------------------------------------------------------------------
-// The recurrence itself, token by token, for fp32 operands. A workgroup takes 16 rows of the
-// state of one (block, head): 16 lanes a row, 16 columns a lane, all in
-// registers; tokens are staged 16 at a time through LDS. lam is used as a sum
-// of two floats, so that its rounding does not compound over the block.
+// The recurrence itself, token by token, for fp32 operands. A workgroup takes
+// 16 rows of the state of one (block, head): 16 lanes a row, 4 NQ columns a lane,
+// all in registers; the next 16 tokens are in flight while 16 are taken from LDS.
+// Bound by its own arithmetic: 2 multiply-adds a state element for the decay
+// (lam as a sum of two floats, so that its rounding does not compound over the
+// block), one for the product and one for the output.
 // STATE_ONLY leaves each block's own sum (from a zero state) in a.states;
 // the other form starts from the block's entering state and writes o.
 // ----------------------------------------------------------------------------
-constexpr int kRecRows = 16, kRecTok = 16, kRecMaxK = 256;
+constexpr int kRecRows = 16, kRecTok = 16;
 
-template <bool STATE_ONLY>
+template <int NQ, bool STATE_ONLY>
 __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
-  __shared__ float qs[kRecTok][kRecMaxK], ks[kRecTok][kRecMaxK], vs[kRecTok][kRecRows];
+  constexpr int kCols = 64 * NQ, kPiecesT = kRecTok * kCols / 4 / 256;   // 16-byte pieces a thread stages
+  __shared__ __align__(16) float ks[kRecTok][kCols], qs[STATE_ONLY ? 1 : kRecTok][STATE_ONLY ? 4 : kCols];
+  __shared__ float vs[kRecTok][kRecRows];
   const int tiles = (a.dv + kRecRows - 1) / kRecRows;
   const long u = blockIdx.x;
   const int row0 = (int)(u % tiles) * kRecRows;
@@ -57,9 +61,9 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
   const double lam = exp((double)fmaxf(a.ld[h], -11356.f));
   const float lam_hi = (float)lam, lam_lo = (float)(lam - (double)lam_hi);
 
-  float s[16];  // columns 128 m + 8 c + j at 8 m + j
+  f32x4 s[NQ];  // columns 64 m + 4 c + 0..3
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s[i] = 0.f;
+  for (int m = 0; m < NQ; ++m) s[m] = f32x4{0.f, 0.f, 0.f, 0.f};
   const long mat = (long)a.dv * a.dk;
   if (!STATE_ONLY) {
     const float* src = p.blk > 0 ? a.states + (slot * a.H + h) * mat : a.init;
@@ -68,59 +72,78 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
     const float sc = p.blk == 0 ? a.init_scale : 1.f;
     if (src && row < a.dv) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int col = 128 * (i >> 3) + 8 * c + (i & 7);
-        if (col < a.dk) s[i] = sc * (tr ? src[(long)col * a.dv + row] : src[(long)row * a.dk + col]);
+      for (int m = 0; m < NQ; ++m) {
+        const int col = 64 * m + 4 * c;
+        if (col >= a.dk) continue;
+        if (tr) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[m][i] = sc * src[(long)(col + i) * a.dv + row];
+        } else {
+          s[m] = *reinterpret_cast<const f32x4*>(src + (long)row * a.dk + col) * sc;
+        }
       }
     }
   }
 
+  f32x4 kn[kPiecesT], qn[kPiecesT];
+  float vn;
+  auto token = [&](int pos) { return p.start + (a.rev ? p.len - 1 - pos : pos); };
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int j = 0; j < kPiecesT; ++j) {
+      const int i = threadIdx.x + 256 * j, t = i / (kCols / 4), col = 4 * (i % (kCols / 4));
+      kn[j] = qn[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (t0 + t < n && col < a.dk) {
+        const long tok = token(pos0 + t0 + t);
+        kn[j] = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.k.base) + tok * a.k.row + (long)(h / a.k.div) * a.dk + col);
+        if (!STATE_ONLY)
+          qn[j] = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.q.base) + tok * a.q.row + (long)(h / a.q.div) * a.dk + col);
+      }
+    }
+    vn = 0.f;
+    if (t0 + r < n && row0 + c < a.dv)
+      vn = static_cast<const float*>(a.v.base)[token(pos0 + t0 + r) * a.v.row + (long)(h / a.v.div) * a.dv + row0 + c];
+  };
+
+  if (n > 0) load(0);
   for (int t0 = 0; t0 < n; t0 += kRecTok) {
     const int nt = min(kRecTok, n - t0);
     __syncthreads();
-    for (int i = threadIdx.x; i < kRecTok * kRecMaxK; i += 256) {
-      const int t = i / kRecMaxK, col = i % kRecMaxK;
-      float kv = 0.f, qv = 0.f;
-      if (t < nt && col < a.dk) {
-        const int pos = pos0 + t0 + t;
-        const long tok = p.start + (a.rev ? p.len - 1 - pos : pos);
-        kv = load_el<false>(a.k.base, tok * a.k.row + (long)(h / a.k.div) * a.dk + col);
-        if (!STATE_ONLY) qv = load_el<false>(a.q.base, tok * a.q.row + (long)(h / a.q.div) * a.dk + col);
-      }
-      ks[t][col] = kv;
-      qs[t][col] = qv;
+#pragma unroll
+    for (int j = 0; j < kPiecesT; ++j) {
+      const int i = threadIdx.x + 256 * j;
+      *reinterpret_cast<f32x4*>(&ks[0][0] + 4 * i) = kn[j];
+      if (!STATE_ONLY) *reinterpret_cast<f32x4*>(&qs[0][0] + 4 * i) = qn[j];
     }
-    {
-      const int t = threadIdx.x >> 4, i = threadIdx.x & 15;
-      float x = 0.f;
-      if (t < nt && row0 + i < a.dv) {
-        const int pos = pos0 + t0 + t;
-        const long tok = p.start + (a.rev ? p.len - 1 - pos : pos);
-        x = load_el<false>(a.v.base, tok * a.v.row + (long)(h / a.v.div) * a.dv + row0 + i);
-      }
-      vs[t][i] = x;
-    }
+    vs[r][c] = vn;
     __syncthreads();
-    for (int t = 0; t < nt; ++t) {
+    if (t0 + kRecTok < n) load(t0 + kRecTok);
+    auto step = [&](int t) {
       const bool keep = a.rev && pos0 + t0 + t == 0;  // the state handed to a reversed scan is not decayed first
       const float hi = keep ? 1.f : lam_hi, lo = keep ? 0.f : lam_lo;
       const float v = vs[t][r];
       float part = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int col = 128 * (i >> 3) + 8 * c + (i & 7);
-        s[i] = fmaf(s[i], hi, fmaf(s[i], lo, v * ks[t][col]));
-        if (!STATE_ONLY) part = fmaf(s[i], qs[t][col], part);
+      for (int m = 0; m < NQ; ++m) {
+        const f32x4 k = *reinterpret_cast<const f32x4*>(&ks[t][64 * m + 4 * c]);
+        f32x4 q = {0.f, 0.f, 0.f, 0.f};
+        if (!STATE_ONLY) q = *reinterpret_cast<const f32x4*>(&qs[t][64 * m + 4 * c]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[m][i] = fmaf(s[m][i], hi, fmaf(s[m][i], lo, v * k[i]));
+          part = fmaf(s[m][i], q[i], part);
+        }
       }
       if (!STATE_ONLY) {
         part = sum16(part) * a.scale;
-        if (c == 0 && row < a.dv) {
-          const int pos = pos0 + t0 + t;
-          const long tok = p.start + (a.rev ? p.len - 1 - pos : pos);
-          const long at = (tok * a.H + h) * a.dv + row;
-          static_cast<float*>(a.o)[at] = part;
-        }
+        if (c == 0 && row < a.dv) static_cast<float*>(a.o)[(token(pos0 + t0 + t) * a.H + h) * a.dv + row] = part;
       }
+    };
+    if (nt == kRecTok) {
+#pragma unroll 4
+      for (int t = 0; t < kRecTok; ++t) step(t);
+    } else {
+      for (int t = 0; t < nt; ++t) step(t);
     }
   }
 
@@ -134,9 +157,9 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
   }
   if (dst && row < a.dv) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int col = 128 * (i >> 3) + 8 * c + (i & 7);
-      if (col < a.dk) dst[(long)row * a.dk + col] = s[i] * sc;
+    for (int m = 0; m < NQ; ++m) {
+      const int col = 64 * m + 4 * c;
+      if (col < a.dk) *reinterpret_cast<f32x4*>(dst + (long)row * a.dk + col) = s[m] * sc;
     }
   }
 }
@@ -364,9 +387,13 @@ int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16, b
 }
 
 namespace {
-dim3 rec_grid(const LinScan& a) {
+template <bool STATE_ONLY>
+void launch_rec(const LinScan& a, hipStream_t stream) {
   const long slots = a.S > 0 ? a.slots_per_row : a.slots_per_row * a.batch;
-  return dim3((unsigned)(slots * a.H * ((a.dv + kRecRows - 1) / kRecRows)));
+  const dim3 grid((unsigned)(slots * a.H * ((a.dv + kRecRows - 1) / kRecRows)));
+  if (a.dk <= 64) hipLaunchKernelGGL((lin_rec_kernel<1, STATE_ONLY>), grid, dim3(256), 0, stream, a);
+  else if (a.dk <= 128) hipLaunchKernelGGL((lin_rec_kernel<2, STATE_ONLY>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((lin_rec_kernel<4, STATE_ONLY>), grid, dim3(256), 0, stream, a);
 }
 }  // namespace
 
@@ -378,8 +405,8 @@ hipError_t launch_lin_states(const LinScan& a, const LinScan* b, hipStream_t str
     const hipError_t e = b && b->L > a.L ? launch_lin_mfma_states(*b, &a, stream) : launch_lin_mfma_states(a, b, stream);
     if (e != hipSuccess) return e;
   } else {
-    hipLaunchKernelGGL(lin_rec_kernel<true>, rec_grid(a), dim3(256), 0, stream, a);
-    if (b) hipLaunchKernelGGL(lin_rec_kernel<true>, rec_grid(*b), dim3(256), 0, stream, *b);
+    launch_rec<true>(a, stream);
+    if (b) launch_rec<true>(*b, stream);
   }
   const unsigned seqs = (unsigned)(a.S > 0 ? a.S : a.batch);
   dim3 grid((unsigned)((a.dv * a.dk / 4 + 255) / 256), (unsigned)a.H, b ? 2 * seqs : seqs);
@@ -390,7 +417,7 @@ hipError_t launch_lin_states(const LinScan& a, const LinScan* b, hipStream_t str
 
 hipError_t launch_lin_outputs(const LinScan& a, hipStream_t stream) {
   if (a.bf16) return launch_lin_mfma(a, stream);
-  hipLaunchKernelGGL(lin_rec_kernel<false>, rec_grid(a), dim3(256), 0, stream, a);
+  launch_rec<false>(a, stream);
   return hipGetLastError();
 }
 
