@@ -614,12 +614,17 @@ def bwd_mamba2(X: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.
 # ---------------------------------------------------------------------------
 
 def _call_on(device: torch.device, fn: str, *args):
-    """_call with `device` current, whichever device the caller's is."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        _call(fn, *args, _stream(device))
+    """_call on the device's current stream, with `device` current, whichever device the caller's is."""
+    stream = torch._C._cuda_getCurrentRawStream(device.index)   # what current_stream(device) wraps, at a tenth of its time
+    if device.index == torch._C._cuda_getDevice():
+        _call(fn, *args, stream)
     else:
         with torch.cuda.device(device):
-            _call(fn, *args, _stream(device))
+            _call(fn, *args, stream)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _check_dtype(t, name: str, dim: str, dims: int):
@@ -751,8 +756,8 @@ def lin_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
         o = torch.empty(b, T, H, Dv, dtype=q.dtype, device=q.device)
     if final_state is None and want_final:
         final_state = torch.empty(st, dtype=torch.float32, device=q.device)
-    _call_on(q.device, "ssd_lin_attn_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), float(scale),
-             _ptr(initial_state), _ptr(o), _ptr(final_state), ctypes.byref(shape), _ptr(workspace), have)
+    _call_on(q.device, "ssd_lin_attn_fwd", _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(cu_seqlens), float(scale),
+             _addr(initial_state), _addr(o), _addr(final_state), ctypes.byref(shape), _addr(workspace), have)
     return o, final_state
 
 
@@ -780,9 +785,9 @@ def lin_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
     out = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=q.device), dk=torch.empty(k.shape, dtype=q.dtype, device=q.device),
                dv=torch.empty(v.shape, dtype=q.dtype, device=q.device),
                dinit=torch.empty(st, dtype=torch.float32, device=q.device) if want_dinit else None)
-    _call_on(q.device, "ssd_lin_attn_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), float(scale),
-             _ptr(initial_state), _ptr(do), _ptr(dfinal_state), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
-             _ptr(out["dinit"]), ctypes.byref(shape), _ptr(workspace), have)
+    _call_on(q.device, "ssd_lin_attn_bwd", _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(cu_seqlens), float(scale),
+             _addr(initial_state), _addr(do), _addr(dfinal_state), _addr(out["dq"]), _addr(out["dk"]), _addr(out["dv"]),
+             _addr(out["dinit"]), ctypes.byref(shape), _addr(workspace), have)
     return out
 
 
@@ -821,8 +826,8 @@ def lin_attn_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     if o is None:
         o = torch.empty(b, H, Dv, dtype=q.dtype, device=q.device)
     shape = LinShape(b, 1, H, Hk, Dk, Dv, 0, _dtype_code(q.dtype), 0, 0, 0)
-    _call_on(q.device, "ssd_lin_attn_step", _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(slots), n,
-             float(scale), _ptr(o), ctypes.byref(shape))
+    _call_on(q.device, "ssd_lin_attn_step", _addr(state), _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(slots), n,
+             float(scale), _addr(o), ctypes.byref(shape))
     return o
 
 
@@ -910,8 +915,8 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if stats is None and want_stats:
         stats = torch.empty(st, dtype=torch.float32, device=x.device)
-    _call_on(x.device, "ssd_group_norm", _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(stats),
-             ctypes.byref(shape), _ptr(workspace), have)
+    _call_on(x.device, "ssd_group_norm", _addr(x), _addr(z), _addr(weight), _addr(bias), float(eps), _addr(y), _addr(stats),
+             ctypes.byref(shape), _addr(workspace), have)
     return y, stats
 
 
@@ -936,9 +941,9 @@ def group_norm_bwd(x: torch.Tensor, groups: int, stats: torch.Tensor, dy: torch.
                dz=None if z is None else torch.empty(x.shape, dtype=x.dtype, device=x.device),
                dweight=None if weight is None else torch.empty(C, dtype=torch.float32, device=x.device),
                dbias=None if bias is None else torch.empty(C, dtype=torch.float32, device=x.device))
-    _call_on(x.device, "ssd_group_norm_bwd", _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(stats), _ptr(dy),
-             _ptr(out["dx"]), _ptr(out["dz"]), _ptr(out["dweight"]), _ptr(out["dbias"]), ctypes.byref(shape),
-             _ptr(workspace), have)
+    _call_on(x.device, "ssd_group_norm_bwd", _addr(x), _addr(z), _addr(weight), _addr(bias), _addr(stats), _addr(dy),
+             _addr(out["dx"]), _addr(out["dz"]), _addr(out["dweight"]), _addr(out["dbias"]), ctypes.byref(shape),
+             _addr(workspace), have)
     return out
 
 
@@ -973,7 +978,7 @@ def pages_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor) -> torc
     _expect_device([(pool, "pool")], pool.device, 1)
     _expect_device([(src, "src"), (dst, "dst")], pool.device, 4)
     if src.numel():
-        _call_on(pool.device, "ssd_pages_copy", _ptr(pool), _ptr(src), _ptr(dst), src.numel(), ctypes.byref(shape))
+        _call_on(pool.device, "ssd_pages_copy", _addr(pool), _addr(src), _addr(dst), src.numel(), ctypes.byref(shape))
     return pool
 
 
@@ -986,7 +991,7 @@ def pages_clear(pool: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
     _expect_device([(pool, "pool")], pool.device, 1)
     _expect_device([(slots, "slots")], pool.device, 4)
     if slots.numel():
-        _call_on(pool.device, "ssd_pages_clear", _ptr(pool), _ptr(slots), slots.numel(), ctypes.byref(shape))
+        _call_on(pool.device, "ssd_pages_clear", _addr(pool), _addr(slots), slots.numel(), ctypes.byref(shape))
     return pool
 
 
@@ -1013,6 +1018,6 @@ def pages_compact(pool: torch.Tensor, live: torch.Tensor, where: Optional[torch.
         where = torch.empty(shape.slots, dtype=torch.int32, device=pool.device)
     if count is None:
         count = torch.empty(1, dtype=torch.int32, device=pool.device)
-    _call_on(pool.device, "ssd_pages_compact", _ptr(pool), _ptr(live), _ptr(where), _ptr(count), ctypes.byref(shape),
-             _ptr(workspace), workspace.numel())
+    _call_on(pool.device, "ssd_pages_compact", _addr(pool), _addr(live), _addr(where), _addr(count), ctypes.byref(shape),
+             _addr(workspace), workspace.numel())
     return where, count

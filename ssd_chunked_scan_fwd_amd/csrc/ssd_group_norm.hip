@@ -403,8 +403,8 @@ __global__ __launch_bounds__(kThreads) void norm_sum_parts_kernel(const float* _
 
 // ---------------------------------------------------------------- several positions a sample
 
-// A workgroup takes `cols` columns of VEC channels (a power of two of threads)
-// by kThreads / cols rows at a time, kSlabRounds rounds: one slab.
+// A workgroup takes `cols` columns of VEC channels by kThreads / cols rows at a
+// time, kSlabRounds rounds: one slab.
 constexpr int kSlabRounds = 8;
 
 struct Slabs {
@@ -414,23 +414,11 @@ struct Slabs {
 inline Slabs slabs_of(long s, int C, int vec) {
   Slabs b;
   const int pieces = (C + vec - 1) / vec;
-  b.cols = 1;
-  while (b.cols < pieces && b.cols < 64) b.cols *= 2;
+  b.tiles = (pieces + 63) / 64;
+  b.cols = (pieces + b.tiles - 1) / b.tiles;
   b.rows = kThreads / b.cols;
-  b.tiles = (pieces + b.cols - 1) / b.cols;
   b.count = (s + (long)b.rows * kSlabRounds - 1) / ((long)b.rows * kSlabRounds);
   return b;
-}
-
-template <bool BF16, int VEC>
-__device__ __forceinline__ void load_u(const NormArgs& a, long row, int c, float* u) {
-  load_vec<BF16, VEC>(a.x, row * a.x_row + c, u);
-  if (a.gate == kGateBefore) {
-    float z[VEC];
-    load_vec<BF16, VEC>(a.z, row * a.z_row + c, z);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) u[j] *= z[j] * sigmoid(z[j]);
-  }
 }
 
 // Sum of v[VEC] over the workgroup's thread rows, in row order; every thread receives its column's.
@@ -438,56 +426,100 @@ template <int VEC>
 __device__ __forceinline__ void rows_total(float* v, int cols, int rows, float* lds) {
   const int tx = threadIdx.x % cols, ty = threadIdx.x / cols;
   __syncthreads();
+  if (ty < rows) {
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) lds[(ty * VEC + j) * cols + tx] = v[j];
+    for (int j = 0; j < VEC; ++j) lds[(ty * VEC + j) * cols + tx] = v[j];
+  }
   __syncthreads();
 #pragma unroll
+  for (int j = 0; j < VEC; ++j) v[j] = 0.f;
+#pragma unroll 2
+  for (int r = 0; r < rows; ++r)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] += lds[(r * VEC + j) * cols + tx];
+}
+
+// The rows of one thread's column in a slab, all in flight at once: rows past
+// the sample's end read its last row, columns past C the first column; neither counts.
+template <bool BF16, int VEC>
+struct SlabRows {
+  Raw<BF16, VEC> v[kSlabRounds];
+  __device__ __forceinline__ void load(const void* p, long row0, long pitch, int rows, int ty, long have, int c) {
+#pragma unroll
+    for (int k = 0; k < kSlabRounds; ++k) v[k].load(p, (row0 + min(ty + (long)k * rows, have - 1)) * pitch + c);
+  }
+};
+
+// A thread's place in the slab form.
+struct SlabAt {
+  int tx, ty, c;       // thread column and row, first channel
+  long slab, n;        // slab and sample
+  long row0, have;     // first row of the slab, its rows
+};
+template <int VEC>
+__device__ __forceinline__ SlabAt slab_at(const NormArgs& a, const Slabs& b) {
+  SlabAt s;
+  const int tile = (int)(blockIdx.x % b.tiles);
+  s.slab = blockIdx.x / b.tiles % b.count;
+  s.n = blockIdx.x / b.tiles / b.count;
+  s.tx = threadIdx.x % b.cols;
+  s.ty = threadIdx.x / b.cols;
+  s.c = s.ty < b.rows ? (tile * b.cols + s.tx) * VEC : a.C;   // threads beyond the last row stand outside
+  const long r0 = s.slab * b.rows * kSlabRounds;
+  s.row0 = s.n * a.s + r0;
+  s.have = min((long)b.rows * kSlabRounds, a.s - r0);
+  return s;
+}
+
+// The groups of VEC channels from c on.
+template <int VEC>
+__device__ __forceinline__ void groups_of(int c, int Cg, int* g) {
+  int at = c / Cg, left = Cg - c % Cg;
+#pragma unroll
   for (int j = 0; j < VEC; ++j) {
-    float t = 0.f;
-    for (int r = 0; r < rows; ++r) t += lds[(r * VEC + j) * cols + tx];
-    v[j] = t;
+    g[j] = at;
+    if (--left == 0) {
+      ++at;
+      left = Cg;
+    }
   }
 }
 
-// ws [n][slab][2][C]: each slab's mean and squared deviations from it, per channel.
+// First launch: ws [n][slab][2][C]: each slab's mean and squared deviations from it, per channel.
 template <bool BF16, int VEC>
 __global__ __launch_bounds__(kThreads) void norm_slab_kernel(NormArgs a, Slabs b) {
   __shared__ float lds[kThreads * VEC];
-  const int tile = (int)(blockIdx.x % b.tiles);
-  const long slab = blockIdx.x / b.tiles % b.count, n = blockIdx.x / b.tiles / b.count;
-  const int tx = threadIdx.x % b.cols, ty = threadIdx.x / b.cols;
-  const int c = (tile * b.cols + tx) * VEC;
-  const long r0 = slab * b.rows * kSlabRounds;
-  const long have = min((long)b.rows * kSlabRounds, a.s - r0);
-  float u[kSlabRounds][VEC], sum[VEC];
+  const SlabAt at = slab_at<VEC>(a, b);
+  const bool in = at.c < a.C;
+  const int c = in ? at.c : 0;
+  SlabRows<BF16, VEC> x, z;
+  x.load(a.x, at.row0, a.x_row, b.rows, at.ty, at.have, c);
+  if (a.gate == kGateBefore) z.load(a.z, at.row0, a.z_row, b.rows, at.ty, at.have, c);
+  float u[kSlabRounds][VEC], sum[VEC], dev[VEC];
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) sum[j] = 0.f;
+  for (int j = 0; j < VEC; ++j) sum[j] = dev[j] = 0.f;
 #pragma unroll
   for (int k = 0; k < kSlabRounds; ++k) {
-    const long r = ty + (long)k * b.rows;
+    const bool row = at.ty + (long)k * b.rows < at.have;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) u[k][j] = 0.f;
-    if (c < a.C && r < have) load_u<BF16, VEC>(a, n * a.s + r0 + r, c, u[k]);
+    for (int j = 0; j < VEC; ++j) {
+      u[k][j] = x.v[k][j];
+      if (a.gate == kGateBefore) u[k][j] *= z.v[k][j] * sigmoid(z.v[k][j]);
+      sum[j] += row ? u[k][j] : 0.f;
+    }
   }
-#pragma unroll
-  for (int k = 0; k < kSlabRounds; ++k)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) sum[j] += u[k][j];
   rows_total<VEC>(sum, b.cols, b.rows, lds);
-  float dev[VEC];
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    sum[j] /= (float)have;
-    dev[j] = 0.f;
+  for (int j = 0; j < VEC; ++j) sum[j] /= (float)at.have;   // divided, so that equal values have exactly their mean
+#pragma unroll
+  for (int k = 0; k < kSlabRounds; ++k) {
+    const bool row = at.ty + (long)k * b.rows < at.have;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) dev[j] += row ? (u[k][j] - sum[j]) * (u[k][j] - sum[j]) : 0.f;
   }
-#pragma unroll
-  for (int k = 0; k < kSlabRounds; ++k)
-    if (ty + (long)k * b.rows < have)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) dev[j] += (u[k][j] - sum[j]) * (u[k][j] - sum[j]);
   rows_total<VEC>(dev, b.cols, b.rows, lds);
-  if (ty == 0 && c < a.C) {
-    float* out = a.ws + (n * b.count + slab) * 2 * a.C + c;
+  if (at.ty == 0 && in) {
+    float* out = a.ws + (at.n * b.count + at.slab) * 2 * a.C + c;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
       out[j] = sum[j];
@@ -506,28 +538,30 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return t;
 }
 
-// One group of one sample: joins its slabs and channels about their common mean.
-__global__ __launch_bounds__(kThreads) void norm_join_kernel(NormArgs a, long slabs, long slab_rows, float* stats) {
+// One group of one sample: joins its slabs and channels about their common
+// mean. Threads take whole slabs, channel by channel, or, with few channels a
+// group, runs of them.
+__global__ __launch_bounds__(kThreads) void norm_join_kernel(NormArgs a, int slabs, int slab_rows, float* stats) {
   __shared__ float red[kThreads / 64];
   const int Cg = a.C / a.G;
   const long n = blockIdx.x / a.G;
   const int g = (int)(blockIdx.x % a.G);
   const float* ws = a.ws + n * slabs * 2 * a.C + (long)g * Cg;
-  const long items = slabs * Cg;
-  float s = 0.f;
-  for (long i = threadIdx.x; i < items; i += kThreads) {
-    const long slab = i / Cg;
-    const float rows = (float)min(slab_rows, a.s - slab * slab_rows);
-    s += ws[slab * 2 * a.C + i % Cg] * (rows / (float)a.s);
-  }
-  const float mean = block_sum(s, red) / (float)Cg;
+  const int per = Cg < kThreads ? Cg : kThreads, lanes = kThreads / per;   // threads across a slab's channels; slabs at a time
+  const int l = threadIdx.x % per, s0 = threadIdx.x / per;
+  const int last = (int)(a.s - (long)(slabs - 1) * slab_rows);             // rows of the last slab
+  float sum = 0.f;
+  if (s0 < lanes)
+    for (int i = s0; i < slabs; i += lanes)
+      for (int c = l; c < Cg; c += per) sum += ws[(long)i * 2 * a.C + c] * (float)(i + 1 < slabs ? slab_rows : last);
+  const float mean = block_sum(sum, red) / ((float)a.s * (float)Cg);
   float d = 0.f;
-  for (long i = threadIdx.x; i < items; i += kThreads) {
-    const long slab = i / Cg;
-    const float rows = (float)min(slab_rows, a.s - slab * slab_rows);
-    const float off = ws[slab * 2 * a.C + i % Cg] - mean;
-    d += ws[(slab * 2 + 1) * a.C + i % Cg] + rows * off * off;
-  }
+  if (s0 < lanes)
+    for (int i = s0; i < slabs; i += lanes)
+      for (int c = l; c < Cg; c += per) {
+        const float off = ws[(long)i * 2 * a.C + c] - mean;
+        d += ws[((long)i * 2 + 1) * a.C + c] + (float)(i + 1 < slabs ? slab_rows : last) * off * off;
+      }
   float var = block_sum(d, red) / ((float)a.s * (float)Cg);
   if (!a.center) var += mean * mean;
   if (threadIdx.x == 0) {
@@ -538,35 +572,34 @@ __global__ __launch_bounds__(kThreads) void norm_join_kernel(NormArgs a, long sl
 
 template <bool BF16, int VEC>
 __global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a, Slabs b, const float* __restrict__ stats) {
-  const int tile = (int)(blockIdx.x % b.tiles);
-  const long slab = blockIdx.x / b.tiles % b.count, n = blockIdx.x / b.tiles / b.count;
-  const int tx = threadIdx.x % b.cols, ty = threadIdx.x / b.cols;
-  const int c = (tile * b.cols + tx) * VEC, Cg = a.C / a.G;
-  if (c >= a.C) return;
+  const SlabAt at = slab_at<VEC>(a, b);
+  if (at.c >= a.C) return;
+  const int c = at.c;
+  SlabRows<BF16, VEC> x, z;
+  x.load(a.x, at.row0, a.x_row, b.rows, at.ty, at.have, c);
+  if (a.gate) z.load(a.z, at.row0, a.z_row, b.rows, at.ty, at.have, c);
   float mean[VEC], rstd[VEC], w[VEC], bias[VEC];
   load_par<VEC>(a.w, c, 1.f, w);
   load_par<VEC>(a.bias, c, 0.f, bias);
+  int g[VEC];
+  groups_of<VEC>(c, a.C / a.G, g);
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
-    const long g = n * a.G + (c + j) / Cg;
-    mean[j] = stats[2 * g];
-    rstd[j] = stats[2 * g + 1];
+    mean[j] = stats[2 * (at.n * a.G + g[j])];
+    rstd[j] = stats[2 * (at.n * a.G + g[j]) + 1];
   }
 #pragma unroll
   for (int k = 0; k < kSlabRounds; ++k) {
-    const long r = slab * b.rows * kSlabRounds + ty + (long)k * b.rows;
-    if (r >= a.s) break;
-    const long row = n * a.s + r;
-    float u[VEC], z[VEC];
-    load_vec<BF16, VEC>(a.x, row * a.x_row + c, u);
-    if (a.gate) load_vec<BF16, VEC>(a.z, row * a.z_row + c, z);
+    const long r = at.ty + (long)k * b.rows;
+    if (r >= at.have) break;
+    float u[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      const float sz = a.gate ? z[j] * sigmoid(z[j]) : 0.f;
-      const float v = a.gate == kGateBefore ? u[j] * sz : u[j];
+      const float sz = a.gate ? z.v[k][j] * sigmoid(z.v[k][j]) : 0.f;
+      const float v = a.gate == kGateBefore ? x.v[k][j] * sz : x.v[k][j];
       u[j] = finish<AnyForm>(a, (v - mean[j]) * rstd[j] * w[j] + bias[j], sz);
     }
-    store_vec<BF16, VEC>(a.y, row * a.C + c, u);
+    store_vec<BF16, VEC>(a.y, (at.row0 + r) * a.C + c, u);
   }
 }
 
@@ -574,46 +607,42 @@ __global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a, Slabs 
 template <bool BF16, int VEC>
 __global__ __launch_bounds__(kThreads) void norm_slab_bwd_kernel(NormArgs a, Slabs b) {
   __shared__ float lds[kThreads * VEC];
-  const int tile = (int)(blockIdx.x % b.tiles);
-  const long slab = blockIdx.x / b.tiles % b.count, n = blockIdx.x / b.tiles / b.count;
-  const int tx = threadIdx.x % b.cols, ty = threadIdx.x / b.cols;
-  const int c = (tile * b.cols + tx) * VEC, Cg = a.C / a.G;
+  const SlabAt at = slab_at<VEC>(a, b);
+  const bool in = at.c < a.C;
+  const int c = in ? at.c : 0;
+  SlabRows<BF16, VEC> x, z, dy;
+  x.load(a.x, at.row0, a.x_row, b.rows, at.ty, at.have, c);
+  if (a.gate) z.load(a.z, at.row0, a.z_row, b.rows, at.ty, at.have, c);
+  dy.load(a.dy, at.row0, a.C, b.rows, at.ty, at.have, c);
   float mean[VEC], rstd[VEC], w[VEC], bias[VEC], s0[VEC], s1[VEC];
+  int g[VEC];
+  groups_of<VEC>(c, a.C / a.G, g);
+  load_par<VEC>(a.w, c, 1.f, w);
+  load_par<VEC>(a.bias, c, 0.f, bias);
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) s0[j] = s1[j] = 0.f;
-  if (c < a.C) {
-    load_par<VEC>(a.w, c, 1.f, w);
-    load_par<VEC>(a.bias, c, 0.f, bias);
+  for (int j = 0; j < VEC; ++j) {
+    mean[j] = a.stats[2 * (at.n * a.G + g[j])];
+    rstd[j] = a.stats[2 * (at.n * a.G + g[j]) + 1];
+    s0[j] = s1[j] = 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < kSlabRounds; ++k) {
+    if (at.ty + (long)k * b.rows >= at.have) break;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      const long g = n * a.G + (c + j) / Cg;
-      mean[j] = a.stats[2 * g];
-      rstd[j] = a.stats[2 * g + 1];
-    }
-#pragma unroll
-    for (int k = 0; k < kSlabRounds; ++k) {
-      const long r = slab * b.rows * kSlabRounds + ty + (long)k * b.rows;
-      if (r >= a.s) break;
-      const long row = n * a.s + r;
-      float u[VEC], z[VEC], dy[VEC];
-      load_vec<BF16, VEC>(a.x, row * a.x_row + c, u);
-      if (a.gate) load_vec<BF16, VEC>(a.z, row * a.z_row + c, z);
-      load_vec<BF16, VEC>(a.dy, row * a.C + c, dy);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float v = a.gate == kGateBefore ? u[j] * z[j] * sigmoid(z[j]) : u[j];
-        const float xh = (v - mean[j]) * rstd[j];
-        float dz;
-        const float gt = unfinish<AnyForm>(a, xh * w[j] + bias[j], a.gate ? z[j] : 0.f, dy[j], dz);
-        s0[j] += gt * xh;
-        s1[j] += gt;
-      }
+      const float zj = a.gate ? z.v[k][j] : 0.f;
+      const float v = a.gate == kGateBefore ? x.v[k][j] * zj * sigmoid(zj) : x.v[k][j];
+      const float xh = (v - mean[j]) * rstd[j];
+      float dz;
+      const float gt = unfinish<AnyForm>(a, xh * w[j] + bias[j], zj, dy.v[k][j], dz);
+      s0[j] += gt * xh;
+      s1[j] += gt;
     }
   }
   rows_total<VEC>(s0, b.cols, b.rows, lds);
   rows_total<VEC>(s1, b.cols, b.rows, lds);
-  if (ty == 0 && c < a.C) {
-    float* out = a.ws + (n * b.count + slab) * 2 * a.C + c;
+  if (at.ty == 0 && in) {
+    float* out = a.ws + (at.n * b.count + at.slab) * 2 * a.C + c;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
       out[j] = s0[j];
@@ -623,19 +652,23 @@ __global__ __launch_bounds__(kThreads) void norm_slab_bwd_kernel(NormArgs a, Sla
 }
 
 // means[n][G][2]: a group's means of g w xh and of g w.
-__global__ __launch_bounds__(kThreads) void norm_join_bwd_kernel(NormArgs a, long slabs, float* means) {
+__global__ __launch_bounds__(kThreads) void norm_join_bwd_kernel(NormArgs a, int slabs, float* means) {
   __shared__ float red[kThreads / 64];
   const int Cg = a.C / a.G;
   const long n = blockIdx.x / a.G;
   const int g = (int)(blockIdx.x % a.G);
   const float* ws = a.ws + n * slabs * 2 * a.C + (long)g * Cg;
+  const int per = Cg < kThreads ? Cg : kThreads, lanes = kThreads / per;
+  const int l = threadIdx.x % per, i0 = threadIdx.x / per;
   float s0 = 0.f, s1 = 0.f;
-  for (long i = threadIdx.x; i < slabs * Cg; i += kThreads) {
-    const int c = (int)(i % Cg);
-    const float w = a.w ? a.w[g * Cg + c] : 1.f;
-    s0 += w * ws[i / Cg * 2 * a.C + c];
-    s1 += w * ws[(i / Cg * 2 + 1) * a.C + c];
-  }
+  if (i0 < lanes)
+    for (int c = l; c < Cg; c += per) {
+      const float w = a.w ? a.w[g * Cg + c] : 1.f;
+      for (int i = i0; i < slabs; i += lanes) {
+        s0 += w * ws[(long)i * 2 * a.C + c];
+        s1 += w * ws[((long)i * 2 + 1) * a.C + c];
+      }
+    }
   const float inv = 1.f / ((float)a.s * (float)Cg);
   const float t0 = block_sum(s0, red) * inv, t1 = block_sum(s1, red) * inv;
   if (threadIdx.x == 0) {
@@ -646,46 +679,47 @@ __global__ __launch_bounds__(kThreads) void norm_join_bwd_kernel(NormArgs a, lon
 
 template <bool BF16, int VEC>
 __global__ __launch_bounds__(kThreads) void norm_apply_bwd_kernel(NormArgs a, Slabs b, const float* __restrict__ means) {
-  const int tile = (int)(blockIdx.x % b.tiles);
-  const long slab = blockIdx.x / b.tiles % b.count, n = blockIdx.x / b.tiles / b.count;
-  const int tx = threadIdx.x % b.cols, ty = threadIdx.x / b.cols;
-  const int c = (tile * b.cols + tx) * VEC, Cg = a.C / a.G;
-  if (c >= a.C) return;
+  const SlabAt at = slab_at<VEC>(a, b);
+  if (at.c >= a.C) return;
+  const int c = at.c;
+  SlabRows<BF16, VEC> x, z, dy;
+  x.load(a.x, at.row0, a.x_row, b.rows, at.ty, at.have, c);
+  if (a.gate) z.load(a.z, at.row0, a.z_row, b.rows, at.ty, at.have, c);
+  dy.load(a.dy, at.row0, a.C, b.rows, at.ty, at.have, c);
   float mean[VEC], rstd[VEC], w[VEC], bias[VEC], m0[VEC], m1[VEC];
+  int g[VEC];
+  groups_of<VEC>(c, a.C / a.G, g);
   load_par<VEC>(a.w, c, 1.f, w);
   load_par<VEC>(a.bias, c, 0.f, bias);
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
-    const long g = n * a.G + (c + j) / Cg;
-    mean[j] = a.stats[2 * g];
-    rstd[j] = a.stats[2 * g + 1];
-    m1[j] = means[2 * g];
-    m0[j] = means[2 * g + 1];
+    const long q = 2 * (at.n * a.G + g[j]);
+    mean[j] = a.stats[q];
+    rstd[j] = a.stats[q + 1];
+    m1[j] = means[q];
+    m0[j] = means[q + 1];
   }
 #pragma unroll
   for (int k = 0; k < kSlabRounds; ++k) {
-    const long r = slab * b.rows * kSlabRounds + ty + (long)k * b.rows;
-    if (r >= a.s) break;
-    const long row = n * a.s + r;
-    float x[VEC], z[VEC], dy[VEC], dx[VEC], dzv[VEC];
-    load_vec<BF16, VEC>(a.x, row * a.x_row + c, x);
-    if (a.gate) load_vec<BF16, VEC>(a.z, row * a.z_row + c, z);
-    load_vec<BF16, VEC>(a.dy, row * a.C + c, dy);
+    const long r = at.ty + (long)k * b.rows;
+    if (r >= at.have) break;
+    float dx[VEC], dzv[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      const float sg = a.gate == kGateBefore ? sigmoid(z[j]) : 0.f;
-      const float u = a.gate == kGateBefore ? x[j] * z[j] * sg : x[j];
+      const float zj = a.gate ? z.v[k][j] : 0.f;
+      const float sg = a.gate == kGateBefore ? sigmoid(zj) : 0.f;
+      const float u = a.gate == kGateBefore ? x.v[k][j] * zj * sg : x.v[k][j];
       const float xh = (u - mean[j]) * rstd[j];
       dzv[j] = 0.f;
-      const float gt = unfinish<AnyForm>(a, xh * w[j] + bias[j], a.gate ? z[j] : 0.f, dy[j], dzv[j]);
+      const float gt = unfinish<AnyForm>(a, xh * w[j] + bias[j], zj, dy.v[k][j], dzv[j]);
       dx[j] = rstd[j] * (gt * w[j] - m0[j] - xh * m1[j]);
       if (a.gate == kGateBefore) {
-        dzv[j] = dx[j] * x[j] * silu_slope(z[j], sg);
-        dx[j] *= z[j] * sg;
+        dzv[j] = dx[j] * x.v[k][j] * silu_slope(zj, sg);
+        dx[j] *= zj * sg;
       }
     }
-    store_vec<BF16, VEC>(a.dx, row * a.C + c, dx);
-    if (a.gate) store_vec<BF16, VEC>(a.dz, row * a.C + c, dzv);
+    store_vec<BF16, VEC>(a.dx, (at.row0 + r) * a.C + c, dx);
+    if (a.gate) store_vec<BF16, VEC>(a.dz, (at.row0 + r) * a.C + c, dzv);
   }
 }
 
@@ -802,7 +836,7 @@ void slab_launch(const NormArgs& a, hipStream_t stream) {
   const dim3 grid((unsigned)(a.n * b.count * b.tiles)), groups((unsigned)(a.n * a.G)), block(kThreads);
   float* stats = a.stats ? a.stats : a.ws + a.n * b.count * 2 * a.C;
   hipLaunchKernelGGL((norm_slab_kernel<BF16, VEC>), grid, block, 0, stream, a, b);
-  hipLaunchKernelGGL(norm_join_kernel, groups, block, 0, stream, a, b.count, (long)b.rows * kSlabRounds, stats);
+  hipLaunchKernelGGL(norm_join_kernel, groups, block, 0, stream, a, (int)b.count, b.rows * kSlabRounds, stats);
   hipLaunchKernelGGL((norm_apply_kernel<BF16, VEC>), grid, block, 0, stream, a, b, (const float*)stats);
 }
 
@@ -812,7 +846,7 @@ void slab_bwd_launch(const NormArgs& a, hipStream_t stream) {
   const dim3 grid((unsigned)(a.n * b.count * b.tiles)), groups((unsigned)(a.n * a.G)), block(kThreads);
   float* means = a.ws + a.n * b.count * 2 * a.C;
   hipLaunchKernelGGL((norm_slab_bwd_kernel<BF16, VEC>), grid, block, 0, stream, a, b);
-  hipLaunchKernelGGL(norm_join_bwd_kernel, groups, block, 0, stream, a, b.count, means);
+  hipLaunchKernelGGL(norm_join_bwd_kernel, groups, block, 0, stream, a, (int)b.count, means);
   hipLaunchKernelGGL((norm_apply_bwd_kernel<BF16, VEC>), grid, block, 0, stream, a, b, (const float*)means);
   if (a.dw || a.db)
     hipLaunchKernelGGL(norm_sum_parts_kernel, dim3((unsigned)((a.C + 15) / 16), 2), block, 0, stream, a.ws,
