@@ -43,6 +43,7 @@ struct LinScan {
   int dk = 0, dv = 0;          // this scan's contraction and value sizes
   int bf16 = 0;
   int q_once = 0;              // no later launch of the call reads q's rows
+  bool fine() const { return fin != nullptr; }   // the state is an fp32 result: carry it in full
   // Sequences are cut into blocks of L tokens (from the end in a reversed
   // scan); block b of packed sequence s has slot floor(cu[s] / L) + s + b, of
   // row r slot r * slots_per_row + b. A sequence without tokens has one block.
@@ -137,6 +138,11 @@ __device__ __forceinline__ LinPiece lin_piece(const LinScan& a, long slot) {
   const long b = slot - ((long)c0 / a.L + p.seq);
   p.blk = b >= 0 && (b == 0 || b * a.L < p.len) ? (int)b : -1;
   return p;
+}
+
+// lam^e in 64 bits (a log decay of -inf: 0 for e > 0, 1 for e = 0).
+__device__ __forceinline__ double lin_power(float log_decay, int e) {
+  return exp((double)fmaxf(log_decay, -11356.f) * (double)e);
 }
 
 // log2 of the decay; a log decay of -inf becomes a finite value whose first

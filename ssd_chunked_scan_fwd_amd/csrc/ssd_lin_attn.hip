@@ -195,9 +195,7 @@ __device__ __forceinline__ void lin_pass(const LinScan& a, int s) {
       D = *reinterpret_cast<const f32x4*>(src + e) * a.init_scale;
     }
   }
-  const float g = lin_log2_decay(a.ld, h);
-  const float w0 = fast_exp2(g * (float)(a.L - (a.rev ? 1 : 0)));
-  const float w = fast_exp2(g * (float)a.L);
+  const float w0 = (float)lin_power(a.ld[h], a.L - (a.rev ? 1 : 0)), w = (float)lin_power(a.ld[h], a.L);
   const long step = (long)a.H * mat;
   float* at = a.states + (slot0 * a.H + h) * mat + e;
   constexpr int kAhead = 8;

@@ -21,8 +21,8 @@ namespace ssd {
 
 namespace {
 
-// KB, VB: dk and dv in units of 32 (2 or 4).
-template <int KB, int VB>
+// KB, VB: dk and dv in units of 32 (2 or 4). TERMS: as in ssd_lin_scan.hip.
+template <int KB, int VB, int TERMS>
 __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOperand vop, void* dk_out) {
   constexpr int kWaves = 4 * VB, kThreads = 64 * kWaves;
   constexpr int kPitchK = lds_pitch(32 * KB), kPitchV = lds_pitch(32 * VB);
@@ -52,10 +52,8 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
   const int vb = wave % (2 * VB), half = wave / (2 * VB);     // value block; half of dk (R) and of the tokens (dV)
   const int kb0 = wave % (2 * KB), tb0 = wave / (2 * KB) * kDkTok;   // dK: key block, first token block
-  const float g2 = lin_log2_decay(a.ld, h);
   const long mat = (long)a.dv * a.dk;
-  fill_powers(pw, g2, 1.f);
-  fill_powers(spw, g2, a.scale);
+  fill_powers(pw, spw, a.ld[h], a.scale);
 
   f32x4 R[KB];   // dv = 16 vb + c16, dk = 16 (KB half + b) + 4 g + r
 #pragma unroll
@@ -235,13 +233,13 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
 #pragma unroll
     for (int t = 0; t < kDkTok; ++t) put(dk_out, a.dk, 16 * (tb0 + t) + c16, 16 * kb0 + 4 * g, OK[t]);
 
-    // R: decay by the chunk, add Q^T (weighted dO), dO's weighted values as two bf16 values each.
-    u32x4 hi[2], lo[2];
+    // R: decay by the chunk, add Q^T (weighted dO).
+    u32x4 part[2][TERMS];
 #pragma unroll
     for (int kp = 0; kp < 2; ++kp) {
       float w[8];
       token_weights(pw, n, kp, g, w);
-      split_weighted(gf[kp], w, hi[kp], lo[kp]);
+      split_weighted<TERMS>(gf[kp], w, part[kp]);
     }
     const float keep = pw[kPowZero + n - 1 + lead];
 #pragma unroll
@@ -250,14 +248,14 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
 #pragma unroll
       for (int kp = 0; kp < 2; ++kp) {
         const u32x4 qf = frag_k_rows_accpair(Qs, kPitchK, 32 * kp, 16 * (KB * half + b), lane);
-        R[b] = mfma16x16x32(qf, hi[kp], R[b]);
-        R[b] = mfma16x16x32(qf, lo[kp], R[b]);
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) R[b] = mfma16x16x32(qf, part[kp][t], R[b]);
       }
     }
   }
 
   if (last && a.fin && dvc < a.dv) {
-    const float sc = a.fin_scale * (p.len > 0 ? fast_exp2(g2) : 1.f);
+    const float sc = a.fin_scale * (p.len > 0 ? pw[kPowZero + 1] : 1.f);
     float* dst = a.fin + ((long)p.seq * a.H + h) * mat;
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
@@ -274,16 +272,19 @@ bool lin_kv_supported(int dk, int dv, int bf16) { return bf16 && dk <= 128 && dv
 // Workgroups that fill the chip: one of sixteen waves a CU, or two of eight.
 int lin_kv_target(int dv) { return dv <= 64 ? 512 : 256; }
 
-hipError_t launch_lin_kv(const LinScan& a, const LinOperand& v, void* dk_out, hipStream_t stream) {
+namespace {
+template <int KB, int VB>
+void kv_launch(const LinScan& a, const LinOperand& v, void* dk_out, hipStream_t stream) {
   const long slots = a.S > 0 ? a.slots_per_row : a.slots_per_row * a.batch;
-  const dim3 grid((unsigned)(slots * a.H));
-  if (a.dv <= 64) {
-    if (a.dk <= 64) hipLaunchKernelGGL((lin_kv_kernel<2, 2>), grid, dim3(512), 0, stream, a, v, dk_out);
-    else hipLaunchKernelGGL((lin_kv_kernel<4, 2>), grid, dim3(512), 0, stream, a, v, dk_out);
-  } else {
-    if (a.dk <= 64) hipLaunchKernelGGL((lin_kv_kernel<2, 4>), grid, dim3(1024), 0, stream, a, v, dk_out);
-    else hipLaunchKernelGGL((lin_kv_kernel<4, 4>), grid, dim3(1024), 0, stream, a, v, dk_out);
-  }
+  const dim3 grid((unsigned)(slots * a.H)), block(256 * VB);
+  if (a.fine()) hipLaunchKernelGGL((lin_kv_kernel<KB, VB, 3>), grid, block, 0, stream, a, v, dk_out);
+  else hipLaunchKernelGGL((lin_kv_kernel<KB, VB, 2>), grid, block, 0, stream, a, v, dk_out);
+}
+}  // namespace
+
+hipError_t launch_lin_kv(const LinScan& a, const LinOperand& v, void* dk_out, hipStream_t stream) {
+  if (a.dv <= 64) a.dk <= 64 ? kv_launch<2, 2>(a, v, dk_out, stream) : kv_launch<4, 2>(a, v, dk_out, stream);
+  else a.dk <= 64 ? kv_launch<2, 4>(a, v, dk_out, stream) : kv_launch<4, 4>(a, v, dk_out, stream);
   return hipGetLastError();
 }
 

@@ -11,14 +11,18 @@ namespace ssd {
 constexpr int kC = 64;                       // tokens a chunk
 constexpr int kPitchP = lds_pitch(kC);       // LDS row of 64 scores
 
-// Powers of the decay, pw[kPowZero + e] = factor lam^e for e = 0 .. 64 and 0 for
-// e = -64 .. -1: the weight of every pair and token of a chunk is one LDS read
-// (an exponential costs a wave as long as sixteen multiplies, and a chunk has
-// some forty weights a lane).
+// Powers of the decay, pw[kPowZero + e] = lam^e for e = 0 .. 64 and 0 for e = -64
+// .. -1, spw scale times them: the weight of every pair and token of a chunk is
+// one LDS read (an exponential costs a wave as long as sixteen multiplies, and
+// a chunk has some forty weights a lane). They are rounded once, from 64 bits:
+// lam^64 carries the state from chunk to chunk, and an error in it compounds.
 constexpr int kPowZero = 64, kPowSize = 132;
-__device__ __forceinline__ void fill_powers(float* pw, float g2, float factor) {
-  for (int i = threadIdx.x; i < kPowSize; i += blockDim.x)
-    pw[i] = i < kPowZero ? 0.f : factor * fast_exp2(g2 * (float)(i - kPowZero));
+__device__ __forceinline__ void fill_powers(float* pw, float* spw, float log_decay, float scale) {
+  for (int i = threadIdx.x; i < kPowSize; i += blockDim.x) {
+    const double x = i < kPowZero ? 0.0 : lin_power(log_decay, i - kPowZero);
+    pw[i] = (float)x;
+    if (spw) spw[i] = (float)(x * (double)scale);
+  }
 }
 
 // Weights of the tokens 32 kp + 16 (s / 4) + 4 g + s % 4, s = 0 .. 7, of a chunk
@@ -38,13 +42,19 @@ __device__ __forceinline__ void token_weights(const float* pw, int n, int kp, in
   }
 }
 
-// v w, element by element, as the sum of two bf16 values, each rounded to nearest.
-__device__ __forceinline__ void split_weighted(u32x4 v, const float* w, u32x4& hi, u32x4& lo) {
+// v w, element by element, as the sum of TERMS bf16 values, each rounded to
+// nearest: two leave 2^-16 of it, three 2^-24.
+template <int TERMS>
+__device__ __forceinline__ void split_weighted(u32x4 v, const float* w, u32x4* part) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const float x = bf16_lo(v[c]) * w[2 * c], y = bf16_hi(v[c]) * w[2 * c + 1];
-    hi[c] = pack_bf16x2(x, y);
-    lo[c] = pack_bf16x2(x - bf16_lo(hi[c]), y - bf16_hi(hi[c]));
+    float x = bf16_lo(v[c]) * w[2 * c], y = bf16_hi(v[c]) * w[2 * c + 1];
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) {
+      part[t][c] = pack_bf16x2(x, y);
+      x -= bf16_lo(part[t][c]);
+      y -= bf16_hi(part[t][c]);
+    }
   }
 }
 

@@ -13,8 +13,10 @@
 //           accumulator pair; Q's columns lie in LDS in that order);
 //   intra   O^T += V^T P^T;
 //   state   D^T += K^T (lam^(C-1-j) V), the weighted V as the sum of two bf16
-//           values (2^-16 of it is dropped): the state is an fp32 result that
-//           is carried on, and one bf16 rounding of each term would show in it.
+//           values: the state is carried on, and one bf16 rounding of each term
+//           would weigh as much as that of the state itself as an operand. Of
+//           three where the last state is asked for, an fp32 result: its error
+//           is then that of 32-bit sums.
 // Roundings to bf16: the weighted scores and the state as operands, and O.
 //
 // A chunk moves C (2 dk + 2 dv) 2 bytes and makes 2 C (C + 3 dk) dv multiplies
@@ -29,8 +31,9 @@ namespace ssd {
 
 namespace {
 
-// KB: dk in units of 32. W waves of CB blocks of 16 value columns.
-template <int KB, int W, int CB, bool STATE_ONLY>
+// KB: dk in units of 32. W waves of CB blocks of 16 value columns. TERMS: bf16
+// terms of the weighted V in the state product.
+template <int KB, int W, int CB, int TERMS, bool STATE_ONLY>
 __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks) {
   constexpr int kDk = 32 * KB, kDv = 16 * W * CB, kThreads = 64 * W;
   constexpr int kPitchK = lds_pitch(kDk), kPitchV = lds_pitch(kDv);
@@ -54,7 +57,6 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
   const bool last = pos0 + total >= p.len;
   if (STATE_ONLY && last) return;  // the scan carries the last block's state itself
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
-  const float g2 = lin_log2_decay(a.ld, h);
   const long mat = (long)a.dv * a.dk;
 
   // The state: block b of column block cb holds D[dv][dk] at dv = dv0 + 16 (CB wave + cb) + c16, dk = 16 b + 4 g + r.
@@ -89,8 +91,7 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
 
   constexpr int kTasks = 8 / W;   // score tasks (16 queries by 32 keys) a wave
 
-  fill_powers(pw, g2, 1.f);
-  if (!STATE_ONLY) fill_powers(spw, g2, a.scale);
+  fill_powers(pw, STATE_ONLY ? nullptr : spw, a.ld[h], a.scale);
 
   const int qrow = (int)a.q.row * 2, krow = (int)a.k.row * 2, vrow = (int)a.v.row * 2;  // 64 rows are fewer than 2^31 bytes
   Piece qp[STATE_ONLY ? 1 : kQK], kp_[kQK], vp[kV];
@@ -140,10 +141,10 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
   // finds the rows that were read last in the memory-side cache.
   const int chunks = (total + kC - 1) / kC;
   if (chunks > 0) load(STATE_ONLY ? (chunks - 1) * kC : 0);
+  float behind = 1.f;   // STATE_ONLY: lam to the tokens of the block behind the chunk
   for (int ci = 0; ci < chunks; ++ci) {
     const int t0 = (STATE_ONLY ? chunks - 1 - ci : ci) * kC;
     const int n = min(kC, total - t0);
-    const int after = STATE_ONLY ? total - t0 - n : 0;  // tokens of the block behind this chunk
     const int lead = a.rev && pos0 + t0 == 0 ? 0 : 1;   // the state handed to a reversed scan is not decayed first
     __syncthreads();
 #pragma unroll
@@ -247,19 +248,19 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
     }
 
     // State: decay by the chunk, add K^T (weighted V). Token of slot s of pair kp: 32 kp + 16 (s / 4) + 4 g + s % 4.
-    u32x4 hi[CB][2], lo[CB][2];
+    u32x4 part[CB][2][TERMS];
 #pragma unroll
     for (int kp = 0; kp < 2; ++kp) {
       float w[8];
       token_weights(pw, n, kp, g, w);
       if (STATE_ONLY) {
-        const float behind = fast_exp2(g2 * (float)after);
 #pragma unroll
         for (int s = 0; s < 8; ++s) w[s] *= behind;
       }
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) split_weighted(vf[cb][kp], w, hi[cb][kp], lo[cb][kp]);
+      for (int cb = 0; cb < CB; ++cb) split_weighted<TERMS>(vf[cb][kp], w, part[cb][kp]);
     }
+    behind *= pw[kPowZero + n];
     const float keep = pw[kPowZero + n - 1 + lead];
 #pragma unroll
     for (int b = 0; b < 2 * KB; ++b) {
@@ -271,9 +272,9 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
       for (int kp = 0; kp < 2; ++kp) {
         const u32x4 kf = frag_k_rows_accpair(Ks, kPitchK, 32 * kp, 16 * b, lane);
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) S[cb][b] = mfma16x16x32(kf, hi[cb][kp], S[cb][b]);
+        for (int t = 0; t < TERMS; ++t)
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) S[cb][b] = mfma16x16x32(kf, lo[cb][kp], S[cb][b]);
+          for (int cb = 0; cb < CB; ++cb) S[cb][b] = mfma16x16x32(kf, part[cb][kp][t], S[cb][b]);
       }
     }
   }
@@ -284,7 +285,7 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
     dst = a.states + (slot * a.H + h) * mat;
   } else if (last && a.fin) {
     dst = a.fin + ((long)p.seq * a.H + h) * mat;
-    sc = a.fin_scale * (a.rev && p.len > 0 ? fast_exp2(g2) : 1.f);
+    sc = a.fin_scale * (a.rev && p.len > 0 ? pw[kPowZero + 1] : 1.f);
   }
   if (dst) {
 #pragma unroll
@@ -299,16 +300,16 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
   }
 }
 
-template <int KB, int W, int CB>
+template <int KB, int W, int CB, int TERMS>
 __global__ __launch_bounds__(64 * W, KB <= 4 ? W / 2 : W / 4) void lin_mfma_kernel(LinScan a) {
-  lin_mfma<KB, W, CB, false>(a, blockIdx.x, gridDim.x);
+  lin_mfma<KB, W, CB, TERMS, false>(a, blockIdx.x, gridDim.x);
 }
 
 // The blocks' own sums of one scan, or of two: the first `na` workgroups are a's.
-template <int KB, int W, int CB>
+template <int KB, int W, int CB, int TERMS>
 __global__ __launch_bounds__(64 * W, KB <= 4 ? W / 2 : W / 4) void lin_mfma_states_kernel(LinScan a, LinScan b, long na) {
-  if ((long)blockIdx.x < na) lin_mfma<KB, W, CB, true>(a, blockIdx.x, na);
-  else lin_mfma<KB, W, CB, true>(b, blockIdx.x - na, gridDim.x - na);
+  if ((long)blockIdx.x < na) lin_mfma<KB, W, CB, TERMS, true>(a, blockIdx.x, na);
+  else lin_mfma<KB, W, CB, TERMS, true>(b, blockIdx.x - na, gridDim.x - na);
 }
 
 long mfma_blocks(const LinScan& a) {
@@ -317,13 +318,18 @@ long mfma_blocks(const LinScan& a) {
   return slots * a.H * ((a.dv + tile - 1) / tile);
 }
 
-// The instance for sizes dk and dv: f(KB, W, CB) as integral constants.
+// The instance for sizes dk and dv and a state that is an fp32 result or not:
+// f(KB, W, TERMS) as integral constants.
 template <typename F>
-void mfma_instance(int dk, int dv, F f) {
+void mfma_instance(int dk, int dv, bool fine, F f) {
   using std::integral_constant;
   auto wide = [&](auto kb) {
-    if (lin_mfma_tile(dv) == 128) f(kb, integral_constant<int, 8>{}, integral_constant<int, 1>{});
-    else f(kb, integral_constant<int, 4>{}, integral_constant<int, 1>{});
+    auto terms = [&](auto w) {
+      if (fine) f(kb, w, integral_constant<int, 3>{});
+      else f(kb, w, integral_constant<int, 2>{});
+    };
+    if (lin_mfma_tile(dv) == 128) terms(integral_constant<int, 8>{});
+    else terms(integral_constant<int, 4>{});
   };
   if (dk <= 32) wide(integral_constant<int, 1>{});
   else if (dk <= 64) wide(integral_constant<int, 2>{});
@@ -339,9 +345,9 @@ int k_class(int dk) { return dk <= 32 ? 1 : dk <= 64 ? 2 : dk <= 128 ? 4 : 8; }
 int lin_mfma_tile(int dv) { return dv <= 64 ? 64 : 128; }
 
 hipError_t launch_lin_mfma(const LinScan& a, hipStream_t stream) {
-  mfma_instance(a.dk, a.dv, [&](auto kb, auto w, auto cb) {
-    constexpr int KB = decltype(kb)::value, W = decltype(w)::value, CB = decltype(cb)::value;
-    hipLaunchKernelGGL((lin_mfma_kernel<KB, W, CB>), dim3((unsigned)mfma_blocks(a)), dim3(64 * W), 0, stream, a);
+  mfma_instance(a.dk, a.dv, a.fine(), [&](auto kb, auto w, auto terms) {
+    constexpr int KB = decltype(kb)::value, W = decltype(w)::value, TERMS = decltype(terms)::value;
+    hipLaunchKernelGGL((lin_mfma_kernel<KB, W, 1, TERMS>), dim3((unsigned)mfma_blocks(a)), dim3(64 * W), 0, stream, a);
   });
   return hipGetLastError();
 }
@@ -351,10 +357,10 @@ hipError_t launch_lin_mfma_states(const LinScan& a, const LinScan* b, hipStream_
     const hipError_t e = launch_lin_mfma_states(a, nullptr, stream);
     return e == hipSuccess ? launch_lin_mfma_states(*b, nullptr, stream) : e;
   }
-  mfma_instance(a.dk, a.dv, [&](auto kb, auto w, auto cb) {
-    constexpr int KB = decltype(kb)::value, W = decltype(w)::value, CB = decltype(cb)::value;
+  mfma_instance(a.dk, a.dv, a.fine() || (b && b->fine()), [&](auto kb, auto w, auto terms) {
+    constexpr int KB = decltype(kb)::value, W = decltype(w)::value, TERMS = decltype(terms)::value;
     const long na = mfma_blocks(a), all = na + (b ? mfma_blocks(*b) : 0);
-    hipLaunchKernelGGL((lin_mfma_states_kernel<KB, W, CB>), dim3((unsigned)all), dim3(64 * W), 0, stream, a, b ? *b : a, na);
+    hipLaunchKernelGGL((lin_mfma_states_kernel<KB, W, 1, TERMS>), dim3((unsigned)all), dim3(64 * W), 0, stream, a, b ? *b : a, na);
   });
   return hipGetLastError();
 }
