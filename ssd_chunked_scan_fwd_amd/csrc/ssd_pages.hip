@@ -197,7 +197,9 @@ hipError_t launch_pages_copy(const PagesArgs& a, const int32_t* src, const int32
     using W = decltype(w);
     const long pieces = a.page / (long)sizeof(W);
     const long ranges = a.layers * ((pieces + lanes - 1) / lanes);
-    const unsigned blocks = (unsigned)(ranges < 2048 ? ranges : 2048);
+    // Two ranges or more a workgroup, so that its list is checked less often (28
+    // pages of 2 MiB forked from 4: 17 us with 1024 workgroups, 19 with 2048, 18.5 with 512).
+    const unsigned blocks = (unsigned)(ranges < 1024 ? ranges : 1024);
     hipLaunchKernelGGL(pages_copy_kernel<W>, dim3(blocks), dim3(kPageThreads), 0, stream, a, src, dst, n, lanes, ranges);
   });
   return hipGetLastError();
