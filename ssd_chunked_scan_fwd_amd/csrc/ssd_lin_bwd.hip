@@ -130,6 +130,7 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
     for (int b = 0; b < KB; ++b)
       *reinterpret_cast<u32x2*>(Rs + dvc * kPitchK + 16 * (KB * half + b) + 4 * g) =
           u32x2{pack_bf16x2(R[b][0], R[b][1]), pack_bf16x2(R[b][2], R[b][3])};
+    if (t0 + kC < total) load(t0 + kC);
     __syncthreads();
 
     // Scores: token j = 16 qb + c16 (columns) with tokens i = 32 kp + 16 t + 4 g + r (rows).
@@ -163,7 +164,6 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
       *reinterpret_cast<u32x4*>(Ps[of_v] + (16 * qb + c16) * kPitchP + 32 * kp + 8 * g) =
           u32x4{pack_bf16x2(s0[0], s0[1]), pack_bf16x2(s0[2], s0[3]), pack_bf16x2(s1[0], s1[1]), pack_bf16x2(s1[2], s1[3])};
     }
-    if (t0 + kC < total) load(t0 + kC);
 
     // Terms of R: dV^T (rows: the wave's value block; two token blocks) and dK^T (rows: its key block).
     f32x4 OV[2], OK[kDkTok];

@@ -161,6 +161,7 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
       const int i = threadIdx.x + kThreads * j;
       *reinterpret_cast<u32x4*>(Vs + i / (kDv / 8) * kPitchV + 8 * (i % (kDv / 8))) = vn[j];
     }
+    if (ci + 1 < chunks) load(STATE_ONLY ? t0 - kC : t0 + kC);
     __syncthreads();
 
     if (!STATE_ONLY) {
@@ -187,7 +188,6 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
             u32x4{pack_bf16x2(s0[0], s0[1]), pack_bf16x2(s0[2], s0[3]), pack_bf16x2(s1[0], s1[1]), pack_bf16x2(s1[2], s1[3])};
       }
     }
-    if (ci + 1 < chunks) load(STATE_ONLY ? t0 - kC : t0 + kC);
 
     u32x4 vf[CB][2];
 #pragma unroll
