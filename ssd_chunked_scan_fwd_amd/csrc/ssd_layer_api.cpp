@@ -313,12 +313,21 @@ ssd_status ssd_lin_attn_bwd(const void* q, const void* k, const void* v, const f
   }
   if (e != hipSuccess) return SSD_ERR_HIP;
   if (rep > 1) {
-    const int bf16 = shape->dtype == SSD_DTYPE_BF16;
-    e = ssd::launch_lin_share_sum(reinterpret_cast<const float*>(ws + L.part_v), dv, cu_seqlens, shape->num_seqs,
-                                  (long)d.tokens, shape->seqlen, H, Hk, shape->dv, hs, bf16);
-    if (e == hipSuccess)
-      e = ssd::launch_lin_share_sum(reinterpret_cast<const float*>(ws + L.part_k), dk, cu_seqlens, shape->num_seqs,
-                                    (long)d.tokens, shape->seqlen, H, Hk, shape->dk, hs, bf16);
+    ssd::LinShareSum sum;
+    sum.in_k = static_cast<const float*>(dk_out);
+    sum.in_v = static_cast<const float*>(dv_out);
+    sum.out_k = dk;
+    sum.out_v = dv;
+    sum.cu = cu_seqlens;
+    sum.tokens = (long)d.tokens;
+    sum.S = shape->num_seqs;
+    sum.T = shape->seqlen;
+    sum.H = H;
+    sum.Hk = Hk;
+    sum.dk = shape->dk;
+    sum.dv = shape->dv;
+    sum.bf16 = shape->dtype == SSD_DTYPE_BF16;
+    e = ssd::launch_lin_share_sum(sum, hs);
   }
   return hip_status(e);
 }

@@ -66,6 +66,7 @@ hipError_t launch_lin_outputs(const LinScan& a, hipStream_t stream);
 // bf16 operands: the scan on matrix instructions (ssd_lin_scan.hip), either the
 // blocks' own sums or, from the entering states, the outputs.
 int lin_mfma_tile(int dv);
+int lin_mfma_target(int dk, int dv);   // workgroups that run at once
 hipError_t launch_lin_mfma(const LinScan& a, hipStream_t stream);
 hipError_t launch_lin_mfma_states(const LinScan& a, const LinScan* b, hipStream_t stream);
 
@@ -73,12 +74,19 @@ hipError_t launch_lin_mfma_states(const LinScan& a, const LinScan* b, hipStream_
 // 128 (ssd_lin_bwd.hip): `a` is the scan for dv; `v` and `dk_out` are what dk
 // takes besides.
 bool lin_kv_supported(int dk, int dv, int bf16);
-int lin_kv_target(int dv);
+int lin_kv_target(int dk, int dv);
 hipError_t launch_lin_kv(const LinScan& a, const LinOperand& v, void* dk_out, hipStream_t stream);
 
-// out[token][kv head][i] = sum of in over the heads that share it, in head order.
-hipError_t launch_lin_share_sum(const float* in, void* out, const int32_t* cu, int S, long tokens, int T, int H, int Hk,
-                                int d, hipStream_t stream, int bf16);
+// out[token][key head][i] = sum of in over the query heads that share it, in
+// head order, for keys (size dk) and values (dv).
+struct LinShareSum {
+  const float *in_k = nullptr, *in_v = nullptr;
+  void *out_k = nullptr, *out_v = nullptr;
+  const int32_t* cu = nullptr;
+  long tokens = 0;
+  int S = 0, T = 0, H = 0, Hk = 0, dk = 0, dv = 0, bf16 = 0;
+};
+hipError_t launch_lin_share_sum(const LinShareSum& a, hipStream_t stream);
 
 struct LinStep {
   float* state = nullptr;      // [num_slots][H][dv][dk]

@@ -38,7 +38,7 @@ __device__ __forceinline__ float load_el(const void* p, long i) {
 // STATE_ONLY leaves each block's own sum (from a zero state) in a.states;
 // the other form starts from the block's entering state and writes o.
 // ----------------------------------------------------------------------------
-constexpr int kRecRows = 16, kRecTok = 16;
+constexpr int kRecRows = 16, kRecTok = 16, kC64 = 64;
 
 template <int NQ, bool STATE_ONLY>
 __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
@@ -207,9 +207,8 @@ __device__ __forceinline__ void lin_pass(const LinScan& a, int s) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int b = b0 + k + 1;
-      if (b >= nb) break;
       D = D * (b == 1 ? w0 : w) + own;
-      *reinterpret_cast<f32x4*>(at + b * step) = D;
+      if (b < nb) *reinterpret_cast<f32x4*>(at + b * step) = D;
       own = next[k];
     }
   }
@@ -224,27 +223,28 @@ __global__ __launch_bounds__(256) void lin_passing2_kernel(LinScan a, LinScan b)
 }
 
 // Sum over the heads that share a key head, eight values a thread, in head
-// order. Packed batches: tokens before the first and behind the last sequence
-// are left as they were.
+// order: the gradients of keys (blockIdx.y = 0) and of values. Packed batches:
+// tokens before the first and behind the last sequence are left as they were.
 template <bool BF16>
-__global__ __launch_bounds__(256) void lin_share_sum_kernel(const float* __restrict__ in, void* __restrict__ out,
-                                                            const int32_t* __restrict__ cu, int S, long tokens, int T,
-                                                            int H, int Hk, int d) {
+__global__ __launch_bounds__(256) void lin_share_sum_kernel(LinShareSum a) {
+  const int d = blockIdx.y ? a.dv : a.dk;
+  const float* __restrict__ in = blockIdx.y ? a.in_v : a.in_k;
+  void* __restrict__ out = blockIdx.y ? a.out_v : a.out_k;
   const int pieces = d >> 3;
   const long i = (long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= tokens * Hk * pieces) return;
+  if (i >= a.tokens * a.Hk * pieces) return;
   const int c = (int)(i % pieces);
   const long th = i / pieces;
-  const long tok = th / Hk;
-  const int hk = (int)(th % Hk), rep = H / Hk;
-  if (cu && (tok < max(cu[0], 0) || tok >= min(cu[S], T))) return;
-  const float* src = in + (tok * H + (long)hk * rep) * d + 8 * c;
+  const long tok = th / a.Hk;
+  const int hk = (int)(th % a.Hk), rep = a.H / a.Hk;
+  if (a.cu && (tok < max(a.cu[0], 0) || tok >= min(a.cu[a.S], a.T))) return;
+  const float* src = in + (tok * a.H + (long)hk * rep) * d + 8 * c;
   f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
   for (int j = 1; j < rep; ++j) {
     lo += *reinterpret_cast<const f32x4*>(src + (long)j * d);
     hi += *reinterpret_cast<const f32x4*>(src + (long)j * d + 4);
   }
-  const long at = (tok * Hk + hk) * d + 8 * c;
+  const long at = (tok * a.Hk + hk) * d + 8 * c;
   if constexpr (BF16) {
     *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + at) =
         u32x4{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
@@ -370,18 +370,36 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStep a, int tpr, int p
 
 }  // namespace
 
-// Sequences are cut only as far as it takes to fill the chip: every cut costs
-// its state's way through memory, and the products k v^T a second time.
+// Sequences are cut so that the chip is filled, but every cut costs its state's
+// way through memory, and the products k v^T a second time; and workgroups that
+// do not fit at once cost a whole further round. So the number of blocks a
+// sequence (of mean length, where packed) is the one of least cost, counted in
+// chunks of 64 tokens: rounds of (chunks + start-up) each, times 1.45 for the
+// blocks' own sums, plus the passing launch and the states' bytes.
 int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16, bool kv) {
   const long seqs = S > 0 ? S : batch;
   const int tile = kv ? dv : bf16 ? lin_mfma_tile(dv) : kRecRows;
-  const long units = (long)H * ((dv + tile - 1) / tile);
-  const long target = kv ? lin_kv_target(dv) : bf16 ? 512 : 1024;
-  long L = seqs * units >= target ? T : (long)batch * T * units / target;
-  L = (L + 63) / 64 * 64;
-  if (L < 64) L = 64;
-  if (L > T) L = ((long)T + 63) / 64 * 64;
-  return (int)L;
+  const long units = (long)H * ((dv + tile - 1) / tile) * seqs;
+  const long fit = kv ? lin_kv_target(dk, dv) : bf16 ? lin_mfma_target(dk, dv) : 1024;   // workgroups that run at once
+  const double start = bf16 ? 2.0 : 0.5, pass = bf16 ? 2.5 : 0.7;
+  const double chunk_us = bf16 ? (dk > 64 && dv > 64 ? 7.0 : 2.5) : 6.4;
+  const long len = ((long)T * batch + seqs - 1) / seqs, chunks = (len + kC64 - 1) / kC64;
+  const double state = (double)seqs * H * dk * dv * 4 * 4 / 5e6 / chunk_us;   // four passes over a block's states, at 5 TB/s
+  long best = chunks;
+  double least = 0.0;
+  for (long nb = 1; nb <= chunks && nb <= 512; ++nb) {
+    const long c = (chunks + nb - 1) / nb, blocks = (chunks + c - 1) / c;
+    const long rounds = (units * blocks + fit - 1) / fit;
+    const double cost = (double)rounds * (double)(c + start) * (blocks > 1 ? 1.45 : 1.0) +
+                        (blocks > 1 ? pass + (double)(blocks - 1) * state : 0.0);
+    if (nb == 1 || cost < least) {
+      least = cost;
+      best = c;
+    }
+  }
+  // One block a sequence: as long as the longest can be.
+  if (best == chunks) return (int)(((long)T + kC64 - 1) / kC64 * kC64);
+  return (int)(best * kC64);
 }
 
 namespace {
@@ -424,12 +442,11 @@ hipError_t launch_lin_scan(const LinScan& a, hipStream_t stream) {
   return e == hipSuccess ? launch_lin_outputs(a, stream) : e;
 }
 
-hipError_t launch_lin_share_sum(const float* in, void* out, const int32_t* cu, int S, long tokens, int T, int H, int Hk,
-                                int d, hipStream_t stream, int bf16) {
-  const long n = tokens * Hk * (d / 8);
-  const dim3 grid((unsigned)((n + 255) / 256));
-  if (bf16) hipLaunchKernelGGL(lin_share_sum_kernel<true>, grid, dim3(256), 0, stream, in, out, cu, S, tokens, T, H, Hk, d);
-  else hipLaunchKernelGGL(lin_share_sum_kernel<false>, grid, dim3(256), 0, stream, in, out, cu, S, tokens, T, H, Hk, d);
+hipError_t launch_lin_share_sum(const LinShareSum& a, hipStream_t stream) {
+  const long n = a.tokens * a.Hk * ((a.dk > a.dv ? a.dk : a.dv) / 8);
+  const dim3 grid((unsigned)((n + 255) / 256), 2);
+  if (a.bf16) hipLaunchKernelGGL(lin_share_sum_kernel<true>, grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL(lin_share_sum_kernel<false>, grid, dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -269,8 +269,8 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
 
 bool lin_kv_supported(int dk, int dv, int bf16) { return bf16 && dk <= 128 && dv <= 128; }
 
-// Workgroups that fill the chip: one of sixteen waves a CU, or two of eight.
-int lin_kv_target(int dv) { return dv <= 64 ? 512 : 256; }
+// Workgroups that run at once: one of sixteen waves a CU, or two of eight where LDS holds them.
+int lin_kv_target(int dk, int dv) { return dv <= 64 && dk <= 64 ? 512 : 256; }
 
 namespace {
 template <int KB, int VB>

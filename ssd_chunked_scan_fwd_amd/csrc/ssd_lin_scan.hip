@@ -344,6 +344,14 @@ int k_class(int dk) { return dk <= 32 ? 1 : dk <= 64 ? 2 : dk <= 128 ? 4 : 8; }
 // Value columns of one workgroup: 64 up to dv = 64, else 128.
 int lin_mfma_tile(int dv) { return dv <= 64 ? 64 : 128; }
 
+// Four waves a SIMD with dk up to 64, and with eight-wave workgroups up to 128
+// (launch bounds, and LDS of two of them a CU); one workgroup a CU above.
+int lin_mfma_target(int dk, int dv) {
+  const int cus = 256;
+  if (dk > 128) return cus;
+  return lin_mfma_tile(dv) == 128 ? 2 * cus : dk <= 64 ? 4 * cus : 2 * cus;
+}
+
 hipError_t launch_lin_mfma(const LinScan& a, hipStream_t stream) {
   mfma_instance(a.dk, a.dv, a.fine(), [&](auto kb, auto w, auto terms) {
     constexpr int KB = decltype(kb)::value, W = decltype(w)::value, TERMS = decltype(terms)::value;
