@@ -8,6 +8,7 @@ current stream. The library is loaded on first use; a missing library raises
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -649,12 +650,14 @@ def _token_row(t: torch.Tensor, name: str) -> int:
 
 def _expect_device(specs, device, align: int = 16):
     """Device and alignment of every given (tensor, name)."""
+    index = device.index if device.type == "cuda" else -1
     for t, name in specs:
         if t is None:
             continue
-        if not t.is_cuda:
+        at = t.get_device()
+        if at < 0:
             raise ValueError(f"{name} must be a device tensor")
-        if t.device != device:
+        if at != index:
             raise ValueError(f"{name} is on {t.device}, expected {device}")
         if t.data_ptr() % align:
             raise ValueError(f"{name} must be {align}-byte aligned")
@@ -701,12 +704,28 @@ def _structure(specs):
             raise ValueError(f"{name} must be contiguous")
 
 
-def _lin_workspace(fn: str, shape: LinShape, workspace, device):
+@functools.lru_cache(maxsize=256)
+def _size_of(fn: str, struct, values, *more) -> int:
+    """A workspace size query: a function of the sizes alone, asked once for each."""
     n = ctypes.c_size_t(0)
-    _call(fn, ctypes.byref(shape), ctypes.byref(n))
-    if workspace is None or workspace.numel() < n.value:
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
-    return workspace, (0 if workspace is None else workspace.numel())
+    _call(fn, ctypes.byref(struct(*values)), *more, ctypes.byref(n))
+    return int(n.value)
+
+
+def _room(size: int, workspace, device):
+    """The workspace of a call and its size: the caller's where it is large enough."""
+    if workspace is not None and workspace.numel() >= size:
+        return workspace, workspace.numel()
+    return (torch.empty(size, dtype=torch.uint8, device=device) if size else None), size
+
+
+def _lin_values(shape: LinShape):
+    return (shape.batch, shape.seqlen, shape.nheads, shape.nkv_heads, shape.dk, shape.dv, shape.num_seqs, shape.dtype,
+            shape.q_row, shape.k_row, shape.v_row)
+
+
+def _lin_workspace(fn: str, shape: LinShape, workspace, device):
+    return _room(_size_of(fn, LinShape, _lin_values(shape)), workspace, device)
 
 
 def lin_attn_shape(q, k, v, cu_seqlens=None) -> LinShape:
@@ -883,11 +902,9 @@ def _norm_shape(x, groups, z, act, gate, center) -> NormShape:
 
 
 def _norm_workspace(shape: NormShape, backward: int, workspace, device):
-    n = ctypes.c_size_t(0)
-    _call("ssd_group_norm_workspace_bytes", ctypes.byref(shape), backward, ctypes.byref(n))
-    if workspace is None or workspace.numel() < n.value:
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
-    return workspace, (0 if workspace is None else workspace.numel())
+    values = (shape.samples, shape.positions, shape.channels, shape.groups, shape.x_row, shape.z_row, shape.dtype, shape.act,
+              shape.gate, shape.center)
+    return _room(_size_of("ssd_group_norm_workspace_bytes", NormShape, values, backward), workspace, device)
 
 
 def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -1010,14 +1027,12 @@ def pages_compact(pool: torch.Tensor, live: torch.Tensor, where: Optional[torch.
     _expect_device([(pool, "pool"), (live, "live")], pool.device, 1)
     _expect_device([(where, "where"), (count, "count")], pool.device, 4)
     _expect_device([(workspace, "workspace")], pool.device, 256)
-    n = ctypes.c_size_t(0)
-    _call("ssd_pages_compact_workspace_bytes", ctypes.byref(shape), ctypes.byref(n))
-    if workspace is None or workspace.numel() < n.value:
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=pool.device)
+    size = _size_of("ssd_pages_compact_workspace_bytes", PagesShape, (shape.layers, shape.slots, shape.page_bytes))
+    workspace, have = _room(size, workspace, pool.device)
     if where is None:
         where = torch.empty(shape.slots, dtype=torch.int32, device=pool.device)
     if count is None:
         count = torch.empty(1, dtype=torch.int32, device=pool.device)
     _call_on(pool.device, "ssd_pages_compact", _addr(pool), _addr(live), _addr(where), _addr(count), ctypes.byref(shape),
-             _addr(workspace), workspace.numel())
+             _addr(workspace), have)
     return where, count
