@@ -460,7 +460,10 @@ ssd_status ssd_step_mamba2(float* state, const void* x, const float* dt, const f
  * and of the gradients before cu[0] or from cu[num_seqs] on are left as they
  * were. Entries outside [0, seqlen] are brought into it.
  * dk and dv: multiples of 8 up to 256. bf16 products are formed with fp32
- * sums; states are carried in fp32.
+ * sums; states are carried in fp32. Every token of a sequence counts, so a
+ * batch padded to one length is passed packed (cu_seqlens); what lies outside
+ * the sequences may be anything. Inside one, a non-finite v may reach the
+ * outputs of up to 63 tokens before it (bf16).
  * ------------------------------------------------------------------------- */
 typedef struct {
   int32_t batch;      /* rows; 1 with cu_seqlens; the step: entries            */
@@ -482,7 +485,7 @@ ssd_status ssd_lin_attn_workspace_bytes(const ssd_lin_shape* shape, size_t* byte
 ssd_status ssd_lin_attn_bwd_workspace_bytes(const ssd_lin_shape* shape, size_t* bytes);
 
 /* The form over prompts. initial_state and final_state may be NULL (zero; not
- * wanted). scale: finite and not 0. */
+ * wanted). scale: a normal number, not 0. */
 ssd_status ssd_lin_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay,
                             const int32_t* cu_seqlens, float scale, const float* initial_state, void* o,
                             float* final_state, const ssd_lin_shape* shape, void* workspace, size_t workspace_bytes,

@@ -18,7 +18,7 @@ namespace {
 ssd_status hip_status(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
-bool scale_ok(float s) { return std::isfinite(s) && s != 0.f; }
+bool scale_ok(float s) { return std::isnormal(s); }  // its reciprocal is taken
 
 // ---------------------------------------------------------------- linear attention
 

@@ -123,14 +123,17 @@ __device__ __forceinline__ LinPiece lin_piece(const LinScan& a, long slot) {
     return p;
   }
   // Slots of sequence s begin at floor(cu[s] / L) + s, which grows with s: count those at or before `slot`.
+  // halving the range down to a wave's width, the rest with one load a lane.
   const int lane = (int)threadIdx.x & 63;
-  int n = 0;
-  for (int i0 = 0; i0 < a.S; i0 += 64) {
-    const int i = i0 + lane;
-    bool in = false;
-    if (i < a.S) in = (long)min(max(a.cu[i], 0), a.T) / a.L + i <= slot;
-    n += __popcll(__ballot(in));
+  auto begins = [&](int i) { return (long)min(max(a.cu[i], 0), a.T) / a.L + i; };
+  int lo = 0, hi = a.S;
+  while (hi - lo > 64) {
+    const int mid = __builtin_amdgcn_readfirstlane((lo + hi) / 2);
+    if (begins(mid) <= slot) lo = mid;
+    else hi = mid;
   }
+  const bool in = lo + lane < hi && begins(lo + lane) <= slot;
+  const int n = lo + __popcll(__ballot(in));
   p.seq = __builtin_amdgcn_readfirstlane(n - 1);
   if (p.seq < 0) {
     p.seq = 0;
@@ -150,13 +153,14 @@ __device__ __forceinline__ LinPiece lin_piece(const LinScan& a, long slot) {
 
 // lam^e in 64 bits (a log decay of -inf: 0 for e > 0, 1 for e = 0).
 __device__ __forceinline__ double lin_power(float log_decay, int e) {
-  return exp((double)fmaxf(log_decay, -11356.f) * (double)e);
+  return exp((double)(log_decay < -11356.f ? -11356.f : log_decay) * (double)e);
 }
 
 // log2 of the decay; a log decay of -inf becomes a finite value whose first
 // power already underflows to 0, while its power 0 stays 1.
 __device__ __forceinline__ float lin_log2_decay(const float* ld, int h) {
-  return fmaxf(ld[h] * 1.4426950408889634f, -16384.f);
+  const float g = ld[h] * 1.4426950408889634f;
+  return g < -16384.f ? -16384.f : g;
 }
 
 #endif

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
   if (STATE_ONLY && last) return;  // the scan carries the last block's state itself
   const int r = threadIdx.x >> 4, c = threadIdx.x & 15;
   const int row = row0 + r;
-  const double lam = exp((double)fmaxf(a.ld[h], -11356.f));
+  const double lam = lin_power(a.ld[h], 1);
   const float lam_hi = (float)lam, lam_lo = (float)(lam - (double)lam_hi);
 
   f32x4 s[NQ];  // columns 64 m + 4 c + 0..3

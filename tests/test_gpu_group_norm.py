@@ -185,3 +185,15 @@ def test_gradient_against_differences():
         diff = (loss(up) - loss(down)) / (2 * h)
         got = (n64(g[gk]) * u).sum()
         assert abs(diff - got) <= 2e-5 * np.abs(n64(g[gk]) * u).sum(), (k, diff, got)
+
+
+@pytest.mark.parametrize("C,G", [(8192, 64), (9000, 1)])
+def test_offsets_beyond_32_bits(C, G):
+    """More than 2^31 elements: the last rows as in a call on them alone."""
+    n = 2 ** 31 // C + 300
+    x = torch.empty(n, C, dtype=BF, device="cuda").normal_()
+    y, stats = ssd.group_norm(x, G)
+    y1, s1 = ssd.group_norm(x[-100:], G)
+    assert torch.equal(y[-100:], y1) and torch.equal(stats[-100:], s1)
+    g = ssd.group_norm_bwd(x, G, stats, y)["dx"]
+    assert torch.equal(g[-100:], ssd.group_norm_bwd(x[-100:], G, s1, y1)["dx"])

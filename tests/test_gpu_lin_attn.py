@@ -155,6 +155,43 @@ def test_many_sequences(dtype):
     check_bwd(d, decays(2), 0.2, cu)
 
 
+@pytest.mark.parametrize("S", [64, 65, 700])
+def test_sequence_of_every_slot(S):
+    """As many sequences as a wave has lanes, one more, and far more, some empty: each alone gives the same."""
+    rng = np.random.default_rng(S)
+    cu = [0] + np.cumsum(rng.integers(0, 4, S)).tolist()
+    say(f"[lin] {S} sequences, {cu[-1]} tokens")
+    d = make(1, cu[-1], 2, 1, 16, 16, F32, 61, nseq=S)
+    check_fwd(d, decays(2), 0.3, cu)
+
+
+def test_decay_not_a_number_shows():
+    d = make(1, 80, 2, 2, 32, 32, BF, 63)
+    ld = torch.tensor([float("nan"), -0.1], device="cuda")
+    o, fin = ssd.lin_attn_fwd(d["q"], d["k"], d["v"], ld, initial_state=d["init"])
+    assert torch.all(torch.isnan(fin[:, 0])) and torch.all(torch.isfinite(fin[:, 1])) and torch.all(torch.isfinite(o[:, :, 1]))
+
+
+def test_offsets_beyond_32_bits():
+    """Rows so wide, and a batch so long, that offsets pass 2^31 elements: the last head and the last
+    tokens against a call on them alone (the same kernels on the same 64-token chunks; blocks may
+    be cut elsewhere, so each side is within its bound of the same values)."""
+    H, D, T = 272, 128, 65600
+    ld = decays(H).cuda()
+    n = T * H * D
+    assert n > 2 ** 31
+    q = torch.empty(1, T, H, D, dtype=BF, device="cuda").normal_()
+    k = torch.empty(1, T, 1, D, dtype=BF, device="cuda").normal_()
+    v = torch.empty(1, T, 1, D, dtype=BF, device="cuda").normal_()
+    o, fin = ssd.lin_attn_fwd(q, k, v, ld, scale=0.1)
+    head = q[:, :, H - 1:]
+    assert head.stride(1) == H * D
+    o1, f1 = ssd.lin_attn_fwd(head, k, v, ld[H - 1:], scale=0.1)
+    a, b = o[:, -4096:, H - 1].double(), o1[:, -4096:, 0].double()
+    assert torch.linalg.norm(a - b) <= 2 * 7e-3 * torch.linalg.norm(b)
+    assert torch.linalg.norm(fin[:, H - 1].double() - f1[:, 0].double()) <= 1e-5 * torch.linalg.norm(f1.double())
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_rows_outside_sequences_left_alone(dtype):
     say(f"[lin] rows before and behind the sequences {dtype}")

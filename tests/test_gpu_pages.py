@@ -117,3 +117,17 @@ def test_pool_not_on_a_boundary():
     want = copied(p, [0, 1], [1, 0])
     ssd.pages_copy(p, i32([0, 1]), i32([1, 0]))
     assert torch.equal(p, want)
+
+
+def test_pool_beyond_32_bits():
+    """A pool of 6 GiB: pages whose offsets pass 2^32 bytes."""
+    p = torch.zeros(1, 6, 1 << 30, dtype=torch.uint8, device="cuda")
+    for i in range(6):
+        p[0, i, :4] = i + 1
+        p[0, i, -4:] = 10 * (i + 1)
+    ssd.pages_copy(p, i32([5, 0]), i32([0, 5]))
+    assert p[0, :, 0].tolist() == [6, 2, 3, 4, 5, 1] and p[0, :, -1].tolist() == [60, 20, 30, 40, 50, 10]
+    w, c = ssd.pages_compact(p, torch.tensor([0, 1, 0, 0, 0, 1], dtype=torch.uint8, device="cuda"))
+    assert w.tolist() == [-1, 1, -1, -1, -1, 0] and c.item() == 2 and p[0, 0, -1].item() == 10
+    ssd.pages_clear(p, i32([4]))
+    assert p[0, :, -1].tolist() == [10, 20, 30, 40, 0, 10]

@@ -51,7 +51,7 @@ def test_lin_fwd_validates():
         a = list(args)
         a[i] = ODD
         assert L.ssd_lin_attn_fwd(*a) == INVALID, i
-    for scale in (0.0, float("nan"), float("inf")):
+    for scale in (0.0, 1e-42, float("nan"), float("inf")):
         a = list(args)
         a[5] = scale
         assert L.ssd_lin_attn_fwd(*a) == INVALID
