@@ -26,11 +26,11 @@ template <int KB, int VB, int TERMS>
 __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOperand vop, void* dk_out) {
   constexpr int kWaves = 4 * VB, kThreads = 64 * kWaves;
   constexpr int kPitchK = lds_pitch(32 * KB), kPitchV = lds_pitch(32 * VB);
-  __shared__ __align__(16) uint16_t Qs[kC * kPitchK], Gs[kC * kPitchV];   // q and dO
-  __shared__ __align__(16) uint16_t Ks[kC * kPitchK], Vs[kC * kPitchV];       // k and v, columns in pair order
-  __shared__ __align__(16) uint16_t Ps[2][kC * kPitchP];                  // weighted K Q^T and V dO^T
-  __shared__ __align__(16) uint16_t Rs[32 * VB * kPitchK];                // R, rounded
-  __shared__ __align__(16) float pw[kPowSize], spw[kPowSize];             // powers of lam, and scale times them
+  __shared__ __align__(16) uint16_t Qs[kC * kPitchK], Gs[kC * kPitchV];   // q and dO, rows by row_shift
+  __shared__ __align__(16) uint16_t Ks[kC * kPitchK], Vs[kC * kPitchV];   // k and v, columns in pair order
+  __shared__ __align__(16) uint16_t Ps[2][kC * kPitchP];            // weighted K Q^T and V dO^T
+  __shared__ __align__(16) uint16_t Rs[32 * VB * kPitchK];          // R, rounded, rows by row_shift
+  __shared__ __align__(16) float pw[kPowSize], spw[kPowSize];       // powers of lam, and scale times them
   // 16-byte pieces: with sixteen waves half of the threads stage q and k, the others dO and v.
   constexpr bool kHalves = VB == 4;
   constexpr int kStage = kHalves ? kThreads / 2 : kThreads;
@@ -113,7 +113,7 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
 #pragma unroll
       for (int j = 0; j < kK; ++j) {
         const int i = tid + kStage * j, r = i / (4 * KB), col = i % (4 * KB);
-        *reinterpret_cast<u32x4*>(Qs + r * kPitchK + 8 * col) = x0[j];
+        *reinterpret_cast<u32x4*>(Qs + r * kPitchK + row_shift(r) + 8 * col) = x0[j];
         store_paired(Ks + r * kPitchK, col >> 2, col & 3, x1[j]);
       }
     }
@@ -122,13 +122,13 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
         const int i = tid + kStage * j, r = i / (4 * VB), col = i % (4 * VB);
-        *reinterpret_cast<u32x4*>(Gs + r * kPitchV + 8 * col) = from0[j];
+        *reinterpret_cast<u32x4*>(Gs + r * kPitchV + row_shift(r) + 8 * col) = from0[j];
         store_paired(Vs + r * kPitchV, col >> 2, col & 3, from1[j]);
       }
     }
 #pragma unroll
     for (int b = 0; b < KB; ++b)
-      *reinterpret_cast<u32x2*>(Rs + dvc * kPitchK + 16 * (KB * half + b) + 4 * g) =
+      *reinterpret_cast<u32x2*>(Rs + dvc * kPitchK + row_shift(dvc) + 16 * (KB * half + b) + 4 * g) =
           u32x2{pack_bf16x2(R[b][0], R[b][1]), pack_bf16x2(R[b][2], R[b][3])};
     if (t0 + kC < total) load(t0 + kC);
     __syncthreads();
@@ -142,16 +142,16 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
       if (of_v) {
 #pragma unroll
         for (int j = 0; j < VB; ++j) {
-          const u32x4 x = frag_k_cols_unpaired(Vs, kPitchV, 16 * qb, 32 * j, lane);
-          s0 = mfma16x16x32(frag_k_cols(Gs, kPitchV, 32 * kp, 32 * j, lane), x, s0);
-          s1 = mfma16x16x32(frag_k_cols(Gs, kPitchV, 32 * kp + 16, 32 * j, lane), x, s1);
+          const u32x4 x = frag_k_cols(Vs, kPitchV, 16 * qb, 32 * j, lane);
+          s0 = mfma16x16x32(frag_k_cols_pairs(Gs, kPitchV, 32 * kp, 32 * j, lane), x, s0);
+          s1 = mfma16x16x32(frag_k_cols_pairs(Gs, kPitchV, 32 * kp + 16, 32 * j, lane), x, s1);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
-          const u32x4 x = frag_k_cols_unpaired(Ks, kPitchK, 16 * qb, 32 * j, lane);
-          s0 = mfma16x16x32(frag_k_cols(Qs, kPitchK, 32 * kp, 32 * j, lane), x, s0);
-          s1 = mfma16x16x32(frag_k_cols(Qs, kPitchK, 32 * kp + 16, 32 * j, lane), x, s1);
+          const u32x4 x = frag_k_cols(Ks, kPitchK, 16 * qb, 32 * j, lane);
+          s0 = mfma16x16x32(frag_k_cols_pairs(Qs, kPitchK, 32 * kp, 32 * j, lane), x, s0);
+          s1 = mfma16x16x32(frag_k_cols_pairs(Qs, kPitchK, 32 * kp + 16, 32 * j, lane), x, s1);
         }
       }
       const int diff = 16 * qb - 32 * kp + c16 - 4 * g;
@@ -182,16 +182,14 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
           rf = u32x4{pack_bf16x2(R[2 * j][0], R[2 * j][1]), pack_bf16x2(R[2 * j][2], R[2 * j][3]),
                      pack_bf16x2(R[2 * j + 1][0], R[2 * j + 1][1]), pack_bf16x2(R[2 * j + 1][2], R[2 * j + 1][3])};
         } else {
-          const uint16_t* at = Rs + dvc * kPitchK + col + 4 * g;
-          const u32x2 x = *reinterpret_cast<const u32x2*>(at), y = *reinterpret_cast<const u32x2*>(at + 16);
-          rf = u32x4{x.x, x.y, y.x, y.y};
+          rf = frag_k_cols_pairs(Rs, kPitchK, 16 * vb, col, lane);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) OV[t] = mfma16x16x32(rf, frag_k_cols(Ks, kPitchK, 32 * half + 16 * t, col, lane), OV[t]);
       }
 #pragma unroll
     for (int j = 0; j < VB; ++j) {
-      const u32x4 rt = frag_k_rows_accpair(Rs, kPitchK, 32 * j, 16 * kb0, lane);
+      const u32x4 rt = frag_k_rows_shifted(Rs, kPitchK, 32 * j, 16 * kb0, lane);
 #pragma unroll
       for (int t = 0; t < kDkTok; ++t)
         OK[t] = mfma16x16x32(rt, frag_k_cols(Vs, kPitchV, 16 * (tb0 + t), 32 * j, lane), OK[t]);
@@ -202,7 +200,7 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
     for (int t = 0; t < kDkTok; ++t) OK[t] *= spw[kPowZero + 16 * (tb0 + t) + c16 + lead];
     u32x4 gf[2];   // dO^T of this wave's value block
 #pragma unroll
-    for (int kp = 0; kp < 2; ++kp) gf[kp] = frag_k_rows_accpair(Gs, kPitchV, 32 * kp, 16 * vb, lane);
+    for (int kp = 0; kp < 2; ++kp) gf[kp] = frag_k_rows_shifted(Gs, kPitchV, 32 * kp, 16 * vb, lane);
     __syncthreads();
 
     // Terms of the chunk's own tokens.
@@ -213,7 +211,7 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
         for (int t = 0; t < 2; ++t)
           OV[t] = mfma16x16x32(gf[kp], frag_k_cols(Ps[0], kPitchP, 32 * half + 16 * t, 32 * kp, lane), OV[t]);
       }
-      const u32x4 qf = frag_k_rows_accpair(Qs, kPitchK, 32 * kp, 16 * kb0, lane);
+      const u32x4 qf = frag_k_rows_shifted(Qs, kPitchK, 32 * kp, 16 * kb0, lane);
 #pragma unroll
       for (int t = 0; t < kDkTok; ++t)
         if (kp <= (tb0 + t) / 2) OK[t] = mfma16x16x32(qf, frag_k_cols(Ps[1], kPitchP, 16 * (tb0 + t), 32 * kp, lane), OK[t]);
@@ -247,7 +245,7 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
       R[b] *= keep;
 #pragma unroll
       for (int kp = 0; kp < 2; ++kp) {
-        const u32x4 qf = frag_k_rows_accpair(Qs, kPitchK, 32 * kp, 16 * (KB * half + b), lane);
+        const u32x4 qf = frag_k_rows_shifted(Qs, kPitchK, 32 * kp, 16 * (KB * half + b), lane);
 #pragma unroll
         for (int t = 0; t < TERMS; ++t) R[b] = mfma16x16x32(qf, part[kp][t], R[b]);
       }

@@ -152,7 +152,7 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
       const int i = threadIdx.x + kThreads * j;
       const int row = i / (4 * KB), col = i % (4 * KB);
       if (kThreads <= 256 * KB || i < 256 * KB) {
-        *reinterpret_cast<u32x4*>(Ks + row * kPitchK + 8 * col) = kn[j];
+        *reinterpret_cast<u32x4*>(Ks + row * kPitchK + row_shift(row) + 8 * col) = kn[j];
         if (!STATE_ONLY) store_paired(Qs + row * kPitchK, col >> 2, col & 3, qn[j]);
       }
     }
@@ -172,9 +172,9 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
         f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
-          const u32x4 q = frag_k_cols_unpaired(Qs, kPitchK, 16 * qb, 32 * j, lane);
-          s0 = mfma16x16x32(frag_k_cols(Ks, kPitchK, 32 * kp, 32 * j, lane), q, s0);
-          s1 = mfma16x16x32(frag_k_cols(Ks, kPitchK, 32 * kp + 16, 32 * j, lane), q, s1);
+          const u32x4 q = frag_k_cols(Qs, kPitchK, 16 * qb, 32 * j, lane);
+          s0 = mfma16x16x32(frag_k_cols_pairs(Ks, kPitchK, 32 * kp, 32 * j, lane), q, s0);
+          s1 = mfma16x16x32(frag_k_cols_pairs(Ks, kPitchK, 32 * kp + 16, 32 * j, lane), q, s1);
         }
         // Query minus key, of the first key (r = 0); weighted, or 0 (selected: a later key may hold anything).
         const int diff = 16 * qb - 32 * kp + c16 - 4 * g;
@@ -270,7 +270,7 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
       }
 #pragma unroll
       for (int kp = 0; kp < 2; ++kp) {
-        const u32x4 kf = frag_k_rows_accpair(Ks, kPitchK, 32 * kp, 16 * b, lane);
+        const u32x4 kf = frag_k_rows_shifted(Ks, kPitchK, 32 * kp, 16 * b, lane);
 #pragma unroll
         for (int t = 0; t < TERMS; ++t)
 #pragma unroll
