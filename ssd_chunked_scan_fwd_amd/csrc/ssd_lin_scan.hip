@@ -31,11 +31,11 @@ namespace ssd {
 
 namespace {
 
-// KB: dk in units of 32. W waves of CB blocks of 16 value columns. TERMS: bf16
-// terms of the weighted V in the state product.
-template <int KB, int W, int CB, int TERMS, bool STATE_ONLY>
+// KB: dk in units of 32. W waves of 16 value columns. TERMS: bf16 terms of the
+// weighted V in the state product.
+template <int KB, int W, int TERMS, bool STATE_ONLY>
 __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks) {
-  constexpr int kDk = 32 * KB, kDv = 16 * W * CB, kThreads = 64 * W;
+  constexpr int kDk = 32 * KB, kDv = 16 * W, kThreads = 64 * W;
   constexpr int kPitchK = lds_pitch(kDk), kPitchV = lds_pitch(kDv);
   __shared__ __align__(16) uint16_t Ks[kC * kPitchK];
   __shared__ __align__(16) uint16_t Vs[kC * kPitchV];
@@ -43,7 +43,7 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
   __shared__ __align__(16) uint16_t Ps[STATE_ONLY ? 8 : kC * kPitchP];
   __shared__ __align__(16) float pw[kPowSize], spw[STATE_ONLY ? 4 : kPowSize];   // powers of lam, and scale times them
   constexpr int kQK = (256 * KB + kThreads - 1) / kThreads;   // 16-byte pieces a thread stages of q and of k,
-  constexpr int kV = 2 * CB;                                  // and of v
+  constexpr int kV = 2;                                       // and of v
 
   const int tiles = (a.dv + kDv - 1) / kDv;
   const long u = xcd_unit(bid, blocks);
@@ -59,31 +59,26 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
   const long mat = (long)a.dv * a.dk;
 
-  // The state: block b of column block cb holds D[dv][dk] at dv = dv0 + 16 (CB wave + cb) + c16, dk = 16 b + 4 g + r.
-  f32x4 S[CB][2 * KB];
+  // The state: block b holds D[dvc][dk] at dk = 16 b + 4 g + r.
+  const int dvc = dv0 + 16 * wave + c16;
+  f32x4 S[2 * KB];
 #pragma unroll
-  for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-    for (int b = 0; b < 2 * KB; ++b) S[cb][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int b = 0; b < 2 * KB; ++b) S[b] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (!STATE_ONLY) {
     const float* src = p.blk > 0 ? a.states + (slot * a.H + h) * mat : a.init;
     if (p.blk == 0 && src) src += ((long)p.seq * a.H + h) * mat;
     const bool tr = p.blk == 0 && a.init_tr;
     const float sc = p.blk == 0 ? a.init_scale : 1.f;
-    if (src) {
+    if (src && dvc < a.dv) {
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-        const int dv = dv0 + 16 * (CB * wave + cb) + c16;
+      for (int b = 0; b < 2 * KB; ++b) {
+        const int dk = 16 * b + 4 * g;
+        if (dk >= a.dk) continue;
+        if (tr) {
 #pragma unroll
-        for (int b = 0; b < 2 * KB; ++b) {
-          const int dk = 16 * b + 4 * g;
-          if (dk >= a.dk || dv >= a.dv) continue;
-          if (tr) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[cb][b][r] = sc * src[(long)(dk + r) * a.dv + dv];
-          } else {
-            S[cb][b] = *reinterpret_cast<const f32x4*>(src + (long)dv * a.dk + dk) * sc;
-          }
+          for (int r = 0; r < 4; ++r) S[b][r] = sc * src[(long)(dk + r) * a.dv + dvc];
+        } else {
+          S[b] = *reinterpret_cast<const f32x4*>(src + (long)dvc * a.dk + dk) * sc;
         }
       }
     }
@@ -130,11 +125,8 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
     for (int j = 0; j < kV; ++j) vn[j] = buf_load16(rv, piece_offset(vp[j], n, vrow, a.rev));
   };
 
-  // This lane's pieces of O at token c16; those of the other token blocks lie 16 rows on.
-  Piece o0[CB];
-#pragma unroll
-  for (int cb = 0; cb < CB; ++cb)
-    o0[cb] = make_piece(c16, dv0 + 16 * (CB * wave + cb) + 4 * g, a.dv, a.H * a.dv * (a.o_f32 ? 4 : 2), a.o_f32 ? 4 : 2, a.rev);
+  // This lane's piece of O at token c16; those of the other token blocks lie 16 rows on.
+  const Piece o0 = make_piece(c16, dv0 + 16 * wave + 4 * g, a.dv, a.H * a.dv * (a.o_f32 ? 4 : 2), a.o_f32 ? 4 : 2, a.rev);
 
   // The blocks' own sums walk their chunks backwards, weighting each V by its whole
   // distance to the block's end: the scan, which walks forwards and comes next,
@@ -189,66 +181,45 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
       }
     }
 
-    u32x4 vf[CB][2];
+    u32x4 vf[2];
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-      for (int kp = 0; kp < 2; ++kp) vf[cb][kp] = frag_k_rows_accpair(Vs, kPitchV, 32 * kp, 16 * (CB * wave + cb), lane);
+    for (int kp = 0; kp < 2; ++kp) vf[kp] = frag_k_rows_accpair(Vs, kPitchV, 32 * kp, 16 * wave, lane);
 
     if (!STATE_ONLY) {
-      f32x4 O[4][CB];
+      f32x4 O[4];
 #pragma unroll
-      for (int qb = 0; qb < 4; ++qb)
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) O[qb][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int qb = 0; qb < 4; ++qb) O[qb] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < KB; ++j) {
-        u32x4 sf[CB];
+        const f32x4 x = S[2 * j], y = S[2 * j + 1];
+        const u32x4 sf = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-          const f32x4 x = S[cb][2 * j], y = S[cb][2 * j + 1];
-          sf[cb] = u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
-        }
-#pragma unroll
-        for (int qb = 0; qb < 4; ++qb) {
-          const u32x4 qf = frag_k_cols(Qs, kPitchK, 16 * qb, 32 * j, lane);
-#pragma unroll
-          for (int cb = 0; cb < CB; ++cb) O[qb][cb] = mfma16x16x32(sf[cb], qf, O[qb][cb]);
-        }
+        for (int qb = 0; qb < 4; ++qb) O[qb] = mfma16x16x32(sf, frag_k_cols(Qs, kPitchK, 16 * qb, 32 * j, lane), O[qb]);
       }
 #pragma unroll
-      for (int qb = 0; qb < 4; ++qb) {
-        const float w = spw[kPowZero + 16 * qb + c16 + lead];
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) O[qb][cb] *= w;
-      }
+      for (int qb = 0; qb < 4; ++qb) O[qb] *= spw[kPowZero + 16 * qb + c16 + lead];
       __syncthreads();
 #pragma unroll
       for (int qb = 0; qb < 4; ++qb)
 #pragma unroll
-        for (int kp = 0; kp <= qb / 2; ++kp) {
-          const u32x4 pf = frag_k_cols(Ps, kPitchP, 16 * qb, 32 * kp, lane);
-#pragma unroll
-          for (int cb = 0; cb < CB; ++cb) O[qb][cb] = mfma16x16x32(vf[cb][kp], pf, O[qb][cb]);
-        }
+        for (int kp = 0; kp <= qb / 2; ++kp)
+          O[qb] = mfma16x16x32(vf[kp], frag_k_cols(Ps, kPitchP, 16 * qb, 32 * kp, lane), O[qb]);
       // O^T: column c16 is the query, rows 4 g + r the value columns.
       const long low = p.start + (a.rev ? (long)p.len - (pos0 + t0) - n : (long)pos0 + t0);
       const int esz = a.o_f32 ? 4 : 2, orow = a.H * a.dv * esz;
       const rsrc_t ro = make_rsrc(static_cast<char*>(a.o) + low * orow + (long)h * a.dv * esz, (uint32_t)(n * orow));
 #pragma unroll
-      for (int qb = 0; qb < 4; ++qb)
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-          const Piece at = {o0[cb].full + (uint32_t)((a.rev ? -16 : 16) * qb * orow), o0[cb].row + 16 * qb};
-          const uint32_t off = piece_offset(at, n, orow, a.rev);
-          const f32x4 o = O[qb][cb];
-          if (a.o_f32) buf_store16(__builtin_bit_cast(u32x4, o), ro, off);
-          else buf_store8(u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])}, ro, off);
-        }
+      for (int qb = 0; qb < 4; ++qb) {
+        const Piece at = {o0.full + (uint32_t)((a.rev ? -16 : 16) * qb * orow), o0.row + 16 * qb};
+        const uint32_t off = piece_offset(at, n, orow, a.rev);
+        const f32x4 o = O[qb];
+        if (a.o_f32) buf_store16(__builtin_bit_cast(u32x4, o), ro, off);
+        else buf_store8(u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])}, ro, off);
+      }
     }
 
     // State: decay by the chunk, add K^T (weighted V). Token of slot s of pair kp: 32 kp + 16 (s / 4) + 4 g + s % 4.
-    u32x4 part[CB][2][TERMS];
+    u32x4 part[2][TERMS];
 #pragma unroll
     for (int kp = 0; kp < 2; ++kp) {
       float w[8];
@@ -257,24 +228,18 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
 #pragma unroll
         for (int s = 0; s < 8; ++s) w[s] *= behind;
       }
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb) split_weighted<TERMS>(vf[cb][kp], w, part[cb][kp]);
+      split_weighted<TERMS>(vf[kp], w, part[kp]);
     }
     behind *= pw[kPowZero + n];
     const float keep = pw[kPowZero + n - 1 + lead];
 #pragma unroll
     for (int b = 0; b < 2 * KB; ++b) {
-      if (!STATE_ONLY) {
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) S[cb][b] *= keep;
-      }
+      if (!STATE_ONLY) S[b] *= keep;
 #pragma unroll
       for (int kp = 0; kp < 2; ++kp) {
         const u32x4 kf = frag_k_rows_shifted(Ks, kPitchK, 32 * kp, 16 * b, lane);
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t)
-#pragma unroll
-          for (int cb = 0; cb < CB; ++cb) S[cb][b] = mfma16x16x32(kf, part[cb][kp][t], S[cb][b]);
+        for (int t = 0; t < TERMS; ++t) S[b] = mfma16x16x32(kf, part[kp][t], S[b]);
       }
     }
   }
@@ -287,29 +252,25 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
     dst = a.fin + ((long)p.seq * a.H + h) * mat;
     sc = a.fin_scale * (a.rev && p.len > 0 ? pw[kPowZero + 1] : 1.f);
   }
-  if (dst) {
+  if (dst && dvc < a.dv) {
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb) {
-      const int dv = dv0 + 16 * (CB * wave + cb) + c16;
-#pragma unroll
-      for (int b = 0; b < 2 * KB; ++b) {
-        const int dk = 16 * b + 4 * g;
-        if (dv < a.dv && dk < a.dk) *reinterpret_cast<f32x4*>(dst + (long)dv * a.dk + dk) = S[cb][b] * sc;
-      }
+    for (int b = 0; b < 2 * KB; ++b) {
+      const int dk = 16 * b + 4 * g;
+      if (dk < a.dk) *reinterpret_cast<f32x4*>(dst + (long)dvc * a.dk + dk) = S[b] * sc;
     }
   }
 }
 
-template <int KB, int W, int CB, int TERMS>
+template <int KB, int W, int TERMS>
 __global__ __launch_bounds__(64 * W, KB <= 4 ? W / 2 : W / 4) void lin_mfma_kernel(LinScan a) {
-  lin_mfma<KB, W, CB, TERMS, false>(a, blockIdx.x, gridDim.x);
+  lin_mfma<KB, W, TERMS, false>(a, blockIdx.x, gridDim.x);
 }
 
 // The blocks' own sums of one scan, or of two: the first `na` workgroups are a's.
-template <int KB, int W, int CB, int TERMS>
+template <int KB, int W, int TERMS>
 __global__ __launch_bounds__(64 * W, KB <= 4 ? W / 2 : W / 4) void lin_mfma_states_kernel(LinScan a, LinScan b, long na) {
-  if ((long)blockIdx.x < na) lin_mfma<KB, W, CB, TERMS, true>(a, blockIdx.x, na);
-  else lin_mfma<KB, W, CB, TERMS, true>(b, blockIdx.x - na, gridDim.x - na);
+  if ((long)blockIdx.x < na) lin_mfma<KB, W, TERMS, true>(a, blockIdx.x, na);
+  else lin_mfma<KB, W, TERMS, true>(b, blockIdx.x - na, gridDim.x - na);
 }
 
 long mfma_blocks(const LinScan& a) {
@@ -355,7 +316,7 @@ int lin_mfma_target(int dk, int dv) {
 hipError_t launch_lin_mfma(const LinScan& a, hipStream_t stream) {
   mfma_instance(a.dk, a.dv, a.fine(), [&](auto kb, auto w, auto terms) {
     constexpr int KB = decltype(kb)::value, W = decltype(w)::value, TERMS = decltype(terms)::value;
-    hipLaunchKernelGGL((lin_mfma_kernel<KB, W, 1, TERMS>), dim3((unsigned)mfma_blocks(a)), dim3(64 * W), 0, stream, a);
+    hipLaunchKernelGGL((lin_mfma_kernel<KB, W, TERMS>), dim3((unsigned)mfma_blocks(a)), dim3(64 * W), 0, stream, a);
   });
   return hipGetLastError();
 }
@@ -368,7 +329,7 @@ hipError_t launch_lin_mfma_states(const LinScan& a, const LinScan* b, hipStream_
   mfma_instance(a.dk, a.dv, a.fine() || (b && b->fine()), [&](auto kb, auto w, auto terms) {
     constexpr int KB = decltype(kb)::value, W = decltype(w)::value, TERMS = decltype(terms)::value;
     const long na = mfma_blocks(a), all = na + (b ? mfma_blocks(*b) : 0);
-    hipLaunchKernelGGL((lin_mfma_states_kernel<KB, W, 1, TERMS>), dim3((unsigned)all), dim3(64 * W), 0, stream, a, b ? *b : a, na);
+    hipLaunchKernelGGL((lin_mfma_states_kernel<KB, W, TERMS>), dim3((unsigned)all), dim3(64 * W), 0, stream, a, b ? *b : a, na);
   });
   return hipGetLastError();
 }
