@@ -122,7 +122,7 @@ __device__ __forceinline__ LinPiece lin_piece(const LinScan& a, long slot) {
     p.start = (long)p.seq * a.T;
     return p;
   }
-  // Slots of sequence s begin at floor(cu[s] / L) + s, which grows with s: count those at or before `slot`.
+  // Slots of sequence s begin at floor(cu[s] / L) + s, which grows with s: count those at or before `slot`,
   // halving the range down to a wave's width, the rest with one load a lane.
   const int lane = (int)threadIdx.x & 63;
   auto begins = [&](int i) { return (long)min(max(a.cu[i], 0), a.T) / a.L + i; };
@@ -156,11 +156,15 @@ __device__ __forceinline__ double lin_power(float log_decay, int e) {
   return exp((double)(log_decay < -11356.f ? -11356.f : log_decay) * (double)e);
 }
 
-// log2 of the decay; a log decay of -inf becomes a finite value whose first
-// power already underflows to 0, while its power 0 stays 1.
-__device__ __forceinline__ float lin_log2_decay(const float* ld, int h) {
-  const float g = ld[h] * 1.4426950408889634f;
-  return g < -16384.f ? -16384.f : g;
+// lam as a sum of two floats: rounded to one, the same error would enter with
+// every token and compound.
+struct LinDecay {
+  float hi, lo;
+};
+__device__ __forceinline__ LinDecay lin_decay(float log_decay) {
+  const double lam = lin_power(log_decay, 1);
+  const float hi = (float)lam;
+  return LinDecay{hi, (float)(lam - (double)hi)};
 }
 
 #endif

@@ -33,8 +33,7 @@ __device__ __forceinline__ float load_el(const void* p, long i) {
 // 16 rows of the state of one (block, head): 16 lanes a row, 4 NQ columns a lane,
 // all in registers; the next 16 tokens are in flight while 16 are taken from LDS.
 // Bound by its own arithmetic: 2 multiply-adds a state element for the decay
-// (lam as a sum of two floats, so that its rounding does not compound over the
-// block), one for the product and one for the output.
+// (LinDecay), one for the product and one for the output.
 // STATE_ONLY leaves each block's own sum (from a zero state) in a.states;
 // the other form starts from the block's entering state and writes o.
 // ----------------------------------------------------------------------------
@@ -58,8 +57,7 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
   if (STATE_ONLY && last) return;  // the scan carries the last block's state itself
   const int r = threadIdx.x >> 4, c = threadIdx.x & 15;
   const int row = row0 + r;
-  const double lam = lin_power(a.ld[h], 1);
-  const float lam_hi = (float)lam, lam_lo = (float)(lam - (double)lam_hi);
+  const LinDecay lam = lin_decay(a.ld[h]);
 
   f32x4 s[NQ];  // columns 64 m + 4 c + 0..3
 #pragma unroll
@@ -120,7 +118,7 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
     if (t0 + kRecTok < n) load(t0 + kRecTok);
     auto step = [&](int t) {
       const bool keep = a.rev && pos0 + t0 + t == 0;  // the state handed to a reversed scan is not decayed first
-      const float hi = keep ? 1.f : lam_hi, lo = keep ? 0.f : lam_lo;
+      const float hi = keep ? 1.f : lam.hi, lo = keep ? 0.f : lam.lo;
       const float v = vs[t][r];
       float part = 0.f;
 #pragma unroll
@@ -153,7 +151,7 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
     dst = a.states + (slot * a.H + h) * mat;
   } else if (last && a.fin) {
     dst = a.fin + ((long)p.seq * a.H + h) * mat;
-    sc = a.fin_scale * (a.rev && p.len > 0 ? lam_hi : 1.f);
+    sc = a.fin_scale * (a.rev && p.len > 0 ? lam.hi : 1.f);
   }
   if (dst && row < a.dv) {
 #pragma unroll
@@ -333,7 +331,7 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStep a, int tpr, int p
 #pragma unroll
   for (int j = 0; j < ROWS; ++j)
     s[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(st + (long)min(r0 + j * rpp, a.dv - 1) * a.dk));
-  const float lam = fast_exp2(lin_log2_decay(a.ld, h));
+  const LinDecay lam = lin_decay(a.ld[h]);
   int next = a.batch;
   if (a.slots && step_peers(a, e, slot, lane, next)) return;  // an earlier entry's workgroup runs this one
   for (;;) {
@@ -351,7 +349,7 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStep a, int tpr, int p
       float acc = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[j][i] = fmaf(s[j][i], lam, v[j] * k[i]);
+        s[j][i] = fmaf(s[j][i], lam.hi, fmaf(s[j][i], lam.lo, v[j] * k[i]));
         acc = fmaf(s[j][i], q[i], acc);
       }
       if (next == a.batch && col_in && r < a.dv)

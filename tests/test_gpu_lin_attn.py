@@ -345,6 +345,39 @@ def test_step_many_repeats():
     assert torch.all(pool[0] == 0)
 
 
+def test_step_decay_does_not_drift():
+    """65536 steps that only decay a state: the decay's own rounding to 32 bits must not enter with every step.
+
+    Of the log decays near -1e-5 the one whose decay is furthest from an fp32 value is taken: rounded once to 32
+    bits it would be off by 65536 times that, 1.9e-3 of the state.
+
+    What is left is the rounding of the state, and it has a sign. With c = 1 - lam, a state of n units in the last
+    place loses d = c n units a step, rounded to a whole m; d itself falls by delta = c m a step. While m stands,
+    d runs from m + 1/2 to m - 1/2 and the errors m - d cancel but for half a unit; a run cut short, at either end
+    or where n passes a power of two, leaves at most 1 / (8 delta) units. Here c >= 1e-5 and n >= 2^23, so m >= 83
+    and 1 / (8 delta) <= 151 units of at most 2^-23 of the state: 1.8e-5. A state of 0.5 to 1.5 that falls by
+    half passes at most two powers of two: six runs cut short, 1.1e-4, and 100 whole ones a power of two, three
+    times 50 units of 2^-23, 1.8e-5.
+    """
+    cand = torch.arange(200, dtype=torch.float32) * -1e-8 - 1e-5
+    lam = torch.exp(cand.double())
+    off = (lam.float().double() - lam).abs()
+    ld = cand[off.argmax()]
+    assert off.max() * 65536 > 1e-3
+    b, dk, dv = 2048, 32, 256
+    pool = torch.rand(1, 1, dv, dk, generator=torch.Generator().manual_seed(8)).cuda() + 0.5
+    first = pool.double()
+    zero = torch.zeros(b, 1, dk, device="cuda")
+    v = torch.ones(b, 1, dv, device="cuda")
+    sl = torch.zeros(b, dtype=torch.int32, device="cuda")
+    for _ in range(32):
+        ssd.lin_attn_step(pool, zero, zero, v, ld.cuda()[None], slots=sl)
+    left = torch.exp(ld.double() * 65536).item()
+    drift = (pool.double() / (first * left) - 1).abs().max().item()
+    say(f"[lin step] drift {drift:.2e}")
+    assert drift < 1.3e-4
+
+
 def test_other_stream_and_two_calls_at_once():
     d = make(1, 500, 4, 4, 64, 64, BF, 51)
     e = make(1, 700, 4, 4, 64, 64, BF, 52)
