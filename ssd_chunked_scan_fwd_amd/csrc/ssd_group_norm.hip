@@ -868,6 +868,16 @@ void by_type(bool bf16, bool vec, F f) {
 
 }  // namespace
 
+bool norm_launchable(const NormArgs& a) {
+  RowPlan p;
+  if (row_plan(a, &p)) {
+    const long workers = p.lanes > 64 ? 1 : kThreads / p.lanes;
+    return launchable((a.n * a.G + workers - 1) / workers, p.threads);
+  }
+  const Slabs b = slabs_of(a.s, a.C, a.vec ? 8 : 1);
+  return launchable(a.n * b.count * b.tiles, kThreads) && launchable(a.n * a.G, kThreads);
+}
+
 hipError_t launch_group_norm(const NormArgs& a, hipStream_t stream) {
   RowPlan p;
   const bool row = row_plan(a, &p);

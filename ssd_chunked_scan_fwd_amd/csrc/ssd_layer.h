@@ -28,6 +28,7 @@ struct NormArgs {
 // Floats of workspace of a forward and of a backward call (an upper bound over
 // alignments).
 size_t norm_ws_floats(long n, long s, int C, int G, bool backward);
+bool norm_launchable(const NormArgs& a);
 hipError_t launch_group_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_group_norm_bwd(const NormArgs& a, hipStream_t stream);
 
@@ -36,6 +37,10 @@ struct PagesArgs {
   int layers = 0, slots = 0;
   long page = 0;
 };
+// Whether the runtime, which counts the threads of a grid's dimension in 32
+// bits, takes that many workgroups.
+inline bool launchable(long workgroups, int threads) { return workgroups <= (long)(UINT32_MAX / (unsigned)threads); }
+
 constexpr int kMaxPagePairs = 1024;
 hipError_t launch_pages_copy(const PagesArgs& a, const int32_t* src, const int32_t* dst, int n, hipStream_t stream);
 hipError_t launch_pages_clear(const PagesArgs& a, const int32_t* slots, int n, hipStream_t stream);

@@ -68,11 +68,13 @@ struct LinPlan {
   int64_t spr, slots;
   size_t state_bytes;  // 0: no sequence is cut
 };
-ssd_status lin_plan(const ssd_lin_shape* s, int dk, int dv, LinPlan* p, bool kv = false) {
+// `scans` of them may share a launch.
+ssd_status lin_plan(const ssd_lin_shape* s, int dk, int dv, LinPlan* p, int scans = 1, bool kv = false) {
   p->L = ssd::lin_block_tokens(s->batch, s->seqlen, s->num_seqs, s->nheads, dk, dv, s->dtype == SSD_DTYPE_BF16, kv);
   p->spr = ssd::lin_slots_per_row(s->seqlen, s->num_seqs, p->L);
   p->slots = s->num_seqs > 0 ? p->spr : p->spr * s->batch;
-  if (p->slots * s->nheads > INT32_MAX / 64) return SSD_ERR_UNSUPPORTED;  // workgroups of one launch
+  if (!ssd::launchable(p->slots * s->nheads * scans, ssd::lin_slot_threads(dv, s->dtype == SSD_DTYPE_BF16, kv)))
+    return SSD_ERR_UNSUPPORTED;
   p->state_bytes = p->L >= s->seqlen ? 0 : (size_t)p->slots * s->nheads * dk * dv * 4;
   return SSD_OK;
 }
@@ -86,9 +88,9 @@ ssd_status lin_bwd_layout(const ssd_lin_shape* s, LinBwdLayout* L) {
   LinDims d;
   ssd_status st = check_lin(s, &d);
   if (st != SSD_OK) return st;
-  if ((st = lin_plan(s, s->dv, s->dk, &L->dq)) != SSD_OK) return st;
+  if ((st = lin_plan(s, s->dv, s->dk, &L->dq, 2)) != SSD_OK) return st;
   L->kv = ssd::lin_kv_supported(s->dk, s->dv, s->dtype == SSD_DTYPE_BF16);
-  if ((st = lin_plan(s, s->dk, s->dv, &L->dv, L->kv)) != SSD_OK) return st;
+  if ((st = lin_plan(s, s->dk, s->dv, &L->dv, 2, L->kv)) != SSD_OK) return st;
   L->dk = LinPlan{};
   if (!L->kv && (st = lin_plan(s, s->dv, s->dk, &L->dk)) != SSD_OK) return st;
   size_t off = 0;
@@ -101,6 +103,8 @@ ssd_status lin_bwd_layout(const ssd_lin_shape* s, LinBwdLayout* L) {
   L->st_dv = take(L->dv.state_bytes);
   L->st_dk = take(L->dk.state_bytes);
   const bool shared = s->nheads != s->nkv_heads;
+  const int64_t pieces = (s->dk > s->dv ? s->dk : s->dv) / 8;   // a thread's share of the sums over shared heads
+  if (shared && !ssd::launchable(d.tokens * s->nkv_heads * pieces / 256 + 1, 256)) return SSD_ERR_UNSUPPORTED;
   L->part_k = take(shared ? (size_t)d.tokens * s->nheads * s->dk * 4 : 0);
   L->part_v = take(shared ? (size_t)d.tokens * s->nheads * s->dv * 4 : 0);
   L->total = off;
@@ -144,7 +148,7 @@ ssd_status check_norm(const ssd_norm_shape* s) {
   if (s->act != SSD_ACT_NONE && s->act != SSD_ACT_SILU) return SSD_ERR_UNSUPPORTED;
   if (s->gate != SSD_GATE_NONE && s->gate != SSD_GATE_AFTER && s->gate != SSD_GATE_BEFORE) return SSD_ERR_UNSUPPORTED;
   if (s->center != 0 && s->center != 1) return SSD_ERR_INVALID_ARGUMENT;
-  // rows, and workgroups of a launch (at most one per eight rows and channel tile, or per row and group)
+  // rows, and what of a launch is counted in 32 bits by the kernels (its threads: norm_launchable)
   const int64_t rows = (int64_t)s->samples * s->positions;
   if (rows > INT32_MAX / 4 || rows * s->groups > INT32_MAX / 4) return SSD_ERR_UNSUPPORTED;
   if (rows * ((s->channels + 63) / 64) > INT32_MAX) return SSD_ERR_UNSUPPORTED;
@@ -383,6 +387,7 @@ ssd_status ssd_group_norm(const void* x, const void* z, const float* weight, con
   a.y = y;
   a.stats = stats;
   if ((st = norm_align(&a)) != SSD_OK) return st;
+  if (!ssd::norm_launchable(a)) return SSD_ERR_UNSUPPORTED;
   size_t need = 0;
   ssd_group_norm_workspace_bytes(shape, 0, &need);
   if ((st = check_ws(workspace, workspace_bytes, need)) != SSD_OK) return st;
@@ -409,6 +414,7 @@ ssd_status ssd_group_norm_bwd(const void* x, const void* z, const float* weight,
   a.dw = dweight;
   a.db = dbias;
   if ((st = norm_align(&a)) != SSD_OK) return st;
+  if (!ssd::norm_launchable(a)) return SSD_ERR_UNSUPPORTED;
   size_t need = 0;
   ssd_group_norm_workspace_bytes(shape, 1, &need);
   if ((st = check_ws(workspace, workspace_bytes, need)) != SSD_OK) return st;

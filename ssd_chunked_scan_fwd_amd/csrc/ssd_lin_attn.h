@@ -55,6 +55,8 @@ struct LinScan {
 // Tokens a block for a scan of these sizes (kv: the scan of launch_lin_kv); a
 // value >= T means that no sequence is cut and no block states are needed.
 int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16, bool kv = false);
+// Threads of a launch for one block of one head.
+int lin_slot_threads(int dv, int bf16, bool kv);
 inline long lin_slots_per_row(int T, int S, int L) { return S > 0 ? (long)(T / L) + S : (T + (long)L - 1) / L; }
 
 hipError_t launch_lin_scan(const LinScan& a, hipStream_t stream);
@@ -75,6 +77,7 @@ hipError_t launch_lin_mfma_states(const LinScan& a, const LinScan* b, hipStream_
 // takes besides.
 bool lin_kv_supported(int dk, int dv, int bf16);
 int lin_kv_target(int dk, int dv);
+int lin_kv_threads(int dv);   // of a workgroup
 hipError_t launch_lin_kv(const LinScan& a, const LinOperand& v, void* dk_out, hipStream_t stream);
 
 // out[token][key head][i] = sum of in over the query heads that share it, in

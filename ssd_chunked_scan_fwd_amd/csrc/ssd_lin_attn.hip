@@ -400,6 +400,12 @@ int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16, b
   return (int)(best * kC64);
 }
 
+int lin_slot_threads(int dv, int bf16, bool kv) {
+  if (kv) return lin_kv_threads(dv);
+  const int tile = bf16 ? lin_mfma_tile(dv) : kRecRows;
+  return (bf16 ? 4 * tile : 256) * ((dv + tile - 1) / tile);
+}
+
 namespace {
 template <bool STATE_ONLY>
 void launch_rec(const LinScan& a, hipStream_t stream) {

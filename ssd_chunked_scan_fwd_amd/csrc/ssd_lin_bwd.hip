@@ -269,6 +269,7 @@ bool lin_kv_supported(int dk, int dv, int bf16) { return bf16 && dk <= 128 && dv
 
 // Workgroups that run at once: one of sixteen waves a CU, or two of eight where LDS holds them.
 int lin_kv_target(int dk, int dv) { return dv <= 64 && dk <= 64 ? 512 : 256; }
+int lin_kv_threads(int dv) { return dv <= 64 ? 512 : 1024; }
 
 namespace {
 template <int KB, int VB>

@@ -37,6 +37,15 @@ def test_lin_shapes(kw, code):
     assert lin_bytes(lin(**kw), True)[0] == code
 
 
+@pytest.mark.parametrize("kw,heads", [(dict(dk=8, dv=8), 255), (dict(dk=8, dv=256), 63), (dict(dk=8, dv=64, dtype=0), 63)])
+def test_lin_launch_limit(kw, heads):
+    """More one-token sequences and heads than a grid has threads for (2^32) are refused, not half launched."""
+    many = dict(batch=1, seqlen=65535, num_seqs=65535, **kw)
+    assert lin_bytes(lin(nheads=heads, nkv_heads=heads, **many))[0] == OK
+    assert lin_bytes(lin(nheads=heads + 2, nkv_heads=heads + 2, **many))[0] == UNSUPPORTED
+    assert lin_bytes(lin(nheads=heads + 2, nkv_heads=heads + 2, **many), True)[0] == UNSUPPORTED
+
+
 def test_lin_fwd_validates():
     L, sh = ssd.lib(), lin(batch=1, nheads=2)
     st, need = lin_bytes(sh)
@@ -138,6 +147,20 @@ def test_norm_validates():
         a = list(args)
         a[i] = bad
         assert L.ssd_group_norm_bwd(*a) == INVALID, (i, bad)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(samples=1 << 21, positions=1, channels=4100, groups=1),     # single channels, in slabs
+    dict(samples=1 << 22, positions=1, channels=2046, groups=1),     # single channels, a row a workgroup
+    dict(samples=1 << 24, positions=1, channels=2048, groups=8),     # a group in half a wave
+    dict(samples=1 << 25, positions=2, channels=8, groups=1)])       # a workgroup a sample
+def test_norm_launch_limit(kw):
+    """More rows and channels than a grid has threads for (2^32) are refused."""
+    L, sh = ssd.lib(), norm(**kw)
+    huge = 1 << 62
+    assert L.ssd_group_norm(FAKE, None, None, None, 1e-5, FAKE, None, ctypes.byref(sh), FAKE, huge, None) == UNSUPPORTED
+    assert L.ssd_group_norm_bwd(FAKE, None, None, None, FAKE, FAKE, FAKE, None, None, None, ctypes.byref(sh), FAKE, huge,
+                                None) == UNSUPPORTED
 
 
 def pages(**kw):
