@@ -635,6 +635,13 @@ def _check_dtype(t, name: str, dim: str, dims: int):
         raise ValueError(f"{name} has dtype {t.dtype}; bfloat16 and float32 are supported")
 
 
+def _int32(sizes: dict):
+    """The sizes that the C ABI takes in 32 bits (ctypes would cut them off)."""
+    for name, n in sizes.items():
+        if n > 0x7FFFFFFF:
+            raise ValueError(f"{name} {n} does not fit 32 bits")
+
+
 def _token_row(t: torch.Tensor, name: str) -> int:
     """Elements from token to token of [batch, seqlen, heads, d]: heads and their
     elements lie together, tokens at one distance, rows of the batch follow on."""
@@ -685,6 +692,7 @@ def _lin_shape(q, k, v, log_decay, cu_seqlens):
         if b != 1:
             raise ValueError("packed sequences (cu_seqlens) need batch 1")
         S = cu_seqlens.numel() - 1
+    _int32(dict(batch=b, seqlen=T, nheads=H, dk=Dk, dv=v.shape[3], num_seqs=S))
     return LinShape(b, T, H, Hk, Dk, v.shape[3], S, _dtype_code(q.dtype), _token_row(q, "q"), _token_row(k, "k"),
                     _token_row(v, "v"))
 
@@ -835,6 +843,7 @@ def lin_attn_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     if log_decay is None:
         raise ValueError("log_decay is required")
     n = state.shape[0]
+    _int32(dict(batch=b, nheads=H, dk=Dk, dv=Dv, num_slots=n))
     if slots is None and n < b:
         raise ValueError(f"state has {n} slots for {b} entries")
     _structure([(q, "q", None, q.dtype), (k, "k", None, q.dtype), (v, "v", None, q.dtype),
@@ -897,6 +906,7 @@ def _norm_shape(x, groups, z, act, gate, center) -> NormShape:
     positions = 1
     for d in x.shape[1:-1]:
         positions *= d
+    _int32(dict(samples=x.shape[0], positions=positions, channels=C))
     return NormShape(x.shape[0], positions, C, int(groups), _row_pitch(x, "x"), 0 if z is None else _row_pitch(z, "z"),
                      _dtype_code(x.dtype), _ACTS[act], 0 if z is None else _GATES[gate], 1 if center else 0)
 
@@ -978,6 +988,7 @@ def _pages_shape(pool) -> PagesShape:
         raise ValueError("pool must be contiguous")
     if pool.numel() == 0:
         raise ValueError("pool is empty")
+    _int32(dict(layers=pool.shape[0], slots=pool.shape[1]))
     return PagesShape(pool.shape[0], pool.shape[1], pool.numel() // (pool.shape[0] * pool.shape[1]) * pool.element_size())
 
 
@@ -992,6 +1003,7 @@ def pages_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor) -> torc
     _structure([(src, "src", None, torch.int32), (dst, "dst", src.shape, torch.int32)])
     if dst is None:
         raise ValueError("dst is required")
+    _int32(dict(pairs=src.numel()))
     _expect_device([(pool, "pool")], pool.device, 1)
     _expect_device([(src, "src"), (dst, "dst")], pool.device, 4)
     if src.numel():
@@ -1005,6 +1017,7 @@ def pages_clear(pool: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a 1-d tensor")
     _structure([(slots, "slots", None, torch.int32)])
+    _int32({"number of slots": slots.numel()})
     _expect_device([(pool, "pool")], pool.device, 1)
     _expect_device([(slots, "slots")], pool.device, 4)
     if slots.numel():

@@ -267,3 +267,21 @@ def test_pages_binding():
     _refused("live", ssd.pages_compact, p, torch.zeros(5, dtype=torch.uint8))
     _refused("live", ssd.pages_compact, p, torch.zeros(4, dtype=torch.int32))
     _refused("device tensor", ssd.pages_compact, p, torch.zeros(4, dtype=torch.bool))
+
+
+def test_sizes_beyond_32_bits():
+    """Sizes that the C structs would cut off to 32 bits are refused (shapes only: nothing is allocated)."""
+    big = 1 << 32
+    t = lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype, device="meta")
+    ld = t(1, dtype=torch.float32)
+    idx = t(4, dtype=torch.int32)
+    for call in (lambda: ssd.lin_attn_fwd(t(1, big + 8, 1, 8), t(1, big + 8, 1, 8), t(1, big + 8, 1, 8), ld),
+                 lambda: ssd.lin_attn_fwd(t(1, 8, 1, big + 8), t(1, 8, 1, big + 8), t(1, 8, 1, 8), ld),
+                 lambda: ssd.lin_attn_step(t(big + 8, 1, 8, 8, dtype=torch.float32), t(4, 1, 8), t(4, 1, 8), t(4, 1, 8), ld),
+                 lambda: ssd.group_norm(t(big + 8, 64), 8),
+                 lambda: ssd.group_norm(t(2, big // 2, 2, 64), 8),
+                 lambda: ssd.pages_copy(t(1, big + 8, 4), idx, idx),
+                 lambda: ssd.pages_copy(t(1, 8, 4), t(big + 1, dtype=torch.int32), t(big + 1, dtype=torch.int32)),
+                 lambda: ssd.pages_clear(t(1, 8, 4), t(big + 1, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
