@@ -1,6 +1,8 @@
 // ssd_pages.hip -- pages of a pool of states, [layers][slots][page]: copied
 // (forked, permuted), compacted, cleared. All are bound by the bytes they
-// read and write.
+// read and write: 4 sequences' pages forked to 28, 2 layers of 1 MB a page, 67 MB
+// with each source read once: 16 us (4.2 TB/s); 60 live pages of 96 of 393 KB
+// made dense, 18 MB: 3 + 5 us of two launches, 15 us a call.
 #include "ssd_device.h"
 #include "ssd_layer.h"
 
@@ -190,7 +192,8 @@ void with_piece(const PagesArgs& a, F f) {
 
 hipError_t launch_pages_copy(const PagesArgs& a, const int32_t* src, const int32_t* dst, int n, hipStream_t stream) {
   // As many consecutive pieces of a page as let a workgroup hold all n pairs:
-  // 64 (1 KiB of a page) up to 64 pairs, 4 (64 bytes) at 1024.
+  // 64 (1 KiB of a page) up to 64 pairs, 4 (64 bytes) at 1024. 28 pairs with 64,
+  // 16 and 4: 16, 19 and 45 us.
   int lanes = 64;
   while (lanes > 4 && n > kCopyHeld * (kPageThreads / lanes)) lanes /= 2;
   with_piece(a, [&](auto w) {
