@@ -13,11 +13,13 @@
 // x is read once. More positions: the rows are cut into slabs; a first launch
 // leaves each slab's mean and squared deviations per channel, a second joins
 // them per group, a third applies them (reading x twice, but with every slab at
-// work at once). 16384 tokens of 32 gated groups of 128: 87 us for 403 MB, 4.6
-// TB/s; backwards, 8192 tokens of 5120 gated channels: 82 us for 420 MB, 5.1 TB/s;
-// 8 samples of 2256 positions, 320 channels, 23 MB (in cache): 21 us, of which the
-// launches are half. Means and deviations are joined about
-// their own means, in 32 bits; nothing subtracts two large sums.
+// work at once). Means and deviations are joined about their own means, in 32
+// bits; nothing subtracts two large sums.
+//
+// 16384 tokens of 32 gated groups of 128: 87 us for 403 MB, 4.6 TB/s; backwards,
+// 8192 tokens of 5120 gated channels: 82 us for 420 MB, 5.1 TB/s; 8 samples of
+// 2256 positions, 320 channels, 23 MB (in cache): 21 us, of which launches and
+// their gaps are half.
 #include <type_traits>
 
 #include "ssd_device.h"

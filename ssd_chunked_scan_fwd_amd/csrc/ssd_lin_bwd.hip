@@ -12,13 +12,16 @@
 // order, products, layouts and roundings are those of ssd_lin_scan.hip with
 // q := K, k := Q, v := dO for dV; dK contracts over R's other index, for which
 // R is laid down in LDS once a chunk as the bf16 operand it is rounded to
-// anyway. T = 8192, 32 heads of 128 x 128: 110 - 122 us against 175 for the two
-// scans; a backward call 254 us (own sums of both scans 71, entering states 18, dQ
-// 68) against 347. Larger heads take the two scans: R and its bf16 copy would not
-// fit. No single unit bounds it (matrix pipes 20 % busy, LDS half); leaving out any
-// one product gains 8 to 14 us. 4 VB waves, four a SIMD: value block w % 2 VB of R and dV a wave, of R
+// anyway. 4 VB waves, four a SIMD: value block w % 2 VB of R and dV a wave, of R
 // one half of the key columns and of dV one half of the chunk's tokens; dK's
 // blocks of 16 key columns by 16 tokens are dealt over the waves.
+//
+// T = 8192, 32 heads of 128 x 128: 110 - 122 us for 417 MB (3.4 - 3.8 TB/s), 254
+// us a backward call (own sums of both scans 71, entering states 18, dQ 68); the
+// one scan in place of two took such a call from 347 to 295 us. Heads of more
+// than 128 take two scans: R and its bf16 copy would not fit. It is bound by its
+// phases between barriers in the one workgroup that a CU holds (matrix pipes 20 %
+// busy, LDS half the time); leaving out any one product gains 8 to 14 us.
 #include "ssd_lin_chunk.h"
 
 namespace ssd {

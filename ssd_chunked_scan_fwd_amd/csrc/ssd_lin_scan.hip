@@ -22,11 +22,12 @@
 // A chunk moves C (2 dk + 2 dv) 2 bytes, reads of k and v by the blocks' own sums
 // apart, and makes 2 C (C + 3 dk) dv multiplies (the doubled state product
 // included). The next chunk's rows are in flight in registers while this one is
-// computed. T = 16384, 32 heads of 128 x 128, 16 blocks a head: own sums 58 us,
-// entering states 13, this scan 125 - 133 (345 MB, 2.7 TB/s), 205 us a call. No
-// single unit bounds the scan: matrix pipes are busy a third of it, LDS 40 %, and
-// without its loads it takes 106 us; what is left is the chain scores - barrier -
-// outputs - state of each chunk in four waves a SIMD, all that registers allow.
+// computed. T = 16384, 32 heads of 128 x 128, 16 blocks a head: own sums 57 us for
+// 283 MB (5.0 TB/s, the rate of a copy), entering states 13, this scan 125 - 133
+// for 571 MB (4.3 - 4.6 TB/s), 205 us a call. Memory bounds the sums, and with the
+// chain scores - barrier - outputs - state of each chunk (four waves a SIMD, all
+// that registers allow) the scan: without its loads it takes 106 us, with matrix
+// pipes busy a third of the time and LDS 40 %.
 #include <type_traits>
 
 #include "ssd_lin_chunk.h"
