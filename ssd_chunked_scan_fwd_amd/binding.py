@@ -693,8 +693,8 @@ def _lin_shape(q, k, v, log_decay, cu_seqlens):
             raise ValueError("packed sequences (cu_seqlens) need batch 1")
         S = cu_seqlens.numel() - 1
     _int32(dict(batch=b, seqlen=T, nheads=H, dk=Dk, dv=v.shape[3], num_seqs=S))
-    return LinShape(b, T, H, Hk, Dk, v.shape[3], S, _dtype_code(q.dtype), _token_row(q, "q"), _token_row(k, "k"),
-                    _token_row(v, "v"))
+    return _lin_struct(b, T, H, Hk, Dk, v.shape[3], S, _dtype_code(q.dtype), _token_row(q, "q"), _token_row(k, "k"),
+                       _token_row(v, "v"))
 
 
 def _structure(specs):
@@ -710,6 +710,31 @@ def _structure(specs):
             raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+
+
+def _check(device, specs):
+    """Structure, device and alignment of every given (tensor, name, shape, dtype, align);
+    dtype None: its structure was checked before. One pass while all is well, as a
+    small call's time is its host's; what is wrong is then found in order."""
+    index = device.index if device.type == "cuda" else -1
+    if index >= 0:
+        for t, name, shape, dtype, align in specs:
+            if t is not None and not (
+                    (dtype is None or (isinstance(t, torch.Tensor) and t.dtype == dtype and
+                                       (shape is None or t.shape == shape) and t.is_contiguous()))
+                    and t.get_device() == index and t.data_ptr() % align == 0):
+                break
+        else:
+            return
+    _structure([(t, name, shape, dtype) for t, name, shape, dtype, _ in specs if dtype is not None])
+    for t, name, _, _, align in specs:
+        _expect_device([(t, name)], device, align)
+
+
+@functools.lru_cache(maxsize=256)
+def _lin_struct(*values) -> LinShape:
+    """The C shape of these sizes (the library only reads it)."""
+    return LinShape(*values)
 
 
 @functools.lru_cache(maxsize=256)
@@ -738,7 +763,7 @@ def _lin_workspace(fn: str, shape: LinShape, workspace, device):
 
 def lin_attn_shape(q, k, v, cu_seqlens=None) -> LinShape:
     """The shape of a call with these tensors (for lin_attn_workspace_bytes)."""
-    return _lin_shape(q, k, v, None, cu_seqlens)
+    return LinShape(*_lin_values(_lin_shape(q, k, v, None, cu_seqlens)))   # the caller's own
 
 
 def lin_attn_workspace_bytes(shape: LinShape) -> int:
@@ -771,13 +796,11 @@ def lin_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
     if log_decay is None:
         raise ValueError("log_decay is required")
     st = (nseq, H, Dv, Dk)
-    _structure([(log_decay, "log_decay", (H,), torch.float32), (cu_seqlens, "cu_seqlens", None, torch.int32),
-                (initial_state, "initial_state", st, torch.float32), (o, "o", (b, T, H, Dv), q.dtype),
-                (final_state, "final_state", st, torch.float32), (workspace, "workspace", None, torch.uint8)])
-    _expect_device([(q, "q"), (k, "k"), (v, "v"), (initial_state, "initial_state"), (o, "o"), (final_state, "final_state")],
-                   q.device)
-    _expect_device([(log_decay, "log_decay"), (cu_seqlens, "cu_seqlens")], q.device, 4)
-    _expect_device([(workspace, "workspace")], q.device, 256)
+    _check(q.device, ((q, "q", None, None, 16), (k, "k", None, None, 16), (v, "v", None, None, 16),
+                      (initial_state, "initial_state", st, torch.float32, 16), (o, "o", (b, T, H, Dv), q.dtype, 16),
+                      (final_state, "final_state", st, torch.float32, 16),
+                      (log_decay, "log_decay", (H,), torch.float32, 4), (cu_seqlens, "cu_seqlens", None, torch.int32, 4),
+                      (workspace, "workspace", None, torch.uint8, 256)))
     workspace, have = _lin_workspace("ssd_lin_attn_workspace_bytes", shape, workspace, q.device)
     if o is None:
         o = torch.empty(b, T, H, Dv, dtype=q.dtype, device=q.device)
@@ -801,13 +824,11 @@ def lin_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
     if log_decay is None or do is None:
         raise ValueError("log_decay and do are required")
     st = (nseq, H, Dv, Dk)
-    _structure([(log_decay, "log_decay", (H,), torch.float32), (cu_seqlens, "cu_seqlens", None, torch.int32),
-                (do, "do", (b, T, H, Dv), q.dtype), (initial_state, "initial_state", st, torch.float32),
-                (dfinal_state, "dfinal_state", st, torch.float32), (workspace, "workspace", None, torch.uint8)])
-    _expect_device([(q, "q"), (k, "k"), (v, "v"), (do, "do"), (initial_state, "initial_state"),
-                    (dfinal_state, "dfinal_state")], q.device)
-    _expect_device([(log_decay, "log_decay"), (cu_seqlens, "cu_seqlens")], q.device, 4)
-    _expect_device([(workspace, "workspace")], q.device, 256)
+    _check(q.device, ((q, "q", None, None, 16), (k, "k", None, None, 16), (v, "v", None, None, 16),
+                      (do, "do", (b, T, H, Dv), q.dtype, 16), (initial_state, "initial_state", st, torch.float32, 16),
+                      (dfinal_state, "dfinal_state", st, torch.float32, 16),
+                      (log_decay, "log_decay", (H,), torch.float32, 4), (cu_seqlens, "cu_seqlens", None, torch.int32, 4),
+                      (workspace, "workspace", None, torch.uint8, 256)))
     workspace, have = _lin_workspace("ssd_lin_attn_bwd_workspace_bytes", shape, workspace, q.device)
     out = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=q.device), dk=torch.empty(k.shape, dtype=q.dtype, device=q.device),
                dv=torch.empty(v.shape, dtype=q.dtype, device=q.device),
@@ -846,15 +867,14 @@ def lin_attn_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     _int32(dict(batch=b, nheads=H, dk=Dk, dv=Dv, num_slots=n))
     if slots is None and n < b:
         raise ValueError(f"state has {n} slots for {b} entries")
-    _structure([(q, "q", None, q.dtype), (k, "k", None, q.dtype), (v, "v", None, q.dtype),
-                (state, "state", (n, H, Dv, Dk), torch.float32), (log_decay, "log_decay", (H,), torch.float32),
-                (slots, "slots", (b,), torch.int32), (o, "o", (b, H, Dv), q.dtype)])
-    _expect_device([(q, "q"), (k, "k"), (v, "v"), (state, "state"), (o, "o")], q.device)
-    _expect_device([(log_decay, "log_decay"), (slots, "slots")], q.device, 4)
+    dtype, device = q.dtype, q.device
+    _check(device, ((q, "q", None, dtype, 16), (k, "k", None, dtype, 16), (v, "v", None, dtype, 16),
+                    (state, "state", (n, H, Dv, Dk), torch.float32, 16), (o, "o", (b, H, Dv), dtype, 16),
+                    (log_decay, "log_decay", (H,), torch.float32, 4), (slots, "slots", (b,), torch.int32, 4)))
     if o is None:
-        o = torch.empty(b, H, Dv, dtype=q.dtype, device=q.device)
-    shape = LinShape(b, 1, H, Hk, Dk, Dv, 0, _dtype_code(q.dtype), 0, 0, 0)
-    _call_on(q.device, "ssd_lin_attn_step", _addr(state), _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(slots), n,
+        o = torch.empty((b, H, Dv), dtype=dtype, device=device)
+    shape = _lin_struct(b, 1, H, Hk, Dk, Dv, 0, _dtype_code(dtype), 0, 0, 0)
+    _call_on(device, "ssd_lin_attn_step", _addr(state), _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(slots), n,
              float(scale), _addr(o), ctypes.byref(shape))
     return o
 
@@ -932,11 +952,10 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
     """
     shape = _norm_shape(x, groups, z, act, gate, center)
     C, st = shape.channels, (shape.samples, shape.groups, 2)
-    _structure([(weight, "weight", (C,), torch.float32), (bias, "bias", (C,), torch.float32), (y, "y", x.shape, x.dtype),
-                (stats, "stats", st, torch.float32), (workspace, "workspace", None, torch.uint8)])
-    _expect_device([(x, "x"), (z, "z"), (weight, "weight"), (bias, "bias"), (y, "y"), (stats, "stats")], x.device,
-                   x.element_size())
-    _expect_device([(workspace, "workspace")], x.device, 256)
+    e = x.element_size()
+    _check(x.device, ((x, "x", None, None, e), (z, "z", None, None, e), (weight, "weight", (C,), torch.float32, e),
+                      (bias, "bias", (C,), torch.float32, e), (y, "y", x.shape, x.dtype, e),
+                      (stats, "stats", st, torch.float32, e), (workspace, "workspace", None, torch.uint8, 256)))
     workspace, have = _norm_workspace(shape, 0, workspace, x.device)
     if y is None:
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
@@ -958,11 +977,10 @@ def group_norm_bwd(x: torch.Tensor, groups: int, stats: torch.Tensor, dy: torch.
     C, st = shape.channels, (shape.samples, shape.groups, 2)
     if stats is None or dy is None:
         raise ValueError("stats and dy are required")
-    _structure([(weight, "weight", (C,), torch.float32), (bias, "bias", (C,), torch.float32), (dy, "dy", x.shape, x.dtype),
-                (stats, "stats", st, torch.float32), (workspace, "workspace", None, torch.uint8)])
-    _expect_device([(x, "x"), (z, "z"), (dy, "dy"), (weight, "weight"), (bias, "bias"), (stats, "stats")], x.device,
-                   x.element_size())
-    _expect_device([(workspace, "workspace")], x.device, 256)
+    e = x.element_size()
+    _check(x.device, ((x, "x", None, None, e), (z, "z", None, None, e), (dy, "dy", x.shape, x.dtype, e),
+                      (weight, "weight", (C,), torch.float32, e), (bias, "bias", (C,), torch.float32, e),
+                      (stats, "stats", st, torch.float32, e), (workspace, "workspace", None, torch.uint8, 256)))
     workspace, have = _norm_workspace(shape, 1, workspace, x.device)
     out = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=x.device),
                dz=None if z is None else torch.empty(x.shape, dtype=x.dtype, device=x.device),
@@ -1000,12 +1018,11 @@ def pages_copy(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor) -> torc
     shape = _pages_shape(pool)
     if not isinstance(src, torch.Tensor) or src.dim() != 1:
         raise ValueError("src must be a 1-d tensor")
-    _structure([(src, "src", None, torch.int32), (dst, "dst", src.shape, torch.int32)])
     if dst is None:
         raise ValueError("dst is required")
     _int32(dict(pairs=src.numel()))
-    _expect_device([(pool, "pool")], pool.device, 1)
-    _expect_device([(src, "src"), (dst, "dst")], pool.device, 4)
+    _check(pool.device, ((pool, "pool", None, None, 1), (src, "src", None, torch.int32, 4),
+                         (dst, "dst", src.shape, torch.int32, 4)))
     if src.numel():
         _call_on(pool.device, "ssd_pages_copy", _addr(pool), _addr(src), _addr(dst), src.numel(), ctypes.byref(shape))
     return pool
@@ -1035,11 +1052,9 @@ def pages_compact(pool: torch.Tensor, live: torch.Tensor, where: Optional[torch.
         live = live.view(torch.uint8)
     if live is None:
         raise ValueError("live is required")
-    _structure([(live, "live", (shape.slots,), torch.uint8), (where, "where", (shape.slots,), torch.int32),
-                (count, "count", (1,), torch.int32), (workspace, "workspace", None, torch.uint8)])
-    _expect_device([(pool, "pool"), (live, "live")], pool.device, 1)
-    _expect_device([(where, "where"), (count, "count")], pool.device, 4)
-    _expect_device([(workspace, "workspace")], pool.device, 256)
+    _check(pool.device, ((pool, "pool", None, None, 1), (live, "live", (shape.slots,), torch.uint8, 1),
+                         (where, "where", (shape.slots,), torch.int32, 4), (count, "count", (1,), torch.int32, 4),
+                         (workspace, "workspace", None, torch.uint8, 256)))
     size = _size_of("ssd_pages_compact_workspace_bytes", PagesShape, (shape.layers, shape.slots, shape.page_bytes))
     workspace, have = _room(size, workspace, pool.device)
     if where is None:

@@ -285,3 +285,10 @@ def test_sizes_beyond_32_bits():
                  lambda: ssd.pages_clear(t(1, 8, 4), t(big + 1, dtype=torch.int32))):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+def test_shapes_handed_out_are_the_callers_own():
+    q = torch.empty(1, 128, 2, 64, dtype=torch.bfloat16, device="meta")
+    one = ssd.lin_attn_shape(q, q, q)
+    one.dk = 8
+    assert ssd.lin_attn_shape(q, q, q).dk == 64
