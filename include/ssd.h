@@ -464,6 +464,8 @@ ssd_status ssd_step_mamba2(float* state, const void* x, const float* dt, const f
  * batch padded to one length is passed packed (cu_seqlens); what lies outside
  * the sequences may be anything. Inside one, a non-finite v may reach the
  * outputs of up to 63 tokens before it (bf16).
+ * No output may overlap an input: a state is continued into another tensor (the
+ * step alone updates in place).
  * SSD_ERR_UNSUPPORTED, here as for the norm, also where a launch would need
  * 2^32 threads or more (65535 one-token sequences of 256 heads).
  * ------------------------------------------------------------------------- */

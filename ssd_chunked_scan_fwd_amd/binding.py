@@ -801,6 +801,8 @@ def lin_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
                       (final_state, "final_state", st, torch.float32, 16),
                       (log_decay, "log_decay", (H,), torch.float32, 4), (cu_seqlens, "cu_seqlens", None, torch.int32, 4),
                       (workspace, "workspace", None, torch.uint8, 256)))
+    if final_state is not None and initial_state is not None and final_state.data_ptr() == initial_state.data_ptr():
+        raise ValueError("final_state must not be initial_state: blocks of a prompt read the one while others write the other")
     workspace, have = _lin_workspace("ssd_lin_attn_workspace_bytes", shape, workspace, q.device)
     if o is None:
         o = torch.empty(b, T, H, Dv, dtype=q.dtype, device=q.device)

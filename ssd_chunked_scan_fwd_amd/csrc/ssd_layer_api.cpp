@@ -224,6 +224,8 @@ ssd_status ssd_lin_attn_fwd(const void* q, const void* k, const void* v, const f
   if ((cu_seqlens != nullptr) != (shape->num_seqs > 0)) return SSD_ERR_INVALID_ARGUMENT;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(initial_state) || !aligned16(final_state))
     return SSD_ERR_INVALID_ARGUMENT;
+  // the last block's state may be written before the first block has read the initial one
+  if (final_state && final_state == initial_state) return SSD_ERR_INVALID_ARGUMENT;
   if ((st = lin_plan(shape, shape->dk, shape->dv, &p)) != SSD_OK) return st;
   if ((st = check_ws(workspace, workspace_bytes, p.state_bytes)) != SSD_OK) return st;
   const int rep = shape->nheads / shape->nkv_heads;
@@ -262,6 +264,7 @@ ssd_status ssd_lin_attn_bwd(const void* q, const void* k, const void* v, const f
   for (const void* t : {q, k, v, d_o, (const void*)initial_state, (const void*)dfinal_state, (const void*)dq, (const void*)dk,
                         (const void*)dv, (const void*)dinitial_state})
     if (!aligned16(t)) return SSD_ERR_INVALID_ARGUMENT;
+  if (dinitial_state && (dinitial_state == dfinal_state || dinitial_state == initial_state)) return SSD_ERR_INVALID_ARGUMENT;
   if ((st = lin_bwd_layout(shape, &L)) != SSD_OK) return st;
   if ((st = check_ws(workspace, workspace_bytes, L.total)) != SSD_OK) return st;
   char* ws = static_cast<char*>(workspace);

@@ -292,3 +292,15 @@ def test_shapes_handed_out_are_the_callers_own():
     one = ssd.lin_attn_shape(q, q, q)
     one.dk = 8
     assert ssd.lin_attn_shape(q, q, q).dk == 64
+
+
+def test_lin_states_not_in_place():
+    """A prompt's final state over its initial one would be raced by the blocks; refused."""
+    L, sh, other = ssd.lib(), lin(batch=1, nheads=2), ctypes.c_void_p(0x2000)
+    _, need = lin_bytes(sh)
+    args = [FAKE, FAKE, FAKE, FAKE, None, 1.0, other, FAKE, other, ctypes.byref(sh), FAKE, need, None]
+    assert L.ssd_lin_attn_fwd(*args) == INVALID
+    _, need = lin_bytes(sh, True)
+    for init, dfinal in ((other, None), (None, other)):
+        args = [FAKE] * 4 + [None, 1.0, init, FAKE, dfinal, FAKE, FAKE, FAKE, other, ctypes.byref(sh), FAKE, need, None]
+        assert L.ssd_lin_attn_bwd(*args) == INVALID
