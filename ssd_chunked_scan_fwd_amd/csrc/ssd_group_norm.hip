@@ -559,8 +559,10 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 }
 
 // One group of one sample: joins its slabs and channels about their common
-// mean. Threads take whole slabs, channel by channel, or, with few channels a
-// group, runs of them.
+// mean. Threads take a channel's slabs one after the other, several at a time
+// where a group has few channels; two in flight (1 x 1024 positions of 512
+// channels in 8 groups: a call of 18.5 us without, 16.0 with two, 15 with four,
+// which cost 64 x 256 positions of 512 in 32 groups 1 us of 22).
 __global__ __launch_bounds__(kThreads) void norm_join_kernel(NormArgs a, int slabs, int slab_rows, float* stats) {
   __shared__ float red[kThreads / 64];
   const int Cg = a.C / a.G;
@@ -572,13 +574,15 @@ __global__ __launch_bounds__(kThreads) void norm_join_kernel(NormArgs a, int sla
   const int last = (int)(a.s - (long)(slabs - 1) * slab_rows);             // rows of the last slab
   float sum = 0.f;
   if (s0 < lanes)
-    for (int i = s0; i < slabs; i += lanes)
-      for (int c = l; c < Cg; c += per) sum += ws[(long)i * 2 * a.C + c] * (float)(i + 1 < slabs ? slab_rows : last);
+    for (int c = l; c < Cg; c += per)
+#pragma unroll 2
+      for (int i = s0; i < slabs; i += lanes) sum += ws[(long)i * 2 * a.C + c] * (float)(i + 1 < slabs ? slab_rows : last);
   const float mean = block_sum(sum, red) / ((float)a.s * (float)Cg);
   float d = 0.f;
   if (s0 < lanes)
-    for (int i = s0; i < slabs; i += lanes)
-      for (int c = l; c < Cg; c += per) {
+    for (int c = l; c < Cg; c += per)
+#pragma unroll 2
+      for (int i = s0; i < slabs; i += lanes) {
         const float off = ws[(long)i * 2 * a.C + c] - mean;
         d += ws[((long)i * 2 + 1) * a.C + c] + (float)(i + 1 < slabs ? slab_rows : last) * off * off;
       }
@@ -684,6 +688,7 @@ __global__ __launch_bounds__(kThreads) void norm_join_bwd_kernel(NormArgs a, int
   if (i0 < lanes)
     for (int c = l; c < Cg; c += per) {
       const float w = a.w ? a.w[g * Cg + c] : 1.f;
+#pragma unroll 2
       for (int i = i0; i < slabs; i += lanes) {
         s0 += w * ws[(long)i * 2 * a.C + c];
         s1 += w * ws[((long)i * 2 + 1) * a.C + c];
