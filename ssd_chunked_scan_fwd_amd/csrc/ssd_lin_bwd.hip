@@ -114,7 +114,8 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
   if (total > 0) load(0);
   for (int t0 = 0; t0 < total; t0 += kC) {
     const int n = min(kC, total - t0);
-    const int lead = pos0 + t0 == 0 ? 0 : 1;  // the state handed in is not decayed before the last token
+    const bool first = pos0 + t0 == 0;
+    const int lead = first ? 0 : 1;  // the state handed in is not decayed before the last token
     __syncthreads();
     if (stage_k) {
 #pragma unroll
@@ -168,8 +169,7 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
         s0[r] = diff >= r ? s0[r] * w[-r] : 0.f;
         s1[r] = diff - 16 >= r ? s1[r] * w[-16 - r] : 0.f;
       }
-      *reinterpret_cast<u32x4*>(Ps[of_v] + (16 * qb + c16) * kPitchP + 32 * kp + 8 * g) =
-          u32x4{pack_bf16x2(s0[0], s0[1]), pack_bf16x2(s0[2], s0[3]), pack_bf16x2(s1[0], s1[1]), pack_bf16x2(s1[2], s1[3])};
+      store_scores(Ps[of_v] + (16 * qb + c16) * kPitchP + 32 * kp + 8 * g, s0, s1, first && qb < 2);
     }
 
     // Terms of R: dV^T (rows: the wave's value block; two token blocks) and dK^T (rows: its key block).
@@ -222,6 +222,15 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
 #pragma unroll
       for (int t = 0; t < kDkTok; ++t)
         if (kp <= (tb0 + t) / 2) OK[t] = mfma16x16x32(qf, frag_k_cols(Ps[1], kPitchP, 16 * (tb0 + t), 32 * kp, lane), OK[t]);
+      if (first && kp == 0) {   // what rounding left of the first 32 tokens' scores
+        if (half == 0) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) OV[t] = mfma16x16x32(gf[0], frag_k_cols(Ps[0], kPitchP, 16 * t, 32, lane), OV[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < kDkTok; ++t)
+          if (tb0 + t < 2) OK[t] = mfma16x16x32(qf, frag_k_cols(Ps[1], kPitchP, 16 * (tb0 + t), 32, lane), OK[t]);
+      }
     }
 
     const long low = p.start + (long)p.len - (pos0 + t0) - n;

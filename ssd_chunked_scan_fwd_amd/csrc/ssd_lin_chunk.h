@@ -104,4 +104,21 @@ __device__ __forceinline__ u32x4 frag_k_rows_shifted(const uint16_t* W, int pitc
   return frag_k_rows_accpair(W + row_shift(4 * (lane >> 4)), pitch, row0, col0, lane);
 }
 
+// Two blocks of 16 weighted scores as bf16 operand (slots of an accumulator pair)
+// at `at`. The first 32 tokens of a sequence have few scores, whose roundings do
+// not average out: what rounding leaves of those goes 32 columns on, a place that
+// their rows do not use (its keys are later), for a product of its own.
+__device__ __forceinline__ void store_scores(uint16_t* at, f32x4 s0, f32x4 s1, bool rest) {
+  const u32x4 hi = {pack_bf16x2(s0[0], s0[1]), pack_bf16x2(s0[2], s0[3]), pack_bf16x2(s1[0], s1[1]), pack_bf16x2(s1[2], s1[3])};
+  *reinterpret_cast<u32x4*>(at) = hi;
+  if (!rest) return;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    s0[r] -= r & 1 ? bf16_hi(hi[r >> 1]) : bf16_lo(hi[r >> 1]);
+    s1[r] -= r & 1 ? bf16_hi(hi[2 + (r >> 1)]) : bf16_lo(hi[2 + (r >> 1)]);
+  }
+  *reinterpret_cast<u32x4*>(at + 32) =
+      u32x4{pack_bf16x2(s0[0], s0[1]), pack_bf16x2(s0[2], s0[3]), pack_bf16x2(s1[0], s1[1]), pack_bf16x2(s1[2], s1[3])};
+}
+
 }  // namespace ssd

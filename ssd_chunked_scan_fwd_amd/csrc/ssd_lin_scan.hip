@@ -17,7 +17,8 @@
 //           would weigh as much as that of the state itself as an operand. Of
 //           three where the last state is asked for, an fp32 result: its error
 //           is then that of 32-bit sums.
-// Roundings to bf16: the weighted scores and the state as operands, and O.
+// Roundings to bf16: the weighted scores (of a sequence's first 32 tokens as the
+// sum of two, store_scores) and the state as operands, and O.
 //
 // A chunk moves C (2 dk + 2 dv) 2 bytes, reads of k and v by the blocks' own sums
 // apart, and makes 2 C (C + 3 dk) dv multiplies (the doubled state product
@@ -142,7 +143,8 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
   for (int ci = 0; ci < chunks; ++ci) {
     const int t0 = (STATE_ONLY ? chunks - 1 - ci : ci) * kC;
     const int n = min(kC, total - t0);
-    const int lead = a.rev && pos0 + t0 == 0 ? 0 : 1;   // the state handed to a reversed scan is not decayed first
+    const bool first = pos0 + t0 == 0;
+    const int lead = a.rev && first ? 0 : 1;   // the state handed to a reversed scan is not decayed first
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kQK; ++j) {
@@ -181,8 +183,7 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
           s0[r] = diff >= r ? s0[r] * w[-r] : 0.f;
           s1[r] = diff - 16 >= r ? s1[r] * w[-16 - r] : 0.f;
         }
-        *reinterpret_cast<u32x4*>(Ps + (16 * qb + c16) * kPitchP + 32 * kp + 8 * g) =
-            u32x4{pack_bf16x2(s0[0], s0[1]), pack_bf16x2(s0[2], s0[3]), pack_bf16x2(s1[0], s1[1]), pack_bf16x2(s1[2], s1[3])};
+        store_scores(Ps + (16 * qb + c16) * kPitchP + 32 * kp + 8 * g, s0, s1, first && qb < 2);
       }
     }
 
@@ -209,6 +210,10 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
 #pragma unroll
         for (int kp = 0; kp <= qb / 2; ++kp)
           O[qb] = mfma16x16x32(vf[kp], frag_k_cols(Ps, kPitchP, 16 * qb, 32 * kp, lane), O[qb]);
+      if (first) {
+#pragma unroll
+        for (int qb = 0; qb < 2; ++qb) O[qb] = mfma16x16x32(vf[0], frag_k_cols(Ps, kPitchP, 16 * qb, 32, lane), O[qb]);
+      }
       // O^T: column c16 is the query, rows 4 g + r the value columns.
       const long low = p.start + (a.rev ? (long)p.len - (pos0 + t0) - n : (long)pos0 + t0);
       const int esz = a.o_f32 ? 4 : 2, orow = a.H * a.dv * esz;

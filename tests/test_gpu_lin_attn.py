@@ -165,6 +165,27 @@ def test_sequence_of_every_slot(S):
     check_fwd(d, decays(2), 0.3, cu)
 
 
+@pytest.mark.parametrize("dims", [(64, 128), (128, 64), (16, 256)])
+@pytest.mark.parametrize("T", [1, 2, 7, 32])
+def test_short_sequences_keep_their_scores(T, dims):
+    """From no state, the first 32 tokens are as exact as their type: their scores enter as the sum of two bf16
+    values, which leaves 2^-16 of each (2^-8 of 2^-8), so that what remains is the result's own rounding:
+    |err| <= 2^-8 |ref| + 2^-16 E + the bound of 32-bit sums; once rounded, a score would add 2^-8 E."""
+    dk, dv = dims
+    say(f"[lin short] {T} {dims}")
+    d = make(2, T, 4, 4, dk, dv, BF, 60 + T)
+    ld = decays(4)
+    q, k, v, do = (n64(d[n]) for n in ("q", "k", "v", "do"))
+    o, _ = ssd.lin_attn_fwd(d["q"], d["k"], d["v"], ld.cuda(), scale=0.25)
+    g = ssd.lin_attn_bwd(d["q"], d["k"], d["v"], ld.cuda(), d["do"], scale=0.25)
+    want, E = ref.attention(q, k, v, n64(ld), 0.25)
+    gw, gE = ref.attention_bwd(q, k, v, n64(ld), 0.25, do)
+    for name, got, w, e in [("o", o, want["o"], E["o"])] + [(n, g[n], gw[n], gE[n]) for n in ("dq", "dk", "dv")]:
+        left = (2.0 ** -16 + (2 * T + max(dk, dv) + 16) * 2.0 ** -24) * e
+        over = abs(n64(got) - w) - (2.0 ** -8 * (abs(w) + left) + left)
+        assert over.max() <= 0, (name, over.max())
+
+
 def test_decay_not_a_number_shows():
     d = make(1, 80, 2, 2, 32, 32, BF, 63)
     ld = torch.tensor([float("nan"), -0.1], device="cuda")
