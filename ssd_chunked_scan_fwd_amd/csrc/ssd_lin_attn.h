@@ -160,13 +160,16 @@ __device__ __forceinline__ double lin_power(float log_decay, int e) {
 }
 
 // lam as a sum of two floats: rounded to one, the same error would enter with
-// every token and compound.
+// every token and compound. Both are above 0 (unless lam is 0): an infinity in
+// a state times a low part of 0 or below would be, or end in, a NaN.
 struct LinDecay {
   float hi, lo;
 };
+constexpr float kOneHi = 1.f - 0x1p-24f, kOneLo = 0x1p-24f;   // 1, for a token that is not decayed
 __device__ __forceinline__ LinDecay lin_decay(float log_decay) {
   const double lam = lin_power(log_decay, 1);
-  const float hi = (float)lam;
+  float hi = (float)lam;
+  if ((double)hi >= lam && hi > 0.f) hi = __uint_as_float(__float_as_uint(hi) - 1);   // the nearest float below
   return LinDecay{hi, (float)(lam - (double)hi)};
 }
 

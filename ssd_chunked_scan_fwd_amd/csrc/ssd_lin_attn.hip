@@ -120,7 +120,7 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
     if (t0 + kRecTok < n) load(t0 + kRecTok);
     auto step = [&](int t) {
       const bool keep = a.rev && pos0 + t0 + t == 0;  // the state handed to a reversed scan is not decayed first
-      const float hi = keep ? 1.f : lam.hi, lo = keep ? 0.f : lam.lo;
+      const float hi = keep ? kOneHi : lam.hi, lo = keep ? kOneLo : lam.lo;
       const float v = vs[t][r];
       float part = 0.f;
 #pragma unroll
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
     dst = a.states + (slot * a.H + h) * mat;
   } else if (last && a.fin) {
     dst = a.fin + ((long)p.seq * a.H + h) * mat;
-    sc = a.fin_scale * (a.rev && p.len > 0 ? lam.hi : 1.f);
+    sc = a.fin_scale * (a.rev && p.len > 0 ? lam.hi + lam.lo : 1.f);
   }
   if (dst && row < a.dv) {
 #pragma unroll
