@@ -166,12 +166,12 @@ struct LinDecay {
   float hi, lo;
 };
 constexpr float kOneHi = 1.f - 0x1p-24f, kOneLo = 0x1p-24f;   // 1, for a token that is not decayed
-__device__ __forceinline__ LinDecay lin_decay(float log_decay) {
-  const double lam = lin_power(log_decay, 1);
+__device__ __forceinline__ LinDecay lin_split(double lam) {
   float hi = (float)lam;
   if ((double)hi >= lam && hi > 0.f) hi = __uint_as_float(__float_as_uint(hi) - 1);   // the nearest float below
   return LinDecay{hi, (float)(lam - (double)hi)};
 }
+__device__ __forceinline__ LinDecay lin_decay(float log_decay) { return lin_split(lin_power(log_decay, 1)); }
 
 #endif
 

@@ -12,16 +12,21 @@ constexpr int kC = 64;                       // tokens a chunk
 constexpr int kPitchP = lds_pitch(kC);       // LDS row of 64 scores
 
 // Powers of the decay, pw[kPowZero + e] = lam^e for e = 0 .. 64 and 0 for e = -64
-// .. -1, spw scale times them: the weight of every pair and token of a chunk is
+// .. -1, spw scale times them, pw[kPowHi] and the next lam as a sum of two floats: the weight of every pair and token of a chunk is
 // one LDS read (an exponential costs a wave as long as sixteen multiplies, and
 // a chunk has some forty weights a lane). They are rounded once, from 64 bits:
 // lam^64 carries the state from chunk to chunk, and an error in it compounds.
-constexpr int kPowZero = 64, kPowSize = 132;
+constexpr int kPowZero = 64, kPowHi = 130, kPowSize = 132;
 __device__ __forceinline__ void fill_powers(float* pw, float* spw, float log_decay, float scale) {
-  for (int i = threadIdx.x; i < kPowSize; i += blockDim.x) {
+  for (int i = threadIdx.x; i < kPowHi; i += blockDim.x) {
     const double x = i < kPowZero ? 0.0 : lin_power(log_decay, i - kPowZero);
     pw[i] = (float)x;
     if (spw) spw[i] = (float)(x * (double)scale);
+    if (i == kPowZero + 1) {
+      const LinDecay lam = lin_split(x);
+      pw[kPowHi] = lam.hi;
+      pw[kPowHi + 1] = lam.lo;
+    }
   }
 }
 
@@ -120,5 +125,7 @@ __device__ __forceinline__ void store_scores(uint16_t* at, f32x4 s0, f32x4 s1, b
   *reinterpret_cast<u32x4*>(at + 32) =
       u32x4{pack_bf16x2(s0[0], s0[1]), pack_bf16x2(s0[2], s0[3]), pack_bf16x2(s1[0], s1[1]), pack_bf16x2(s1[2], s1[3])};
 }
+
+__device__ __forceinline__ f32x4 four(u32x2 w) { return f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)}; }
 
 }  // namespace ssd

@@ -37,10 +37,160 @@ namespace ssd {
 
 namespace {
 
+// What a workgroup takes: 128 or 64 value columns (DV) of one head's block.
+struct LinUnit {
+  int dv0, h, pos0, total;   // first column, head, the block's first token and tokens in the sequence
+  long slot;
+  bool last;                 // of the sequence
+  LinPiece p;                // p.blk < 0: nothing
+};
+template <int DV>
+__device__ __forceinline__ LinUnit lin_unit(const LinScan& a, long bid, long blocks) {
+  LinUnit w;
+  const int tiles = (a.dv + DV - 1) / DV;
+  const long u = xcd_unit(bid, blocks);
+  w.dv0 = (int)(u % tiles) * DV;
+  w.h = (int)((u / tiles) % a.H);
+  w.slot = u / ((long)tiles * a.H);
+  w.p = lin_piece(a, w.slot);
+  w.pos0 = w.p.blk * a.L;
+  w.total = min(w.p.len - w.pos0, a.L);
+  w.last = w.pos0 + w.total >= w.p.len;
+  return w;
+}
+
+// The state that enters the block: S[b] holds D[dvc][dk] at dk = 16 b + 4 g + r.
+template <int KB, bool STATE_ONLY>
+__device__ __forceinline__ void enter_state(const LinScan& a, const LinUnit& w, int dvc, int g, f32x4 (&S)[2 * KB]) {
+#pragma unroll
+  for (int b = 0; b < 2 * KB; ++b) S[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (STATE_ONLY) return;
+  const long mat = (long)a.dv * a.dk;
+  const float* src = w.p.blk > 0 ? a.states + (w.slot * a.H + w.h) * mat : a.init;
+  if (w.p.blk == 0 && src) src += ((long)w.p.seq * a.H + w.h) * mat;
+  const bool tr = w.p.blk == 0 && a.init_tr;
+  const float sc = w.p.blk == 0 ? a.init_scale : 1.f;
+  if (!src || dvc >= a.dv) return;
+#pragma unroll
+  for (int b = 0; b < 2 * KB; ++b) {
+    const int dk = 16 * b + 4 * g;
+    if (dk >= a.dk) continue;
+    if (tr) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[b][r] = sc * src[(long)(dk + r) * a.dv + dvc];
+    } else {
+      S[b] = *reinterpret_cast<const f32x4*>(src + (long)dvc * a.dk + dk) * sc;
+    }
+  }
+}
+
+// The state that leaves it, where it is wanted: the block's own sum or the last state.
+template <int KB, bool STATE_ONLY>
+__device__ __forceinline__ void leave_state(const LinScan& a, const LinUnit& w, int dvc, int g, const f32x4 (&S)[2 * KB],
+                                            const float* pw) {
+  const long mat = (long)a.dv * a.dk;
+  float* dst = nullptr;
+  float sc = 1.f;
+  if (STATE_ONLY) {
+    dst = a.states + (w.slot * a.H + w.h) * mat;
+  } else if (w.last && a.fin) {
+    dst = a.fin + ((long)w.p.seq * a.H + w.h) * mat;
+    sc = a.fin_scale * (a.rev && w.p.len > 0 ? pw[kPowZero + 1] : 1.f);
+  }
+  if (!dst || dvc >= a.dv) return;
+#pragma unroll
+  for (int b = 0; b < 2 * KB; ++b) {
+    const int dk = 16 * b + 4 * g;
+    if (dk < a.dk) *reinterpret_cast<f32x4*>(dst + (long)dvc * a.dk + dk) = S[b] * sc;
+  }
+}
+
+// What a wave needs to find its block again. It lies in LDS, and the arguments
+// are read from where the launch put them: kept at hand through the loop of the
+// matrix form they take scalar registers that cost it up to 6 % (heads of 256).
+struct LinAgain {
+  const LinScan* args;
+  int bid, blocks;
+};
+__device__ __forceinline__ void remember(LinAgain* to, int which, long bid, long blocks) {
+  static_assert(sizeof(LinScan) % 8 == 0, "scans lie one behind the other from the first argument on");
+  if (threadIdx.x == 0) *to = LinAgain{(const LinScan*)__builtin_amdgcn_kernarg_segment_ptr() + which, (int)bid, (int)blocks};
+}
+
+// A wave's columns of a block by the recurrence itself, token by token in fp32.
+// In a matrix product a masked score (0) times an infinity or NaN of v is a NaN in
+// the output of an earlier token, and the bf16 terms of an infinity are that
+// infinity and a NaN; here a value meets only what it belongs to. Some 1.1 us a
+// token, the way from one state to the next with the next rows in flight: a NaN in
+// 16384 tokens of 32 heads of 128 x 128, 16 blocks a head, makes 0.2 ms 2.3.
+template <int KB, int W, bool STATE_ONLY>
+__device__ __forceinline__ void lin_by_token(const LinAgain* again, const float* pw) {
+  int tid = threadIdx.x;
+  asm volatile("s_waitcnt vmcnt(0)" : "+v"(tid) : : "memory");   // the outputs of the first time are written
+  const uint64_t at = (uint64_t)again->args;
+  const LinScan& a = *reinterpret_cast<const LinScan*>((uint64_t)(uint32_t)uniform((int)at) |
+                                                       (uint64_t)(uint32_t)uniform((int)(at >> 32)) << 32);
+  const int bid = uniform(again->bid), blocks = uniform(again->blocks);
+  const LinUnit u = lin_unit<16 * W>(a, bid, blocks);
+  const int g = (tid & 63) >> 4, dvc = u.dv0 + 16 * (tid >> 6) + (tid & 15);
+  f32x4 S[2 * KB];
+  enter_state<KB, STATE_ONLY>(a, u, dvc, g, S);
+  const float lam_hi = pw[kPowHi], lam_lo = pw[kPowHi + 1];
+  const int end = a.dk - 4 * g, dv = a.dv, rev = a.rev, o_f32 = a.o_f32;
+  const bool in = dvc < dv;
+  const long krow = a.k.row, qrow = a.q.row, vrow = a.v.row, orow = (long)a.H * dv;
+  const uint16_t* k0 = static_cast<const uint16_t*>(a.k.base) + (long)(u.h / a.k.div) * a.dk + 4 * g;
+  const uint16_t* q0 = static_cast<const uint16_t*>(a.q.base) + (long)(u.h / a.q.div) * a.dk + 4 * g;
+  const uint16_t* v0 = static_cast<const uint16_t*>(a.v.base) + (long)(u.h / a.v.div) * dv + (in ? dvc : 0);
+  const long o0 = (long)u.h * dv + dvc;
+  void* const out = a.o;
+  const float scale = a.scale;
+  u32x2 k[2 * KB], q[2 * KB];   // the next token's rows
+  uint16_t v = 0;
+  auto token = [&](int j) { return u.p.start + (rev ? u.p.len - 1 - (u.pos0 + j) : u.pos0 + j); };
+  auto load = [&](int j) {
+    const long tok = token(min(j, u.total - 1));
+#pragma unroll
+    for (int b = 0; b < 2 * KB; ++b) {
+      const int col = 16 * b < end ? 16 * b : 0;
+      k[b] = *reinterpret_cast<const u32x2*>(k0 + tok * krow + col);
+      if (!STATE_ONLY) q[b] = *reinterpret_cast<const u32x2*>(q0 + tok * qrow + col);
+    }
+    v = v0[tok * vrow];
+  };
+  load(0);
+#pragma unroll 1
+  for (int j = 0; j < u.total; ++j) {
+    const bool keep = rev && u.pos0 + j == 0;   // the state handed to a reversed scan is not decayed first
+    const float hi = keep ? kOneHi : lam_hi, lo = keep ? kOneLo : lam_lo, x = bf16_to_f32(v);
+    float part = 0.f;
+#pragma unroll
+    for (int b = 0; b < 2 * KB; ++b) {
+      const f32x4 kb = four(k[b]), qb = four(STATE_ONLY ? k[b] : q[b]);
+      if (16 * b >= end) continue;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        S[b][r] = fmaf(S[b][r], hi, fmaf(S[b][r], lo, x * kb[r]));
+        if (!STATE_ONLY) part = fmaf(S[b][r], qb[r], part);
+      }
+    }
+    load(j + 1);
+    if (STATE_ONLY) continue;
+    part += __shfl_xor(part, 16);
+    part = (part + __shfl_xor(part, 32)) * scale;
+    const long at = token(j) * orow + o0;
+    if (g == 0 && in) {
+      if (o_f32) static_cast<float*>(out)[at] = part;
+      else static_cast<uint16_t*>(out)[at] = f32_to_bf16(part);
+    }
+  }
+  leave_state<KB, STATE_ONLY>(a, u, dvc, g, S, pw);
+}
+
 // KB: dk in units of 32. W waves of 16 value columns. TERMS: bf16 terms of the
-// weighted V in the state product.
+// weighted V in the state product. `which` of the launch's scans is a.
 template <int KB, int W, int TERMS, bool STATE_ONLY>
-__device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks) {
+__device__ __forceinline__ void lin_mfma(const LinScan& a, int which, long bid, long blocks) {
   constexpr int kDk = 32 * KB, kDv = 16 * W, kThreads = 64 * W;
   constexpr int kPitchK = lds_pitch(kDk), kPitchV = lds_pitch(kDv);
   __shared__ __align__(16) uint16_t Ks[kC * kPitchK];
@@ -51,44 +201,18 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
   constexpr int kQK = (256 * KB + kThreads - 1) / kThreads;   // 16-byte pieces a thread stages of q and of k,
   constexpr int kV = 2;                                       // and of v
 
-  const int tiles = (a.dv + kDv - 1) / kDv;
-  const long u = xcd_unit(bid, blocks);
-  const int dv0 = (int)(u % tiles) * kDv;
-  const int h = (int)((u / tiles) % a.H);
-  const long slot = u / ((long)tiles * a.H);
-  const LinPiece p = lin_piece(a, slot);
-  if (p.blk < 0) return;
-  const int pos0 = p.blk * a.L;
-  const int total = min(p.len - pos0, a.L);
-  const bool last = pos0 + total >= p.len;
-  if (STATE_ONLY && last) return;  // the scan carries the last block's state itself
+  __shared__ LinAgain again;
+  remember(&again, which, bid, blocks);
+  const LinUnit u = lin_unit<kDv>(a, bid, blocks);
+  if (u.p.blk < 0) return;
+  if (STATE_ONLY && u.last) return;  // the scan carries the last block's state itself
+  const LinPiece& p = u.p;
+  const int dv0 = u.dv0, h = u.h, pos0 = u.pos0, total = u.total;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
-  const long mat = (long)a.dv * a.dk;
 
-  // The state: block b holds D[dvc][dk] at dk = 16 b + 4 g + r.
   const int dvc = dv0 + 16 * wave + c16;
   f32x4 S[2 * KB];
-#pragma unroll
-  for (int b = 0; b < 2 * KB; ++b) S[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (!STATE_ONLY) {
-    const float* src = p.blk > 0 ? a.states + (slot * a.H + h) * mat : a.init;
-    if (p.blk == 0 && src) src += ((long)p.seq * a.H + h) * mat;
-    const bool tr = p.blk == 0 && a.init_tr;
-    const float sc = p.blk == 0 ? a.init_scale : 1.f;
-    if (src && dvc < a.dv) {
-#pragma unroll
-      for (int b = 0; b < 2 * KB; ++b) {
-        const int dk = 16 * b + 4 * g;
-        if (dk >= a.dk) continue;
-        if (tr) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) S[b][r] = sc * src[(long)(dk + r) * a.dv + dvc];
-        } else {
-          S[b] = *reinterpret_cast<const f32x4*>(src + (long)dvc * a.dk + dk) * sc;
-        }
-      }
-    }
-  }
+  enter_state<KB, STATE_ONLY>(a, u, dvc, g, S);
 
   constexpr int kTasks = 8 / W;   // score tasks (16 queries by 32 keys) a wave
 
@@ -254,33 +378,27 @@ __device__ __forceinline__ void lin_mfma(const LinScan& a, long bid, long blocks
     }
   }
 
-  float* dst = nullptr;
-  float sc = 1.f;
-  if (STATE_ONLY) {
-    dst = a.states + (slot * a.H + h) * mat;
-  } else if (last && a.fin) {
-    dst = a.fin + ((long)p.seq * a.H + h) * mat;
-    sc = a.fin_scale * (a.rev && p.len > 0 ? pw[kPowZero + 1] : 1.f);
-  }
-  if (dst && dvc < a.dv) {
+  // A value of v or k that is not finite is left in its columns of the state, whatever comes behind it:
+  // a wave that finds one there takes them again. (A sequence without tokens has none to take.)
+  float none = 0.f;
 #pragma unroll
-    for (int b = 0; b < 2 * KB; ++b) {
-      const int dk = 16 * b + 4 * g;
-      if (dk < a.dk) *reinterpret_cast<f32x4*>(dst + (long)dvc * a.dk + dk) = S[b] * sc;
-    }
-  }
+  for (int b = 0; b < 2 * KB; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) none = fmaf(S[b][r], 0.f, none);
+  if (__builtin_expect(__ballot(none != 0.f) != 0 && u.p.len > 0, 0)) return lin_by_token<KB, W, STATE_ONLY>(&again, pw);
+  leave_state<KB, STATE_ONLY>(a, u, dvc, g, S, pw);
 }
 
 template <int KB, int W, int TERMS>
 __global__ __launch_bounds__(64 * W, KB <= 4 ? W / 2 : W / 4) void lin_mfma_kernel(LinScan a) {
-  lin_mfma<KB, W, TERMS, false>(a, blockIdx.x, gridDim.x);
+  lin_mfma<KB, W, TERMS, false>(a, 0, blockIdx.x, gridDim.x);
 }
 
 // The blocks' own sums of one scan, or of two: the first `na` workgroups are a's.
 template <int KB, int W, int TERMS>
 __global__ __launch_bounds__(64 * W, KB <= 4 ? W / 2 : W / 4) void lin_mfma_states_kernel(LinScan a, LinScan b, long na) {
-  if ((long)blockIdx.x < na) lin_mfma<KB, W, TERMS, true>(a, blockIdx.x, na);
-  else lin_mfma<KB, W, TERMS, true>(b, blockIdx.x - na, gridDim.x - na);
+  if ((long)blockIdx.x < na) lin_mfma<KB, W, TERMS, true>(a, 0, blockIdx.x, na);
+  else lin_mfma<KB, W, TERMS, true>(b, 1, blockIdx.x - na, gridDim.x - na);
 }
 
 long mfma_blocks(const LinScan& a) {

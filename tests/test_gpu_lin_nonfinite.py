@@ -1,0 +1,64 @@
+"""GPU: linear attention of bf16 operands with values that are not finite. A
+result that such a value enters by the recurrence is not finite; every other one
+is as without it: the places are compared with the recurrence in 64 bits, the
+finite values held to the bounds of layer_ref.py, and infinite states are those
+of the recurrence. fp32 operands are held to the same.
+"""
+import pytest
+import torch
+
+import layer_ref as ref
+import ssd_chunked_scan_fwd_amd as ssd
+from test_gpu_lin_infinite import _need_gpu, decays, hold, make, n64  # noqa: F401
+
+pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore::RuntimeWarning")]
+BF, F32 = torch.bfloat16, torch.float32
+NAN, INF = float("nan"), float("inf")
+
+# T, H, Hk, dk, dv, packed sequences
+SHAPES = [(200, 2, 1, 64, 64, None), (300, 2, 2, 128, 128, None), (130, 2, 1, 40, 96, None), (130, 2, 2, 96, 40, None),
+          (150, 1, 1, 256, 200, None), (200, 2, 2, 16, 24, [0, 100, 100, 170, 200])]
+# Tensors, and tokens with such a value in one channel: in a sequence's first (and, backwards, last) 32 tokens, in
+# the middle of a chunk, on its last and first place.
+PLACES = [("v", (20, 100)), ("v", (63,)), ("k", (20, 100)), ("k", (129,)), ("q", (64,)), ("q", (37, 100)), ("do", (20, 100))]
+
+
+def inputs(shape, value, dtype, name, tokens):
+    T, H, Hk, dk, dv, cu = shape
+    print(f"[lin non-finite] {shape} {value} {dtype} {name} {tokens}", flush=True)
+    d = make(T, H, Hk, dk, dv, dtype, T + dk, nseq=1 if cu is None else len(cu) - 1)
+    for i, t in enumerate(tokens):
+        d[name][0, t, 0, 5 + 2 * i] = value
+    cut = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    return d, {n: n64(t) for n, t in d.items()}, decays(H), cut
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_forwards(shape, value, dtype):
+    """o, the final state, and dq, which is carried forwards too."""
+    T, H, Hk, dk, dv, cu = shape
+    kind, state = ("bf16", "state") if dtype == BF else ("fp32", "fp32")
+    for name, tokens in PLACES:
+        d, x, ld, cut = inputs(shape, value, dtype, name, tokens)
+        o, fin = ssd.lin_attn_fwd(d["q"], d["k"], d["v"], ld.cuda(), cu_seqlens=cut, scale=0.25, initial_state=d["init"])
+        g = ssd.lin_attn_bwd(d["q"], d["k"], d["v"], ld.cuda(), d["do"], cu_seqlens=cut, scale=0.25, initial_state=d["init"])
+        want, E = ref.attention(x["q"], x["k"], x["v"], n64(ld), 0.25, x["init"], cu)
+        gw, gE = ref.attention_bwd(x["q"], x["k"], x["v"], n64(ld), 0.25, x["do"], x["init"], None, cu)
+        hold(o, want["o"], E["o"], kind, T, dk, f"{name} o")
+        hold(fin, want["final"], E["final"], state, T, dk, f"{name} final", infinite=True)
+        hold(g["dq"], gw["dq"], gE["dq"], kind, T, max(dk, dv), f"{name} dq")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_sequences_without_tokens(dtype):
+    """What is not finite in their states stays, and reaches no neighbour."""
+    cu = [0, 0, 70, 70, 130, 130]
+    d = make(130, 2, 2, 64, 64, dtype, 21, nseq=5)
+    d["init"][0, :, 3, 5], d["init"][2, :, 6, 1], d["init"][4, :, 2, 2] = INF, NAN, -INF
+    cut = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    o, fin = ssd.lin_attn_fwd(d["q"], d["k"], d["v"], decays(2).cuda(), cu_seqlens=cut, initial_state=d["init"])
+    for s in (0, 2, 4):
+        assert torch.equal(fin[s].view(torch.int32), d["init"][s].view(torch.int32))
+    assert torch.all(torch.isfinite(o)) and torch.all(torch.isfinite(fin[[1, 3]]))
