@@ -60,6 +60,29 @@ __device__ __forceinline__ float wave_incl_scan(float v) {
   return v;
 }
 
+// Sum over aligned groups of n lanes, n a power of two from LEAST to 64; every lane
+// of a group receives it (DPP within rows of 16 lanes, then lane swaps across rows).
+template <int CTRL>
+__device__ __forceinline__ float dpp_plus(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+template <int LEAST = 1>
+__device__ __forceinline__ float lanes_sum(float v, int n) {
+  if (LEAST > 1 || n > 1) v = dpp_plus<0xB1>(v);    // quad_perm [1, 0, 3, 2]
+  if (LEAST > 2 || n > 2) v = dpp_plus<0x4E>(v);    // quad_perm [2, 3, 0, 1]
+  if (n > 4) v = dpp_plus<0x141>(v);                // row_half_mirror
+  if (n > 8) v = dpp_plus<0x140>(v);                // row_mirror
+  if (n > 16) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  }
+  if (n > 32) {
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  }
+  return v;
+}
+
 // One 16x16x32 bf16 MFMA with fp32 accumulation (gfx950).
 // A: lane l holds row (l % 16), 8 consecutive k of slot group (l / 16).
 // B: lane l holds column (l % 16), the same 8 k. D: lane l holds column

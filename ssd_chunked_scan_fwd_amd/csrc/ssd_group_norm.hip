@@ -33,27 +33,6 @@ constexpr int kThreads = 256;
 constexpr int kCus = 256, kMaxParts = 1024;
 constexpr int kMaxWaves = 16;   // of a workgroup that shares one group
 
-template <int CTRL>
-__device__ __forceinline__ float dpp_plus(float v) {
-  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
-}
-// Sum over aligned groups of n lanes (a power of two up to 64); every lane receives it.
-__device__ __forceinline__ float lanes_sum(float v, int n) {
-  if (n > 1) v = dpp_plus<0xB1>(v);
-  if (n > 2) v = dpp_plus<0x4E>(v);
-  if (n > 4) v = dpp_plus<0x141>(v);
-  if (n > 8) v = dpp_plus<0x140>(v);
-  if (n > 16) {
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  }
-  if (n > 32) {
-    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(b[0]) + __uint_as_float(b[1]);
-  }
-  return v;
-}
-
 // Sums over the `lanes` threads that share a group: a power of two up to 64, or
 // the whole workgroup, then through LDS (`red`, a slot of two floats a wave;
 // calls in turn use the two halves of it, so that one barrier a call is enough).

@@ -1,26 +1,12 @@
 // ssd_lin_attn.hip -- linear attention with one fixed decay a head: the scan
 // token by token (fp32 operands), the states passed between blocks of tokens,
 // the sums over shared heads, and the one-token step on a pool of states.
-#include <type_traits>
-
 #include "ssd_device.h"
 #include "ssd_lin_attn.h"
 
 namespace ssd {
 
 namespace {
-
-// Sum over aligned groups of 16 lanes; every lane receives it.
-template <int CTRL>
-__device__ __forceinline__ float dpp_plus(float v) {
-  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
-}
-__device__ __forceinline__ float sum16(float v) {
-  v = dpp_plus<0xB1>(v);    // quad_perm [1, 0, 3, 2]
-  v = dpp_plus<0x4E>(v);    // quad_perm [2, 3, 0, 1]
-  v = dpp_plus<0x141>(v);   // row_half_mirror
-  return dpp_plus<0x140>(v);  // row_mirror
-}
 
 template <bool BF16>
 __device__ __forceinline__ float load_el(const void* p, long i) {
@@ -135,7 +121,7 @@ __global__ __launch_bounds__(256) void lin_rec_kernel(LinScan a) {
         }
       }
       if (!STATE_ONLY) {
-        part = sum16(part) * a.scale;
+        part = lanes_sum(part, 16) * a.scale;
         if (c == 0 && row < a.dv) static_cast<float*>(a.o)[(token(pos0 + t0 + t) * a.H + h) * a.dv + row] = part;
       }
     };
@@ -270,22 +256,6 @@ __global__ __launch_bounds__(256) void lin_share_sum_kernel(LinShareSum a) {
 // the batch: the first one's workgroup runs them all, so a stream may bring
 // several tokens in one call and nothing is raced.
 // ----------------------------------------------------------------------------
-__device__ __forceinline__ float lanes_sum(float v, int n) {
-  if (n > 1) v = dpp_plus<0xB1>(v);
-  if (n > 2) v = dpp_plus<0x4E>(v);
-  if (n > 4) v = dpp_plus<0x141>(v);
-  if (n > 8) v = dpp_plus<0x140>(v);
-  if (n > 16) {
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  }
-  if (n > 32) {
-    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(b[0]) + __uint_as_float(b[1]);
-  }
-  return v;
-}
-
 template <bool BF16>
 __device__ __forceinline__ f32x4 load4(const void* p, long i) {
   if constexpr (BF16) {
