@@ -462,8 +462,10 @@ ssd_status ssd_step_mamba2(float* state, const void* x, const float* dt, const f
  * dk and dv: multiples of 8 up to 256. bf16 products are formed with fp32
  * sums; states are carried in fp32. Every token of a sequence counts, so a
  * batch padded to one length is passed packed (cu_seqlens); what lies outside
- * the sequences may be anything. Inside one, a non-finite v may reach the
- * outputs of up to 63 tokens before it (bf16).
+ * the sequences may be anything. Inside one, a value that is not finite makes
+ * those results not finite that the formulas bring it to, and leaves every
+ * other as it is, in gradients too. (bf16: a call with such values takes some
+ * ten times as long, as their blocks are walked token by token.)
  * No output may overlap an input: a state is continued into another tensor (the
  * step alone updates in place).
  * SSD_ERR_UNSUPPORTED, here as for the norm, also where a launch would need

@@ -28,9 +28,152 @@ namespace ssd {
 
 namespace {
 
+struct KvArgs {
+  LinScan a;        // the scan for dv
+  LinOperand v;
+  void* dk_out;
+};
+
+// What a workgroup takes: one head's block.
+struct KvUnit {
+  int h, pos0, total;   // head, the block's first token and tokens in the sequence
+  long slot;
+  bool last;            // of the sequence
+  LinPiece p;           // p.blk < 0: nothing
+};
+__device__ __forceinline__ KvUnit kv_unit(const LinScan& a) {
+  KvUnit w;
+  const long u = xcd_unit(blockIdx.x, gridDim.x);
+  w.h = (int)(u % a.H);
+  w.slot = u / a.H;
+  w.p = lin_piece(a, w.slot);
+  w.pos0 = w.p.blk * a.L;
+  w.total = min(w.p.len - w.pos0, a.L);
+  w.last = w.pos0 + w.total >= w.p.len;
+  return w;
+}
+
+// A wave's part of R, dv = dvc and dk = dk0 + 16 b + r: as it enters the block,
+template <int KB>
+__device__ __forceinline__ void enter_state(const LinScan& a, const KvUnit& w, int dvc, int dk0, f32x4 (&R)[KB]) {
+  const long mat = (long)a.dv * a.dk;
+#pragma unroll
+  for (int b = 0; b < KB; ++b) R[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const float* src = w.p.blk > 0 ? a.states + (w.slot * a.H + w.h) * mat : a.init;
+  if (w.p.blk == 0 && src) src += ((long)w.p.seq * a.H + w.h) * mat;
+  const float sc = w.p.blk == 0 ? a.init_scale : 1.f;
+  if (!src || dvc >= a.dv) return;
+#pragma unroll
+  for (int b = 0; b < KB; ++b) {
+    const int dk = dk0 + 16 * b;
+    if (dk < a.dk) R[b] = *reinterpret_cast<const f32x4*>(src + (long)dvc * a.dk + dk) * sc;
+  }
+}
+// and as it leaves the sequence.
+template <int KB>
+__device__ __forceinline__ void leave_state(const LinScan& a, const KvUnit& w, int dvc, int dk0, const f32x4 (&R)[KB],
+                                            const float* pw) {
+  if (!w.last || !a.fin || dvc >= a.dv) return;
+  const float sc = a.fin_scale * (w.p.len > 0 ? pw[kPowZero + 1] : 1.f);
+  float* dst = a.fin + ((long)w.p.seq * a.H + w.h) * a.dv * a.dk;
+#pragma unroll
+  for (int b = 0; b < KB; ++b) {
+    const int dk = dk0 + 16 * b;
+    if (dk < a.dk) *reinterpret_cast<f32x4*>(dst + (long)dvc * a.dk + dk) = R[b] * sc;
+  }
+}
+
+// The block by the recurrence itself, token by token in fp32, where a value of q
+// or dO is not finite (see lin_by_token). R lies over the waves as in the matrix
+// form. Of every token each wave leaves its sums over its part of R in `part`, of
+// even tokens in one half and of odd ones in the other, and behind a barrier they
+// are joined in order. `again`, in LDS: where the launch put the arguments.
+template <int KB, int VB>
+__device__ __forceinline__ void kv_by_token(const KvArgs* const* again, float* part, const float* pw) {
+  constexpr int kThreads = 256 * VB, kHalf = 2 * 32 * VB + 2 * VB * 32 * KB;
+  static_assert(2 * kHalf * 4 <= 2 * kC * kPitchP * 2, "lies in the scores' place");
+  int tid = threadIdx.x;
+  asm volatile("s_waitcnt vmcnt(0)" : "+v"(tid) : : "memory");   // the outputs of the first time are written
+  const KvArgs* args = uniform(*again);
+  const LinScan& a = args->a;
+  const KvUnit u = kv_unit(a);
+  const int wave = uniform(tid >> 6), c16 = tid & 15, g = (tid & 63) >> 4;
+  const int vb = wave % (2 * VB), half = wave / (2 * VB);
+  const int dvc = 16 * vb + c16, dk0 = 16 * KB * half + 4 * g;
+  const int dk = a.dk, dv = a.dv, H = a.H, o_f32 = a.o_f32;
+  const bool in = dvc < dv;
+  const long krow = a.q.row, qrow = a.k.row, grow = a.v.row, vrow = args->v.row;
+  auto base = [&](const LinOperand& x, int d) { return static_cast<const uint16_t*>(x.base) + (long)(u.h / x.div) * d; };
+  const uint16_t *k0 = base(a.q, dk), *q0 = base(a.k, dk), *g0 = base(a.v, dv) + (in ? dvc : 0),
+                 *v0 = base(args->v, dv) + (in ? dvc : 0);
+  void *const out_v = a.o, *const out_k = args->dk_out;
+  const float scale = a.scale, lam_hi = pw[kPowHi], lam_lo = pw[kPowHi + 1];
+  f32x4 R[KB];
+  enter_state<KB>(a, u, dvc, dk0, R);
+  u32x2 k[KB], q[KB];   // the next token's rows
+  uint16_t dO = 0, v = 0;
+  auto token = [&](int j) { return u.p.start + (u.p.len - 1 - (u.pos0 + j)); };
+  auto load = [&](int j) {
+    const long tok = token(min(j, u.total - 1));
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      const int col = dk0 + 16 * b < dk ? dk0 + 16 * b : 0;
+      k[b] = *reinterpret_cast<const u32x2*>(k0 + tok * krow + col);
+      q[b] = *reinterpret_cast<const u32x2*>(q0 + tok * qrow + col);
+    }
+    dO = g0[tok * grow];
+    v = v0[tok * vrow];
+  };
+  auto put = [&](void* out, int d, int j, int i, float o) {
+    const long at = (token(j) * H + u.h) * d + i;
+    if (o_f32) static_cast<float*>(out)[at] = o * scale;
+    else static_cast<uint16_t*>(out)[at] = f32_to_bf16(o * scale);
+  };
+  load(0);
+#pragma unroll 1
+  for (int j = 0; j < u.total; ++j) {
+    const bool keep = u.pos0 + j == 0;   // the state handed in is not decayed before the last token
+    const float hi = keep ? kOneHi : lam_hi, lo = keep ? kOneLo : lam_lo;
+    const float x = bf16_to_f32(dO), y = bf16_to_f32(v);
+    float *sum_v = part + (j & 1) * kHalf, *sum_k = sum_v + 2 * 32 * VB, to_v = 0.f;
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      const f32x4 kb = four(k[b]), qb = four(q[b]);
+      f32x4 to_k = {0.f, 0.f, 0.f, 0.f};
+      if (in && dk0 + 16 * b < dk) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          R[b][r] = fmaf(R[b][r], hi, fmaf(R[b][r], lo, x * qb[r]));
+          to_v = fmaf(R[b][r], kb[r], to_v);
+          to_k[r] = R[b][r] * y;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) to_k[r] = lanes_sum(to_k[r], 16);
+      if (c16 == 0) *reinterpret_cast<f32x4*>(sum_k + vb * 32 * KB + dk0 + 16 * b) = to_k;
+    }
+    load(j + 1);
+    to_v += __shfl_xor(to_v, 16);
+    to_v += __shfl_xor(to_v, 32);
+    if (g == 0) sum_v[half * 32 * VB + dvc] = to_v;
+    __syncthreads();
+    if (tid < dk) {
+      float o = 0.f;
+      for (int i = 0; i < 2 * VB; ++i) o += sum_k[i * 32 * KB + tid];
+      put(out_k, dk, j, tid, o);
+    }
+    const int i = kThreads - 1 - tid;
+    if (i < dv) put(out_v, dv, j, i, sum_v[i] + sum_v[32 * VB + i]);
+  }
+  leave_state<KB>(a, u, dvc, dk0, R, pw);
+}
+
 // KB, VB: dk and dv in units of 32 (2 or 4). TERMS: as in ssd_lin_scan.hip.
 template <int KB, int VB, int TERMS>
-__global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOperand vop, void* dk_out) {
+__global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(KvArgs args) {
+  const LinScan& a = args.a;
+  const LinOperand& vop = args.v;
+  void* const dk_out = args.dk_out;
   constexpr int kWaves = 4 * VB, kThreads = 64 * kWaves;
   constexpr int kPitchK = lds_pitch(32 * KB), kPitchV = lds_pitch(32 * VB);
   __shared__ __align__(16) uint16_t Qs[kC * kPitchK], Gs[kC * kPitchV];   // q and dO, rows by row_shift
@@ -48,36 +191,20 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
   // dK: blocks of 16 key columns by 16 tokens a wave.
   constexpr int kDkTok = 2 * KB / VB;
 
-  const long u = xcd_unit(blockIdx.x, gridDim.x);
-  const int h = (int)(u % a.H);
-  const long slot = u / a.H;
-  const LinPiece p = lin_piece(a, slot);
-  if (p.blk < 0) return;
-  const int pos0 = p.blk * a.L;
-  const int total = min(p.len - pos0, a.L);
-  const bool last = pos0 + total >= p.len;
+  __shared__ const KvArgs* again;
+  if (threadIdx.x == 0) again = (const KvArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  const KvUnit u = kv_unit(a);
+  if (u.p.blk < 0) return;
+  const LinPiece& p = u.p;
+  const int h = u.h, pos0 = u.pos0, total = u.total;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
   const int vb = wave % (2 * VB), half = wave / (2 * VB);     // value block; half of dk (R) and of the tokens (dV)
   const int kb0 = wave % (2 * KB), tb0 = wave / (2 * KB) * kDkTok;   // dK: key block, first token block
-  const long mat = (long)a.dv * a.dk;
   fill_powers(pw, spw, a.ld[h], a.scale);
 
-  f32x4 R[KB];   // dv = 16 vb + c16, dk = 16 (KB half + b) + 4 g + r
-#pragma unroll
-  for (int b = 0; b < KB; ++b) R[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int dvc = 16 * vb + c16;
-  {
-    const float* src = p.blk > 0 ? a.states + (slot * a.H + h) * mat : a.init;
-    if (p.blk == 0 && src) src += ((long)p.seq * a.H + h) * mat;
-    const float sc = p.blk == 0 ? a.init_scale : 1.f;
-    if (src && dvc < a.dv) {
-#pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        const int dk = 16 * (KB * half + b) + 4 * g;
-        if (dk < a.dk) R[b] = *reinterpret_cast<const f32x4*>(src + (long)dvc * a.dk + dk) * sc;
-      }
-    }
-  }
+  const int dvc = 16 * vb + c16, dk0 = 16 * KB * half + 4 * g;
+  f32x4 R[KB];   // dv = dvc, dk = dk0 + 16 b + r
+  enter_state<KB>(a, u, dvc, dk0, R);
 
   const int qrow = (int)a.k.row * 2, krow = (int)a.q.row * 2, grow = (int)a.v.row * 2, vrow = (int)vop.row * 2;
   const int tid = kHalves ? threadIdx.x % kStage : threadIdx.x;
@@ -268,15 +395,15 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(LinScan a, LinOpera
     }
   }
 
-  if (last && a.fin && dvc < a.dv) {
-    const float sc = a.fin_scale * (p.len > 0 ? pw[kPowZero + 1] : 1.f);
-    float* dst = a.fin + ((long)p.seq * a.H + h) * mat;
+  // A value of q or dO that is not finite is left in R, whatever comes behind it.
+  float none = 0.f;
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      const int dk = 16 * (KB * half + b) + 4 * g;
-      if (dk < a.dk) *reinterpret_cast<f32x4*>(dst + (long)dvc * a.dk + dk) = R[b] * sc;
-    }
-  }
+  for (int b = 0; b < KB; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) none = fmaf(R[b][r], 0.f, none);
+  if (__builtin_expect(__syncthreads_or(none != 0.f), 0))
+    return kv_by_token<KB, VB>(&again, reinterpret_cast<float*>(&Ps[0][0]), pw);
+  leave_state<KB>(a, u, dvc, dk0, R, pw);
 }
 
 }  // namespace
@@ -292,8 +419,9 @@ template <int KB, int VB>
 void kv_launch(const LinScan& a, const LinOperand& v, void* dk_out, hipStream_t stream) {
   const long slots = a.S > 0 ? a.slots_per_row : a.slots_per_row * a.batch;
   const dim3 grid((unsigned)(slots * a.H)), block(256 * VB);
-  if (a.fine()) hipLaunchKernelGGL((lin_kv_kernel<KB, VB, 3>), grid, block, 0, stream, a, v, dk_out);
-  else hipLaunchKernelGGL((lin_kv_kernel<KB, VB, 2>), grid, block, 0, stream, a, v, dk_out);
+  const KvArgs args = {a, v, dk_out};
+  if (a.fine()) hipLaunchKernelGGL((lin_kv_kernel<KB, VB, 3>), grid, block, 0, stream, args);
+  else hipLaunchKernelGGL((lin_kv_kernel<KB, VB, 2>), grid, block, 0, stream, args);
 }
 }  // namespace
 

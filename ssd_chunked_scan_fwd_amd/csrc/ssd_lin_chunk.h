@@ -126,6 +126,12 @@ __device__ __forceinline__ void store_scores(uint16_t* at, f32x4 s0, f32x4 s1, b
       u32x4{pack_bf16x2(s0[0], s0[1]), pack_bf16x2(s0[2], s0[3]), pack_bf16x2(s1[0], s1[1]), pack_bf16x2(s1[2], s1[3])};
 }
 
+// A pointer that all lanes hold, in scalar registers.
+template <typename T>
+__device__ __forceinline__ const T* uniform(const T* p) {
+  const uint64_t at = (uint64_t)p;
+  return (const T*)((uint64_t)(uint32_t)uniform((int)at) | (uint64_t)(uint32_t)uniform((int)(at >> 32)) << 32);
+}
 __device__ __forceinline__ f32x4 four(u32x2 w) { return f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)}; }
 
 }  // namespace ssd

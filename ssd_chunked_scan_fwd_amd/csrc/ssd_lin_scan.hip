@@ -127,9 +127,7 @@ template <int KB, int W, bool STATE_ONLY>
 __device__ __forceinline__ void lin_by_token(const LinAgain* again, const float* pw) {
   int tid = threadIdx.x;
   asm volatile("s_waitcnt vmcnt(0)" : "+v"(tid) : : "memory");   // the outputs of the first time are written
-  const uint64_t at = (uint64_t)again->args;
-  const LinScan& a = *reinterpret_cast<const LinScan*>((uint64_t)(uint32_t)uniform((int)at) |
-                                                       (uint64_t)(uint32_t)uniform((int)(at >> 32)) << 32);
+  const LinScan& a = *uniform(again->args);
   const int bid = uniform(again->bid), blocks = uniform(again->blocks);
   const LinUnit u = lin_unit<16 * W>(a, bid, blocks);
   const int g = (tid & 63) >> 4, dvc = u.dv0 + 16 * (tid >> 6) + (tid & 15);
@@ -395,8 +393,10 @@ __global__ __launch_bounds__(64 * W, KB <= 4 ? W / 2 : W / 4) void lin_mfma_kern
 }
 
 // The blocks' own sums of one scan, or of two: the first `na` workgroups are a's.
+// Five waves a SIMD up to dk = 64, as the matrix form takes: without the bound
+// lin_by_token's registers left four.
 template <int KB, int W, int TERMS>
-__global__ __launch_bounds__(64 * W, KB <= 4 ? W / 2 : W / 4) void lin_mfma_states_kernel(LinScan a, LinScan b, long na) {
+__global__ __launch_bounds__(64 * W, KB <= 2 ? 5 : KB <= 4 ? 4 : W / 4) void lin_mfma_states_kernel(LinScan a, LinScan b, long na) {
   if ((long)blockIdx.x < na) lin_mfma<KB, W, TERMS, true>(a, 0, blockIdx.x, na);
   else lin_mfma<KB, W, TERMS, true>(b, 1, blockIdx.x - na, gridDim.x - na);
 }

@@ -52,6 +52,24 @@ def test_forwards(shape, value, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_backwards(shape, value, dtype):
+    """dk, dv and the initial state's gradient, carried from the last token to the first."""
+    T, H, Hk, dk, dv, cu = shape
+    kind, state = ("bf16", "state") if dtype == BF else ("fp32", "fp32")
+    n = max(dk, dv) * (H // Hk)
+    for name, tokens in PLACES:
+        d, x, ld, cut = inputs(shape, value, dtype, name, tokens)
+        g = ssd.lin_attn_bwd(d["q"], d["k"], d["v"], ld.cuda(), d["do"], cu_seqlens=cut, scale=0.25, initial_state=d["init"],
+                             dfinal_state=d["dfinal"], want_dinit=True)
+        want, E = ref.attention_bwd(x["q"], x["k"], x["v"], n64(ld), 0.25, x["do"], x["init"], x["dfinal"], cu)
+        for out in ("dk", "dv"):
+            hold(g[out], want[out], E[out], kind, T, n, f"{name} {out}")
+        hold(g["dinit"], want["dinit"], E["dinit"], state, T, n, f"{name} dinit", infinite=True)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_sequences_without_tokens(dtype):
     """What is not finite in their states stays, and reaches no neighbour."""
     cu = [0, 0, 70, 70, 130, 130]
@@ -62,3 +80,8 @@ def test_sequences_without_tokens(dtype):
     for s in (0, 2, 4):
         assert torch.equal(fin[s].view(torch.int32), d["init"][s].view(torch.int32))
     assert torch.all(torch.isfinite(o)) and torch.all(torch.isfinite(fin[[1, 3]]))
+    g = ssd.lin_attn_bwd(d["q"], d["k"], d["v"], decays(2).cuda(), d["do"], cu_seqlens=cut, initial_state=d["init"],
+                         dfinal_state=d["init"], want_dinit=True)
+    for s in (0, 2, 4):
+        assert torch.equal(g["dinit"][s].isfinite(), d["init"][s].isfinite())
+    assert all(torch.all(torch.isfinite(g[n])) for n in ("dq", "dk", "dv")) and torch.all(torch.isfinite(g["dinit"][[1, 3]]))
