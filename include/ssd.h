@@ -466,8 +466,10 @@ ssd_status ssd_step_mamba2(float* state, const void* x, const float* dt, const f
  * those results not finite that the formulas bring it to, and leaves every
  * other as it is, in gradients too. (bf16: a call with such values takes some
  * ten times as long, as their blocks are walked token by token.)
- * No output may overlap an input: a state is continued into another tensor (the
- * step alone updates in place).
+ * An output that shares memory with an input, another output or the workspace
+ * is refused (SSD_ERR_INVALID_ARGUMENT), as blocks read the one while others
+ * write the other: a state is continued into another tensor (the step alone
+ * updates in place).
  * SSD_ERR_UNSUPPORTED, here as for the norm, also where a launch would need
  * 2^32 threads or more (65535 one-token sequences of 256 heads).
  * ------------------------------------------------------------------------- */
@@ -539,8 +541,9 @@ ssd_status ssd_lin_attn_step(float* state, const void* q, const void* k, const v
  *   NULL exactly when gate is none; stats [samples][groups][2] fp32: mean (0
  *   when not centred) and 1 / sqrt(var + eps), may be NULL in the forward call
  *   and is what the backward call needs of it. eps > 0. dweight and dbias
- *   [channels] fp32, each may be NULL. Sums are fixed in order: results repeat
- *   bit for bit.
+ *   [channels] fp32, each may be NULL. y, dx and dz may be an input of the same
+ *   contiguous rows (x, z, dy); a partial overlap is refused. Sums are fixed in
+ *   order: results repeat bit for bit.
  * ------------------------------------------------------------------------- */
 typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1 } ssd_act;
 typedef enum { SSD_GATE_NONE = 0, SSD_GATE_AFTER = 1, SSD_GATE_BEFORE = 2 } ssd_gate;

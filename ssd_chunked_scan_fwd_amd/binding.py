@@ -752,6 +752,12 @@ def _room(size: int, workspace, device):
     return (torch.empty(size, dtype=torch.uint8, device=device) if size else None), size
 
 
+def _share(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two contiguous tensors share memory."""
+    return (a.data_ptr() < b.data_ptr() + b.numel() * b.element_size() and
+            b.data_ptr() < a.data_ptr() + a.numel() * a.element_size())
+
+
 def _lin_values(shape: LinShape):
     return (shape.batch, shape.seqlen, shape.nheads, shape.nkv_heads, shape.dk, shape.dv, shape.num_seqs, shape.dtype,
             shape.q_row, shape.k_row, shape.v_row)
@@ -801,8 +807,8 @@ def lin_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
                       (final_state, "final_state", st, torch.float32, 16),
                       (log_decay, "log_decay", (H,), torch.float32, 4), (cu_seqlens, "cu_seqlens", None, torch.int32, 4),
                       (workspace, "workspace", None, torch.uint8, 256)))
-    if final_state is not None and initial_state is not None and final_state.data_ptr() == initial_state.data_ptr():
-        raise ValueError("final_state must not be initial_state: blocks of a prompt read the one while others write the other")
+    if final_state is not None and initial_state is not None and _share(final_state, initial_state):
+        raise ValueError("final_state must not overlap initial_state: blocks of a prompt read the one while others write the other")
     workspace, have = _lin_workspace("ssd_lin_attn_workspace_bytes", shape, workspace, q.device)
     if o is None:
         o = torch.empty(b, T, H, Dv, dtype=q.dtype, device=q.device)

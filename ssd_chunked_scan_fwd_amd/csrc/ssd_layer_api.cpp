@@ -5,9 +5,11 @@
 // or thrown.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "ssd.h"
 #include "ssd_layer.h"
@@ -19,6 +21,33 @@ ssd_status hip_status(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 bool scale_ok(float s) { return std::isnormal(s); }  // its reciprocal is taken
+
+// Rows of `width` bytes, `pitch` bytes apart; a null base has none.
+struct Span {
+  const void* base;
+  int64_t rows, pitch, width;
+};
+Span whole(const void* p, int64_t bytes) { return Span{p, 1, bytes, bytes}; }
+// Whether a, one row, and b share a byte.
+bool meet(const Span& a, const Span& b) {
+  if (!a.base || !b.base || a.width < 1 || b.width < 1 || b.rows < 1) return false;
+  const intptr_t at = (intptr_t)a.base - (intptr_t)b.base, end = at + a.width;   // a, from b's first row on
+  if (end <= 0) return false;
+  // the first of b's rows that ends behind a's start
+  const int64_t first = at < b.width ? 0 : (at - b.width) / b.pitch + 1;
+  return first < b.rows && first * b.pitch < end;
+}
+// Whether one of the outputs shares memory with an input or another output: kernels
+// read the one while others write the other.
+bool overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (meet(*o, i)) return true;
+    for (const Span* p = outs.begin(); p != o; ++p)
+      if (meet(*o, *p)) return true;
+  }
+  return false;
+}
 
 // ---------------------------------------------------------------- linear attention
 
@@ -61,6 +90,23 @@ ssd_status check_lin(const ssd_lin_shape* s, LinDims* d) {
   d->nseq = s->num_seqs > 0 ? s->num_seqs : s->batch;
   return SSD_OK;
 }
+
+// The memory of a call's tensors.
+struct LinSpans {
+  const ssd_lin_shape* s;
+  LinDims d;
+  LinSpans(const ssd_lin_shape* shape, const LinDims& dims) : s(shape), d(dims) {}
+  Span rows(const void* p, int64_t row, int64_t heads, int64_t size) const {
+    return Span{p, d.tokens, row * d.esz, heads * size * d.esz};
+  }
+  Span q(const void* p) const { return rows(p, d.q_row, s->nheads, s->dk); }
+  Span k(const void* p) const { return rows(p, d.k_row, s->nkv_heads, s->dk); }
+  Span v(const void* p) const { return rows(p, d.v_row, s->nkv_heads, s->dv); }
+  Span queries(const void* p) const { return whole(p, d.tokens * s->nheads * s->dk * d.esz); }
+  Span values(const void* p) const { return whole(p, d.tokens * s->nheads * s->dv * d.esz); }
+  Span keys(const void* p, int64_t size) const { return whole(p, d.tokens * s->nkv_heads * size * d.esz); }
+  Span state(const void* p) const { return whole(p, d.nseq * s->nheads * s->dk * s->dv * 4); }
+};
 
 // The blocks of one scan with contraction size dk and value size dv.
 struct LinPlan {
@@ -182,6 +228,14 @@ ssd_status norm_align(ssd::NormArgs* a) {
   return SSD_OK;
 }
 
+// An output of contiguous rows over an input: they may be the same rows, which a
+// thread reads before it writes them, or lie apart.
+bool norm_apart(const ssd::NormArgs& a, const void* out, const void* in, long in_row) {
+  const int64_t esz = a.bf16 ? 2 : 4, rows = a.n * a.s;
+  if (out == in && in_row == a.C) return true;
+  return !meet(whole(out, rows * a.C * esz), Span{in, rows, std::min<int64_t>(in_row, INT64_MAX / 32) * esz, a.C * esz});
+}
+
 ssd_status check_pages(const ssd_pages_shape* s) {
   if (!s) return SSD_ERR_INVALID_ARGUMENT;
   if (s->layers < 1 || s->slots < 1 || s->page_bytes < 1) return SSD_ERR_INVALID_ARGUMENT;
@@ -224,10 +278,12 @@ ssd_status ssd_lin_attn_fwd(const void* q, const void* k, const void* v, const f
   if ((cu_seqlens != nullptr) != (shape->num_seqs > 0)) return SSD_ERR_INVALID_ARGUMENT;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(initial_state) || !aligned16(final_state))
     return SSD_ERR_INVALID_ARGUMENT;
-  // the last block's state may be written before the first block has read the initial one
-  if (final_state && final_state == initial_state) return SSD_ERR_INVALID_ARGUMENT;
   if ((st = lin_plan(shape, shape->dk, shape->dv, &p)) != SSD_OK) return st;
   if ((st = check_ws(workspace, workspace_bytes, p.state_bytes)) != SSD_OK) return st;
+  const LinSpans t(shape, d);
+  if (overlap({t.values(o), t.state(final_state), whole(workspace, p.state_bytes)},
+              {t.q(q), t.k(k), t.v(v), t.state(initial_state)}))
+    return SSD_ERR_INVALID_ARGUMENT;
   const int rep = shape->nheads / shape->nkv_heads;
   ssd::LinScan a = base_scan(shape, log_decay, cu_seqlens, scale);
   a.q = {q, (long)d.q_row, 1};
@@ -264,9 +320,12 @@ ssd_status ssd_lin_attn_bwd(const void* q, const void* k, const void* v, const f
   for (const void* t : {q, k, v, d_o, (const void*)initial_state, (const void*)dfinal_state, (const void*)dq, (const void*)dk,
                         (const void*)dv, (const void*)dinitial_state})
     if (!aligned16(t)) return SSD_ERR_INVALID_ARGUMENT;
-  if (dinitial_state && (dinitial_state == dfinal_state || dinitial_state == initial_state)) return SSD_ERR_INVALID_ARGUMENT;
   if ((st = lin_bwd_layout(shape, &L)) != SSD_OK) return st;
   if ((st = check_ws(workspace, workspace_bytes, L.total)) != SSD_OK) return st;
+  const LinSpans t(shape, d);
+  if (overlap({t.queries(dq), t.keys(dk, shape->dk), t.keys(dv, shape->dv), t.state(dinitial_state), whole(workspace, L.total)},
+              {t.q(q), t.k(k), t.v(v), t.values(d_o), t.state(initial_state), t.state(dfinal_state)}))
+    return SSD_ERR_INVALID_ARGUMENT;
   char* ws = static_cast<char*>(workspace);
   hipStream_t hs = (hipStream_t)stream;
   const int H = shape->nheads, Hk = shape->nkv_heads, rep = H / Hk;
@@ -348,6 +407,12 @@ ssd_status ssd_lin_attn_step(float* state, const void* q, const void* k, const v
   if (!state || !q || !k || !v || !log_decay || !o || !scale_ok(scale)) return SSD_ERR_INVALID_ARGUMENT;
   if (num_slots < 1 || (!slots && num_slots < shape->batch)) return SSD_ERR_INVALID_ARGUMENT;
   if (!aligned16(state) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return SSD_ERR_INVALID_ARGUMENT;
+  const int64_t esz = shape->dtype == SSD_DTYPE_BF16 ? 2 : 4, heads = shape->nheads, keys = shape->nkv_heads;
+  const auto entries = [&](const void* p, int64_t values) { return whole(p, shape->batch * values * esz); };
+  const int64_t slot = heads * shape->dk * shape->dv * 4;
+  if (overlap({entries(o, heads * shape->dv), whole(state, std::min<int64_t>(num_slots, INT64_MAX / 8 / slot) * slot)},
+              {entries(q, heads * shape->dk), entries(k, keys * shape->dk), entries(v, keys * shape->dv)}))
+    return SSD_ERR_INVALID_ARGUMENT;
   ssd::LinStep a;
   a.state = state;
   a.q = q;
@@ -394,6 +459,7 @@ ssd_status ssd_group_norm(const void* x, const void* z, const float* weight, con
   size_t need = 0;
   ssd_group_norm_workspace_bytes(shape, 0, &need);
   if ((st = check_ws(workspace, workspace_bytes, need)) != SSD_OK) return st;
+  if (!norm_apart(a, y, x, a.x_row) || !norm_apart(a, y, z, a.z_row)) return SSD_ERR_INVALID_ARGUMENT;
   a.ws = static_cast<float*>(workspace);
   return hip_status(ssd::launch_group_norm(a, (hipStream_t)stream));
 }
@@ -421,6 +487,11 @@ ssd_status ssd_group_norm_bwd(const void* x, const void* z, const float* weight,
   size_t need = 0;
   ssd_group_norm_workspace_bytes(shape, 1, &need);
   if ((st = check_ws(workspace, workspace_bytes, need)) != SSD_OK) return st;
+  for (const void* out : {(const void*)dx, (const void*)dz})
+    if (!norm_apart(a, out, x, a.x_row) || !norm_apart(a, out, z, a.z_row) || !norm_apart(a, out, dy, a.C))
+      return SSD_ERR_INVALID_ARGUMENT;
+  if (overlap({whole(dx, a.n * a.s * a.C * (a.bf16 ? 2 : 4))}, {whole(dz, a.n * a.s * a.C * (a.bf16 ? 2 : 4))}))
+    return SSD_ERR_INVALID_ARGUMENT;
   a.ws = static_cast<float*>(workspace);
   return hip_status(ssd::launch_group_norm_bwd(a, (hipStream_t)stream));
 }
