@@ -105,6 +105,8 @@ struct LinSpans {
   Span queries(const void* p) const { return whole(p, d.tokens * s->nheads * s->dk * d.esz); }
   Span values(const void* p) const { return whole(p, d.tokens * s->nheads * s->dv * d.esz); }
   Span keys(const void* p, int64_t size) const { return whole(p, d.tokens * s->nkv_heads * size * d.esz); }
+  Span decays(const void* p) const { return whole(p, s->nheads * 4); }
+  Span starts(const void* p) const { return whole(p, (d.nseq + 1) * 4); }
   Span state(const void* p) const { return whole(p, d.nseq * s->nheads * s->dk * s->dv * 4); }
 };
 
@@ -282,7 +284,7 @@ ssd_status ssd_lin_attn_fwd(const void* q, const void* k, const void* v, const f
   if ((st = check_ws(workspace, workspace_bytes, p.state_bytes)) != SSD_OK) return st;
   const LinSpans t(shape, d);
   if (overlap({t.values(o), t.state(final_state), whole(workspace, p.state_bytes)},
-              {t.q(q), t.k(k), t.v(v), t.state(initial_state)}))
+              {t.q(q), t.k(k), t.v(v), t.state(initial_state), t.decays(log_decay), t.starts(cu_seqlens)}))
     return SSD_ERR_INVALID_ARGUMENT;
   const int rep = shape->nheads / shape->nkv_heads;
   ssd::LinScan a = base_scan(shape, log_decay, cu_seqlens, scale);
@@ -324,7 +326,8 @@ ssd_status ssd_lin_attn_bwd(const void* q, const void* k, const void* v, const f
   if ((st = check_ws(workspace, workspace_bytes, L.total)) != SSD_OK) return st;
   const LinSpans t(shape, d);
   if (overlap({t.queries(dq), t.keys(dk, shape->dk), t.keys(dv, shape->dv), t.state(dinitial_state), whole(workspace, L.total)},
-              {t.q(q), t.k(k), t.v(v), t.values(d_o), t.state(initial_state), t.state(dfinal_state)}))
+              {t.q(q), t.k(k), t.v(v), t.values(d_o), t.state(initial_state), t.state(dfinal_state), t.decays(log_decay),
+               t.starts(cu_seqlens)}))
     return SSD_ERR_INVALID_ARGUMENT;
   char* ws = static_cast<char*>(workspace);
   hipStream_t hs = (hipStream_t)stream;
@@ -411,7 +414,8 @@ ssd_status ssd_lin_attn_step(float* state, const void* q, const void* k, const v
   const auto entries = [&](const void* p, int64_t values) { return whole(p, shape->batch * values * esz); };
   const int64_t slot = heads * shape->dk * shape->dv * 4;
   if (overlap({entries(o, heads * shape->dv), whole(state, std::min<int64_t>(num_slots, INT64_MAX / 8 / slot) * slot)},
-              {entries(q, heads * shape->dk), entries(k, keys * shape->dk), entries(v, keys * shape->dv)}))
+              {entries(q, heads * shape->dk), entries(k, keys * shape->dk), entries(v, keys * shape->dv),
+               whole(log_decay, heads * 4), whole(slots, shape->batch * 4)}))
     return SSD_ERR_INVALID_ARGUMENT;
   ssd::LinStep a;
   a.state = state;

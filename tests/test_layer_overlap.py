@@ -57,7 +57,7 @@ def test_outputs_over_inputs():
     _, need = lin_bytes(sh)
     base = 1 << 40
     rows = dict(q=ptr(base), k=ptr(base + 256), v=ptr(base + 512))     # one projection's rows of 768 bytes
-    for o in (base, base + 512, base + 4095 * 768, base - 16):
+    for o in (base, base + 512, base + 4095 * 768, base - 16, 64 * MB * 4):   # the last: over log_decay
         assert ssd.lib().ssd_lin_attn_fwd(*fwd_args(sh, need, o=ptr(o), **rows)) == INVALID
     for ws in (base + 768, 64 * MB * 8):
         assert ssd.lib().ssd_lin_attn_fwd(*fwd_args(sh, need, ws=ptr(ws), **rows)) == INVALID
@@ -72,7 +72,7 @@ def test_step():
     sh = lin(batch=4)
     # state, q, k, v, ld, slots, num_slots, scale, o, shape, stream
     far = [ptr(64 * MB * (i + 1)) for i in range(9)]
-    for i in (0, 1, 2, 3):
+    for i in (0, 1, 2, 3, 4, 5):
         a = far[:6] + [4, 1.0, far[i], ctypes.byref(sh), None]
         assert ssd.lib().ssd_lin_attn_step(*a) == INVALID, i
     a = far[:6] + [4, 1.0, ptr(64 * MB + 4 * 8 * 64 * 64 * 4 - 16), ctypes.byref(sh), None]   # inside the last slot
