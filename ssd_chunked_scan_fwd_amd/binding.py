@@ -649,6 +649,8 @@ def _token_row(t: torch.Tensor, name: str) -> int:
     st = t.stride()
     if (D > 1 and st[3] != 1) or (H > 1 and st[2] != D):
         raise ValueError(f"{name} must have its heads contiguous (strides {st})")
+    if t.numel() == 0:
+        return H * D
     row = st[1] if T > 1 else (st[0] if b > 1 else H * D)
     if row < H * D or (b > 1 and st[0] != T * row):
         raise ValueError(f"{name} must have its tokens at one distance (strides {st})")
@@ -670,7 +672,7 @@ def _expect_device(specs, device, align: int = 16):
             raise ValueError(f"{name} must be {align}-byte aligned")
 
 
-def _lin_shape(q, k, v, log_decay, cu_seqlens):
+def _lin_shape(q, k, v, cu_seqlens):
     """The shape of a call over prompts, its tensors checked against one another
     (their devices and alignment come after, with the outputs')."""
     _check_dtype(q, "q", "[batch, seqlen, nheads, dk]", 4)
@@ -693,7 +695,8 @@ def _lin_shape(q, k, v, log_decay, cu_seqlens):
             raise ValueError("packed sequences (cu_seqlens) need batch 1")
         S = cu_seqlens.numel() - 1
     _int32(dict(batch=b, seqlen=T, nheads=H, dk=Dk, dv=v.shape[3], num_seqs=S))
-    return _lin_struct(b, T, H, Hk, Dk, v.shape[3], S, _dtype_code(q.dtype), _token_row(q, "q"), _token_row(k, "k"),
+    # A batch without tokens runs nothing: its heads and sizes are checked as those of one token.
+    return _lin_struct(max(b, 1), max(T, 1), H, Hk, Dk, v.shape[3], S, _dtype_code(q.dtype), _token_row(q, "q"), _token_row(k, "k"),
                        _token_row(v, "v"))
 
 
@@ -758,6 +761,21 @@ def _share(a: torch.Tensor, b: torch.Tensor) -> bool:
             b.data_ptr() < a.data_ptr() + a.numel() * a.element_size())
 
 
+def _check_scale(scale: float):
+    """As the C ABI does, to which a batch without tokens does not get."""
+    if not 2.0 ** -126 <= abs(scale) < 2.0 ** 128:
+        raise ValueError(f"scale {scale} must be a normal fp32 number, not 0")
+
+
+def _state_of_no_tokens(state: Optional[torch.Tensor], out: Optional[torch.Tensor], want: bool, shape, device):
+    """What a batch without tokens makes of a state: the state itself, or zeros."""
+    if out is None and want:
+        out = torch.empty(shape, dtype=torch.float32, device=device)
+    if out is not None:
+        out.copy_(state) if state is not None else out.zero_()
+    return out
+
+
 def _lin_values(shape: LinShape):
     return (shape.batch, shape.seqlen, shape.nheads, shape.nkv_heads, shape.dk, shape.dv, shape.num_seqs, shape.dtype,
             shape.q_row, shape.k_row, shape.v_row)
@@ -769,7 +787,7 @@ def _lin_workspace(fn: str, shape: LinShape, workspace, device):
 
 def lin_attn_shape(q, k, v, cu_seqlens=None) -> LinShape:
     """The shape of a call with these tensors (for lin_attn_workspace_bytes)."""
-    return LinShape(*_lin_values(_lin_shape(q, k, v, None, cu_seqlens)))   # the caller's own
+    return LinShape(*_lin_values(_lin_shape(q, k, v, cu_seqlens)))   # the caller's own
 
 
 def lin_attn_workspace_bytes(shape: LinShape) -> int:
@@ -793,10 +811,11 @@ def lin_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
 
     q [b, T, H, dk], k [b, T, Hk, dk], v [b, T, Hk, dv] (bf16 or fp32; tokens may lie
     in wider rows, as slices of one projection do), log_decay [H] fp32 <= 0, states
-    fp32 [rows or sequences, H, dv, dk]. cu_seqlens may hold empty sequences; rows
+    fp32 [rows or sequences, H, dv, dk]. cu_seqlens may hold empty sequences, and a
+    batch no rows or tokens at all (its final states are the initial ones); rows
     of o that belong to no sequence are left as they were (undefined in an o made here).
     """
-    shape = _lin_shape(q, k, v, log_decay, cu_seqlens)
+    shape = _lin_shape(q, k, v, cu_seqlens)
     b, T, H, Dk = q.shape
     Dv, nseq = v.shape[3], shape.num_seqs or b
     if log_decay is None:
@@ -812,6 +831,9 @@ def lin_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
     workspace, have = _lin_workspace("ssd_lin_attn_workspace_bytes", shape, workspace, q.device)
     if o is None:
         o = torch.empty(b, T, H, Dv, dtype=q.dtype, device=q.device)
+    if b * T == 0:
+        _check_scale(scale)
+        return o, _state_of_no_tokens(initial_state, final_state, want_final, st, q.device)
     if final_state is None and want_final:
         final_state = torch.empty(st, dtype=torch.float32, device=q.device)
     _call_on(q.device, "ssd_lin_attn_fwd", _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(cu_seqlens), float(scale),
@@ -826,7 +848,7 @@ def lin_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
     """Gradients of <do, o> + <dfinal_state, final_state> of lin_attn_fwd with these
     inputs (ssd_lin_attn_bwd). Returns dict(dq, dk, dv, dinit or None); log_decay is
     a constant of the layer. Rows that belong to no sequence are undefined."""
-    shape = _lin_shape(q, k, v, log_decay, cu_seqlens)
+    shape = _lin_shape(q, k, v, cu_seqlens)
     b, T, H, Dk = q.shape
     Dv, nseq = v.shape[3], shape.num_seqs or b
     if log_decay is None or do is None:
@@ -841,6 +863,10 @@ def lin_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: t
     out = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=q.device), dk=torch.empty(k.shape, dtype=q.dtype, device=q.device),
                dv=torch.empty(v.shape, dtype=q.dtype, device=q.device),
                dinit=torch.empty(st, dtype=torch.float32, device=q.device) if want_dinit else None)
+    if b * T == 0:
+        _check_scale(scale)
+        _state_of_no_tokens(dfinal_state, out["dinit"], want_dinit, st, q.device)
+        return out
     _call_on(q.device, "ssd_lin_attn_bwd", _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(cu_seqlens), float(scale),
              _addr(initial_state), _addr(do), _addr(dfinal_state), _addr(out["dq"]), _addr(out["dk"]), _addr(out["dv"]),
              _addr(out["dinit"]), ctypes.byref(shape), _addr(workspace), have)
@@ -855,7 +881,7 @@ def lin_attn_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
 
     q [b, H, dk], k [b, Hk, dk], v [b, Hk, dv]; slots int32 [b]: the state each entry
     uses (None: entry i uses state i). Slots outside the pool are padding (o = 0);
-    entries that name one slot are taken in the order of the batch.
+    entries that name one slot are taken in the order of the batch; there may be none.
     """
     _check_dtype(q, "q", "[batch, nheads, dk]", 3)
     b, H, Dk = q.shape
@@ -881,6 +907,10 @@ def lin_attn_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
                     (log_decay, "log_decay", (H,), torch.float32, 4), (slots, "slots", (b,), torch.int32, 4)))
     if o is None:
         o = torch.empty((b, H, Dv), dtype=dtype, device=device)
+    if b == 0:
+        _check_scale(scale)
+        _size_of("ssd_lin_attn_workspace_bytes", LinShape, (1, 1, H, Hk, Dk, Dv, 0, _dtype_code(dtype), 0, 0, 0))   # its sizes
+        return o
     shape = _lin_struct(b, 1, H, Hk, Dk, Dv, 0, _dtype_code(dtype), 0, 0, 0)
     _call_on(device, "ssd_lin_attn_step", _addr(state), _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(slots), n,
              float(scale), _addr(o), ctypes.byref(shape))
@@ -935,7 +965,8 @@ def _norm_shape(x, groups, z, act, gate, center) -> NormShape:
     for d in x.shape[1:-1]:
         positions *= d
     _int32(dict(samples=x.shape[0], positions=positions, channels=C))
-    return NormShape(x.shape[0], positions, C, int(groups), _row_pitch(x, "x"), 0 if z is None else _row_pitch(z, "z"),
+    # No samples: nothing is run, and the rest is checked as for one.
+    return NormShape(max(x.shape[0], 1), positions, C, int(groups), _row_pitch(x, "x"), 0 if z is None else _row_pitch(z, "z"),
                      _dtype_code(x.dtype), _ACTS[act], 0 if z is None else _GATES[gate], 1 if center else 0)
 
 
@@ -956,10 +987,11 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
     with z, gate "after" multiplies y by silu(z), "before" the input. weight and
     bias are fp32 [channels]; center=False takes the root mean square. x and z may
     have rows in wider rows. stats [samples, groups, 2] fp32 are the mean and
-    1 / sqrt(var + eps) that group_norm_bwd takes.
+    1 / sqrt(var + eps) that group_norm_bwd takes. There may be no samples.
     """
     shape = _norm_shape(x, groups, z, act, gate, center)
-    C, st = shape.channels, (shape.samples, shape.groups, 2)
+    n, C = x.shape[0], shape.channels
+    st = (n, shape.groups, 2)
     e = x.element_size()
     _check(x.device, ((x, "x", None, None, e), (z, "z", None, None, e), (weight, "weight", (C,), torch.float32, e),
                       (bias, "bias", (C,), torch.float32, e), (y, "y", x.shape, x.dtype, e),
@@ -969,6 +1001,10 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if stats is None and want_stats:
         stats = torch.empty(st, dtype=torch.float32, device=x.device)
+    if n == 0:
+        if not 0.0 < eps < float("inf"):
+            raise ValueError(f"eps {eps} must be above 0")
+        return y, stats
     _call_on(x.device, "ssd_group_norm", _addr(x), _addr(z), _addr(weight), _addr(bias), float(eps), _addr(y), _addr(stats),
              ctypes.byref(shape), _addr(workspace), have)
     return y, stats
@@ -982,7 +1018,8 @@ def group_norm_bwd(x: torch.Tensor, groups: int, stats: torch.Tensor, dy: torch.
     (ssd_group_norm_bwd). Returns dict(dx, dz, dweight, dbias), dz, dweight and
     dbias None where z, weight or bias is."""
     shape = _norm_shape(x, groups, z, act, gate, center)
-    C, st = shape.channels, (shape.samples, shape.groups, 2)
+    n, C = x.shape[0], shape.channels
+    st = (n, shape.groups, 2)
     if stats is None or dy is None:
         raise ValueError("stats and dy are required")
     e = x.element_size()
@@ -994,6 +1031,11 @@ def group_norm_bwd(x: torch.Tensor, groups: int, stats: torch.Tensor, dy: torch.
                dz=None if z is None else torch.empty(x.shape, dtype=x.dtype, device=x.device),
                dweight=None if weight is None else torch.empty(C, dtype=torch.float32, device=x.device),
                dbias=None if bias is None else torch.empty(C, dtype=torch.float32, device=x.device))
+    if n == 0:
+        for name in ("dweight", "dbias"):
+            if out[name] is not None:
+                out[name].zero_()
+        return out
     _call_on(x.device, "ssd_group_norm_bwd", _addr(x), _addr(z), _addr(weight), _addr(bias), _addr(stats), _addr(dy),
              _addr(out["dx"]), _addr(out["dz"]), _addr(out["dweight"]), _addr(out["dbias"]), ctypes.byref(shape),
              _addr(workspace), have)
