@@ -184,7 +184,14 @@ __device__ __forceinline__ void lin_pass(const LinScan& a, int s) {
       D = *reinterpret_cast<const f32x4*>(src + e) * a.init_scale;
     }
   }
-  const float w0 = (float)lin_power(a.ld[h], a.L - (a.rev ? 1 : 0)), w = (float)lin_power(a.ld[h], a.L);
+  // A block's decay is at least the smallest normal number, unless the head remembers nothing: an infinity
+  // times a power that fp32 rounds to 0 would be a NaN.
+  const float ld = a.ld[h], least = ld == -INFINITY ? 0.f : 0x1p-126f;
+  auto decay = [&](int tokens) {
+    const float w = (float)lin_power(ld, tokens);
+    return w < least ? least : w;
+  };
+  const float w0 = decay(a.L - (a.rev ? 1 : 0)), w = decay(a.L);
   const long step = (long)a.H * mat;
   float* at = a.states + (slot0 * a.H + h) * mat + e;
   constexpr int kAhead = 8;

@@ -103,3 +103,25 @@ def test_in_a_step():
         o = ssd.lin_attn_step(state, d["q"][:, t], d["k"][:, t], d["v"][:, t], ld.cuda())
         hold(o, want["o"][:, t], E["o"][:, t], "fp32", 5, dk, f"o {t}")
     hold(state, want["final"], E["final"], "fp32", 5, dk, "state", infinite=True)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_over_blocks(dtype):
+    """A prompt cut into blocks, whose whole decay is below what fp32 holds: what is infinite at its start, or its end,
+    is so at the other. The last head remembers nothing: its infinity times 0 is no number."""
+    T, H, dk, dv = 900, 4, 32, 48
+    ld = torch.tensor([-0.5, -2.0, -30.0, -INF], dtype=F32)
+    d = make(T, H, H, dk, dv, dtype, 11)
+    sh = ssd.lin_attn_shape(d["q"], d["k"], d["v"])
+    assert ssd.lin_attn_workspace_bytes(sh) >= 4 * H * dk * dv * 4
+    d["init"][:, :, 3, 7] = INF
+    d["dfinal"][:, :, 4, 6] = -INF
+    o, fin = ssd.lin_attn_fwd(d["q"], d["k"], d["v"], ld.cuda(), scale=0.25, initial_state=d["init"])
+    g = ssd.lin_attn_bwd(d["q"], d["k"], d["v"], ld.cuda(), d["do"], scale=0.25, initial_state=d["init"],
+                         dfinal_state=d["dfinal"], want_dinit=True)
+    x = {n: n64(t) for n, t in d.items()}
+    want, E = ref.attention(x["q"], x["k"], x["v"], n64(ld), 0.25, x["init"])
+    gw, gE = ref.attention_bwd(x["q"], x["k"], x["v"], n64(ld), 0.25, x["do"], x["init"], x["dfinal"])
+    state = "state" if dtype == BF else "fp32"
+    hold(fin, want["final"], E["final"], state, T, dk, "final", infinite=True)
+    hold(g["dinit"], gw["dinit"], gE["dinit"], state, T, dv, "dinit", infinite=True)
