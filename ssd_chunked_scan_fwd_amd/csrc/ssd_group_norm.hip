@@ -17,9 +17,13 @@
 // bits; nothing subtracts two large sums.
 //
 // 16384 tokens of 32 gated groups of 128: 85 us for 403 MB, 4.7 TB/s; backwards,
-// 8192 tokens of 5120 gated channels: 82 us for 420 MB, 5.1 TB/s; 8 samples of
-// 2256 positions, 320 channels, 23 MB (in cache): 21 us, of which launches and
-// their gaps are half.
+// 8192 tokens of 5120 gated channels: 82 us for 420 MB, 5.1 TB/s. 8 samples of
+// 2256 positions, 320 channels, 23 MB (in cache): 7 + 4 + 10 us of three launches,
+// 21 a call, 35 backwards; the 376 workgroups of 256 threads of the first and the
+// third hide little of each other's waits. Groups that are no whole pieces of
+// eight channels are read channel by channel: 16384 tokens of 32 groups of 10, 21
+// MB, 47 us, of 70, 147 MB, 404 us. Groups beyond the registers take the slabs with
+// one row each: 4096 tokens of 10240 channels, 168 MB, 652 us.
 #include <type_traits>
 
 #include "ssd_device.h"

@@ -22,8 +22,9 @@ __device__ __forceinline__ float load_el(const void* p, long i) {
 // (LinDecay), one for the product and one for the output.
 // STATE_ONLY leaves each block's own sum (from a zero state) in a.states;
 // the other form starts from the block's entering state and writes o. 256 tokens
-// of 2 heads of 16 x 16: 8 + 2 + 16 us of three launches, 25 us a call (442 in
-// plain operations).
+// of 2 heads of 16 x 16: 8 + 3 + 16 us of three launches, 26 us a call (442 in
+// plain operations). 16384 tokens of 32 heads of 128 x 128: 2300 us, the chain of
+// 4096 tokens a block; backwards, 8192 tokens, three such scans, 3300.
 // ----------------------------------------------------------------------------
 constexpr int kRecRows = 16, kRecTok = 16, kC64 = 64;
 
@@ -358,7 +359,11 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStep a, int tpr, int p
 // do not fit at once cost a whole further round. So the number of blocks a
 // sequence (of mean length, where packed) is the one of least cost, counted in
 // chunks of 64 tokens: rounds of (chunks + start-up) each, times 1.45 for the
-// blocks' own sums, plus the passing launch and the states' bytes.
+// blocks' own sums, plus the passing launch and the states' bytes. The times of a
+// chunk were measured for heads of 128 x 128 and of 64 x 64. The host does not know
+// the lengths of packed sequences: one long sequence among many short ones, whose
+// mean needs no cut, is one block (16384 tokens and 15 single ones, 32 heads of 128
+// x 128: 1060 us, the long one alone 210).
 int lin_block_tokens(int batch, int T, int S, int H, int dk, int dv, int bf16, bool kv) {
   const long seqs = S > 0 ? S : batch;
   const int tile = kv ? dv : bf16 ? lin_mfma_tile(dv) : kRecRows;

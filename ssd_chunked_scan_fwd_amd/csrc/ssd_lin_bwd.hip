@@ -16,8 +16,9 @@
 // one half of the key columns and of dV one half of the chunk's tokens; dK's
 // blocks of 16 key columns by 16 tokens are dealt over the waves.
 //
-// T = 8192, 32 heads of 128 x 128: 110 - 122 us for 417 MB (3.4 - 3.8 TB/s), 254
-// us a backward call (own sums of both scans 71, entering states 18, dQ 68); the
+// T = 8192, 32 heads of 128 x 128: mean 127 us, least 111, for 417 MB (3.3 and 3.8
+// TB/s), 254 - 258 us a backward call (own sums of both scans 73, entering states
+// 18, dQ 73); the
 // one scan in place of two took such a call from 347 to 295 us. Heads of more
 // than 128 take two scans: R and its bf16 copy would not fit. It is bound by its
 // phases between barriers in the one workgroup that a CU holds (matrix pipes 20 %

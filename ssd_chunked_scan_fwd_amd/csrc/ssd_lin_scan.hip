@@ -23,12 +23,14 @@
 // A chunk moves C (2 dk + 2 dv) 2 bytes, reads of k and v by the blocks' own sums
 // apart, and makes 2 C (C + 3 dk) dv multiplies (the doubled state product
 // included). The next chunk's rows are in flight in registers while this one is
-// computed. T = 16384, 32 heads of 128 x 128, 16 blocks a head: own sums 57 us for
-// 283 MB (5.0 TB/s, the rate of a copy), entering states 13, this scan 125 - 133
-// for 571 MB (4.3 - 4.6 TB/s), 205 us a call. Memory bounds the sums, and with the
-// chain scores - barrier - outputs - state of each chunk (four waves a SIMD, all
-// that registers allow) the scan: without its loads it takes 106 us, with matrix
-// pipes busy a third of the time and LDS 40 %.
+// computed. T = 16384, 32 heads of 128 x 128, 16 blocks a head: 200 - 213 us a call.
+// Under the trace, which lengthens them, means of 19 and the least: own sums 70 us
+// and 58 for 283 MB (4.1 and 4.9 TB/s; a copy reaches 4.9), entering states 13.5,
+// this scan 149 and 125 for 571 MB (3.8 and 4.6 TB/s). Memory bounds the sums, and
+// with the chain scores - barrier - outputs - state of each chunk (four waves a
+// SIMD, all that registers allow) the scan: without its loads it took 106 us, with
+// matrix pipes busy a third of the time and LDS 40 %. Heads of 256 x 256 (T 4096, 16
+// heads) leave one workgroup a CU: 104 - 114 us for 138 MB.
 #include <type_traits>
 
 #include "ssd_lin_chunk.h"

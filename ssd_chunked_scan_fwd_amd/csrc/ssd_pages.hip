@@ -1,8 +1,10 @@
 // ssd_pages.hip -- pages of a pool of states, [layers][slots][page]: copied
 // (forked, permuted), compacted, cleared. All are bound by the bytes they
 // read and write: 4 sequences' pages forked to 28, 2 layers of 1 MB a page, 67 MB
-// with each source read once: 16 us (4.2 TB/s); 60 live pages of 96 of 393 KB
-// made dense, 18 MB: 3 + 5 us of two launches, 15 us a call.
+// with each source read once: 16 us (4.2 TB/s). Lists of disjoint pairs, 2 layers
+// of 1 MB a page: 64 pairs 42 us (6.4 TB/s), 256 238 (4.5), 1024 1520 (2.8), as longer
+// lists leave shorter runs. 60 live pages of 96 of 393 KB made dense, 18 MB: 3 + 6
+// us of two launches, 15 us a call. 28 pages cleared, 59 MB: 10 us (6.0 TB/s).
 #include "ssd_device.h"
 #include "ssd_layer.h"
 
