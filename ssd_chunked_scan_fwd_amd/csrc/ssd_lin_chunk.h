@@ -12,10 +12,11 @@ constexpr int kC = 64;                       // tokens a chunk
 constexpr int kPitchP = lds_pitch(kC);       // LDS row of 64 scores
 
 // Powers of the decay, pw[kPowZero + e] = lam^e for e = 0 .. 64 and 0 for e = -64
-// .. -1, spw scale times them, pw[kPowHi] and the next lam as a sum of two floats: the weight of every pair and token of a chunk is
-// one LDS read (an exponential costs a wave as long as sixteen multiplies, and
-// a chunk has some forty weights a lane). They are rounded once, from 64 bits:
-// lam^64 carries the state from chunk to chunk, and an error in it compounds.
+// .. -1, spw scale times them, pw[kPowHi] and the next lam as a sum of two floats:
+// the weight of every pair and token of a chunk is one LDS read (an exponential
+// costs a wave as long as sixteen multiplies, and a chunk has some forty weights a
+// lane). They are rounded once, from 64 bits: lam^64 carries the state from chunk
+// to chunk, and an error in it compounds.
 constexpr int kPowZero = 64, kPowHi = 130, kPowSize = 132;
 __device__ __forceinline__ void fill_powers(float* pw, float* spw, float log_decay, float scale) {
   for (int i = threadIdx.x; i < kPowHi; i += blockDim.x) {

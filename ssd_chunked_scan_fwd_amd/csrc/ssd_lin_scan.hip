@@ -152,7 +152,7 @@ __device__ __forceinline__ void lin_by_token(const LinAgain* again, const float*
     const long tok = token(min(j, u.total - 1));
 #pragma unroll
     for (int b = 0; b < 2 * KB; ++b) {
-      const int col = 16 * b < end ? 16 * b : 0;
+      const int col = 16 * b < end ? 16 * b : -4 * g;   // behind the end: the head's first (with dk = 8 all that g >= 2 has)
       k[b] = *reinterpret_cast<const u32x2*>(k0 + tok * krow + col);
       if (!STATE_ONLY) q[b] = *reinterpret_cast<const u32x2*>(q0 + tok * qrow + col);
     }

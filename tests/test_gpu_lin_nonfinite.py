@@ -17,7 +17,7 @@ NAN, INF = float("nan"), float("inf")
 
 # T, H, Hk, dk, dv, packed sequences
 SHAPES = [(200, 2, 1, 64, 64, None), (300, 2, 2, 128, 128, None), (130, 2, 1, 40, 96, None), (130, 2, 2, 96, 40, None),
-          (150, 1, 1, 256, 200, None), (200, 2, 2, 16, 24, [0, 100, 100, 170, 200])]
+          (130, 3, 3, 8, 8, None), (130, 2, 1, 8, 136, None), (150, 1, 1, 256, 200, None), (200, 2, 2, 16, 24, [0, 100, 100, 170, 200])]
 # Tensors, and tokens with such a value in one channel: in a sequence's first (and, backwards, last) 32 tokens, in
 # the middle of a chunk, on its last and first place.
 PLACES = [("v", (20, 100)), ("v", (63,)), ("k", (20, 100)), ("k", (129,)), ("q", (64,)), ("q", (37, 100)), ("do", (20, 100))]
