@@ -396,13 +396,14 @@ __global__ __launch_bounds__(256 * VB, 4) void lin_kv_kernel(KvArgs args) {
     }
   }
 
-  // A value of q or dO that is not finite is left in R, whatever comes behind it.
+  // A value of q or dO that is not finite is left in R, whatever comes behind it. (A sequence without
+  // tokens has none, and none to read: it may start at the tensors' end.)
   float none = 0.f;
 #pragma unroll
   for (int b = 0; b < KB; ++b)
 #pragma unroll
     for (int r = 0; r < 4; ++r) none = fmaf(R[b][r], 0.f, none);
-  if (__builtin_expect(__syncthreads_or(none != 0.f), 0))
+  if (__builtin_expect(__syncthreads_or(none != 0.f && u.p.len > 0), 0))
     return kv_by_token<KB, VB>(&again, reinterpret_cast<float*>(&Ps[0][0]), pw);
   leave_state<KB>(a, u, dvc, dk0, R, pw);
 }
