@@ -85,3 +85,42 @@ def test_sequences_without_tokens(dtype):
     for s in (0, 2, 4):
         assert torch.equal(g["dinit"][s].isfinite(), d["init"][s].isfinite())
     assert all(torch.all(torch.isfinite(g[n])) for n in ("dq", "dk", "dv")) and torch.all(torch.isfinite(g["dinit"][[1, 3]]))
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (136, 40)])
+def test_captured_and_in_wider_rows(dims):
+    """Rows of one projection with such values, forwards and backwards in a graph: every replay gives what the eager
+    call on contiguous rows gave, with eager work between the replays."""
+    dk, dv = dims
+    T, H, Hk = 700, 4, 2
+    g = torch.Generator().manual_seed(17)
+    w = torch.randn(1, T, H * dk + Hk * (dk + dv), generator=g).to(BF).cuda()
+    w[0, 300, 3], w[0, 500, H * dk + 9], w[0, 40, (H + Hk) * dk + 2] = NAN, INF, -INF
+    q, k, v = (t.unflatten(-1, (-1, d)) for t, d in zip(w.split([H * dk, Hk * dk, Hk * dv], -1), (dk, dk, dv)))
+    do = torch.randn(1, T, H, dv, generator=g).to(BF).cuda()
+    ld = decays(H).cuda()
+
+    def run(q, k, v):
+        o, fin = ssd.lin_attn_fwd(q, k, v, ld, scale=0.2)
+        return [o, fin] + [ssd.lin_attn_bwd(q, k, v, ld, do, scale=0.2)[n] for n in ("dq", "dk", "dv")]
+
+    want = run(q.contiguous(), k.contiguous(), v.contiguous())
+    assert not all(torch.all(torch.isfinite(t)) for t in want) and all(torch.any(torch.isfinite(t)) for t in want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(q, k, v)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="relaxed"):
+        out = run(q, k, v)
+    for i in range(3):
+        for t in out:
+            t.zero_()
+        run(q.contiguous(), k.contiguous(), v.contiguous())
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b)) and torch.equal(a.isnan(), b.isnan()), i
