@@ -1,7 +1,7 @@
 /*
  * ssd.h -- C ABI of the MI355X (gfx950) chunked SSD forward pass and decode step,
- * and (last three parts) of linear attention with one decay a head, group norm and
- * the pages of a state pool.
+ * and (last five parts) of linear attention with one decay a head, group norm, the
+ * pages of a state pool, the gated delta rule and rotary positions.
  *
  * The operator is the scalar-decay state space model of "Transformers are
  * SSMs" (paper card at wikillm.com/papers/2405.21060, Method 1 and Method 2,
@@ -600,6 +600,122 @@ ssd_status ssd_pages_clear(void* pool, const int32_t* slots, int32_t count, cons
 ssd_status ssd_pages_compact_workspace_bytes(const ssd_pages_shape* shape, size_t* bytes);
 ssd_status ssd_pages_compact(void* pool, const uint8_t* live, int32_t* where, int32_t* count,
                              const ssd_pages_shape* shape, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The gated delta rule: linear attention whose state is corrected by what it
+ * answers already. For value head h, with a = exp(log_decay) and beta of the token
+ * and head, and S the head's state [dv][dk]:
+ *     u_t = beta_t (v_t - a_t S_{t-1} k_t),  S_t = a_t S_{t-1} + u_t k_t^T,
+ *     o_t = scale S_t q_t.
+ * Query and key heads are shared: value head h reads query and key head
+ * h / (nheads / nqk_heads). Keys are meant to have norm 1 and beta to lie in
+ * [0, 1] (the state is bounded then; nothing is normalised here).
+ *   q, k [batch, seqlen, nqk_heads, dk], v [batch, seqlen, nheads, dv] dtype:
+ *       element (token, head, i) at token * row + head * d + i, with row the
+ *       shape's q_row, k_row or v_row (0: contiguous); 16-byte aligned rows
+ *   log_decay [batch, seqlen, nheads] fp32, <= 0, or NULL: no decay. Below -200,
+ *       -inf included, a decay is 0.
+ *   beta [batch, seqlen, nheads] fp32
+ *   o [batch, seqlen, nheads, dv] dtype, contiguous
+ *   states fp32 [batch or num_seqs, nheads, dv, dk], 16-byte aligned, as those of
+ *       linear attention: one pool of slots serves both
+ * cu_seqlens, rows outside the sequences, empty sequences, sizes (dk, dv:
+ * multiples of 8 up to 256), overlaps and the limit on a launch: as for linear
+ * attention above. bf16 inputs enter the matrix products as they are, everything
+ * computed as sums of three bf16 terms (24 bits) with fp32 sums, fp32 inputs
+ * likewise; o and the gradients of q, k and v are rounded once, when written.
+ * A value that is not finite makes the results of its sequence from its chunk (64
+ * tokens, fp32: 32) on not finite, and of the chunk itself also earlier ones; in
+ * the backward call any of its sequence. Other sequences are not touched.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t batch;      /* rows; 1 with cu_seqlens; the step: entries            */
+  int32_t seqlen;     /* tokens a row (packed: in all); ignored by the step    */
+  int32_t nheads;     /* value heads: of v, o, the gates and the states        */
+  int32_t nqk_heads;  /* query and key heads, nheads % nqk_heads == 0          */
+  int32_t dk;         /* size of a query and of a key                          */
+  int32_t dv;         /* size of a value                                       */
+  int32_t num_seqs;   /* packed sequences with cu_seqlens, else 0              */
+  int32_t dtype;      /* ssd_dtype of q, k, v, o and their gradients           */
+  int64_t q_row;      /* elements from token to token, 0: nqk_heads * dk       */
+  int64_t k_row;      /* 0: nqk_heads * dk                                     */
+  int64_t v_row;      /* 0: nheads * dv                                        */
+} ssd_delta_shape;
+
+/* Workspace of a forward and of a backward call. */
+ssd_status ssd_gated_delta_workspace_bytes(const ssd_delta_shape* shape, size_t* bytes);
+ssd_status ssd_gated_delta_bwd_workspace_bytes(const ssd_delta_shape* shape, size_t* bytes);
+
+/* The form over prompts. initial_state and final_state may be NULL (zero; not
+ * wanted). scale: a normal number, not 0. */
+ssd_status ssd_gated_delta_fwd(const void* q, const void* k, const void* v, const float* log_decay, const float* beta,
+                               const int32_t* cu_seqlens, float scale, const float* initial_state, void* o,
+                               float* final_state, const ssd_delta_shape* shape, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
+ * Gradients of <d_o, o> + <dfinal_state, final_state> with respect to every input:
+ * dq, dk, dv contiguous, of q's, k's and v's shapes (dq and dk summed over the
+ * value heads that share them), dlog_decay (NULL: not wanted, as without decays)
+ * and dbeta fp32 of the gates' shape, dinitial_state (may be NULL). Everything is
+ * recomputed from the inputs.
+ */
+ssd_status ssd_gated_delta_bwd(const void* q, const void* k, const void* v, const float* log_decay, const float* beta,
+                               const int32_t* cu_seqlens, float scale, const float* initial_state, const void* d_o,
+                               const float* dfinal_state, void* dq, void* dk, void* dv, float* dlog_decay, float* dbeta,
+                               float* dinitial_state, const ssd_delta_shape* shape, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * One token for each of `batch` entries (q, k [batch, nqk_heads, dk], v, o
+ * [batch, nheads, dv], log_decay, beta [batch, nheads], contiguous; the shape's
+ * rows and num_seqs are ignored), against state [num_slots, nheads, dv, dk] fp32,
+ * updated in place. slots: as in ssd_lin_attn_step.
+ */
+ssd_status ssd_gated_delta_step(float* state, const void* q, const void* k, const void* v, const float* log_decay,
+                                const float* beta, const int32_t* slots, int32_t num_slots, float scale, void* o,
+                                const ssd_delta_shape* shape, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions of queries and keys. Of each head the first `rot` elements are
+ * pairs (x, y), turned by the angle t = position * freq[i], i = 0 .. rot / 2 - 1:
+ *     (x cos t - y sin t, y cos t + x sin t) * scale
+ * with pair i the elements i and i + rot / 2 (SSD_ROTARY_HALF) or 2 i and 2 i + 1
+ * (SSD_ROTARY_INTERLEAVED); the elements from rot on are copied. inverse = 1 turns
+ * by -t: the gradient of the call, with the same scale.
+ *   q [batch, seqlen, q_heads, dim], k [batch, seqlen, k_heads, dim] dtype: rows
+ *       q_row and k_row elements apart (0: contiguous); k NULL with k_heads = 0
+ *   q_out, k_out: likewise, rows q_out_row and k_out_row apart; may be q and k
+ *       themselves (the same rows: in place), any other overlap is refused
+ *   freq [rot / 2] fp32, taken as they are: frequencies of any base, scaled for
+ *       long contexts or not
+ *   positions int32 [batch, seqlen], or NULL: a token's place in its row or packed
+ *       sequence, plus offsets[row or sequence] (int32; NULL: 0)
+ *   cu_seqlens as for linear attention; rows outside the sequences are left as they
+ *       were.
+ * Angles are formed and reduced in 64 bits. dim up to 1024; rows of 16-byte pieces
+ * (dim % 8 == 0, rot % 16 == 0, interleaved % 8) move as such, others by element.
+ * ------------------------------------------------------------------------- */
+typedef enum { SSD_ROTARY_HALF = 0, SSD_ROTARY_INTERLEAVED = 1 } ssd_rotary_layout;
+typedef struct {
+  int32_t batch;
+  int32_t seqlen;
+  int32_t q_heads;
+  int32_t k_heads;    /* 0: no keys                                      */
+  int32_t dim;
+  int32_t rot;        /* even, 2 .. dim                                  */
+  int32_t num_seqs;   /* packed sequences with cu_seqlens, else 0        */
+  int32_t dtype;      /* ssd_dtype of q, k and their outputs             */
+  int32_t layout;     /* ssd_rotary_layout                               */
+  int32_t inverse;    /* 1: turn back (the gradient)                     */
+  int64_t q_row;      /* elements from token to token, 0: q_heads * dim  */
+  int64_t k_row;
+  int64_t q_out_row;
+  int64_t k_out_row;
+} ssd_rotary_shape;
+ssd_status ssd_rotary(const void* q, const void* k, const float* freq, const int32_t* positions,
+                      const int32_t* cu_seqlens, const int32_t* offsets, float scale, void* q_out, void* k_out,
+                      const ssd_rotary_shape* shape, void* stream);
 
 #ifdef __cplusplus
 }

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 from typing import Optional, Tuple
 
@@ -33,7 +34,9 @@ EXPORTS = ("ssd_abi_version", "ssd_status_string", "ssd_default_state_block", "s
            "ssd_chunk_scan_kernel", "ssd_bwd_mamba2_workspace_bytes", "ssd_bwd_mamba2", "ssd_fwd_noalloc",
            "ssd_lin_attn_workspace_bytes", "ssd_lin_attn_bwd_workspace_bytes", "ssd_lin_attn_fwd", "ssd_lin_attn_bwd",
            "ssd_lin_attn_step", "ssd_group_norm_workspace_bytes", "ssd_group_norm", "ssd_group_norm_bwd",
-           "ssd_pages_copy", "ssd_pages_clear", "ssd_pages_compact_workspace_bytes", "ssd_pages_compact")
+           "ssd_pages_copy", "ssd_pages_clear", "ssd_pages_compact_workspace_bytes", "ssd_pages_compact",
+           "ssd_gated_delta_workspace_bytes", "ssd_gated_delta_bwd_workspace_bytes", "ssd_gated_delta_fwd",
+           "ssd_gated_delta_bwd", "ssd_gated_delta_step", "ssd_rotary")
 
 
 class SSDError(RuntimeError):
@@ -71,6 +74,21 @@ class NormShape(ctypes.Structure):
 
 class PagesShape(ctypes.Structure):
     _fields_ = [("layers", ctypes.c_int32), ("slots", ctypes.c_int32), ("page_bytes", ctypes.c_int64)]
+
+
+class DeltaShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32), ("nheads", ctypes.c_int32),
+                ("nqk_heads", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
+                ("num_seqs", ctypes.c_int32), ("dtype", ctypes.c_int32), ("q_row", ctypes.c_int64),
+                ("k_row", ctypes.c_int64), ("v_row", ctypes.c_int64)]
+
+
+class RotaryShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("k_heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("num_seqs", ctypes.c_int32), ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("q_row", ctypes.c_int64), ("k_row", ctypes.c_int64),
+                ("q_out_row", ctypes.c_int64), ("k_out_row", ctypes.c_int64)]
 
 
 def library_path() -> str:
@@ -131,6 +149,7 @@ def lib():
         L.ssd_bwd_mamba2.restype = ctypes.c_int
         L.ssd_bwd_mamba2.argtypes = [vp] * 12 + [i32, i32] + [vp] * 9 + [shp, vp, sz, vp]
         f32, lin, norm, pages = ctypes.c_float, ctypes.POINTER(LinShape), ctypes.POINTER(NormShape), ctypes.POINTER(PagesShape)
+        delta = ctypes.POINTER(DeltaShape)
         for name, args in (("ssd_lin_attn_workspace_bytes", [lin, ctypes.POINTER(sz)]),
                            ("ssd_lin_attn_bwd_workspace_bytes", [lin, ctypes.POINTER(sz)]),
                            ("ssd_lin_attn_fwd", [vp] * 5 + [f32] + [vp] * 3 + [lin, vp, sz, vp]),
@@ -142,7 +161,13 @@ def lib():
                            ("ssd_pages_copy", [vp, vp, vp, i32, pages, vp]),
                            ("ssd_pages_clear", [vp, vp, i32, pages, vp]),
                            ("ssd_pages_compact_workspace_bytes", [pages, ctypes.POINTER(sz)]),
-                           ("ssd_pages_compact", [vp] * 4 + [pages, vp, sz, vp])):
+                           ("ssd_pages_compact", [vp] * 4 + [pages, vp, sz, vp]),
+                           ("ssd_gated_delta_workspace_bytes", [delta, ctypes.POINTER(sz)]),
+                           ("ssd_gated_delta_bwd_workspace_bytes", [delta, ctypes.POINTER(sz)]),
+                           ("ssd_gated_delta_fwd", [vp] * 6 + [f32] + [vp] * 3 + [delta, vp, sz, vp]),
+                           ("ssd_gated_delta_bwd", [vp] * 6 + [f32] + [vp] * 9 + [delta, vp, sz, vp]),
+                           ("ssd_gated_delta_step", [vp] * 7 + [i32, f32, vp, delta, vp]),
+                           ("ssd_rotary", [vp] * 6 + [f32] + [vp] * 2 + [ctypes.POINTER(RotaryShape), vp])):
             getattr(L, name).restype = ctypes.c_int
             getattr(L, name).argtypes = args
         _lib = L
@@ -1114,3 +1139,331 @@ def pages_compact(pool: torch.Tensor, live: torch.Tensor, where: Optional[torch.
     _call_on(pool.device, "ssd_pages_compact", _addr(pool), _addr(live), _addr(where), _addr(count), ctypes.byref(shape),
              _addr(workspace), have)
     return where, count
+
+
+# ---------------------------------------------------------------------------
+# The gated delta rule
+# ---------------------------------------------------------------------------
+
+def _delta_shape(q, k, v, cu_seqlens):
+    """The shape of a call over prompts, its tensors checked against one another."""
+    _check_dtype(q, "q", "[batch, seqlen, nqk_heads, dk]", 4)
+    b, T, Hk, Dk = q.shape
+    if not isinstance(k, torch.Tensor) or tuple(k.shape) != (b, T, Hk, Dk):
+        raise ValueError(f"k must be a 4-d tensor [{b}, {T}, {Hk}, {Dk}]")
+    if not isinstance(v, torch.Tensor) or v.dim() != 4 or tuple(v.shape[:2]) != (b, T):
+        raise ValueError(f"v must be a 4-d tensor [{b}, {T}, nheads, dv]")
+    H = v.shape[2]
+    if Hk < 1 or H < 1 or H % Hk:
+        raise ValueError(f"nheads {H} must be a multiple of nqk_heads {Hk}")
+    for t, name in ((k, "k"), (v, "v")):
+        if t.dtype != q.dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {q.dtype}")
+    S = 0
+    if cu_seqlens is not None:
+        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be a 1-d tensor of num_seqs + 1 >= 2 entries")
+        if b != 1:
+            raise ValueError("packed sequences (cu_seqlens) need batch 1")
+        S = cu_seqlens.numel() - 1
+    _int32(dict(batch=b, seqlen=T, nheads=H, dk=Dk, dv=v.shape[3], num_seqs=S))
+    # A batch without tokens runs nothing: its heads and sizes are checked as those of one token.
+    return _delta_struct(max(b, 1), max(T, 1), H, Hk, Dk, v.shape[3], S, _dtype_code(q.dtype), _token_row(q, "q"),
+                         _token_row(k, "k"), _token_row(v, "v"))
+
+
+@functools.lru_cache(maxsize=256)
+def _delta_struct(*values) -> DeltaShape:
+    """The C shape of these sizes (the library only reads it)."""
+    return DeltaShape(*values)
+
+
+def _delta_values(shape: DeltaShape):
+    return tuple(getattr(shape, name) for name, _ in DeltaShape._fields_)
+
+
+def _delta_workspace(fn: str, shape: DeltaShape, workspace, device):
+    return _room(_size_of(fn, DeltaShape, _delta_values(shape)), workspace, device)
+
+
+def gated_delta_shape(q, k, v, cu_seqlens=None) -> DeltaShape:
+    """The shape of a call with these tensors (for gated_delta_workspace_bytes)."""
+    return DeltaShape(*_delta_values(_delta_shape(q, k, v, cu_seqlens)))   # the caller's own
+
+
+def gated_delta_workspace_bytes(shape: DeltaShape) -> int:
+    n = ctypes.c_size_t(0)
+    _call("ssd_gated_delta_workspace_bytes", ctypes.byref(shape), ctypes.byref(n))
+    return int(n.value)
+
+
+def gated_delta_bwd_workspace_bytes(shape: DeltaShape) -> int:
+    n = ctypes.c_size_t(0)
+    _call("ssd_gated_delta_bwd_workspace_bytes", ctypes.byref(shape), ctypes.byref(n))
+    return int(n.value)
+
+
+def gated_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: Optional[torch.Tensor],
+                    beta: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, scale: float = 1.0,
+                    initial_state: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
+                    final_state: Optional[torch.Tensor] = None, want_final: bool = True,
+                    workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The gated delta rule over prompts (ssd_gated_delta_fwd). Returns (o, final_state or None).
+
+    q, k [b, T, Hk, dk], v [b, T, H, dv] (bf16 or fp32; tokens may lie in wider rows,
+    as slices of one projection do; value head h reads query and key head
+    h / (H / Hk)), log_decay [b, T, H] fp32 <= 0 or None (no decay), beta [b, T, H]
+    fp32, states fp32 [rows or sequences, H, dv, dk]. cu_seqlens may hold empty
+    sequences, and a batch no rows or tokens at all (its final states are the initial
+    ones); rows of o that belong to no sequence are left as they were (undefined in an
+    o made here).
+    """
+    shape = _delta_shape(q, k, v, cu_seqlens)
+    b, T, H, Dv = v.shape
+    Dk, nseq = q.shape[3], shape.num_seqs or b
+    if beta is None:
+        raise ValueError("beta is required")
+    st = (nseq, H, Dv, Dk)
+    _check(q.device, ((q, "q", None, None, 16), (k, "k", None, None, 16), (v, "v", None, None, 16),
+                      (initial_state, "initial_state", st, torch.float32, 16), (o, "o", (b, T, H, Dv), q.dtype, 16),
+                      (final_state, "final_state", st, torch.float32, 16),
+                      (log_decay, "log_decay", (b, T, H), torch.float32, 4), (beta, "beta", (b, T, H), torch.float32, 4),
+                      (cu_seqlens, "cu_seqlens", None, torch.int32, 4), (workspace, "workspace", None, torch.uint8, 256)))
+    if final_state is not None and initial_state is not None and _share(final_state, initial_state):
+        raise ValueError("final_state must not overlap initial_state")
+    if b * T == 0:
+        _check_scale(scale)
+        if o is None:
+            o = torch.empty(b, T, H, Dv, dtype=q.dtype, device=q.device)
+        return o, _state_of_no_tokens(initial_state, final_state, want_final, st, q.device)
+    workspace, have = _delta_workspace("ssd_gated_delta_workspace_bytes", shape, workspace, q.device)
+    if o is None:
+        o = torch.empty(b, T, H, Dv, dtype=q.dtype, device=q.device)
+    if final_state is None and want_final:
+        final_state = torch.empty(st, dtype=torch.float32, device=q.device)
+    _call_on(q.device, "ssd_gated_delta_fwd", _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(beta), _addr(cu_seqlens),
+             float(scale), _addr(initial_state), _addr(o), _addr(final_state), ctypes.byref(shape), _addr(workspace), have)
+    return o, final_state
+
+
+def gated_delta_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: Optional[torch.Tensor],
+                    beta: torch.Tensor, do: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, scale: float = 1.0,
+                    initial_state: Optional[torch.Tensor] = None, dfinal_state: Optional[torch.Tensor] = None,
+                    want_dinit: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Gradients of <do, o> + <dfinal_state, final_state> of gated_delta_fwd with these
+    inputs (ssd_gated_delta_bwd). Returns dict(dq, dk, dv, dlog_decay, dbeta, dinit),
+    dlog_decay None without decays and dinit unless it is wanted. Rows that belong to
+    no sequence are undefined."""
+    shape = _delta_shape(q, k, v, cu_seqlens)
+    b, T, H, Dv = v.shape
+    Dk, nseq = q.shape[3], shape.num_seqs or b
+    if beta is None or do is None:
+        raise ValueError("beta and do are required")
+    st = (nseq, H, Dv, Dk)
+    _check(q.device, ((q, "q", None, None, 16), (k, "k", None, None, 16), (v, "v", None, None, 16),
+                      (do, "do", (b, T, H, Dv), q.dtype, 16), (initial_state, "initial_state", st, torch.float32, 16),
+                      (dfinal_state, "dfinal_state", st, torch.float32, 16),
+                      (log_decay, "log_decay", (b, T, H), torch.float32, 4), (beta, "beta", (b, T, H), torch.float32, 4),
+                      (cu_seqlens, "cu_seqlens", None, torch.int32, 4), (workspace, "workspace", None, torch.uint8, 256)))
+    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=q.device)   # noqa: E731
+    out = dict(dq=new(q.shape, q.dtype), dk=new(k.shape, q.dtype), dv=new(v.shape, q.dtype),
+               dlog_decay=None if log_decay is None else new((b, T, H), torch.float32), dbeta=new((b, T, H), torch.float32),
+               dinit=new(st, torch.float32) if want_dinit else None)
+    if b * T == 0:
+        _check_scale(scale)
+        _state_of_no_tokens(dfinal_state, out["dinit"], want_dinit, st, q.device)
+        return out
+    workspace, have = _delta_workspace("ssd_gated_delta_bwd_workspace_bytes", shape, workspace, q.device)
+    _call_on(q.device, "ssd_gated_delta_bwd", _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(beta), _addr(cu_seqlens),
+             float(scale), _addr(initial_state), _addr(do), _addr(dfinal_state), _addr(out["dq"]), _addr(out["dk"]),
+             _addr(out["dv"]), _addr(out["dlog_decay"]), _addr(out["dbeta"]), _addr(out["dinit"]), ctypes.byref(shape),
+             _addr(workspace), have)
+    return out
+
+
+def gated_delta_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     log_decay: Optional[torch.Tensor], beta: torch.Tensor, slots: Optional[torch.Tensor] = None,
+                     scale: float = 1.0, o: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token for each entry of a batch (ssd_gated_delta_step): updates `state`
+    [num_slots, H, dv, dk] fp32 in place and returns o [b, H, dv].
+
+    q, k [b, Hk, dk], v [b, H, dv], log_decay (or None) and beta [b, H] fp32; slots
+    int32 [b]: the state each entry uses (None: entry i uses state i). Slots outside
+    the pool are padding (o = 0); entries that name one slot are taken in the order
+    of the batch; there may be none.
+    """
+    _check_dtype(q, "q", "[batch, nqk_heads, dk]", 3)
+    b, Hk, Dk = q.shape
+    if not isinstance(k, torch.Tensor) or tuple(k.shape) != (b, Hk, Dk):
+        raise ValueError(f"k must be a 3-d tensor [{b}, {Hk}, {Dk}]")
+    if not isinstance(v, torch.Tensor) or v.dim() != 3 or v.shape[0] != b:
+        raise ValueError(f"v must be a 3-d tensor [{b}, nheads, dv]")
+    H, Dv = v.shape[1:]
+    if Hk < 1 or H < 1 or H % Hk:
+        raise ValueError(f"nheads {H} must be a multiple of nqk_heads {Hk}")
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be a 4-d tensor [num_slots, nheads, dv, dk]")
+    if beta is None:
+        raise ValueError("beta is required")
+    n = state.shape[0]
+    _int32(dict(batch=b, nheads=H, dk=Dk, dv=Dv, num_slots=n))
+    if slots is None and n < b:
+        raise ValueError(f"state has {n} slots for {b} entries")
+    dtype, device = q.dtype, q.device
+    _check(device, ((q, "q", None, dtype, 16), (k, "k", None, dtype, 16), (v, "v", None, dtype, 16),
+                    (state, "state", (n, H, Dv, Dk), torch.float32, 16), (o, "o", (b, H, Dv), dtype, 16),
+                    (log_decay, "log_decay", (b, H), torch.float32, 4), (beta, "beta", (b, H), torch.float32, 4),
+                    (slots, "slots", (b,), torch.int32, 4)))
+    if o is None:
+        o = torch.empty((b, H, Dv), dtype=dtype, device=device)
+    if b == 0:
+        _check_scale(scale)
+        _size_of("ssd_gated_delta_workspace_bytes", DeltaShape, (1, 1, H, Hk, Dk, Dv, 0, _dtype_code(dtype), 0, 0, 0))   # its sizes
+        return o
+    shape = _delta_struct(b, 1, H, Hk, Dk, Dv, 0, _dtype_code(dtype), 0, 0, 0)
+    _call_on(device, "ssd_gated_delta_step", _addr(state), _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(beta),
+             _addr(slots), n, float(scale), _addr(o), ctypes.byref(shape))
+    return o
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions
+# ---------------------------------------------------------------------------
+
+_ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                       original_length: int = 0, slow: float = 1.0, fast: float = 32.0, device=None):
+    """The frequencies base^(-2 i / rot), i < rot / 2, as rotary takes them (fp32), and the
+    scale that goes with them: (freq, scale). For contexts `factor` times as long as
+    the one that a model was trained on:
+
+      "none"      as they are;
+      "linear"    divided by factor;
+      "ntk"       of the base times factor^(rot / (rot - 2)): the fastest stays, the slowest
+                  is divided by factor;
+      "by_parts"  divided by factor where they turn less than `slow` times over
+                  original_length, kept where more than `fast` times, mixed in between;
+                  scale 1 + 0.1 ln factor, of queries and of keys.
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot {rot} must be even and at least 2")
+    if scaling not in ("none", "linear", "ntk", "by_parts"):
+        raise ValueError(f"scaling {scaling!r} must be none, linear, ntk or by_parts")
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be above 0")
+    i = torch.arange(0, rot, 2, dtype=torch.float64)
+    if scaling == "ntk":
+        if rot < 4:
+            raise ValueError("ntk scaling needs rot of at least 4")
+        base = base * factor ** (rot / (rot - 2))
+    freq, scale = base ** (-i / rot), 1.0
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "by_parts":
+        if original_length < 1 or not fast > slow:
+            raise ValueError("by_parts scaling needs original_length and fast > slow")
+        turns = original_length * freq / (2 * math.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0, 1)
+        freq = freq * keep + freq / factor * (1 - keep)
+        scale = 1 + 0.1 * math.log(factor) if factor > 1 else 1.0
+    return freq.float().to(device), scale
+
+
+@functools.lru_cache(maxsize=256)
+def _rotary_struct(*values) -> RotaryShape:
+    return RotaryShape(*values)
+
+
+def _rotary_rows(t: torch.Tensor, name: str, like: torch.Tensor) -> torch.Tensor:
+    """As [b, T, heads, dim]; a token an entry [b, heads, dim] counts as one row of b tokens."""
+    if not isinstance(t, torch.Tensor) or t.dim() != like.dim() or t.shape[:-2] != like.shape[:-2] or t.shape[-1] != like.shape[-1]:
+        raise ValueError(f"{name} must be a tensor [..., heads, {like.shape[-1]}] of q's leading sizes {tuple(like.shape[:-2])}")
+    if t.dtype != like.dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {like.dtype}")
+    return t if t.dim() == 4 else t.unsqueeze(0)
+
+
+def _rotary(q, k, freq, positions, cu_seqlens, offsets, layout, scale, q_out, k_out, inverse):
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be a tensor [batch, seqlen, heads, dim] or [batch, heads, dim]")
+    if q.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"q has dtype {q.dtype}; bfloat16 and float32 are supported")
+    if layout not in _ROTARY_LAYOUTS:
+        raise ValueError(f"layout {layout!r} must be half or interleaved")
+    if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
+        raise ValueError("freq must be a 1-d tensor of rot / 2 frequencies")
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    step, dim, H = q.dim() == 3, q.shape[-1], q.shape[-2]
+    if step and positions is None:
+        raise ValueError("positions are required for one token an entry")
+    if step and cu_seqlens is not None:
+        raise ValueError("cu_seqlens needs q [1, seqlen, heads, dim]")
+    if positions is not None and offsets is not None:
+        raise ValueError("positions and offsets exclude each other")
+    q4 = _rotary_rows(q, "q", q)
+    k4 = None if k is None else _rotary_rows(k, "k", q)
+    b, T = q4.shape[:2]
+    Hk = 0 if k is None else k4.shape[2]
+    if H < 1 or (k is not None and Hk < 1):
+        raise ValueError("q and k must have at least one head")
+    S = 0
+    if cu_seqlens is not None:
+        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be a 1-d tensor of num_seqs + 1 >= 2 entries")
+        if b != 1:
+            raise ValueError("packed sequences (cu_seqlens) need batch 1")
+        S = cu_seqlens.numel() - 1
+    _int32(dict(batch=b, seqlen=T, q_heads=H, k_heads=Hk, dim=dim, num_seqs=S))
+    rot = 2 * freq.numel()
+    if not 2 <= rot <= dim:
+        raise ValueError(f"freq has {freq.numel()} entries for heads of {dim}")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    for t, name, src in ((q_out, "q_out", q), (k_out, "k_out", k)):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.shape != src.shape):
+            raise ValueError(f"{name} must have shape {tuple(src.shape)}")
+    q_to = _rotary_rows(q_out, "q_out", q)
+    k_to = None if k is None else _rotary_rows(k_out, "k_out", q)
+    e = q.element_size()
+    _check(q.device, ((q, "q", None, None, e), (k, "k", None, None, e), (q_out, "q_out", None, None, e),
+                      (k_out, "k_out", None, None, e), (freq, "freq", None, torch.float32, 4),
+                      (positions, "positions", q.shape[:-2], torch.int32, 4), (cu_seqlens, "cu_seqlens", None, torch.int32, 4),
+                      (offsets, "offsets", (S or b,), torch.int32, 4)))
+    rows = lambda t, name: 0 if t is None else _token_row(t, name)   # noqa: E731
+    shape = _rotary_struct(max(b, 1), max(T, 1), H, Hk, dim, rot, S, _dtype_code(q.dtype), _ROTARY_LAYOUTS[layout], inverse,
+                           rows(q4, "q"), rows(k4, "k"), rows(q_to, "q_out"), rows(k_to, "k_out"))
+    if b * T == 0:
+        _check_scale(scale)
+        return q_out, k_out
+    _call_on(q.device, "ssd_rotary", _addr(q), _addr(k), _addr(freq), _addr(positions), _addr(cu_seqlens), _addr(offsets),
+             float(scale), _addr(q_out), _addr(k_out), ctypes.byref(shape))
+    return q_out, k_out
+
+
+def rotary(q: torch.Tensor, k: Optional[torch.Tensor], freq: torch.Tensor, positions: Optional[torch.Tensor] = None,
+           cu_seqlens: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None, layout: str = "half",
+           scale: float = 1.0, q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """Rotary positions of queries and keys (ssd_rotary). Returns (q_out, k_out or None).
+
+    q [b, T, H, dim] and k [b, T, Hk, dim] or None (bf16 or fp32; tokens may lie in wider
+    rows), or one token an entry [b, H, dim] with its positions [b]. Of each head the
+    first 2 * len(freq) elements are turned, in pairs (i, i + len(freq)) for layout
+    "half" or (2 i, 2 i + 1) for "interleaved", by position * freq[i]; freq fp32, of
+    rotary_frequencies or any other. positions int32 [b, T], or None: a token's place in
+    its row or packed sequence, plus offsets [rows or sequences] int32. q_out and k_out
+    may be q and k (in place).
+    """
+    return _rotary(q, k, freq, positions, cu_seqlens, offsets, layout, scale, q_out, k_out, 0)
+
+
+def rotary_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], freq: torch.Tensor, positions: Optional[torch.Tensor] = None,
+               cu_seqlens: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None, layout: str = "half",
+               scale: float = 1.0, q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """Gradients of q and k from those of rotary's results with these arguments: turned
+    back, the same scale. Returns (gradient of q, gradient of k or None)."""
+    return _rotary(dq, dk, freq, positions, cu_seqlens, offsets, layout, scale, q_out, k_out, 1)

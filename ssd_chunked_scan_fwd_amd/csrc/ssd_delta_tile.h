@@ -1,0 +1,174 @@
+// ssd_delta_tile.h -- what the delta rule's kernels share: fp32 values as sums
+// of bf16 terms, operands of v_mfma_f32_16x16x32_bf16 made of them, rows of a
+// chunk as operands.
+//
+// The rule feeds what it computes back into itself (the state, and the inverse
+// of I + A), and its states and gate gradients are fp32 results. So every
+// computed operand enters its products as the sum of three bf16 terms, which
+// hold all 24 bits of an fp32 value; bf16 inputs are exact with one, fp32 inputs
+// take three. Of a product of terms i and j those with i + j < 3 are formed: what
+// is left out is below 2^-24 of the product.
+#pragma once
+
+#include "ssd_delta.h"
+#include "ssd_device.h"
+#include "ssd_lin_chunk.h"
+
+namespace ssd {
+
+constexpr int kTerms = 3;
+// Terms of the operands that only o, a result of the inputs' type, depends on:
+// two leave 2^-16 of it, where o itself is rounded by 2^-9.
+constexpr int out_terms(int nx) { return nx == 1 ? 2 : kTerms; }
+
+// Eight (four) floats as the sum of N terms each.
+template <int N>
+__device__ __forceinline__ void split8(const float* x, u32x4* out) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float lo = x[2 * c], hi = x[2 * c + 1];
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+      const uint32_t w = pack_bf16x2(lo, hi);
+      out[t][c] = w;
+      lo -= bf16_lo(w);
+      hi -= bf16_hi(w);
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void split4(f32x4 x, u32x2* out) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    float lo = x[2 * c], hi = x[2 * c + 1];
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+      const uint32_t w = pack_bf16x2(lo, hi);
+      out[t][c] = w;
+      lo -= bf16_lo(w);
+      hi -= bf16_hi(w);
+    }
+  }
+}
+
+// acc += a b, of terms i and j with i + j < ORD; the small ones first.
+template <int NA, int NB, int ORD>
+__device__ __forceinline__ f32x4 mma(const u32x4* a, const u32x4* b, f32x4 acc) {
+#pragma unroll
+  for (int s = ORD - 1; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB) acc = mfma16x16x32(a[i], b[s - i], acc);
+  return acc;
+}
+
+// Eight values of a row as they come from memory, and as terms. NX: terms of an
+// input, 1 for bf16 and 3 for fp32.
+template <int NX>
+struct Raw8 {
+  u32x4 w[NX == 1 ? 1 : 2];
+};
+// Columns col .. col + 7 at byte offset `off` (kOffNone: zeros).
+template <int NX>
+__device__ __forceinline__ Raw8<NX> load8(rsrc_t r, uint32_t off) {
+  Raw8<NX> x;
+  x.w[0] = buf_load16(r, off);
+  if constexpr (NX > 1) x.w[1] = buf_load16(r, off + 16);
+  return x;
+}
+// Columns col .. col + 3 and col + 16 .. col + 19, the order of an accumulator pair.
+template <int NX>
+__device__ __forceinline__ Raw8<NX> load_pair(rsrc_t r, uint32_t lo, uint32_t hi) {
+  Raw8<NX> x;
+  if constexpr (NX == 1) {
+    const u32x2 a = buf_load8(r, lo), b = buf_load8(r, hi);
+    x.w[0] = u32x4{a.x, a.y, b.x, b.y};
+  } else {
+    x.w[0] = buf_load16(r, lo);
+    x.w[1] = buf_load16(r, hi);
+  }
+  return x;
+}
+__device__ __forceinline__ void floats8(const Raw8<1>& x, float* f) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    f[2 * c] = bf16_lo(x.w[0][c]);
+    f[2 * c + 1] = bf16_hi(x.w[0][c]);
+  }
+}
+__device__ __forceinline__ void floats8(const Raw8<3>& x, float* f) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) f[c] = __uint_as_float(x.w[c >> 2][c & 3]);
+}
+template <int NX>
+__device__ __forceinline__ void terms8(const Raw8<NX>& x, u32x4* out) {
+  if constexpr (NX == 1) {
+    out[0] = x.w[0];
+  } else {
+    float f[8];
+    floats8(x, f);
+    split8<NX>(f, out);
+  }
+}
+
+// Four values of a row.
+template <int NX>
+struct Raw4 {
+  uint32_t w[NX == 1 ? 2 : 4];
+};
+template <int NX>
+__device__ __forceinline__ Raw4<NX> load4(rsrc_t r, uint32_t off) {
+  Raw4<NX> x;
+  if constexpr (NX == 1) {
+    const u32x2 a = buf_load8(r, off);
+    x.w[0] = a.x;
+    x.w[1] = a.y;
+  } else {
+    const u32x4 a = buf_load16(r, off);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x.w[c] = a[c];
+  }
+  return x;
+}
+template <int NX>
+__device__ __forceinline__ f32x4 floats4(const Raw4<NX>& x) {
+  if constexpr (NX == 1) return f32x4{bf16_lo(x.w[0]), bf16_hi(x.w[0]), bf16_lo(x.w[1]), bf16_hi(x.w[1])};
+  else return f32x4{__uint_as_float(x.w[0]), __uint_as_float(x.w[1]), __uint_as_float(x.w[2]), __uint_as_float(x.w[3])};
+}
+template <int NX>
+__device__ __forceinline__ void store4(f32x4 x, rsrc_t r, uint32_t off) {
+  if constexpr (NX == 1) buf_store8(u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, r, off);
+  else buf_store16(__builtin_bit_cast(u32x4, x), r, off);
+}
+
+// Operands of C x C matrices in the workspace: those of 16 rows and 32 columns
+// (columns in the order of an accumulator pair), `n` terms each of 64 lanes of 16
+// bytes, one behind the other.
+constexpr int kOperand = 512;   // elements
+__host__ __device__ constexpr long operands(int C, int n) { return (long)(C / 16) * (C / 32) * n * kOperand; }
+__device__ __forceinline__ long operand_at(int C, int n, int rb, int kp) { return ((long)rb * (C / 32) + kp) * n * kOperand; }
+
+// LDS rows of 16 nv values that are read transposed: 24 values apart for nv = 1
+// (two workgroups a CU need the room), else an odd multiple of 32 bytes.
+__host__ __device__ constexpr int value_pitch(int nv) { return nv == 1 ? 24 : lds_pitch(16 * nv); }
+
+// The chunk of a workgroup.
+struct DeltaChunk {
+  LinPiece p;    // p.blk < 0: none
+  long row0;     // first token, flattened
+  int n;         // tokens
+};
+template <int C>
+__device__ __forceinline__ DeltaChunk delta_slot(const DeltaArgs& a, long slot) {
+  DeltaChunk c;
+  c.p = lin_piece(a.cu, a.S, a.T, C, a.slots_per_row, slot);
+  c.row0 = c.p.start + (long)max(c.p.blk, 0) * C;
+  c.n = min(C, c.p.len - max(c.p.blk, 0) * C);
+  return c;
+}
+// Rows of a chunk of one head: row 0 at the buffer's start.
+__device__ __forceinline__ rsrc_t chunk_rows(const void* base, long row0, long row, long col, int n, int esz) {
+  return make_rsrc(static_cast<const char*>(base) + (row0 * row + col) * esz, (uint32_t)(n * row * esz));
+}
+
+}  // namespace ssd

@@ -1,5 +1,5 @@
-// ssd_layer.h -- internal launchers of the group norm and of the pages of a
-// state pool. Arguments have been validated by the C-ABI layer.
+// ssd_layer.h -- internal launchers of the group norm, of the pages of a state
+// pool and of rotary positions. Arguments have been validated by the C-ABI layer.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -47,5 +47,20 @@ hipError_t launch_pages_clear(const PagesArgs& a, const int32_t* slots, int n, h
 size_t pages_compact_ws_bytes(int slots);
 hipError_t launch_pages_compact(const PagesArgs& a, const uint8_t* live, int32_t* where, int32_t* count, void* ws,
                                 hipStream_t stream);
+
+struct RotaryArgs {
+  const void* x[2] = {nullptr, nullptr};   // queries and keys, rows x_row apart
+  void* y[2] = {nullptr, nullptr};
+  long x_row[2] = {0, 0}, y_row[2] = {0, 0};
+  int heads[2] = {0, 0};
+  const float* freq = nullptr;             // [rot / 2]
+  const int32_t* positions = nullptr;      // [tokens] or null: the token's place in its sequence
+  const int32_t* cu = nullptr;
+  const int32_t* offsets = nullptr;        // [sequences] added to those places, or null
+  float scale = 1.f;
+  int batch = 1, T = 0, S = 0, d = 0, rot = 0, interleaved = 0, inverse = 0, bf16 = 0;
+};
+bool rotary_launchable(const RotaryArgs& a);
+hipError_t launch_rotary(const RotaryArgs& a, hipStream_t stream);
 
 }  // namespace ssd

@@ -113,23 +113,24 @@ struct LinPiece {
   long start;  // its first token, flattened over rows
 };
 
-// The sequence and block of a slot. cu's entries are brought into [0, T] and
+// The sequence and block of a slot: rows or packed sequences (cu, S of them) of T
+// tokens in all, cut into blocks of L. cu's entries are brought into [0, T] and
 // into order, so that no content of cu leads outside the tensors. Every lane of
 // the calling wave must be active; all receive the same answer.
-__device__ __forceinline__ LinPiece lin_piece(const LinScan& a, long slot) {
+__device__ __forceinline__ LinPiece lin_piece(const int32_t* cu, int S, int T, int L, long slots_per_row, long slot) {
   LinPiece p;
-  if (!a.cu) {
-    p.seq = (int)(slot / a.slots_per_row);
-    p.blk = (int)(slot % a.slots_per_row);
-    p.len = a.T;
-    p.start = (long)p.seq * a.T;
+  if (!cu) {
+    p.seq = (int)(slot / slots_per_row);
+    p.blk = (int)(slot % slots_per_row);
+    p.len = T;
+    p.start = (long)p.seq * T;
     return p;
   }
   // Slots of sequence s begin at floor(cu[s] / L) + s, which grows with s: count those at or before `slot`,
   // halving the range down to a wave's width, the rest with one load a lane.
   const int lane = (int)threadIdx.x & 63;
-  auto begins = [&](int i) { return (long)min(max(a.cu[i], 0), a.T) / a.L + i; };
-  int lo = 0, hi = a.S;
+  auto begins = [&](int i) { return (long)min(max(cu[i], 0), T) / L + i; };
+  int lo = 0, hi = S;
   while (hi - lo > 64) {
     const int mid = __builtin_amdgcn_readfirstlane((lo + hi) / 2);
     if (begins(mid) <= slot) lo = mid;
@@ -145,13 +146,16 @@ __device__ __forceinline__ LinPiece lin_piece(const LinScan& a, long slot) {
     p.start = 0;
     return p;
   }
-  const int c0 = min(max(a.cu[p.seq], 0), a.T);
-  const int c1 = min(max(a.cu[p.seq + 1], c0), a.T);
+  const int c0 = min(max(cu[p.seq], 0), T);
+  const int c1 = min(max(cu[p.seq + 1], c0), T);
   p.start = c0;
   p.len = c1 - c0;
-  const long b = slot - ((long)c0 / a.L + p.seq);
-  p.blk = b >= 0 && (b == 0 || b * a.L < p.len) ? (int)b : -1;
+  const long b = slot - ((long)c0 / L + p.seq);
+  p.blk = b >= 0 && (b == 0 || b * L < p.len) ? (int)b : -1;
   return p;
+}
+__device__ __forceinline__ LinPiece lin_piece(const LinScan& a, long slot) {
+  return lin_piece(a.cu, a.S, a.T, a.L, a.slots_per_row, slot);
 }
 
 // lam^e in 64 bits (a log decay of -inf: 0 for e > 0, 1 for e = 0).
@@ -172,6 +176,22 @@ __device__ __forceinline__ LinDecay lin_split(double lam) {
   return LinDecay{hi, (float)(lam - (double)hi)};
 }
 __device__ __forceinline__ LinDecay lin_decay(float log_decay) { return lin_split(lin_power(log_decay, 1)); }
+
+// The one-token steps. Whether an earlier entry names entry e's slot, and the next
+// entry that does (batch if none). Each wave looks for itself: no barrier stands
+// between the state's loads and their use.
+__device__ __forceinline__ bool step_peers(const int32_t* slots, int batch, int e, int slot, int lane, int& next) {
+  next = batch;
+  bool before = false;
+  for (int i0 = 0; i0 < batch; i0 += 64) {
+    const int i = i0 + lane;
+    const bool same = i < batch && i != e && slots[i] == slot;
+    before |= __ballot(same && i < e) != 0;
+    const unsigned long long later = __ballot(same && i > e);
+    if (later && next == batch) next = i0 + __builtin_ctzll(later);
+  }
+  return before;
+}
 
 #endif
 

@@ -274,22 +274,6 @@ __device__ __forceinline__ f32x4 load4(const void* p, long i) {
   }
 }
 
-// Whether an earlier entry names entry e's slot, and the next entry that does
-// (a.batch if none). Each wave looks for itself: no barrier stands between the
-// state's loads and their use.
-__device__ __forceinline__ bool step_peers(const LinStep& a, int e, int slot, int lane, int& next) {
-  next = a.batch;
-  bool before = false;
-  for (int i0 = 0; i0 < a.batch; i0 += 64) {
-    const int i = i0 + lane;
-    const bool same = i < a.batch && i != e && a.slots[i] == slot;
-    before |= __ballot(same && i < e) != 0;
-    const unsigned long long later = __ballot(same && i > e);
-    if (later && next == a.batch) next = i0 + __builtin_ctzll(later);
-  }
-  return before;
-}
-
 template <bool BF16, int ROWS>
 __global__ __launch_bounds__(256) void lin_step_kernel(LinStep a, int tpr, int parts) {
   const int h = (int)(blockIdx.x / parts), part = (int)(blockIdx.x % parts);
@@ -319,7 +303,7 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStep a, int tpr, int p
     s[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(st + (long)min(r0 + j * rpp, a.dv - 1) * a.dk));
   const LinDecay lam = lin_decay(a.ld[h]);
   int next = a.batch;
-  if (a.slots && step_peers(a, e, slot, lane, next)) return;  // an earlier entry's workgroup runs this one
+  if (a.slots && step_peers(a.slots, a.batch, e, slot, lane, next)) return;  // an earlier entry's workgroup runs this one
   for (;;) {
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     const long ek = (long)e * a.Hk + hk, eh = (long)e * a.H + h;
@@ -348,7 +332,7 @@ __global__ __launch_bounds__(256) void lin_step_kernel(LinStep a, int tpr, int p
     }
     if (next == a.batch) break;
     e = next;
-    step_peers(a, e, slot, lane, next);
+    step_peers(a.slots, a.batch, e, slot, lane, next);
   }
 }
 
