@@ -28,7 +28,7 @@ struct Share {
   static constexpr int kBlocks = 2 * KB, kB = kBlocks >= 4 ? kBlocks / 4 : 1;
   static constexpr int kS = kBlocks >= 4 ? NV : (NV + 1) / 2;
   int wave, tb, group;
-  __device__ __forceinline__ explicit Share(int w) : wave(w), tb(w % kTb), group(w / kTb) {}
+  __device__ __forceinline__ explicit Share(int w) : wave(w), tb(w % kTb), group(kGroups > 1 ? w / kTb : 0) {}
   __device__ __forceinline__ int vb(int i) const { return group + kGroups * i; }
   __device__ __forceinline__ int kb(int i) const { return kBlocks >= 4 ? wave * kB + i : wave & 1; }
   __device__ __forceinline__ int sb(int i) const { return kBlocks >= 4 ? i : (wave >> 1) + 2 * i; }
@@ -75,17 +75,27 @@ __device__ __forceinline__ void read_state(const DeltaArgs& a, const float* from
       S[i][j] = in ? *reinterpret_cast<const f32x4*>(from + (long)dv * a.dk + dk) : f32x4{0.f, 0.f, 0.f, 0.f};
     }
 }
+// Bytes of this lane's pieces of a state from its start, kOffNone where they lie outside.
 template <int C, int KB, int NV>
-__device__ __forceinline__ void write_state(const DeltaArgs& a, float* to, int dv0, const Share<C, KB, NV>& w, int c16, int g,
-                                            const State<C, KB, NV>& S) {
+struct StatePieces {
+  uint32_t at[Share<C, KB, NV>::kB][Share<C, KB, NV>::kS];
+  __device__ __forceinline__ StatePieces(const DeltaArgs& a, int dv0, const Share<C, KB, NV>& w, int c16, int g) {
 #pragma unroll
-  for (int i = 0; i < w.kB; ++i)
+    for (int i = 0; i < w.kB; ++i)
 #pragma unroll
-    for (int j = 0; j < w.kS; ++j) {
-      const int dk = 16 * w.kb(i) + 4 * g, dv = dv0 + 16 * w.sb(j) + c16;
-      if (w.sb(j) < NV && dk < a.dk && dv < a.dv) *reinterpret_cast<f32x4*>(to + (long)dv * a.dk + dk) = S[i][j];
-    }
-}
+      for (int j = 0; j < w.kS; ++j) {
+        const int dk = 16 * w.kb(i) + 4 * g, dv = dv0 + 16 * w.sb(j) + c16;
+        at[i][j] = w.sb(j) < NV && dk < a.dk && dv < a.dv ? (uint32_t)((dv * a.dk + dk) * 4) : kOffNone;
+      }
+  }
+  __device__ __forceinline__ void store(const DeltaArgs& a, float* to, const State<C, KB, NV>& S) const {
+    const rsrc_t r = make_rsrc(to, (uint32_t)(a.dk * a.dv * 4));
+#pragma unroll
+    for (int i = 0; i < Share<C, KB, NV>::kB; ++i)
+#pragma unroll
+      for (int j = 0; j < Share<C, KB, NV>::kS; ++j) buf_store16(__builtin_bit_cast(u32x4, S[i][j]), r, at[i][j]);
+  }
+};
 // The state's terms in LDS, [term][16 NV][kPitchK].
 template <int C, int KB, int NV>
 __device__ __forceinline__ void stage_state(uint16_t* Sl, const Share<C, KB, NV>& w, int c16, int g, const State<C, KB, NV>& S) {
@@ -155,7 +165,24 @@ __global__ __launch_bounds__(kThreads, KB <= 4 ? 2 : 1) void delta_fwd_kernel(De
   Raw4<NX> vr[Sh::kV];
   u32x4 tf[kKp][kTerms], pf[KEEP ? 1 : kKp][kOut];
   float eg = 0.f, wt = 0.f, keep = 0.f;
-  const int krow = (int)a.k_row * kEsz, qrow = (int)a.q_row * kEsz, vrow = (int)a.v_row * kEsz;
+  // Byte offsets of this lane's pieces from a chunk's first row; rows behind the chunk lie behind its buffer's end.
+  const int krow = (int)a.k_row * kEsz, qrow = (int)a.q_row * kEsz, vrow = (int)a.v_row * kEsz, orow = a.H * a.dv * kEsz;
+  uint32_t kat[KB], qat[KB], vat[Sh::kV], oat[Sh::kV], uat[Sh::kV];
+#pragma unroll
+  for (int b = 0; b < KB; ++b) {
+    const int col = 32 * b + 8 * g;
+    kat[b] = col < a.dk ? (uint32_t)(tok * krow + col * kEsz) : kOffNone;
+    qat[b] = col < a.dk ? (uint32_t)(tok * qrow + col * kEsz) : kOffNone;
+  }
+#pragma unroll
+  for (int i = 0; i < Sh::kV; ++i) {
+    const int col = u.dv0 + 16 * w.vb(i) + 4 * g;
+    const bool in = w.vb(i) < NV && col < a.dv;
+    vat[i] = in ? (uint32_t)(tok * vrow + col * kEsz) : kOffNone;
+    oat[i] = in ? (uint32_t)(tok * orow + col * kEsz) : kOffNone;
+    uat[i] = in ? (uint32_t)((tok * a.dv + col) * 4) : kOffNone;
+  }
+  const StatePieces<C, KB, NV> pieces(a, u.dv0, w, c16, g);
   auto rows_of = [&](int c) { return min(C, u.len - c * C); };
   auto load_rows = [&](int c) {
     const int n = rows_of(c);
@@ -164,45 +191,41 @@ __global__ __launch_bounds__(kThreads, KB <= 4 ? 2 : 1) void delta_fwd_kernel(De
     const rsrc_t rq = chunk_rows(a.q, row0, a.q_row, (long)hk * a.dk, n, kEsz);
     const rsrc_t rv = chunk_rows(a.v, row0, a.v_row, (long)u.h * a.dv, n, kEsz);
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      const int col = 32 * b + 8 * g;
-      const bool in = tok < n && col < a.dk;
-      kr[b] = load8<NX>(rk, in ? (uint32_t)(tok * krow + col * kEsz) : kOffNone);
-      if (!KEEP) qr[b] = load8<NX>(rq, in ? (uint32_t)(tok * qrow + col * kEsz) : kOffNone);
-    }
+    for (int b = 0; b < KB; ++b) kr[b] = load8<NX>(rk, kat[b]);
 #pragma unroll
-    for (int i = 0; i < Sh::kV; ++i) {
-      const int col = u.dv0 + 16 * w.vb(i) + 4 * g;
-      vr[i] = load4<NX>(rv, tok < n && w.vb(i) < NV && col < a.dv ? (uint32_t)(tok * vrow + col * kEsz) : kOffNone);
-    }
+    for (int i = 0; i < Sh::kV; ++i) vr[i] = load4<NX>(rv, vat[i]);
     const float* gates = a.gates + ((u.slot0 + c) * a.H + u.h) * kGateRows * C;
     eg = gates[tok];
     wt = gates[C + tok];
     keep = gates[5 * C];
+#pragma unroll
+    for (int b = 0; b < (KEEP ? 0 : KB); ++b) qr[b] = load8<NX>(rq, qat[b]);
   };
+  // Operands above the diagonal are not used: the wave's last one again.
   auto load_t = [&](int c) {
     const uint16_t* at = a.tf + ((u.slot0 + c) * a.H + u.h) * operands(C, kTerms);
 #pragma unroll
-    for (int kp = 0; kp < kKp; ++kp)
-      if (kp <= w.tb / 2) load_operand<kTerms>(at + operand_at(C, kTerms, w.tb, kp), lane, tf[kp]);
+    for (int kp = 0; kp < kKp; ++kp) load_operand<kTerms>(at + operand_at(C, kTerms, w.tb, min(kp, w.tb / 2)), lane, tf[kp]);
   };
   auto load_p = [&](int c) {
     const uint16_t* at = a.pf + ((u.slot0 + c) * a.H + u.h) * operands(C, kOut);
 #pragma unroll
     for (int kp = 0; kp < (KEEP ? 0 : kKp); ++kp)
-      if (kp <= w.tb / 2) load_operand<kOut>(at + operand_at(C, kOut, w.tb, kp), lane, pf[kp]);
+      load_operand<kOut>(at + operand_at(C, kOut, w.tb, min(kp, w.tb / 2)), lane, pf[kp]);
   };
   if (u.chunks > 0) {
     load_rows(0);
     load_t(0);
     if (!KEEP) load_p(0);
   }
+  loads_done();
   __syncthreads();
 
   for (int c = 0; c < u.chunks; ++c) {
     const int n = rows_of(c);
     const long row0 = u.start + (long)c * C, sh = (u.slot0 + c) * a.H + u.h;
-    if (KEEP) write_state<C, KB, NV>(a, a.states + sh * mat, u.dv0, w, c16, g, S);
+    const int ahead = min(c + 1, u.chunks - 1);   // loaded without a branch, which would wait for the loads in flight
+    if (KEEP) pieces.store(a, a.states + sh * mat, S);
     // X = V - e^G (K S^T), and Q S^T: lane token c16, value columns 4 g + r.
     f32x4 X[Sh::kV], O[Sh::kV];
 #pragma unroll
@@ -236,7 +259,7 @@ __global__ __launch_bounds__(kThreads, KB <= 4 ? 2 : 1) void delta_fwd_kernel(De
       stage4<C, kTerms, kPitchV>(Xl, tok, 16 * w.vb(i) + 4 * g, X[i]);
     }
     const float wt_now = wt, keep_now = keep;
-    if (c + 1 < u.chunks) load_rows(c + 1);
+    load_rows(ahead);
     __syncthreads();
 
     // U = T diag(beta) X.
@@ -254,12 +277,9 @@ __global__ __launch_bounds__(kThreads, KB <= 4 ? 2 : 1) void delta_fwd_kernel(De
       }
       if (!KEEP) stage4<C, kOut, kPitchV>(Ul, tok, 16 * w.vb(i) + 4 * g, U[i]);
       stage4<C, kTerms, kPitchV>(Wl, tok, 16 * w.vb(i) + 4 * g, U[i] * wt_now);
-      if (KEEP) {
-        const int dv = u.dv0 + 16 * w.vb(i) + 4 * g;
-        if (dv < a.dv) *reinterpret_cast<f32x4*>(a.u + (sh * C + tok) * a.dv + dv) = U[i];
-      }
+      if (KEEP) buf_store16(__builtin_bit_cast(u32x4, U[i]), make_rsrc(a.u + sh * C * a.dv, (uint32_t)(C * a.dv * 4)), uat[i]);
     }
-    if (c + 1 < u.chunks) load_t(c + 1);
+    load_t(ahead);
     __syncthreads();
 
     // S = e^(G_C) S + (e^(G_C - G) U)^T K.
@@ -295,14 +315,13 @@ __global__ __launch_bounds__(kThreads, KB <= 4 ? 2 : 1) void delta_fwd_kernel(De
           tokens_operand<C, kOut, kPitchV>(Ul, kp, 16 * w.vb(i), lane, ut);
           O[i] = mma<kOut, kOut, kOut>(ut, pf[kp], O[i]);
         }
-        const int dv = u.dv0 + 16 * w.vb(i) + 4 * g;
-        store4<NX>(O[i], ro, tok < n && dv < a.dv ? (uint32_t)((tok * a.H * a.dv + dv) * kEsz) : kOffNone);
+        store4<NX>(O[i], ro, oat[i]);
       }
-      if (c + 1 < u.chunks) load_p(c + 1);
+      load_p(ahead);
     }
     __syncthreads();
   }
-  if (a.fin) write_state<C, KB, NV>(a, a.fin + ((long)u.seq * a.H + u.h) * mat, u.dv0, w, c16, g, S);
+  if (a.fin) pieces.store(a, a.fin + ((long)u.seq * a.H + u.h) * mat, S);
 }
 
 // The adjoint, from the last chunk to the first: U', dV, the gradients of the states before the chunks.
@@ -330,7 +349,23 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 2 : 1) void delta_re
   Raw4<NX> dor[Sh::kV];
   u32x4 tt[kKp][kTerms], pt[kKp][kTerms];
   float eg = 0.f, wt = 0.f, be = 0.f, keep = 0.f;
+  // Byte offsets of this lane's pieces from a chunk's first row; rows behind the chunk lie behind its buffer's end.
   const int krow = (int)a.k_row * kEsz, qrow = (int)a.q_row * kEsz, orow = a.H * a.dv * kEsz;
+  uint32_t kat[KB], qat[KB], oat[Sh::kV], uat[Sh::kV];
+#pragma unroll
+  for (int b = 0; b < KB; ++b) {
+    const int col = 32 * b + 8 * g;
+    kat[b] = col < a.dk ? (uint32_t)(tok * krow + col * kEsz) : kOffNone;
+    qat[b] = col < a.dk ? (uint32_t)(tok * qrow + col * kEsz) : kOffNone;
+  }
+#pragma unroll
+  for (int i = 0; i < Sh::kV; ++i) {
+    const int col = u.dv0 + 16 * w.vb(i) + 4 * g;
+    const bool in = w.vb(i) < NV && col < a.dv;
+    oat[i] = in ? (uint32_t)(tok * orow + col * kEsz) : kOffNone;
+    uat[i] = in ? (uint32_t)((tok * a.dv + col) * 4) : kOffNone;
+  }
+  const StatePieces<C, KB, NV> pieces(a, u.dv0, w, c16, g);
   auto rows_of = [&](int c) { return min(C, u.len - c * C); };
   auto load_rows = [&](int c) {
     const int n = rows_of(c);
@@ -339,28 +374,22 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 2 : 1) void delta_re
     const rsrc_t rq = chunk_rows(a.q, row0, a.q_row, (long)hk * a.dk, n, kEsz);
     const rsrc_t ro = chunk_rows(a.d_o, row0, (long)a.H * a.dv, (long)u.h * a.dv, n, kEsz);
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      const int col = 32 * b + 8 * g;
-      const bool in = tok < n && col < a.dk;
-      kr[b] = load8<NX>(rk, in ? (uint32_t)(tok * krow + col * kEsz) : kOffNone);
-      qr[b] = load8<NX>(rq, in ? (uint32_t)(tok * qrow + col * kEsz) : kOffNone);
-    }
+    for (int b = 0; b < KB; ++b) kr[b] = load8<NX>(rk, kat[b]);
 #pragma unroll
-    for (int i = 0; i < Sh::kV; ++i) {
-      const int col = u.dv0 + 16 * w.vb(i) + 4 * g;
-      dor[i] = load4<NX>(ro, tok < n && w.vb(i) < NV && col < a.dv ? (uint32_t)(tok * orow + col * kEsz) : kOffNone);
-    }
+    for (int i = 0; i < Sh::kV; ++i) dor[i] = load4<NX>(ro, oat[i]);
     const float* gates = a.gates + ((u.slot0 + c) * a.H + u.h) * kGateRows * C;
     eg = gates[tok];
     wt = gates[C + tok];
     be = gates[2 * C + tok];
     keep = gates[5 * C];
+#pragma unroll
+    for (int b = 0; b < KB; ++b) qr[b] = load8<NX>(rq, qat[b]);
   };
+  // Operands below the diagonal are not used: the wave's first one again.
   auto load_operands = [&](const uint16_t* from, int c, u32x4 (*to)[kTerms]) {
     const uint16_t* at = from + ((u.slot0 + c) * a.H + u.h) * operands(C, kTerms);
 #pragma unroll
-    for (int kp = 0; kp < kKp; ++kp)
-      if (kp >= w.tb / 2) load_operand<kTerms>(at + operand_at(C, kTerms, w.tb, kp), lane, to[kp]);
+    for (int kp = 0; kp < kKp; ++kp) load_operand<kTerms>(at + operand_at(C, kTerms, w.tb, max(kp, w.tb / 2)), lane, to[kp]);
   };
   auto stage_do = [&]() {
 #pragma unroll
@@ -373,12 +402,14 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 2 : 1) void delta_re
     load_operands(a.pt, u.chunks - 1, pt);
     stage_do();
   }
+  loads_done();
   __syncthreads();
 
   for (int c = u.chunks - 1; c >= 0; --c) {
     const int n = rows_of(c);
     const long row0 = u.start + (long)c * C, sh = (u.slot0 + c) * a.H + u.h;
-    write_state<C, KB, NV>(a, a.dstates + sh * mat, u.dv0, w, c16, g, L);
+    const int ahead = max(c - 1, 0);   // loaded without a branch, which would wait for the loads in flight
+    pieces.store(a, a.dstates + sh * mat, L);
     // Y = e^(G_C - G) (K L^T) + P^T dO.
     f32x4 Y[Sh::kV];
 #pragma unroll
@@ -416,10 +447,8 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 2 : 1) void delta_re
       stage4<C, kTerms, kPitchV>(Yl, tok, col, Y[i]);
     }
     const float eg_now = eg, be_now = be, keep_now = keep;
-    if (c > 0) {
-      load_rows(c - 1);
-      load_operands(a.pt, c - 1, pt);
-    }
+    load_rows(ahead);
+    load_operands(a.pt, ahead, pt);
     __syncthreads();
 
     // U' = T^T Y, dV = beta U'.
@@ -436,12 +465,11 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 2 : 1) void delta_re
         tokens_operand<C, kTerms, kPitchV>(Yl, kp, 16 * w.vb(i), lane, yt);
         U[i] = mma<kTerms, kTerms, kTerms>(yt, tt[kp], U[i]);
       }
-      const int dv = u.dv0 + 16 * w.vb(i) + 4 * g;
-      if (dv < a.dv) *reinterpret_cast<f32x4*>(a.ub + (sh * C + tok) * a.dv + dv) = U[i];
-      store4<NX>(U[i] * be_now, rv, tok < n && dv < a.dv ? (uint32_t)((tok * a.H * a.dv + dv) * kEsz) : kOffNone);
+      buf_store16(__builtin_bit_cast(u32x4, U[i]), make_rsrc(a.ub + sh * C * a.dv, (uint32_t)(C * a.dv * 4)), uat[i]);
+      store4<NX>(U[i] * be_now, rv, oat[i]);
       stage4<C, kTerms, kPitchV>(Xl, tok, 16 * w.vb(i) + 4 * g, U[i] * (-eg_now * be_now));
     }
-    if (c > 0) load_operands(a.tt, c - 1, tt);
+    load_operands(a.tt, ahead, tt);
     __syncthreads();
 
     // L = e^(G_C) L + scale (e^G dO)^T Q - (e^G beta U')^T K.
@@ -472,10 +500,10 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 2 : 1) void delta_re
       }
     }
     stage_state<C, KB, NV>(Ll, w, c16, g, L);
-    if (c > 0) stage_do();
+    stage_do();
     __syncthreads();
   }
-  if (a.dinit) write_state<C, KB, NV>(a, a.dinit + ((long)u.seq * a.H + u.h) * mat, u.dv0, w, c16, g, L);
+  if (a.dinit) pieces.store(a, a.dinit + ((long)u.seq * a.H + u.h) * mat, L);
 }
 
 // Value blocks a workgroup: with keys of 256, fp32 rows leave LDS for one.

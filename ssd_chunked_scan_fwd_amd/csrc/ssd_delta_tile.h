@@ -148,6 +148,10 @@ constexpr int kOperand = 512;   // elements
 __host__ __device__ constexpr long operands(int C, int n) { return (long)(C / 16) * (C / 32) * n * kOperand; }
 __device__ __forceinline__ long operand_at(int C, int n, int rb, int kp) { return ((long)rb * (C / 32) + kp) * n * kOperand; }
 
+// Everything loaded so far is there. Before a loop that loads ahead: the compiler's waits inside it are for the order
+// of its own loads then, not for that of the loads before it.
+__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }   // vmcnt(0)
+
 // LDS rows of 16 nv values that are read transposed: 24 values apart for nv = 1
 // (two workgroups a CU need the room), else an odd multiple of 32 bytes.
 __host__ __device__ constexpr int value_pitch(int nv) { return nv == 1 ? 24 : lds_pitch(16 * nv); }
