@@ -38,9 +38,9 @@ struct DeltaArgs {
   // sequence s slot floor(cu[s] / C) + s + c, of row r slot r * slots_per_row + c.
   long slots_per_row = 0, slots = 0;
   float* gates = nullptr;        // [slots][H][kGateRows][C]
-  uint16_t *tf = nullptr, *pf = nullptr;     // T diag(beta) and P, operands (ssd_delta_tile.h)
+  float *tf = nullptr, *pf = nullptr;     // T diag(beta) and P, operands (ssd_delta_tile.h)
   // Gradients.
-  uint16_t *tt = nullptr, *pt = nullptr;     // T^T and P^T, operands
+  float *tt = nullptr, *pt = nullptr;     // T^T and P^T, operands
   const void* d_o = nullptr;     // [tokens][H][dv]
   const float* dfin = nullptr;   // gradient of the last state, or null
   float* dinit = nullptr;        // of the first, or null
@@ -56,8 +56,7 @@ constexpr int delta_chunk(bool bf16) { return bf16 ? 64 : 32; }
 // Bytes of a chunk's workspace arrays, of one head.
 constexpr int kGateRows = 6;     // e^G, e^(G_C - G), beta, G as the sum of two floats, e^(G_C) (its first element)
 size_t delta_gates_bytes(bool bf16);
-size_t delta_tf_bytes(bool bf16);
-size_t delta_pf_bytes(bool bf16);   // of O's products; P^T of the gradients' has delta_tf_bytes
+size_t delta_matrix_bytes(bool bf16);   // of T, P and their transposes, each
 
 int delta_prep_threads();
 long delta_chain_blocks(const DeltaArgs& a, bool reverse);

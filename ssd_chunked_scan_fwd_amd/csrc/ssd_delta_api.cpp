@@ -99,12 +99,12 @@ DeltaLayout delta_layout(const ssd_delta_shape* s, const DeltaDims& d, bool back
     return o;
   };
   L.gates = take(units * ssd::delta_gates_bytes(bf16));
-  L.tf = take(units * ssd::delta_tf_bytes(bf16));
+  L.tf = take(units * ssd::delta_matrix_bytes(bf16));
   if (!backward) {
-    L.pf = take(units * ssd::delta_pf_bytes(bf16));
+    L.pf = take(units * ssd::delta_matrix_bytes(bf16));
   } else {
-    L.tt = take(units * ssd::delta_tf_bytes(bf16));
-    L.pt = take(units * ssd::delta_tf_bytes(bf16));
+    L.tt = take(units * ssd::delta_matrix_bytes(bf16));
+    L.pt = take(units * ssd::delta_matrix_bytes(bf16));
     L.states = take(units * mat);
     L.dstates = take(units * mat);
     L.u = take(units * rows);
@@ -200,8 +200,8 @@ ssd_status ssd_gated_delta_fwd(const void* q, const void* k, const void* v, cons
   a.fin = final_state;
   a.o = o;
   a.gates = reinterpret_cast<float*>(ws + L.gates);
-  a.tf = reinterpret_cast<uint16_t*>(ws + L.tf);
-  a.pf = reinterpret_cast<uint16_t*>(ws + L.pf);
+  a.tf = reinterpret_cast<float*>(ws + L.tf);
+  a.pf = reinterpret_cast<float*>(ws + L.pf);
   const hipError_t e = ssd::launch_delta_prep(a, false, (hipStream_t)stream);
   if (e != hipSuccess) return hip_status(e);
   return hip_status(ssd::launch_delta_fwd(a, false, (hipStream_t)stream));
@@ -242,9 +242,9 @@ ssd_status ssd_gated_delta_bwd(const void* q, const void* k, const void* v, cons
   a.scale = scale;
   a.init = initial_state;
   a.gates = floats(L.gates);
-  a.tf = reinterpret_cast<uint16_t*>(ws + L.tf);
-  a.tt = reinterpret_cast<uint16_t*>(ws + L.tt);
-  a.pt = reinterpret_cast<uint16_t*>(ws + L.pt);
+  a.tf = floats(L.tf);
+  a.tt = floats(L.tt);
+  a.pt = floats(L.pt);
   a.d_o = d_o;
   a.dfin = dfinal_state;
   a.dinit = dinitial_state;

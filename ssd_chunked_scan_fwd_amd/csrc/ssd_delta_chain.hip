@@ -1,26 +1,26 @@
 // ssd_delta_chain.hip -- the walk of the delta rule over the chunks of each
 // sequence, forwards and, for the gradients, backwards (formulas: ssd_delta.h).
 //
-// Columns of V, rows of the state, do not mix: a workgroup of four waves takes
-// NV blocks of 16 of them of one head and carries their state [16 NV][dk] in the
-// accumulators of its own products. What a chunk waits for is a chain of three
-// phases, each ending in a barrier:
-//     state times keys (a wave 16 tokens: X, or Y)  ->  times T  ->  state update
-//     (a wave a quarter of dk).
-// The longest chain of a call is its longest sequence's chunks times these three;
-// so the phases are cut over the waves of a workgroup and kept short, O is made
-// beside them, and the next chunk's rows and operands are loaded into the registers
-// of this one's as soon as these have been used.
+// Columns of V, rows of the state, do not mix: a workgroup takes NV blocks of 16
+// of them of one head. What a chunk waits for is a chain of three phases, each
+// ending in a barrier: state times keys (X, or Y)  ->  times T (U, or U')  ->  state
+// update. The longest chain of a call is its longest sequence's chunks times these
+// three, and few heads leave a SIMD one wave of it. So the phases are kept short:
+// four waves, the token waves, take the first two, 16 tokens each, and do nothing
+// else; four others, the state waves, hold the state in the accumulators of its
+// update, a quarter of dk each, and make what nothing waits for (O; backwards the
+// terms of dO) while the token waves work. The next chunk's rows and operands are
+// loaded into the registers of this one's as soon as these have been used.
 #include "ssd_delta_tile.h"
 
 namespace ssd {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;   // four token waves, four state waves
 
-// What a wave takes of 16 NV value columns and C tokens: in the products over
-// tokens block tb of 16 tokens and value blocks vb(0 .. kV - 1); of the state,
+// What wave w of four takes of 16 NV value columns and C tokens: in the products
+// over tokens block tb of 16 tokens and value blocks vb(0 .. kV - 1); of the state,
 // blocks of 16 key columns kb(0 .. kB - 1) and value blocks sb(0 .. kS - 1).
 template <int C, int KB, int NV>
 struct Share {
@@ -135,375 +135,486 @@ __device__ __forceinline__ void tokens_operand(const uint16_t* L, int kp, int co
 #pragma unroll
   for (int t = 0; t < N; ++t) out[t] = frag_k_rows_accpair(L + t * C * PITCH, PITCH, 32 * kp, col, lane);
 }
-template <int N>
-__device__ __forceinline__ void load_operand(const uint16_t* from, int lane, u32x4* out) {
+// The lane's pieces of a chunk, byte offsets from its first row: of rows of keys (row elements apart), 32 columns
+// a piece, and of rows of values, 16 columns a piece; kOffNone behind the columns. Rows behind the chunk lie behind
+// its buffer's end.
+template <int KB>
+struct KeyPieces {
+  uint32_t at[KB];
+  __device__ __forceinline__ KeyPieces(int tok, int g, long row, int end, int esz) {
 #pragma unroll
-  for (int t = 0; t < N; ++t) out[t] = *reinterpret_cast<const u32x4*>(from + t * kOperand + lane * 8);
+    for (int b = 0; b < KB; ++b) {
+      const int col = 32 * b + 8 * g;
+      at[b] = col < end ? (uint32_t)((tok * (int)row + col) * esz) : kOffNone;
+    }
+  }
+};
+template <int C, int KB, int NV>
+struct ValuePieces {
+  uint32_t at[Share<C, KB, NV>::kV];
+  __device__ __forceinline__ ValuePieces(const Share<C, KB, NV>& w, int tok, int g, int dv0, long row, int end, int esz) {
+#pragma unroll
+    for (int i = 0; i < Share<C, KB, NV>::kV; ++i) {
+      const int col = dv0 + 16 * w.vb(i) + 4 * g;
+      at[i] = w.vb(i) < NV && col < end ? (uint32_t)((tok * (int)row + col) * esz) : kOffNone;
+    }
+  }
+};
+// The state (N of its terms, value block vb) times rows of keys: lane token c16, value columns 4 g + r. The operands
+// of four pieces are on their way at once, and the terms' products are chains of their own.
+template <int KB, int NV, int NX, int N>
+__device__ __forceinline__ f32x4 state_times(const uint16_t* Sl, int vb, const u32x4 (*kt)[NX], int lane) {
+  constexpr int kPitchK = lds_pitch(32 * KB), kAtOnce = KB < 4 ? KB : 4;
+  f32x4 sum[N];
+#pragma unroll
+  for (int t = 0; t < N; ++t) sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int b0 = 0; b0 < KB; b0 += kAtOnce) {
+    u32x4 st[kAtOnce][N];
+#pragma unroll
+    for (int b = 0; b < kAtOnce; ++b)
+#pragma unroll
+      for (int t = 0; t < N; ++t) st[b][t] = frag_k_cols(Sl + t * 16 * NV * kPitchK, kPitchK, 16 * vb, 32 * (b0 + b), lane);
+#pragma unroll
+    for (int b = 0; b < kAtOnce; ++b)
+#pragma unroll
+      for (int t = 0; t < N; ++t) sum[t] = mma<1, NX, N>(&st[b][t], kt[b0 + b], t, sum[t]);
+  }
+  f32x4 x = sum[N - 1];
+#pragma unroll
+  for (int t = N - 2; t >= 0; --t) x += sum[t];
+  return x;
+}
+// S += M^T Y over the tokens 32 kp .., M rows of keys and Y of values in LDS.
+template <int C, int KB, int NV, int NX>
+__device__ __forceinline__ void state_update(const uint16_t* M, const uint16_t* Y, const Share<C, KB, NV>& w, int kp, int lane,
+                                             State<C, KB, NV>& S) {
+  using Sh = Share<C, KB, NV>;
+  constexpr int kPitchK = lds_pitch(32 * KB), kPitchV = value_pitch(NV);
+  u32x4 yt[Sh::kS][kTerms];
+#pragma unroll
+  for (int j = 0; j < Sh::kS; ++j)
+    if (w.sb(j) < NV) tokens_operand<C, kTerms, kPitchV>(Y, kp, 16 * w.sb(j), lane, yt[j]);
+#pragma unroll
+  for (int i = 0; i < Sh::kB; ++i) {
+    u32x4 mt[NX];
+    tokens_operand<C, NX, kPitchK>(M, kp, 16 * w.kb(i), lane, mt);
+#pragma unroll
+    for (int j = 0; j < Sh::kS; ++j)
+      if (w.sb(j) < NV) S[i][j] = mma<NX, kTerms, kTerms>(mt, yt[j], S[i][j]);
+  }
+}
+template <int C, int KB, int NV>
+__device__ __forceinline__ void scale_state(State<C, KB, NV>& S, float by) {
+#pragma unroll
+  for (int i = 0; i < Share<C, KB, NV>::kB; ++i)
+#pragma unroll
+    for (int j = 0; j < Share<C, KB, NV>::kS; ++j) S[i][j] *= by;
 }
 
 // NX: terms of an input. KEEP: for the gradients; the states before the chunks and U are written, not O.
 template <int C, int KB, int NV, int NX, bool KEEP>
-__global__ __launch_bounds__(kThreads, KB <= 4 ? 2 : 1) void delta_fwd_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fwd_kernel(DeltaArgs a) {
   using Sh = Share<C, KB, NV>;
   constexpr int kEsz = NX == 1 ? 2 : 4, kOut = out_terms(NX), kKp = C / 32;
   constexpr int kPitchK = lds_pitch(32 * KB), kPitchV = value_pitch(NV);
   __shared__ __align__(16) uint16_t Sl[kTerms * 16 * NV * kPitchK];
   __shared__ __align__(16) uint16_t Kl[NX * C * kPitchK];
-  __shared__ __align__(16) uint16_t Xl[kTerms * C * kPitchV], Wl[kTerms * C * kPitchV];
-  __shared__ __align__(16) uint16_t Ul[KEEP ? 8 : kOut * C * kPitchV];
-  const Sh w(uniform(threadIdx.x >> 6));
+  __shared__ __align__(16) uint16_t Xl[kTerms * C * kPitchV], Wl[kTerms * C * kPitchV];   // X; e^(G_C - G) U
+  constexpr int kU = kOut * C * kPitchV;
+  __shared__ __align__(16) uint16_t Ul[KEEP ? 8 : 2 * kU];   // U of this chunk and of the one before
+  const int wave = uniform(threadIdx.x >> 6);
+  const Sh w(wave & 3);
   const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
   const Unit u = delta_unit<C, NV>(a);
-  const int hk = u.h / (a.H / a.Hk), tok = 16 * w.tb + c16;
-  const long mat = (long)a.dk * a.dv;
-  State<C, KB, NV> S;
-  read_state<C, KB, NV>(a, a.init ? a.init + ((long)u.seq * a.H + u.h) * mat : nullptr, u.dv0, w, c16, g, S);
-  stage_state<C, KB, NV>(Sl, w, c16, g, S);
+  const int hk = u.h / (a.H / a.Hk), tok = 16 * w.tb + c16, last = u.chunks - 1;
+  const long mat = (long)a.dk * a.dv, sh0 = u.slot0 * a.H + u.h;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  auto rows = [&](const void* x, int c, long row, long col) {
+    return chunk_rows(x, u.start + (long)c * C, row, col, min(C, u.len - c * C), kEsz);
+  };
 
-  Raw8<NX> kr[KB], qr[KEEP ? 1 : KB];
-  Raw4<NX> vr[Sh::kV];
-  u32x4 tf[kKp][kTerms], pf[KEEP ? 1 : kKp][kOut];
-  float eg = 0.f, wt = 0.f, keep = 0.f;
-  // Byte offsets of this lane's pieces from a chunk's first row; rows behind the chunk lie behind its buffer's end.
-  const int krow = (int)a.k_row * kEsz, qrow = (int)a.q_row * kEsz, vrow = (int)a.v_row * kEsz, orow = a.H * a.dv * kEsz;
-  uint32_t kat[KB], qat[KB], vat[Sh::kV], oat[Sh::kV], uat[Sh::kV];
+  if (wave < 4) {
+    const KeyPieces<KB> kat(tok, g, a.k_row, a.dk, kEsz);
+    const ValuePieces<C, KB, NV> vat(w, tok, g, u.dv0, a.v_row, a.dv, kEsz), uat(w, tok, g, u.dv0, a.dv, a.dv, 4);
+    Raw8<NX> kr[KB];
+    Raw4<NX> vr[Sh::kV];
+    RawOperand tr[kKp];        // of the next chunk
+    u32x4 tf[kKp][kTerms];
+    float eg, wt, eg_next, wt_next;
+    auto load_rows = [&](int c) {
+      const rsrc_t rk = rows(a.k, c, a.k_row, (long)hk * a.dk), rv = rows(a.v, c, a.v_row, (long)u.h * a.dv);
 #pragma unroll
-  for (int b = 0; b < KB; ++b) {
-    const int col = 32 * b + 8 * g;
-    kat[b] = col < a.dk ? (uint32_t)(tok * krow + col * kEsz) : kOffNone;
-    qat[b] = col < a.dk ? (uint32_t)(tok * qrow + col * kEsz) : kOffNone;
-  }
+      for (int b = 0; b < KB; ++b) kr[b] = load8<NX>(rk, kat.at[b]);
 #pragma unroll
-  for (int i = 0; i < Sh::kV; ++i) {
-    const int col = u.dv0 + 16 * w.vb(i) + 4 * g;
-    const bool in = w.vb(i) < NV && col < a.dv;
-    vat[i] = in ? (uint32_t)(tok * vrow + col * kEsz) : kOffNone;
-    oat[i] = in ? (uint32_t)(tok * orow + col * kEsz) : kOffNone;
-    uat[i] = in ? (uint32_t)((tok * a.dv + col) * 4) : kOffNone;
-  }
-  const StatePieces<C, KB, NV> pieces(a, u.dv0, w, c16, g);
-  auto rows_of = [&](int c) { return min(C, u.len - c * C); };
-  auto load_rows = [&](int c) {
-    const int n = rows_of(c);
-    const long row0 = u.start + (long)c * C;
-    const rsrc_t rk = chunk_rows(a.k, row0, a.k_row, (long)hk * a.dk, n, kEsz);
-    const rsrc_t rq = chunk_rows(a.q, row0, a.q_row, (long)hk * a.dk, n, kEsz);
-    const rsrc_t rv = chunk_rows(a.v, row0, a.v_row, (long)u.h * a.dv, n, kEsz);
+      for (int i = 0; i < Sh::kV; ++i) vr[i] = load4<NX>(rv, vat.at[i]);
+    };
+    auto load_gates = [&](int c) {
+      const float* gates = a.gates + (sh0 + (long)c * a.H) * kGateRows * C;
+      eg_next = gates[tok];
+      wt_next = gates[C + tok];
+    };
+    auto next_gates = [&]() {
+      eg = eg_next;
+      wt = wt_next;
+    };
+    auto load_t = [&](int c) { load_operands<C>(a.tf, sh0 + (long)c * a.H, w.tb, 0, w.tb / 2, lane, tr); };
+    auto split_t = [&]() {
 #pragma unroll
-    for (int b = 0; b < KB; ++b) kr[b] = load8<NX>(rk, kat[b]);
+      for (int kp = 0; kp < kKp; ++kp) terms8<kTerms>(tr[kp], tf[kp]);
+    };
+    if (last >= 0) {
+      load_rows(0);
+      load_gates(0);
+      load_t(0);
+      split_t();
+      next_gates();
+      load_t(min(1, last));
+      load_gates(min(1, last));
+    }
+    loads_done();
+    __syncthreads();
+    for (int c = 0; c <= last; ++c) {
+      const int ahead = min(c + 1, last);
+      const long sh = sh0 + (long)c * a.H;
+      // X = V - e^G (K S^T): lane token c16, value columns 4 g + r.
+      f32x4 X[Sh::kV];
+      u32x4 kt[KB][NX];
 #pragma unroll
-    for (int i = 0; i < Sh::kV; ++i) vr[i] = load4<NX>(rv, vat[i]);
-    const float* gates = a.gates + ((u.slot0 + c) * a.H + u.h) * kGateRows * C;
-    eg = gates[tok];
-    wt = gates[C + tok];
-    keep = gates[5 * C];
-#pragma unroll
-    for (int b = 0; b < (KEEP ? 0 : KB); ++b) qr[b] = load8<NX>(rq, qat[b]);
-  };
-  // Operands above the diagonal are not used: the wave's last one again.
-  auto load_t = [&](int c) {
-    const uint16_t* at = a.tf + ((u.slot0 + c) * a.H + u.h) * operands(C, kTerms);
-#pragma unroll
-    for (int kp = 0; kp < kKp; ++kp) load_operand<kTerms>(at + operand_at(C, kTerms, w.tb, min(kp, w.tb / 2)), lane, tf[kp]);
-  };
-  auto load_p = [&](int c) {
-    const uint16_t* at = a.pf + ((u.slot0 + c) * a.H + u.h) * operands(C, kOut);
-#pragma unroll
-    for (int kp = 0; kp < (KEEP ? 0 : kKp); ++kp)
-      load_operand<kOut>(at + operand_at(C, kOut, w.tb, min(kp, w.tb / 2)), lane, pf[kp]);
-  };
-  if (u.chunks > 0) {
-    load_rows(0);
-    load_t(0);
-    if (!KEEP) load_p(0);
-  }
-  loads_done();
-  __syncthreads();
-
-  for (int c = 0; c < u.chunks; ++c) {
-    const int n = rows_of(c);
-    const long row0 = u.start + (long)c * C, sh = (u.slot0 + c) * a.H + u.h;
-    const int ahead = min(c + 1, u.chunks - 1);   // loaded without a branch, which would wait for the loads in flight
-    if (KEEP) pieces.store(a, a.states + sh * mat, S);
-    // X = V - e^G (K S^T), and Q S^T: lane token c16, value columns 4 g + r.
-    f32x4 X[Sh::kV], O[Sh::kV];
-#pragma unroll
-    for (int i = 0; i < Sh::kV; ++i) X[i] = O[i] = zero;
-#pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      u32x4 kt[NX], qt[NX];
-      terms8<NX>(kr[b], kt);
-      stage_rows<C, KB, NV, NX>(Kl, w, c16, g, b, kt);
-      if (!KEEP) terms8<NX>(qr[b], qt);
+      for (int b = 0; b < KB; ++b) terms8<NX>(kr[b], kt[b]);
 #pragma unroll
       for (int i = 0; i < Sh::kV; ++i) {
         if (w.vb(i) >= NV) continue;
-        u32x4 st[kTerms];
+        const f32x4 v = floats4<NX>(vr[i]);
+        X[i] = state_times<KB, NV, NX, kTerms>(Sl, w.vb(i), kt, lane);
 #pragma unroll
-        for (int t = 0; t < kTerms; ++t)
-          st[t] = frag_k_cols(Sl + t * 16 * NV * kPitchK, kPitchK, 16 * w.vb(i), 32 * b, lane);
-        X[i] = mma<kTerms, NX, kTerms>(st, kt, X[i]);
-        if (!KEEP) O[i] = mma<kOut, NX, kOut>(st, qt, O[i]);
+        for (int r = 0; r < 4; ++r) X[i][r] = fmaf(-eg, X[i][r], v[r]);
+        stage4<C, kTerms, kPitchV>(Xl, tok, 16 * w.vb(i) + 4 * g, X[i]);
       }
-    }
 #pragma unroll
-    for (int i = 0; i < Sh::kV; ++i) {
-      if (w.vb(i) >= NV) continue;
-      const f32x4 v = floats4<NX>(vr[i]);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        X[i][r] = fmaf(-eg, X[i][r], v[r]);
-        O[i][r] *= eg * a.scale;
-      }
-      stage4<C, kTerms, kPitchV>(Xl, tok, 16 * w.vb(i) + 4 * g, X[i]);
-    }
-    const float wt_now = wt, keep_now = keep;
-    load_rows(ahead);
-    __syncthreads();
+      for (int b = 0; b < KB; ++b) stage_rows<C, KB, NV, NX>(Kl, w, c16, g, b, kt[b]);
+      load_rows(ahead);
+      __syncthreads();
 
-    // U = T diag(beta) X.
-    f32x4 U[Sh::kV];
+      // U = T diag(beta) X.
+      f32x4 U[Sh::kV];
 #pragma unroll
-    for (int i = 0; i < Sh::kV; ++i) {
-      if (w.vb(i) >= NV) continue;
-      U[i] = zero;
+      for (int i = 0; i < Sh::kV; ++i) {
+        if (w.vb(i) >= NV) continue;
+        U[i] = zero;
 #pragma unroll
-      for (int kp = 0; kp < kKp; ++kp) {
-        if (kp > w.tb / 2) continue;
-        u32x4 xt[kTerms];
-        tokens_operand<C, kTerms, kPitchV>(Xl, kp, 16 * w.vb(i), lane, xt);
-        U[i] = mma<kTerms, kTerms, kTerms>(xt, tf[kp], U[i]);
+        for (int kp = 0; kp < kKp; ++kp) {
+          if (kp > w.tb / 2) continue;
+          u32x4 xt[kTerms];
+          tokens_operand<C, kTerms, kPitchV>(Xl, kp, 16 * w.vb(i), lane, xt);
+          U[i] = mma<kTerms, kTerms, kTerms>(xt, tf[kp], U[i]);
+        }
+        stage4<C, kTerms, kPitchV>(Wl, tok, 16 * w.vb(i) + 4 * g, U[i] * wt);
+        if (KEEP) buf_store16(__builtin_bit_cast(u32x4, U[i]), make_rsrc(a.u + sh * C * a.dv, (uint32_t)(C * a.dv * 4)), uat.at[i]);
+        else stage4<C, kOut, kPitchV>(Ul + (c & 1) * kU, tok, 16 * w.vb(i) + 4 * g, U[i]);
       }
-      if (!KEEP) stage4<C, kOut, kPitchV>(Ul, tok, 16 * w.vb(i) + 4 * g, U[i]);
-      stage4<C, kTerms, kPitchV>(Wl, tok, 16 * w.vb(i) + 4 * g, U[i] * wt_now);
-      if (KEEP) buf_store16(__builtin_bit_cast(u32x4, U[i]), make_rsrc(a.u + sh * C * a.dv, (uint32_t)(C * a.dv * 4)), uat[i]);
+      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);   // while the state is updated, and not before the barrier
+      split_t();
+      next_gates();
+      load_t(min(c + 2, last));
+      load_gates(min(c + 2, last));
+      __syncthreads();
     }
-    load_t(ahead);
-    __syncthreads();
-
-    // S = e^(G_C) S + (e^(G_C - G) U)^T K.
-#pragma unroll
-    for (int i = 0; i < Sh::kB; ++i)
-#pragma unroll
-      for (int j = 0; j < Sh::kS; ++j) S[i][j] *= keep_now;
-#pragma unroll
-    for (int kp = 0; kp < kKp; ++kp) {
-      u32x4 ut[Sh::kS][kTerms];
-#pragma unroll
-      for (int j = 0; j < Sh::kS; ++j)
-        if (w.sb(j) < NV) tokens_operand<C, kTerms, kPitchV>(Wl, kp, 16 * w.sb(j), lane, ut[j]);
-#pragma unroll
-      for (int i = 0; i < Sh::kB; ++i) {
-        u32x4 kt[NX];
-        tokens_operand<C, NX, kPitchK>(Kl, kp, 16 * w.kb(i), lane, kt);
-#pragma unroll
-        for (int j = 0; j < Sh::kS; ++j)
-          if (w.sb(j) < NV) S[i][j] = mma<NX, kTerms, kTerms>(kt, ut[j], S[i][j]);
-      }
-    }
+  } else {
+    const KeyPieces<KB> qat(tok, g, a.q_row, a.dk, kEsz);
+    const ValuePieces<C, KB, NV> oat(w, tok, g, u.dv0, (long)a.H * a.dv, a.dv, kEsz);
+    const StatePieces<C, KB, NV> pieces(a, u.dv0, w, c16, g);
+    State<C, KB, NV> S;
+    read_state<C, KB, NV>(a, a.init ? a.init + ((long)u.seq * a.H + u.h) * mat : nullptr, u.dv0, w, c16, g, S);
     stage_state<C, KB, NV>(Sl, w, c16, g, S);
-    if (!KEEP) {
-      const rsrc_t ro = chunk_rows(a.o, row0, (long)a.H * a.dv, (long)u.h * a.dv, n, kEsz);
+    Raw8<NX> qr[KEEP ? 1 : KB];
+    RawOperand pf[KEEP ? 1 : kKp];
+    f32x4 O[Sh::kV];
+    float eg = 0.f, keep = 0.f;
+    auto load_q = [&](int c) {
+      const float* gates = a.gates + (sh0 + (long)c * a.H) * kGateRows * C;
+      eg = gates[tok];
+      const rsrc_t rq = rows(a.q, c, a.q_row, (long)hk * a.dk);
+#pragma unroll
+      for (int b = 0; b < (KEEP ? 0 : KB); ++b) qr[b] = load8<NX>(rq, qat.at[b]);
+    };
+    auto load_keep = [&](int c) { keep = a.gates[((sh0 + (long)c * a.H) * kGateRows + 5) * C]; };
+    // O += P U of a chunk: while the token waves make U of the next.
+    auto finish = [&](int c) {
+      const rsrc_t ro = rows(a.o, c, (long)a.H * a.dv, (long)u.h * a.dv);
 #pragma unroll
       for (int i = 0; i < Sh::kV; ++i) {
         if (w.vb(i) >= NV) continue;
 #pragma unroll
         for (int kp = 0; kp < kKp; ++kp) {
           if (kp > w.tb / 2) continue;
-          u32x4 ut[kOut];
-          tokens_operand<C, kOut, kPitchV>(Ul, kp, 16 * w.vb(i), lane, ut);
-          O[i] = mma<kOut, kOut, kOut>(ut, pf[kp], O[i]);
+          u32x4 ut[kOut], pt[kOut];
+          tokens_operand<C, kOut, kPitchV>(Ul + (c & 1) * kU, kp, 16 * w.vb(i), lane, ut);
+          terms8<kOut>(pf[kp], pt);
+          O[i] = mma<kOut, kOut, kOut>(ut, pt, O[i]);
         }
-        store4<NX>(O[i], ro, oat[i]);
+        store4<NX>(O[i], ro, oat.at[i]);
       }
-      load_p(ahead);
+    };
+    if (last >= 0) {
+      load_keep(0);
+      if (!KEEP) load_q(0);
     }
+    loads_done();
     __syncthreads();
+    for (int c = 0; c <= last; ++c) {
+      const int ahead = min(c + 1, last);
+      f32x4 Q[Sh::kV];
+      if (KEEP) pieces.store(a, a.states + (sh0 + (long)c * a.H) * mat, S);
+      if constexpr (!KEEP) {   // scale e^G (Q S^T)
+        u32x4 qt[KB][NX];
+#pragma unroll
+        for (int b = 0; b < KB; ++b) terms8<NX>(qr[b], qt[b]);
+#pragma unroll
+        for (int i = 0; i < Sh::kV; ++i)
+          if (w.vb(i) < NV) Q[i] = state_times<KB, NV, NX, kOut>(Sl, w.vb(i), qt, lane) * (eg * a.scale);
+        load_q(ahead);
+      }
+      __syncthreads();
+      if constexpr (!KEEP) {
+        if (c > 0) finish(c - 1);
+        load_operands<C>(a.pf, sh0 + (long)c * a.H, w.tb, 0, w.tb / 2, lane, pf);
+#pragma unroll
+        for (int i = 0; i < Sh::kV; ++i) O[i] = Q[i];
+      }
+      scale_state<C, KB, NV>(S, keep);
+      load_keep(ahead);
+      __syncthreads();
+      // S = e^(G_C) S + (e^(G_C - G) U)^T K.
+#pragma unroll
+      for (int kp = 0; kp < kKp; ++kp) state_update<C, KB, NV, NX>(Kl, Wl, w, kp, lane, S);
+      stage_state<C, KB, NV>(Sl, w, c16, g, S);
+      __syncthreads();
+    }
+    if (!KEEP && last >= 0) finish(last);
+    if (a.fin) pieces.store(a, a.fin + ((long)u.seq * a.H + u.h) * mat, S);
   }
-  if (a.fin) pieces.store(a, a.fin + ((long)u.seq * a.H + u.h) * mat, S);
 }
 
-// The adjoint, from the last chunk to the first: U', dV, the gradients of the states before the chunks.
+// The adjoint, from the last chunk to the first: U', dV, the gradients of the states before the chunks. What the
+// state waves make ahead of the token waves: dO's terms of the state, (e^G dO)^T Q, while these make Y, and P^T dO
+// of the next chunk while they make U'.
 template <int C, int KB, int NV, int NX>
-__global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 2 : 1) void delta_rev_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
   using Sh = Share<C, KB, NV>;
   constexpr int kEsz = NX == 1 ? 2 : 4, kKp = C / 32;
-  constexpr int kPitchK = lds_pitch(32 * KB), kPitchV = value_pitch(NV);
+  constexpr int kPitchK = lds_pitch(32 * KB), kPitchV = value_pitch(NV), kPitchD = 16 * NV + 4;
   __shared__ __align__(16) uint16_t Ll[kTerms * 16 * NV * kPitchK];
   __shared__ __align__(16) uint16_t Kl[NX * C * kPitchK], Ql[NX * C * kPitchK];
-  __shared__ __align__(16) uint16_t Ol[NX * C * kPitchV];                                  // dO
+  __shared__ __align__(16) uint16_t Ol[NX * C * kPitchV];                                  // dO of the next chunk
   __shared__ __align__(16) uint16_t Gl[kTerms * C * kPitchV], Yl[kTerms * C * kPitchV];    // scale e^G dO; Y
   __shared__ __align__(16) uint16_t Xl[kTerms * C * kPitchV];                              // -e^G beta U'
-  const Sh w(uniform(threadIdx.x >> 6));
+  __shared__ __align__(16) float Dl[C * kPitchD];                                          // P^T dO
+  const int wave = uniform(threadIdx.x >> 6);
+  const Sh w(wave & 3);
   const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
   const Unit u = delta_unit<C, NV>(a);
-  const int hk = u.h / (a.H / a.Hk), tok = 16 * w.tb + c16;
-  const long mat = (long)a.dk * a.dv;
-  State<C, KB, NV> L;
-  read_state<C, KB, NV>(a, a.dfin ? a.dfin + ((long)u.seq * a.H + u.h) * mat : nullptr, u.dv0, w, c16, g, L);
-  stage_state<C, KB, NV>(Ll, w, c16, g, L);
+  const int hk = u.h / (a.H / a.Hk), tok = 16 * w.tb + c16, last = u.chunks - 1;
+  const long mat = (long)a.dk * a.dv, sh0 = u.slot0 * a.H + u.h;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  auto rows = [&](const void* x, int c, long row, long col) {
+    return chunk_rows(x, u.start + (long)c * C, row, col, min(C, u.len - c * C), kEsz);
+  };
 
-  Raw8<NX> kr[KB], qr[KB];
-  Raw4<NX> dor[Sh::kV];
-  u32x4 tt[kKp][kTerms], pt[kKp][kTerms];
-  float eg = 0.f, wt = 0.f, be = 0.f, keep = 0.f;
-  // Byte offsets of this lane's pieces from a chunk's first row; rows behind the chunk lie behind its buffer's end.
-  const int krow = (int)a.k_row * kEsz, qrow = (int)a.q_row * kEsz, orow = a.H * a.dv * kEsz;
-  uint32_t kat[KB], qat[KB], oat[Sh::kV], uat[Sh::kV];
+  if (wave < 4) {
+    const KeyPieces<KB> kat(tok, g, a.k_row, a.dk, kEsz);
+    const ValuePieces<C, KB, NV> vat(w, tok, g, u.dv0, (long)a.H * a.dv, a.dv, kEsz), uat(w, tok, g, u.dv0, a.dv, a.dv, 4);
+    Raw8<NX> kr[KB];
+    RawOperand tr[kKp];        // of the next chunk
+    u32x4 tt[kKp][kTerms];
+    float eg, wt, be, eg_next, wt_next, be_next;
+    auto load_rows = [&](int c) {
+      const rsrc_t rk = rows(a.k, c, a.k_row, (long)hk * a.dk);
 #pragma unroll
-  for (int b = 0; b < KB; ++b) {
-    const int col = 32 * b + 8 * g;
-    kat[b] = col < a.dk ? (uint32_t)(tok * krow + col * kEsz) : kOffNone;
-    qat[b] = col < a.dk ? (uint32_t)(tok * qrow + col * kEsz) : kOffNone;
-  }
+      for (int b = 0; b < KB; ++b) kr[b] = load8<NX>(rk, kat.at[b]);
+    };
+    auto load_gates = [&](int c) {
+      const float* gates = a.gates + (sh0 + (long)c * a.H) * kGateRows * C;
+      eg_next = gates[tok];
+      wt_next = gates[C + tok];
+      be_next = gates[2 * C + tok];
+    };
+    auto next_gates = [&]() {
+      eg = eg_next;
+      wt = wt_next;
+      be = be_next;
+    };
+    auto load_t = [&](int c) { load_operands<C>(a.tt, sh0 + (long)c * a.H, w.tb, w.tb / 2, kKp - 1, lane, tr); };
+    auto split_t = [&]() {
 #pragma unroll
-  for (int i = 0; i < Sh::kV; ++i) {
-    const int col = u.dv0 + 16 * w.vb(i) + 4 * g;
-    const bool in = w.vb(i) < NV && col < a.dv;
-    oat[i] = in ? (uint32_t)(tok * orow + col * kEsz) : kOffNone;
-    uat[i] = in ? (uint32_t)((tok * a.dv + col) * 4) : kOffNone;
-  }
-  const StatePieces<C, KB, NV> pieces(a, u.dv0, w, c16, g);
-  auto rows_of = [&](int c) { return min(C, u.len - c * C); };
-  auto load_rows = [&](int c) {
-    const int n = rows_of(c);
-    const long row0 = u.start + (long)c * C;
-    const rsrc_t rk = chunk_rows(a.k, row0, a.k_row, (long)hk * a.dk, n, kEsz);
-    const rsrc_t rq = chunk_rows(a.q, row0, a.q_row, (long)hk * a.dk, n, kEsz);
-    const rsrc_t ro = chunk_rows(a.d_o, row0, (long)a.H * a.dv, (long)u.h * a.dv, n, kEsz);
+      for (int kp = 0; kp < kKp; ++kp) terms8<kTerms>(tr[kp], tt[kp]);
+    };
+    if (last >= 0) {
+      load_rows(last);
+      load_gates(last);
+      load_t(last);
+      split_t();
+      next_gates();
+      load_t(max(last - 1, 0));
+      load_gates(max(last - 1, 0));
+    }
+    loads_done();
+    __syncthreads();
+    __syncthreads();
+    for (int c = last; c >= 0; --c) {
+      const int ahead = max(c - 1, 0);
+      const long sh = sh0 + (long)c * a.H;
+      // Y = e^(G_C - G) (K L^T) + P^T dO.
+      f32x4 Y[Sh::kV];
+      u32x4 kt[KB][NX];
 #pragma unroll
-    for (int b = 0; b < KB; ++b) kr[b] = load8<NX>(rk, kat[b]);
-#pragma unroll
-    for (int i = 0; i < Sh::kV; ++i) dor[i] = load4<NX>(ro, oat[i]);
-    const float* gates = a.gates + ((u.slot0 + c) * a.H + u.h) * kGateRows * C;
-    eg = gates[tok];
-    wt = gates[C + tok];
-    be = gates[2 * C + tok];
-    keep = gates[5 * C];
-#pragma unroll
-    for (int b = 0; b < KB; ++b) qr[b] = load8<NX>(rq, qat[b]);
-  };
-  // Operands below the diagonal are not used: the wave's first one again.
-  auto load_operands = [&](const uint16_t* from, int c, u32x4 (*to)[kTerms]) {
-    const uint16_t* at = from + ((u.slot0 + c) * a.H + u.h) * operands(C, kTerms);
-#pragma unroll
-    for (int kp = 0; kp < kKp; ++kp) load_operand<kTerms>(at + operand_at(C, kTerms, w.tb, max(kp, w.tb / 2)), lane, to[kp]);
-  };
-  auto stage_do = [&]() {
-#pragma unroll
-    for (int i = 0; i < Sh::kV; ++i)
-      if (w.vb(i) < NV) stage4<C, NX, kPitchV>(Ol, tok, 16 * w.vb(i) + 4 * g, floats4<NX>(dor[i]));
-  };
-  if (u.chunks > 0) {
-    load_rows(u.chunks - 1);
-    load_operands(a.tt, u.chunks - 1, tt);
-    load_operands(a.pt, u.chunks - 1, pt);
-    stage_do();
-  }
-  loads_done();
-  __syncthreads();
-
-  for (int c = u.chunks - 1; c >= 0; --c) {
-    const int n = rows_of(c);
-    const long row0 = u.start + (long)c * C, sh = (u.slot0 + c) * a.H + u.h;
-    const int ahead = max(c - 1, 0);   // loaded without a branch, which would wait for the loads in flight
-    pieces.store(a, a.dstates + sh * mat, L);
-    // Y = e^(G_C - G) (K L^T) + P^T dO.
-    f32x4 Y[Sh::kV];
-#pragma unroll
-    for (int i = 0; i < Sh::kV; ++i) Y[i] = zero;
-#pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      u32x4 kt[NX], qt[NX];
-      terms8<NX>(kr[b], kt);
-      terms8<NX>(qr[b], qt);
-      stage_rows<C, KB, NV, NX>(Kl, w, c16, g, b, kt);
-      stage_rows<C, KB, NV, NX>(Ql, w, c16, g, b, qt);
+      for (int b = 0; b < KB; ++b) terms8<NX>(kr[b], kt[b]);
 #pragma unroll
       for (int i = 0; i < Sh::kV; ++i) {
         if (w.vb(i) >= NV) continue;
-        u32x4 st[kTerms];
+        const int col = 16 * w.vb(i) + 4 * g;
+        const f32x4 d = *reinterpret_cast<const f32x4*>(Dl + tok * kPitchD + col);
+        Y[i] = state_times<KB, NV, NX, kTerms>(Ll, w.vb(i), kt, lane);
 #pragma unroll
-        for (int t = 0; t < kTerms; ++t)
-          st[t] = frag_k_cols(Ll + t * 16 * NV * kPitchK, kPitchK, 16 * w.vb(i), 32 * b, lane);
-        Y[i] = mma<kTerms, NX, kTerms>(st, kt, Y[i]);
+        for (int r = 0; r < 4; ++r) Y[i][r] = fmaf(wt, Y[i][r], d[r]);
+        stage4<C, kTerms, kPitchV>(Yl, tok, col, Y[i]);
       }
-    }
 #pragma unroll
-    for (int i = 0; i < Sh::kV; ++i) {
-      if (w.vb(i) >= NV) continue;
-      Y[i] *= wt;
-#pragma unroll
-      for (int kp = 0; kp < kKp; ++kp) {
-        if (kp < w.tb / 2) continue;
-        u32x4 ot[NX];
-        tokens_operand<C, NX, kPitchV>(Ol, kp, 16 * w.vb(i), lane, ot);
-        Y[i] = mma<NX, kTerms, kTerms>(ot, pt[kp], Y[i]);
-      }
-      const int col = 16 * w.vb(i) + 4 * g;
-      stage4<C, kTerms, kPitchV>(Gl, tok, col, floats4<NX>(dor[i]) * (eg * a.scale));
-      stage4<C, kTerms, kPitchV>(Yl, tok, col, Y[i]);
-    }
-    const float eg_now = eg, be_now = be, keep_now = keep;
-    load_rows(ahead);
-    load_operands(a.pt, ahead, pt);
-    __syncthreads();
+      for (int b = 0; b < KB; ++b) stage_rows<C, KB, NV, NX>(Kl, w, c16, g, b, kt[b]);
+      load_rows(ahead);
+      __syncthreads();
 
-    // U' = T^T Y, dV = beta U'.
-    f32x4 U[Sh::kV];
-    const rsrc_t rv = chunk_rows(a.dv_out, row0, (long)a.H * a.dv, (long)u.h * a.dv, n, kEsz);
+      // U' = T^T Y, dV = beta U'.
+      f32x4 U[Sh::kV];
+      const rsrc_t rv = rows(a.dv_out, c, (long)a.H * a.dv, (long)u.h * a.dv);
 #pragma unroll
-    for (int i = 0; i < Sh::kV; ++i) {
-      if (w.vb(i) >= NV) continue;
-      U[i] = zero;
+      for (int i = 0; i < Sh::kV; ++i) {
+        if (w.vb(i) >= NV) continue;
+        U[i] = zero;
 #pragma unroll
-      for (int kp = 0; kp < kKp; ++kp) {
-        if (kp < w.tb / 2) continue;
-        u32x4 yt[kTerms];
-        tokens_operand<C, kTerms, kPitchV>(Yl, kp, 16 * w.vb(i), lane, yt);
-        U[i] = mma<kTerms, kTerms, kTerms>(yt, tt[kp], U[i]);
-      }
-      buf_store16(__builtin_bit_cast(u32x4, U[i]), make_rsrc(a.ub + sh * C * a.dv, (uint32_t)(C * a.dv * 4)), uat[i]);
-      store4<NX>(U[i] * be_now, rv, oat[i]);
-      stage4<C, kTerms, kPitchV>(Xl, tok, 16 * w.vb(i) + 4 * g, U[i] * (-eg_now * be_now));
-    }
-    load_operands(a.tt, ahead, tt);
-    __syncthreads();
-
-    // L = e^(G_C) L + scale (e^G dO)^T Q - (e^G beta U')^T K.
-#pragma unroll
-    for (int i = 0; i < Sh::kB; ++i)
-#pragma unroll
-      for (int j = 0; j < Sh::kS; ++j) L[i][j] *= keep_now;
-#pragma unroll
-    for (int kp = 0; kp < kKp; ++kp) {
-      u32x4 gt[Sh::kS][kTerms], xt[Sh::kS][kTerms];
-#pragma unroll
-      for (int j = 0; j < Sh::kS; ++j) {
-        if (w.sb(j) >= NV) continue;
-        tokens_operand<C, kTerms, kPitchV>(Gl, kp, 16 * w.sb(j), lane, gt[j]);
-        tokens_operand<C, kTerms, kPitchV>(Xl, kp, 16 * w.sb(j), lane, xt[j]);
-      }
-#pragma unroll
-      for (int i = 0; i < Sh::kB; ++i) {
-        u32x4 kt[NX], qt[NX];
-        tokens_operand<C, NX, kPitchK>(Kl, kp, 16 * w.kb(i), lane, kt);
-        tokens_operand<C, NX, kPitchK>(Ql, kp, 16 * w.kb(i), lane, qt);
-#pragma unroll
-        for (int j = 0; j < Sh::kS; ++j) {
-          if (w.sb(j) >= NV) continue;
-          L[i][j] = mma<NX, kTerms, kTerms>(qt, gt[j], L[i][j]);
-          L[i][j] = mma<NX, kTerms, kTerms>(kt, xt[j], L[i][j]);
+        for (int kp = 0; kp < kKp; ++kp) {
+          if (kp < w.tb / 2) continue;
+          u32x4 yt[kTerms];
+          tokens_operand<C, kTerms, kPitchV>(Yl, kp, 16 * w.vb(i), lane, yt);
+          U[i] = mma<kTerms, kTerms, kTerms>(yt, tt[kp], U[i]);
         }
+        stage4<C, kTerms, kPitchV>(Xl, tok, 16 * w.vb(i) + 4 * g, U[i] * (-eg * be));
+        buf_store16(__builtin_bit_cast(u32x4, U[i]), make_rsrc(a.ub + sh * C * a.dv, (uint32_t)(C * a.dv * 4)), uat.at[i]);
+        store4<NX>(U[i] * be, rv, vat.at[i]);
       }
+      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);   // while the state is updated, and not before the barrier
+      split_t();
+      next_gates();
+      load_t(max(c - 2, 0));
+      load_gates(max(c - 2, 0));
+      __syncthreads();
     }
+  } else {
+    const KeyPieces<KB> qat(tok, g, a.q_row, a.dk, kEsz);
+    const ValuePieces<C, KB, NV> oat(w, tok, g, u.dv0, (long)a.H * a.dv, a.dv, kEsz);
+    const StatePieces<C, KB, NV> pieces(a, u.dv0, w, c16, g);
+    State<C, KB, NV> L;
+    read_state<C, KB, NV>(a, a.dfin ? a.dfin + ((long)u.seq * a.H + u.h) * mat : nullptr, u.dv0, w, c16, g, L);
     stage_state<C, KB, NV>(Ll, w, c16, g, L);
-    stage_do();
+    Raw8<NX> qr[KB];
+    Raw4<NX> d1[Sh::kV], d2[Sh::kV];   // dO of the chunk before the present one, and of the one before that
+    RawOperand pr[kKp];
+    float eg1 = 0.f, eg2 = 0.f, keep = 0.f;
+    auto load_do = [&](int c, Raw4<NX>* to, float& eg) {
+      const rsrc_t ro = rows(a.d_o, c, (long)a.H * a.dv, (long)u.h * a.dv);
+#pragma unroll
+      for (int i = 0; i < Sh::kV; ++i) to[i] = load4<NX>(ro, oat.at[i]);
+      eg = a.gates[(sh0 + (long)c * a.H) * kGateRows * C + tok];
+    };
+    auto load_q = [&](int c) {
+      const rsrc_t rq = rows(a.q, c, a.q_row, (long)hk * a.dk);
+#pragma unroll
+      for (int b = 0; b < KB; ++b) qr[b] = load8<NX>(rq, qat.at[b]);
+    };
+    auto load_p = [&](int c) { load_operands<C>(a.pt, sh0 + (long)c * a.H, w.tb, w.tb / 2, kKp - 1, lane, pr); };
+    auto load_keep = [&](int c) { keep = a.gates[((sh0 + (long)c * a.H) * kGateRows + 5) * C]; };
+    auto stage_q = [&]() {
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        u32x4 qt[NX];
+        terms8<NX>(qr[b], qt);
+        stage_rows<C, KB, NV, NX>(Ql, w, c16, g, b, qt);
+      }
+    };
+    auto stage_g = [&](const Raw4<NX>* x, float eg) {
+#pragma unroll
+      for (int i = 0; i < Sh::kV; ++i)
+        if (w.vb(i) < NV) stage4<C, kTerms, kPitchV>(Gl, tok, 16 * w.vb(i) + 4 * g, floats4<NX>(x[i]) * (eg * a.scale));
+    };
+    auto stage_o = [&](const Raw4<NX>* x) {
+#pragma unroll
+      for (int i = 0; i < Sh::kV; ++i)
+        if (w.vb(i) < NV) stage4<C, NX, kPitchV>(Ol, tok, 16 * w.vb(i) + 4 * g, floats4<NX>(x[i]));
+    };
+    auto scores = [&]() {   // P^T dO of the chunk whose dO is staged
+#pragma unroll
+      for (int i = 0; i < Sh::kV; ++i) {
+        if (w.vb(i) >= NV) continue;
+        f32x4 D = zero;
+#pragma unroll
+        for (int kp = 0; kp < kKp; ++kp) {
+          if (kp < w.tb / 2) continue;
+          u32x4 ot[NX], pt[kTerms];
+          tokens_operand<C, NX, kPitchV>(Ol, kp, 16 * w.vb(i), lane, ot);
+          terms8<kTerms>(pr[kp], pt);
+          D = mma<NX, kTerms, kTerms>(ot, pt, D);
+        }
+        *reinterpret_cast<f32x4*>(Dl + tok * kPitchD + 16 * w.vb(i) + 4 * g) = D;
+      }
+    };
+    if (last >= 0) {
+      load_do(last, d1, eg1);
+      load_q(last);
+      load_p(last);
+      load_keep(last);
+      stage_q();
+      stage_g(d1, eg1);
+      stage_o(d1);
+    }
     __syncthreads();
+    if (last >= 0) {
+      scores();
+      load_do(max(last - 1, 0), d1, eg1);
+      load_do(max(last - 2, 0), d2, eg2);
+      load_q(max(last - 1, 0));
+      load_p(max(last - 1, 0));
+    }
+    loads_done();
+    __syncthreads();
+    if (last >= 0) stage_o(d1);
+    for (int c = last; c >= 0; --c) {
+      pieces.store(a, a.dstates + (sh0 + (long)c * a.H) * mat, L);
+      // L = e^(G_C) L + scale (e^G dO)^T Q - (e^G beta U')^T K, the last term when U' is there.
+      scale_state<C, KB, NV>(L, keep);
+      load_keep(max(c - 1, 0));
+#pragma unroll
+      for (int kp = 0; kp < kKp; ++kp) state_update<C, KB, NV, NX>(Ql, Gl, w, kp, lane, L);
+      __syncthreads();
+      scores();
+      load_p(max(c - 2, 0));
+      __syncthreads();
+#pragma unroll
+      for (int kp = 0; kp < kKp; ++kp) state_update<C, KB, NV, NX>(Kl, Xl, w, kp, lane, L);
+      stage_state<C, KB, NV>(Ll, w, c16, g, L);
+      stage_q();
+      load_q(max(c - 2, 0));
+      stage_g(d1, eg1);
+      stage_o(d2);
+#pragma unroll
+      for (int i = 0; i < Sh::kV; ++i) d1[i] = d2[i];
+      eg1 = eg2;
+      load_do(max(c - 3, 0), d2, eg2);
+      __syncthreads();
+    }
+    if (a.dinit) pieces.store(a, a.dinit + ((long)u.seq * a.H + u.h) * mat, L);
   }
-  if (a.dinit) pieces.store(a, a.dinit + ((long)u.seq * a.H + u.h) * mat, L);
 }
 
 // Value blocks a workgroup: with keys of 256, fp32 rows leave LDS for one.

@@ -99,24 +99,20 @@ __device__ __forceinline__ void invert(const float* Am, float* Tm, int wave, int
 }
 
 // Operand (rb, kp) of a matrix, or of its transpose, its columns times w.
-template <int C, int N, bool TR>
-__device__ __forceinline__ void put_operand(const float* M, uint16_t* to, int rb, int kp, const float* w, int lane) {
+template <int C, bool TR>
+__device__ __forceinline__ void put_operand(const float* M, float* to, int rb, int kp, const float* w, int lane) {
   const int c16 = lane & 15, g = lane >> 4, row = 16 * rb + c16;
-  float x[8];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int col = 32 * kp + 16 * t + 4 * g;
+    f32x4 x;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      x[4 * t + r] = TR ? M[(col + r) * kPitch<C> + row] : M[row * kPitch<C> + col + r];
-      if (w) x[4 * t + r] *= w[col + r];
+      x[r] = TR ? M[(col + r) * kPitch<C> + row] : M[row * kPitch<C> + col + r];
+      if (w) x[r] *= w[col + r];
     }
+    *reinterpret_cast<f32x4*>(to + operand_at(C, rb, kp) + 256 * t + lane * 4) = x;
   }
-  u32x4 part[N];
-  split8<N>(x, part);
-  uint16_t* at = to + operand_at(C, N, rb, kp) + lane * 8;
-#pragma unroll
-  for (int t = 0; t < N; ++t) *reinterpret_cast<u32x4*>(at + t * kOperand) = part[t];
 }
 
 // The pairs of 16 rows and 16 columns on or below the diagonal that wave w takes: (row, column), -1: none.
@@ -139,7 +135,7 @@ __device__ __forceinline__ void tile_of(int wave, int e, int& ib, int& jb) {
 template <int C, int KB, int NX, bool BWD>
 __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(DeltaArgs a) {
   constexpr int kTiles = C == 64 ? 3 : 1;   // a wave
-  constexpr int kEsz = NX == 1 ? 2 : 4, kOut = out_terms(NX);
+  constexpr int kEsz = NX == 1 ? 2 : 4;
   __shared__ __align__(16) float Am[C * kPitch<C>], Tm[C * kPitch<C>], Pm[C * kPitch<C>];
   __shared__ __align__(16) float Gh[C], Gl[C], Be[C];
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
@@ -230,19 +226,16 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(DeltaArgs a) {
     invert<C>(Am, Tm, wave, lane);
     __syncthreads();
     // Operands on or below the diagonal, of the transposes on or above it.
-    uint16_t* tf = a.tf + sh * operands(C, kTerms);
-    uint16_t* pf = BWD ? nullptr : a.pf + sh * operands(C, kOut);
-    uint16_t* tt = BWD ? a.tt + sh * operands(C, kTerms) : nullptr;
-    uint16_t* pt = BWD ? a.pt + sh * operands(C, kTerms) : nullptr;
+    const long at = sh * operands(C);
     for (int t = wave; t < (C / 16) * (C / 32); t += 4) {
       const int rb = t / (C / 32), kp = t % (C / 32);
       if (kp <= rb / 2) {
-        put_operand<C, kTerms, false>(Tm, tf, rb, kp, Be, lane);
-        if (!BWD) put_operand<C, kOut, false>(Pm, pf, rb, kp, nullptr, lane);
+        put_operand<C, false>(Tm, a.tf + at, rb, kp, Be, lane);
+        if (!BWD) put_operand<C, false>(Pm, a.pf + at, rb, kp, nullptr, lane);
       }
       if (BWD && kp >= rb / 2) {
-        put_operand<C, kTerms, true>(Tm, tt, rb, kp, nullptr, lane);
-        put_operand<C, kTerms, true>(Pm, pt, rb, kp, nullptr, lane);
+        put_operand<C, true>(Tm, a.tt + at, rb, kp, nullptr, lane);
+        put_operand<C, true>(Pm, a.pt + at, rb, kp, nullptr, lane);
       }
     }
   }
@@ -260,8 +253,7 @@ void prep(const DeltaArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t delta_gates_bytes(bool bf16) { return (size_t)kGateRows * delta_chunk(bf16) * 4; }
-size_t delta_tf_bytes(bool bf16) { return (size_t)operands(delta_chunk(bf16), kTerms) * 2; }
-size_t delta_pf_bytes(bool bf16) { return (size_t)operands(delta_chunk(bf16), out_terms(bf16 ? 1 : 3)) * 2; }
+size_t delta_matrix_bytes(bool bf16) { return (size_t)operands(delta_chunk(bf16)) * 4; }
 int delta_prep_threads() { return kThreads; }
 
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stream) {

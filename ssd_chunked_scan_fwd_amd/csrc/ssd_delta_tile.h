@@ -62,6 +62,15 @@ __device__ __forceinline__ f32x4 mma(const u32x4* a, const u32x4* b, f32x4 acc) 
   return acc;
 }
 
+// acc += a b of one term of a, the i-th.
+template <int NA, int NB, int ORD>
+__device__ __forceinline__ f32x4 mma(const u32x4* a, const u32x4* b, int i, f32x4 acc) {
+#pragma unroll
+  for (int j = NB - 1; j >= 0; --j)
+    if (i + j < ORD) acc = mfma16x16x32(a[0], b[j], acc);
+  return acc;
+}
+
 // Eight values of a row as they come from memory, and as terms. NX: terms of an
 // input, 1 for bf16 and 3 for fp32.
 template <int NX>
@@ -141,12 +150,34 @@ __device__ __forceinline__ void store4(f32x4 x, rsrc_t r, uint32_t off) {
   else buf_store16(__builtin_bit_cast(u32x4, x), r, off);
 }
 
-// Operands of C x C matrices in the workspace: those of 16 rows and 32 columns
-// (columns in the order of an accumulator pair), `n` terms each of 64 lanes of 16
-// bytes, one behind the other.
-constexpr int kOperand = 512;   // elements
-__host__ __device__ constexpr long operands(int C, int n) { return (long)(C / 16) * (C / 32) * n * kOperand; }
-__device__ __forceinline__ long operand_at(int C, int n, int rb, int kp) { return ((long)rb * (C / 32) + kp) * n * kOperand; }
+// C x C matrices in the workspace, fp32, as operands of 16 rows and 32 columns (columns in the order of an
+// accumulator pair): 64 lanes of the columns 4 g .., then 64 of the columns 16 + 4 g ... In fp32 they are two thirds
+// of their terms, in memory and on the way through the first-level cache (64 bytes a cycle: a walk's rows and
+// operands of a chunk take a third of its time), and a triangle's zero operands are not loaded.
+constexpr int kOperand = 512;   // floats
+__host__ __device__ constexpr long operands(int C) { return (long)(C / 16) * (C / 32) * kOperand; }
+__device__ __forceinline__ int operand_at(int C, int rb, int kp) { return (rb * (C / 32) + kp) * kOperand; }
+struct RawOperand {
+  u32x4 w[2];
+};
+template <int N>
+__device__ __forceinline__ void terms8(const RawOperand& x, u32x4* out) {
+  float f[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) f[c] = __uint_as_float(x.w[c >> 2][c & 3]);
+  split8<N>(f, out);
+}
+// Row block rb of matrix sh; the operands from `least` to `most`, zeros in the place of the others.
+template <int C>
+__device__ __forceinline__ void load_operands(const float* from, long sh, int rb, int least, int most, int lane, RawOperand* to) {
+  const rsrc_t r = make_rsrc(from + sh * operands(C), (uint32_t)(operands(C) * 4));
+#pragma unroll
+  for (int kp = 0; kp < C / 32; ++kp) {
+    const uint32_t off = kp >= least && kp <= most ? (uint32_t)(operand_at(C, rb, kp) * 4 + lane * 16) : kOffNone;
+    to[kp].w[0] = buf_load16(r, off);
+    to[kp].w[1] = buf_load16(r, off + 1024);
+  }
+}
 
 // Everything loaded so far is there. Before a loop that loads ahead: the compiler's waits inside it are for the order
 // of its own loads then, not for that of the loads before it.
