@@ -1371,77 +1371,89 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", f
     return freq.float().to(device), scale
 
 
+def _row_of(shape, stride, name: str) -> int:
+    """Elements from token to token of [batch, seqlen, heads, d] or [batch, heads, d] (one row of tokens): heads and
+    their elements lie together, tokens at one distance, rows of the batch follow on."""
+    if len(shape) == 3:
+        shape, stride = (1,) + tuple(shape), (0,) + tuple(stride)
+    b, T, H, D = shape
+    if (D > 1 and stride[3] != 1) or (H > 1 and stride[2] != D):
+        raise ValueError(f"{name} must have its heads contiguous (strides {stride})")
+    if b * T * H * D == 0:
+        return H * D
+    row = stride[1] if T > 1 else (stride[0] if b > 1 else H * D)
+    if row < H * D or (b > 1 and stride[0] != T * row):
+        raise ValueError(f"{name} must have its tokens at one distance (strides {stride})")
+    return row
+
+
 @functools.lru_cache(maxsize=256)
-def _rotary_struct(*values) -> RotaryShape:
-    return RotaryShape(*values)
-
-
-def _rotary_rows(t: torch.Tensor, name: str, like: torch.Tensor) -> torch.Tensor:
-    """As [b, T, heads, dim]; a token an entry [b, heads, dim] counts as one row of b tokens."""
-    if not isinstance(t, torch.Tensor) or t.dim() != like.dim() or t.shape[:-2] != like.shape[:-2] or t.shape[-1] != like.shape[-1]:
-        raise ValueError(f"{name} must be a tensor [..., heads, {like.shape[-1]}] of q's leading sizes {tuple(like.shape[:-2])}")
-    if t.dtype != like.dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {like.dtype}")
-    return t if t.dim() == 4 else t.unsqueeze(0)
+def _rotary_struct(dtype, layout, inverse, entries, starts, q, k, q_out, k_out) -> RotaryShape:
+    """The C shape of tensors of these (shape, strides), checked against one another; once for each call's sizes, as a
+    token's call is its host's time. entries: frequencies; starts: entries of cu_seqlens, 0 without."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"q has dtype {dtype}; bfloat16 and float32 are supported")
+    if layout not in _ROTARY_LAYOUTS:
+        raise ValueError(f"layout {layout!r} must be half or interleaved")
+    shape = q[0]
+    if len(shape) not in (3, 4):
+        raise ValueError("q must be a tensor [batch, seqlen, heads, dim] or [batch, heads, dim]")
+    if k is not None and (len(k[0]) != len(shape) or k[0][:-2] != shape[:-2] or k[0][-1] != shape[-1]):
+        raise ValueError(f"k must be a tensor [..., heads, {shape[-1]}] of q's leading sizes {tuple(shape[:-2])}")
+    for name, src, out in (("q_out", q, q_out), ("k_out", k, k_out)):
+        if out is not None and (src is None or out[0] != src[0]):
+            raise ValueError(f"{name} must have the shape of what is turned")
+    b, T = (1, shape[0]) if len(shape) == 3 else shape[:2]
+    H, dim, Hk = shape[-2], shape[-1], 0 if k is None else k[0][-2]
+    if H < 1 or (k is not None and Hk < 1):
+        raise ValueError("q and k must have at least one head")
+    if starts == 1 or (starts and (len(shape) == 3 or b != 1)):
+        raise ValueError("cu_seqlens must have num_seqs + 1 >= 2 entries, for q [1, seqlen, heads, dim]")
+    if not 2 <= 2 * entries <= dim:
+        raise ValueError(f"freq has {entries} entries for heads of {dim}")
+    S = starts - 1 if starts else 0
+    _int32(dict(batch=b, seqlen=T, q_heads=H, k_heads=Hk, dim=dim, num_seqs=S))
+    row = lambda t, name: 0 if t is None else _row_of(*t, name)   # noqa: E731
+    # A batch without tokens runs nothing: its heads and sizes are checked as those of one token.
+    return RotaryShape(max(b, 1), max(T, 1), H, Hk, dim, 2 * entries, S, _dtype_code(dtype), _ROTARY_LAYOUTS[layout], inverse,
+                       row(q, "q"), row(k, "k"), row(q_out, "q_out"), row(k_out, "k_out"))
 
 
 def _rotary(q, k, freq, positions, cu_seqlens, offsets, layout, scale, q_out, k_out, inverse):
-    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
-        raise ValueError("q must be a tensor [batch, seqlen, heads, dim] or [batch, heads, dim]")
-    if q.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"q has dtype {q.dtype}; bfloat16 and float32 are supported")
-    if layout not in _ROTARY_LAYOUTS:
-        raise ValueError(f"layout {layout!r} must be half or interleaved")
-    if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
-        raise ValueError("freq must be a 1-d tensor of rot / 2 frequencies")
-    if k is None and k_out is not None:
-        raise ValueError("k_out without k")
-    step, dim, H = q.dim() == 3, q.shape[-1], q.shape[-2]
-    if step and positions is None:
-        raise ValueError("positions are required for one token an entry")
-    if step and cu_seqlens is not None:
-        raise ValueError("cu_seqlens needs q [1, seqlen, heads, dim]")
-    if positions is not None and offsets is not None:
+    for t, name, none in ((q, "q", False), (k, "k", True), (freq, "freq", False), (positions, "positions", True),
+                          (cu_seqlens, "cu_seqlens", True), (offsets, "offsets", True), (q_out, "q_out", True),
+                          (k_out, "k_out", True)):
+        if not (isinstance(t, torch.Tensor) or (none and t is None)):
+            raise ValueError(f"{name} must be a torch tensor")
+    if freq.dim() != 1 or (cu_seqlens is not None and cu_seqlens.dim() != 1):
+        raise ValueError("freq and cu_seqlens must be 1-d tensors")
+    if positions is None:
+        if q.dim() == 3:
+            raise ValueError("positions are required for one token an entry")
+    elif offsets is not None:
         raise ValueError("positions and offsets exclude each other")
-    q4 = _rotary_rows(q, "q", q)
-    k4 = None if k is None else _rotary_rows(k, "k", q)
-    b, T = q4.shape[:2]
-    Hk = 0 if k is None else k4.shape[2]
-    if H < 1 or (k is not None and Hk < 1):
-        raise ValueError("q and k must have at least one head")
-    S = 0
-    if cu_seqlens is not None:
-        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-            raise ValueError("cu_seqlens must be a 1-d tensor of num_seqs + 1 >= 2 entries")
-        if b != 1:
-            raise ValueError("packed sequences (cu_seqlens) need batch 1")
-        S = cu_seqlens.numel() - 1
-    _int32(dict(batch=b, seqlen=T, q_heads=H, k_heads=Hk, dim=dim, num_seqs=S))
-    rot = 2 * freq.numel()
-    if not 2 <= rot <= dim:
-        raise ValueError(f"freq has {freq.numel()} entries for heads of {dim}")
+    of = lambda t: None if t is None else (t.shape, t.stride())   # noqa: E731
+    dtype, device, e = q.dtype, q.device, q.element_size()
+    shape = _rotary_struct(dtype, layout, inverse, freq.numel(), 0 if cu_seqlens is None else cu_seqlens.numel(), of(q), of(k),
+                           of(q_out), of(k_out))
+    index = device.index if device.type == "cuda" else -1
+    for t, name in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out")):
+        if t is not None and not (t.dtype == dtype and t.get_device() == index >= 0 and t.data_ptr() % e == 0):
+            if t.dtype != dtype:
+                raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+            _expect_device([(t, name)], device, e)
+    _check(device, ((freq, "freq", None, torch.float32, 4), (positions, "positions", q.shape[:-2], torch.int32, 4),
+                    (cu_seqlens, "cu_seqlens", None, torch.int32, 4),
+                    (offsets, "offsets", None if offsets is None else (shape.num_seqs or q.shape[0],), torch.int32, 4)))
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty(q.shape, dtype=dtype, device=device)
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    for t, name, src in ((q_out, "q_out", q), (k_out, "k_out", k)):
-        if t is not None and (not isinstance(t, torch.Tensor) or t.shape != src.shape):
-            raise ValueError(f"{name} must have shape {tuple(src.shape)}")
-    q_to = _rotary_rows(q_out, "q_out", q)
-    k_to = None if k is None else _rotary_rows(k_out, "k_out", q)
-    e = q.element_size()
-    _check(q.device, ((q, "q", None, None, e), (k, "k", None, None, e), (q_out, "q_out", None, None, e),
-                      (k_out, "k_out", None, None, e), (freq, "freq", None, torch.float32, 4),
-                      (positions, "positions", q.shape[:-2], torch.int32, 4), (cu_seqlens, "cu_seqlens", None, torch.int32, 4),
-                      (offsets, "offsets", (S or b,), torch.int32, 4)))
-    rows = lambda t, name: 0 if t is None else _token_row(t, name)   # noqa: E731
-    shape = _rotary_struct(max(b, 1), max(T, 1), H, Hk, dim, rot, S, _dtype_code(q.dtype), _ROTARY_LAYOUTS[layout], inverse,
-                           rows(q4, "q"), rows(k4, "k"), rows(q_to, "q_out"), rows(k_to, "k_out"))
-    if b * T == 0:
+        k_out = torch.empty(k.shape, dtype=dtype, device=device)
+    if q.numel() == 0:
         _check_scale(scale)
         return q_out, k_out
-    _call_on(q.device, "ssd_rotary", _addr(q), _addr(k), _addr(freq), _addr(positions), _addr(cu_seqlens), _addr(offsets),
-             float(scale), _addr(q_out), _addr(k_out), ctypes.byref(shape))
+    _call_on(device, "ssd_rotary", q.data_ptr(), _addr(k), freq.data_ptr(), _addr(positions), _addr(cu_seqlens), _addr(offsets),
+             float(scale), q_out.data_ptr(), _addr(k_out), ctypes.byref(shape))
     return q_out, k_out
 
 

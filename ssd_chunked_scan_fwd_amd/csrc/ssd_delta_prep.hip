@@ -4,14 +4,15 @@
 // One workgroup takes a chunk of one query and key head and, one after the
 // other, the value heads that share it: K K^T and Q K^T are formed once, on
 // matrix instructions, and stay in registers.
-// The inverse is taken by blocks, in fp32 throughout (matrix instructions on
-// fp32): diagonal blocks of 16 by substitution, a lane a column, and twice
-// T21 = -T22 A21 T11. That is substitution in another order, whose error is that
-// of 32-bit sums for any A; sums of powers of A, which would need no
+// The inverse is taken by blocks, in place in LDS, in fp32 throughout (matrix
+// instructions on fp32): diagonal blocks of 16 by substitution, a lane a column, and
+// twice T21 = -T22 A21 T11. That is substitution in another order, whose error is
+// that of 32-bit sums for any A; sums of powers of A, which would need no
 // substitution, cancel to nothing when keys repeat (A^32 of 64 equal keys
 // reaches 10^17).
 // T (with beta of its columns folded in) and P are stored as the operands that
-// the walk over the chunks loads, and for the gradients their transposes.
+// the walk over the chunks loads, and for the gradients their transposes. A tile of
+// P is such an operand as its accumulators hold it.
 #include "ssd_delta_tile.h"
 
 namespace ssd {
@@ -56,32 +57,40 @@ __device__ __forceinline__ void put_cols(float* M, int rb, int cb, int c16, int 
   for (int r = 0; r < 4; ++r) M[(16 * rb + 4 * g + r) * kPitch<C> + 16 * cb + c16] = -x[r];
 }
 
-// Tm := (I + Am)^-1, lower triangles. Tm's blocks above the diagonal are zero.
+// M := (I + M)^-1, lower triangles; M's blocks above the diagonal are zero.
 template <int C>
-__device__ __forceinline__ void invert(const float* Am, float* Tm, int wave, int lane) {
+__device__ __forceinline__ void invert(float* M, int wave, int lane) {
   const int c16 = lane & 15, g = lane >> 4;
   if (wave == 0 && lane < C) {
     float t[16];
-    const float* A = Am + 16 * g * kPitch<C> + 16 * g;
-    float* out = Tm + 16 * g * kPitch<C> + 16 * g + c16;
+    float* A = M + 16 * g * kPitch<C> + 16 * g;
+    f32x4 row[3][4];   // two rows ahead
+    auto load = [&](int i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (4 * j < i && i < 16) row[i % 3][j] = *reinterpret_cast<const f32x4*>(A + i * kPitch<C> + 4 * j);
+    };
+    load(1);
+    load(2);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      f32x4 row[4];
+      float x = c16 == i ? 1.f : 0.f, y = 0.f;   // two chains
 #pragma unroll
-      for (int j = 0; 4 * j < i; ++j) row[j] = *reinterpret_cast<const f32x4*>(A + i * kPitch<C> + 4 * j);
-      float x = c16 == i ? 1.f : 0.f;
-#pragma unroll
-      for (int j = 0; j < i; ++j) x = fmaf(-row[j >> 2][j & 3], t[j], x);
-      t[i] = x;
-      out[i * kPitch<C>] = x;
+      for (int j = 0; j < i; ++j) {
+        float& to = j & 1 ? y : x;
+        to = fmaf(-row[i % 3][j >> 2][j & 3], t[j], to);
+      }
+      t[i] = x + y;
+      load(i + 3);
+      A[i * kPitch<C> + c16] = t[i];
     }
   }
   __syncthreads();
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   if (wave < C / 32) {
     const int lo = 2 * wave, hi = lo + 1;
-    const f32x4 R = mfma_f32(block_rows<C>(Am, hi, lo, c16, g), block_cols<C>(Tm, lo, lo, c16, g), zero);
-    put_cols<C>(Tm, hi, lo, c16, g, mfma_f32(block_rows<C>(Tm, hi, hi, c16, g), R, zero));
+    const f32x4 R = mfma_f32(block_rows<C>(M, hi, lo, c16, g), block_cols<C>(M, lo, lo, c16, g), zero);
+    put_cols<C>(M, hi, lo, c16, g, mfma_f32(block_rows<C>(M, hi, hi, c16, g), R, zero));
   }
   if constexpr (C == 64) {
     __syncthreads();
@@ -91,10 +100,11 @@ __device__ __forceinline__ void invert(const float* Am, float* Tm, int wave, int
     for (int m = 0; m < 2; ++m) {
       f32x4 R = zero;
 #pragma unroll
-      for (int n = 0; n < 2; ++n) R = mfma_f32(block_rows<C>(Am, 2 + m, n, c16, g), block_cols<C>(Tm, n, jc, c16, g), R);
-      x = mfma_f32(block_rows<C>(Tm, 2 + ir, 2 + m, c16, g), R, x);
+      for (int n = 0; n < 2; ++n) R = mfma_f32(block_rows<C>(M, 2 + m, n, c16, g), block_cols<C>(M, n, jc, c16, g), R);
+      x = mfma_f32(block_rows<C>(M, 2 + ir, 2 + m, c16, g), R, x);
     }
-    put_cols<C>(Tm, 2 + ir, jc, c16, g, x);
+    __syncthreads();   // all have read what is replaced
+    put_cols<C>(M, 2 + ir, jc, c16, g, x);
   }
 }
 
@@ -133,11 +143,17 @@ __device__ __forceinline__ void tile_of(int wave, int e, int& ib, int& jb) {
 }
 
 template <int C, int KB, int NX, bool BWD>
-__global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kThreads, 3) void delta_prep_kernel(DeltaArgs a) {
   constexpr int kTiles = C == 64 ? 3 : 1;   // a wave
   constexpr int kEsz = NX == 1 ? 2 : 4;
-  __shared__ __align__(16) float Am[C * kPitch<C>], Tm[C * kPitch<C>], Pm[C * kPitch<C>];
-  __shared__ __align__(16) float Gh[C], Gl[C], Be[C];
+  // Rows of K and Q, kSlab pieces of 32 columns at a time, and in their place the matrix.
+  constexpr int kSlab = NX == 1 ? (KB < 4 ? KB : 4) : (KB < 2 ? KB : 2), kPitchK = lds_pitch(32 * kSlab);
+  constexpr int kRows = NX * C * kPitchK, kBytes = 4 * kRows > 4 * C * kPitch<C> ? 4 * kRows : 4 * C * kPitch<C>;
+  __shared__ __align__(16) char shared[kBytes];
+  uint16_t* const Kl = reinterpret_cast<uint16_t*>(shared);
+  uint16_t* const Ql = Kl + kRows;
+  float* const Am = reinterpret_cast<float*>(shared);
+  __shared__ __align__(16) float Gh[4][C], Gl[4][C], Be[4][C];   // of four heads at a time
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
   const long unit = xcd_unit(blockIdx.x, gridDim.x);
   const int hk = (int)(unit % a.Hk);
@@ -148,60 +164,39 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(DeltaArgs a) {
   const rsrc_t rk = chunk_rows(a.k, ch.row0, a.k_row, (long)hk * a.dk, n, kEsz);
   const rsrc_t rq = chunk_rows(a.q, ch.row0, a.q_row, (long)hk * a.dk, n, kEsz);
   const int krow = (int)a.k_row * kEsz, qrow = (int)a.q_row * kEsz;
-  for (int i = threadIdx.x; i < C * kPitch<C>; i += kThreads) Tm[i] = Pm[i] = 0.f;
-
-  f32x4 kk[kTiles], qk[kTiles];   // of queries and keys i (columns c16) and keys j (rows 4 g + r)
+  float gx = 0.f, bx = 0.f;   // the gates of this lane's token, of head m0 + wave
+  auto load_gates = [&](int m0) {
+    const long at = (ch.row0 + min(lane, n - 1)) * a.H + hk * rep + min(m0 + wave, rep - 1);
+    if (a.g) gx = a.g[at];
+    bx = a.beta[at];
+  };
+  load_gates(0);
+  // Of keys j (rows 4 g + r) and queries or keys i (columns c16); BWD: Q K^T the other way round, as its transpose is stored.
+  f32x4 kk[kTiles], qk[kTiles];
 #pragma unroll
-  for (int e = 0; e < kTiles; ++e) {
-    kk[e] = qk[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-    int ib, jb;
-    tile_of<C>(wave, e, ib, jb);
-    if (ib < 0) continue;
-    const int i = 16 * ib + c16, j = 16 * jb + c16;
-    Raw8<NX> xi[KB], xj[KB], xq[KB];
+  for (int e = 0; e < kTiles; ++e) kk[e] = qk[e] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      const int col = 32 * b + 8 * g;
-      const bool in = col < a.dk;
-      xi[b] = load8<NX>(rk, in && i < n ? (uint32_t)(i * krow + col * kEsz) : kOffNone);
-      xj[b] = load8<NX>(rk, in && j < n ? (uint32_t)(j * krow + col * kEsz) : kOffNone);
-      xq[b] = load8<NX>(rq, in && i < n ? (uint32_t)(i * qrow + col * kEsz) : kOffNone);
+  for (int s0 = 0; s0 < KB; s0 += kSlab) {
+    if (s0 > 0) __syncthreads();
+    // A wave's 16 rows of K and of Q; with 32 tokens of one of the two. Rows behind the chunk lie behind the buffers' ends.
+    Raw8<NX> xk[kSlab], xq[kSlab];
+    const int rb = wave % (C / 16), row = 16 * rb + c16;
+    const bool of_k = C == 64 || wave < 2, of_q = C == 64 || wave >= 2;
+#pragma unroll
+    for (int b = 0; b < kSlab; ++b) {
+      const int col = 32 * (s0 + b) + 8 * g;
+      xk[b] = load8<NX>(rk, of_k && col < a.dk ? (uint32_t)(row * krow + col * kEsz) : kOffNone);
+      xq[b] = load8<NX>(rq, of_q && col < a.dk ? (uint32_t)(row * qrow + col * kEsz) : kOffNone);
     }
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      u32x4 ti[NX], tj[NX], tq[NX];
-      terms8<NX>(xi[b], ti);
-      terms8<NX>(xj[b], tj);
+    for (int b = 0; b < kSlab; ++b) {
+      u32x4 tk[NX], tq[NX];
+      terms8<NX>(xk[b], tk);
       terms8<NX>(xq[b], tq);
-      kk[e] = mma<NX, NX, NX>(tj, ti, kk[e]);
-      qk[e] = mma<NX, NX, NX>(tj, tq, qk[e]);
-    }
-  }
-
-  for (int m = 0; m < rep; ++m) {
-    const int h = hk * rep + m;
-    const long sh = slot * a.H + h;
-    float* gates = a.gates + sh * kGateRows * C;
-    if (m > 0) __syncthreads();   // the last head's operands are out
-    if (wave == 0) {
-      const bool in = lane < n;
-      const long at = (ch.row0 + min(lane, n - 1)) * a.H + h;
-      // Below -200 a decay is 0 in fp32, as e^-200 is, and its sums stay finite.
-      float x = in && a.g ? a.g[at] : 0.f;
-      x = x < -200.f ? -200.f : x;
-      const float be = in ? a.beta[at] : 0.f;
-      const double G = lanes_up((double)x, lane), end = __shfl(G, C - 1);
-      if (lane < C) {
-        const float hi = (float)G, lo = (float)(G - (double)hi);
-        Gh[lane] = hi;
-        Gl[lane] = lo;
-        Be[lane] = be;
-        gates[lane] = (float)exp(G);
-        gates[C + lane] = in ? (float)exp(end - G) : 0.f;
-        gates[2 * C + lane] = be;
-        gates[3 * C + lane] = hi;
-        gates[4 * C + lane] = lo;
-        if (lane == 0) gates[5 * C] = (float)exp(end);
+#pragma unroll
+      for (int t = 0; t < NX; ++t) {
+        if (of_k) *reinterpret_cast<u32x4*>(Kl + (t * C + row) * kPitchK + 32 * b + 8 * g) = tk[t];
+        if (of_q) *reinterpret_cast<u32x4*>(Ql + (t * C + row) * kPitchK + 32 * b + 8 * g) = tq[t];
       }
     }
     __syncthreads();
@@ -210,33 +205,91 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(DeltaArgs a) {
       int ib, jb;
       tile_of<C>(wave, e, ib, jb);
       if (ib < 0) continue;
+#pragma unroll
+      for (int b = 0; b < kSlab; ++b) {
+        u32x4 ti[NX], tj[NX], tq[NX];
+#pragma unroll
+        for (int t = 0; t < NX; ++t) {
+          ti[t] = frag_k_cols(Kl + t * C * kPitchK, kPitchK, 16 * ib, 32 * b, lane);
+          tj[t] = frag_k_cols(Kl + t * C * kPitchK, kPitchK, 16 * jb, 32 * b, lane);
+          tq[t] = frag_k_cols(Ql + t * C * kPitchK, kPitchK, 16 * ib, 32 * b, lane);
+        }
+        kk[e] = mma<NX, NX, NX>(tj, ti, kk[e]);
+        qk[e] = BWD ? mma<NX, NX, NX>(tq, tj, qk[e]) : mma<NX, NX, NX>(tj, tq, qk[e]);
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < C * kPitch<C>; i += kThreads) Am[i] = 0.f;
+
+  for (int m = 0; m < rep; ++m) {
+    const int h = hk * rep + m, mw = m & 3;
+    const long sh = slot * a.H + h, at = sh * operands(C);
+    if (m > 0) __syncthreads();   // the last head's operands are out
+    if (mw == 0) {
+      if (m + wave < rep) {
+        float* gates = a.gates + (sh + wave) * kGateRows * C;
+        const bool in = lane < n;
+        // Below -200 a decay is 0 in fp32, as e^-200 is, and its sums stay finite.
+        const float x = !in ? 0.f : gx < -200.f ? -200.f : gx, be = in ? bx : 0.f;
+        const double G = lanes_up((double)x, lane), end = __shfl(G, C - 1);
+        if (lane < C) {
+          const float hi = (float)G, lo = (float)(G - (double)hi);
+          Gh[wave][lane] = hi;
+          Gl[wave][lane] = lo;
+          Be[wave][lane] = be;
+          const double left = end - G;
+          const float lh = (float)left, ll = (float)(left - (double)lh);
+          gates[lane] = expf(hi) * (1.f + lo);
+          gates[C + lane] = in ? expf(lh) * (1.f + ll) : 0.f;
+          gates[2 * C + lane] = be;
+          gates[3 * C + lane] = hi;
+          gates[4 * C + lane] = lo;
+          if (lane == C - 1) gates[5 * C] = expf(hi) * (1.f + lo);
+        }
+      }
+      if (m + 4 < rep) load_gates(m + 4);
+      __syncthreads();
+    }
+    const float *gh = Gh[mw], *gl = Gl[mw], *bt = Be[mw];
+#pragma unroll
+    for (int e = 0; e < kTiles; ++e) {
+      int ib, jb;
+      tile_of<C>(wave, e, ib, jb);
+      if (ib < 0) continue;
       const int i = 16 * ib + c16, j = 16 * jb + 4 * g;
-      const float hi = Gh[i], lo = Gl[i], be = Be[i];
+      f32x4 d;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) d[r] = j + r <= i ? expf((gh[i] - gh[j + r]) + (gl[i] - gl[j + r])) : 0.f;
       f32x4 A, P;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float d = j + r <= i ? expf((hi - Gh[j + r]) + (lo - Gl[j + r])) : 0.f;
-        A[r] = j + r < i ? be * d * kk[e][r] : 0.f;
-        P[r] = j + r <= i ? a.scale * d * qk[e][r] : 0.f;
-      }
+      for (int r = 0; r < 4; ++r) A[r] = j + r < i ? bt[i] * d[r] * kk[e][r] : 0.f;
       *reinterpret_cast<f32x4*>(Am + i * kPitch<C> + j) = A;
-      *reinterpret_cast<f32x4*>(Pm + i * kPitch<C> + j) = P;
+      const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+      if (BWD) {
+        const int i4 = 16 * ib + 4 * g, j1 = 16 * jb + c16;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          P[r] = j1 <= i4 + r ? a.scale * expf((gh[i4 + r] - gh[j1]) + (gl[i4 + r] - gl[j1])) * qk[e][r] : 0.f;
+        float* to = a.pt + at + lane * 4;
+        *reinterpret_cast<f32x4*>(to + operand_at(C, jb, ib / 2) + 256 * (ib & 1)) = P;
+        if (ib == jb && (ib & 1)) *reinterpret_cast<f32x4*>(to + operand_at(C, jb, ib / 2)) = zero;
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) P[r] = j + r <= i ? a.scale * d[r] * qk[e][r] : 0.f;
+        float* to = a.pf + at + lane * 4;
+        *reinterpret_cast<f32x4*>(to + operand_at(C, ib, jb / 2) + 256 * (jb & 1)) = P;
+        if (ib == jb && !(ib & 1)) *reinterpret_cast<f32x4*>(to + operand_at(C, ib, jb / 2) + 256) = zero;
+      }
     }
     __syncthreads();
-    invert<C>(Am, Tm, wave, lane);
+    invert<C>(Am, wave, lane);
     __syncthreads();
-    // Operands on or below the diagonal, of the transposes on or above it.
-    const long at = sh * operands(C);
+    // Operands on or below the diagonal, of the transpose on or above it.
     for (int t = wave; t < (C / 16) * (C / 32); t += 4) {
       const int rb = t / (C / 32), kp = t % (C / 32);
-      if (kp <= rb / 2) {
-        put_operand<C, false>(Tm, a.tf + at, rb, kp, Be, lane);
-        if (!BWD) put_operand<C, false>(Pm, a.pf + at, rb, kp, nullptr, lane);
-      }
-      if (BWD && kp >= rb / 2) {
-        put_operand<C, true>(Tm, a.tt + at, rb, kp, nullptr, lane);
-        put_operand<C, true>(Pm, a.pt + at, rb, kp, nullptr, lane);
-      }
+      if (kp <= rb / 2) put_operand<C, false>(Am, a.tf + at, rb, kp, bt, lane);
+      if (BWD && kp >= rb / 2) put_operand<C, true>(Am, a.tt + at, rb, kp, nullptr, lane);
     }
   }
 }
