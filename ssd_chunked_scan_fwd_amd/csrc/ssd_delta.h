@@ -38,9 +38,16 @@ struct DeltaArgs {
   // sequence s slot floor(cu[s] / C) + s + c, of row r slot r * slots_per_row + c.
   long slots_per_row = 0, slots = 0;
   float* gates = nullptr;        // [slots][H][kGateRows][C]
-  float *tf = nullptr, *pf = nullptr;     // T diag(beta) and P, operands (ssd_delta_tile.h)
+  float* tf = nullptr;           // T diag(beta) and
+  uint16_t* pf = nullptr;        // P, operands (ssd_delta_tile.h)
+  // Sequences cut into segments of `seg` chunks (0: not cut), numbered as chunks are, by which one long sequence
+  // of few heads fills the card (ssd_delta_chain.hip).
+  int seg = 0;
+  long segs_per_row = 0, segs = 0;
+  float* seg_states = nullptr;   // [segs][H][dv][dk]: a segment's own last state, then the state behind it
+  float* seg_maps = nullptr;     // [segs][H][dk][dk]: what the segment makes of a state's row
   // Gradients.
-  float *tt = nullptr, *pt = nullptr;     // T^T and P^T, operands
+  float *tt = nullptr, *pt = nullptr;            // T^T and P^T, operands
   const void* d_o = nullptr;     // [tokens][H][dv]
   const float* dfin = nullptr;   // gradient of the last state, or null
   float* dinit = nullptr;        // of the first, or null
@@ -56,16 +63,21 @@ constexpr int delta_chunk(bool bf16) { return bf16 ? 64 : 32; }
 // Bytes of a chunk's workspace arrays, of one head.
 constexpr int kGateRows = 6;     // e^G, e^(G_C - G), beta, G as the sum of two floats, e^(G_C) (its first element)
 size_t delta_gates_bytes(bool bf16);
-size_t delta_matrix_bytes(bool bf16);   // of T, P and their transposes, each
+size_t delta_tf_bytes(bool bf16);   // of T and the transposes, each
+size_t delta_pf_bytes(bool bf16);
+
+// Chunks a segment of a forward walk over these sizes, 0: no sequence is cut.
+int delta_segment(int batch, int T, int S, int H, int dk, int dv, bool bf16);
 
 int delta_prep_threads();
-long delta_chain_blocks(const DeltaArgs& a, bool reverse);
+long delta_chain_blocks(const DeltaArgs& a);
+long delta_segment_blocks(const DeltaArgs& a);   // of the segments' own states and maps
 int delta_chain_threads();
 long delta_bwd_blocks(const DeltaArgs& a);
 int delta_bwd_threads();
 
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stream);
-hipError_t launch_delta_fwd(const DeltaArgs& a, bool keep, hipStream_t stream);   // keep: states and u instead of o
+hipError_t launch_delta_fwd(const DeltaArgs& a, bool keep, hipStream_t stream);   // keep: states and u instead of o, not cut
 hipError_t launch_delta_rev(const DeltaArgs& a, hipStream_t stream);
 hipError_t launch_delta_grads(const DeltaArgs& a, hipStream_t stream);
 

@@ -17,8 +17,8 @@ namespace {
 // ---------------------------------------------------------------- gated delta rule
 
 struct DeltaDims {
-  int64_t q_row, k_row, v_row, tokens, nseq, spr, slots;
-  int esz;
+  int64_t q_row, k_row, v_row, tokens, nseq, spr, slots, segs_per_row, segs;
+  int esz, seg;
 };
 
 ssd_status check_delta_heads(const ssd_delta_shape* s) {
@@ -46,6 +46,9 @@ ssd::DeltaArgs delta_args(const ssd_delta_shape* s, const DeltaDims& d) {
   a.bf16 = s->dtype == SSD_DTYPE_BF16;
   a.slots_per_row = (long)d.spr;
   a.slots = (long)d.slots;
+  a.seg = d.seg;
+  a.segs_per_row = (long)d.segs_per_row;
+  a.segs = (long)d.segs;
   return a;
 }
 
@@ -73,19 +76,22 @@ ssd_status check_delta(const ssd_delta_shape* s, DeltaDims* d, bool backward) {
   const int C = ssd::delta_chunk(s->dtype == SSD_DTYPE_BF16);
   d->spr = ssd::lin_slots_per_row(s->seqlen, s->num_seqs, C);
   d->slots = s->num_seqs > 0 ? d->spr : d->spr * s->batch;
+  d->seg = backward ? 0 : ssd::delta_segment(s->batch, s->seqlen, s->num_seqs, s->nheads, s->dk, s->dv, s->dtype == SSD_DTYPE_BF16);
+  d->segs_per_row = d->seg ? ssd::lin_slots_per_row(s->seqlen, s->num_seqs, d->seg * C) : 0;
+  d->segs = s->num_seqs > 0 ? d->segs_per_row : d->segs_per_row * s->batch;
   const ssd::DeltaArgs a = delta_args(s, *d);
   if (!ssd::launchable(a.slots * a.Hk, ssd::delta_prep_threads()) ||
-      !ssd::launchable(ssd::delta_chain_blocks(a, false), ssd::delta_chain_threads()))
+      !ssd::launchable(ssd::delta_chain_blocks(a), ssd::delta_chain_threads()) ||
+      !ssd::launchable(ssd::delta_segment_blocks(a), ssd::delta_chain_threads()))
     return SSD_ERR_UNSUPPORTED;
-  if (backward && (!ssd::launchable(ssd::delta_chain_blocks(a, true), ssd::delta_chain_threads()) ||
-                   !ssd::launchable(ssd::delta_bwd_blocks(a), ssd::delta_bwd_threads()) ||
+  if (backward && (!ssd::launchable(ssd::delta_bwd_blocks(a), ssd::delta_bwd_threads()) ||
                    !ssd::launchable(d->tokens * s->nqk_heads * (s->dk / 8) / 256 + 1, 256)))
     return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
 }
 
 struct DeltaLayout {
-  size_t gates, tf, pf, tt, pt, states, dstates, u, ub, part_q, part_k, total;
+  size_t gates, tf, pf, seg_states, seg_maps, tt, pt, states, dstates, u, ub, part_q, part_k, total;
 };
 DeltaLayout delta_layout(const ssd_delta_shape* s, const DeltaDims& d, bool backward) {
   DeltaLayout L{};
@@ -99,12 +105,14 @@ DeltaLayout delta_layout(const ssd_delta_shape* s, const DeltaDims& d, bool back
     return o;
   };
   L.gates = take(units * ssd::delta_gates_bytes(bf16));
-  L.tf = take(units * ssd::delta_matrix_bytes(bf16));
+  L.tf = take(units * ssd::delta_tf_bytes(bf16));
   if (!backward) {
-    L.pf = take(units * ssd::delta_matrix_bytes(bf16));
+    L.pf = take(units * ssd::delta_pf_bytes(bf16));
+    L.seg_states = take((size_t)d.segs * s->nheads * mat);
+    L.seg_maps = take((size_t)d.segs * s->nheads * s->dk * s->dk * 4);
   } else {
-    L.tt = take(units * ssd::delta_matrix_bytes(bf16));
-    L.pt = take(units * ssd::delta_matrix_bytes(bf16));
+    L.tt = take(units * ssd::delta_tf_bytes(bf16));
+    L.pt = take(units * ssd::delta_tf_bytes(bf16));
     L.states = take(units * mat);
     L.dstates = take(units * mat);
     L.u = take(units * rows);
@@ -201,7 +209,9 @@ ssd_status ssd_gated_delta_fwd(const void* q, const void* k, const void* v, cons
   a.o = o;
   a.gates = reinterpret_cast<float*>(ws + L.gates);
   a.tf = reinterpret_cast<float*>(ws + L.tf);
-  a.pf = reinterpret_cast<float*>(ws + L.pf);
+  a.pf = reinterpret_cast<uint16_t*>(ws + L.pf);
+  a.seg_states = reinterpret_cast<float*>(ws + L.seg_states);
+  a.seg_maps = reinterpret_cast<float*>(ws + L.seg_maps);
   const hipError_t e = ssd::launch_delta_prep(a, false, (hipStream_t)stream);
   if (e != hipSuccess) return hip_status(e);
   return hip_status(ssd::launch_delta_fwd(a, false, (hipStream_t)stream));
@@ -242,7 +252,7 @@ ssd_status ssd_gated_delta_bwd(const void* q, const void* k, const void* v, cons
   a.scale = scale;
   a.init = initial_state;
   a.gates = floats(L.gates);
-  a.tf = floats(L.tf);
+  a.tf = reinterpret_cast<float*>(ws + L.tf);
   a.tt = floats(L.tt);
   a.pt = floats(L.pt);
   a.d_o = d_o;

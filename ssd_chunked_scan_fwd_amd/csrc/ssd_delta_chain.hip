@@ -11,6 +11,9 @@
 // update, a quarter of dk each, and make what nothing waits for (O; backwards the
 // terms of dO) while the token waves work. The next chunk's rows and operands are
 // loaded into the registers of this one's as soon as these have been used.
+#include <algorithm>
+#include <cmath>
+
 #include "ssd_delta_tile.h"
 
 namespace ssd {
@@ -34,29 +37,58 @@ struct Share {
   __device__ __forceinline__ int sb(int i) const { return kBlocks >= 4 ? i : (wave >> 1) + 2 * i; }
 };
 
+// What a workgroup walks: columns dv0 .. of one head over a sequence, or over one of its segments. Of a segment's own
+// states, after those of its value columns, the rows of its map: V = 0, and the rows of the unit matrix as the state
+// before it.
 struct Unit {
-  int dv0, h, seq, len, chunks;
+  int dv0, h, len, chunks, rows;   // rows of the state
   long start, slot0;
+  bool map, none;
+  const float* from;               // the state before, null: zero
+  float* to;                       // the state behind, null: not wanted
 };
-template <int C, int NV>
-__device__ __forceinline__ Unit delta_unit(const DeltaArgs& a) {
+template <int C, int NV, bool OWN>
+__device__ __forceinline__ Unit delta_unit(const DeltaArgs& a, const float* init, float* fin) {
   Unit u;
-  const int tiles = (a.dv + 16 * NV - 1) / (16 * NV);
-  const long id = xcd_unit(blockIdx.x, gridDim.x);
-  u.dv0 = (int)(id % tiles) * 16 * NV;
+  const int values = (a.dv + 16 * NV - 1) / (16 * NV), tiles = values + (OWN ? (a.dk + 16 * NV - 1) / (16 * NV) : 0);
+  const long id = xcd_unit(blockIdx.x, gridDim.x), mat = (long)a.dk * a.dv, map = (long)a.dk * a.dk;
+  const int tile = (int)(id % tiles);
   u.h = (int)((id / tiles) % a.H);
-  u.seq = (int)(id / ((long)tiles * a.H));
-  if (a.cu) {
-    const int c0 = min(max(a.cu[u.seq], 0), a.T), c1 = min(max(a.cu[u.seq + 1], c0), a.T);
-    u.start = c0;
-    u.len = c1 - c0;
-    u.slot0 = (long)c0 / C + u.seq;
-  } else {
-    u.start = (long)u.seq * a.T;
-    u.len = a.T;
-    u.slot0 = (long)u.seq * a.slots_per_row;
+  const long n = id / ((long)tiles * a.H);   // sequence or segment
+  u.map = OWN && tile >= values;
+  u.dv0 = (u.map ? tile - values : tile) * 16 * NV;
+  u.rows = u.map ? a.dk : a.dv;
+  u.none = false;
+  const LinPiece p = lin_piece(a.cu, a.S, a.T, a.seg ? a.seg * C : max(a.T, 1), a.seg ? a.segs_per_row : 1, n);
+  const int blk = a.seg ? p.blk : 0;
+  LinPiece q = p;
+  if (!a.seg) {   // n is the sequence
+    q.seq = (int)n;
+    if (a.cu) {
+      const int c0 = min(max(a.cu[n], 0), a.T);
+      q.start = c0;
+      q.len = min(max(a.cu[n + 1], c0), a.T) - c0;
+    }
   }
+  if (blk < 0) {
+    u.none = true;
+    return u;
+  }
+  const long first = (long)blk * a.seg * C;
+  u.len = a.seg ? (int)min((long)q.len - first, (long)a.seg * C) : q.len;
   u.chunks = (u.len + C - 1) / C;
+  u.start = q.start + first;
+  u.slot0 = (a.cu ? q.start / C + q.seq : (long)q.seq * a.slots_per_row) + first / C;
+  const bool last = first + u.len >= q.len;
+  const long sh = (long)q.seq * a.H + u.h;
+  if (OWN) {
+    u.none = last || (u.map && blk == 0);   // nothing comes behind it; the state before it is known
+    u.from = blk == 0 && init && !u.map ? init + sh * mat : nullptr;
+    u.to = u.map ? a.seg_maps + (n * a.H + u.h) * map : a.seg_states + (n * a.H + u.h) * mat;
+  } else {
+    u.from = blk > 0 ? a.seg_states + ((n - 1) * a.H + u.h) * mat : init ? init + sh * mat : nullptr;
+    u.to = last && fin ? fin + sh * mat : nullptr;
+  }
   return u;
 }
 
@@ -64,32 +96,38 @@ template <int C, int KB, int NV>
 using State = f32x4[Share<C, KB, NV>::kB][Share<C, KB, NV>::kS];   // lane: value column c16, key columns 4 g + r
 
 template <int C, int KB, int NV>
-__device__ __forceinline__ void read_state(const DeltaArgs& a, const float* from, int dv0, const Share<C, KB, NV>& w, int c16, int g,
+__device__ __forceinline__ void read_state(const DeltaArgs& a, const Unit& u, const Share<C, KB, NV>& w, int c16, int g,
                                            State<C, KB, NV>& S) {
 #pragma unroll
   for (int i = 0; i < w.kB; ++i)
 #pragma unroll
     for (int j = 0; j < w.kS; ++j) {
-      const int dk = 16 * w.kb(i) + 4 * g, dv = dv0 + 16 * w.sb(j) + c16;
-      const bool in = from && w.sb(j) < NV && dk < a.dk && dv < a.dv;
-      S[i][j] = in ? *reinterpret_cast<const f32x4*>(from + (long)dv * a.dk + dk) : f32x4{0.f, 0.f, 0.f, 0.f};
+      const int dk = 16 * w.kb(i) + 4 * g, dv = u.dv0 + 16 * w.sb(j) + c16;
+      const bool in = u.from && w.sb(j) < NV && dk < a.dk && dv < u.rows;
+      S[i][j] = in ? *reinterpret_cast<const f32x4*>(u.from + (long)dv * a.dk + dk) : f32x4{0.f, 0.f, 0.f, 0.f};
+      if (u.map) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[i][j][r] = dk + r == dv ? 1.f : 0.f;
+      }
     }
 }
 // Bytes of this lane's pieces of a state from its start, kOffNone where they lie outside.
 template <int C, int KB, int NV>
 struct StatePieces {
   uint32_t at[Share<C, KB, NV>::kB][Share<C, KB, NV>::kS];
-  __device__ __forceinline__ StatePieces(const DeltaArgs& a, int dv0, const Share<C, KB, NV>& w, int c16, int g) {
+  uint32_t bytes;
+  __device__ __forceinline__ StatePieces(const DeltaArgs& a, const Unit& u, const Share<C, KB, NV>& w, int c16, int g)
+      : bytes((uint32_t)(a.dk * u.rows * 4)) {
 #pragma unroll
     for (int i = 0; i < w.kB; ++i)
 #pragma unroll
       for (int j = 0; j < w.kS; ++j) {
-        const int dk = 16 * w.kb(i) + 4 * g, dv = dv0 + 16 * w.sb(j) + c16;
-        at[i][j] = w.sb(j) < NV && dk < a.dk && dv < a.dv ? (uint32_t)((dv * a.dk + dk) * 4) : kOffNone;
+        const int dk = 16 * w.kb(i) + 4 * g, dv = u.dv0 + 16 * w.sb(j) + c16;
+        at[i][j] = w.sb(j) < NV && dk < a.dk && dv < u.rows ? (uint32_t)((dv * a.dk + dk) * 4) : kOffNone;
       }
   }
-  __device__ __forceinline__ void store(const DeltaArgs& a, float* to, const State<C, KB, NV>& S) const {
-    const rsrc_t r = make_rsrc(to, (uint32_t)(a.dk * a.dv * 4));
+  __device__ __forceinline__ void store(float* to, const State<C, KB, NV>& S) const {
+    const rsrc_t r = make_rsrc(to, bytes);
 #pragma unroll
     for (int i = 0; i < Share<C, KB, NV>::kB; ++i)
 #pragma unroll
@@ -212,10 +250,15 @@ __device__ __forceinline__ void scale_state(State<C, KB, NV>& S, float by) {
     for (int j = 0; j < Share<C, KB, NV>::kS; ++j) S[i][j] *= by;
 }
 
-// NX: terms of an input. KEEP: for the gradients; the states before the chunks and U are written, not O.
-template <int C, int KB, int NV, int NX, bool KEEP>
+// What a forward walk writes: O; for the gradients, the states before the chunks and U; of a segment, its own last
+// state or map.
+enum { kOutputs, kKeep, kOwn };
+
+// NX: terms of an input.
+template <int C, int KB, int NV, int NX, int WHAT>
 __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fwd_kernel(DeltaArgs a) {
   using Sh = Share<C, KB, NV>;
+  constexpr bool KEEP = WHAT != kOutputs;
   constexpr int kEsz = NX == 1 ? 2 : 4, kOut = out_terms(NX), kKp = C / 32;
   constexpr int kPitchK = lds_pitch(32 * KB), kPitchV = value_pitch(NV);
   __shared__ __align__(16) uint16_t Sl[kTerms * 16 * NV * kPitchK];
@@ -226,7 +269,8 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
   const int wave = uniform(threadIdx.x >> 6);
   const Sh w(wave & 3);
   const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
-  const Unit u = delta_unit<C, NV>(a);
+  const Unit u = delta_unit<C, NV, WHAT == kOwn>(a, a.init, a.fin);
+  if (u.none) return;
   const int hk = u.h / (a.H / a.Hk), tok = 16 * w.tb + c16, last = u.chunks - 1;
   const long mat = (long)a.dk * a.dv, sh0 = u.slot0 * a.H + u.h;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -236,11 +280,11 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
 
   if (wave < 4) {
     const KeyPieces<KB> kat(tok, g, a.k_row, a.dk, kEsz);
-    const ValuePieces<C, KB, NV> vat(w, tok, g, u.dv0, a.v_row, a.dv, kEsz), uat(w, tok, g, u.dv0, a.dv, a.dv, 4);
+    const ValuePieces<C, KB, NV> vat(w, tok, g, u.dv0, a.v_row, u.map ? 0 : a.dv, kEsz), uat(w, tok, g, u.dv0, a.dv, a.dv, 4);
     Raw8<NX> kr[KB];
     Raw4<NX> vr[Sh::kV];
-    RawOperand tr[kKp];        // of the next chunk
     u32x4 tf[kKp][kTerms];
+    RawOperand tn[kKp];   // of the next chunk
     float eg, wt, eg_next, wt_next;
     auto load_rows = [&](int c) {
       const rsrc_t rk = rows(a.k, c, a.k_row, (long)hk * a.dk), rv = rows(a.v, c, a.v_row, (long)u.h * a.dv);
@@ -254,21 +298,18 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
       eg_next = gates[tok];
       wt_next = gates[C + tok];
     };
-    auto next_gates = [&]() {
+    auto next = [&]() {
       eg = eg_next;
       wt = wt_next;
-    };
-    auto load_t = [&](int c) { load_operands<C>(a.tf, sh0 + (long)c * a.H, w.tb, 0, w.tb / 2, lane, tr); };
-    auto split_t = [&]() {
 #pragma unroll
-      for (int kp = 0; kp < kKp; ++kp) terms8<kTerms>(tr[kp], tf[kp]);
+      for (int kp = 0; kp < kKp; ++kp) terms8<kTerms>(tn[kp], tf[kp]);
     };
+    auto load_t = [&](int c) { load_operands<C>(a.tf, sh0 + (long)c * a.H, w.tb, 0, w.tb / 2, lane, tn); };
     if (last >= 0) {
       load_rows(0);
       load_gates(0);
       load_t(0);
-      split_t();
-      next_gates();
+      next();
       load_t(min(1, last));
       load_gates(min(1, last));
     }
@@ -310,13 +351,12 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
           U[i] = mma<kTerms, kTerms, kTerms>(xt, tf[kp], U[i]);
         }
         stage4<C, kTerms, kPitchV>(Wl, tok, 16 * w.vb(i) + 4 * g, U[i] * wt);
-        if (KEEP) buf_store16(__builtin_bit_cast(u32x4, U[i]), make_rsrc(a.u + sh * C * a.dv, (uint32_t)(C * a.dv * 4)), uat.at[i]);
-        else stage4<C, kOut, kPitchV>(Ul + (c & 1) * kU, tok, 16 * w.vb(i) + 4 * g, U[i]);
+        if (WHAT == kKeep) buf_store16(__builtin_bit_cast(u32x4, U[i]), make_rsrc(a.u + sh * C * a.dv, (uint32_t)(C * a.dv * 4)), uat.at[i]);
+        if (WHAT == kOutputs) stage4<C, kOut, kPitchV>(Ul + (c & 1) * kU, tok, 16 * w.vb(i) + 4 * g, U[i]);
       }
       __syncthreads();
       __builtin_amdgcn_sched_barrier(0);   // while the state is updated, and not before the barrier
-      split_t();
-      next_gates();
+      next();
       load_t(min(c + 2, last));
       load_gates(min(c + 2, last));
       __syncthreads();
@@ -324,12 +364,12 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
   } else {
     const KeyPieces<KB> qat(tok, g, a.q_row, a.dk, kEsz);
     const ValuePieces<C, KB, NV> oat(w, tok, g, u.dv0, (long)a.H * a.dv, a.dv, kEsz);
-    const StatePieces<C, KB, NV> pieces(a, u.dv0, w, c16, g);
+    const StatePieces<C, KB, NV> pieces(a, u, w, c16, g);
     State<C, KB, NV> S;
-    read_state<C, KB, NV>(a, a.init ? a.init + ((long)u.seq * a.H + u.h) * mat : nullptr, u.dv0, w, c16, g, S);
+    read_state<C, KB, NV>(a, u, w, c16, g, S);
     stage_state<C, KB, NV>(Sl, w, c16, g, S);
     Raw8<NX> qr[KEEP ? 1 : KB];
-    RawOperand pf[KEEP ? 1 : kKp];
+    u32x4 pf[KEEP ? 1 : kKp][kOut];
     f32x4 O[Sh::kV];
     float eg = 0.f, keep = 0.f;
     auto load_q = [&](int c) {
@@ -349,10 +389,9 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
 #pragma unroll
         for (int kp = 0; kp < kKp; ++kp) {
           if (kp > w.tb / 2) continue;
-          u32x4 ut[kOut], pt[kOut];
+          u32x4 ut[kOut];
           tokens_operand<C, kOut, kPitchV>(Ul + (c & 1) * kU, kp, 16 * w.vb(i), lane, ut);
-          terms8<kOut>(pf[kp], pt);
-          O[i] = mma<kOut, kOut, kOut>(ut, pt, O[i]);
+          O[i] = mma<kOut, kOut, kOut>(ut, pf[kp], O[i]);
         }
         store4<NX>(O[i], ro, oat.at[i]);
       }
@@ -366,7 +405,7 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
     for (int c = 0; c <= last; ++c) {
       const int ahead = min(c + 1, last);
       f32x4 Q[Sh::kV];
-      if (KEEP) pieces.store(a, a.states + (sh0 + (long)c * a.H) * mat, S);
+      if (WHAT == kKeep) pieces.store(a.states + (sh0 + (long)c * a.H) * mat, S);
       if constexpr (!KEEP) {   // scale e^G (Q S^T)
         u32x4 qt[KB][NX];
 #pragma unroll
@@ -379,7 +418,7 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
       __syncthreads();
       if constexpr (!KEEP) {
         if (c > 0) finish(c - 1);
-        load_operands<C>(a.pf, sh0 + (long)c * a.H, w.tb, 0, w.tb / 2, lane, pf);
+        load_operands<C, kOut>(a.pf, sh0 + (long)c * a.H, w.tb, 0, w.tb / 2, lane, pf);
 #pragma unroll
         for (int i = 0; i < Sh::kV; ++i) O[i] = Q[i];
       }
@@ -393,7 +432,7 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
       __syncthreads();
     }
     if (!KEEP && last >= 0) finish(last);
-    if (a.fin) pieces.store(a, a.fin + ((long)u.seq * a.H + u.h) * mat, S);
+    if (u.to) pieces.store(u.to, S);
   }
 }
 
@@ -414,7 +453,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
   const int wave = uniform(threadIdx.x >> 6);
   const Sh w(wave & 3);
   const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
-  const Unit u = delta_unit<C, NV>(a);
+  const Unit u = delta_unit<C, NV, false>(a, a.dfin, a.dinit);
   const int hk = u.h / (a.H / a.Hk), tok = 16 * w.tb + c16, last = u.chunks - 1;
   const long mat = (long)a.dk * a.dv, sh0 = u.slot0 * a.H + u.h;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -426,8 +465,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
     const KeyPieces<KB> kat(tok, g, a.k_row, a.dk, kEsz);
     const ValuePieces<C, KB, NV> vat(w, tok, g, u.dv0, (long)a.H * a.dv, a.dv, kEsz), uat(w, tok, g, u.dv0, a.dv, a.dv, 4);
     Raw8<NX> kr[KB];
-    RawOperand tr[kKp];        // of the next chunk
     u32x4 tt[kKp][kTerms];
+    RawOperand tn[kKp];   // of the next chunk
     float eg, wt, be, eg_next, wt_next, be_next;
     auto load_rows = [&](int c) {
       const rsrc_t rk = rows(a.k, c, a.k_row, (long)hk * a.dk);
@@ -440,22 +479,19 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
       wt_next = gates[C + tok];
       be_next = gates[2 * C + tok];
     };
-    auto next_gates = [&]() {
+    auto next = [&]() {
       eg = eg_next;
       wt = wt_next;
       be = be_next;
-    };
-    auto load_t = [&](int c) { load_operands<C>(a.tt, sh0 + (long)c * a.H, w.tb, w.tb / 2, kKp - 1, lane, tr); };
-    auto split_t = [&]() {
 #pragma unroll
-      for (int kp = 0; kp < kKp; ++kp) terms8<kTerms>(tr[kp], tt[kp]);
+      for (int kp = 0; kp < kKp; ++kp) terms8<kTerms>(tn[kp], tt[kp]);
     };
+    auto load_t = [&](int c) { load_operands<C>(a.tt, sh0 + (long)c * a.H, w.tb, w.tb / 2, kKp - 1, lane, tn); };
     if (last >= 0) {
       load_rows(last);
       load_gates(last);
       load_t(last);
-      split_t();
-      next_gates();
+      next();
       load_t(max(last - 1, 0));
       load_gates(max(last - 1, 0));
     }
@@ -505,8 +541,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
       }
       __syncthreads();
       __builtin_amdgcn_sched_barrier(0);   // while the state is updated, and not before the barrier
-      split_t();
-      next_gates();
+      next();
       load_t(max(c - 2, 0));
       load_gates(max(c - 2, 0));
       __syncthreads();
@@ -514,9 +549,9 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
   } else {
     const KeyPieces<KB> qat(tok, g, a.q_row, a.dk, kEsz);
     const ValuePieces<C, KB, NV> oat(w, tok, g, u.dv0, (long)a.H * a.dv, a.dv, kEsz);
-    const StatePieces<C, KB, NV> pieces(a, u.dv0, w, c16, g);
+    const StatePieces<C, KB, NV> pieces(a, u, w, c16, g);
     State<C, KB, NV> L;
-    read_state<C, KB, NV>(a, a.dfin ? a.dfin + ((long)u.seq * a.H + u.h) * mat : nullptr, u.dv0, w, c16, g, L);
+    read_state<C, KB, NV>(a, u, w, c16, g, L);
     stage_state<C, KB, NV>(Ll, w, c16, g, L);
     Raw8<NX> qr[KB];
     Raw4<NX> d1[Sh::kV], d2[Sh::kV];   // dO of the chunk before the present one, and of the one before that
@@ -590,7 +625,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
     __syncthreads();
     if (last >= 0) stage_o(d1);
     for (int c = last; c >= 0; --c) {
-      pieces.store(a, a.dstates + (sh0 + (long)c * a.H) * mat, L);
+      pieces.store(a.dstates + (sh0 + (long)c * a.H) * mat, L);
       // L = e^(G_C) L + scale (e^G dO)^T Q - (e^G beta U')^T K, the last term when U' is there.
       scale_state<C, KB, NV>(L, keep);
       load_keep(max(c - 1, 0));
@@ -613,7 +648,62 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
       load_do(max(c - 3, 0), d2, eg2);
       __syncthreads();
     }
-    if (a.dinit) pieces.store(a, a.dinit + ((long)u.seq * a.H + u.h) * mat, L);
+    if (u.to) pieces.store(u.to, L);
+  }
+}
+
+// The states behind the segments of a sequence, one after the other: R := R M + own, of 16 rows of one head, in fp32
+// (matrix instructions on fp32). A wave makes 16 of the key columns; R goes round through LDS, and the next segment's
+// map is on its way while this one's is taken.
+template <int KB>
+__global__ __launch_bounds__(128 * KB) void delta_join_kernel(DeltaArgs a, int C) {
+  constexpr int kBlocks = 2 * KB;   // waves
+  __shared__ __align__(16) f32x4 Rl[kBlocks * 64];   // blocks of 16 key columns as accumulators hold them
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
+  const int tiles = (a.dv + 15) / 16, tile = (int)(blockIdx.x % tiles), h = (int)((blockIdx.x / tiles) % a.H);
+  const long seq = blockIdx.x / ((long)tiles * a.H), mat = (long)a.dk * a.dv, map = (long)a.dk * a.dk;
+  const int L = a.seg * C;
+  long n0, len;
+  if (a.cu) {
+    const int c0 = min(max(a.cu[seq], 0), a.T);
+    len = min(max(a.cu[seq + 1], c0), a.T) - c0;
+    n0 = (long)c0 / L + seq;
+  } else {
+    len = a.T;
+    n0 = seq * a.segs_per_row;
+  }
+  const int segs = (int)((len + L - 1) / L), dv = 16 * tile + c16;
+  if (segs < 3) return;   // the state behind the first segment is its own
+  f32x4 R, own, M[kBlocks];   // M: rows 16 k + 4 g + t of the map, column c16 of this wave's block
+  const int dk = 16 * wave + 4 * g, col = 16 * wave + c16;
+  const uint32_t at = dv < a.dv && dk < a.dk ? (uint32_t)((dv * a.dk + dk) * 4) : kOffNone;
+  const uint32_t mat0 = col < a.dk ? (uint32_t)((4 * g * a.dk + col) * 4) : kOffNone;   // rows behind the map: behind its end
+  auto state = [&](int s) { return make_rsrc(a.seg_states + ((n0 + s) * a.H + h) * mat, (uint32_t)(mat * 4)); };
+  auto load = [&](int s) {
+    const rsrc_t rm = make_rsrc(a.seg_maps + ((n0 + s) * a.H + h) * map, (uint32_t)(map * 4));
+    own = __builtin_bit_cast(f32x4, buf_load16(state(s), at));
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) M[k][t] = buf_load_f32(rm, mat0 + (uint32_t)((16 * k + t) * a.dk * 4));
+  };
+  R = __builtin_bit_cast(f32x4, buf_load16(state(0), at));
+  load(1);
+  loads_done();
+  for (int s = 1; s < segs - 1; ++s) {
+    Rl[wave * 64 + lane] = R;
+    __syncthreads();
+    f32x4 x[2] = {own, f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+      const f32x4 r = Rl[k * 64 + lane];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) x[k & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(M[k][t], r[t], x[k & 1], 0, 0, 0);
+    }
+    R = x[0] + x[1];
+    buf_store16(__builtin_bit_cast(u32x4, R), state(s), at);
+    load(min(s + 1, segs - 2));
+    __syncthreads();
   }
 }
 
@@ -621,30 +711,68 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
 constexpr int kNv64 = 1;
 constexpr int nv32(int kb) { return kb > 4 ? 1 : 2; }
 
+template <int KB, int WHAT>
+void walk(const DeltaArgs& a, long blocks, hipStream_t stream) {
+  const dim3 grid((unsigned)blocks);
+  if (a.bf16) hipLaunchKernelGGL((delta_fwd_kernel<64, KB, kNv64, 1, WHAT>), grid, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((delta_fwd_kernel<32, KB, nv32(KB), 3, WHAT>), grid, dim3(kThreads), 0, stream, a);
+}
 template <int KB>
 void fwd(const DeltaArgs& a, bool keep, hipStream_t stream) {
-  const dim3 grid((unsigned)delta_chain_blocks(a, false));
-  if (a.bf16) {
-    if (keep) hipLaunchKernelGGL((delta_fwd_kernel<64, KB, kNv64, 1, true>), grid, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((delta_fwd_kernel<64, KB, kNv64, 1, false>), grid, dim3(kThreads), 0, stream, a);
-  } else {
-    if (keep) hipLaunchKernelGGL((delta_fwd_kernel<32, KB, nv32(KB), 3, true>), grid, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((delta_fwd_kernel<32, KB, nv32(KB), 3, false>), grid, dim3(kThreads), 0, stream, a);
+  if (a.seg) {
+    walk<KB, kOwn>(a, delta_segment_blocks(a), stream);
+    const dim3 grid((unsigned)((long)(a.S > 0 ? a.S : a.batch) * a.H * ((a.dv + 15) / 16)));
+    hipLaunchKernelGGL(delta_join_kernel<KB>, grid, dim3(128 * KB), 0, stream, a, delta_chunk(a.bf16));
   }
+  if (keep) walk<KB, kKeep>(a, delta_chain_blocks(a), stream);
+  else walk<KB, kOutputs>(a, delta_chain_blocks(a), stream);
 }
 template <int KB>
 void rev(const DeltaArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)delta_chain_blocks(a, true));
+  const dim3 grid((unsigned)delta_chain_blocks(a));
   if (a.bf16) hipLaunchKernelGGL((delta_rev_kernel<64, KB, kNv64, 1>), grid, dim3(kThreads), 0, stream, a);
   else hipLaunchKernelGGL((delta_rev_kernel<32, KB, nv32(KB), 3>), grid, dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace
 
-long delta_chain_blocks(const DeltaArgs& a, bool) {
-  const int cols = 16 * (a.bf16 ? kNv64 : nv32((a.dk + 31) / 32));
-  return (long)(a.S > 0 ? a.S : a.batch) * a.H * ((a.dv + cols - 1) / cols);
+static int tile_columns(int dk, bool bf16) { return 16 * (bf16 ? kNv64 : nv32((dk + 31) / 32)); }
+static int tiles_of(int d, int dk, bool bf16) { return (d + tile_columns(dk, bf16) - 1) / tile_columns(dk, bf16); }
+long delta_chain_blocks(const DeltaArgs& a) {
+  return (a.seg ? a.segs : (long)(a.S > 0 ? a.S : a.batch)) * a.H * tiles_of(a.dv, a.dk, a.bf16);
 }
+long delta_segment_blocks(const DeltaArgs& a) {
+  return a.segs * a.H * (tiles_of(a.dv, a.dk, a.bf16) + tiles_of(a.dk, a.dk, a.bf16));
+}
+
+// A walk of few heads leaves most of the card idle for as long as its longest sequence is. Cut into segments, every
+// segment's own last state (from a state of zero) and its map of a state are made at once, the states behind the
+// segments follow from these one after the other, and all segments are walked at once: twice to three times the
+// work, in chains of a segment's length. The number of segments is the one of least cost in steps of a chunk: two
+// workgroups a CU run at once; a step of two takes about 1.3 times one's, a step without O 0.8 of one with it; a
+// segment's join takes about one step, the two launches more five. The host does not know the lengths of packed
+// sequences: the longest is taken to be three times the mean.
+int delta_segment(int batch, int T, int S, int H, int dk, int dv, bool bf16) {
+  const int C = delta_chunk(bf16);
+  const long seqs = S > 0 ? S : batch, tokens = (long)batch * T;
+  const long longest = S > 0 ? std::min((long)T, 3 * ((tokens + S - 1) / S)) : T;
+  const long chunks = (longest + C - 1) / C, all = (tokens + C - 1) / C;
+  const int values = tiles_of(dv, dk, bf16), rows = values + tiles_of(dk, dk, bf16);
+  auto rounds = [](double units) { return units <= 256 ? 1.0 : 1.3 * std::ceil(units / 512); };
+  double least = rounds((double)seqs * H * values) * chunks;
+  int best = 0;
+  for (long n = 2; n <= 64 && n <= chunks; ++n) {
+    const long c = (chunks + n - 1) / n;
+    const double segs = std::max((double)all / c, (double)seqs);
+    const double cost = 0.8 * rounds((segs - seqs) * H * rows) * c + (double)n + 5.0 + rounds(segs * H * values) * c;
+    if (cost < 0.9 * least) {
+      least = cost / 0.9;
+      best = (int)c;
+    }
+  }
+  return best;
+}
+
 int delta_chain_threads() { return kThreads; }
 
 hipError_t launch_delta_fwd(const DeltaArgs& a, bool keep, hipStream_t stream) {

@@ -108,7 +108,7 @@ __device__ __forceinline__ void invert(float* M, int wave, int lane) {
   }
 }
 
-// Operand (rb, kp) of a matrix, or of its transpose, its columns times w.
+// Operand (rb, kp) of a matrix, or of its transpose, its columns times w, in fp32.
 template <int C, bool TR>
 __device__ __forceinline__ void put_operand(const float* M, float* to, int rb, int kp, const float* w, int lane) {
   const int c16 = lane & 15, g = lane >> 4, row = 16 * rb + c16;
@@ -121,8 +121,21 @@ __device__ __forceinline__ void put_operand(const float* M, float* to, int rb, i
       x[r] = TR ? M[(col + r) * kPitch<C> + row] : M[row * kPitch<C> + col + r];
       if (w) x[r] *= w[col + r];
     }
-    *reinterpret_cast<f32x4*>(to + operand_at(C, rb, kp) + 256 * t + lane * 4) = x;
+    *reinterpret_cast<f32x4*>(to + operand_at(C, 1, rb, kp) + 256 * t + lane * 4) = x;
   }
+}
+// Half of an operand, the columns 16 cb ..: a tile as its accumulators hold it (rows c16, columns 4 g + r).
+template <int C>
+__device__ __forceinline__ void put_tile(f32x4 x, float* to, int rb, int cb, int lane) {
+  *reinterpret_cast<f32x4*>(to + operand_at(C, 1, rb, cb / 2) + 256 * (cb & 1) + lane * 4) = x;
+}
+template <int C, int N>
+__device__ __forceinline__ void put_tile(f32x4 x, uint16_t* to, int rb, int cb, int lane) {
+  u32x2 part[N];
+  split4<N>(x, part);
+  uint16_t* at = to + operand_at(C, N, rb, cb / 2) + lane * 8 + 4 * (cb & 1);
+#pragma unroll
+  for (int t = 0; t < N; ++t) *reinterpret_cast<u32x2*>(at + t * kOperand) = part[t];
 }
 
 // The pairs of 16 rows and 16 columns on or below the diagonal that wave w takes: (row, column), -1: none.
@@ -145,7 +158,7 @@ __device__ __forceinline__ void tile_of(int wave, int e, int& ib, int& jb) {
 template <int C, int KB, int NX, bool BWD>
 __global__ __launch_bounds__(kThreads, 3) void delta_prep_kernel(DeltaArgs a) {
   constexpr int kTiles = C == 64 ? 3 : 1;   // a wave
-  constexpr int kEsz = NX == 1 ? 2 : 4;
+  constexpr int kEsz = NX == 1 ? 2 : 4, kOut = out_terms(NX);
   // Rows of K and Q, kSlab pieces of 32 columns at a time, and in their place the matrix.
   constexpr int kSlab = NX == 1 ? (KB < 4 ? KB : 4) : (KB < 2 ? KB : 2), kPitchK = lds_pitch(32 * kSlab);
   constexpr int kRows = NX * C * kPitchK, kBytes = 4 * kRows > 4 * C * kPitch<C> ? 4 * kRows : 4 * C * kPitch<C>;
@@ -224,7 +237,7 @@ __global__ __launch_bounds__(kThreads, 3) void delta_prep_kernel(DeltaArgs a) {
 
   for (int m = 0; m < rep; ++m) {
     const int h = hk * rep + m, mw = m & 3;
-    const long sh = slot * a.H + h, at = sh * operands(C);
+    const long sh = slot * a.H + h;
     if (m > 0) __syncthreads();   // the last head's operands are out
     if (mw == 0) {
       if (m + wave < rep) {
@@ -271,15 +284,15 @@ __global__ __launch_bounds__(kThreads, 3) void delta_prep_kernel(DeltaArgs a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           P[r] = j1 <= i4 + r ? a.scale * expf((gh[i4 + r] - gh[j1]) + (gl[i4 + r] - gl[j1])) * qk[e][r] : 0.f;
-        float* to = a.pt + at + lane * 4;
-        *reinterpret_cast<f32x4*>(to + operand_at(C, jb, ib / 2) + 256 * (ib & 1)) = P;
-        if (ib == jb && (ib & 1)) *reinterpret_cast<f32x4*>(to + operand_at(C, jb, ib / 2)) = zero;
+        float* to = a.pt + sh * operands(C, 1);
+        put_tile<C>(P, to, jb, ib, lane);
+        if (ib == jb && (ib & 1)) put_tile<C>(zero, to, jb, ib - 1, lane);
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r) P[r] = j + r <= i ? a.scale * d[r] * qk[e][r] : 0.f;
-        float* to = a.pf + at + lane * 4;
-        *reinterpret_cast<f32x4*>(to + operand_at(C, ib, jb / 2) + 256 * (jb & 1)) = P;
-        if (ib == jb && !(ib & 1)) *reinterpret_cast<f32x4*>(to + operand_at(C, ib, jb / 2) + 256) = zero;
+        uint16_t* to = a.pf + sh * operands(C, kOut);
+        put_tile<C, kOut>(P, to, ib, jb, lane);
+        if (ib == jb && !(ib & 1)) put_tile<C, kOut>(zero, to, ib, jb + 1, lane);
       }
     }
     __syncthreads();
@@ -288,8 +301,8 @@ __global__ __launch_bounds__(kThreads, 3) void delta_prep_kernel(DeltaArgs a) {
     // Operands on or below the diagonal, of the transpose on or above it.
     for (int t = wave; t < (C / 16) * (C / 32); t += 4) {
       const int rb = t / (C / 32), kp = t % (C / 32);
-      if (kp <= rb / 2) put_operand<C, false>(Am, a.tf + at, rb, kp, bt, lane);
-      if (BWD && kp >= rb / 2) put_operand<C, true>(Am, a.tt + at, rb, kp, nullptr, lane);
+      if (kp <= rb / 2) put_operand<C, false>(Am, a.tf + sh * operands(C, 1), rb, kp, bt, lane);
+      if (BWD && kp >= rb / 2) put_operand<C, true>(Am, a.tt + sh * operands(C, 1), rb, kp, nullptr, lane);
     }
   }
 }
@@ -306,7 +319,8 @@ void prep(const DeltaArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t delta_gates_bytes(bool bf16) { return (size_t)kGateRows * delta_chunk(bf16) * 4; }
-size_t delta_matrix_bytes(bool bf16) { return (size_t)operands(delta_chunk(bf16)) * 4; }
+size_t delta_tf_bytes(bool bf16) { return (size_t)operands(delta_chunk(bf16), 1) * 4; }
+size_t delta_pf_bytes(bool bf16) { return (size_t)operands(delta_chunk(bf16), out_terms(bf16 ? 1 : 3)) * 2; }
 int delta_prep_threads() { return kThreads; }
 
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stream) {

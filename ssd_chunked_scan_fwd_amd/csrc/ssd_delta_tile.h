@@ -150,13 +150,15 @@ __device__ __forceinline__ void store4(f32x4 x, rsrc_t r, uint32_t off) {
   else buf_store16(__builtin_bit_cast(u32x4, x), r, off);
 }
 
-// C x C matrices in the workspace, fp32, as operands of 16 rows and 32 columns (columns in the order of an
-// accumulator pair): 64 lanes of the columns 4 g .., then 64 of the columns 16 + 4 g ... In fp32 they are two thirds
-// of their terms, in memory and on the way through the first-level cache (64 bytes a cycle: a walk's rows and
-// operands of a chunk take a third of its time), and a triangle's zero operands are not loaded.
-constexpr int kOperand = 512;   // floats
-__host__ __device__ constexpr long operands(int C) { return (long)(C / 16) * (C / 32) * kOperand; }
-__device__ __forceinline__ int operand_at(int C, int rb, int kp) { return (rb * (C / 32) + kp) * kOperand; }
+// C x C matrices in the workspace as operands of 16 rows and 32 columns, columns in the order of an accumulator
+// pair. P, of which o's products take two terms of bf16 inputs: those terms, each 64 lanes of 16 bytes, one behind the
+// other. T and the transposes, of which three are taken: fp32, 64 lanes of the columns 4 g .., then 64 of the columns
+// 16 + 4 g .., split into terms where they are used. What a CU has on its way from memory bounds the walks of few
+// heads: with three terms in memory, half as much again, they took 9 to 13 % longer.
+// A triangle's zero operands are not loaded.
+constexpr int kOperand = 512;   // elements
+__host__ __device__ constexpr long operands(int C, int n) { return (long)(C / 16) * (C / 32) * n * kOperand; }
+__device__ __forceinline__ int operand_at(int C, int n, int rb, int kp) { return (rb * (C / 32) + kp) * n * kOperand; }
 struct RawOperand {
   u32x4 w[2];
 };
@@ -170,12 +172,22 @@ __device__ __forceinline__ void terms8(const RawOperand& x, u32x4* out) {
 // Row block rb of matrix sh; the operands from `least` to `most`, zeros in the place of the others.
 template <int C>
 __device__ __forceinline__ void load_operands(const float* from, long sh, int rb, int least, int most, int lane, RawOperand* to) {
-  const rsrc_t r = make_rsrc(from + sh * operands(C), (uint32_t)(operands(C) * 4));
+  const rsrc_t r = make_rsrc(from + sh * operands(C, 1), (uint32_t)(operands(C, 1) * 4));
 #pragma unroll
   for (int kp = 0; kp < C / 32; ++kp) {
-    const uint32_t off = kp >= least && kp <= most ? (uint32_t)(operand_at(C, rb, kp) * 4 + lane * 16) : kOffNone;
+    const uint32_t off = kp >= least && kp <= most ? (uint32_t)(operand_at(C, 1, rb, kp) * 4 + lane * 16) : kOffNone;
     to[kp].w[0] = buf_load16(r, off);
     to[kp].w[1] = buf_load16(r, off + 1024);
+  }
+}
+template <int C, int N>
+__device__ __forceinline__ void load_operands(const uint16_t* from, long sh, int rb, int least, int most, int lane, u32x4 (*to)[N]) {
+  const rsrc_t r = make_rsrc(from + sh * operands(C, N), (uint32_t)(operands(C, N) * 2));
+#pragma unroll
+  for (int kp = 0; kp < C / 32; ++kp) {
+    const uint32_t off = kp >= least && kp <= most ? (uint32_t)(operand_at(C, N, rb, kp) * 2 + lane * 16) : kOffNone;
+#pragma unroll
+    for (int t = 0; t < N; ++t) to[kp][t] = buf_load16(r, off + t * kOperand * 2);
   }
 }
 

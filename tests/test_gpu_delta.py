@@ -115,6 +115,25 @@ def test_backward(shape, dtype):
     check_bwd(make(*shape, dtype, seed=100 + shape[1]), name=str(shape))
 
 
+# Long sequences of few heads: cut into segments that are walked at once.
+LONG = [(1, 4000, 1, 1, 64, 40, None), (2, 3001, 2, 1, 128, 128, None), (1, 2600, 1, 1, 256, 24, None), (1, 3500, 2, 2, 16, 256, None),
+        (1, 4200, 1, 1, 32, 64, [0, 1500, 1500, 1501, 4200]), (1, 3900, 1, 1, 64, 64, [3, 20, 3900])]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", LONG)
+def test_long_sequences(shape, dtype):
+    say(f"[delta long] {shape} {dtype}")
+    *sizes, cu = shape
+    d = make(*sizes, dtype, seed=sizes[1], nseq=None if cu is None else len(cu) - 1)
+    d["g"] *= 0.1   # a memory of some 70 tokens
+    check_fwd(d, cu=cu, name=str(shape))
+    d["init"] = None
+    check_fwd(d, cu=cu, name=str(shape))
+    if dtype == BF and sizes[1] == 4000:
+        check_bwd(d, cu=cu, name=str(shape))
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_no_states_no_decay(dtype):
     say(f"[delta] no states, no decay {dtype}")
