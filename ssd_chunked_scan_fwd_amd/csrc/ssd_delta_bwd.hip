@@ -12,29 +12,32 @@
 //     dg_t = <dS1, S1> + sum_{i >= t} E_i   (tokens of the chunk),
 //     <dS1, S1> = e^(G_C) <dS1, S0> + sum_j e^(G_C - G_j) k_j . (U dS1)_j.
 //
-// A workgroup takes one chunk of one head. First, over the value columns 32 at a
-// time, the products with the states (contraction over the columns, the states'
-// terms in LDS) and Z1, Z2 of the wave's own tokens, both as rows and as columns;
-// then the products of the masked Z with Q and K, whose rows take the states'
-// place in LDS.
+// A workgroup takes one chunk of one head, two waves 16 tokens, each half of the key
+// columns. First, over the value columns 32 at a time, the products with the states
+// (contraction over the columns, the states' terms in LDS) and, one of the two waves
+// each, Z1 and Z2 of the tokens, both as rows and as columns; then the products of
+// the masked Z, which go round through LDS, with Q and K, whose rows take the
+// states' place there.
 #include "ssd_delta_tile.h"
 
 namespace ssd {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int threads_of(int C) { return 8 * C; }   // two waves for 16 tokens
 constexpr int kPitchT = lds_pitch(32);   // rows of 32 value columns, in the order of an accumulator pair
 
 template <int C, int KB, int NX>
-__global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs a) {
-  constexpr int kEsz = NX == 1 ? 2 : 4, kTb = C / 16, kKp = C / 32, kHalves = 4 / kTb, kB = 2 * KB / kHalves;
+__global__ __launch_bounds__(threads_of(C), C == 64 ? 2 : 1) void delta_grads_kernel(DeltaArgs a) {
+  constexpr int kEsz = NX == 1 ? 2 : 4, kTb = C / 16, kKp = C / 32, kHalves = 2, kB = KB, kThreads = threads_of(C);
   constexpr int kPitchK = lds_pitch(32 * KB);
-  constexpr int kStateRows = 2 * kTerms * 32;
-  static_assert(kStateRows >= 2 * NX * C, "Q and K take the states' place");
-  __shared__ __align__(16) uint16_t Sl[kStateRows * kPitchK];   // [S0, dS1][term][32 value columns]; K, Q [term][C]
-  __shared__ __align__(16) uint16_t Tl[(2 * kTerms + NX) * C * kPitchT];   // U, U', dO [term][C]
-  __shared__ float Gh[C], Gl[C], Be[C], Ev[C], Sw[C], Kr[C], dots[4];
+  // [S0, dS1][term][32 value columns] and U, U', dO [term][C]; then K, Q [term][C] and, of every wave, three operands.
+  constexpr int kStates = 2 * kTerms * 32 * kPitchK, kTokens = (2 * kTerms + NX) * C * kPitchT;
+  constexpr int kRows = 2 * NX * C * kPitchK, kWave = 3 * kTerms * kOperand, kMasked = kThreads / 64 * kWave;
+  constexpr int kSize = kStates + kTokens > kRows + kMasked ? kStates + kTokens : kRows + kMasked;
+  __shared__ __align__(16) uint16_t Sl[kSize];
+  __shared__ __align__(16) float Gh[C], Gl[C], Be[C], Ev[C], Sw[C], Kr[C], dots[kThreads / 64];
+  uint16_t* const Tl = Sl + kStates;
   uint16_t* const Ut = Tl;
   uint16_t* const Vt = Tl + kTerms * C * kPitchT;       // U'
   uint16_t* const Ot = Tl + 2 * kTerms * C * kPitchT;   // dO
@@ -63,14 +66,15 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs a) {
   const rsrc_t rb = make_rsrc(a.ub + sh * C * a.dv, (uint32_t)(C * a.dv * 4));
   const rsrc_t ro = chunk_rows(a.d_o, ch.row0, (long)a.H * a.dv, (long)h * a.dv, n, kEsz);
   const rsrc_t rv = chunk_rows(a.v, ch.row0, a.v_row, (long)h * a.dv, n, kEsz);
-  f32x4 s0[KB], s1[KB];   // this thread's pieces of four of the states' rows
+  constexpr int kPieces = (256 * KB + kThreads - 1) / kThreads;
+  f32x4 s0[kPieces], s1[kPieces];   // this thread's pieces of four of the states' rows
   Raw8<3> xu, xb;
   Raw8<NX> xo, xv;
   auto load = [&](int kv) {
 #pragma unroll
-    for (int i = 0; i < KB; ++i) {
+    for (int i = 0; i < kPieces; ++i) {
       const int at = threadIdx.x + kThreads * i, dv = 32 * kv + at / (8 * KB), dk = 4 * (at % (8 * KB));
-      const bool in = dv < a.dv && dk < a.dk;
+      const bool in = at < 256 * KB && dv < a.dv && dk < a.dk;
       s0[i] = in ? *reinterpret_cast<const f32x4*>(S0 + (long)dv * a.dk + dk) : zero;
       s1[i] = in ? *reinterpret_cast<const f32x4*>(S1 + (long)dv * a.dk + dk) : zero;
     }
@@ -95,9 +99,10 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs a) {
   for (int b = 0; b < kB; ++b) dQ[b] = R[b] = W[b] = zero;
   // Products with the tokens 16 blk + 4 g + r: entry e <= tb has blk = e and tok as the row (i), the others
   // blk = e - 1 and tok as the column (j).
-  f32x4 Z1[kTb + 1], Z2[kTb + 1];
+  // The first of the tokens' two waves makes Z1, the second Z2.
+  f32x4 Z[kTb + 1];
 #pragma unroll
-  for (int e = 0; e <= kTb; ++e) Z1[e] = Z2[e] = zero;
+  for (int e = 0; e <= kTb; ++e) Z[e] = zero;
   float uv = 0.f, dot = 0.f;
 
   const int steps = (a.dv + 31) / 32;
@@ -115,19 +120,18 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs a) {
       for (int i = 0; i < 8; ++i) uv = fmaf(x[i], y[i], uv);
       terms8<NX>(xo, ot);
     }
-    if (half == 0) {
+    {
       const int at = tok * kPitchT + 8 * g;
 #pragma unroll
-      for (int t = 0; t < kTerms; ++t) {
-        *reinterpret_cast<u32x4*>(Ut + t * C * kPitchT + at) = ut[t];
-        *reinterpret_cast<u32x4*>(Vt + t * C * kPitchT + at) = vt[t];
-      }
+      for (int t = 0; t < kTerms; ++t) *reinterpret_cast<u32x4*>((half ? Vt : Ut) + t * C * kPitchT + at) = half ? vt[t] : ut[t];
 #pragma unroll
-      for (int t = 0; t < NX; ++t) *reinterpret_cast<u32x4*>(Ot + t * C * kPitchT + at) = ot[t];
+      for (int t = 0; t < NX; ++t)
+        if (half == 0) *reinterpret_cast<u32x4*>(Ot + t * C * kPitchT + at) = ot[t];
     }
 #pragma unroll
-    for (int i = 0; i < KB; ++i) {
+    for (int i = 0; i < kPieces; ++i) {
       const int at = threadIdx.x + kThreads * i, row = at / (8 * KB), col = 4 * (at % (8 * KB));
+      if (256 * KB % kThreads && at >= 256 * KB) continue;
       u32x2 p0[kTerms], p1[kTerms];
       split4<kTerms>(s0[i], p0);
       split4<kTerms>(s1[i], p1);
@@ -156,19 +160,25 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs a) {
     }
 #pragma unroll
     for (int e = 0; e <= kTb; ++e) {
-      u32x4 x[kTerms], y[kTerms];
-      if (e <= tb) {
+      const bool row = e <= tb;
+      const int at = 16 * (row ? e : e - 1);
+      u32x4 x[kTerms];
+      if (half == 0) {
+        if (row) {
 #pragma unroll
-        for (int t = 0; t < kTerms; ++t) x[t] = frag_k_cols(Ut + t * C * kPitchT, kPitchT, 16 * e, 0, lane);
-        Z1[e] = mma<kTerms, NX, kTerms>(x, ot, Z1[e]);
-        Z2[e] = mma<kTerms, kTerms, kTerms>(x, vt, Z2[e]);
+          for (int t = 0; t < kTerms; ++t) x[t] = frag_k_cols(Ut + t * C * kPitchT, kPitchT, at, 0, lane);
+          Z[e] = mma<kTerms, NX, kTerms>(x, ot, Z[e]);
+        } else {
+#pragma unroll
+          for (int t = 0; t < NX; ++t) x[t] = frag_k_cols(Ot + t * C * kPitchT, kPitchT, at, 0, lane);
+          Z[e] = mma<NX, kTerms, kTerms>(x, ut, Z[e]);
+        }
       } else {
+        const uint16_t* from = row ? Ut : Vt;
 #pragma unroll
-        for (int t = 0; t < NX; ++t) x[t] = frag_k_cols(Ot + t * C * kPitchT, kPitchT, 16 * (e - 1), 0, lane);
-#pragma unroll
-        for (int t = 0; t < kTerms; ++t) y[t] = frag_k_cols(Vt + t * C * kPitchT, kPitchT, 16 * (e - 1), 0, lane);
-        Z1[e] = mma<NX, kTerms, kTerms>(x, ut, Z1[e]);
-        Z2[e] = mma<kTerms, kTerms, kTerms>(y, ut, Z2[e]);
+        for (int t = 0; t < kTerms; ++t) x[t] = frag_k_cols(from + t * C * kPitchT, kPitchT, at, 0, lane);
+        if (row) Z[e] = mma<kTerms, kTerms, kTerms>(x, vt, Z[e]);
+        else Z[e] = mma<kTerms, kTerms, kTerms>(x, ut, Z[e]);
       }
     }
     __syncthreads();
@@ -178,95 +188,126 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs a) {
   uint16_t* const Kl = Sl;
   uint16_t* const Ql = Sl + NX * C * kPitchK;
   {
-    const rsrc_t rk = chunk_rows(a.k, ch.row0, a.k_row, (long)hk * a.dk, n, kEsz);
-    const rsrc_t rq = chunk_rows(a.q, ch.row0, a.q_row, (long)hk * a.dk, n, kEsz);
-    const int krow = (int)a.k_row * kEsz, qrow = (int)a.q_row * kEsz;
+    // The tokens' first wave stages K, the second Q.
+    const int xrow = (int)(half ? a.q_row : a.k_row) * kEsz;
+    const rsrc_t rx = chunk_rows(half ? a.q : a.k, ch.row0, half ? a.q_row : a.k_row, (long)hk * a.dk, n, kEsz);
+    uint16_t* const to = half ? Ql : Kl;
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
-      if (kHalves > 1 && KB > 1 && b % kHalves != half) continue;
       const int col = 32 * b + 8 * g;
-      const bool in = tok < n && col < a.dk;
-      u32x4 kt[NX], qt[NX];
-      terms8<NX>(load8<NX>(rk, in ? (uint32_t)(tok * krow + col * kEsz) : kOffNone), kt);
-      terms8<NX>(load8<NX>(rq, in ? (uint32_t)(tok * qrow + col * kEsz) : kOffNone), qt);
+      u32x4 x[NX];
+      terms8<NX>(load8<NX>(rx, col < a.dk ? (uint32_t)(tok * xrow + col * kEsz) : kOffNone), x);
 #pragma unroll
-      for (int t = 0; t < NX; ++t) {
-        *reinterpret_cast<u32x4*>(Kl + (t * C + tok) * kPitchK + col) = kt[t];
-        *reinterpret_cast<u32x4*>(Ql + (t * C + tok) * kPitchK + col) = qt[t];
-      }
+      for (int t = 0; t < NX; ++t) *reinterpret_cast<u32x4*>(to + (t * C + tok) * kPitchK + col) = x[t];
     }
   }
-  // Weights of the pairs; masked ones are 0 whatever their product was.
+  // Weights of the pairs; masked ones are 0 whatever their product was. As operands, of every wave: row blocks kp up
+  // to tb / 2 at kp, columns from tb / 2 on at kp + 1.
+  uint16_t* const Ml = Sl + kRows;
   {
     const float hi = Gh[tok], lo = Gl[tok];
 #pragma unroll
     for (int e = 0; e <= kTb; ++e) {
       const bool row = e <= tb;
       const int o = 16 * (row ? e : e - 1) + 4 * g;
+      const f32x4 ho = *reinterpret_cast<const f32x4*>(Gh + o), lo4 = *reinterpret_cast<const f32x4*>(Gl + o);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int i = row ? tok : o + r, j = row ? o + r : tok;
-        const float dh = hi - Gh[o + r], dl = lo - Gl[o + r];
-        const float d = i >= j ? expf(row ? dh + dl : -dh - dl) : 0.f;
-        Z1[e][r] = i >= j ? Z1[e][r] * d * (row ? 1.f : a.scale) : 0.f;
-        Z2[e][r] = i > j ? -Z2[e][r] * d * (row ? 1.f : Be[o + r]) : 0.f;
+        const float dh = hi - ho[r], dl = lo - lo4[r];
+        const float d = i >= j ? exp_of(row ? dh + dl : -dh - dl) : 0.f;
+        const float w = half ? -d * (row ? 1.f : Be[o + r]) : d * (row ? 1.f : a.scale);
+        Z[e][r] = i > j || (i == j && half == 0) ? Z[e][r] * w : 0.f;
+      }
+    }
+    uint16_t* const to = Ml + wave * kWave + lane * 8;
+#pragma unroll
+    for (int m = 0; m < kKp; ++m) {
+      float x[8], y[8];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int b = 2 * m + t;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          x[4 * t + r] = b <= tb ? Z[b][r] : 0.f;
+          y[4 * t + r] = b >= tb ? Z[b + 1][r] : 0.f;
+        }
+      }
+      u32x4 part[kTerms];
+      if (m <= tb / 2) {
+        split8<kTerms>(x, part);
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t) *reinterpret_cast<u32x4*>(to + (m * kTerms + t) * kOperand) = part[t];
+      }
+      if (m >= tb / 2) {
+        split8<kTerms>(y, part);
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t) *reinterpret_cast<u32x4*>(to + ((m + 1) * kTerms + t) * kOperand) = part[t];
       }
     }
   }
   __syncthreads();
-  u32x4 r1[kKp][kTerms], r2[kKp][kTerms], c1[kKp][kTerms], c2[kKp][kTerms];
-#pragma unroll
-  for (int m = 0; m < kKp; ++m) {
-    float x1[8], x2[8], y1[8], y2[8];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int b = 2 * m + t;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        x1[4 * t + r] = b <= tb ? Z1[b][r] : 0.f;
-        x2[4 * t + r] = b <= tb ? Z2[b][r] : 0.f;
-        y1[4 * t + r] = b >= tb ? Z1[b + 1][r] : 0.f;
-        y2[4 * t + r] = b >= tb ? Z2[b + 1][r] : 0.f;
-      }
-    }
-    split8<kTerms>(x1, r1[m]);
-    split8<kTerms>(x2, r2[m]);
-    split8<kTerms>(y1, c1[m]);
-    split8<kTerms>(y2, c2[m]);
-  }
+  const uint16_t *const z1 = Ml + tb * kWave + lane * 8, *const z2 = Ml + (tb + kTb) * kWave + lane * 8;
   const float be = Be[tok];
   const bool shared = a.part_q != nullptr;
   const long heads = shared ? a.H : a.Hk, hout = shared ? h : hk;
   const rsrc_t wq = chunk_rows(shared ? (void*)a.part_q : a.dq, ch.row0, heads * a.dk, hout * a.dk, n, shared ? 4 : kEsz);
   const rsrc_t wk = chunk_rows(shared ? (void*)a.part_k : a.dk_out, ch.row0, heads * a.dk, hout * a.dk, n, shared ? 4 : kEsz);
   float e_q = 0.f, e_r = 0.f, e_w = 0.f, e_s = 0.f;
+  auto row_of = [&](const uint16_t* L, int b) {   // this lane's four of the token's row
+    f32x4 x = zero;
+#pragma unroll
+    for (int t = NX - 1; t >= 0; --t) x += four(*reinterpret_cast<const u32x2*>(L + (t * C + tok) * kPitchK + 16 * (half * kB + b) + 4 * g));
+    return x;
+  };
 #pragma unroll
   for (int b = 0; b < kB; ++b) {
-    const int col = 16 * (half * kB + b), dk = col + 4 * g;
-    f32x4 kv = zero, qv = zero;
-#pragma unroll
-    for (int t = NX - 1; t >= 0; --t) {
-      kv += four(*reinterpret_cast<const u32x2*>(Kl + (t * C + tok) * kPitchK + dk));
-      qv += four(*reinterpret_cast<const u32x2*>(Ql + (t * C + tok) * kPitchK + dk));
-    }
+    const f32x4 kv = row_of(Kl, b);
     dQ[b] *= eg;
     R[b] *= -eg;
     W[b] *= wt;
 #pragma unroll
     for (int r = 0; r < 4; ++r) e_s = fmaf(kv[r], W[b][r], e_s);
+  }
+  auto masked = [&](const uint16_t* z, int at, u32x4* out) {
 #pragma unroll
-    for (int m = 0; m < kKp; ++m) {
-      u32x4 kt[NX], qt[NX];
+    for (int t = 0; t < kTerms; ++t) out[t] = *reinterpret_cast<const u32x4*>(z + (at * kTerms + t) * kOperand);
+  };
 #pragma unroll
-      for (int t = 0; t < NX; ++t) {
-        kt[t] = frag_k_rows_accpair(Kl + t * C * kPitchK, kPitchK, 32 * m, col, lane);
-        qt[t] = frag_k_rows_accpair(Ql + t * C * kPitchK, kPitchK, 32 * m, col, lane);
+  for (int m = 0; m < kKp; ++m) {
+    u32x4 x[kTerms], y[kTerms];
+    if (m <= tb / 2) {
+      masked(z1, m, x);
+      masked(z2, m, y);
+#pragma unroll
+      for (int b = 0; b < kB; ++b) {
+        u32x4 kt[NX];
+#pragma unroll
+        for (int t = 0; t < NX; ++t) kt[t] = frag_k_rows_accpair(Kl + t * C * kPitchK, kPitchK, 32 * m, 16 * (half * kB + b), lane);
+        dQ[b] = mma<NX, kTerms, kTerms>(kt, x, dQ[b]);
+        R[b] = mma<NX, kTerms, kTerms>(kt, y, R[b]);
       }
-      dQ[b] = mma<NX, kTerms, kTerms>(kt, r1[m], dQ[b]);
-      R[b] = mma<NX, kTerms, kTerms>(kt, r2[m], R[b]);
-      W[b] = mma<NX, kTerms, kTerms>(qt, c1[m], W[b]);
-      W[b] = mma<NX, kTerms, kTerms>(kt, c2[m], W[b]);
     }
+    if (m >= tb / 2) {
+      masked(z1, m + 1, x);
+      masked(z2, m + 1, y);
+#pragma unroll
+      for (int b = 0; b < kB; ++b) {
+        u32x4 kt[NX], qt[NX];
+#pragma unroll
+        for (int t = 0; t < NX; ++t) {
+          kt[t] = frag_k_rows_accpair(Kl + t * C * kPitchK, kPitchK, 32 * m, 16 * (half * kB + b), lane);
+          qt[t] = frag_k_rows_accpair(Ql + t * C * kPitchK, kPitchK, 32 * m, 16 * (half * kB + b), lane);
+        }
+        W[b] = mma<NX, kTerms, kTerms>(qt, x, W[b]);
+        W[b] = mma<NX, kTerms, kTerms>(kt, y, W[b]);
+      }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < kB; ++b) {
+    const int dk = 16 * (half * kB + b) + 4 * g;
+    const f32x4 kv = row_of(Kl, b), qv = row_of(Ql, b);
     dQ[b] *= a.scale;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -317,7 +358,9 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs a) {
       all += __shfl_xor(all, d);
       sw += __shfl_xor(sw, d);
     }
-    const double cross = (double)keep * ((double)dots[0] + (double)dots[1] + (double)dots[2] + (double)dots[3]) + sw;
+    double cross = 0.0;
+    for (int i = 0; i < kThreads / 64; ++i) cross += (double)dots[i];
+    cross = (double)keep * cross + sw;
     if (lane < n) a.dg[(ch.row0 + lane) * a.H + h] = (float)(cross + (all - up + ev));
   }
 }
@@ -325,16 +368,16 @@ __global__ __launch_bounds__(kThreads, 1) void delta_grads_kernel(DeltaArgs a) {
 template <int C, int NX>
 void grads(const DeltaArgs& a, hipStream_t stream) {
   const dim3 grid((unsigned)delta_bwd_blocks(a));
-  if (a.dk <= 32) hipLaunchKernelGGL((delta_grads_kernel<C, 1, NX>), grid, dim3(kThreads), 0, stream, a);
-  else if (a.dk <= 64) hipLaunchKernelGGL((delta_grads_kernel<C, 2, NX>), grid, dim3(kThreads), 0, stream, a);
-  else if (a.dk <= 128) hipLaunchKernelGGL((delta_grads_kernel<C, 4, NX>), grid, dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL((delta_grads_kernel<C, 8, NX>), grid, dim3(kThreads), 0, stream, a);
+  if (a.dk <= 32) hipLaunchKernelGGL((delta_grads_kernel<C, 1, NX>), grid, dim3(threads_of(C)), 0, stream, a);
+  else if (a.dk <= 64) hipLaunchKernelGGL((delta_grads_kernel<C, 2, NX>), grid, dim3(threads_of(C)), 0, stream, a);
+  else if (a.dk <= 128) hipLaunchKernelGGL((delta_grads_kernel<C, 4, NX>), grid, dim3(threads_of(C)), 0, stream, a);
+  else hipLaunchKernelGGL((delta_grads_kernel<C, 8, NX>), grid, dim3(threads_of(C)), 0, stream, a);
 }
 
 }  // namespace
 
 long delta_bwd_blocks(const DeltaArgs& a) { return a.slots * a.H; }
-int delta_bwd_threads() { return kThreads; }
+int delta_bwd_threads() { return threads_of(64); }
 
 hipError_t launch_delta_grads(const DeltaArgs& a, hipStream_t stream) {
   if (a.bf16) grads<64, 1>(a, stream);

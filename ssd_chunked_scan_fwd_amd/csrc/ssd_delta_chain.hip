@@ -12,7 +12,6 @@
 // terms of dO) while the token waves work. The next chunk's rows and operands are
 // loaded into the registers of this one's as soon as these have been used.
 #include <algorithm>
-#include <cmath>
 
 #include "ssd_delta_tile.h"
 
@@ -53,23 +52,25 @@ __device__ __forceinline__ Unit delta_unit(const DeltaArgs& a, const float* init
   const int values = (a.dv + 16 * NV - 1) / (16 * NV), tiles = values + (OWN ? (a.dk + 16 * NV - 1) / (16 * NV) : 0);
   const long id = xcd_unit(blockIdx.x, gridDim.x), mat = (long)a.dk * a.dv, map = (long)a.dk * a.dk;
   const int tile = (int)(id % tiles);
-  u.h = (int)((id / tiles) % a.H);
-  const long n = id / ((long)tiles * a.H);   // sequence or segment
+  // Sequence or segment before head: an XCD takes a contiguous range of units, and all sequences, long and short, of
+  // its heads. (Heads first, an XCD had one of eight ragged sequences: 102 us for what now takes 70.)
+  const long all = a.seg ? a.segs : (long)(a.S > 0 ? a.S : a.batch), n = (id / tiles) % all;
+  u.h = (int)(id / (tiles * all));
   u.map = OWN && tile >= values;
   u.dv0 = (u.map ? tile - values : tile) * 16 * NV;
   u.rows = u.map ? a.dk : a.dv;
   u.none = false;
-  const LinPiece p = lin_piece(a.cu, a.S, a.T, a.seg ? a.seg * C : max(a.T, 1), a.seg ? a.segs_per_row : 1, n);
-  const int blk = a.seg ? p.blk : 0;
-  LinPiece q = p;
-  if (!a.seg) {   // n is the sequence
+  LinPiece q;
+  if (a.seg) {
+    q = lin_piece(a.cu, a.S, a.T, a.seg * C, a.segs_per_row, n);
+  } else {
+    const int c0 = a.cu ? min(max(a.cu[n], 0), a.T) : 0;
     q.seq = (int)n;
-    if (a.cu) {
-      const int c0 = min(max(a.cu[n], 0), a.T);
-      q.start = c0;
-      q.len = min(max(a.cu[n + 1], c0), a.T) - c0;
-    }
+    q.blk = 0;
+    q.start = a.cu ? c0 : n * a.T;
+    q.len = a.cu ? min(max(a.cu[n + 1], c0), a.T) - c0 : a.T;
   }
+  const int blk = q.blk;
   if (blk < 0) {
     u.none = true;
     return u;
@@ -156,7 +157,7 @@ __device__ __forceinline__ void stage4(uint16_t* L, int row, int col, f32x4 x) {
   u32x2 part[N];
   split4<N>(x, part);
 #pragma unroll
-  for (int t = 0; t < N; ++t) *reinterpret_cast<u32x2*>(L + (t * C + row) * PITCH + col) = part[t];
+  for (int t = 0; t < N; ++t) *reinterpret_cast<u32x2*>(L + t * C * PITCH + value_at<PITCH>(row, col)) = part[t];
 }
 // Rows of the wave's tokens, 32 columns a piece, in LDS [term][C][kPitchK]. Waves that hold the same rows share the pieces out.
 template <int C, int KB, int NV, int NX>
@@ -167,7 +168,18 @@ __device__ __forceinline__ void stage_rows(uint16_t* L, const Share<C, KB, NV>& 
   for (int t = 0; t < NX; ++t)
     *reinterpret_cast<u32x4*>(L + (t * C + 16 * w.tb + c16) * kPitchK + 32 * b + 8 * g) = part[t];
 }
-// Operands with k along the tokens 32 kp .. (order of an accumulator pair), N terms.
+// Operands with k along the tokens 32 kp .. (order of an accumulator pair), N terms, of rows of values
+template <int C, int N, int PITCH>
+__device__ __forceinline__ void values_operand(const uint16_t* L, int kp, int col, int lane, u32x4* out) {
+  const int i = lane & 15, g = lane >> 4;
+  const uint16_t* p0 = L + value_at<PITCH>(32 * kp + 4 * g + (i >> 2), col + 4 * (i & 3));
+#pragma unroll
+  for (int t = 0; t < N; ++t) {
+    const u32x2 lo = lds_read_tr16(p0 + t * C * PITCH), hi = lds_read_tr16(p0 + (t * C + 16) * PITCH);
+    out[t] = u32x4{lo.x, lo.y, hi.x, hi.y};
+  }
+}
+// and of rows of keys, [term][C][PITCH].
 template <int C, int N, int PITCH>
 __device__ __forceinline__ void tokens_operand(const uint16_t* L, int kp, int col, int lane, u32x4* out) {
 #pragma unroll
@@ -232,7 +244,7 @@ __device__ __forceinline__ void state_update(const uint16_t* M, const uint16_t* 
   u32x4 yt[Sh::kS][kTerms];
 #pragma unroll
   for (int j = 0; j < Sh::kS; ++j)
-    if (w.sb(j) < NV) tokens_operand<C, kTerms, kPitchV>(Y, kp, 16 * w.sb(j), lane, yt[j]);
+    if (w.sb(j) < NV) values_operand<C, kTerms, kPitchV>(Y, kp, 16 * w.sb(j), lane, yt[j]);
 #pragma unroll
   for (int i = 0; i < Sh::kB; ++i) {
     u32x4 mt[NX];
@@ -316,7 +328,6 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
     loads_done();
     __syncthreads();
     for (int c = 0; c <= last; ++c) {
-      const int ahead = min(c + 1, last);
       const long sh = sh0 + (long)c * a.H;
       // X = V - e^G (K S^T): lane token c16, value columns 4 g + r.
       f32x4 X[Sh::kV];
@@ -334,7 +345,7 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
       }
 #pragma unroll
       for (int b = 0; b < KB; ++b) stage_rows<C, KB, NV, NX>(Kl, w, c16, g, b, kt[b]);
-      load_rows(ahead);
+      load_rows(min(c + 1, last));
       __syncthreads();
 
       // U = T diag(beta) X.
@@ -347,7 +358,7 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
         for (int kp = 0; kp < kKp; ++kp) {
           if (kp > w.tb / 2) continue;
           u32x4 xt[kTerms];
-          tokens_operand<C, kTerms, kPitchV>(Xl, kp, 16 * w.vb(i), lane, xt);
+          values_operand<C, kTerms, kPitchV>(Xl, kp, 16 * w.vb(i), lane, xt);
           U[i] = mma<kTerms, kTerms, kTerms>(xt, tf[kp], U[i]);
         }
         stage4<C, kTerms, kPitchV>(Wl, tok, 16 * w.vb(i) + 4 * g, U[i] * wt);
@@ -390,7 +401,7 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
         for (int kp = 0; kp < kKp; ++kp) {
           if (kp > w.tb / 2) continue;
           u32x4 ut[kOut];
-          tokens_operand<C, kOut, kPitchV>(Ul + (c & 1) * kU, kp, 16 * w.vb(i), lane, ut);
+          values_operand<C, kOut, kPitchV>(Ul + (c & 1) * kU, kp, 16 * w.vb(i), lane, ut);
           O[i] = mma<kOut, kOut, kOut>(ut, pf[kp], O[i]);
         }
         store4<NX>(O[i], ro, oat.at[i]);
@@ -499,7 +510,6 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
     __syncthreads();
     __syncthreads();
     for (int c = last; c >= 0; --c) {
-      const int ahead = max(c - 1, 0);
       const long sh = sh0 + (long)c * a.H;
       // Y = e^(G_C - G) (K L^T) + P^T dO.
       f32x4 Y[Sh::kV];
@@ -518,7 +528,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
       }
 #pragma unroll
       for (int b = 0; b < KB; ++b) stage_rows<C, KB, NV, NX>(Kl, w, c16, g, b, kt[b]);
-      load_rows(ahead);
+      load_rows(max(c - 1, 0));
       __syncthreads();
 
       // U' = T^T Y, dV = beta U'.
@@ -532,7 +542,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
         for (int kp = 0; kp < kKp; ++kp) {
           if (kp < w.tb / 2) continue;
           u32x4 yt[kTerms];
-          tokens_operand<C, kTerms, kPitchV>(Yl, kp, 16 * w.vb(i), lane, yt);
+          values_operand<C, kTerms, kPitchV>(Yl, kp, 16 * w.vb(i), lane, yt);
           U[i] = mma<kTerms, kTerms, kTerms>(yt, tt[kp], U[i]);
         }
         stage4<C, kTerms, kPitchV>(Xl, tok, 16 * w.vb(i) + 4 * g, U[i] * (-eg * be));
@@ -597,7 +607,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
         for (int kp = 0; kp < kKp; ++kp) {
           if (kp < w.tb / 2) continue;
           u32x4 ot[NX], pt[kTerms];
-          tokens_operand<C, NX, kPitchV>(Ol, kp, 16 * w.vb(i), lane, ot);
+          values_operand<C, NX, kPitchV>(Ol, kp, 16 * w.vb(i), lane, ot);
           terms8<kTerms>(pr[kp], pt);
           D = mma<NX, kTerms, kTerms>(ot, pt, D);
         }
@@ -748,25 +758,28 @@ long delta_segment_blocks(const DeltaArgs& a) {
 // A walk of few heads leaves most of the card idle for as long as its longest sequence is. Cut into segments, every
 // segment's own last state (from a state of zero) and its map of a state are made at once, the states behind the
 // segments follow from these one after the other, and all segments are walked at once: twice to three times the
-// work, in chains of a segment's length. The number of segments is the one of least cost in steps of a chunk: two
-// workgroups a CU run at once; a step of two takes about 1.3 times one's, a step without O 0.8 of one with it; a
-// segment's join takes about one step, the two launches more five. The host does not know the lengths of packed
-// sequences: the longest is taken to be three times the mean.
+// work, in chains of a segment's length (8192 tokens, 4 heads of 128 x 128: 220 us whole, 90 in eight segments). The
+// number of segments is the one of least cost, counted in steps of a chunk: a walk takes as long as its longest chain,
+// or as its steps shared out over 256 CUs, one at a time (workgroups on one CU do not overlap by more than a tenth);
+// a step without O 0.8 of one with it; a segment's join about one step, the two launches five. The host does not
+// know the lengths of packed sequences: the longest is taken to be three times the mean. (Eight ragged sequences of
+// 5087 tokens, 16 heads: 99 us whole, 110 in segments of nine chunks.)
 int delta_segment(int batch, int T, int S, int H, int dk, int dv, bool bf16) {
   const int C = delta_chunk(bf16);
   const long seqs = S > 0 ? S : batch, tokens = (long)batch * T;
   const long longest = S > 0 ? std::min((long)T, 3 * ((tokens + S - 1) / S)) : T;
   const long chunks = (longest + C - 1) / C, all = (tokens + C - 1) / C;
   const int values = tiles_of(dv, dk, bf16), rows = values + tiles_of(dk, dk, bf16);
-  auto rounds = [](double units) { return units <= 256 ? 1.0 : 1.3 * std::ceil(units / 512); };
-  double least = rounds((double)seqs * H * values) * chunks;
+  auto steps = [](double chain, double work) { return std::max(chain, work / 256); };
+  const double outputs = (double)all * H * values;
+  double least = 0.9 * steps((double)chunks, outputs);
   int best = 0;
   for (long n = 2; n <= 64 && n <= chunks; ++n) {
     const long c = (chunks + n - 1) / n;
-    const double segs = std::max((double)all / c, (double)seqs);
-    const double cost = 0.8 * rounds((segs - seqs) * H * rows) * c + (double)n + 5.0 + rounds(segs * H * values) * c;
-    if (cost < 0.9 * least) {
-      least = cost / 0.9;
+    const double own = std::max((double)all - (double)seqs * c, 0.0) * H * rows;   // not of the last segments
+    const double cost = 0.8 * steps((double)c, own) + (double)n + 5.0 + steps((double)c, outputs);
+    if (cost < least) {
+      least = cost;
       best = (int)c;
     }
   }

@@ -24,13 +24,21 @@ constexpr int kThreads = 256;
 template <int C>
 constexpr int kPitch = C + 4;   // floats; rows of 16-byte pieces
 
-// Inclusive sum over the lanes 0..l, in 64 bits.
-__device__ __forceinline__ double lanes_up(double x, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const double y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
+// Inclusive sum over the lanes 0..l, in 64 bits: wave_incl_scan on both halves of a double.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double pick64(double x) {
+  const long v = __builtin_bit_cast(long, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(v & 0xffffffffL), CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, (long)((uint64_t)hi << 32 | lo));
+}
+__device__ __forceinline__ double lanes_up(double x) {
+  x += pick64<0x111, 0xF>(x);
+  x += pick64<0x112, 0xF>(x);
+  x += pick64<0x114, 0xF>(x);
+  x += pick64<0x118, 0xF>(x);
+  x += pick64<0x142, 0xA>(x);
+  x += pick64<0x143, 0xC>(x);
   return x;
 }
 
@@ -156,7 +164,7 @@ __device__ __forceinline__ void tile_of(int wave, int e, int& ib, int& jb) {
 }
 
 template <int C, int KB, int NX, bool BWD>
-__global__ __launch_bounds__(kThreads, 3) void delta_prep_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kThreads, BWD ? 3 : 4) void delta_prep_kernel(DeltaArgs a, int heads) {
   constexpr int kTiles = C == 64 ? 3 : 1;   // a wave
   constexpr int kEsz = NX == 1 ? 2 : 4, kOut = out_terms(NX);
   // Rows of K and Q, kSlab pieces of 32 columns at a time, and in their place the matrix.
@@ -169,21 +177,22 @@ __global__ __launch_bounds__(kThreads, 3) void delta_prep_kernel(DeltaArgs a) {
   __shared__ __align__(16) float Gh[4][C], Gl[4][C], Be[4][C];   // of four heads at a time
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
   const long unit = xcd_unit(blockIdx.x, gridDim.x);
-  const int hk = (int)(unit % a.Hk);
-  const long slot = unit / a.Hk;
+  const int rep = a.H / a.Hk, parts = (rep + heads - 1) / heads;   // `heads` value heads a workgroup
+  const int part = (int)(unit % parts), hk = (int)((unit / parts) % a.Hk), first = part * heads, end = min(first + heads, rep);
+  const long slot = unit / ((long)parts * a.Hk);
   const DeltaChunk ch = delta_slot<C>(a, slot);
   if (ch.p.blk < 0 || ch.n <= 0) return;
-  const int n = ch.n, rep = a.H / a.Hk;
+  const int n = ch.n;
   const rsrc_t rk = chunk_rows(a.k, ch.row0, a.k_row, (long)hk * a.dk, n, kEsz);
   const rsrc_t rq = chunk_rows(a.q, ch.row0, a.q_row, (long)hk * a.dk, n, kEsz);
   const int krow = (int)a.k_row * kEsz, qrow = (int)a.q_row * kEsz;
   float gx = 0.f, bx = 0.f;   // the gates of this lane's token, of head m0 + wave
   auto load_gates = [&](int m0) {
-    const long at = (ch.row0 + min(lane, n - 1)) * a.H + hk * rep + min(m0 + wave, rep - 1);
+    const long at = (ch.row0 + min(lane, n - 1)) * a.H + hk * rep + min(m0 + wave, end - 1);
     if (a.g) gx = a.g[at];
     bx = a.beta[at];
   };
-  load_gates(0);
+  load_gates(first);
   // Of keys j (rows 4 g + r) and queries or keys i (columns c16); BWD: Q K^T the other way round, as its transpose is stored.
   f32x4 kk[kTiles], qk[kTiles];
 #pragma unroll
@@ -235,17 +244,17 @@ __global__ __launch_bounds__(kThreads, 3) void delta_prep_kernel(DeltaArgs a) {
   __syncthreads();
   for (int i = threadIdx.x; i < C * kPitch<C>; i += kThreads) Am[i] = 0.f;
 
-  for (int m = 0; m < rep; ++m) {
-    const int h = hk * rep + m, mw = m & 3;
+  for (int m = first; m < end; ++m) {
+    const int h = hk * rep + m, mw = (m - first) & 3;
     const long sh = slot * a.H + h;
-    if (m > 0) __syncthreads();   // the last head's operands are out
+    if (m > first) __syncthreads();   // the last head's operands are out
     if (mw == 0) {
-      if (m + wave < rep) {
+      if (m + wave < end) {
         float* gates = a.gates + (sh + wave) * kGateRows * C;
         const bool in = lane < n;
         // Below -200 a decay is 0 in fp32, as e^-200 is, and its sums stay finite.
         const float x = !in ? 0.f : gx < -200.f ? -200.f : gx, be = in ? bx : 0.f;
-        const double G = lanes_up((double)x, lane), end = __shfl(G, C - 1);
+        const double G = lanes_up((double)x), end = __shfl(G, C - 1);
         if (lane < C) {
           const float hi = (float)G, lo = (float)(G - (double)hi);
           Gh[wave][lane] = hi;
@@ -253,15 +262,15 @@ __global__ __launch_bounds__(kThreads, 3) void delta_prep_kernel(DeltaArgs a) {
           Be[wave][lane] = be;
           const double left = end - G;
           const float lh = (float)left, ll = (float)(left - (double)lh);
-          gates[lane] = expf(hi) * (1.f + lo);
-          gates[C + lane] = in ? expf(lh) * (1.f + ll) : 0.f;
+          gates[lane] = exp_of(hi) * (1.f + lo);
+          gates[C + lane] = in ? exp_of(lh) * (1.f + ll) : 0.f;
           gates[2 * C + lane] = be;
           gates[3 * C + lane] = hi;
           gates[4 * C + lane] = lo;
-          if (lane == C - 1) gates[5 * C] = expf(hi) * (1.f + lo);
+          if (lane == C - 1) gates[5 * C] = exp_of(hi) * (1.f + lo);
         }
       }
-      if (m + 4 < rep) load_gates(m + 4);
+      if (m + 4 < end) load_gates(m + 4);
       __syncthreads();
     }
     const float *gh = Gh[mw], *gl = Gl[mw], *bt = Be[mw];
@@ -271,19 +280,22 @@ __global__ __launch_bounds__(kThreads, 3) void delta_prep_kernel(DeltaArgs a) {
       tile_of<C>(wave, e, ib, jb);
       if (ib < 0) continue;
       const int i = 16 * ib + c16, j = 16 * jb + 4 * g;
-      f32x4 d;
+      const f32x4 hj = *reinterpret_cast<const f32x4*>(gh + j), lj = *reinterpret_cast<const f32x4*>(gl + j);
+      const float hi = gh[i], lo = gl[i], be = bt[i];
+      f32x4 d, A, P;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) d[r] = j + r <= i ? expf((gh[i] - gh[j + r]) + (gl[i] - gl[j + r])) : 0.f;
-      f32x4 A, P;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) A[r] = j + r < i ? bt[i] * d[r] * kk[e][r] : 0.f;
+      for (int r = 0; r < 4; ++r) {
+        d[r] = j + r <= i ? exp_of((hi - hj[r]) + (lo - lj[r])) : 0.f;
+        A[r] = j + r < i ? be * d[r] * kk[e][r] : 0.f;
+      }
       *reinterpret_cast<f32x4*>(Am + i * kPitch<C> + j) = A;
       const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
       if (BWD) {
         const int i4 = 16 * ib + 4 * g, j1 = 16 * jb + c16;
+        const f32x4 hr = *reinterpret_cast<const f32x4*>(gh + i4), lr = *reinterpret_cast<const f32x4*>(gl + i4);
+        const float h1 = gh[j1], l1 = gl[j1];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          P[r] = j1 <= i4 + r ? a.scale * expf((gh[i4 + r] - gh[j1]) + (gl[i4 + r] - gl[j1])) * qk[e][r] : 0.f;
+        for (int r = 0; r < 4; ++r) P[r] = j1 <= i4 + r ? a.scale * exp_of((hr[r] - h1) + (lr[r] - l1)) * qk[e][r] : 0.f;
         float* to = a.pt + sh * operands(C, 1);
         put_tile<C>(P, to, jb, ib, lane);
         if (ib == jb && (ib & 1)) put_tile<C>(zero, to, jb, ib - 1, lane);
@@ -307,13 +319,23 @@ __global__ __launch_bounds__(kThreads, 3) void delta_prep_kernel(DeltaArgs a) {
   }
 }
 
+// Value heads a workgroup: all that share its keys, whose products it makes once, or so few that the launch has
+// four workgroups for every CU. A workgroup's time is mostly waits: 348 of four heads took 28 us, 1392 of one 17.
+int heads_a_workgroup(const DeltaArgs& a) {
+  const int rep = a.H / a.Hk;
+  int heads = rep;
+  while (heads > 1 && a.slots * a.Hk * ((rep + heads - 1) / heads) < 1024) heads = (heads + 1) / 2;
+  return heads;
+}
+
 template <int C, int NX, bool BWD>
 void prep(const DeltaArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.slots * a.Hk));
-  if (a.dk <= 32) hipLaunchKernelGGL((delta_prep_kernel<C, 1, NX, BWD>), grid, dim3(kThreads), 0, stream, a);
-  else if (a.dk <= 64) hipLaunchKernelGGL((delta_prep_kernel<C, 2, NX, BWD>), grid, dim3(kThreads), 0, stream, a);
-  else if (a.dk <= 128) hipLaunchKernelGGL((delta_prep_kernel<C, 4, NX, BWD>), grid, dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL((delta_prep_kernel<C, 8, NX, BWD>), grid, dim3(kThreads), 0, stream, a);
+  const int heads = heads_a_workgroup(a), rep = a.H / a.Hk;
+  const dim3 grid((unsigned)(a.slots * a.Hk * ((rep + heads - 1) / heads)));
+  if (a.dk <= 32) hipLaunchKernelGGL((delta_prep_kernel<C, 1, NX, BWD>), grid, dim3(kThreads), 0, stream, a, heads);
+  else if (a.dk <= 64) hipLaunchKernelGGL((delta_prep_kernel<C, 2, NX, BWD>), grid, dim3(kThreads), 0, stream, a, heads);
+  else if (a.dk <= 128) hipLaunchKernelGGL((delta_prep_kernel<C, 4, NX, BWD>), grid, dim3(kThreads), 0, stream, a, heads);
+  else hipLaunchKernelGGL((delta_prep_kernel<C, 8, NX, BWD>), grid, dim3(kThreads), 0, stream, a, heads);
 }
 
 }  // namespace

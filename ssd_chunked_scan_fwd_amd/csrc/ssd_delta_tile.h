@@ -195,9 +195,23 @@ __device__ __forceinline__ void load_operands(const uint16_t* from, long sh, int
 // of its own loads then, not for that of the loads before it.
 __device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }   // vmcnt(0)
 
-// LDS rows of 16 nv values that are read transposed: 24 values apart for nv = 1
-// (two workgroups a CU need the room), else an odd multiple of 32 bytes.
-__host__ __device__ constexpr int value_pitch(int nv) { return nv == 1 ? 24 : lds_pitch(16 * nv); }
+// LDS rows of 16 nv values of a token, written 8 bytes a lane (16 rows) and read transposed (8 rows a half wave). One
+// block of 16: rows of 32 bytes, one behind the other, the two halves of every second 8 rows exchanged; both accesses
+// then cover the 64 banks once. (Padded rows of 48 bytes cost a walk 760 of its 1710 LDS cycles a chunk in conflicts.)
+// More blocks: an odd multiple of 32 bytes.
+__host__ __device__ constexpr int value_pitch(int nv) { return nv == 1 ? 16 : lds_pitch(16 * nv); }
+template <int PITCH>
+__device__ __forceinline__ int value_at(int row, int col) {
+  return row * PITCH + (PITCH == 16 ? col ^ (row & 8) : col);
+}
+
+// e^x to an ulp or two, with the hardware's 2^y: what rounds off y = x log2(e) is put back to first order. (The
+// library's exponential took a third of the time of the chunks' matrices.)
+__device__ __forceinline__ float exp_of(float x) {
+  const float y = x * kLog2e, rest = fmaf(x, kLog2e, -y);
+  const float p = fast_exp2(y);
+  return fmaf(p, rest * 0.69314718f, p);
+}
 
 // The chunk of a workgroup.
 struct DeltaChunk {
