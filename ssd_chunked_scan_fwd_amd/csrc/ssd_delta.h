@@ -46,6 +46,7 @@ struct DeltaArgs {
   long segs_per_row = 0, segs = 0;
   float* seg_states = nullptr;   // [segs][H][dv][dk]: a segment's own last state, then the state behind it
   float* seg_maps = nullptr;     // [segs][H][dk][dk]: what the segment makes of a state's row
+  float* seg_adj = nullptr;      // [segs][H][dv][dk]: the gradient of the state before a segment, its own, then all of it
   // Gradients.
   float *tt = nullptr, *pt = nullptr;            // T^T and P^T, operands
   const void* d_o = nullptr;     // [tokens][H][dv]
@@ -66,7 +67,7 @@ size_t delta_gates_bytes(bool bf16);
 size_t delta_tf_bytes(bool bf16);   // of T and the transposes, each
 size_t delta_pf_bytes(bool bf16);
 
-// Chunks a segment of a forward walk over these sizes, 0: no sequence is cut.
+// Chunks a segment of a walk over these sizes, 0: no sequence is cut.
 int delta_segment(int batch, int T, int S, int H, int dk, int dv, bool bf16);
 
 int delta_prep_threads();
@@ -77,7 +78,7 @@ long delta_bwd_blocks(const DeltaArgs& a);
 int delta_bwd_threads();
 
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stream);
-hipError_t launch_delta_fwd(const DeltaArgs& a, bool keep, hipStream_t stream);   // keep: states and u instead of o, not cut
+hipError_t launch_delta_fwd(const DeltaArgs& a, bool keep, hipStream_t stream);   // keep: states and u instead of o
 hipError_t launch_delta_rev(const DeltaArgs& a, hipStream_t stream);
 hipError_t launch_delta_grads(const DeltaArgs& a, hipStream_t stream);
 

@@ -76,7 +76,7 @@ ssd_status check_delta(const ssd_delta_shape* s, DeltaDims* d, bool backward) {
   const int C = ssd::delta_chunk(s->dtype == SSD_DTYPE_BF16);
   d->spr = ssd::lin_slots_per_row(s->seqlen, s->num_seqs, C);
   d->slots = s->num_seqs > 0 ? d->spr : d->spr * s->batch;
-  d->seg = backward ? 0 : ssd::delta_segment(s->batch, s->seqlen, s->num_seqs, s->nheads, s->dk, s->dv, s->dtype == SSD_DTYPE_BF16);
+  d->seg = ssd::delta_segment(s->batch, s->seqlen, s->num_seqs, s->nheads, s->dk, s->dv, s->dtype == SSD_DTYPE_BF16);
   d->segs_per_row = d->seg ? ssd::lin_slots_per_row(s->seqlen, s->num_seqs, d->seg * C) : 0;
   d->segs = s->num_seqs > 0 ? d->segs_per_row : d->segs_per_row * s->batch;
   const ssd::DeltaArgs a = delta_args(s, *d);
@@ -91,7 +91,7 @@ ssd_status check_delta(const ssd_delta_shape* s, DeltaDims* d, bool backward) {
 }
 
 struct DeltaLayout {
-  size_t gates, tf, pf, seg_states, seg_maps, tt, pt, states, dstates, u, ub, part_q, part_k, total;
+  size_t gates, tf, pf, seg_states, seg_maps, seg_adj, tt, pt, states, dstates, u, ub, part_q, part_k, total;
 };
 DeltaLayout delta_layout(const ssd_delta_shape* s, const DeltaDims& d, bool backward) {
   DeltaLayout L{};
@@ -106,11 +106,12 @@ DeltaLayout delta_layout(const ssd_delta_shape* s, const DeltaDims& d, bool back
   };
   L.gates = take(units * ssd::delta_gates_bytes(bf16));
   L.tf = take(units * ssd::delta_tf_bytes(bf16));
+  L.seg_states = take((size_t)d.segs * s->nheads * mat);
+  L.seg_maps = take((size_t)d.segs * s->nheads * s->dk * s->dk * 4);
   if (!backward) {
     L.pf = take(units * ssd::delta_pf_bytes(bf16));
-    L.seg_states = take((size_t)d.segs * s->nheads * mat);
-    L.seg_maps = take((size_t)d.segs * s->nheads * s->dk * s->dk * 4);
   } else {
+    L.seg_adj = take((size_t)d.segs * s->nheads * mat);
     L.tt = take(units * ssd::delta_tf_bytes(bf16));
     L.pt = take(units * ssd::delta_tf_bytes(bf16));
     L.states = take(units * mat);
@@ -253,6 +254,9 @@ ssd_status ssd_gated_delta_bwd(const void* q, const void* k, const void* v, cons
   a.init = initial_state;
   a.gates = floats(L.gates);
   a.tf = reinterpret_cast<float*>(ws + L.tf);
+  a.seg_states = floats(L.seg_states);
+  a.seg_maps = floats(L.seg_maps);
+  a.seg_adj = floats(L.seg_adj);
   a.tt = floats(L.tt);
   a.pt = floats(L.pt);
   a.d_o = d_o;

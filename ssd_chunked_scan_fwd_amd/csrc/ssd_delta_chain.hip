@@ -46,17 +46,18 @@ struct Unit {
   const float* from;               // the state before, null: zero
   float* to;                       // the state behind, null: not wanted
 };
-template <int C, int NV, bool OWN>
-__device__ __forceinline__ Unit delta_unit(const DeltaArgs& a, const float* init, float* fin) {
+// REV: backwards, `first` and `last` the gradients of the last and of the first state.
+template <int C, int NV, bool OWN, bool REV>
+__device__ __forceinline__ Unit delta_unit(const DeltaArgs& a, const float* first, float* last) {
   Unit u;
-  const int values = (a.dv + 16 * NV - 1) / (16 * NV), tiles = values + (OWN ? (a.dk + 16 * NV - 1) / (16 * NV) : 0);
+  const int values = (a.dv + 16 * NV - 1) / (16 * NV), tiles = values + (OWN && !REV ? (a.dk + 16 * NV - 1) / (16 * NV) : 0);
   const long id = xcd_unit(blockIdx.x, gridDim.x), mat = (long)a.dk * a.dv, map = (long)a.dk * a.dk;
   const int tile = (int)(id % tiles);
   // Sequence or segment before head: an XCD takes a contiguous range of units, and all sequences, long and short, of
   // its heads. (Heads first, an XCD had one of eight ragged sequences: 102 us for what now takes 70.)
   const long all = a.seg ? a.segs : (long)(a.S > 0 ? a.S : a.batch), n = (id / tiles) % all;
   u.h = (int)(id / (tiles * all));
-  u.map = OWN && tile >= values;
+  u.map = OWN && !REV && tile >= values;
   u.dv0 = (u.map ? tile - values : tile) * 16 * NV;
   u.rows = u.map ? a.dk : a.dv;
   u.none = false;
@@ -75,20 +76,21 @@ __device__ __forceinline__ Unit delta_unit(const DeltaArgs& a, const float* init
     u.none = true;
     return u;
   }
-  const long first = (long)blk * a.seg * C;
-  u.len = a.seg ? (int)min((long)q.len - first, (long)a.seg * C) : q.len;
+  const long begin = (long)blk * a.seg * C;
+  u.len = a.seg ? (int)min((long)q.len - begin, (long)a.seg * C) : q.len;
   u.chunks = (u.len + C - 1) / C;
-  u.start = q.start + first;
-  u.slot0 = (a.cu ? q.start / C + q.seq : (long)q.seq * a.slots_per_row) + first / C;
-  const bool last = first + u.len >= q.len;
+  u.start = q.start + begin;
+  u.slot0 = (a.cu ? q.start / C + q.seq : (long)q.seq * a.slots_per_row) + begin / C;
+  const bool at_end = begin + u.len >= q.len, entry = REV ? at_end : blk == 0, exit = REV ? blk == 0 : at_end;
   const long sh = (long)q.seq * a.H + u.h;
+  float* const states = REV ? a.seg_adj : a.seg_states;
   if (OWN) {
-    u.none = last || (u.map && blk == 0);   // nothing comes behind it; the state before it is known
-    u.from = blk == 0 && init && !u.map ? init + sh * mat : nullptr;
-    u.to = u.map ? a.seg_maps + (n * a.H + u.h) * map : a.seg_states + (n * a.H + u.h) * mat;
+    u.none = exit || (u.map && entry);   // nothing comes behind it; the state before it is known
+    u.from = entry && first && !u.map ? first + sh * mat : nullptr;
+    u.to = u.map ? a.seg_maps + (n * a.H + u.h) * map : states + (n * a.H + u.h) * mat;
   } else {
-    u.from = blk > 0 ? a.seg_states + ((n - 1) * a.H + u.h) * mat : init ? init + sh * mat : nullptr;
-    u.to = last && fin ? fin + sh * mat : nullptr;
+    u.from = !entry ? states + ((REV ? n + 1 : n - 1) * a.H + u.h) * mat : first ? first + sh * mat : nullptr;
+    u.to = exit && last ? last + sh * mat : nullptr;
   }
   return u;
 }
@@ -268,7 +270,7 @@ enum { kOutputs, kKeep, kOwn };
 
 // NX: terms of an input.
 template <int C, int KB, int NV, int NX, int WHAT>
-__global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fwd_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 && NV == 1 ? 4 : 2) void delta_fwd_kernel(DeltaArgs a) {
   using Sh = Share<C, KB, NV>;
   constexpr bool KEEP = WHAT != kOutputs;
   constexpr int kEsz = NX == 1 ? 2 : 4, kOut = out_terms(NX), kKp = C / 32;
@@ -281,7 +283,7 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
   const int wave = uniform(threadIdx.x >> 6);
   const Sh w(wave & 3);
   const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
-  const Unit u = delta_unit<C, NV, WHAT == kOwn>(a, a.init, a.fin);
+  const Unit u = delta_unit<C, NV, WHAT == kOwn, false>(a, a.init, a.fin);
   if (u.none) return;
   const int hk = u.h / (a.H / a.Hk), tok = 16 * w.tb + c16, last = u.chunks - 1;
   const long mat = (long)a.dk * a.dv, sh0 = u.slot0 * a.H + u.h;
@@ -450,7 +452,8 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 ? 4 : 2) void delta_fw
 // The adjoint, from the last chunk to the first: U', dV, the gradients of the states before the chunks. What the
 // state waves make ahead of the token waves: dO's terms of the state, (e^G dO)^T Q, while these make Y, and P^T dO
 // of the next chunk while they make U'.
-template <int C, int KB, int NV, int NX>
+// OWN: of a segment, its own gradient of the state before it alone.
+template <int C, int KB, int NV, int NX, bool OWN>
 __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
   using Sh = Share<C, KB, NV>;
   constexpr int kEsz = NX == 1 ? 2 : 4, kKp = C / 32;
@@ -464,7 +467,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
   const int wave = uniform(threadIdx.x >> 6);
   const Sh w(wave & 3);
   const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
-  const Unit u = delta_unit<C, NV, false>(a, a.dfin, a.dinit);
+  const Unit u = delta_unit<C, NV, OWN, true>(a, a.dfin, a.dinit);
+  if (u.none) return;
   const int hk = u.h / (a.H / a.Hk), tok = 16 * w.tb + c16, last = u.chunks - 1;
   const long mat = (long)a.dk * a.dv, sh0 = u.slot0 * a.H + u.h;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -546,6 +550,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
           U[i] = mma<kTerms, kTerms, kTerms>(yt, tt[kp], U[i]);
         }
         stage4<C, kTerms, kPitchV>(Xl, tok, 16 * w.vb(i) + 4 * g, U[i] * (-eg * be));
+        if (OWN) continue;
         buf_store16(__builtin_bit_cast(u32x4, U[i]), make_rsrc(a.ub + sh * C * a.dv, (uint32_t)(C * a.dv * 4)), uat.at[i]);
         store4<NX>(U[i] * be, rv, vat.at[i]);
       }
@@ -635,7 +640,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
     __syncthreads();
     if (last >= 0) stage_o(d1);
     for (int c = last; c >= 0; --c) {
-      pieces.store(a.dstates + (sh0 + (long)c * a.H) * mat, L);
+      if (!OWN) pieces.store(a.dstates + (sh0 + (long)c * a.H) * mat, L);
       // L = e^(G_C) L + scale (e^G dO)^T Q - (e^G beta U')^T K, the last term when U' is there.
       scale_state<C, KB, NV>(L, keep);
       load_keep(max(c - 1, 0));
@@ -662,10 +667,11 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
   }
 }
 
-// The states behind the segments of a sequence, one after the other: R := R M + own, of 16 rows of one head, in fp32
+// The states behind the segments of a sequence, one after the other: R := R M + own (REV: the gradients of the states
+// before them, from the last to the first, R := R M^T + own), of 16 rows of one head, in fp32
 // (matrix instructions on fp32). A wave makes 16 of the key columns; R goes round through LDS, and the next segment's
 // map is on its way while this one's is taken.
-template <int KB>
+template <int KB, bool REV>
 __global__ __launch_bounds__(128 * KB) void delta_join_kernel(DeltaArgs a, int C) {
   constexpr int kBlocks = 2 * KB;   // waves
   __shared__ __align__(16) f32x4 Rl[kBlocks * 64];   // blocks of 16 key columns as accumulators hold them
@@ -684,23 +690,31 @@ __global__ __launch_bounds__(128 * KB) void delta_join_kernel(DeltaArgs a, int C
   }
   const int segs = (int)((len + L - 1) / L), dv = 16 * tile + c16;
   if (segs < 3) return;   // the state behind the first segment is its own
-  f32x4 R, own, M[kBlocks];   // M: rows 16 k + 4 g + t of the map, column c16 of this wave's block
+  f32x4 R, own, M[kBlocks];   // M: rows 16 k + 4 g + t of the map, column c16 of this wave's block; REV: of its transpose
   const int dk = 16 * wave + 4 * g, col = 16 * wave + c16;
   const uint32_t at = dv < a.dv && dk < a.dk ? (uint32_t)((dv * a.dk + dk) * 4) : kOffNone;
-  const uint32_t mat0 = col < a.dk ? (uint32_t)((4 * g * a.dk + col) * 4) : kOffNone;   // rows behind the map: behind its end
-  auto state = [&](int s) { return make_rsrc(a.seg_states + ((n0 + s) * a.H + h) * mat, (uint32_t)(mat * 4)); };
+  const uint32_t mat0 = col >= a.dk ? kOffNone : REV ? (uint32_t)(col * a.dk * 4) : (uint32_t)((4 * g * a.dk + col) * 4);
+  float* const states = REV ? a.seg_adj : a.seg_states;
+  auto state = [&](int s) { return make_rsrc(states + ((n0 + s) * a.H + h) * mat, (uint32_t)(mat * 4)); };
   auto load = [&](int s) {
     const rsrc_t rm = make_rsrc(a.seg_maps + ((n0 + s) * a.H + h) * map, (uint32_t)(map * 4));
     own = __builtin_bit_cast(f32x4, buf_load16(state(s), at));
 #pragma unroll
-    for (int k = 0; k < kBlocks; ++k)
+    for (int k = 0; k < kBlocks; ++k) {
+      if constexpr (REV) {
+        M[k] = __builtin_bit_cast(f32x4, buf_load16(rm, 16 * k + 4 * g < a.dk ? mat0 + (uint32_t)((16 * k + 4 * g) * 4) : kOffNone));
+      } else {   // rows behind the map lie behind its end
 #pragma unroll
-      for (int t = 0; t < 4; ++t) M[k][t] = buf_load_f32(rm, mat0 + (uint32_t)((16 * k + t) * a.dk * 4));
+        for (int t = 0; t < 4; ++t) M[k][t] = buf_load_f32(rm, mat0 + (uint32_t)((16 * k + t) * a.dk * 4));
+      }
+    }
   };
-  R = __builtin_bit_cast(f32x4, buf_load16(state(0), at));
-  load(1);
+  const int first = REV ? segs - 1 : 0, step = REV ? -1 : 1, middle = segs - 2;   // segments between the first and the last
+  R = __builtin_bit_cast(f32x4, buf_load16(state(first), at));
+  load(first + step);
   loads_done();
-  for (int s = 1; s < segs - 1; ++s) {
+  for (int i = 1; i <= middle; ++i) {
+    const int s = first + step * i;
     Rl[wave * 64 + lane] = R;
     __syncthreads();
     f32x4 x[2] = {own, f32x4{0.f, 0.f, 0.f, 0.f}};
@@ -712,64 +726,89 @@ __global__ __launch_bounds__(128 * KB) void delta_join_kernel(DeltaArgs a, int C
     }
     R = x[0] + x[1];
     buf_store16(__builtin_bit_cast(u32x4, R), state(s), at);
-    load(min(s + 1, segs - 2));
+    load(first + step * min(i + 1, middle));
     __syncthreads();
   }
 }
 
-// Value blocks a workgroup: with keys of 256, fp32 rows leave LDS for one.
-constexpr int kNv64 = 1;
+// Value blocks a workgroup. Two, which read a chunk's rows and operands once, where workgroups of one would be more
+// than the CUs (of packed sequences, the longest of which are taken to be three times the mean, three times as many);
+// else one. Heads of 128 x 128, us with one and with two: 2 x 4096 tokens of 32 heads (512 workgroups of one) 260 and
+// 219, 4096 of 48 235 and 193; 5087 ragged tokens of 16 heads of 64 x 96 (768) 84 and 93. fp32: two; with keys of
+// 256, whose rows leave LDS for one, one.
 constexpr int nv32(int kb) { return kb > 4 ? 1 : 2; }
+int value_blocks(const DeltaArgs& a) {
+  if (!a.bf16) return nv32((a.dk + 31) / 32);
+  const long units = (long)(a.S > 0 ? a.S : a.batch) * a.H * ((a.dv + 15) / 16);
+  return units > (a.S > 0 ? 3 * 256 : 256) && a.dk <= 128 ? 2 : 1;
+}
 
 template <int KB, int WHAT>
 void walk(const DeltaArgs& a, long blocks, hipStream_t stream) {
   const dim3 grid((unsigned)blocks);
-  if (a.bf16) hipLaunchKernelGGL((delta_fwd_kernel<64, KB, kNv64, 1, WHAT>), grid, dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL((delta_fwd_kernel<32, KB, nv32(KB), 3, WHAT>), grid, dim3(kThreads), 0, stream, a);
+  constexpr int kWideNv = KB <= 4 ? 2 : 1;
+  if (!a.bf16) hipLaunchKernelGGL((delta_fwd_kernel<32, KB, nv32(KB), 3, WHAT>), grid, dim3(kThreads), 0, stream, a);
+  else if (value_blocks(a) == 1) hipLaunchKernelGGL((delta_fwd_kernel<64, KB, 1, 1, WHAT>), grid, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((delta_fwd_kernel<64, KB, kWideNv, 1, WHAT>), grid, dim3(kThreads), 0, stream, a);
+}
+template <int KB, bool REV>
+void join(const DeltaArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((long)(a.S > 0 ? a.S : a.batch) * a.H * ((a.dv + 15) / 16)));
+  hipLaunchKernelGGL((delta_join_kernel<KB, REV>), grid, dim3(128 * KB), 0, stream, a, delta_chunk(a.bf16));
 }
 template <int KB>
 void fwd(const DeltaArgs& a, bool keep, hipStream_t stream) {
   if (a.seg) {
     walk<KB, kOwn>(a, delta_segment_blocks(a), stream);
-    const dim3 grid((unsigned)((long)(a.S > 0 ? a.S : a.batch) * a.H * ((a.dv + 15) / 16)));
-    hipLaunchKernelGGL(delta_join_kernel<KB>, grid, dim3(128 * KB), 0, stream, a, delta_chunk(a.bf16));
+    join<KB, false>(a, stream);
   }
   if (keep) walk<KB, kKeep>(a, delta_chain_blocks(a), stream);
   else walk<KB, kOutputs>(a, delta_chain_blocks(a), stream);
 }
-template <int KB>
-void rev(const DeltaArgs& a, hipStream_t stream) {
+template <int KB, bool OWN>
+void walk_back(const DeltaArgs& a, hipStream_t stream) {
   const dim3 grid((unsigned)delta_chain_blocks(a));
-  if (a.bf16) hipLaunchKernelGGL((delta_rev_kernel<64, KB, kNv64, 1>), grid, dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL((delta_rev_kernel<32, KB, nv32(KB), 3>), grid, dim3(kThreads), 0, stream, a);
+  constexpr int kWideNv = KB <= 4 ? 2 : 1;
+  if (!a.bf16) hipLaunchKernelGGL((delta_rev_kernel<32, KB, nv32(KB), 3, OWN>), grid, dim3(kThreads), 0, stream, a);
+  else if (value_blocks(a) == 1) hipLaunchKernelGGL((delta_rev_kernel<64, KB, 1, 1, OWN>), grid, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((delta_rev_kernel<64, KB, kWideNv, 1, OWN>), grid, dim3(kThreads), 0, stream, a);
+}
+template <int KB>
+void rev(const DeltaArgs& a, hipStream_t stream) {   // the maps are those of the forward walk
+  if (a.seg) {
+    walk_back<KB, true>(a, stream);
+    join<KB, true>(a, stream);
+  }
+  walk_back<KB, false>(a, stream);
 }
 
 }  // namespace
 
-static int tile_columns(int dk, bool bf16) { return 16 * (bf16 ? kNv64 : nv32((dk + 31) / 32)); }
-static int tiles_of(int d, int dk, bool bf16) { return (d + tile_columns(dk, bf16) - 1) / tile_columns(dk, bf16); }
+static int tiles_of(int d, int blocks) { return (d + 16 * blocks - 1) / (16 * blocks); }
 long delta_chain_blocks(const DeltaArgs& a) {
-  return (a.seg ? a.segs : (long)(a.S > 0 ? a.S : a.batch)) * a.H * tiles_of(a.dv, a.dk, a.bf16);
+  return (a.seg ? a.segs : (long)(a.S > 0 ? a.S : a.batch)) * a.H * tiles_of(a.dv, value_blocks(a));
 }
 long delta_segment_blocks(const DeltaArgs& a) {
-  return a.segs * a.H * (tiles_of(a.dv, a.dk, a.bf16) + tiles_of(a.dk, a.dk, a.bf16));
+  return a.segs * a.H * (tiles_of(a.dv, value_blocks(a)) + tiles_of(a.dk, value_blocks(a)));
 }
 
 // A walk of few heads leaves most of the card idle for as long as its longest sequence is. Cut into segments, every
 // segment's own last state (from a state of zero) and its map of a state are made at once, the states behind the
 // segments follow from these one after the other, and all segments are walked at once: twice to three times the
-// work, in chains of a segment's length (8192 tokens, 4 heads of 128 x 128: 220 us whole, 90 in eight segments). The
+// work, in chains of a segment's length (8192 tokens, 4 heads of 128 x 128: 220 us whole, 91 in eight segments). The
+// backward walk is cut alike, its maps the forward's transposed (both with the gradients 462 us whole, 240 cut; 8 heads
+// of 4096 tokens 272 and 218; fp32, 2048 tokens of 4 heads of 64 x 128, 249 and 114). The
 // number of segments is the one of least cost, counted in steps of a chunk: a walk takes as long as its longest chain,
 // or as its steps shared out over 256 CUs, one at a time (workgroups on one CU do not overlap by more than a tenth);
 // a step without O 0.8 of one with it; a segment's join about one step, the two launches five. The host does not
 // know the lengths of packed sequences: the longest is taken to be three times the mean. (Eight ragged sequences of
-// 5087 tokens, 16 heads: 99 us whole, 110 in segments of nine chunks.)
+// 5087 tokens, 16 heads of 64 x 96: 99 us whole, 110 in segments of nine chunks.)
 int delta_segment(int batch, int T, int S, int H, int dk, int dv, bool bf16) {
   const int C = delta_chunk(bf16);
   const long seqs = S > 0 ? S : batch, tokens = (long)batch * T;
   const long longest = S > 0 ? std::min((long)T, 3 * ((tokens + S - 1) / S)) : T;
   const long chunks = (longest + C - 1) / C, all = (tokens + C - 1) / C;
-  const int values = tiles_of(dv, dk, bf16), rows = values + tiles_of(dk, dk, bf16);
+  const int blocks = bf16 ? 1 : nv32((dk + 31) / 32), values = tiles_of(dv, blocks), rows = values + tiles_of(dk, blocks);
   auto steps = [](double chain, double work) { return std::max(chain, work / 256); };
   const double outputs = (double)all * H * values;
   double least = 0.9 * steps((double)chunks, outputs);
