@@ -12,12 +12,11 @@
 //     dg_t = <dS1, S1> + sum_{i >= t} E_i   (tokens of the chunk),
 //     <dS1, S1> = e^(G_C) <dS1, S0> + sum_j e^(G_C - G_j) k_j . (U dS1)_j.
 //
-// A workgroup takes one chunk of one head, two waves 16 tokens, each half of the key
-// columns. First, over the value columns 32 at a time, the products with the states
-// (contraction over the columns, the states' terms in LDS) and, one of the two waves
-// each, Z1 and Z2 of the tokens, both as rows and as columns; then the products of
-// the masked Z, which go round through LDS, with Q and K, whose rows take the
-// states' place there.
+// A workgroup takes one chunk of one head, two waves 16 tokens: one makes what belongs to their reads (dq and r, from
+// S0, U', dO and the Z of the tokens as rows i), the other what belongs to their writes (w, from dS1, U and the Z of
+// the tokens as columns j). First, over the value columns 32 at a time, the products with the states (contraction over
+// the columns, the states' terms in LDS) and the Z; then the products of the masked Z, which stay in registers, with Q
+// and K, whose rows take the states' place in LDS.
 #include "ssd_delta_tile.h"
 
 namespace ssd {
@@ -29,20 +28,20 @@ constexpr int kPitchT = lds_pitch(32);   // rows of 32 value columns, in the ord
 
 template <int C, int KB, int NX>
 __global__ __launch_bounds__(threads_of(C), C == 64 ? 2 : 1) void delta_grads_kernel(DeltaArgs a) {
-  constexpr int kEsz = NX == 1 ? 2 : 4, kTb = C / 16, kKp = C / 32, kHalves = 2, kB = KB, kThreads = threads_of(C);
+  constexpr int kEsz = NX == 1 ? 2 : 4, kTb = C / 16, kKp = C / 32, kB = 2 * KB, kThreads = threads_of(C);
   constexpr int kPitchK = lds_pitch(32 * KB);
-  // [S0, dS1][term][32 value columns] and U, U', dO [term][C]; then K, Q [term][C] and, of every wave, three operands.
+  // [S0, dS1][term][32 value columns] and U, U', dO [term][C]; then K, Q [term][C] and beta r in fp32.
   constexpr int kStates = 2 * kTerms * 32 * kPitchK, kTokens = (2 * kTerms + NX) * C * kPitchT;
-  constexpr int kRows = 2 * NX * C * kPitchK, kWave = 3 * kTerms * kOperand, kMasked = kThreads / 64 * kWave;
-  constexpr int kSize = kStates + kTokens > kRows + kMasked ? kStates + kTokens : kRows + kMasked;
+  constexpr int kRows = 2 * NX * C * kPitchK, kReads = kTb * kB * 64 * 8;
+  constexpr int kSize = kStates + kTokens > kRows + kReads ? kStates + kTokens : kRows + kReads;
   __shared__ __align__(16) uint16_t Sl[kSize];
-  __shared__ __align__(16) float Gh[C], Gl[C], Be[C], Ev[C], Sw[C], Kr[C], dots[kThreads / 64];
-  uint16_t* const Tl = Sl + kStates;
-  uint16_t* const Ut = Tl;
-  uint16_t* const Vt = Tl + kTerms * C * kPitchT;       // U'
-  uint16_t* const Ot = Tl + 2 * kTerms * C * kPitchT;   // dO
+  __shared__ __align__(16) float Gh[C], Gl[C], Be[C], Ev[C], Sw[C], dots[kThreads / 64];
+  uint16_t* const Ut = Sl + kStates;
+  uint16_t* const Vt = Ut + kTerms * C * kPitchT;       // U'
+  uint16_t* const Ot = Ut + 2 * kTerms * C * kPitchT;   // dO
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
-  const int tb = wave % kTb, half = wave / kTb, tok = 16 * tb + c16;
+  const int tb = wave % kTb, tok = 16 * tb + c16;
+  const bool reads = wave < kTb;   // else the writes
   const long unit = xcd_unit(blockIdx.x, gridDim.x);
   const int h = (int)(unit % a.H);
   const long slot = unit / a.H;
@@ -55,28 +54,25 @@ __global__ __launch_bounds__(threads_of(C), C == 64 ? 2 : 1) void delta_grads_ke
     Gh[threadIdx.x] = gates[3 * C + threadIdx.x];
     Gl[threadIdx.x] = gates[4 * C + threadIdx.x];
     Be[threadIdx.x] = gates[2 * C + threadIdx.x];
-    Ev[threadIdx.x] = Sw[threadIdx.x] = Kr[threadIdx.x] = 0.f;
   }
   const float eg = gates[tok], wt = gates[C + tok], keep = gates[5 * C];
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
-  const float* S0 = a.states + sh * mat;
-  const float* S1 = a.dstates + sh * mat;
-  const rsrc_t ru = make_rsrc(a.u + sh * C * a.dv, (uint32_t)(C * a.dv * 4));
-  const rsrc_t rb = make_rsrc(a.ub + sh * C * a.dv, (uint32_t)(C * a.dv * 4));
+  const rsrc_t rs0 = make_rsrc(a.states + sh * mat, (uint32_t)(mat * 4)), rs1 = make_rsrc(a.dstates + sh * mat, (uint32_t)(mat * 4));
+  const rsrc_t ru = make_rsrc((reads ? a.ub : a.u) + sh * C * a.dv, (uint32_t)(C * a.dv * 4));
   const rsrc_t ro = chunk_rows(a.d_o, ch.row0, (long)a.H * a.dv, (long)h * a.dv, n, kEsz);
   const rsrc_t rv = chunk_rows(a.v, ch.row0, a.v_row, (long)h * a.dv, n, kEsz);
   constexpr int kPieces = (256 * KB + kThreads - 1) / kThreads;
   f32x4 s0[kPieces], s1[kPieces];   // this thread's pieces of four of the states' rows
-  Raw8<3> xu, xb;
+  Raw8<3> xu;                       // of U' or U
   Raw8<NX> xo, xv;
   auto load = [&](int kv) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int at = threadIdx.x + kThreads * i, dv = 32 * kv + at / (8 * KB), dk = 4 * (at % (8 * KB));
-      const bool in = at < 256 * KB && dv < a.dv && dk < a.dk;
-      s0[i] = in ? *reinterpret_cast<const f32x4*>(S0 + (long)dv * a.dk + dk) : zero;
-      s1[i] = in ? *reinterpret_cast<const f32x4*>(S1 + (long)dv * a.dk + dk) : zero;
+      const uint32_t off = at < 256 * KB && dv < a.dv && dk < a.dk ? (uint32_t)((dv * a.dk + dk) * 4) : kOffNone;
+      s0[i] = __builtin_bit_cast(f32x4, buf_load16(rs0, off));
+      s1[i] = __builtin_bit_cast(f32x4, buf_load16(rs1, off));
     }
     const int lo = 32 * kv + 4 * g, hi = lo + 16;
     auto pair = [&](bool row, int pitch, int esz, uint32_t& x, uint32_t& y) {
@@ -86,35 +82,30 @@ __global__ __launch_bounds__(threads_of(C), C == 64 ? 2 : 1) void delta_grads_ke
     uint32_t x, y;
     pair(true, a.dv * 4, 4, x, y);
     xu = load_pair<3>(ru, x, y);
-    xb = load_pair<3>(rb, x, y);
-    pair(tok < n, a.H * a.dv * kEsz, kEsz, x, y);
+    pair(reads && tok < n, a.H * a.dv * kEsz, kEsz, x, y);
     xo = load_pair<NX>(ro, x, y);
-    pair(tok < n, (int)a.v_row * kEsz, kEsz, x, y);
+    pair(reads && tok < n, (int)a.v_row * kEsz, kEsz, x, y);
     xv = load_pair<NX>(rv, x, y);
   };
 
-  // Lane: token tok, key columns 16 (half kB + b) + 4 g + r.
-  f32x4 dQ[kB], R[kB], W[kB];
+  // Lane: token tok, key columns 16 b + 4 g + r. P: r or w. Z of the tokens 16 blk + 4 g + r, before tok and in its
+  // block (reads) or behind it and in its block (writes); zeros of the other blocks.
+  f32x4 dQ[kB], P[kB], Z1[kTb], Z2[kTb];
 #pragma unroll
-  for (int b = 0; b < kB; ++b) dQ[b] = R[b] = W[b] = zero;
-  // Products with the tokens 16 blk + 4 g + r: entry e <= tb has blk = e and tok as the row (i), the others
-  // blk = e - 1 and tok as the column (j).
-  // The first of the tokens' two waves makes Z1, the second Z2.
-  f32x4 Z[kTb + 1];
+  for (int b = 0; b < kB; ++b) dQ[b] = P[b] = zero;
 #pragma unroll
-  for (int e = 0; e <= kTb; ++e) Z[e] = zero;
+  for (int e = 0; e < kTb; ++e) Z1[e] = Z2[e] = zero;
   float uv = 0.f, dot = 0.f;
 
   const int steps = (a.dv + 31) / 32;
   load(0);
+  loads_done();
   for (int kv = 0; kv < steps; ++kv) {
-    u32x4 ut[kTerms], vt[kTerms], ot[NX];
+    u32x4 own[kTerms], ot[NX];
     {
       float x[8], y[8];
       floats8(xu, x);
-      split8<kTerms>(x, ut);
-      floats8(xb, x);
-      split8<kTerms>(x, vt);
+      split8<kTerms>(x, own);
       floats8(xv, y);
 #pragma unroll
       for (int i = 0; i < 8; ++i) uv = fmaf(x[i], y[i], uv);
@@ -123,10 +114,10 @@ __global__ __launch_bounds__(threads_of(C), C == 64 ? 2 : 1) void delta_grads_ke
     {
       const int at = tok * kPitchT + 8 * g;
 #pragma unroll
-      for (int t = 0; t < kTerms; ++t) *reinterpret_cast<u32x4*>((half ? Vt : Ut) + t * C * kPitchT + at) = half ? vt[t] : ut[t];
+      for (int t = 0; t < kTerms; ++t) *reinterpret_cast<u32x4*>((reads ? Vt : Ut) + t * C * kPitchT + at) = own[t];
 #pragma unroll
       for (int t = 0; t < NX; ++t)
-        if (half == 0) *reinterpret_cast<u32x4*>(Ot + t * C * kPitchT + at) = ot[t];
+        if (reads) *reinterpret_cast<u32x4*>(Ot + t * C * kPitchT + at) = ot[t];
     }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
@@ -143,55 +134,43 @@ __global__ __launch_bounds__(threads_of(C), C == 64 ? 2 : 1) void delta_grads_ke
         *reinterpret_cast<u32x2*>(Sl + ((kTerms + t) * 32 + row) * kPitchK + col) = p1[t];
       }
     }
-    if (kv + 1 < steps) load(kv + 1);
+    load(min(kv + 1, steps - 1));
     __syncthreads();
+    const uint16_t* const states = Sl + (reads ? 0 : kTerms * 32 * kPitchK);
 #pragma unroll
     for (int b = 0; b < kB; ++b) {
-      const int col = 16 * (half * kB + b);
-      u32x4 st[kTerms], dt[kTerms];
+      u32x4 st[kTerms];
 #pragma unroll
-      for (int t = 0; t < kTerms; ++t) {
-        st[t] = frag_k_rows_accpair(Sl + t * 32 * kPitchK, kPitchK, 0, col, lane);
-        dt[t] = frag_k_rows_accpair(Sl + (kTerms + t) * 32 * kPitchK, kPitchK, 0, col, lane);
-      }
-      dQ[b] = mma<kTerms, NX, kTerms>(st, ot, dQ[b]);
-      R[b] = mma<kTerms, kTerms, kTerms>(st, vt, R[b]);
-      W[b] = mma<kTerms, kTerms, kTerms>(dt, ut, W[b]);
+      for (int t = 0; t < kTerms; ++t) st[t] = frag_k_rows_accpair(states + t * 32 * kPitchK, kPitchK, 0, 16 * b, lane);
+      P[b] = mma<kTerms, kTerms, kTerms>(st, own, P[b]);
+      if (reads) dQ[b] = mma<kTerms, NX, kTerms>(st, ot, dQ[b]);
     }
 #pragma unroll
-    for (int e = 0; e <= kTb; ++e) {
-      const bool row = e <= tb;
-      const int at = 16 * (row ? e : e - 1);
-      u32x4 x[kTerms];
-      if (half == 0) {
-        if (row) {
+    for (int e = 0; e < kTb; ++e) {
+      if (reads ? e > tb : e < tb) continue;
+      u32x4 x[kTerms], y[NX];
 #pragma unroll
-          for (int t = 0; t < kTerms; ++t) x[t] = frag_k_cols(Ut + t * C * kPitchT, kPitchT, at, 0, lane);
-          Z[e] = mma<kTerms, NX, kTerms>(x, ot, Z[e]);
-        } else {
-#pragma unroll
-          for (int t = 0; t < NX; ++t) x[t] = frag_k_cols(Ot + t * C * kPitchT, kPitchT, at, 0, lane);
-          Z[e] = mma<NX, kTerms, kTerms>(x, ut, Z[e]);
-        }
+      for (int t = 0; t < kTerms; ++t) x[t] = frag_k_cols((reads ? Ut : Vt) + t * C * kPitchT, kPitchT, 16 * e, 0, lane);
+      Z2[e] = mma<kTerms, kTerms, kTerms>(x, own, Z2[e]);
+      if (reads) {
+        Z1[e] = mma<kTerms, NX, kTerms>(x, ot, Z1[e]);
       } else {
-        const uint16_t* from = row ? Ut : Vt;
 #pragma unroll
-        for (int t = 0; t < kTerms; ++t) x[t] = frag_k_cols(from + t * C * kPitchT, kPitchT, at, 0, lane);
-        if (row) Z[e] = mma<kTerms, kTerms, kTerms>(x, vt, Z[e]);
-        else Z[e] = mma<kTerms, kTerms, kTerms>(x, ut, Z[e]);
+        for (int t = 0; t < NX; ++t) y[t] = frag_k_cols(Ot + t * C * kPitchT, kPitchT, 16 * e, 0, lane);
+        Z1[e] = mma<NX, kTerms, kTerms>(y, own, Z1[e]);
       }
     }
     __syncthreads();
   }
 
-  // Rows of K and Q where the states were.
+  // Rows of K and Q where the states were: the reads' waves stage K, the others Q.
   uint16_t* const Kl = Sl;
   uint16_t* const Ql = Sl + NX * C * kPitchK;
+  f32x4* const Rl = reinterpret_cast<f32x4*>(Sl + kRows) + tb * kB * 64 + lane;   // beta r, as the lanes hold it
   {
-    // The tokens' first wave stages K, the second Q.
-    const int xrow = (int)(half ? a.q_row : a.k_row) * kEsz;
-    const rsrc_t rx = chunk_rows(half ? a.q : a.k, ch.row0, half ? a.q_row : a.k_row, (long)hk * a.dk, n, kEsz);
-    uint16_t* const to = half ? Ql : Kl;
+    const int xrow = (int)(reads ? a.k_row : a.q_row) * kEsz;
+    const rsrc_t rx = chunk_rows(reads ? a.k : a.q, ch.row0, reads ? a.k_row : a.q_row, (long)hk * a.dk, n, kEsz);
+    uint16_t* const to = reads ? Kl : Ql;
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
       const int col = 32 * b + 8 * g;
@@ -201,154 +180,134 @@ __global__ __launch_bounds__(threads_of(C), C == 64 ? 2 : 1) void delta_grads_ke
       for (int t = 0; t < NX; ++t) *reinterpret_cast<u32x4*>(to + (t * C + tok) * kPitchK + col) = x[t];
     }
   }
-  // Weights of the pairs; masked ones are 0 whatever their product was. As operands, of every wave: row blocks kp up
-  // to tb / 2 at kp, columns from tb / 2 on at kp + 1.
-  uint16_t* const Ml = Sl + kRows;
+  // Weights of the pairs; masked ones are 0 whatever their product was.
+  u32x4 z1[kKp][kTerms], z2[kKp][kTerms];
   {
     const float hi = Gh[tok], lo = Gl[tok];
 #pragma unroll
-    for (int e = 0; e <= kTb; ++e) {
-      const bool row = e <= tb;
-      const int o = 16 * (row ? e : e - 1) + 4 * g;
-      const f32x4 ho = *reinterpret_cast<const f32x4*>(Gh + o), lo4 = *reinterpret_cast<const f32x4*>(Gl + o);
+    for (int e = 0; e < kTb; ++e) {
+      const int o = 16 * e + 4 * g;
+      const f32x4 ho = *reinterpret_cast<const f32x4*>(Gh + o), lo4 = *reinterpret_cast<const f32x4*>(Gl + o),
+                  beo = *reinterpret_cast<const f32x4*>(Be + o);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = row ? tok : o + r, j = row ? o + r : tok;
+        const int i = reads ? tok : o + r, j = reads ? o + r : tok;
         const float dh = hi - ho[r], dl = lo - lo4[r];
-        const float d = i >= j ? exp_of(row ? dh + dl : -dh - dl) : 0.f;
-        const float w = half ? -d * (row ? 1.f : Be[o + r]) : d * (row ? 1.f : a.scale);
-        Z[e][r] = i > j || (i == j && half == 0) ? Z[e][r] * w : 0.f;
+        const float d = exp_of(reads ? dh + dl : -dh - dl);
+        Z1[e][r] = i >= j ? Z1[e][r] * (d * (reads ? 1.f : a.scale)) : 0.f;
+        Z2[e][r] = i > j ? Z2[e][r] * (d * (reads ? -1.f : -beo[r])) : 0.f;
       }
     }
-    uint16_t* const to = Ml + wave * kWave + lane * 8;
 #pragma unroll
     for (int m = 0; m < kKp; ++m) {
       float x[8], y[8];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int b = 2 * m + t;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          x[4 * t + r] = b <= tb ? Z[b][r] : 0.f;
-          y[4 * t + r] = b >= tb ? Z[b + 1][r] : 0.f;
-        }
+      for (int t = 0; t < 8; ++t) {
+        x[t] = Z1[2 * m + t / 4][t % 4];
+        y[t] = Z2[2 * m + t / 4][t % 4];
       }
-      u32x4 part[kTerms];
-      if (m <= tb / 2) {
-        split8<kTerms>(x, part);
-#pragma unroll
-        for (int t = 0; t < kTerms; ++t) *reinterpret_cast<u32x4*>(to + (m * kTerms + t) * kOperand) = part[t];
-      }
-      if (m >= tb / 2) {
-        split8<kTerms>(y, part);
-#pragma unroll
-        for (int t = 0; t < kTerms; ++t) *reinterpret_cast<u32x4*>(to + ((m + 1) * kTerms + t) * kOperand) = part[t];
-      }
+      split8<kTerms>(x, z1[m]);
+      split8<kTerms>(y, z2[m]);
     }
   }
   __syncthreads();
-  const uint16_t *const z1 = Ml + tb * kWave + lane * 8, *const z2 = Ml + (tb + kTb) * kWave + lane * 8;
   const float be = Be[tok];
   const bool shared = a.part_q != nullptr;
   const long heads = shared ? a.H : a.Hk, hout = shared ? h : hk;
-  const rsrc_t wq = chunk_rows(shared ? (void*)a.part_q : a.dq, ch.row0, heads * a.dk, hout * a.dk, n, shared ? 4 : kEsz);
-  const rsrc_t wk = chunk_rows(shared ? (void*)a.part_k : a.dk_out, ch.row0, heads * a.dk, hout * a.dk, n, shared ? 4 : kEsz);
-  float e_q = 0.f, e_r = 0.f, e_w = 0.f, e_s = 0.f;
+  auto out = [&](float* part, void* whole) {
+    return chunk_rows(shared ? (void*)part : whole, ch.row0, heads * a.dk, hout * a.dk, n, shared ? 4 : kEsz);
+  };
+  auto store = [&](f32x4 x, rsrc_t to, int b) {
+    const int dk = 16 * b + 4 * g;
+    const bool in = tok < n && dk < a.dk;
+    if (shared) store4<3>(x, to, in ? (uint32_t)((tok * (int)heads * a.dk + dk) * 4) : kOffNone);
+    else store4<NX>(x, to, in ? (uint32_t)((tok * (int)heads * a.dk + dk) * kEsz) : kOffNone);
+  };
   auto row_of = [&](const uint16_t* L, int b) {   // this lane's four of the token's row
     f32x4 x = zero;
 #pragma unroll
-    for (int t = NX - 1; t >= 0; --t) x += four(*reinterpret_cast<const u32x2*>(L + (t * C + tok) * kPitchK + 16 * (half * kB + b) + 4 * g));
+    for (int t = NX - 1; t >= 0; --t) x += four(*reinterpret_cast<const u32x2*>(L + (t * C + tok) * kPitchK + 16 * b + 4 * g));
     return x;
   };
+  auto operand = [&](const uint16_t* L, int m, int b, u32x4* x) {
 #pragma unroll
-  for (int b = 0; b < kB; ++b) {
-    const f32x4 kv = row_of(Kl, b);
-    dQ[b] *= eg;
-    R[b] *= -eg;
-    W[b] *= wt;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) e_s = fmaf(kv[r], W[b][r], e_s);
-  }
-  auto masked = [&](const uint16_t* z, int at, u32x4* out) {
-#pragma unroll
-    for (int t = 0; t < kTerms; ++t) out[t] = *reinterpret_cast<const u32x4*>(z + (at * kTerms + t) * kOperand);
+    for (int t = 0; t < NX; ++t) x[t] = frag_k_rows_accpair(L + t * C * kPitchK, kPitchK, 32 * m, 16 * b, lane);
   };
-#pragma unroll
-  for (int m = 0; m < kKp; ++m) {
-    u32x4 x[kTerms], y[kTerms];
-    if (m <= tb / 2) {
-      masked(z1, m, x);
-      masked(z2, m, y);
-#pragma unroll
-      for (int b = 0; b < kB; ++b) {
-        u32x4 kt[NX];
-#pragma unroll
-        for (int t = 0; t < NX; ++t) kt[t] = frag_k_rows_accpair(Kl + t * C * kPitchK, kPitchK, 32 * m, 16 * (half * kB + b), lane);
-        dQ[b] = mma<NX, kTerms, kTerms>(kt, x, dQ[b]);
-        R[b] = mma<NX, kTerms, kTerms>(kt, y, R[b]);
-      }
-    }
-    if (m >= tb / 2) {
-      masked(z1, m + 1, x);
-      masked(z2, m + 1, y);
-#pragma unroll
-      for (int b = 0; b < kB; ++b) {
-        u32x4 kt[NX], qt[NX];
-#pragma unroll
-        for (int t = 0; t < NX; ++t) {
-          kt[t] = frag_k_rows_accpair(Kl + t * C * kPitchK, kPitchK, 32 * m, 16 * (half * kB + b), lane);
-          qt[t] = frag_k_rows_accpair(Ql + t * C * kPitchK, kPitchK, 32 * m, 16 * (half * kB + b), lane);
-        }
-        W[b] = mma<NX, kTerms, kTerms>(qt, x, W[b]);
-        W[b] = mma<NX, kTerms, kTerms>(kt, y, W[b]);
-      }
-    }
-  }
-#pragma unroll
-  for (int b = 0; b < kB; ++b) {
-    const int dk = 16 * (half * kB + b) + 4 * g;
-    const f32x4 kv = row_of(Kl, b), qv = row_of(Ql, b);
-    dQ[b] *= a.scale;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      e_q = fmaf(qv[r], dQ[b][r], e_q);
-      e_r = fmaf(kv[r], R[b][r], e_r);
-      e_w = fmaf(kv[r], W[b][r], e_w);
-    }
-    const f32x4 dk4 = R[b] * be + W[b];
-    const bool in = tok < n && dk < a.dk;
-    if (shared) {
-      const uint32_t off = in ? (uint32_t)((tok * (int)heads * a.dk + dk) * 4) : kOffNone;
-      store4<3>(dQ[b], wq, off);
-      store4<3>(dk4, wk, off);
-    } else {
-      const uint32_t off = in ? (uint32_t)((tok * (int)heads * a.dk + dk) * kEsz) : kOffNone;
-      store4<NX>(dQ[b], wq, off);
-      store4<NX>(dk4, wk, off);
-    }
-  }
   auto over_g = [](float x) {
     x += __shfl_xor(x, 16);
     return x + __shfl_xor(x, 32);
   };
-  e_q = over_g(e_q);
-  e_r = over_g(e_r);
-  e_w = over_g(e_w);
-  e_s = over_g(e_s);
-  uv = over_g(uv);
+  float e_r = 0.f;
+  if (reads) {
+    float e_q = 0.f;
+    const rsrc_t wq = out(a.part_q, a.dq);
+#pragma unroll
+    for (int b = 0; b < kB; ++b) {
+      dQ[b] *= eg;
+      P[b] *= -eg;
+#pragma unroll
+      for (int m = 0; m < kKp; ++m) {
+        if (m > tb / 2) continue;
+        u32x4 kt[NX];
+        operand(Kl, m, b, kt);
+        dQ[b] = mma<NX, kTerms, kTerms>(kt, z1[m], dQ[b]);
+        P[b] = mma<NX, kTerms, kTerms>(kt, z2[m], P[b]);
+      }
+      dQ[b] *= a.scale;
+      const f32x4 kv = row_of(Kl, b), qv = row_of(Ql, b);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        e_q = fmaf(qv[r], dQ[b][r], e_q);
+        e_r = fmaf(kv[r], P[b][r], e_r);
+      }
+      Rl[b * 64] = P[b] * be;
+      store(dQ[b], wq, b);
+    }
+    e_r = over_g(e_r);
+    e_q = over_g(e_q);
+    if (g == 0) Ev[tok] = e_q + be * e_r;
+    uv = over_g(uv);
+    if (g == 0 && tok < n) a.dbeta[(ch.row0 + tok) * a.H + h] = uv + e_r;
+  } else {
+    float e_s = 0.f;
+#pragma unroll
+    for (int b = 0; b < kB; ++b) {
+      P[b] *= wt;
+      const f32x4 kv = row_of(Kl, b);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) e_s = fmaf(kv[r], P[b][r], e_s);
+#pragma unroll
+      for (int m = 0; m < kKp; ++m) {
+        if (m < tb / 2) continue;
+        u32x4 kt[NX], qt[NX];
+        operand(Kl, m, b, kt);
+        operand(Ql, m, b, qt);
+        P[b] = mma<NX, kTerms, kTerms>(qt, z1[m], P[b]);
+        P[b] = mma<NX, kTerms, kTerms>(kt, z2[m], P[b]);
+      }
+    }
+    e_s = over_g(e_s);
+    if (g == 0) Sw[tok] = e_s;
+  }
   dot = lanes_sum<64>(dot, 64);
   if (lane == 0) dots[wave] = dot;
+  __syncthreads();
+  if (!reads) {
+    float e_w = 0.f;
+    const rsrc_t wk = out(a.part_k, a.dk_out);
 #pragma unroll
-  for (int s = 0; s < kHalves; ++s) {   // one half of the key columns after the other
-    if (half == s && g == 0) {
-      Ev[tok] += e_q + be * e_r - e_w;
-      Sw[tok] += e_s;
-      Kr[tok] += e_r;
+    for (int b = 0; b < kB; ++b) {
+      const f32x4 kv = row_of(Kl, b);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) e_w = fmaf(kv[r], P[b][r], e_w);
+      store(Rl[b * 64] + P[b], wk, b);
     }
-    __syncthreads();
+    e_w = over_g(e_w);
+    if (g == 0) Ev[tok] -= e_w;
   }
-  if (half == 0 && g == 0 && tok < n) a.dbeta[(ch.row0 + tok) * a.H + h] = uv + Kr[tok];
-  if (wave == 0 && a.dg) {
+  if (!a.dg) return;
+  __syncthreads();
+  if (wave == 0) {
     const double ev = lane < C ? (double)Ev[lane] : 0.0;
     double up = ev, all = ev, sw = lane < C ? (double)Sw[lane] : 0.0;
 #pragma unroll
