@@ -56,7 +56,9 @@ struct DeltaArgs {
   float *dg = nullptr, *dbeta = nullptr;                      // [tokens][H]; dg may be null
   float *states = nullptr, *dstates = nullptr;   // [slots][H][dv][dk]: S0 and dS1 of every chunk
   float *u = nullptr, *ub = nullptr;             // [slots][H][C][dv]: U and U'
-  float *part_q = nullptr, *part_k = nullptr;    // [tokens][H][dk]: gradients of a value head, where heads share q and k
+  int grad_heads = 1;            // value heads that a workgroup of the gradients takes
+  float *part_q = nullptr, *part_k = nullptr;   // where heads share q and k: [tokens][H][dk], or with all of them in a
+                                                // workgroup [tokens][Hk][dk]
 };
 
 // Tokens a chunk.
@@ -74,6 +76,7 @@ int delta_prep_threads();
 long delta_chain_blocks(const DeltaArgs& a);
 long delta_segment_blocks(const DeltaArgs& a);   // of the segments' own states and maps
 int delta_chain_threads();
+int delta_grad_heads(long slots, int H, int Hk, int dk);
 long delta_bwd_blocks(const DeltaArgs& a);
 int delta_bwd_threads();
 

@@ -18,6 +18,7 @@ namespace {
 
 struct DeltaDims {
   int64_t q_row, k_row, v_row, tokens, nseq, spr, slots, segs_per_row, segs;
+  int grad_heads;
   int esz, seg;
 };
 
@@ -47,6 +48,7 @@ ssd::DeltaArgs delta_args(const ssd_delta_shape* s, const DeltaDims& d) {
   a.slots_per_row = (long)d.spr;
   a.slots = (long)d.slots;
   a.seg = d.seg;
+  a.grad_heads = d.grad_heads;
   a.segs_per_row = (long)d.segs_per_row;
   a.segs = (long)d.segs;
   return a;
@@ -76,6 +78,7 @@ ssd_status check_delta(const ssd_delta_shape* s, DeltaDims* d, bool backward) {
   const int C = ssd::delta_chunk(s->dtype == SSD_DTYPE_BF16);
   d->spr = ssd::lin_slots_per_row(s->seqlen, s->num_seqs, C);
   d->slots = s->num_seqs > 0 ? d->spr : d->spr * s->batch;
+  d->grad_heads = ssd::delta_grad_heads(d->slots, s->nheads, s->nqk_heads, s->dk);
   d->seg = ssd::delta_segment(s->batch, s->seqlen, s->num_seqs, s->nheads, s->dk, s->dv, s->dtype == SSD_DTYPE_BF16);
   d->segs_per_row = d->seg ? ssd::lin_slots_per_row(s->seqlen, s->num_seqs, d->seg * C) : 0;
   d->segs = s->num_seqs > 0 ? d->segs_per_row : d->segs_per_row * s->batch;
@@ -97,7 +100,7 @@ DeltaLayout delta_layout(const ssd_delta_shape* s, const DeltaDims& d, bool back
   DeltaLayout L{};
   const bool bf16 = s->dtype == SSD_DTYPE_BF16, shared = s->nheads != s->nqk_heads;
   const size_t units = (size_t)d.slots * s->nheads, mat = (size_t)s->dk * s->dv * 4;
-  const size_t rows = (size_t)ssd::delta_chunk(bf16) * s->dv * 4, part = (size_t)d.tokens * s->nheads * s->dk * 4;
+  const size_t rows = (size_t)ssd::delta_chunk(bf16) * s->dv * 4, part = (size_t)d.tokens * (d.grad_heads > 1 ? s->nqk_heads : s->nheads) * s->dk * 4;
   size_t off = 0;
   auto take = [&](size_t b) {
     const size_t o = off;
@@ -281,7 +284,7 @@ ssd_status ssd_gated_delta_bwd(const void* q, const void* k, const void* v, cons
   if (e == hipSuccess) e = ssd::launch_delta_fwd(a, true, s);
   if (e == hipSuccess) e = ssd::launch_delta_rev(a, s);
   if (e == hipSuccess) e = ssd::launch_delta_grads(a, s);
-  if (e == hipSuccess && shared) {
+  if (e == hipSuccess && shared && d.grad_heads == 1) {
     ssd::LinShareSum p;
     p.in_k = a.part_q;
     p.in_v = a.part_k;

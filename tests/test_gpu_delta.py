@@ -115,6 +115,15 @@ def test_backward(shape, dtype):
     check_bwd(make(*shape, dtype, seed=100 + shape[1]), name=str(shape))
 
 
+# Chunks and key heads enough that one workgroup takes the gradients of all value heads of a key head.
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", [(58, 67, 18, 9, 16, 24, None), (58, 70, 27, 9, 72, 8, None), (1, 900, 76, 38, 8, 32, [2, 2, 451, 460, 897])])
+def test_backward_of_many_shared_heads(shape, dtype):
+    *sizes, cu = shape
+    say(f"[delta bwd shared] {shape} {dtype}")
+    check_bwd(make(*sizes, dtype, seed=sizes[1], nseq=None if cu is None else len(cu) - 1), cu=cu, name=str(shape))
+
+
 # Long sequences of few heads: cut into segments that are walked at once.
 LONG = [(1, 4000, 1, 1, 64, 40, None), (2, 3001, 2, 1, 128, 128, None), (1, 2600, 1, 1, 256, 24, None), (1, 3500, 2, 2, 16, 256, None),
         (1, 4200, 1, 1, 32, 64, [0, 1500, 1500, 1501, 4200]), (1, 3900, 1, 1, 64, 64, [3, 20, 3900])]
