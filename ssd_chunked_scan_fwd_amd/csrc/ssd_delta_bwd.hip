@@ -17,6 +17,11 @@
 // the tokens as columns j). First, over the value columns 32 at a time, the products with the states (contraction over
 // the columns, the states' terms in LDS) and the Z; then the products of the masked Z, which stay in registers, with Q
 // and K, whose rows take the states' place in LDS.
+// 8192 tokens, 32 heads on 16 of 128 x 128: 430 to 450 us. 1.2 GB are read, the states of all chunks and U twice half
+// of it, and 0.2 GB written: 3.2 TB/s, with one workgroup a CU, whose waves keep 256 registers: a step of 32 columns
+// takes 4 us, of which 1 is a wait for memory, the vector units are busy 37 % of the time, matrix units 21 %. (Rows of
+// Q and K loaded with the first columns: no faster, fp32 412 -> 447 us. With both kinds of waves for half of the key
+// columns each, U and U' split twice: 30 us more.)
 #include "ssd_delta_tile.h"
 
 namespace ssd {

@@ -13,6 +13,8 @@
 // T (with beta of its columns folded in) and P are stored as the operands that
 // the walk over the chunks loads, and for the gradients their transposes. A tile of
 // P is such an operand as its accumulators hold it.
+// 16384 tokens, 32 heads on 16 of 128 x 128: 100 us, 141 MB read and 225 MB written (3.7 TB/s), the vector units
+// busy 33 % of the time, matrix units 17 %, LDS 28 %: the inverse's dependent steps bound it, four workgroups a CU.
 #include "ssd_delta_tile.h"
 
 namespace ssd {
@@ -320,7 +322,8 @@ __global__ __launch_bounds__(kThreads, BWD ? 3 : 4) void delta_prep_kernel(Delta
 }
 
 // Value heads a workgroup: all that share its keys, whose products it makes once, or so few that the launch has
-// four workgroups for every CU. A workgroup's time is mostly waits: 348 of four heads took 28 us, 1392 of one 17.
+// four workgroups for every CU. A workgroup's time is mostly waits: 5087 tokens of 16 heads on 4, 348 workgroups of four
+// heads took 25.4 us, 1392 of one 22.5; 8192 of 4 on 2, 256 of two 15.7 and 512 of one 14.3.
 int heads_a_workgroup(const DeltaArgs& a) {
   const int rep = a.H / a.Hk;
   int heads = rep;

@@ -197,7 +197,8 @@ __device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70
 
 // LDS rows of 16 nv values of a token, written 8 bytes a lane (16 rows) and read transposed (8 rows a half wave). One
 // block of 16: rows of 32 bytes, one behind the other, the two halves of every second 8 rows exchanged; both accesses
-// then cover the 64 banks once. (Padded rows of 48 bytes cost a walk 760 of its 1710 LDS cycles a chunk in conflicts.)
+// then cover the 64 banks once. (Padded rows of 48 bytes cost a walk 760 of its 1710 LDS cycles a chunk in conflicts;
+// a third of them are left, and neither their number nor other pitches of the keys' rows show in its time.)
 // More blocks: an odd multiple of 32 bytes.
 __host__ __device__ constexpr int value_pitch(int nv) { return nv == 1 ? 16 : lds_pitch(16 * nv); }
 template <int PITCH>
@@ -205,8 +206,8 @@ __device__ __forceinline__ int value_at(int row, int col) {
   return row * PITCH + (PITCH == 16 ? col ^ (row & 8) : col);
 }
 
-// e^x to an ulp or two, with the hardware's 2^y: what rounds off y = x log2(e) is put back to first order. (The
-// library's exponential took a third of the time of the chunks' matrices.)
+// e^x to an ulp or two, with the hardware's 2^y: what rounds off y = x log2(e) is put back to first order. (With the
+// library's exponential the matrices of 16384 tokens, 32 heads, took 119 us for 108.)
 __device__ __forceinline__ float exp_of(float x) {
   const float y = x * kLog2e, rest = fmaf(x, kLog2e, -y);
   const float p = fast_exp2(y);

@@ -391,3 +391,66 @@ def test_values_that_are_not_finite(dtype):
         for n in ("dq", "dk", "dv", "dlog_decay", "dbeta"):
             assert torch.equal(gg[n][:, out], gw[n][:, out]), (name, n)
         assert torch.equal(gg["dinit"][[0, 2]], gw["dinit"][[0, 2]])
+
+
+# A walk in segments, value heads summed in one workgroup, and added up by a launch of their own.
+PATHS = [(1, 2600, 2, 1, 64, 64), (58, 67, 18, 9, 16, 24), (1, 150, 4, 2, 32, 48)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", PATHS)
+def test_workspace_of_any_contents(shape, dtype):
+    """Nothing is read from the workspace that the call has not written, and nothing written behind it."""
+    say(f"[delta] workspace of NaN {shape} {dtype}")
+    d = make(*shape, dtype, 50)
+    size = ssd.gated_delta_bwd_workspace_bytes(ssd.gated_delta_shape(d["q"], d["k"], d["v"]))
+    want, grads = run_fwd(d), run_bwd(d)
+    assert all(torch.isfinite(x.float()).all() for x in [*want, *grads.values()])
+    ws = torch.full((size + 256,), 255, dtype=torch.uint8, device="cuda")
+    g2 = run_bwd(d, workspace=ws)
+    ws[:size].fill_(255)
+    got = run_fwd(d, workspace=ws)
+    assert all(torch.equal(x, y) for x, y in zip(want, got)) and all(torch.equal(grads[n], g2[n]) for n in grads)
+    assert (ws[size:] == 255).all()
+
+
+def test_graphs_that_share_a_workspace():
+    """Two graphs on one workspace, replayed in turn, with eager calls on another workspace between."""
+    say("[delta] graphs on one workspace")
+    ds = [make(*PATHS[0], BF, 51), make(*PATHS[2], BF, 52)]
+    size = max(ssd.gated_delta_bwd_workspace_bytes(ssd.gated_delta_shape(d["q"], d["k"], d["v"])) for d in ds)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    want = [(run_fwd(d), run_bwd(d)) for d in ds]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for d in ds:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append((run_fwd(d, workspace=ws), run_bwd(d, workspace=ws)))
+        graphs.append(g)
+    for r in range(3):
+        for i in (0, 1, 0):
+            for x in [*outs[i][0], *outs[i][1].values()]:
+                x.zero_()
+            graphs[i].replay()
+            other = run_fwd(ds[1 - i])
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(want[1 - i][0], other))
+            assert all(torch.equal(x, y) for x, y in zip(want[i][0], outs[i][0]))
+            assert all(torch.equal(want[i][1][n], outs[i][1][n]) for n in want[i][1])
+
+
+def test_two_streams_at_once():
+    say("[delta] two streams")
+    ds = [make(*PATHS[0], BF, 53), make(1, 700, 8, 4, 128, 128, BF, 54)]
+    want = [(run_fwd(d), run_bwd(d)) for d in ds]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(4):
+        for s, d in zip(streams, ds):
+            with torch.cuda.stream(s):
+                got.append((run_fwd(d), run_bwd(d)))
+    torch.cuda.synchronize()
+    for i, (fwd, grads) in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(want[i % 2][0], fwd))
+        assert all(torch.equal(want[i % 2][1][n], grads[n]) for n in grads)
