@@ -393,6 +393,29 @@ def test_values_that_are_not_finite(dtype):
         assert torch.equal(gg["dinit"][[0, 2]], gw["dinit"][[0, 2]])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_values_that_are_not_finite_in_segments(dtype):
+    """The same where a walk is cut: a segment's map and own state carry them forwards only."""
+    say(f"[delta] not finite, segments {dtype}")
+    cu = [0, 1500, 3100]
+    d = make(1, 3100, 1, 1, 32, 32, dtype, 38, nseq=2)
+    want, gw = run_fwd(d, cu=cu), run_bwd(d, cu=cu)
+    for name, at, bad in (("v", 700, float("nan")), ("k", 700, float("inf")), ("g", 2000, float("nan")), ("v", 1499, float("inf"))):
+        e = {n: x.clone() for n, x in d.items()}
+        e[name][0, at] = bad
+        got, gg = run_fwd(e, cu=cu), run_bwd(e, cu=cu)
+        s = int(at >= cu[1])
+        first = cu[s] + (at - cu[s]) // 64 * 64   # where its chunk begins, at the earliest
+        keep = [t for t in range(3100) if t < first or not cu[s] <= t < cu[s + 1]]
+        out = [t for t in range(3100) if not cu[s] <= t < cu[s + 1]]
+        assert torch.equal(got[0][:, keep], want[0][:, keep]), name
+        assert torch.equal(got[1][1 - s], want[1][1 - s]), name
+        assert not torch.isfinite(got[0][:, at].float()).all() and not torch.isfinite(got[1][s]).all()
+        for n in ("dq", "dk", "dv", "dlog_decay", "dbeta"):
+            assert torch.equal(gg[n][:, out], gw[n][:, out]), (name, n)
+        assert torch.equal(gg["dinit"][1 - s], gw["dinit"][1 - s])
+
+
 # A walk in segments, value heads summed in one workgroup, and added up by a launch of their own.
 PATHS = [(1, 2600, 2, 1, 64, 64), (58, 67, 18, 9, 16, 24), (1, 150, 4, 2, 32, 48)]
 
