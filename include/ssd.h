@@ -623,8 +623,7 @@ ssd_status ssd_pages_compact(void* pool, const uint8_t* live, int32_t* where, in
  * multiples of 8 up to 256), overlaps and the limit on a launch: as for linear
  * attention above. bf16 inputs enter the matrix products as they are, everything
  * computed as sums of three bf16 terms (24 bits) with fp32 sums, fp32 inputs
- * likewise; only the products that o of bf16 alone depends on take two terms. o and
- * the gradients of q, k and v are rounded once, when written.
+ * likewise. o and the gradients of q, k and v are rounded once, when written.
  * A value that is not finite makes the results of its sequence from its chunk (64
  * tokens, fp32: 32) on not finite, and of the chunk itself also earlier ones; in
  * the backward call any of its sequence. Other sequences are not touched.

@@ -39,7 +39,7 @@ struct DeltaArgs {
   long slots_per_row = 0, slots = 0;
   float* gates = nullptr;        // [slots][H][kGateRows][C]
   float* tf = nullptr;           // T diag(beta) and
-  uint16_t* pf = nullptr;        // P, operands (ssd_delta_tile.h)
+  void* pf = nullptr;            // P, operands (ssd_delta_tile.h)
   // Sequences cut into segments of `seg` chunks (0: not cut), numbered as chunks are, by which one long sequence
   // of few heads fills the card (ssd_delta_chain.hip).
   int seg = 0;

@@ -213,7 +213,7 @@ ssd_status ssd_gated_delta_fwd(const void* q, const void* k, const void* v, cons
   a.o = o;
   a.gates = reinterpret_cast<float*>(ws + L.gates);
   a.tf = reinterpret_cast<float*>(ws + L.tf);
-  a.pf = reinterpret_cast<uint16_t*>(ws + L.pf);
+  a.pf = ws + L.pf;
   a.seg_states = reinterpret_cast<float*>(ws + L.seg_states);
   a.seg_maps = reinterpret_cast<float*>(ws + L.seg_maps);
   const hipError_t e = ssd::launch_delta_prep(a, false, (hipStream_t)stream);

@@ -278,12 +278,12 @@ template <int C, int KB, int NV, int NX, int WHAT>
 __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 && NV == 1 ? 4 : 2) void delta_fwd_kernel(DeltaArgs a) {
   using Sh = Share<C, KB, NV>;
   constexpr bool KEEP = WHAT != kOutputs;
-  constexpr int kEsz = NX == 1 ? 2 : 4, kOut = out_terms(NX), kKp = C / 32;
+  constexpr int kEsz = NX == 1 ? 2 : 4, kKp = C / 32;
   constexpr int kPitchK = lds_pitch(32 * KB), kPitchV = value_pitch(NV);
   __shared__ __align__(16) uint16_t Sl[kTerms * 16 * NV * kPitchK];
   __shared__ __align__(16) uint16_t Kl[NX * C * kPitchK];
   __shared__ __align__(16) uint16_t Xl[kTerms * C * kPitchV], Wl[kTerms * C * kPitchV];   // X; e^(G_C - G) U
-  constexpr int kU = kOut * C * kPitchV;
+  constexpr int kU = kTerms * C * kPitchV;
   __shared__ __align__(16) uint16_t Ul[KEEP ? 8 : 2 * kU];   // U of this chunk and of the one before
   const int wave = uniform(threadIdx.x >> 6);
   const Sh w(wave & 3);
@@ -370,7 +370,7 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 && NV == 1 ? 4 : 2) vo
         }
         stage4<C, kTerms, kPitchV>(Wl, tok, 16 * w.vb(i) + 4 * g, U[i] * wt);
         if (WHAT == kKeep) buf_store16(__builtin_bit_cast(u32x4, U[i]), make_rsrc(a.u + sh * C * a.dv, (uint32_t)(C * a.dv * 4)), uat.at[i]);
-        if (WHAT == kOutputs) stage4<C, kOut, kPitchV>(Ul + (c & 1) * kU, tok, 16 * w.vb(i) + 4 * g, U[i]);
+        if (WHAT == kOutputs) stage4<C, kTerms, kPitchV>(Ul + (c & 1) * kU, tok, 16 * w.vb(i) + 4 * g, U[i]);
       }
       __syncthreads();
       __builtin_amdgcn_sched_barrier(0);   // while the state is updated, and not before the barrier
@@ -387,7 +387,7 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 && NV == 1 ? 4 : 2) vo
     read_state<C, KB, NV>(a, u, w, c16, g, S);
     stage_state<C, KB, NV>(Sl, w, c16, g, S);
     Raw8<NX> qr[KEEP ? 1 : KB];
-    u32x4 pf[KEEP ? 1 : kKp][kOut];
+    Scores<NX> pr[KEEP ? 1 : kKp];
     f32x4 O[Sh::kV];
     float eg = 0.f, keep = 0.f;
     auto load_q = [&](int c) {
@@ -407,9 +407,10 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 && NV == 1 ? 4 : 2) vo
 #pragma unroll
         for (int kp = 0; kp < kKp; ++kp) {
           if (kp > w.tb / 2) continue;
-          u32x4 ut[kOut];
-          values_operand<C, kOut, kPitchV>(Ul + (c & 1) * kU, kp, 16 * w.vb(i), lane, ut);
-          O[i] = mma<kOut, kOut, kOut>(ut, pf[kp], O[i]);
+          u32x4 ut[kTerms], pt[kTerms];
+          values_operand<C, kTerms, kPitchV>(Ul + (c & 1) * kU, kp, 16 * w.vb(i), lane, ut);
+          terms8<kTerms>(pr[kp], pt);
+          O[i] = mma<kTerms, kTerms, kTerms>(ut, pt, O[i]);
         }
         store4<NX>(O[i], ro, oat.at[i]);
       }
@@ -430,13 +431,13 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 && NV == 1 ? 4 : 2) vo
         for (int b = 0; b < KB; ++b) terms8<NX>(qr[b], qt[b]);
 #pragma unroll
         for (int i = 0; i < Sh::kV; ++i)
-          if (w.vb(i) < NV) Q[i] = state_times<KB, NV, NX, kOut>(Sl, w.vb(i), qt, lane) * (eg * a.scale);
+          if (w.vb(i) < NV) Q[i] = state_times<KB, NV, NX, kTerms>(Sl, w.vb(i), qt, lane) * (eg * a.scale);
         load_q(ahead);
       }
       __syncthreads();
       if constexpr (!KEEP) {
         if (c > 0) finish(c - 1);
-        load_operands<C, kOut>(a.pf, sh0 + (long)c * a.H, w.tb, 0, w.tb / 2, lane, pf);
+        load_operands<C>(static_cast<const ScoresIn<NX>*>(a.pf), sh0 + (long)c * a.H, w.tb, 0, w.tb / 2, lane, pr);
 #pragma unroll
         for (int i = 0; i < Sh::kV; ++i) O[i] = Q[i];
       }

@@ -131,21 +131,21 @@ __device__ __forceinline__ void put_operand(const float* M, float* to, int rb, i
       x[r] = TR ? M[(col + r) * kPitch<C> + row] : M[row * kPitch<C> + col + r];
       if (w) x[r] *= w[col + r];
     }
-    *reinterpret_cast<f32x4*>(to + operand_at(C, 1, rb, kp) + 256 * t + lane * 4) = x;
+    *reinterpret_cast<f32x4*>(to + operand_at(C, rb, kp) + 256 * t + lane * 4) = x;
   }
 }
 // Half of an operand, the columns 16 cb ..: a tile as its accumulators hold it (rows c16, columns 4 g + r).
 template <int C>
 __device__ __forceinline__ void put_tile(f32x4 x, float* to, int rb, int cb, int lane) {
-  *reinterpret_cast<f32x4*>(to + operand_at(C, 1, rb, cb / 2) + 256 * (cb & 1) + lane * 4) = x;
+  *reinterpret_cast<f32x4*>(to + operand_at(C, rb, cb / 2) + 256 * (cb & 1) + lane * 4) = x;
 }
-template <int C, int N>
+template <int C>
 __device__ __forceinline__ void put_tile(f32x4 x, uint16_t* to, int rb, int cb, int lane) {
-  u32x2 part[N];
-  split4<N>(x, part);
-  uint16_t* at = to + operand_at(C, N, rb, cb / 2) + lane * 8 + 4 * (cb & 1);
+  u32x2 part[kTerms];
+  split4<kTerms>(x, part);
+  uint16_t* at = to + kTerms * operand_at(C, rb, cb / 2) + lane * 8 + 4 * (cb & 1);
 #pragma unroll
-  for (int t = 0; t < N; ++t) *reinterpret_cast<u32x2*>(at + t * kOperand) = part[t];
+  for (int t = 0; t < kTerms; ++t) *reinterpret_cast<u32x2*>(at + t * kOperand) = part[t];
 }
 
 // The pairs of 16 rows and 16 columns on or below the diagonal that wave w takes: (row, column), -1: none.
@@ -168,7 +168,7 @@ __device__ __forceinline__ void tile_of(int wave, int e, int& ib, int& jb) {
 template <int C, int KB, int NX, bool BWD>
 __global__ __launch_bounds__(kThreads, BWD ? 3 : 4) void delta_prep_kernel(DeltaArgs a, int heads) {
   constexpr int kTiles = C == 64 ? 3 : 1;   // a wave
-  constexpr int kEsz = NX == 1 ? 2 : 4, kOut = out_terms(NX);
+  constexpr int kEsz = NX == 1 ? 2 : 4;
   // Rows of K and Q, kSlab pieces of 32 columns at a time, and in their place the matrix.
   constexpr int kSlab = NX == 1 ? (KB < 4 ? KB : 4) : (KB < 2 ? KB : 2), kPitchK = lds_pitch(32 * kSlab);
   constexpr int kRows = NX * C * kPitchK, kBytes = 4 * kRows > 4 * C * kPitch<C> ? 4 * kRows : 4 * C * kPitch<C>;
@@ -298,15 +298,16 @@ __global__ __launch_bounds__(kThreads, BWD ? 3 : 4) void delta_prep_kernel(Delta
         const float h1 = gh[j1], l1 = gl[j1];
 #pragma unroll
         for (int r = 0; r < 4; ++r) P[r] = j1 <= i4 + r ? a.scale * exp_of((hr[r] - h1) + (lr[r] - l1)) * qk[e][r] : 0.f;
-        float* to = a.pt + sh * operands(C, 1);
+        float* to = a.pt + sh * operands(C);
         put_tile<C>(P, to, jb, ib, lane);
         if (ib == jb && (ib & 1)) put_tile<C>(zero, to, jb, ib - 1, lane);
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r) P[r] = j + r <= i ? a.scale * d[r] * qk[e][r] : 0.f;
-        uint16_t* to = a.pf + sh * operands(C, kOut);
-        put_tile<C, kOut>(P, to, ib, jb, lane);
-        if (ib == jb && !(ib & 1)) put_tile<C, kOut>(zero, to, ib, jb + 1, lane);
+        ScoresIn<NX>* to = static_cast<ScoresIn<NX>*>(a.pf);
+        to += scores_at<C>(to, sh);
+        put_tile<C>(P, to, ib, jb, lane);
+        if (ib == jb && !(ib & 1)) put_tile<C>(zero, to, ib, jb + 1, lane);
       }
     }
     __syncthreads();
@@ -315,8 +316,8 @@ __global__ __launch_bounds__(kThreads, BWD ? 3 : 4) void delta_prep_kernel(Delta
     // Operands on or below the diagonal, of the transpose on or above it.
     for (int t = wave; t < (C / 16) * (C / 32); t += 4) {
       const int rb = t / (C / 32), kp = t % (C / 32);
-      if (kp <= rb / 2) put_operand<C, false>(Am, a.tf + sh * operands(C, 1), rb, kp, bt, lane);
-      if (BWD && kp >= rb / 2) put_operand<C, true>(Am, a.tt + sh * operands(C, 1), rb, kp, nullptr, lane);
+      if (kp <= rb / 2) put_operand<C, false>(Am, a.tf + sh * operands(C), rb, kp, bt, lane);
+      if (BWD && kp >= rb / 2) put_operand<C, true>(Am, a.tt + sh * operands(C), rb, kp, nullptr, lane);
     }
   }
 }
@@ -344,8 +345,8 @@ void prep(const DeltaArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t delta_gates_bytes(bool bf16) { return (size_t)kGateRows * delta_chunk(bf16) * 4; }
-size_t delta_tf_bytes(bool bf16) { return (size_t)operands(delta_chunk(bf16), 1) * 4; }
-size_t delta_pf_bytes(bool bf16) { return (size_t)operands(delta_chunk(bf16), out_terms(bf16 ? 1 : 3)) * 2; }
+size_t delta_tf_bytes(bool bf16) { return (size_t)operands(delta_chunk(bf16)) * 4; }
+size_t delta_pf_bytes(bool bf16) { return (size_t)operands(delta_chunk(bf16)) * (bf16 ? 4 : 2 * kTerms); }
 int delta_prep_threads() { return kThreads; }
 
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stream) {

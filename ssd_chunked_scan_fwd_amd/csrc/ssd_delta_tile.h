@@ -3,12 +3,16 @@
 // chunk as operands.
 //
 // The rule feeds what it computes back into itself (the state, and the inverse
-// of I + A), and its states and gate gradients are fp32 results. So every
+// of I + A), its states and gate gradients are fp32 results, and o may be small
+// beside the terms that it is summed of (a query that is almost orthogonal to what
+// the state holds), far below where 16 bits of them end. So every
 // computed operand enters its products as the sum of three bf16 terms, which
 // hold all 24 bits of an fp32 value; bf16 inputs are exact with one, fp32 inputs
 // take three. Of a product of terms i and j those with i + j < 3 are formed: what
 // is left out is below 2^-24 of the product.
 #pragma once
+
+#include <type_traits>
 
 #include "ssd_delta.h"
 #include "ssd_device.h"
@@ -17,9 +21,6 @@
 namespace ssd {
 
 constexpr int kTerms = 3;
-// Terms of the operands that only o, a result of the inputs' type, depends on:
-// two leave 2^-16 of it, where o itself is rounded by 2^-9.
-constexpr int out_terms(int nx) { return nx == 1 ? 2 : kTerms; }
 
 // Eight (four) floats as the sum of N terms each.
 template <int N>
@@ -151,17 +152,30 @@ __device__ __forceinline__ void store4(f32x4 x, rsrc_t r, uint32_t off) {
 }
 
 // C x C matrices in the workspace as operands of 16 rows and 32 columns, columns in the order of an accumulator
-// pair. P, of which o's products take two terms of bf16 inputs: those terms, each 64 lanes of 16 bytes, one behind the
-// other. T and the transposes, of which three are taken: fp32, 64 lanes of the columns 4 g .., then 64 of the columns
-// 16 + 4 g .., split into terms where they are used. What a CU has on its way from memory bounds the walks of few
-// heads: with three terms in memory, half as much again, they took 9 to 13 % longer.
-// A triangle's zero operands are not loaded.
+// pair, in fp32: 64 lanes of the columns 4 g .., then 64 of the columns 16 + 4 g .., split into terms where they are
+// used. What a CU has on its way from memory bounds the walks of few heads: with three terms in memory, half as much
+// again, they took 9 to 13 % longer. A triangle's zero operands are not loaded.
 constexpr int kOperand = 512;   // elements
-__host__ __device__ constexpr long operands(int C, int n) { return (long)(C / 16) * (C / 32) * n * kOperand; }
-__device__ __forceinline__ int operand_at(int C, int n, int rb, int kp) { return (rb * (C / 32) + kp) * n * kOperand; }
+__host__ __device__ constexpr long operands(int C) { return (long)(C / 16) * (C / 32) * kOperand; }
+__device__ __forceinline__ int operand_at(int C, int rb, int kp) { return (rb * (C / 32) + kp) * kOperand; }
 struct RawOperand {
   u32x4 w[2];
 };
+// P of fp32 inputs is there as its three terms, each 64 lanes of 16 bytes, one behind the other: the waves that take it
+// have all other operands to split, and 8192 tokens, 32 heads on 16 of 128 x 128, took 833 us with it in fp32 for 794. With
+// bf16 inputs it is the memory that counts, as above: 16384 tokens 579 us in fp32, 604 in terms (with two value blocks a
+// workgroup the other way round: 2 x 4096 tokens 244 and 239).
+template <int NX>
+using ScoresIn = std::conditional_t<NX == 1, float, uint16_t>;
+template <int C>
+__device__ __forceinline__ long scores_at(const float*, long sh) { return sh * operands(C); }
+template <int C>
+__device__ __forceinline__ long scores_at(const uint16_t*, long sh) { return sh * kTerms * operands(C); }
+struct TermOperand {
+  u32x4 w[kTerms];
+};
+template <int NX>
+using Scores = std::conditional_t<NX == 1, RawOperand, TermOperand>;
 template <int N>
 __device__ __forceinline__ void terms8(const RawOperand& x, u32x4* out) {
   float f[8];
@@ -169,25 +183,30 @@ __device__ __forceinline__ void terms8(const RawOperand& x, u32x4* out) {
   for (int c = 0; c < 8; ++c) f[c] = __uint_as_float(x.w[c >> 2][c & 3]);
   split8<N>(f, out);
 }
+template <int N>
+__device__ __forceinline__ void terms8(const TermOperand& x, u32x4* out) {
+#pragma unroll
+  for (int t = 0; t < N; ++t) out[t] = x.w[t];
+}
 // Row block rb of matrix sh; the operands from `least` to `most`, zeros in the place of the others.
 template <int C>
 __device__ __forceinline__ void load_operands(const float* from, long sh, int rb, int least, int most, int lane, RawOperand* to) {
-  const rsrc_t r = make_rsrc(from + sh * operands(C, 1), (uint32_t)(operands(C, 1) * 4));
+  const rsrc_t r = make_rsrc(from + sh * operands(C), (uint32_t)(operands(C) * 4));
 #pragma unroll
   for (int kp = 0; kp < C / 32; ++kp) {
-    const uint32_t off = kp >= least && kp <= most ? (uint32_t)(operand_at(C, 1, rb, kp) * 4 + lane * 16) : kOffNone;
+    const uint32_t off = kp >= least && kp <= most ? (uint32_t)(operand_at(C, rb, kp) * 4 + lane * 16) : kOffNone;
     to[kp].w[0] = buf_load16(r, off);
     to[kp].w[1] = buf_load16(r, off + 1024);
   }
 }
-template <int C, int N>
-__device__ __forceinline__ void load_operands(const uint16_t* from, long sh, int rb, int least, int most, int lane, u32x4 (*to)[N]) {
-  const rsrc_t r = make_rsrc(from + sh * operands(C, N), (uint32_t)(operands(C, N) * 2));
+template <int C>
+__device__ __forceinline__ void load_operands(const uint16_t* from, long sh, int rb, int least, int most, int lane, TermOperand* to) {
+  const rsrc_t r = make_rsrc(from + scores_at<C>(from, sh), (uint32_t)(kTerms * operands(C) * 2));
 #pragma unroll
   for (int kp = 0; kp < C / 32; ++kp) {
-    const uint32_t off = kp >= least && kp <= most ? (uint32_t)(operand_at(C, N, rb, kp) * 2 + lane * 16) : kOffNone;
+    const uint32_t off = kp >= least && kp <= most ? (uint32_t)(kTerms * operand_at(C, rb, kp) * 2 + lane * 16) : kOffNone;
 #pragma unroll
-    for (int t = 0; t < N; ++t) to[kp][t] = buf_load16(r, off + t * kOperand * 2);
+    for (int t = 0; t < kTerms; ++t) to[kp].w[t] = buf_load16(r, off + t * kOperand * 2);
   }
 }
 
