@@ -225,10 +225,12 @@ __device__ __forceinline__ int value_at(int row, int col) {
   return row * PITCH + (PITCH == 16 ? col ^ (row & 8) : col);
 }
 
-// e^x to an ulp or two, with the hardware's 2^y: what rounds off y = x log2(e) is put back to first order. (With the
-// library's exponential the matrices of 16384 tokens, 32 heads, took 119 us for 108.)
+// e^x to an ulp or two, with the hardware's 2^y: what rounds off y = x log2(e) is put back to first order, and so is
+// what log2(e) itself has below 24 bits, 1.3e-8 of it, which would be 9 ulp at x = -80. (With the library's exponential
+// the matrices of 16384 tokens, 32 heads, took 119 us for 108.)
+constexpr float kLog2eLow = 1.925963033e-8f;
 __device__ __forceinline__ float exp_of(float x) {
-  const float y = x * kLog2e, rest = fmaf(x, kLog2e, -y);
+  const float y = x * kLog2e, rest = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -y));
   const float p = fast_exp2(y);
   return fmaf(p, rest * 0.69314718f, p);
 }

@@ -84,3 +84,21 @@ def test_scores_and_updates(dtype):
     assert np.all(np.abs(o[0] - beta[0][:, None]) <= (ref.UBF if dtype == BF else ref.U32) * beta[0][:, None])
     worst = np.abs(o[1] - want[:, None]).max() / ref.U32
     assert worst <= 12, worst
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 3])
+def test_decay_of_a_state(T, dtype):
+    """A state of ones that only decays, down to e^-86: e^G in fp32. One token, in units of 2^-24 of the result: 2 of the
+    hardware's 2^y (its last place), 1 of what puts y's rounding back; 4 are allowed. The log decays of more tokens add
+    up in 64 bits, and what their sum has below 32 bits is a factor: 1 for it, 1 for the product, 6 allowed."""
+    say(f"[delta bits] decay of a state {T} {dtype}")
+    H, r = 4096, np.random.default_rng(T)
+    total = -np.exp(np.linspace(np.log(1e-3), np.log(86.0), H))
+    g = np.ascontiguousarray(total * r.dirichlet(np.ones(T), H).T, np.float32)
+    q, k, v = (torch.randn(1, T, n, 8, generator=torch.Generator().manual_seed(n)).to(dtype).cuda() for n in (1, 1, H))
+    init = torch.ones(1, H, 8, 8, device="cuda")
+    _, fin = ssd.gated_delta_fwd(q, k, v, torch.tensor(g)[None].cuda(), torch.zeros(1, T, H, device="cuda"), initial_state=init)
+    want = np.exp(g.astype(np.float64).sum(0))[:, None, None]
+    worst = (np.abs(fin[0].cpu().double().numpy() - want) / want).max() / ref.U32
+    assert worst <= (4 if T == 1 else 6), worst
