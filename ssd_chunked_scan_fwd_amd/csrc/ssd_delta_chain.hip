@@ -741,10 +741,11 @@ __global__ __launch_bounds__(128 * KB) void delta_join_kernel(DeltaArgs a, int C
 // than the CUs (of packed sequences, the longest of which are taken to be three times the mean, three times as many);
 // else one. Heads of 128 x 128, us with one and with two: 2 x 4096 tokens of 32 heads (512 workgroups of one) 260 and
 // 219, 4096 of 48 235 and 193; 5087 ragged tokens of 16 heads of 64 x 96 (768) 84 and 93. fp32: two; with keys of
-// 256, whose rows leave LDS for one, one.
+// 256, whose rows leave LDS for one, one. Walks that are cut fill the card as they are: one (bf16).
 constexpr int nv32(int kb) { return kb > 4 ? 1 : 2; }
 int value_blocks(const DeltaArgs& a) {
   if (!a.bf16) return nv32((a.dk + 31) / 32);
+  if (a.seg) return 1;
   const long units = (long)(a.S > 0 ? a.S : a.batch) * a.H * ((a.dv + 15) / 16);
   return units > (a.S > 0 ? 3 * 256 : 256) && a.dk <= 128 ? 2 : 1;
 }
@@ -752,10 +753,14 @@ int value_blocks(const DeltaArgs& a) {
 template <int KB, int WHAT>
 void walk(const DeltaArgs& a, long blocks, hipStream_t stream) {
   const dim3 grid((unsigned)blocks);
-  constexpr int kWideNv = KB <= 4 ? 2 : 1;
-  if (!a.bf16) hipLaunchKernelGGL((delta_fwd_kernel<32, KB, nv32(KB), 3, WHAT>), grid, dim3(kThreads), 0, stream, a);
-  else if (value_blocks(a) == 1) hipLaunchKernelGGL((delta_fwd_kernel<64, KB, 1, 1, WHAT>), grid, dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL((delta_fwd_kernel<64, KB, kWideNv, 1, WHAT>), grid, dim3(kThreads), 0, stream, a);
+  if constexpr (KB <= 4 && WHAT != kOwn) {
+    if (a.bf16 && value_blocks(a) == 2) {
+      hipLaunchKernelGGL((delta_fwd_kernel<64, KB, 2, 1, WHAT>), grid, dim3(kThreads), 0, stream, a);
+      return;
+    }
+  }
+  if (a.bf16) hipLaunchKernelGGL((delta_fwd_kernel<64, KB, 1, 1, WHAT>), grid, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((delta_fwd_kernel<32, KB, nv32(KB), 3, WHAT>), grid, dim3(kThreads), 0, stream, a);
 }
 template <int KB, bool REV>
 void join(const DeltaArgs& a, hipStream_t stream) {
@@ -774,10 +779,14 @@ void fwd(const DeltaArgs& a, bool keep, hipStream_t stream) {
 template <int KB, bool OWN>
 void walk_back(const DeltaArgs& a, hipStream_t stream) {
   const dim3 grid((unsigned)delta_chain_blocks(a));
-  constexpr int kWideNv = KB <= 4 ? 2 : 1;
-  if (!a.bf16) hipLaunchKernelGGL((delta_rev_kernel<32, KB, nv32(KB), 3, OWN>), grid, dim3(kThreads), 0, stream, a);
-  else if (value_blocks(a) == 1) hipLaunchKernelGGL((delta_rev_kernel<64, KB, 1, 1, OWN>), grid, dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL((delta_rev_kernel<64, KB, kWideNv, 1, OWN>), grid, dim3(kThreads), 0, stream, a);
+  if constexpr (KB <= 4 && !OWN) {
+    if (a.bf16 && value_blocks(a) == 2) {
+      hipLaunchKernelGGL((delta_rev_kernel<64, KB, 2, 1, OWN>), grid, dim3(kThreads), 0, stream, a);
+      return;
+    }
+  }
+  if (a.bf16) hipLaunchKernelGGL((delta_rev_kernel<64, KB, 1, 1, OWN>), grid, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((delta_rev_kernel<32, KB, nv32(KB), 3, OWN>), grid, dim3(kThreads), 0, stream, a);
 }
 template <int KB>
 void rev(const DeltaArgs& a, hipStream_t stream) {   // the maps are those of the forward walk
