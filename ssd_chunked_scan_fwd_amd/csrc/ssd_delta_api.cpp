@@ -3,6 +3,7 @@
 // before any HIP call; nothing is allocated, synchronised or thrown.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cstdint>
 
@@ -312,10 +313,10 @@ ssd_status ssd_gated_delta_step(float* state, const void* q, const void* k, cons
   if (!slots && num_slots < shape->batch) return SSD_ERR_INVALID_ARGUMENT;
   if (!aligned16(state) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return SSD_ERR_INVALID_ARGUMENT;
   if (!aligned4(log_decay) || !aligned4(beta) || !aligned4(slots)) return SSD_ERR_INVALID_ARGUMENT;
-  // a workgroup of 256 threads for every head and up to 128 row ranges of it
-  if (!ssd::launchable((int64_t)shape->nheads * ((shape->dv + 1) / 2), 256)) return SSD_ERR_UNSUPPORTED;
+  // A workgroup of 256 threads for every head and up to 64 row ranges of it (4 rows each at least): below 2^31 threads.
   const int64_t b = shape->batch, H = shape->nheads, Hk = shape->nqk_heads, esz = shape->dtype == SSD_DTYPE_BF16 ? 2 : 4;
-  const Span states = whole(state, (int64_t)num_slots * H * shape->dk * shape->dv * 4), out = whole(o, b * H * shape->dv * esz);
+  const int64_t slot = H * shape->dk * shape->dv * 4;
+  const Span states = whole(state, std::min<int64_t>(num_slots, INT64_MAX / 8 / slot) * slot), out = whole(o, b * H * shape->dv * esz);
   if (overlap({out, states}, {whole(q, b * Hk * shape->dk * esz), whole(k, b * Hk * shape->dk * esz),
                               whole(v, b * H * shape->dv * esz), whole(log_decay, b * H * 4), whole(beta, b * H * 4),
                               whole(slots, b * 4)}))
