@@ -1182,8 +1182,9 @@ def _delta_values(shape: DeltaShape):
     return tuple(getattr(shape, name) for name, _ in DeltaShape._fields_)
 
 
-def _delta_workspace(fn: str, shape: DeltaShape, workspace, device):
-    return _room(_size_of(fn, DeltaShape, _delta_values(shape)), workspace, device)
+def _delta_size(fn: str, shape: DeltaShape) -> int:
+    """Workspace bytes; refuses sizes that the library does not take, of a batch without tokens too."""
+    return _size_of(fn, DeltaShape, _delta_values(shape))
 
 
 def gated_delta_shape(q, k, v, cu_seqlens=None) -> DeltaShape:
@@ -1231,14 +1232,13 @@ def gated_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
                       (cu_seqlens, "cu_seqlens", None, torch.int32, 4), (workspace, "workspace", None, torch.uint8, 256)))
     if final_state is not None and initial_state is not None and _share(final_state, initial_state):
         raise ValueError("final_state must not overlap initial_state")
-    if b * T == 0:
-        _check_scale(scale)
-        if o is None:
-            o = torch.empty(b, T, H, Dv, dtype=q.dtype, device=q.device)
-        return o, _state_of_no_tokens(initial_state, final_state, want_final, st, q.device)
-    workspace, have = _delta_workspace("ssd_gated_delta_workspace_bytes", shape, workspace, q.device)
+    size = _delta_size("ssd_gated_delta_workspace_bytes", shape)
     if o is None:
         o = torch.empty(b, T, H, Dv, dtype=q.dtype, device=q.device)
+    if b * T == 0:
+        _check_scale(scale)
+        return o, _state_of_no_tokens(initial_state, final_state, want_final, st, q.device)
+    workspace, have = _room(size, workspace, q.device)
     if final_state is None and want_final:
         final_state = torch.empty(st, dtype=torch.float32, device=q.device)
     _call_on(q.device, "ssd_gated_delta_fwd", _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(beta), _addr(cu_seqlens),
@@ -1265,6 +1265,7 @@ def gated_delta_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
                       (dfinal_state, "dfinal_state", st, torch.float32, 16),
                       (log_decay, "log_decay", (b, T, H), torch.float32, 4), (beta, "beta", (b, T, H), torch.float32, 4),
                       (cu_seqlens, "cu_seqlens", None, torch.int32, 4), (workspace, "workspace", None, torch.uint8, 256)))
+    size = _delta_size("ssd_gated_delta_bwd_workspace_bytes", shape)
     new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=q.device)   # noqa: E731
     out = dict(dq=new(q.shape, q.dtype), dk=new(k.shape, q.dtype), dv=new(v.shape, q.dtype),
                dlog_decay=None if log_decay is None else new((b, T, H), torch.float32), dbeta=new((b, T, H), torch.float32),
@@ -1273,7 +1274,7 @@ def gated_delta_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
         _check_scale(scale)
         _state_of_no_tokens(dfinal_state, out["dinit"], want_dinit, st, q.device)
         return out
-    workspace, have = _delta_workspace("ssd_gated_delta_bwd_workspace_bytes", shape, workspace, q.device)
+    workspace, have = _room(size, workspace, q.device)
     _call_on(q.device, "ssd_gated_delta_bwd", _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(beta), _addr(cu_seqlens),
              float(scale), _addr(initial_state), _addr(do), _addr(dfinal_state), _addr(out["dq"]), _addr(out["dk"]),
              _addr(out["dv"]), _addr(out["dlog_decay"]), _addr(out["dbeta"]), _addr(out["dinit"]), ctypes.byref(shape),
@@ -1331,6 +1332,7 @@ def gated_delta_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
 # ---------------------------------------------------------------------------
 
 _ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROTARY_MOST = 1024   # elements of a head, as the C ABI checks
 
 
 def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -1451,6 +1453,8 @@ def _rotary(q, k, freq, positions, cu_seqlens, offsets, layout, scale, q_out, k_
         k_out = torch.empty(k.shape, dtype=dtype, device=device)
     if q.numel() == 0:
         _check_scale(scale)
+        if shape.dim > _ROTARY_MOST:
+            raise ValueError(f"heads of {shape.dim} elements; up to {_ROTARY_MOST} are supported")
         return q_out, k_out
     _call_on(device, "ssd_rotary", q.data_ptr(), _addr(k), freq.data_ptr(), _addr(positions), _addr(cu_seqlens), _addr(offsets),
              float(scale), q_out.data_ptr(), _addr(k_out), ctypes.byref(shape))
