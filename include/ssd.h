@@ -609,7 +609,8 @@ ssd_status ssd_pages_compact(void* pool, const uint8_t* live, int32_t* where, in
  *     o_t = scale S_t q_t.
  * Query and key heads are shared: value head h reads query and key head
  * h / (nheads / nqk_heads). Keys are meant to have norm 1 and beta to lie in
- * [0, 1] (the state is bounded then; nothing is normalised here).
+ * [0, 2] (I - beta k k^T has norm 1 at most then, and the state is bounded; nothing
+ * is normalised or refused here).
  *   q, k [batch, seqlen, nqk_heads, dk], v [batch, seqlen, nheads, dv] dtype:
  *       element (token, head, i) at token * row + head * d + i, with row the
  *       shape's q_row, k_row or v_row (0: contiguous); 16-byte aligned rows

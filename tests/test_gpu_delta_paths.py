@@ -86,3 +86,26 @@ def test_bits_of_ordinary_results(shape, dtype):
     for n, x in got.items():
         back_twice = 2 if n[0] == "d" else 1   # the gradients' walk begins with what the forward one left
         assert x <= back_twice * (RELBF if dtype == BF and n in ("o", "dq", "dk", "dv") else REL24), (n, x)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("equal", [False, True])
+def test_beta_up_to_two(equal, dtype):
+    """What a state answers is taken out up to twice (eigenvalues down to -1): I - beta k k^T has norm at most 1 still, on
+    which the bounds rest. Equal keys with beta = 2 and no decay turn the state's answer over at every token."""
+    say(f"[delta paths] beta up to two {equal} {dtype}")
+    d = make(2, 200, 4, 2, 64, 48, dtype, 12)
+    d["beta"] *= 2
+    if equal:
+        d["k"][:] = 0.125
+        d["beta"][:] = 2.0
+        d["g"][:] = 0.0
+    check_fwd(d)
+    check_bwd(d)
+    pool, o = d["init"].clone(), []
+    for t in range(3):
+        o.append(ssd.gated_delta_step(pool, *(d[n][:, t].contiguous() for n in ("q", "k", "v", "g", "beta")), scale=0.5))
+    short = {n: d[n][:, :3].contiguous() for n in ("q", "k", "v", "g", "beta")}
+    want = ref.batch_forward(*arrays(short), 0.5, n64(d["init"]))
+    ref.check(n64(torch.stack(o, 1)), want["o"], ref.rel_forward(3, 64), dtype == BF, "o of steps")
+    ref.check(n64(pool), want["final"], ref.rel_forward(3, 64), False, "state after steps")
