@@ -625,9 +625,11 @@ ssd_status ssd_pages_compact(void* pool, const uint8_t* live, int32_t* where, in
  * attention above. bf16 inputs enter the matrix products as they are, everything
  * computed as sums of three bf16 terms (24 bits) with fp32 sums, fp32 inputs
  * likewise. o and the gradients of q, k and v are rounded once, when written.
- * A value that is not finite makes the results of its sequence from its chunk (64
- * tokens, fp32: 32) on not finite, and of the chunk itself also earlier ones; in
- * the backward call any of its sequence. Other sequences are not touched.
+ * A value that is not finite reaches, forwards, what the rule brings it to: of q
+ * its token, of k and the gates all of their heads from its token on, of v and of a
+ * state its value column alone; there results are not finite (an infinity may be a
+ * NaN). In the backward call it reaches any gradient of its sequence. Other
+ * sequences are not touched.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int32_t batch;      /* rows; 1 with cu_seqlens; the step: entries            */

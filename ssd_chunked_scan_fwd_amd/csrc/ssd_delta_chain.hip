@@ -53,10 +53,10 @@ struct Unit {
 };
 // REV: backwards, `first` and `last` the gradients of the last and of the first state.
 template <int C, int NV, bool OWN, bool REV>
-__device__ __forceinline__ Unit delta_unit(const DeltaArgs& a, const float* first, float* last) {
+__device__ __forceinline__ Unit delta_unit(const DeltaArgs& a, int block, const float* first, float* last) {
   Unit u;
   const int values = (a.dv + 16 * NV - 1) / (16 * NV), tiles = values + (OWN && !REV ? (a.dk + 16 * NV - 1) / (16 * NV) : 0);
-  const long id = xcd_unit(blockIdx.x, gridDim.x), mat = (long)a.dk * a.dv, map = (long)a.dk * a.dk;
+  const long id = xcd_unit(block, gridDim.x), mat = (long)a.dk * a.dv, map = (long)a.dk * a.dk;
   const int tile = (int)(id % tiles);
   // Sequence or segment before head: an XCD takes a contiguous range of units, and all sequences, long and short, of
   // its heads. (Heads first, an XCD had one of eight ragged sequences: 102 us for what then took 70.)
@@ -269,13 +269,65 @@ __device__ __forceinline__ void scale_state(State<C, KB, NV>& S, float by) {
     for (int j = 0; j < Share<C, KB, NV>::kS; ++j) S[i][j] *= by;
 }
 
+// x, of token tok and four value columns, is not finite: where its own share is, the sum over the tokens up to tok alone,
+// which those behind it do not reach. (Matrix instructions take all tokens, the later ones times zero: what is not
+// finite in one of them would run against time.) w: a row of weights of the tokens, L: [term][C][PITCH] of their values.
+template <int C, int PITCH, typename Matrix>
+__device__ __forceinline__ f32x4 sum_so_far(f32x4 x, f32x4 own, const Matrix* w, const uint16_t* L, int tok, int col) {
+  f32x4 sum = own;
+#pragma unroll 1
+  for (int k = 0; k <= tok; ++k) {
+    const float weight = operand_value<C>(w, tok / 16, tok & 15, k);
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = kTerms - 1; t >= 0; --t) y += four(*reinterpret_cast<const u32x2*>(L + t * C * PITCH + value_at<PITCH>(k, col)));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sum[r] = fmaf(weight, y[r], sum[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (x[r] * 0.f != 0.f && own[r] * 0.f == 0.f) x[r] = sum[r];
+  return x;
+}
+// U of a chunk's n tokens one after the other, U_i = beta_i (X_i - sum_{j < i} D_ij k_i.k_j U_j), a lane a value column: as
+// the inverse, made by blocks, holds zeros times what is not finite in rows that this does not reach. One wave.
+template <int C, int KB, int NV, int NX, int PITCH>
+__device__ __forceinline__ void updates_by_token(const float* gates, const uint16_t* Kl, const uint16_t* Xl, float* Uf, int n, int lane) {
+  constexpr int kPitchK = lds_pitch(32 * KB), kWide = 16 * NV;
+  const int col = min(lane, kWide - 1);
+  auto key = [&](int row) {   // this lane's four of it
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    if (4 * lane < 32 * KB) {
+#pragma unroll
+      for (int t = NX - 1; t >= 0; --t) x += four(*reinterpret_cast<const u32x2*>(Kl + (t * C + row) * kPitchK + 4 * lane));
+    }
+    return x;
+  };
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const f32x4 ki = key(i);
+    float x = 0.f;
+#pragma unroll
+    for (int t = kTerms - 1; t >= 0; --t) x += bf16_to_f32(Xl[t * C * PITCH + value_at<PITCH>(i, col)]);
+#pragma unroll 1
+    for (int j = 0; j < i; ++j) {
+      const f32x4 kj = key(j);
+      const float kk = lanes_sum<64>(fmaf(ki[0], kj[0], fmaf(ki[1], kj[1], fmaf(ki[2], kj[2], ki[3] * kj[3]))), 64);
+      const float d = exp_of((gates[3 * C + i] - gates[3 * C + j]) + (gates[4 * C + i] - gates[4 * C + j]));
+      x = fmaf(-d * kk, Uf[j * kWide + col], x);
+    }
+    if (lane < kWide) Uf[i * kWide + col] = gates[2 * C + i] * x;
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 // What a forward walk writes: O; for the gradients, the states before the chunks and U; of a segment, its own last
 // state or map.
 enum { kOutputs, kKeep, kOwn };
 
 // NX: terms of an input.
 template <int C, int KB, int NV, int NX, int WHAT>
-__global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 && NV == 1 ? 4 : 2) void delta_fwd_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 && NV == 1 ? 4 : 2) void delta_fwd_kernel(DeltaArgs args) {
   using Sh = Share<C, KB, NV>;
   constexpr bool KEEP = WHAT != kOutputs;
   constexpr int kEsz = NX == 1 ? 2 : 4, kKp = C / 32;
@@ -285,173 +337,240 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 && NV == 1 ? 4 : 2) vo
   __shared__ __align__(16) uint16_t Xl[kTerms * C * kPitchV], Wl[kTerms * C * kPitchV];   // X; e^(G_C - G) U
   constexpr int kU = kTerms * C * kPitchV;
   __shared__ __align__(16) uint16_t Ul[KEEP ? 8 : 2 * kU];   // U of this chunk and of the one before
-  const int wave = uniform(threadIdx.x >> 6);
-  const Sh w(wave & 3);
-  const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
-  const Unit u = delta_unit<C, NV, WHAT == kOwn, false>(a, a.init, a.fin);
-  if (u.none) return;
-  const int hk = u.h / (a.H / a.Hk), tok = 16 * w.tb + c16, last = u.chunks - 1;
-  const long mat = (long)a.dk * a.dv, sh0 = u.slot0 * a.H + u.h;
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  auto rows = [&](const void* x, int c, long row, long col) {
-    return chunk_rows(x, u.start + (long)c * C, row, col, min(C, u.len - c * C), kEsz);
-  };
+  __shared__ int lost, again;   // the last state is not finite; updates of a chunk are to be made again
+  // CAREFUL: with what is not finite kept to where the rule brings it. A walk of outputs that ends in a state that is not
+  // finite (once it is not, no later one is) is walked once more so, in code of its own, which leaves the other's time as
+  // it is (16384 tokens 579 us for 580; a check of every chunk's O in one walk for both took 617, 8192 tokens of fp32 901 for
+  // 795). The walks that keep or make states alone need none of it: U that is not finite makes its state so.
+  auto walk = [&](auto careful, const DeltaArgs& a) {
+    constexpr bool CAREFUL = decltype(careful)::value;
+    int tid = threadIdx.x, block = blockIdx.x;
+    if (CAREFUL) asm volatile("" : "+v"(tid), "+s"(block));   // what follows from them is made anew, not kept over the walk
+    const int wave = uniform(tid >> 6);
+    const Sh w(wave & 3);
+    const int lane = tid & 63, c16 = lane & 15, g = lane >> 4;
+    const Unit u = delta_unit<C, NV, WHAT == kOwn, false>(a, block, a.init, a.fin);
+    if (u.none) return false;
+    const int hk = u.h / (a.H / a.Hk), tok = 16 * w.tb + c16, last = u.chunks - 1;
+    const long mat = (long)a.dk * a.dv, sh0 = u.slot0 * a.H + u.h;
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    auto rows = [&](const void* x, int c, long row, long col) {
+      return chunk_rows(x, u.start + (long)c * C, row, col, min(C, u.len - c * C), kEsz);
+    };
 
-  if (wave < 4) {
-    const KeyPieces<KB> kat(tok, g, a.k_row, a.dk, kEsz);
-    const ValuePieces<C, KB, NV> vat(w, tok, g, u.dv0, a.v_row, u.map ? 0 : a.dv, kEsz), uat(w, tok, g, u.dv0, a.dv, a.dv, 4);
-    Raw8<NX> kr[KB];
-    Raw4<NX> vr[Sh::kV];
-    u32x4 tf[kKp][kTerms];
-    RawOperand tn[kKp];   // of the next chunk
-    float eg, wt, eg_next, wt_next;
-    auto load_rows = [&](int c) {
-      const rsrc_t rk = rows(a.k, c, a.k_row, (long)hk * a.dk), rv = rows(a.v, c, a.v_row, (long)u.h * a.dv);
+    if (wave < 4) {
+      const KeyPieces<KB> kat(tok, g, a.k_row, a.dk, kEsz);
+      const ValuePieces<C, KB, NV> vat(w, tok, g, u.dv0, a.v_row, u.map ? 0 : a.dv, kEsz), uat(w, tok, g, u.dv0, a.dv, a.dv, 4);
+      Raw8<NX> kr[KB];
+      Raw4<NX> vr[Sh::kV];
+      u32x4 tf[kKp][kTerms];
+      RawOperand tn[kKp];   // of the next chunk
+      float eg, wt, eg_next, wt_next;
+      auto load_rows = [&](int c) {
+        const rsrc_t rk = rows(a.k, c, a.k_row, (long)hk * a.dk), rv = rows(a.v, c, a.v_row, (long)u.h * a.dv);
 #pragma unroll
-      for (int b = 0; b < KB; ++b) kr[b] = load8<NX>(rk, kat.at[b]);
+        for (int b = 0; b < KB; ++b) kr[b] = load8<NX>(rk, kat.at[b]);
 #pragma unroll
-      for (int i = 0; i < Sh::kV; ++i) vr[i] = load4<NX>(rv, vat.at[i]);
-    };
-    auto load_gates = [&](int c) {
-      const float* gates = a.gates + (sh0 + (long)c * a.H) * kGateRows * C;
-      eg_next = gates[tok];
-      wt_next = gates[C + tok];
-    };
-    auto next = [&]() {
-      eg = eg_next;
-      wt = wt_next;
+        for (int i = 0; i < Sh::kV; ++i) vr[i] = load4<NX>(rv, vat.at[i]);
+      };
+      auto load_gates = [&](int c) {
+        const float* gates = a.gates + (sh0 + (long)c * a.H) * kGateRows * C;
+        eg_next = gates[tok];
+        wt_next = gates[C + tok];
+      };
+      auto next = [&]() {
+        eg = eg_next;
+        wt = wt_next;
 #pragma unroll
-      for (int kp = 0; kp < kKp; ++kp) terms8<kTerms>(tn[kp], tf[kp]);
-    };
-    auto load_t = [&](int c) { load_operands<C>(a.tf, sh0 + (long)c * a.H, w.tb, 0, w.tb / 2, lane, tn); };
-    if (last >= 0) {
-      load_rows(0);
-      load_gates(0);
-      load_t(0);
-      next();
-      load_t(min(1, last));
-      load_gates(min(1, last));
-    }
-    loads_done();
-    __syncthreads();
-    for (int c = 0; c <= last; ++c) {
-      const long sh = sh0 + (long)c * a.H;
-      // X = V - e^G (K S^T): lane token c16, value columns 4 g + r.
-      f32x4 X[Sh::kV];
-      u32x4 kt[KB][NX];
-#pragma unroll
-      for (int b = 0; b < KB; ++b) terms8<NX>(kr[b], kt[b]);
-#pragma unroll
-      for (int i = 0; i < Sh::kV; ++i) {
-        if (w.vb(i) >= NV) continue;
-        const f32x4 v = floats4<NX>(vr[i]);
-        X[i] = state_times<KB, NV, NX, kTerms>(Sl, w.vb(i), kt, lane);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) X[i][r] = fmaf(-eg, X[i][r], v[r]);
-        stage4<C, kTerms, kPitchV>(Xl, tok, 16 * w.vb(i) + 4 * g, X[i]);
+        for (int kp = 0; kp < kKp; ++kp) terms8<kTerms>(tn[kp], tf[kp]);
+      };
+      auto load_t = [&](int c) { load_operands<C>(a.tf, sh0 + (long)c * a.H, w.tb, 0, w.tb / 2, lane, tn); };
+      if (last >= 0) {
+        load_rows(0);
+        load_gates(0);
+        load_t(0);
+        next();
+        load_t(min(1, last));
+        load_gates(min(1, last));
       }
-#pragma unroll
-      for (int b = 0; b < KB; ++b) stage_rows<C, KB, NV, NX>(Kl, w, c16, g, b, kt[b]);
-      load_rows(min(c + 1, last));
+      loads_done();
       __syncthreads();
+      for (int c = 0; c <= last; ++c) {
+        const long sh = sh0 + (long)c * a.H;
+        // X = V - e^G (K S^T): lane token c16, value columns 4 g + r.
+        f32x4 X[Sh::kV];
+        u32x4 kt[KB][NX];
+#pragma unroll
+        for (int b = 0; b < KB; ++b) terms8<NX>(kr[b], kt[b]);
+#pragma unroll
+        for (int i = 0; i < Sh::kV; ++i) {
+          if (w.vb(i) >= NV) continue;
+          const f32x4 v = floats4<NX>(vr[i]);
+          X[i] = state_times<KB, NV, NX, kTerms>(Sl, w.vb(i), kt, lane);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) X[i][r] = fmaf(-eg, X[i][r], v[r]);
+          stage4<C, kTerms, kPitchV>(Xl, tok, 16 * w.vb(i) + 4 * g, X[i]);
+        }
+#pragma unroll
+        for (int b = 0; b < KB; ++b) stage_rows<C, KB, NV, NX>(Kl, w, c16, g, b, kt[b]);
+        load_rows(min(c + 1, last));
+        __syncthreads();
 
-      // U = T diag(beta) X.
-      f32x4 U[Sh::kV];
+        // U = T diag(beta) X.
+        f32x4 U[Sh::kV];
 #pragma unroll
-      for (int i = 0; i < Sh::kV; ++i) {
-        if (w.vb(i) >= NV) continue;
-        U[i] = zero;
+        for (int i = 0; i < Sh::kV; ++i) {
+          if (w.vb(i) >= NV) continue;
+          U[i] = zero;
 #pragma unroll
-        for (int kp = 0; kp < kKp; ++kp) {
-          if (kp > w.tb / 2) continue;
-          u32x4 xt[kTerms];
-          values_operand<C, kTerms, kPitchV>(Xl, kp, 16 * w.vb(i), lane, xt);
-          U[i] = mma<kTerms, kTerms, kTerms>(xt, tf[kp], U[i]);
+          for (int kp = 0; kp < kKp; ++kp) {
+            if (kp > w.tb / 2) continue;
+            u32x4 xt[kTerms];
+            values_operand<C, kTerms, kPitchV>(Xl, kp, 16 * w.vb(i), lane, xt);
+            U[i] = mma<kTerms, kTerms, kTerms>(xt, tf[kp], U[i]);
+          }
+          if (CAREFUL) continue;
+          stage4<C, kTerms, kPitchV>(Wl, tok, 16 * w.vb(i) + 4 * g, U[i] * wt);
+          if (WHAT == kKeep) buf_store16(__builtin_bit_cast(u32x4, U[i]), make_rsrc(a.u + sh * C * a.dv, (uint32_t)(C * a.dv * 4)), uat.at[i]);
+          if (WHAT == kOutputs) stage4<C, kTerms, kPitchV>(Ul + (c & 1) * kU, tok, 16 * w.vb(i) + 4 * g, U[i]);
         }
-        stage4<C, kTerms, kPitchV>(Wl, tok, 16 * w.vb(i) + 4 * g, U[i] * wt);
-        if (WHAT == kKeep) buf_store16(__builtin_bit_cast(u32x4, U[i]), make_rsrc(a.u + sh * C * a.dv, (uint32_t)(C * a.dv * 4)), uat.at[i]);
-        if (WHAT == kOutputs) stage4<C, kTerms, kPitchV>(Ul + (c & 1) * kU, tok, 16 * w.vb(i) + 4 * g, U[i]);
-      }
-      __syncthreads();
-      __builtin_amdgcn_sched_barrier(0);   // while the state is updated, and not before the barrier
-      next();
-      load_t(min(c + 2, last));
-      load_gates(min(c + 2, last));
-      __syncthreads();
-    }
-  } else {
-    const KeyPieces<KB> qat(tok, g, a.q_row, a.dk, kEsz);
-    const ValuePieces<C, KB, NV> oat(w, tok, g, u.dv0, (long)a.H * a.dv, a.dv, kEsz);
-    const StatePieces<C, KB, NV> pieces(a, u, w, c16, g);
-    State<C, KB, NV> S;
-    read_state<C, KB, NV>(a, u, w, c16, g, S);
-    stage_state<C, KB, NV>(Sl, w, c16, g, S);
-    Raw8<NX> qr[KEEP ? 1 : KB];
-    Scores<NX> pr[KEEP ? 1 : kKp];
-    f32x4 O[Sh::kV];
-    float eg = 0.f, keep = 0.f;
-    auto load_q = [&](int c) {
-      const float* gates = a.gates + (sh0 + (long)c * a.H) * kGateRows * C;
-      eg = gates[tok];
-      const rsrc_t rq = rows(a.q, c, a.q_row, (long)hk * a.dk);
+        if constexpr (CAREFUL) {
+          float* const Uf = reinterpret_cast<float*>(Wl);   // [C][16 NV], until W is staged
+          const float* gates = a.gates + sh * kGateRows * C;
 #pragma unroll
-      for (int b = 0; b < (KEEP ? 0 : KB); ++b) qr[b] = load8<NX>(rq, qat.at[b]);
-    };
-    auto load_keep = [&](int c) { keep = a.gates[((sh0 + (long)c * a.H) * kGateRows + 5) * C]; };
-    // O += P U of a chunk: while the token waves make U of the next.
-    auto finish = [&](int c) {
-      const rsrc_t ro = rows(a.o, c, (long)a.H * a.dv, (long)u.h * a.dv);
+          for (int i = 0; i < Sh::kV; ++i)
+            if (w.vb(i) < NV && not_finite(U[i]) && !not_finite(X[i])) again = 1;
+          __syncthreads();
+          if (uniform(again) && wave == 0) updates_by_token<C, KB, NV, NX, kPitchV>(gates, Kl, Xl, Uf, min(C, u.len - c * C), lane);
+          __syncthreads();
 #pragma unroll
-      for (int i = 0; i < Sh::kV; ++i) {
-        if (w.vb(i) >= NV) continue;
+          for (int i = 0; i < Sh::kV; ++i) {
+            if (w.vb(i) >= NV) continue;
+            const f32x4 by_token = *reinterpret_cast<const f32x4*>(Uf + tok * 16 * NV + 16 * w.vb(i) + 4 * g);
 #pragma unroll
-        for (int kp = 0; kp < kKp; ++kp) {
-          if (kp > w.tb / 2) continue;
-          u32x4 ut[kTerms], pt[kTerms];
-          values_operand<C, kTerms, kPitchV>(Ul + (c & 1) * kU, kp, 16 * w.vb(i), lane, ut);
-          terms8<kTerms>(pr[kp], pt);
-          O[i] = mma<kTerms, kTerms, kTerms>(ut, pt, O[i]);
+            for (int r = 0; r < 4; ++r)
+              if (uniform(again) && tok < u.len - c * C && U[i][r] * 0.f != 0.f && X[i][r] * 0.f == 0.f) U[i][r] = by_token[r];
+          }
+          __syncthreads();
+          if (tid == 0) again = 0;
+#pragma unroll
+          for (int i = 0; i < Sh::kV; ++i) {
+            if (w.vb(i) >= NV) continue;
+            stage4<C, kTerms, kPitchV>(Wl, tok, 16 * w.vb(i) + 4 * g, U[i] * wt);
+            stage4<C, kTerms, kPitchV>(Ul + (c & 1) * kU, tok, 16 * w.vb(i) + 4 * g, U[i]);
+          }
         }
-        store4<NX>(O[i], ro, oat.at[i]);
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);   // while the state is updated, and not before the barrier
+        next();
+        load_t(min(c + 2, last));
+        load_gates(min(c + 2, last));
+        __syncthreads();
       }
-    };
-    if (last >= 0) {
-      load_keep(0);
-      if (!KEEP) load_q(0);
-    }
-    loads_done();
-    __syncthreads();
-    for (int c = 0; c <= last; ++c) {
-      const int ahead = min(c + 1, last);
-      f32x4 Q[Sh::kV];
-      if (WHAT == kKeep) pieces.store(a.states + (sh0 + (long)c * a.H) * mat, S);
-      if constexpr (!KEEP) {   // scale e^G (Q S^T)
-        u32x4 qt[KB][NX];
-#pragma unroll
-        for (int b = 0; b < KB; ++b) terms8<NX>(qr[b], qt[b]);
-#pragma unroll
-        for (int i = 0; i < Sh::kV; ++i)
-          if (w.vb(i) < NV) Q[i] = state_times<KB, NV, NX, kTerms>(Sl, w.vb(i), qt, lane) * (eg * a.scale);
-        load_q(ahead);
-      }
-      __syncthreads();
-      if constexpr (!KEEP) {
-        if (c > 0) finish(c - 1);
-        load_operands<C>(static_cast<const ScoresIn<NX>*>(a.pf), sh0 + (long)c * a.H, w.tb, 0, w.tb / 2, lane, pr);
-#pragma unroll
-        for (int i = 0; i < Sh::kV; ++i) O[i] = Q[i];
-      }
-      scale_state<C, KB, NV>(S, keep);
-      load_keep(ahead);
-      __syncthreads();
-      // S = e^(G_C) S + (e^(G_C - G) U)^T K.
-#pragma unroll
-      for (int kp = 0; kp < kKp; ++kp) state_update<C, KB, NV, NX>(Kl, Wl, w, kp, lane, S);
+    } else {
+      const KeyPieces<KB> qat(tok, g, a.q_row, a.dk, kEsz);
+      const ValuePieces<C, KB, NV> oat(w, tok, g, u.dv0, (long)a.H * a.dv, a.dv, kEsz);
+      const StatePieces<C, KB, NV> pieces(a, u, w, c16, g);
+      State<C, KB, NV> S;
+      read_state<C, KB, NV>(a, u, w, c16, g, S);
       stage_state<C, KB, NV>(Sl, w, c16, g, S);
+      Raw8<NX> qr[KEEP ? 1 : KB];
+      Scores<NX> pr[KEEP ? 1 : kKp];
+      f32x4 O[Sh::kV];
+      float eg = 0.f, keep = 0.f;
+      auto load_q = [&](int c) {
+        const float* gates = a.gates + (sh0 + (long)c * a.H) * kGateRows * C;
+        eg = gates[tok];
+        const rsrc_t rq = rows(a.q, c, a.q_row, (long)hk * a.dk);
+#pragma unroll
+        for (int b = 0; b < (KEEP ? 0 : KB); ++b) qr[b] = load8<NX>(rq, qat.at[b]);
+      };
+      auto load_keep = [&](int c) { keep = a.gates[((sh0 + (long)c * a.H) * kGateRows + 5) * C]; };
+      // O += P U of a chunk: while the token waves make U of the next.
+      auto finish = [&](int c) {
+        const rsrc_t ro = rows(a.o, c, (long)a.H * a.dv, (long)u.h * a.dv);
+#pragma unroll
+        for (int i = 0; i < Sh::kV; ++i) {
+          if (w.vb(i) >= NV) continue;
+          const f32x4 own = O[i];
+#pragma unroll
+          for (int kp = 0; kp < kKp; ++kp) {
+            if (kp > w.tb / 2) continue;
+            u32x4 ut[kTerms], pt[kTerms];
+            values_operand<C, kTerms, kPitchV>(Ul + (c & 1) * kU, kp, 16 * w.vb(i), lane, ut);
+            terms8<kTerms>(pr[kp], pt);
+            O[i] = mma<kTerms, kTerms, kTerms>(ut, pt, O[i]);
+          }
+          if (CAREFUL && __any(not_finite(O[i]))) {
+            const ScoresIn<NX>* p = static_cast<const ScoresIn<NX>*>(a.pf);
+            p += scores_at<C>(p, sh0 + (long)c * a.H);
+            O[i] = sum_so_far<C, kPitchV>(O[i], own, p, Ul + (c & 1) * kU, tok, 16 * w.vb(i) + 4 * g);
+          }
+          store4<NX>(O[i], ro, oat.at[i]);
+        }
+      };
+      if (last >= 0) {
+        load_keep(0);
+        if (!KEEP) load_q(0);
+      }
+      if (!KEEP && !CAREFUL && tid == kThreads / 2) lost = again = 0;
+      loads_done();
       __syncthreads();
+      for (int c = 0; c <= last; ++c) {
+        const int ahead = min(c + 1, last);
+        f32x4 Q[Sh::kV];
+        if (WHAT == kKeep) pieces.store(a.states + (sh0 + (long)c * a.H) * mat, S);
+        if constexpr (!KEEP) {   // scale e^G (Q S^T)
+          u32x4 qt[KB][NX];
+#pragma unroll
+          for (int b = 0; b < KB; ++b) terms8<NX>(qr[b], qt[b]);
+#pragma unroll
+          for (int i = 0; i < Sh::kV; ++i)
+            if (w.vb(i) < NV) Q[i] = state_times<KB, NV, NX, kTerms>(Sl, w.vb(i), qt, lane) * (eg * a.scale);
+          load_q(ahead);
+        }
+        __syncthreads();
+        if constexpr (!KEEP) {
+          if (c > 0) finish(c - 1);
+          load_operands<C>(static_cast<const ScoresIn<NX>*>(a.pf), sh0 + (long)c * a.H, w.tb, 0, w.tb / 2, lane, pr);
+#pragma unroll
+          for (int i = 0; i < Sh::kV; ++i) O[i] = Q[i];
+        }
+        scale_state<C, KB, NV>(S, keep);
+        load_keep(ahead);
+        if constexpr (CAREFUL) {   // the token waves' three
+          __syncthreads();
+          __syncthreads();
+          __syncthreads();
+        }
+        __syncthreads();
+        // S = e^(G_C) S + (e^(G_C - G) U)^T K.
+#pragma unroll
+        for (int kp = 0; kp < kKp; ++kp) state_update<C, KB, NV, NX>(Kl, Wl, w, kp, lane, S);
+        stage_state<C, KB, NV>(Sl, w, c16, g, S);
+        __syncthreads();
+      }
+      if (!KEEP && last >= 0) finish(last);
+      if (u.to) pieces.store(u.to, S);
+      if (!KEEP && !CAREFUL) {
+#pragma unroll
+        for (int i = 0; i < w.kB; ++i)
+#pragma unroll
+          for (int j = 0; j < w.kS; ++j)
+            if (not_finite(S[i][j])) lost = 1;
+      }
     }
-    if (!KEEP && last >= 0) finish(last);
-    if (u.to) pieces.store(u.to, S);
+    return true;
+  };
+  const bool walked = walk(std::false_type{}, args);
+  if constexpr (!KEEP) {
+    if (!walked) return;
+    __syncthreads();
+    if (uniform(lost)) {
+      auto anew = __builtin_amdgcn_kernarg_segment_ptr();   // the arguments too
+      asm volatile("" : "+s"(anew));
+      walk(std::true_type{}, *(const DeltaArgs*)anew);
+    }
   }
 }
 
@@ -473,7 +592,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_rev_kernel(DeltaArgs a) {
   const int wave = uniform(threadIdx.x >> 6);
   const Sh w(wave & 3);
   const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
-  const Unit u = delta_unit<C, NV, OWN, true>(a, a.dfin, a.dinit);
+  const Unit u = delta_unit<C, NV, OWN, true>(a, blockIdx.x, a.dfin, a.dinit);
   if (u.none) return;
   const int hk = u.h / (a.H / a.Hk), tok = 16 * w.tb + c16, last = u.chunks - 1;
   const long mat = (long)a.dk * a.dv, sh0 = u.slot0 * a.H + u.h;

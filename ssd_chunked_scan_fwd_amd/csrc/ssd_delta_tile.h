@@ -210,6 +210,25 @@ __device__ __forceinline__ void load_operands(const uint16_t* from, long sh, int
   }
 }
 
+// Element (16 rb + row, col) of such a matrix.
+template <int C>
+__device__ __forceinline__ float operand_value(const float* m, int rb, int row, int col) {
+  return m[operand_at(C, rb, col / 32) + 256 * (col / 16 & 1) + (row + 16 * (col / 4 & 3)) * 4 + (col & 3)];
+}
+template <int C>
+__device__ __forceinline__ float operand_value(const uint16_t* m, int rb, int row, int col) {
+  const uint16_t* at = m + kTerms * operand_at(C, rb, col / 32) + (row + 16 * (col / 4 & 3)) * 8 + 4 * (col / 16 & 1) + (col & 3);
+  float x = 0.f;
+#pragma unroll
+  for (int t = kTerms - 1; t >= 0; --t) x += bf16_to_f32(at[t * kOperand]);
+  return x;
+}
+
+__device__ __forceinline__ bool not_finite(f32x4 x) {
+  const float y = fmaf(x[0], 0.f, fmaf(x[1], 0.f, fmaf(x[2], 0.f, x[3] * 0.f)));
+  return y != y;
+}
+
 // Everything loaded so far is there. Before a loop that loads ahead: the compiler's waits inside it are for the order
 // of its own loads then, not for that of the loads before it.
 __device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }   // vmcnt(0)
