@@ -857,16 +857,18 @@ __global__ __launch_bounds__(128 * KB) void delta_join_kernel(DeltaArgs a, int C
 }
 
 // Value blocks a workgroup. Two, which read a chunk's rows and operands once, where workgroups of one would be more
-// than the CUs (of packed sequences, the longest of which are taken to be three times the mean, three times as many);
-// else one. Heads of 128 x 128, us with one and with two: 2 x 4096 tokens of 32 heads (512 workgroups of one) 260 and
-// 219, 4096 of 48 235 and 193; 5087 ragged tokens of 16 heads of 64 x 96 (768) 84 and 93. fp32: two; with keys of
-// 256, whose rows leave LDS for one, one. Walks that are cut fill the card as they are: one (bf16).
+// than the CUs; else one. Prompts, us with one and with two (the workgroups of one): heads of 128 x 128, 2 x 4096 tokens of
+// 32 (512) 269 and 243, 4096 of 40 (320) 227 and 205, 2 x 2048 of 17 (272) 128 and 119, 4096 of 32 (256) 141 and 208; heads
+// of 64 x 64 gain nothing (8 x 1024 of 16 (512) 66 and 67, with gradients 254 and 241). Packed sequences take one: what
+// counts there is the longest, which two make longer: 8 of 5117 tokens, 16 heads of 64 x 96 (768) 110 and 123, 32 heads
+// (1536) 125 and 144, 8 of 7996, 16 of 128 x 128 (1024) 187 and 241, 64 of 7652, 8 heads (4096) 119 and 127 (sequences that are
+// equally long, which the host cannot know, would gain: 8 of 1024, 16 heads of 128 x 128, 161 and 150). fp32: two; with
+// keys of 256, whose rows leave LDS for one, one. Walks that are cut fill the card as they are: one (bf16).
 constexpr int nv32(int kb) { return kb > 4 ? 1 : 2; }
 int value_blocks(const DeltaArgs& a) {
   if (!a.bf16) return nv32((a.dk + 31) / 32);
-  if (a.seg) return 1;
-  const long units = (long)(a.S > 0 ? a.S : a.batch) * a.H * ((a.dv + 15) / 16);
-  return units > (a.S > 0 ? 3 * 256 : 256) && a.dk <= 128 ? 2 : 1;
+  if (a.seg || a.S > 0) return 1;
+  return (long)a.batch * a.H * ((a.dv + 15) / 16) > 256 && a.dk <= 128 ? 2 : 1;
 }
 
 template <int KB, int WHAT>

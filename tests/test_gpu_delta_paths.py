@@ -24,8 +24,8 @@ def starts(lens):
     return [0, *np.cumsum(lens).tolist()]
 
 
-# Workgroups of one block of 16 value columns enough (256; packed 768) that bf16 walks take two, keys of 24 to 128, value
-# columns that fill the last pair of blocks, half of it or less. The packed ones: sequences of no and of one token.
+# Workgroups of one block of 16 value columns enough (256) that bf16 walks take two, keys of 24 to 128, value columns that
+# fill the last pair of blocks, half of it or less. Packed sequences, some of no and of one token, take one, however many.
 RAGGED = [65, 0, 1, 130, 64, 2, 33, 0, 128, 70]
 WIDE = [(3, 130, 12, 6, 128, 128, None), (6, 100, 16, 8, 128, 40, None), (5, 70, 20, 10, 72, 40, None), (9, 67, 16, 4, 64, 32, None),
         (5, 129, 14, 7, 64, 128, None), (4, 200, 16, 16, 24, 96, None), (7, 65, 42, 21, 24, 8, None), (4, 128, 12, 12, 40, 200, None),
