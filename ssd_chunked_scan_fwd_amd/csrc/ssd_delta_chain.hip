@@ -11,11 +11,14 @@
 // update, a quarter of dk each, and make what nothing waits for (O; backwards the
 // terms of dO) while the token waves work. The next chunk's rows and operands are
 // loaded into the registers of this one's as soon as these have been used.
-// 16384 tokens, 32 heads on 16 of 128 x 128: 455 us for 256 chunks, 1.8 a chunk (475 MB read, 136 MB written: 1.3
-// TB/s); backwards 8192 tokens 320 us. LDS is busy 37 % of the time, the vector units 28 %, the matrix units 18 %,
+// 16384 tokens, 32 heads on 16 of 128 x 128: 480 us for 256 chunks, 1.9 a chunk (475 MB read, 136 MB written: 1.3
+// TB/s), where its products, 28 million operations a chunk and head in their terms, would take 213 at the rate of a large
+// product; backwards 8192 tokens 320 us. LDS is busy 38 % of the time, the vector units 35 %, the matrix units 20 %,
 // hardly at the same time: the phases' dependent reads, products and splits into terms bound it. With the loads of
-// every chunk from the first's rows, out of the caches, the walk of 8192 tokens takes 30 us less of 234; two
-// workgroups on a CU together gain a tenth on one after the other.
+// every chunk from the first's rows, out of the caches, the walk of 8192 tokens took 30 us less of 234; two
+// workgroups on a CU together gained a tenth on one after the other (both with two terms in o's products).
+// Where the workgroups of ragged sequences fall, long ones side by side on a CU or not, moves a call by up to 20 us of
+// 100 with anything that shifts their start.
 #include <algorithm>
 
 #include "ssd_delta_tile.h"
@@ -931,7 +934,7 @@ long delta_segment_blocks(const DeltaArgs& a) {
 // A walk of few heads leaves most of the card idle for as long as its longest sequence is. Cut into segments, every
 // segment's own last state (from a state of zero) and its map of a state are made at once, the states behind the
 // segments follow from these one after the other, and all segments are walked at once: twice to three times the
-// work, in chains of a segment's length (8192 tokens, 4 heads of 128 x 128: 220 us whole, 91 in eight segments). The
+// work, in chains of a segment's length (8192 tokens, 4 heads of 128 x 128: 220 us whole, 93 in eight segments). The
 // backward walk is cut alike, its maps the forward's transposed (both with the gradients 462 us whole, 240 cut; 8 heads
 // of 4096 tokens 272 and 218; fp32, 2048 tokens of 4 heads of 64 x 128, 249 and 114). The
 // number of segments is the one of least cost, counted in steps of a chunk: a walk takes as long as its longest chain,

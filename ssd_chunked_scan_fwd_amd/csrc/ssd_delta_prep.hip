@@ -13,7 +13,7 @@
 // T (with beta of its columns folded in) and P are stored as the operands that
 // the walk over the chunks loads, and for the gradients their transposes. A tile of
 // P is such an operand as its accumulators hold it.
-// 16384 tokens, 32 heads on 16 of 128 x 128: 100 us, 141 MB read and 225 MB written (3.7 TB/s), the vector units
+// 16384 tokens, 32 heads on 16 of 128 x 128: 100 us, 143 MB read and 237 MB written (3.8 TB/s), the vector units
 // busy 33 % of the time, matrix units 17 %, LDS 28 %: the inverse's dependent steps bound it, four workgroups a CU.
 #include "ssd_delta_tile.h"
 
