@@ -11,14 +11,14 @@
 // update, a quarter of dk each, and make what nothing waits for (O; backwards the
 // terms of dO) while the token waves work. The next chunk's rows and operands are
 // loaded into the registers of this one's as soon as these have been used.
-// 16384 tokens, 32 heads on 16 of 128 x 128: 480 us for 256 chunks, 1.9 a chunk (475 MB read, 136 MB written: 1.3
-// TB/s), where its products, 28 million operations a chunk and head in their terms, would take 213 at the rate of a large
-// product; backwards 8192 tokens 320 us. LDS is busy 38 % of the time, the vector units 35 %, the matrix units 20 %,
-// hardly at the same time: the phases' dependent reads, products and splits into terms bound it. With the loads of
-// every chunk from the first's rows, out of the caches, the walk of 8192 tokens took 30 us less of 234; two
-// workgroups on a CU together gained a tenth on one after the other (both with two terms in o's products).
-// Where the workgroups of ragged sequences fall, long ones side by side on a CU or not, moves a call by up to 20 us of
-// 100 with anything that shifts their start.
+// 16384 tokens, 32 heads on 16 of 128 x 128: 506 us for 256 chunks, 2.0 a chunk, at the least in a trace, which slows
+// calls (back to back matrices and walk take 580, of which the matrices 100); 475 MB read, 136 MB written: 1.2 TB/s. Its
+// products, 28 million operations a chunk and head in their terms, would take 213 us at the rate of a large product.
+// Backwards 8192 tokens 321 us. LDS is busy 38 % of the time, the vector units 35 %, the matrix units 20 %, hardly at the
+// same time: the phases' dependent reads, products and splits into terms bound it. With the loads of every chunk from the
+// first's rows, out of the caches, the walk of 8192 tokens took 30 us less of 234; two workgroups on a CU together gained
+// a tenth on one after the other (both with two terms in o's products). Where the workgroups of ragged sequences fall,
+// long ones side by side on a CU or not, moves a call by up to 20 us of 100 with anything that shifts their start.
 #include <algorithm>
 
 #include "ssd_delta_tile.h"
