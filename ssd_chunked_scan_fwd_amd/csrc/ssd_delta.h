@@ -76,7 +76,7 @@ int delta_prep_threads();
 long delta_chain_blocks(const DeltaArgs& a);
 long delta_segment_blocks(const DeltaArgs& a);   // of the segments' own states and maps
 int delta_chain_threads();
-int delta_grad_heads(long slots, int H, int Hk, int dk);
+int delta_grad_heads(long slots, int H, int Hk, int dk, bool bf16);
 long delta_bwd_blocks(const DeltaArgs& a);
 int delta_bwd_threads();
 

@@ -79,7 +79,7 @@ ssd_status check_delta(const ssd_delta_shape* s, DeltaDims* d, bool backward) {
   const int C = ssd::delta_chunk(s->dtype == SSD_DTYPE_BF16);
   d->spr = ssd::lin_slots_per_row(s->seqlen, s->num_seqs, C);
   d->slots = s->num_seqs > 0 ? d->spr : d->spr * s->batch;
-  d->grad_heads = ssd::delta_grad_heads(d->slots, s->nheads, s->nqk_heads, s->dk);
+  d->grad_heads = ssd::delta_grad_heads(d->slots, s->nheads, s->nqk_heads, s->dk, s->dtype == SSD_DTYPE_BF16);
   d->seg = ssd::delta_segment(s->batch, s->seqlen, s->num_seqs, s->nheads, s->dk, s->dv, s->dtype == SSD_DTYPE_BF16);
   d->segs_per_row = d->seg ? ssd::lin_slots_per_row(s->seqlen, s->num_seqs, d->seg * C) : 0;
   d->segs = s->num_seqs > 0 ? d->segs_per_row : d->segs_per_row * s->batch;

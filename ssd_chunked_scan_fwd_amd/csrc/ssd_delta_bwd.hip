@@ -366,11 +366,14 @@ void grads(const DeltaArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Value heads a workgroup, one after the other: all that share their keys, where that leaves the card four rounds of
-// workgroups (no partial sums of every head to write and to add up then: 8192 tokens, 32 heads on 16 of 128 x 128,
-// with the walks 1110 us one a workgroup, 1063 two); else one, and so with keys of 256, which leave no registers for
-// the sums.
-int delta_grad_heads(long slots, int H, int Hk, int dk) { return slots * Hk >= 1024 && dk <= 128 ? H / Hk : 1; }
+// Value heads a workgroup, one after the other: all that share their keys, where that leaves a workgroup for every CU, in
+// fp32 two (no partial sums of every head to write and to add up then); else one, and so with keys of 256, which leave no registers for
+// the sums. With the walks, us with one and with all, heads of 128 x 128 two on a key (the workgroups of all): 8192 tokens of
+// 32 (2048) 1114 and 1069, 4096 of 24 (768) 472 and 452, 1024 of 32 (256) 148 and 141, 768 of 32 (192) 122 and 118, 512 of
+// 32 (128) 86 and 101; four on a key, 64 x 64: 2 x 2048 of 16 (256) 175 and 169, half of them (128) 130 and 142. fp32, 64 x
+// 64: 2048 of 32 (1024) 249 and 238, 128 x 64 2048 of 16 (512) 275 and 272; 64 x 64, four on a key, 1024 of 32 (256) 145
+// and 151, half of them (128) 96 and 116.
+int delta_grad_heads(long slots, int H, int Hk, int dk, bool bf16) { return slots * Hk >= (bf16 ? 256 : 512) && dk <= 128 ? H / Hk : 1; }
 long delta_bwd_blocks(const DeltaArgs& a) { return a.slots * (a.H / a.grad_heads); }
 int delta_bwd_threads() { return threads_of(64); }
 
