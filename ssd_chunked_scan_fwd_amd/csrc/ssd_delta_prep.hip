@@ -324,7 +324,9 @@ __global__ __launch_bounds__(kThreads, BWD ? 3 : 4) void delta_prep_kernel(Delta
 
 // Value heads a workgroup: all that share its keys, whose products it makes once, or so few that the launch has
 // four workgroups for every CU. A workgroup's time is mostly waits: 5087 tokens of 16 heads on 4, 348 workgroups of four
-// heads took 25.4 us, 1392 of one 22.5; 8192 of 4 on 2, 256 of two 15.7 and 512 of one 14.3.
+// heads took 25.4 us, 1392 of one 22.5; 8192 of 4 on 2, 256 of two 15.7 and 512 of one 14.3. From 1024 on the products count
+// (calls, us): 4096 tokens of 32 on 16, 128 x 128, 1024 of two 140, 2048 of one 146; 4 x 2048 of 32 on 8, 64 x 64, 1024 of
+// four 105, 4096 of one 128; 16384 of 32 on 16, 4096 of two 581, 8192 of one 605.
 int heads_a_workgroup(const DeltaArgs& a) {
   const int rep = a.H / a.Hk;
   int heads = rep;
