@@ -441,8 +441,12 @@ __global__ __launch_bounds__(kThreads, KB <= 4 && NX == 1 && NV == 1 ? 4 : 2) vo
           float* const Uf = reinterpret_cast<float*>(Wl);   // [C][16 NV], until W is staged
           const float* gates = a.gates + sh * kGateRows * C;
 #pragma unroll
-          for (int i = 0; i < Sh::kV; ++i)
-            if (w.vb(i) < NV && not_finite(U[i]) && !not_finite(X[i])) again = 1;
+          for (int i = 0; i < Sh::kV; ++i) {
+            if (w.vb(i) >= NV) continue;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (U[i][r] * 0.f != 0.f && X[i][r] * 0.f == 0.f) again = 1;
+          }
           __syncthreads();
           if (uniform(again) && wave == 0) updates_by_token<C, KB, NV, NX, kPitchV>(gates, Kl, Xl, Uf, min(C, u.len - c * C), lane);
           __syncthreads();

@@ -129,3 +129,22 @@ def test_packed(dtype):
         finite_but(o, reach)
         check_rest(o, want, reach, d, name)
         assert not torch.isfinite(fin[2]).any() and torch.isfinite(fin[[0, 1, 3]]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_columns_side_by_side(dtype):
+    """A state's column that is not finite from the start, and tokens of the columns beside it, one after the other."""
+    say(f"[delta causal] columns {dtype}")
+    b, T, H, dv = 1, 150, 2, 32
+    d = make(b, T, H, 1, 64, dv, dtype, seed=72)
+    want = ref.batch_forward(*arrays(d), 0.5, n64(d["init"]))["o"]
+    reach = torch.zeros(b, T, H, dv, dtype=torch.bool, device="cuda")
+    d["init"][0, 1, 9] = NAN
+    reach[0, :, 1, 9] = True
+    for t, j in ((40, 8), (41, 11), (70, 10), (149, 12)):
+        d["v"][0, t, 1, j] = INF
+        reach[0, t:, 1, j] = True
+    o, fin = run_fwd(d)
+    finite_but(o, reach)
+    check_rest(o, want, reach, d, "columns")
+    finite_but(fin, reach[:, -1, :, :, None].expand(b, H, dv, 64))
